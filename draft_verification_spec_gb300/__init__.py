@@ -13,6 +13,11 @@ The operation follows the AngelSpec / DFly description of verification:
 alpha = sum min(p, q) = 1 - TV, serial acceptance with a first-rejection cut,
 residual / bonus draws, greedy argmax matching at T = 0, and a batch-level
 budget over prefix confidences prod alpha.
+
+The operators around that call (module ``step``): ``sample_tokens`` (the
+drafts' tokens and truncated logits), ``rope_append`` (positions of the new
+tokens, cache write) and ``chunk_attention`` (the new tokens over the paged
+cache).
 """
 from __future__ import annotations
 
@@ -24,9 +29,10 @@ import torch
 
 from . import _lib
 
-SPEC_F32, SPEC_BF16 = 0, 1
+SPEC_F32, SPEC_BF16, SPEC_F16 = 0, 1, 2
 STATUS_NAMES = {0: "SPEC_OK", 1: "SPEC_ERR_INVALID_ARG", 2: "SPEC_ERR_UNSUPPORTED", 3: "SPEC_ERR_CUDA",
-                4: "SPEC_ERR_DEVICE_TIMEOUT", 5: "SPEC_ERR_TOKEN_RANGE", 6: "SPEC_ERR_WORKSPACE"}
+                4: "SPEC_ERR_DEVICE_TIMEOUT", 5: "SPEC_ERR_TOKEN_RANGE", 6: "SPEC_ERR_WORKSPACE",
+                7: "SPEC_ERR_PAGE_RANGE"}
 
 
 class SpecError(RuntimeError):
@@ -87,6 +93,17 @@ class Workspace:
     def __init__(self, device=None):
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf: Optional[torch.Tensor] = None
+        self.step_buf: Optional[torch.Tensor] = None    # the step operators' status word and partial results
+
+    def get_step(self, need: int, stream) -> torch.Tensor:
+        """The buffer of the step operators (rope_append, chunk_attention), at least `need` bytes."""
+        if self.step_buf is None or self.step_buf.numel() < need:
+            buf = torch.empty(max(need, 4096), dtype=torch.uint8, device=self.device)
+            if stream is not None:
+                buf.record_stream(stream)
+            _check(lib().spec_workspace_init(_ptr(buf), 256, _stream_ptr(stream)), "spec_workspace_init")
+            self.step_buf = buf
+        return self.step_buf
 
     def get(self, B: int, K: int, V: int, dtype_code: int, stream) -> torch.Tensor:
         need = int(lib().spec_workspace_bytes(B, K, V, dtype_code))
@@ -98,12 +115,15 @@ class Workspace:
         return self.buf
 
     def status(self, stream=None) -> int:
-        """Read and clear the device status word (synchronises the stream)."""
-        if self.buf is None:
-            return 0
-        out = ctypes.c_int32(0)
-        _check(lib().spec_get_status(_ptr(self.buf), _stream_ptr(stream), ctypes.byref(out)), "spec_get_status")
-        return out.value
+        """Read and clear the device status words (synchronises the stream)."""
+        found = 0
+        for buf in (self.buf, self.step_buf):
+            if buf is None:
+                continue
+            out = ctypes.c_int32(0)
+            _check(lib().spec_get_status(_ptr(buf), _stream_ptr(stream), ctypes.byref(out)), "spec_get_status")
+            found = found or out.value
+        return found
 
     def reset(self, stream=None):
         if self.buf is not None:
@@ -355,5 +375,8 @@ def draft_budget(draft, tokens, temperature: float, budget: Optional[int] = None
     return n_out, depth, conf
 
 
+from .step import RopePlan, SampleOutput, chunk_attention, rope_append, sample_tokens  # noqa: E402
+
 __all__ = ["verify_chain", "verify_block", "overlap_alpha", "alloc_budget", "alloc_budget_adaptive",
-           "draft_budget", "Workspace", "VerifyOutput", "Tuning", "SpecError", "lib"]
+           "draft_budget", "Workspace", "VerifyOutput", "Tuning", "SpecError", "lib",
+           "chunk_attention", "rope_append", "sample_tokens", "RopePlan", "SampleOutput"]

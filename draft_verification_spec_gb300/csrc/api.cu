@@ -14,6 +14,7 @@
 #include "../../include/spec_verify.h"
 #include "api_range.h"
 #include "spec_internal.h"
+#include "step_internal.h"
 
 namespace sv {
 const void* sample_kernel_bf16(bool aligned);
@@ -547,6 +548,7 @@ const char* spec_error_string(int status) {
     case SPEC_ERR_DEVICE_TIMEOUT: return "a bounded device wait ran out";
     case SPEC_ERR_TOKEN_RANGE: return "draft token id outside [0, V)";
     case SPEC_ERR_WORKSPACE: return "workspace too small or not 256-byte aligned";
+    case SPEC_ERR_PAGE_RANGE: return "page id outside the cache, or position beyond the page table";
     default: return "unknown status";
   }
 }
@@ -576,7 +578,8 @@ spec_status_t spec_get_status(void* workspace, void* stream, int32_t* out_status
   if (cudaMemsetAsync(workspace, 0, sizeof(h), s) != cudaSuccess) return SPEC_ERR_CUDA;
   *out_status = (h & sv::kStatusTimeout) ? SPEC_ERR_DEVICE_TIMEOUT
                 : (h & sv::kStatusTokenRange) ? SPEC_ERR_TOKEN_RANGE
-                                              : SPEC_OK;
+                : (h & sv::kStatusPageRange) ? SPEC_ERR_PAGE_RANGE
+                                             : SPEC_OK;
   return SPEC_OK;
 }
 

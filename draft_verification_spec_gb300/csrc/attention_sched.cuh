@@ -1,0 +1,173 @@
+// Work split of the paged attention.
+//
+// An item is one tile of query rows (the new tokens of a request x the query heads of one key
+// head, token-major) of one (request, key head); its units are the key tiles it has to read.  The
+// units of all items, in the order (request, key head, row tile, key tile), are cut into n equal
+// runs, one per CTA, whatever the lengths are: a long cache with few rows is split over many CTAs
+// and a short one shares a CTA.  An item that crosses a cut leaves one partial result (maximum,
+// sum, unnormalised rows) per CTA, and the combine kernel joins them in the order of the keys, so
+// results do not depend on timing.  Lengths are read on the device: the host knows only bounds.
+#pragma once
+
+#include "spec_device.cuh"
+#include "step_internal.h"
+
+namespace sv {
+
+struct AttnReq {
+  int q0, nq, kv;
+};
+__device__ __forceinline__ AttnReq attn_request(const PagedBatch& c, int b) {
+  AttnReq r;
+  const long long cap = static_cast<long long>(c.table_width) * c.page_size;
+  r.q0 = min(max(__ldg(c.cu_q + b), 0), c.N);
+  r.nq = max(min(__ldg(c.cu_q + b + 1), c.N) - r.q0, 0);
+  const int kv = max(__ldg(c.kv_lens + b), 0);
+  r.kv = kv > cap ? static_cast<int>(cap) : kv;
+  return r;
+}
+
+// Keys [lo, hi) that rows [r0, r1) of the request can see.
+__device__ __forceinline__ void attn_keys(const AttnParams& p, const AttnReq& r, int r0, int r1, int* lo, int* hi) {
+  const int first = r.kv - r.nq + r0 / p.G, last = r.kv - r.nq + (r1 - 1) / p.G;
+  *hi = p.causal ? max(min(last + 1, r.kv), 0) : r.kv;
+  *lo = p.window > 0 ? max(first - p.window + 1, 0) : 0;
+}
+// First key tile and number of key tiles of row tile t (an item has one at least: its rows are
+// written even where they see no key).
+template <int BN>
+__device__ __forceinline__ int attn_tiles(const AttnParams& p, const AttnReq& r, int t, int bm, int* first) {
+  const int r0 = t * bm, r1 = min(r.nq * p.G, r0 + bm);
+  int lo, hi;
+  attn_keys(p, r, r0, r1, &lo, &hi);
+  *first = lo / BN;
+  return max((hi + BN - 1) / BN - *first, 1);
+}
+__device__ __forceinline__ int attn_row_tiles(const AttnParams& p, const AttnReq& r, int bm) {
+  return (r.nq * p.G + bm - 1) / bm;
+}
+template <int BN>
+__device__ __forceinline__ long long attn_request_units(const AttnParams& p, const AttnReq& r, int bm) {
+  const int nt = attn_row_tiles(p, r, bm);
+  long long n = 0;
+  for (int t = 0; t < nt; ++t) {
+    int first;
+    n += attn_tiles<BN>(p, r, t, bm, &first);
+  }
+  return n;
+}
+
+struct AttnSplit {
+  long long total;   // units of the call
+  int n;             // CTAs that share them
+  __device__ __forceinline__ long long begin(int c) const { return total * c / n; }
+  __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * n - 1) / total); }
+};
+
+// Position of a unit: the item and the unit's index in it.
+struct AttnCursor {
+  int b, h, t;
+  AttnReq req;
+  int first, count;   // the item's key tiles
+  int at;             // the unit's place among them
+};
+
+template <int THREADS>
+struct AttnSchedSmem {
+  long long warp[THREADS / 32];
+  long long rem;
+  int b;
+};
+
+// Block-wide: the units of the call and how many CTAs share them.
+template <int BN, int THREADS>
+__device__ __forceinline__ AttnSplit attn_split(const AttnParams& p, int bm, AttnSchedSmem<THREADS>& s) {
+  long long mine = 0;
+  for (int b = threadIdx.x; b < p.c.B; b += THREADS)
+    mine += attn_request_units<BN>(p, attn_request(p.c, b), bm) * p.c.Hkv;
+#pragma unroll
+  for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if ((threadIdx.x & 31) == 0) s.warp[threadIdx.x / 32] = mine;
+  __syncthreads();
+  AttnSplit sp;
+  sp.total = 0;
+#pragma unroll
+  for (int w = 0; w < THREADS / 32; ++w) sp.total += s.warp[w];
+  const long long n = (sp.total + p.min_units - 1) / p.min_units;
+  sp.n = static_cast<int>(n < p.n_max ? n : p.n_max);
+  __syncthreads();
+  return sp;
+}
+
+// The item at unit `rem` of request b's units.
+template <int BN>
+__device__ __forceinline__ void attn_enter(const AttnParams& p, int bm, int b, long long rem, AttnCursor* c) {
+  c->b = b;
+  c->req = attn_request(p.c, b);
+  const long long per_head = attn_request_units<BN>(p, c->req, bm);
+  c->h = static_cast<int>(rem / per_head);
+  rem -= per_head * c->h;
+  c->t = 0;
+  while (true) {
+    c->count = attn_tiles<BN>(p, c->req, c->t, bm, &c->first);
+    if (rem < c->count) break;
+    rem -= c->count;
+    ++c->t;
+  }
+  c->at = static_cast<int>(rem);
+}
+
+// Block-wide: the position of unit u (u < total).
+template <int BN, int THREADS>
+__device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, long long u, AttnSchedSmem<THREADS>& s) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
+  for (int base = 0; base < p.c.B; base += THREADS) {
+    const int b = base + threadIdx.x;
+    const long long mine = b < p.c.B ? attn_request_units<BN>(p, attn_request(p.c, b), bm) * p.c.Hkv : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 31) s.warp[w] = incl;
+    __syncthreads();
+    long long all = 0;
+#pragma unroll
+    for (int k = 0; k < THREADS / 32; ++k) {
+      if (k < w) incl += s.warp[k];
+      all += s.warp[k];
+    }
+    if (u >= incl - mine && u < incl) {
+      s.b = b;
+      s.rem = u - (incl - mine);
+    }
+    __syncthreads();
+    if (u < all) break;
+    u -= all;
+  }
+  AttnCursor c;
+  attn_enter<BN>(p, bm, s.b, s.rem, &c);
+  __syncthreads();
+  return c;
+}
+
+// The item after the cursor's (the caller knows that there is one).
+template <int BN>
+__device__ __forceinline__ void attn_next(const AttnParams& p, int bm, AttnCursor* c) {
+  c->at = 0;
+  if (++c->t < attn_row_tiles(p, c->req, bm)) {
+    c->count = attn_tiles<BN>(p, c->req, c->t, bm, &c->first);
+    return;
+  }
+  c->t = 0;
+  if (++c->h == p.c.Hkv) {
+    c->h = 0;
+    do {
+      c->req = attn_request(p.c, ++c->b);
+    } while (c->req.nq == 0);
+  }
+  c->count = attn_tiles<BN>(p, c->req, c->t, bm, &c->first);
+}
+
+}  // namespace sv

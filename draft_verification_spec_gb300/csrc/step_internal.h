@@ -1,0 +1,84 @@
+// Declarations shared by the kernels and the host code of the operators around a verification:
+// paged-cache attention, rotary positions with the cache write, and sampling.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+#include <cuda_runtime.h>
+
+namespace sv {
+
+// Status bit (with those of spec_internal.h): a page id outside the cache, or a position beyond the page table.
+constexpr int kStatusPageRange = 4;
+
+// A batch of requests over a paged cache.  Strides are in elements.
+struct PagedBatch {
+  uint8_t* k;
+  uint8_t* v;
+  long long k_page, k_token, k_head, v_page, v_token, v_head;
+  const int32_t* table;      // [B, table_width], rows table_stride apart
+  long long table_stride;
+  int table_width, pages, page_size;
+  const int32_t* kv_lens;    // [B] cached tokens, the new ones included
+  const int32_t* cu_q;       // [B + 1] first new token of every request
+  int B, N;                  // requests, new tokens
+  int Hkv, D;
+};
+
+struct AttnParams {
+  PagedBatch c;
+  const uint8_t* q;
+  long long q_token, q_head;
+  uint8_t* out;              // [N, Hq, D]
+  float* lse;                // [N, Hq] or null
+  int Hq, G;                 // query heads, query heads per key head
+  int causal, window;
+  float scale_log2;          // softmax scale x log2(e)
+  float* part_o;             // [2 n, BM, D] partial rows of items that more than one CTA works on
+  float* part_ml;            // [2 n, BM, 2] their maximum and sum
+  int min_units;             // fewest key tiles worth a CTA of their own
+  int n_max;                 // CTAs launched
+  long long wait_limit;      // ns per bounded wait (tcgen05 kernel)
+  int32_t* status;
+};
+
+// Kernel families of the attention: rows per tile, keys per tile.
+struct AttnPlan {
+  int kind;                  // 0: 16-row tiles, 1: 64-row tiles (mma.sync); 2: 256-row tiles (tcgen05)
+  int bm, bn, grid, smem, dp;
+};
+
+cudaError_t launch_attention_mma(bool bf16, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream);
+cudaError_t attention_mma_plan(bool bf16, int rows, int D, int sms, AttnPlan* plan);
+cudaError_t launch_attention_combine(int dtype, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream);
+
+struct RopeParams {
+  PagedBatch c;              // k / v may be null: nothing is stored
+  const uint8_t *q, *k, *v;  // new tokens
+  uint8_t *q_out, *k_out;    // rotated queries; rotated keys (or null)
+  long long q_token, q_head, k_token, k_head, v_token, v_head, qo_token, qo_head, ko_token, ko_head;
+  const unsigned long long* freq;  // [rotary / 2] turns a position x 2^64
+  float factor;
+  int Hq, rotary, interleaved;
+  int32_t* status;
+};
+cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream);
+
+struct SampleParams {
+  const void* logits;
+  long long stride;
+  int R, V;
+  const float* uniforms;
+  const float *temperature, *top_p, *min_p;   // per row, or null: the scalars
+  const int32_t* top_k;
+  float temperature0, top_p0, min_p0;
+  int top_k0;
+  int32_t* tokens;
+  float* probs;
+  int32_t* kept;
+  void* filtered;
+  long long filtered_stride;
+};
+cudaError_t launch_sample(int dtype, const SampleParams& p, cudaStream_t stream);
+
+}  // namespace sv

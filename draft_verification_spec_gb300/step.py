@@ -1,0 +1,338 @@
+"""The operators of a speculative decoding step around its verification.
+
+    from draft_verification_spec_gb300 import RopePlan, chunk_attention, rope_append, sample_tokens
+    rope = RopePlan(head_dim, theta=10000.0)
+    q = rope_append(q, k, v, rope, k_cache, v_cache, page_table, kv_lens, cu_q)
+    out = chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q)
+    s = sample_tokens(logits, uniforms, temperature=0.8, top_p=0.95, want_filtered=True)
+
+A batch is packed: tokens ``cu_q[b]:cu_q[b+1]`` are the new ones of request b, the last of its
+``kv_lens[b]`` tokens; its token t is slot ``t % page_size`` of page ``page_table[b, t // page_size]``
+of caches [pages, page_size, kv_heads, dim].  Lengths stay on the device.  As in the rest of the
+package, this file checks arguments, allocates outputs and passes pointers; the contracts are in
+include/spec_verify.h.
+"""
+from __future__ import annotations
+
+import ctypes
+import math
+from dataclasses import dataclass
+from typing import Optional
+
+import torch
+
+from . import _lib
+
+_CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def _top():
+    import draft_verification_spec_gb300 as m
+    return m
+
+
+def _stream(stream):
+    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+
+
+def _on(dev, *named):
+    """Every (tensor, name) is a CUDA tensor of `dev`, which is the current device."""
+    if dev.type != "cuda":
+        raise ValueError(f"{named[0][1]} must be a CUDA tensor")
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"{named[0][1]} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+    for t, name in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+
+
+def _int32(t, name, dim):
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1) or (dim == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]):
+        raise ValueError(f"{name} must be a {dim}-dimensional tensor with contiguous rows")
+
+
+def _heads(t, name, n=None, dim=None):
+    """A [tokens, heads, dim] tensor whose heads are contiguous."""
+    if t.dim() != 3 or (n is not None and t.shape[0] != n) or (dim is not None and t.shape[2] != dim):
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(t.shape)}")
+    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+        raise ValueError(f"{name}: the values of a head must be contiguous")
+
+
+def _batch(k_cache, v_cache, page_table, kv_lens, cu_q, tokens, kv_heads, dim, dtype):
+    _int32(kv_lens, "kv_lens", 1)
+    _int32(cu_q, "cu_q", 1)
+    B = kv_lens.shape[0]
+    if cu_q.shape[0] != B + 1:
+        raise ValueError(f"cu_q has {cu_q.shape[0]} entries, expected {B + 1}")
+    c = _lib.PagedBatch()
+    c.batch, c.tokens, c.kv_heads, c.dim = B, tokens, kv_heads, dim
+    c.kv_lens, c.cu_q = kv_lens.data_ptr(), cu_q.data_ptr()
+    if k_cache is None:
+        return c
+    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.dim() != 4 or t.shape != k_cache.shape or t.shape[2] != kv_heads or t.shape[3] != dim:
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [pages, page_size, {kv_heads}, {dim}]")
+        if t.stride(3) != 1 and dim > 1:
+            raise ValueError(f"{name}: the values of a head must be contiguous")
+    _int32(page_table, "page_table", 2)
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table has {page_table.shape[0]} rows, expected {B}")
+    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
+    c.k_page, c.k_token, c.k_head, _ = k_cache.stride()
+    c.v_page, c.v_token, c.v_head, _ = v_cache.stride()
+    c.pages, c.page_size = k_cache.shape[0], k_cache.shape[1]
+    c.page_table, c.table_width = page_table.data_ptr(), page_table.shape[1]
+    c.table_stride = max(page_table.stride(0), page_table.shape[1])
+    return c
+
+
+_ws_bytes: dict = {}
+
+
+def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, *, causal: bool = True,
+                    window: int = 0, scale: Optional[float] = None, want_lse: bool = False, out=None, stream=None,
+                    workspace=None):
+    """Attention of the new tokens q [tokens, q_heads, dim] over the paged cache (spec_chunk_attention).
+
+    ``max_q`` bounds the new tokens of a request.  ``causal``: a token sees the keys up to its own;
+    otherwise all of its request.  ``window`` > 0: only keys within that many positions back, its
+    own included.  ``scale`` defaults to dim ** -0.5.  Returns out [tokens, q_heads, dim], with
+    ``want_lse`` (out, lse [tokens, q_heads] float32); a row that sees no key gives 0 and -inf.
+    """
+    m = _top()
+    code = _CODES.get(q.dtype)
+    if code not in (1, 2):
+        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
+    _heads(q, "q")
+    dev = q.device
+    _on(dev, (q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"), (kv_lens, "kv_lens"),
+        (cu_q, "cu_q"), (out, "out"))
+    n, hq, d = q.shape
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [pages, page_size, kv_heads, dim]")
+    hkv = k_cache.shape[2]
+    c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, hkv, d, q.dtype)
+    if out is None:
+        out = torch.empty(n, hq, d, dtype=q.dtype, device=dev)
+        if stream is not None:
+            out.record_stream(stream)
+    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
+    lse = None
+    if want_lse:
+        lse = torch.empty(n, hq, dtype=torch.float32, device=dev)
+        if stream is not None:
+            lse.record_stream(stream)
+    key = (dev.index, code, hq, hkv, d, int(max_q))
+    need = _ws_bytes.get(key)
+    if need is None:
+        need = _ws_bytes[key] = int(m.lib().spec_attention_workspace_bytes(code, hq, hkv, d, int(max_q)))
+    ws = workspace or m.default_workspace(stream)
+    buf = ws.get_step(need, stream)
+    m._check(m.lib().spec_chunk_attention(q.data_ptr(), q.stride(0), q.stride(1), code, hq, ctypes.byref(c), int(max_q),
+                                          d ** -0.5 if scale is None else float(scale), int(causal), int(window),
+                                          out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(),
+                                          buf.numel(), _stream(stream)), "spec_chunk_attention")
+    return (out, lse) if want_lse else out
+
+
+class RopePlan:
+    """Rotation frequencies of the rotary positions: theta^(-2j/r) turns of 2 pi a position for the r/2 pairs
+    of the first r = ``rotary_dim`` values of a head, as 64-bit fractions of a turn on the device.
+
+    layout: "half" pairs (j, j + r/2), "interleaved" pairs (2j, 2j + 1).
+    scaling (for contexts longer than the trained one):
+      {"type": "linear", "factor": s}  every frequency / s;
+      {"type": "ntk", "factor": s}     theta s^(r / (r - 2)), which divides the slowest frequency by s and
+                                       keeps the fastest;
+      {"type": "yarn", "factor": s, "original": L, "beta_fast": 32, "beta_slow": 1, "attention_factor": None}
+        frequencies with more than beta_fast turns over the trained length L stay, those with less than
+        beta_slow are divided by s, a ramp over the pairs' index between; rotated values are multiplied by
+        attention_factor (0.1 ln s + 1).
+    """
+
+    def __init__(self, head_dim: int, rotary_dim: Optional[int] = None, theta: float = 10000.0, layout: str = "half",
+                 scaling: Optional[dict] = None, device=None):
+        r = head_dim if rotary_dim is None else int(rotary_dim)
+        if r < 2 or r % 2 or r > head_dim:
+            raise ValueError(f"rotary_dim must be even, in [2, {head_dim}], got {r}")
+        if layout not in ("half", "interleaved"):
+            raise ValueError(f"layout must be 'half' or 'interleaved', got {layout!r}")
+        if not theta > 0:
+            raise ValueError("theta must be positive")
+        self.head_dim, self.rotary_dim, self.theta, self.layout = int(head_dim), r, float(theta), layout
+        self.frequencies, self.factor = self._frequencies(r, float(theta), scaling)
+        turns = [int(round(f / (2.0 * math.pi) * 2.0 ** 64)) % 2 ** 64 for f in self.frequencies]
+        signed = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        self.turns = torch.tensor(signed, dtype=torch.int64, device=device)
+
+    @staticmethod
+    def _frequencies(r, theta, scaling):
+        base = [theta ** (-2.0 * j / r) for j in range(r // 2)]
+        if scaling is None:
+            return base, 1.0
+        kind, s = scaling.get("type"), float(scaling.get("factor", 0.0))
+        if not s > 0:
+            raise ValueError("scaling needs a positive factor")
+        if kind == "linear":
+            return [f / s for f in base], 1.0
+        if kind == "ntk":
+            if r < 4:
+                raise ValueError("ntk scaling needs rotary_dim >= 4")
+            t = theta * s ** (r / (r - 2.0))
+            return [t ** (-2.0 * j / r) for j in range(r // 2)], 1.0
+        if kind == "yarn":
+            L = float(scaling["original"])
+
+            def pair(turns):   # the (fractional) pair that makes this many turns over L positions
+                return r * math.log(L / (turns * 2.0 * math.pi)) / (2.0 * math.log(theta))
+
+            lo = max(0, math.floor(pair(float(scaling.get("beta_fast", 32.0)))))
+            hi = min(r - 1, math.ceil(pair(float(scaling.get("beta_slow", 1.0)))))
+            out = []
+            for j, f in enumerate(base):
+                ramp = min(max((j - lo) / max(hi - lo, 1e-3), 0.0), 1.0)
+                out.append(f / s * ramp + f * (1.0 - ramp))
+            m = scaling.get("attention_factor")
+            return out, (0.1 * math.log(s) + 1.0 if s > 1 else 1.0) if m is None else float(m)
+        raise ValueError(f"unknown scaling type {kind!r}")
+
+
+def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, cu_q, *, q_out=None, k_out=None,
+                stream=None, workspace=None):
+    """Rotary positions of the new tokens and the write of rotated keys and values into the paged cache
+    (spec_rope_append).
+
+    q [tokens, q_heads, dim], k and v [tokens, kv_heads, dim], float32, bfloat16 or float16.  Returns the
+    rotated queries (in ``q_out``, which may be q).  ``k_out`` receives the rotated keys too (may be k);
+    it is required where k_cache, v_cache and page_table are None and nothing is stored.
+    """
+    m = _top()
+    code = _CODES.get(q.dtype)
+    if code is None:
+        raise TypeError(f"q must be float32, bfloat16 or float16, got {q.dtype}")
+    _heads(q, "q")
+    n, hq, d = q.shape
+    _heads(k, "k", n, d)
+    dev = q.device
+    _on(dev, (q, "q"), (k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"),
+        (kv_lens, "kv_lens"), (cu_q, "cu_q"), (q_out, "q_out"), (k_out, "k_out"), (rope.turns, "rope"))
+    if rope.head_dim != d:
+        raise ValueError(f"the plan is for heads of {rope.head_dim}, q has {d}")
+    if k.dtype != q.dtype:
+        raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
+    if k_cache is not None:
+        _heads(v, "v", n, d)
+        if v.dtype != q.dtype:
+            raise TypeError(f"v must be {q.dtype}, got {v.dtype}")
+        if v.shape[1] != k.shape[1]:
+            raise ValueError(f"v has {v.shape[1]} heads, k {k.shape[1]}")
+    elif k_out is None:
+        raise ValueError("k_out is required where there is no cache")
+    c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, k.shape[1], d, q.dtype)
+    if q_out is None:
+        q_out = torch.empty(n, hq, d, dtype=q.dtype, device=dev)
+        if stream is not None:
+            q_out.record_stream(stream)
+    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
+        if t is not None:
+            if t.shape != like.shape or t.dtype != like.dtype:
+                raise ValueError(f"{name} must have the shape and dtype of the tensor it holds")
+            _heads(t, name)
+    r = _lib.RopeTensors()
+    r.q, r.k, r.q_out = q.data_ptr(), k.data_ptr(), q_out.data_ptr()
+    r.q_token, r.q_head, _ = q.stride()
+    r.k_token, r.k_head, _ = k.stride()
+    r.q_out_token, r.q_out_head, _ = q_out.stride()
+    ws = None
+    if k_cache is not None:
+        r.v = v.data_ptr()
+        r.v_token, r.v_head, _ = v.stride()
+        ws = (workspace or m.default_workspace(stream)).get_step(256, stream).data_ptr()
+    if k_out is not None:
+        r.k_out = k_out.data_ptr()
+        r.k_out_token, r.k_out_head, _ = k_out.stride()
+    m._check(m.lib().spec_rope_append(ctypes.byref(r), code, hq, ctypes.byref(c), rope.turns.data_ptr(), rope.rotary_dim,
+                                      rope.factor, int(rope.layout == "interleaved"), ws, _stream(stream)),
+             "spec_rope_append")
+    return q_out
+
+
+@dataclass
+class SampleOutput:
+    tokens: torch.Tensor                     # [rows] int32; -1 for a row without a logit above -inf
+    probs: torch.Tensor                      # [rows] float32: the token's probability among the kept ones
+    kept: torch.Tensor                       # [rows] int32: how many tokens the filters keep
+    filtered: Optional[torch.Tensor] = None  # [rows, V]: the kept tokens' logits, -inf elsewhere
+
+
+def _setting(c, name, value, dtype, rows, dev):
+    if isinstance(value, torch.Tensor):
+        if value.device != dev:
+            raise ValueError(f"{name} is on {value.device}, expected {dev}")
+        if value.dtype != dtype or tuple(value.shape) != (rows,) or not value.is_contiguous():
+            raise ValueError(f"{name} must be a number or a contiguous {dtype} tensor of {rows}")
+        setattr(c, name + "_rows", value.data_ptr())
+    else:
+        setattr(c, name, value)
+
+
+def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, want_filtered: bool = False,
+                  stream=None, out: Optional[SampleOutput] = None) -> SampleOutput:
+    """Temperature, top-k, top-p and min-p sampling from given uniforms (spec_sample_tokens).
+
+    logits [rows, V] bfloat16 or float32 (rows may be strided), uniforms [rows] float32.  Each setting is
+    a number or a tensor of one per row (float32, top_k int32); top_k <= 0, top_p >= 1 and min_p <= 0 keep
+    all, temperature 0 is greedy.  With ``want_filtered`` the truncated logits come too: what
+    verify_chain / verify_block take as the distribution that the token was drawn from.
+    """
+    m = _top()
+    if logits.dim() != 2:
+        raise ValueError("logits must be [rows, V]")
+    code = _CODES.get(logits.dtype)
+    if code not in (0, 1):
+        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    R, V = logits.shape
+    dev = logits.device
+    _on(dev, (logits, "logits"), (uniforms, "uniforms"))
+    if (V > 1 and logits.stride(1) != 1) or (R > 1 and logits.stride(0) < V):
+        raise ValueError("logits: the values of a row must be contiguous, and rows must not overlap")
+    if uniforms.dtype != torch.float32 or tuple(uniforms.shape) != (R,) or not uniforms.is_contiguous():
+        raise ValueError(f"uniforms must be a contiguous float32 tensor of {R}")
+    c = _lib.Sampling()
+    _setting(c, "temperature", temperature, torch.float32, R, dev)
+    _setting(c, "top_k", top_k, torch.int32, R, dev)
+    _setting(c, "top_p", top_p, torch.float32, R, dev)
+    _setting(c, "min_p", min_p, torch.float32, R, dev)
+    if out is None:
+        out = SampleOutput(torch.empty(R, dtype=torch.int32, device=dev), torch.empty(R, dtype=torch.float32, device=dev),
+                           torch.empty(R, dtype=torch.int32, device=dev),
+                           torch.empty(R, V, dtype=logits.dtype, device=dev) if want_filtered else None)
+        if stream is not None:
+            for t in (out.tokens, out.probs, out.kept, out.filtered):
+                if t is not None:
+                    t.record_stream(stream)
+    else:
+        for t, name, dtype in ((out.tokens, "tokens", torch.int32), (out.probs, "probs", torch.float32),
+                               (out.kept, "kept", torch.int32)):
+            if t.dtype != dtype or tuple(t.shape) != (R,) or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"out.{name} must be a contiguous {dtype} tensor of {R} on {dev}")
+        f = out.filtered
+        if f is not None and (f.dtype != logits.dtype or f.shape != logits.shape or f.device != dev or
+                              (V > 1 and f.stride(1) != 1) or (R > 1 and f.stride(0) < V)):
+            raise ValueError("out.filtered must have the shape, dtype and device of logits and contiguous rows")
+    f = out.filtered
+    m._check(m.lib().spec_sample_tokens(logits.data_ptr(), max(logits.stride(0), V), code, R, V, uniforms.data_ptr(),
+                                        ctypes.byref(c), out.tokens.data_ptr(), out.probs.data_ptr(),
+                                        out.kept.data_ptr(), None if f is None else f.data_ptr(),
+                                        V if f is None else max(f.stride(0), V), _stream(stream)), "spec_sample_tokens")
+    return out
+
+
+__all__ = ["RopePlan", "SampleOutput", "chunk_attention", "rope_append", "sample_tokens"]

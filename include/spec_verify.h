@@ -64,10 +64,12 @@ typedef enum {
   SPEC_ERR_CUDA = 3,            /* a launch or runtime call failed */
   SPEC_ERR_DEVICE_TIMEOUT = 4,  /* a bounded on-device wait ran out */
   SPEC_ERR_TOKEN_RANGE = 5,     /* a draft token id outside [0, V) */
-  SPEC_ERR_WORKSPACE = 6        /* workspace too small or misaligned */
+  SPEC_ERR_WORKSPACE = 6,       /* workspace too small or misaligned */
+  SPEC_ERR_PAGE_RANGE = 7       /* a page id outside the cache, or a position beyond the page table */
 } spec_status_t;
 
-typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1 } spec_dtype_t;
+/* SPEC_F16: rope and attention only. */
+typedef enum { SPEC_F32 = 0, SPEC_BF16 = 1, SPEC_F16 = 2 } spec_dtype_t;
 
 /* Library version (major*10000 + minor*100 + patch). */
 int spec_version(void);
@@ -83,9 +85,9 @@ spec_status_t spec_workspace_init(void* workspace, size_t ws_bytes, void* stream
 
 /*
  * Read and clear the device status word of a workspace.  Synchronises
- * `stream`.  *out_status receives SPEC_OK, SPEC_ERR_TOKEN_RANGE or
- * SPEC_ERR_DEVICE_TIMEOUT (the first two bits found, in that priority:
- * timeout first).  After SPEC_ERR_DEVICE_TIMEOUT re-initialise the
+ * `stream`.  *out_status receives SPEC_OK, SPEC_ERR_DEVICE_TIMEOUT,
+ * SPEC_ERR_TOKEN_RANGE or SPEC_ERR_PAGE_RANGE (the first of them found, in
+ * that priority).  After SPEC_ERR_DEVICE_TIMEOUT re-initialise the
  * workspace before reuse.
  */
 spec_status_t spec_get_status(void* workspace, void* stream, int32_t* out_status);
@@ -299,6 +301,148 @@ spec_status_t spec_verify_tuned(const void* target_logits, const void* draft_log
                                 float* out_cum_alpha, float* out_expected_len, int32_t* out_depth,
                                 void* workspace, size_t ws_bytes, void* stream,
                                 const spec_tuning_t* tuning);
+
+/* ------------------------------------------------------------------------
+ * The operators around a verification: what produces the logits it reads and
+ * the tokens it tests.  One speculative step is
+ *   spec_sample_tokens  (the draft's tokens and their truncated logits)
+ *   spec_rope_append    (positions of the K + 1 new tokens, cache write)
+ *   spec_chunk_attention (the new tokens over the cache)
+ *   spec_sample_tokens with out_filtered (the target's truncated logits)
+ *   spec_verify_chain / spec_verify_block.
+ * A rejected draft needs no undoing: the next step's kv_lens are shorter and
+ * its tokens overwrite the slots.
+ */
+
+/*
+ * A batch of requests over a paged cache.  New token n of request b
+ * (cu_q[b] <= n < cu_q[b+1]) sits at position kv_lens[b] - (cu_q[b+1] - n)
+ * of its request, whose token t is in page page_table[b][t / page_size],
+ * slot t % page_size.  Device pointers; strides in elements, multiples of 16
+ * bytes, as are the bases of k and v; a head's `dim` values are contiguous
+ * (both [pages, page_size, heads, dim] and [pages, heads, page_size, dim]
+ * are described by their strides).  Lengths are read on the device only.
+ * kv_lens[b] counts the new tokens; 0 (an idle slot) and less than the
+ * number of new tokens are allowed: the tokens before position 0 see
+ * nothing and are not stored.  Lengths beyond table_width * page_size are
+ * cut to it.  Page ids are looked at only where a token is read or written;
+ * one outside [0, pages) reads as zeros, is not written, and sets
+ * SPEC_ERR_PAGE_RANGE in the status word.
+ */
+typedef struct spec_paged_batch {
+  void* k;
+  void* v;
+  long long k_page, k_token, k_head;
+  long long v_page, v_token, v_head;
+  int pages, page_size, kv_heads, dim;
+  const int32_t* page_table;     /* [batch, table_width], rows table_stride apart */
+  long long table_stride;
+  int table_width;
+  int batch;
+  const int32_t* kv_lens;        /* [batch] */
+  const int32_t* cu_q;           /* [batch + 1], from 0, not decreasing */
+  int tokens;                    /* new tokens: cu_q[batch] */
+} spec_paged_batch_t;
+
+/*
+ * Workspace of spec_chunk_attention (256-byte aligned; status word first, so
+ * spec_workspace_init and spec_get_status apply; nothing else in it outlives
+ * a call).  Depends on the current device; 0 for sizes that are refused.
+ */
+size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int dim, int max_q);
+
+/*
+ * Attention of the new tokens over the cache:
+ *   out[n, h] = sum_t softmax_t(scale q[n, h] . k[t, g]) v[t, g],
+ *   lse[n, h] = ln sum_t exp(scale q[n, h] . k[t, g]),  g = h / (q_heads / kv_heads)
+ * over the keys t < kv_lens[b] with, for causal != 0, t <= position of n and,
+ * for window > 0, t > position of n - window.  A row that sees no key gives
+ * out = 0, lse = -inf.  Keys and values at or beyond kv_lens[b] are never
+ * used (they may be anything); those before it must be finite.
+ *   q         [tokens, q_heads, dim] with strides (multiples of 16 bytes)
+ *   dtype     SPEC_BF16 or SPEC_F16, of q, k, v and out
+ *   max_q     an upper bound of the new tokens per request (chooses the
+ *             kernel; a wrong one costs speed, not results)
+ *   out       [tokens, q_heads, dim] contiguous, 16-byte aligned
+ *   out_lse   [tokens, q_heads] float32 or NULL
+ * dim a multiple of 8, at most 256; q_heads a multiple of kv_heads.
+ * Rows of tokens that no request has stay unwritten.  Results do not depend
+ * on timing.  Two launches, the second chained by programmatic dependent
+ * launch.
+ */
+spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
+                                   const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
+                                   void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream);
+
+/* New tokens of spec_rope_append; strides in elements, values of a head contiguous. */
+typedef struct spec_rope_tensors {
+  const void* q;        /* [tokens, q_heads, dim] */
+  const void* k;        /* [tokens, kv_heads, dim] */
+  const void* v;        /* [tokens, kv_heads, dim]; unused without a cache */
+  void* q_out;          /* rotated queries; may be q */
+  void* k_out;          /* rotated keys, or NULL (they go to the cache); may be k */
+  long long q_token, q_head, k_token, k_head, v_token, v_head;
+  long long q_out_token, q_out_head, k_out_token, k_out_head;
+} spec_rope_tensors_t;
+
+/*
+ * Rotary positions: of the first rotary_dim values of every head of q and k,
+ * pairs (x, y) = (j, j + rotary_dim/2), or (2j, 2j+1) if interleaved, become
+ *   factor (x cos a - y sin a), factor (y cos a + x sin a),
+ *   a = 2 pi position freq[j] / 2^64;
+ * the values behind them are copied.  Rotated keys and the values v go to the
+ * cache's slots (batch->k != NULL) and the rotated keys to k_out (if given).
+ *   freq      device uint64 [rotary_dim / 2]: turns a position x 2^64
+ *   dtype     SPEC_F32, SPEC_BF16 or SPEC_F16, of every tensor
+ *   workspace as spec_chunk_attention's (status word only); may be NULL
+ *             without a cache
+ * dim at most 1024.  One launch.
+ */
+spec_status_t spec_rope_append(const spec_rope_tensors_t* t, int dtype, int q_heads, const spec_paged_batch_t* batch,
+                               const unsigned long long* freq, int rotary_dim, float factor, int interleaved,
+                               void* workspace, void* stream);
+
+/* Sampling settings: a scalar each, or a device array of one per row where its pointer is not NULL. */
+typedef struct spec_sampling {
+  float temperature;             /* <= 0: greedy */
+  int top_k;                     /* <= 0: all */
+  float top_p;                   /* >= 1: all */
+  float min_p;                   /* <= 0: all */
+  const float* temperature_rows;
+  const int32_t* top_k_rows;
+  const float* top_p_rows;
+  const float* min_p_rows;
+} spec_sampling_t;
+
+/*
+ * Sampling from given uniforms.  A row's tokens are ordered by (logit
+ * descending, index ascending); w = exp((z - max) / temperature).  Kept are
+ * the first n = min(n_k, n_p, n_m), at least 1, of that order:
+ *   n_k  top_k;
+ *   n_p  the shortest prefix whose weight is >= top_p x the weight of the
+ *        first n_k;
+ *   n_m  the tokens with w >= min_p.
+ * The token drawn is the first whose inclusive prefix weight is strictly
+ * above uniforms[r] x the weight of the kept ones.  Temperature <= 0 (or
+ * NaN in an array) keeps the first token alone.
+ *   logits       [rows, V] SPEC_BF16 or SPEC_F32, rows row_stride apart
+ *   uniforms     [rows] float32 in [0, 1) (clamped to it)
+ *   out_tokens   [rows] int32; -1 for a row without a logit above -inf
+ *   out_probs    [rows] float32 or NULL: the drawn token's probability among
+ *                the kept ones (0 for such a row)
+ *   out_kept     [rows] int32 or NULL: n (0 for such a row)
+ *   out_filtered [rows, V] of the logits' type, rows filtered_stride apart,
+ *                or NULL: the kept tokens' logits, -inf elsewhere (what the
+ *                verification calls take as the truncated distribution); must
+ *                not overlap logits
+ * NaN logits count as -inf.  Sums are exact integers (weights in units of
+ * 2^-44), so results do not depend on timing.  V <= 262144.  One launch, no
+ * workspace.
+ */
+spec_status_t spec_sample_tokens(const void* logits, long long row_stride, int dtype, int rows, int V,
+                                 const float* uniforms, const spec_sampling_t* how, int32_t* out_tokens,
+                                 float* out_probs, int32_t* out_kept, void* out_filtered, long long filtered_stride,
+                                 void* stream);
 
 #ifdef __cplusplus
 }
