@@ -136,10 +136,14 @@ _workspaces: dict = {}
 
 def default_workspace(stream=None) -> Workspace:
     s = torch.cuda.current_stream() if stream is None else stream
-    key = (s.device.index if s.device.index is not None else torch.cuda.current_device(), s.cuda_stream)
+    return _workspace_of(s.device.index if s.device.index is not None else torch.cuda.current_device(), s.cuda_stream)
+
+
+def _workspace_of(index: int, raw_stream: int) -> Workspace:
+    key = (index, raw_stream)
     ws = _workspaces.get(key)
     if ws is None:
-        ws = Workspace(torch.device("cuda", key[0]))
+        ws = Workspace(torch.device("cuda", index))
         _workspaces[key] = ws
     return ws
 

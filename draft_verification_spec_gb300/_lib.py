@@ -20,31 +20,6 @@ class SpecTuning(ctypes.Structure):
     _fields_ = [("wait_limit_us", c_longlong), ("cluster", c_int), ("greedy_variant", c_int),
                 ("plan_out", c_void_p), ("split_event", c_void_p)]
 
-
-class PagedBatch(ctypes.Structure):
-    """spec_paged_batch_t: a batch of requests over a paged cache."""
-    _fields_ = [("k", c_void_p), ("v", c_void_p),
-                ("k_page", c_longlong), ("k_token", c_longlong), ("k_head", c_longlong),
-                ("v_page", c_longlong), ("v_token", c_longlong), ("v_head", c_longlong),
-                ("pages", c_int), ("page_size", c_int), ("kv_heads", c_int), ("dim", c_int),
-                ("page_table", c_void_p), ("table_stride", c_longlong), ("table_width", c_int), ("batch", c_int),
-                ("kv_lens", c_void_p), ("cu_q", c_void_p), ("tokens", c_int)]
-
-
-class RopeTensors(ctypes.Structure):
-    """spec_rope_tensors_t."""
-    _fields_ = [(n, c_void_p) for n in ("q", "k", "v", "q_out", "k_out")] + \
-               [(n, c_longlong) for n in ("q_token", "q_head", "k_token", "k_head", "v_token", "v_head",
-                                          "q_out_token", "q_out_head", "k_out_token", "k_out_head")]
-
-
-class Sampling(ctypes.Structure):
-    """spec_sampling_t."""
-    _fields_ = [("temperature", c_float), ("top_k", c_int), ("top_p", c_float), ("min_p", c_float),
-                ("temperature_rows", c_void_p), ("top_k_rows", c_void_p), ("top_p_rows", c_void_p),
-                ("min_p_rows", c_void_p)]
-
-
 # name -> (restype, argtypes), mirroring include/spec_verify.h
 SIGNATURES = {
     "spec_version": (c_int, []),

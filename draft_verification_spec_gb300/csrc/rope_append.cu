@@ -47,10 +47,10 @@ __device__ __forceinline__ float2 phase_cs(unsigned long long phase) {
   return make_float2(c, s);
 }
 
-// One CTA per token: the token's request and cache slot, its r/2 angles in shared memory, then every
+// Any size, alignment and stride: one CTA per token: the token's request and cache slot, its r/2 angles in shared memory, then every
 // head's values, 1 pair (or 1 value behind the rotated part) per thread and step.
 template <int DTYPE>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(const RopeParams p) {
   using T = typename RopeType<DTYPE>::T;
   extern __shared__ float2 cs[];   // [rotary / 2]
   __shared__ int s_b;
@@ -118,14 +118,198 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p) 
     }
 }
 
+
+constexpr int kRopeMaxTokens = 8;   // tokens per CTA: one warp each finds the request and the slot
+
+// Largest b with cu[b] <= n, by a 32-way search of one warp (-1: none).
+__device__ __forceinline__ int request_of(const int32_t* cu, int B, int n, int lane) {
+  int lo = -1, hi = B + 1;   // cu[lo] <= n < cu[hi], with cu[-1] = -inf and cu[B + 1] = +inf
+  while (hi - lo > 1) {
+    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+    const bool le = at < hi && __ldg(cu + at) <= n;
+    const int k = __popc(__ballot_sync(0xffffffffu, le));
+    const int nlo = lo + k * step;
+    hi = min(hi, nlo + step);
+    lo = nlo;
+  }
+  return lo;
+}
+
+// 16-byte pieces of VEC values; V of a token's pieces are pairs of pieces (half layout), single
+// pieces of pairs (interleaved), or copies.
+template <int DTYPE>
+struct Piece {
+  using T = typename RopeType<DTYPE>::T;
+  static constexpr int VEC = 16 / sizeof(T);
+  uint4 raw;
+  __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<uint4*>(p) = raw; }
+  __device__ __forceinline__ float get(int i) const { return to_f(reinterpret_cast<const T*>(&raw)[i]); }
+  __device__ __forceinline__ void put(int i, float x) { from_f(x, reinterpret_cast<T*>(&raw) + i); }
+};
+
+// The fast form: heads, halves and strides are whole 16-byte pieces.  A CTA takes `per_cta` tokens:
+// a warp each looks up the request, position and cache slot; the CTA computes the tokens' angles once
+// for all heads; then each thread moves 16-byte pieces (a piece and its partner in the half layout),
+// the next pieces' loads issued ahead of the current ones' stores.
+// Bound: HBM (2 x (q + k + v) bytes, no reuse).
+template <int DTYPE, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int per_cta) {
+  using T = typename RopeType<DTYPE>::T;
+  using Pc = Piece<DTYPE>;
+  constexpr int VEC = Pc::VEC;
+  extern __shared__ float2 s_cs[];   // [per_cta][rotary / 2]
+  __shared__ long long s_k[kRopeMaxTokens], s_v[kRopeMaxTokens];
+  __shared__ int s_pos[kRopeMaxTokens], s_req[kRopeMaxTokens];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n0 = blockIdx.x * per_cta, tokens = min(per_cta, p.c.N - n0);
+  const int half = p.rotary / 2, D = p.c.D, Hk = p.c.Hkv;
+  const int turn = (INTERLEAVED ? p.rotary : half) / VEC;   // rotated units per head
+  const int per_head = turn + (D - p.rotary) / VEC;
+  const int rot_units = (p.Hq + Hk) * per_head;
+  const int units = rot_units + (p.c.k ? Hk * (D / VEC) : 0);   // per token
+  const int total = tokens * units;
+
+  struct Unit {
+    Pc a, b;
+    T *d0, *d1;
+    int t, kind, at;   // kind 0: rotate, 1: copy
+  };
+  auto load = [&](int u, Unit& x) {
+    x.t = u / units;
+    int r = u - x.t * units;
+    const long long n = n0 + x.t;
+    const T* src;
+    if (r < rot_units) {
+      const int h = r / per_head, j = r - h * per_head, hk = h - p.Hq;
+      x.kind = j < turn ? 0 : 1;
+      x.at = j < turn ? j * VEC : p.rotary + (j - turn) * VEC;
+      src = hk < 0 ? reinterpret_cast<const T*>(p.q) + n * p.q_token + h * p.q_head
+                   : reinterpret_cast<const T*>(p.k) + n * p.k_token + hk * p.k_head;
+      x.d0 = hk < 0 ? reinterpret_cast<T*>(p.q_out) + n * p.qo_token + h * p.qo_head
+                    : (p.k_out ? reinterpret_cast<T*>(p.k_out) + n * p.ko_token + hk * p.ko_head : nullptr);
+      x.d1 = hk < 0 || !p.c.k ? nullptr : reinterpret_cast<T*>(p.c.k) + hk * p.c.k_head;
+      x.a.load(src + x.at);
+      if (!INTERLEAVED && x.kind == 0) x.b.load(src + x.at + half);
+    } else {
+      r -= rot_units;
+      const int h = r / (D / VEC), j = r - h * (D / VEC);
+      x.kind = 2;
+      x.at = j * VEC;
+      x.d0 = nullptr;
+      x.d1 = reinterpret_cast<T*>(p.c.v) + h * p.c.v_head;
+      x.a.load(reinterpret_cast<const T*>(p.v) + n * p.v_token + h * p.v_head + x.at);
+    }
+  };
+  Unit cur;
+  int u = tid;
+  if (u < total) load(u, cur);   // in flight while the tokens' slots are looked up
+
+  for (int t = warp; t < tokens; t += kRopeThreads / 32) {
+    const int n = n0 + t, b = request_of(p.c.cu_q, p.c.B, n, lane);
+    if (lane == 0) {
+      long long ks = -1, vs = -1;
+      int pos = 0;
+      const bool has = b >= 0 && b < p.c.B;
+      if (has) {
+        pos = __ldg(p.c.kv_lens + b) - (__ldg(p.c.cu_q + b + 1) - n);
+        if (p.c.k && pos >= 0) {
+          const int col = pos / p.c.page_size, in = pos % p.c.page_size;
+          const int pg = col < p.c.table_width ? __ldg(p.c.table + b * p.c.table_stride + col) : -1;
+          if (pg < 0 || pg >= p.c.pages) {
+            atomicOr(p.status, kStatusPageRange);
+          } else {
+            ks = pg * p.c.k_page + in * p.c.k_token;
+            vs = pg * p.c.v_page + in * p.c.v_token;
+          }
+        }
+      }
+      s_k[t] = ks;
+      s_v[t] = vs;
+      s_pos[t] = pos;
+      s_req[t] = has;
+    }
+  }
+  __syncthreads();
+  for (int i = tid; i < tokens * half; i += kRopeThreads) {
+    const int t = i / half;
+    const float2 c = phase_cs(p.freq[i - t * half] * static_cast<unsigned long long>(static_cast<long long>(s_pos[t])));
+    s_cs[i] = make_float2(c.x * p.factor, c.y * p.factor);
+  }
+  __syncthreads();
+  while (u < total) {
+    Unit next;
+    const int un = u + kRopeThreads;
+    if (un < total) load(un, next);
+    if (s_req[cur.t]) {
+      const float2* cs = s_cs + cur.t * half;
+      if (cur.kind == 0) {
+        if (INTERLEAVED) {
+#pragma unroll
+          for (int i = 0; i < VEC; i += 2) {
+            const float2 c = cs[(cur.at + i) / 2];
+            const float x = cur.a.get(i), y = cur.a.get(i + 1);
+            cur.a.put(i, x * c.x - y * c.y);
+            cur.a.put(i + 1, y * c.x + x * c.y);
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < VEC; ++i) {
+            const float2 c = cs[cur.at + i];
+            const float x = cur.a.get(i), y = cur.b.get(i);
+            cur.a.put(i, x * c.x - y * c.y);
+            cur.b.put(i, y * c.x + x * c.y);
+          }
+        }
+      }
+      const long long slot = cur.kind == 2 ? s_v[cur.t] : s_k[cur.t];
+      const bool pair = !INTERLEAVED && cur.kind == 0;
+      if (cur.d0) {
+        cur.a.store(cur.d0 + cur.at);
+        if (pair) cur.b.store(cur.d0 + cur.at + half);
+      }
+      if (cur.d1 && slot >= 0) {
+        cur.a.store(cur.d1 + slot + cur.at);
+        if (pair) cur.b.store(cur.d1 + slot + cur.at + half);
+      }
+    }
+    cur = next;
+    u = un;
+  }
+}
+
 }  // namespace
 
 cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream) {
-  const dim3 grid(p.c.N), block(kRopeThreads);
-  const size_t smem = sizeof(float2) * (p.rotary / 2);
-  if (dtype == 0) rope_kernel<0><<<grid, block, smem, stream>>>(p);
-  if (dtype == 1) rope_kernel<1><<<grid, block, smem, stream>>>(p);
-  if (dtype == 2) rope_kernel<2><<<grid, block, smem, stream>>>(p);
+  const int vec = dtype == 0 ? 4 : 8, esz = dtype == 0 ? 4 : 2;
+  // whole 16-byte pieces: sizes, strides and bases
+  const long long strides[] = {p.q_token, p.q_head, p.k_token, p.k_head, p.qo_token, p.qo_head,
+                               p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0, p.c.k ? p.v_token : 0, p.c.k ? p.v_head : 0};
+  bool whole = p.c.D % vec == 0 && p.rotary % (p.interleaved ? vec : 2 * vec) == 0;
+  for (long long s : strides) whole = whole && s % vec == 0;
+  const void* bases[] = {p.q, p.k, p.c.k ? p.v : nullptr, p.q_out, p.k_out};
+  for (const void* b : bases) whole = whole && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
+  if (!whole) {
+    const dim3 grid(p.c.N), block(kRopeThreads);
+    const size_t smem = sizeof(float2) * (p.rotary / 2);
+    if (dtype == 0) rope_scalar_kernel<0><<<grid, block, smem, stream>>>(p);
+    if (dtype == 1) rope_scalar_kernel<1><<<grid, block, smem, stream>>>(p);
+    if (dtype == 2) rope_scalar_kernel<2><<<grid, block, smem, stream>>>(p);
+    return cudaGetLastError();
+  }
+  // few tokens: a CTA each; many: as many tokens a CTA as leave about a thousand units (four a thread)
+  const int units = (p.Hq + 2 * p.c.Hkv) * (p.c.D / vec);
+  int per = p.c.N <= 608 ? 1 : 2048 / (units > 0 ? units : 1);
+  per = per < 1 ? 1 : per > kRopeMaxTokens ? kRopeMaxTokens : per;
+  const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);
+  const size_t smem = sizeof(float2) * (p.rotary / 2) * per;
+  const int kind = dtype * 2 + (p.interleaved ? 1 : 0);
+  if (kind == 0) rope_kernel<0, false><<<grid, block, smem, stream>>>(p, per);
+  if (kind == 1) rope_kernel<0, true><<<grid, block, smem, stream>>>(p, per);
+  if (kind == 2) rope_kernel<1, false><<<grid, block, smem, stream>>>(p, per);
+  if (kind == 3) rope_kernel<1, true><<<grid, block, smem, stream>>>(p, per);
+  if (kind == 4) rope_kernel<2, false><<<grid, block, smem, stream>>>(p, per);
+  if (kind == 5) rope_kernel<2, true><<<grid, block, smem, stream>>>(p, per);
   return cudaGetLastError();
 }
 

@@ -14,16 +14,20 @@ include/spec_verify.h.
 """
 from __future__ import annotations
 
-import ctypes
 import math
+import struct
 from dataclasses import dataclass
 from typing import Optional
 
 import torch
 
-from . import _lib
-
 _CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+# the ABI's structures, packed in one go (a ctypes field costs as much as a check): native alignment
+_BATCH = struct.Struct("@PPqqqqqqiiiiPqiiPPi4x")     # spec_paged_batch_t
+_ROPE = struct.Struct("@PPPPPqqqqqqqqqq")            # spec_rope_tensors_t
+_SAMPLING = struct.Struct("@fiffPPPP")               # spec_sampling_t
 
 
 def _top():
@@ -31,19 +35,24 @@ def _top():
     return m
 
 
-def _stream(stream):
-    return (torch.cuda.current_stream() if stream is None else stream).cuda_stream
+def _raw_stream(stream, index):
+    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
 
 
-def _on(dev, *named):
-    """Every (tensor, name) is a CUDA tensor of `dev`, which is the current device."""
-    if dev.type != "cuda":
-        raise ValueError(f"{named[0][1]} must be a CUDA tensor")
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"{named[0][1]} is on {dev}, the current device is cuda:{torch.cuda.current_device()}")
+def _on(*named):
+    """Every (tensor, name) is on the current device; its index."""
+    index = torch.cuda.current_device()
     for t, name in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+        if t is not None and t.get_device() != index:
+            raise ValueError(f"{name} must be on the current device cuda:{index}, it is on {t.device}")
+    return index
+
+
+def _fresh(stream, *shape, dtype, device):
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream)
+    return t
 
 
 def _int32(t, name, dim):
@@ -67,28 +76,23 @@ def _batch(k_cache, v_cache, page_table, kv_lens, cu_q, tokens, kv_heads, dim, d
     B = kv_lens.shape[0]
     if cu_q.shape[0] != B + 1:
         raise ValueError(f"cu_q has {cu_q.shape[0]} entries, expected {B + 1}")
-    c = _lib.PagedBatch()
-    c.batch, c.tokens, c.kv_heads, c.dim = B, tokens, kv_heads, dim
-    c.kv_lens, c.cu_q = kv_lens.data_ptr(), cu_q.data_ptr()
     if k_cache is None:
-        return c
+        return _BATCH.pack(0, 0, 0, 0, 0, 0, 0, 0, 0, 0, kv_heads, dim, 0, 0, 0, B, kv_lens.data_ptr(), cu_q.data_ptr(), tokens)
     for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
         if t.dtype != dtype:
             raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
         if t.dim() != 4 or t.shape != k_cache.shape or t.shape[2] != kv_heads or t.shape[3] != dim:
             raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [pages, page_size, {kv_heads}, {dim}]")
-        if t.stride(3) != 1 and dim > 1:
-            raise ValueError(f"{name}: the values of a head must be contiguous")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    if (ks[3] != 1 or vs[3] != 1) and dim > 1:
+        raise ValueError("k_cache and v_cache: the values of a head must be contiguous")
     _int32(page_table, "page_table", 2)
-    if page_table.shape[0] != B:
-        raise ValueError(f"page_table has {page_table.shape[0]} rows, expected {B}")
-    c.k, c.v = k_cache.data_ptr(), v_cache.data_ptr()
-    c.k_page, c.k_token, c.k_head, _ = k_cache.stride()
-    c.v_page, c.v_token, c.v_head, _ = v_cache.stride()
-    c.pages, c.page_size = k_cache.shape[0], k_cache.shape[1]
-    c.page_table, c.table_width = page_table.data_ptr(), page_table.shape[1]
-    c.table_stride = max(page_table.stride(0), page_table.shape[1])
-    return c
+    rows, width = page_table.shape
+    if rows != B:
+        raise ValueError(f"page_table has {rows} rows, expected {B}")
+    return _BATCH.pack(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
+                       k_cache.shape[0], k_cache.shape[1], kv_heads, dim, page_table.data_ptr(),
+                       max(page_table.stride(0), width), width, B, kv_lens.data_ptr(), cu_q.data_ptr(), tokens)
 
 
 _ws_bytes: dict = {}
@@ -109,35 +113,29 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     if code not in (1, 2):
         raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
     _heads(q, "q")
-    dev = q.device
-    _on(dev, (q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"), (kv_lens, "kv_lens"),
-        (cu_q, "cu_q"), (out, "out"))
+    index = _on((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"), (kv_lens, "kv_lens"),
+                (cu_q, "cu_q"), (out, "out"))
     n, hq, d = q.shape
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, page_size, kv_heads, dim]")
     hkv = k_cache.shape[2]
     c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, hkv, d, q.dtype)
     if out is None:
-        out = torch.empty(n, hq, d, dtype=q.dtype, device=dev)
-        if stream is not None:
-            out.record_stream(stream)
+        out = _fresh(stream, n, hq, d, dtype=q.dtype, device=q.device)
     elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape and dtype")
-    lse = None
-    if want_lse:
-        lse = torch.empty(n, hq, dtype=torch.float32, device=dev)
-        if stream is not None:
-            lse.record_stream(stream)
-    key = (dev.index, code, hq, hkv, d, int(max_q))
+    lse = _fresh(stream, n, hq, dtype=torch.float32, device=q.device) if want_lse else None
+    key = (index, code, hq, hkv, d, max_q)
     need = _ws_bytes.get(key)
     if need is None:
         need = _ws_bytes[key] = int(m.lib().spec_attention_workspace_bytes(code, hq, hkv, d, int(max_q)))
-    ws = workspace or m.default_workspace(stream)
-    buf = ws.get_step(need, stream)
-    m._check(m.lib().spec_chunk_attention(q.data_ptr(), q.stride(0), q.stride(1), code, hq, ctypes.byref(c), int(max_q),
-                                          d ** -0.5 if scale is None else float(scale), int(causal), int(window),
-                                          out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(),
-                                          buf.numel(), _stream(stream)), "spec_chunk_attention")
+    raw = _raw_stream(stream, index)
+    buf = (workspace or m._workspace_of(index, raw)).get_step(need, stream)
+    q_token, q_head, _ = q.stride()
+    m._check(m.lib().spec_chunk_attention(q.data_ptr(), q_token, q_head, code, hq, c, max_q,
+                                          d ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
+                                          None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), raw),
+             "spec_chunk_attention")
     return (out, lse) if want_lse else out
 
 
@@ -220,9 +218,8 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
     _heads(q, "q")
     n, hq, d = q.shape
     _heads(k, "k", n, d)
-    dev = q.device
-    _on(dev, (q, "q"), (k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"),
-        (kv_lens, "kv_lens"), (cu_q, "cu_q"), (q_out, "q_out"), (k_out, "k_out"), (rope.turns, "rope"))
+    index = _on((q, "q"), (k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"),
+                (kv_lens, "kv_lens"), (cu_q, "cu_q"), (q_out, "q_out"), (k_out, "k_out"), (rope.turns, "rope"))
     if rope.head_dim != d:
         raise ValueError(f"the plan is for heads of {rope.head_dim}, q has {d}")
     if k.dtype != q.dtype:
@@ -237,30 +234,22 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
         raise ValueError("k_out is required where there is no cache")
     c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, k.shape[1], d, q.dtype)
     if q_out is None:
-        q_out = torch.empty(n, hq, d, dtype=q.dtype, device=dev)
-        if stream is not None:
-            q_out.record_stream(stream)
+        q_out = _fresh(stream, n, hq, d, dtype=q.dtype, device=q.device)
     for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
         if t is not None:
             if t.shape != like.shape or t.dtype != like.dtype:
                 raise ValueError(f"{name} must have the shape and dtype of the tensor it holds")
             _heads(t, name)
-    r = _lib.RopeTensors()
-    r.q, r.k, r.q_out = q.data_ptr(), k.data_ptr(), q_out.data_ptr()
-    r.q_token, r.q_head, _ = q.stride()
-    r.k_token, r.k_head, _ = k.stride()
-    r.q_out_token, r.q_out_head, _ = q_out.stride()
-    ws = None
-    if k_cache is not None:
-        r.v = v.data_ptr()
-        r.v_token, r.v_head, _ = v.stride()
-        ws = (workspace or m.default_workspace(stream)).get_step(256, stream).data_ptr()
-    if k_out is not None:
-        r.k_out = k_out.data_ptr()
-        r.k_out_token, r.k_out_head, _ = k_out.stride()
-    m._check(m.lib().spec_rope_append(ctypes.byref(r), code, hq, ctypes.byref(c), rope.turns.data_ptr(), rope.rotary_dim,
-                                      rope.factor, int(rope.layout == "interleaved"), ws, _stream(stream)),
-             "spec_rope_append")
+    raw = _raw_stream(stream, index)
+    stored = k_cache is not None
+    ws = (workspace or m._workspace_of(index, raw)).get_step(256, stream).data_ptr() if stored else None
+    qs, ks, vs = q.stride(), k.stride(), v.stride() if stored else (0, 0, 0)
+    qo, ko = q_out.stride(), (0, 0, 0) if k_out is None else k_out.stride()
+    r = _ROPE.pack(q.data_ptr(), k.data_ptr(), v.data_ptr() if stored else 0, q_out.data_ptr(),
+                   0 if k_out is None else k_out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qo[0], qo[1],
+                   ko[0], ko[1])
+    m._check(m.lib().spec_rope_append(r, code, hq, c, rope.turns.data_ptr(), rope.rotary_dim, rope.factor,
+                                      rope.layout == "interleaved", ws, raw), "spec_rope_append")
     return q_out
 
 
@@ -272,15 +261,15 @@ class SampleOutput:
     filtered: Optional[torch.Tensor] = None  # [rows, V]: the kept tokens' logits, -inf elsewhere
 
 
-def _setting(c, name, value, dtype, rows, dev):
-    if isinstance(value, torch.Tensor):
-        if value.device != dev:
-            raise ValueError(f"{name} is on {value.device}, expected {dev}")
-        if value.dtype != dtype or tuple(value.shape) != (rows,) or not value.is_contiguous():
-            raise ValueError(f"{name} must be a number or a contiguous {dtype} tensor of {rows}")
-        setattr(c, name + "_rows", value.data_ptr())
-    else:
-        setattr(c, name, value)
+def _setting(name, value, dtype, rows, index):
+    """(number, pointer) of a setting that is a number or a tensor of one per row."""
+    if not isinstance(value, torch.Tensor):
+        return value, 0
+    if value.get_device() != index:
+        raise ValueError(f"{name} must be a number or on the current device cuda:{index}, it is on {value.device}")
+    if value.dtype != dtype or tuple(value.shape) != (rows,) or not value.is_contiguous():
+        raise ValueError(f"{name} must be a number or a contiguous {dtype} tensor of {rows}")
+    return 0, value.data_ptr()
 
 
 def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, *, want_filtered: bool = False,
@@ -299,25 +288,20 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     if code not in (0, 1):
         raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
     R, V = logits.shape
-    dev = logits.device
-    _on(dev, (logits, "logits"), (uniforms, "uniforms"))
+    index, dev = _on((logits, "logits"), (uniforms, "uniforms")), logits.device
     if (V > 1 and logits.stride(1) != 1) or (R > 1 and logits.stride(0) < V):
         raise ValueError("logits: the values of a row must be contiguous, and rows must not overlap")
     if uniforms.dtype != torch.float32 or tuple(uniforms.shape) != (R,) or not uniforms.is_contiguous():
         raise ValueError(f"uniforms must be a contiguous float32 tensor of {R}")
-    c = _lib.Sampling()
-    _setting(c, "temperature", temperature, torch.float32, R, dev)
-    _setting(c, "top_k", top_k, torch.int32, R, dev)
-    _setting(c, "top_p", top_p, torch.float32, R, dev)
-    _setting(c, "min_p", min_p, torch.float32, R, dev)
+    t0, t1 = _setting("temperature", temperature, torch.float32, R, index)
+    k0, k1 = _setting("top_k", top_k, torch.int32, R, index)
+    p0, p1 = _setting("top_p", top_p, torch.float32, R, index)
+    m0, m1 = _setting("min_p", min_p, torch.float32, R, index)
+    c = _SAMPLING.pack(t0, k0, p0, m0, t1, k1, p1, m1)
     if out is None:
-        out = SampleOutput(torch.empty(R, dtype=torch.int32, device=dev), torch.empty(R, dtype=torch.float32, device=dev),
-                           torch.empty(R, dtype=torch.int32, device=dev),
-                           torch.empty(R, V, dtype=logits.dtype, device=dev) if want_filtered else None)
-        if stream is not None:
-            for t in (out.tokens, out.probs, out.kept, out.filtered):
-                if t is not None:
-                    t.record_stream(stream)
+        out = SampleOutput(_fresh(stream, R, dtype=torch.int32, device=dev), _fresh(stream, R, dtype=torch.float32, device=dev),
+                           _fresh(stream, R, dtype=torch.int32, device=dev),
+                           _fresh(stream, R, V, dtype=logits.dtype, device=dev) if want_filtered else None)
     else:
         for t, name, dtype in ((out.tokens, "tokens", torch.int32), (out.probs, "probs", torch.float32),
                                (out.kept, "kept", torch.int32)):
@@ -328,10 +312,10 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
                               (V > 1 and f.stride(1) != 1) or (R > 1 and f.stride(0) < V)):
             raise ValueError("out.filtered must have the shape, dtype and device of logits and contiguous rows")
     f = out.filtered
-    m._check(m.lib().spec_sample_tokens(logits.data_ptr(), max(logits.stride(0), V), code, R, V, uniforms.data_ptr(),
-                                        ctypes.byref(c), out.tokens.data_ptr(), out.probs.data_ptr(),
-                                        out.kept.data_ptr(), None if f is None else f.data_ptr(),
-                                        V if f is None else max(f.stride(0), V), _stream(stream)), "spec_sample_tokens")
+    m._check(m.lib().spec_sample_tokens(logits.data_ptr(), max(logits.stride(0), V), code, R, V, uniforms.data_ptr(), c,
+                                        out.tokens.data_ptr(), out.probs.data_ptr(), out.kept.data_ptr(),
+                                        None if f is None else f.data_ptr(), V if f is None else max(f.stride(0), V),
+                                        _raw_stream(stream, index)), "spec_sample_tokens")
     return out
 
 
