@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libspecverify.so")
 SOURCES = ["row_bf16.cu", "row_f32.cu", "budget_cut.cu", "draft_conf.cu", "api.cu", "static_scratch.cu",
-           "attention_mma_bf16.cu", "attention_mma_f16.cu", "attention.cu", "rope_append.cu", "sample_tokens.cu",
+           "attention_mma_bf16.cu", "attention_mma_f16.cu", "attention_tc_bf16.cu", "attention_tc_f16.cu",
+           "attention.cu", "rope_append.cu", "sample_tokens.cu",
            "step_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 

@@ -4,7 +4,7 @@
 #include <mutex>
 #include <tuple>
 
-#include "attention_mma.cuh"
+#include "attention_tc.cuh"
 
 namespace sv {
 
@@ -12,6 +12,10 @@ template <>
 const void* attn_mma_fn<true>(int dp, int bm);
 template <>
 const void* attn_mma_fn<false>(int dp, int bm);
+template <>
+const void* attn_tc_fn<true>(int dp);
+template <>
+const void* attn_tc_fn<false>(int dp);
 
 // One warp per row of the item that begins in CTA blockIdx.x's run and goes on in others': the
 // partials in key order, each scaled by 2^(its maximum - the largest).  fp32.
@@ -94,24 +98,82 @@ static cudaError_t resident(const void* fn, int threads, int smem, int* out) {
   return cudaSuccess;
 }
 
-cudaError_t attention_mma_plan(bool bf16, int rows, int D, int sms, AttnPlan* plan) {
-  plan->kind = rows <= 16 ? 0 : 1;
-  plan->bm = rows <= 16 ? 16 : 64;
-  plan->bn = kAttnBN;
+static const void* kernel_of(bool bf16, const AttnPlan& plan) {
+  if (plan.kind == 2) return bf16 ? attn_tc_fn<true>(plan.dp) : attn_tc_fn<false>(plan.dp);
+  return bf16 ? attn_mma_fn<true>(plan.dp, plan.bm) : attn_mma_fn<false>(plan.dp, plan.bm);
+}
+
+cudaError_t attention_plan(bool bf16, int kind, int D, int sms, AttnPlan* plan) {
+  plan->kind = kind;
+  plan->bm = kind == 0 ? 16 : kind == 1 ? 64 : kTcBM;
+  plan->bn = kind == 2 ? kTcBN : kAttnBN;
   plan->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
-  plan->smem = bf16 ? attn_mma_smem<true>(plan->dp, plan->bm) : attn_mma_smem<false>(plan->dp, plan->bm);
-  const void* fn = bf16 ? attn_mma_fn<true>(plan->dp, plan->bm) : attn_mma_fn<false>(plan->dp, plan->bm);
+  int threads = kAttnThreads;
+  if (kind == 2) {
+    plan->smem = plan->dp == 64 ? AttnTcGeom<64>::kSmem : AttnTcGeom<128>::kSmem;
+    threads = kTcThreads;
+  } else {
+    plan->smem = bf16 ? attn_mma_smem<true>(plan->dp, plan->bm) : attn_mma_smem<false>(plan->dp, plan->bm);
+  }
   int occ = 0;
-  const cudaError_t e = resident(fn, kAttnThreads, plan->smem, &occ);
-  plan->grid = sms * occ;
+  const cudaError_t e = resident(kernel_of(bf16, *plan), threads, plan->smem, &occ);
+  plan->grid = sms * (kind == 2 ? 1 : occ);   // the tcgen05 kernel takes all of an SM's TMEM
   return e;
 }
 
-cudaError_t launch_attention_mma(bool bf16, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream) {
-  const void* fn = bf16 ? attn_mma_fn<true>(plan.dp, plan.bm) : attn_mma_fn<false>(plan.dp, plan.bm);
+// The 16-row kernel where the rows of a request and key head fit one tile; the tcgen05 kernel where
+// they are more than 64, heads are of 64 to 128 values and pages are whole TMA boxes; else 64-row tiles.
+int attention_kind(int rows, int D, int page_size, float scale) {
+  if (rows <= 16) return 0;
+  const bool pow2 = (page_size & (page_size - 1)) == 0;
+  return rows > 64 && D >= 64 && D <= 128 && pow2 && page_size >= 8 && scale > 0.f ? 2 : 1;
+}
+
+// cuTensorMapEncodeTiled, looked up once through the runtime (the library does not link the driver).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                              const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+static EncodeFn encode_fn() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult r;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &r) != cudaSuccess ||
+        r != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// A cache [pages, heads, page_size, dim] as TMA sees it; boxes of 64 values x one page (128 tokens at most).
+static bool encode_cache(bool bf16, const PagedBatch& c, void* at, long long page, long long token, long long head,
+                         CUtensorMap* map) {
+  const EncodeFn fn = encode_fn();
+  if (!fn || page <= 0 || token <= 0 || head <= 0) return false;
+  const cuuint64_t dims[4] = {static_cast<cuuint64_t>(c.D), static_cast<cuuint64_t>(c.page_size),
+                              static_cast<cuuint64_t>(c.Hkv), static_cast<cuuint64_t>(c.pages)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(token) * 2, static_cast<cuuint64_t>(head) * 2,
+                                 static_cast<cuuint64_t>(page) * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(c.page_size < kTcBN ? c.page_size : kTcBN), 1, 1};
+  const cuuint32_t step[4] = {1, 1, 1, 1};
+  return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, at, dims, strides, box, step,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+bool attention_maps(bool bf16, const PagedBatch& c, AttnMaps* maps) {
+  static_assert(sizeof(CUtensorMap) == sizeof(maps->k), "a tensor map is 128 bytes");
+  return encode_cache(bf16, c, c.k, c.k_page, c.k_token, c.k_head, reinterpret_cast<CUtensorMap*>(maps->k)) &&
+         encode_cache(bf16, c, c.v, c.v_page, c.v_token, c.v_head, reinterpret_cast<CUtensorMap*>(maps->v));
+}
+
+cudaError_t launch_attention(bool bf16, const AttnPlan& plan, const AttnParams& p, const AttnMaps& maps, cudaStream_t stream) {
   AttnParams copy = p;
-  void* args[] = {&copy};
-  return cudaLaunchKernel(fn, dim3(plan.grid), dim3(kAttnThreads), args, plan.smem, stream);
+  AttnMaps m = maps;
+  void* tc[] = {m.k, m.v, &copy};
+  void* mma[] = {&copy};
+  return cudaLaunchKernel(kernel_of(bf16, plan), dim3(plan.grid), dim3(plan.kind == 2 ? kTcThreads : kAttnThreads),
+                          plan.kind == 2 ? tc : mma, plan.smem, stream);
 }
 
 cudaError_t launch_attention_combine(int dtype, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream) {

@@ -1,0 +1,12 @@
+// bf16 instances of the tcgen05 attention kernel.
+#include "attention_tc.cuh"
+
+namespace sv {
+
+template <>
+const void* attn_tc_fn<true>(int dp) {
+  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64>)
+                  : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128>);
+}
+
+}  // namespace sv

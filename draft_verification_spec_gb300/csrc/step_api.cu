@@ -14,6 +14,7 @@ namespace {
 
 constexpr size_t kStatusBytes = 256;
 constexpr int kMaxSampleV = 262144;
+constexpr long long kWaitNs = 2000000000ll;   // wall time per bounded on-device wait
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
@@ -87,9 +88,15 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
   int sms = 0;
   if (sm_count(&sms) != SPEC_OK) return 0;
   const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
-  sv::AttnPlan plan;
-  if (sv::attention_mma_plan(dtype == SPEC_BF16, static_cast<int>(rows < 1024 ? rows : 1024), dim, sms, &plan) != cudaSuccess) return 0;
-  return kStatusBytes + (partial_bytes(plan, dim) + 255) / 256 * 256;
+  size_t most = 0;   // over the kernels that rows and dim admit
+  for (int kind = 0; kind < 3; ++kind) {
+    if ((kind == 0) != (rows <= 16) || (kind == 2 && (rows <= 64 || dim < 64 || dim > 128))) continue;
+    sv::AttnPlan plan;
+    if (sv::attention_plan(dtype == SPEC_BF16, kind, dim, sms, &plan) != cudaSuccess) return 0;
+    const size_t n = partial_bytes(plan, dim);
+    most = n > most ? n : most;
+  }
+  return kStatusBytes + (most + 255) / 256 * 256;
 }
 
 spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
@@ -107,11 +114,14 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   if (!workspace || !aligned(workspace, 256)) return SPEC_ERR_WORKSPACE;
   int sms = 0;
   if ((st = sm_count(&sms)) != SPEC_OK) return st;
-  sv::AttnPlan plan;
+  const bool bf16 = dtype == SPEC_BF16;
   const int G = q_heads / batch->kv_heads;
   const long long rows = static_cast<long long>(max_q) * G;
-  if (sv::attention_mma_plan(dtype == SPEC_BF16, static_cast<int>(rows < 1024 ? rows : 1024), batch->dim, sms, &plan) != cudaSuccess)
-    return SPEC_ERR_CUDA;
+  sv::AttnMaps maps;
+  int kind = sv::attention_kind(static_cast<int>(rows < 1024 ? rows : 1024), batch->dim, batch->page_size, scale);
+  if (kind == 2 && !sv::attention_maps(bf16, internal_batch(*batch), &maps)) kind = 1;
+  sv::AttnPlan plan;
+  if (sv::attention_plan(bf16, kind, batch->dim, sms, &plan) != cudaSuccess) return SPEC_ERR_CUDA;
   if (ws_bytes < kStatusBytes + partial_bytes(plan, batch->dim)) return SPEC_ERR_WORKSPACE;
   sv::AttnParams p;
   std::memset(&p, 0, sizeof(p));
@@ -130,10 +140,11 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   p.status = reinterpret_cast<int32_t*>(ws);
   p.part_ml = reinterpret_cast<float*>(ws + kStatusBytes);
   p.part_o = p.part_ml + static_cast<size_t>(plan.grid) * 2 * plan.bm * 2;
-  p.min_units = 4;
+  p.min_units = 256 / plan.bn;   // a CTA of its own: 256 keys at least
+  p.wait_limit = kWaitNs;
   p.n_max = plan.grid;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (sv::launch_attention_mma(dtype == SPEC_BF16, plan, p, s) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (sv::launch_attention(bf16, plan, p, maps, s) != cudaSuccess) return SPEC_ERR_CUDA;
   return sv::launch_attention_combine(dtype, plan, p, s) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 

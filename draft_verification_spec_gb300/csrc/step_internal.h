@@ -48,8 +48,16 @@ struct AttnPlan {
   int bm, bn, grid, smem, dp;
 };
 
-cudaError_t launch_attention_mma(bool bf16, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream);
-cudaError_t attention_mma_plan(bool bf16, int rows, int D, int sms, AttnPlan* plan);
+// TMA descriptors of the two caches.
+struct AttnMaps {
+  alignas(64) uint8_t k[128];
+  alignas(64) uint8_t v[128];
+};
+
+int attention_kind(int rows, int D, int page_size, float scale);
+cudaError_t attention_plan(bool bf16, int kind, int D, int sms, AttnPlan* plan);
+bool attention_maps(bool bf16, const PagedBatch& c, AttnMaps* maps);   // false: TMA cannot describe the caches
+cudaError_t launch_attention(bool bf16, const AttnPlan& plan, const AttnParams& p, const AttnMaps& maps, cudaStream_t stream);
 cudaError_t launch_attention_combine(int dtype, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream);
 
 struct RopeParams {
