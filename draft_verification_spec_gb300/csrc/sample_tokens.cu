@@ -6,12 +6,21 @@
 //   top-p   of those, the shortest prefix whose weight reaches top_p x the weight of the k;
 //   min-p   the tokens with w >= min_p (the largest w is 1);
 // the kept ones are the first n = min of the three (at least one), and the drawn token is the first
-// whose inclusive prefix weight is strictly above u x the weight of the n.
+// whose inclusive prefix weight is strictly above u x the weight of the n.  Every question is "which
+// element of the order does a count or a weight reach".
 //
-// Every question is "which element of the order does a count or a weight reach", answered by a
-// descent over the digits of the logits' ordered keys: a histogram of counts and weights per digit,
-// then the digit that the target falls in, then the next one among the elements that match so far.
-// Equal logits are told apart by their index at the end.
+// One CTA per row.  A histogram over the 16 top bits of the logits (those of magnitude 2^-40 to 2^8,
+// in descending order, and zero: 12,290 bins) answers it: the non-empty bins, a few hundred to a few
+// thousand, become a list whose counts and weights are summed once over the block, and a question is
+// a search in those sums.  A bf16 bin is one value, so its weight is count x weight and the row needs
+// neither its maximum first nor an exponential per token.  An fp32 bin also sums its tokens' weights,
+// and the element is then found among the bin's own by the digits of its low 16 bits.
+// Rows with logits outside the bins' range (nothing sensible has them) go the general way: a descent
+// over all digits of the ordered keys, 11 bits at a time.
+// Equal logits are told apart by their index in a last ordered pass, which also writes the filtered row.
+//
+// Bound: shared-memory atomics of the histogram (one per token, at most a few of a warp's 32 falling
+// on one bin), then the last passes, which read the row from L2.
 #include <cuda_bf16.h>
 
 #include "sample_weight.cuh"
@@ -21,245 +30,580 @@ namespace sv {
 
 namespace {
 
-constexpr int kThreads = 1024;
-constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;
+constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;   // the general descent
+constexpr int kMagLow = (127 - 40) * 128, kMags = 48 * 128;   // magnitudes of the histogram, in 7-bit mantissa steps
+constexpr int kHist = 2 * kMags + 2;                      // positive, zero, negative, below -2^8
+constexpr int kZeroBin = kMags, kLowBin = kHist - 1;
 
 template <int DTYPE>
-__device__ __forceinline__ float row_logit(const void* row, int i) {
-  if (DTYPE == 1) return __uint_as_float(static_cast<unsigned>(__ldg(static_cast<const uint16_t*>(row) + i)) << 16);
-  return __ldg(static_cast<const float*>(row) + i);
+struct Geo;
+template <>
+struct Geo<1> {   // bf16: counts only
+  using Raw = uint16_t;
+  static constexpr int kThreads = 512, kVec = 8, kPer = 25;   // bins per thread: odd, so a warp's reads fall on distinct banks
+  static constexpr int kHistWords = kThreads * kPer;
+  static constexpr int kDigitWords = 0;                   // the general descent reuses the histogram
+};
+template <>
+struct Geo<0> {   // fp32: counts and weights
+  using Raw = uint32_t;
+  static constexpr int kThreads = 1024, kVec = 4, kPer = 13;
+  static constexpr int kHistWords = 3 * kThreads * kPer;
+  static constexpr int kDigitWords = 3 * kBins;
+};
+static_assert(Geo<1>::kThreads * Geo<1>::kPer >= kHist && Geo<0>::kThreads * Geo<0>::kPer >= kHist, "every bin has a thread");
+static_assert(Geo<1>::kHistWords >= 3 * kBins, "the general descent fits the histogram");
+
+template <int DTYPE>
+constexpr int smem_bytes() {
+  return 4 * (Geo<DTYPE>::kHistWords + Geo<DTYPE>::kDigitWords) + 2 * ((kHist + 7) / 8 * 8);
 }
-// Ordered key; NaN counts as -inf, which is never drawn.
-__device__ __forceinline__ uint32_t sample_key(float z) { return ord_key(z != z ? ninf() : z); }
-__device__ __forceinline__ float key_logit(uint32_t k) {
+
+template <int DTYPE>
+__device__ __forceinline__ float value_of(typename Geo<DTYPE>::Raw b) {
+  return __uint_as_float(DTYPE == 1 ? static_cast<uint32_t>(b) << 16 : static_cast<uint32_t>(b));
+}
+// Ordered key, right-aligned (16 or 32 bits); NaN counts as -inf, which is never drawn.
+template <int DTYPE>
+__device__ __forceinline__ uint32_t sample_key(float z) {
+  const uint32_t k = ord_key(z != z ? ninf() : z);
+  return DTYPE == 1 ? k >> 16 : k;
+}
+template <int DTYPE>
+__device__ __forceinline__ float key_value(uint32_t k) {
+  if (DTYPE == 1) k = k << 16 | (k & 0x8000u ? 0u : 0xffffu);
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-struct Prefix {
-  unsigned cnt;            // elements before the group in the order
-  unsigned long long mass;
-  uint32_t key;            // the group's key
+// Bin of a finite logit's 16 top bits; -1: not drawn (-inf, NaN); -2: outside the bins' range.
+template <int DTYPE>
+__device__ __forceinline__ int bin_of(typename Geo<DTYPE>::Raw b) {
+  const uint32_t top = DTYPE == 1 ? b : static_cast<uint32_t>(b) >> 16;
+  const int mag = top & 0x7fff, mi = mag - kMagLow;
+  const bool neg = top & 0x8000;
+  if (mi >= 0 && mi < kMags) return neg ? kZeroBin + 1 + mi : kZeroBin - 1 - mi;
+  if (mi < 0) return (DTYPE == 1 ? mag : static_cast<int>(b & 0x7fffffffu)) == 0 ? kZeroBin : -2;
+  const bool nan = DTYPE == 1 ? mag > 0x7f80 : (static_cast<uint32_t>(b) & 0x7fffffffu) > 0x7f800000u;
+  return nan || (neg && mag == 0x7f80) ? -1 : neg ? kLowBin : -2;
+}
+// A bin's value with the lowest magnitude (bf16: its value); its key's 16 top bits.
+__device__ __forceinline__ float bin_value(int bin) {
+  if (bin == kZeroBin) return 0.f;
+  const uint32_t top = bin < kZeroBin ? kMagLow + (kZeroBin - 1 - bin) : 0x8000u | (kMagLow + (bin - kZeroBin - 1));
+  return __uint_as_float(top << 16);
+}
+__device__ __forceinline__ uint32_t bin_key16(int bin) {
+  if (bin == kZeroBin) return 0x8000u;
+  return bin < kZeroBin ? 0x8000u | (kMagLow + (kZeroBin - 1 - bin)) : 0x7fffu & ~static_cast<uint32_t>(kMagLow + (bin - kZeroBin - 1));
+}
+
+// A row in units of one 16-byte piece: unit 0 is what lies before the first 16-byte boundary (possibly
+// nothing), the last one what lies behind the last.
+template <int DTYPE>
+struct Row {
+  using Raw = typename Geo<DTYPE>::Raw;
+  static constexpr int VEC = Geo<DTYPE>::kVec;
+  const Raw* p;
+  int V, head, units;
+  __device__ __forceinline__ Row(const void* base, int v) : p(static_cast<const Raw*>(base)), V(v) {
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 15u) / static_cast<int>(sizeof(Raw));
+    head = min(V, mis ? VEC - mis : 0);
+    units = 1 + (V - head + VEC - 1) / VEC;
+  }
+  __device__ __forceinline__ int first(int u) const { return u == 0 ? 0 : head + (u - 1) * VEC; }
+  __device__ __forceinline__ int count(int u) const { return u == 0 ? head : min(VEC, V - first(u)); }
+  // the unit's values; places beyond its count hold -inf
+  __device__ __forceinline__ void load(int u, Raw (&x)[VEC]) const {
+    const int i0 = first(u), n = count(u);
+    if (n == VEC && u > 0) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + i0));
+      memcpy(x, &v, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) x[e] = e < n ? __ldg(p + i0 + e) : static_cast<Raw>(DTYPE == 1 ? 0xff80u : 0xff800000u);
+    }
+  }
 };
 
-struct Smem {
-  unsigned long long tab[64];
-  unsigned cnt[kBins], lo[kBins], hi[kBins];
-  unsigned wcnt[32];
-  unsigned long long wmass[32];
-  float wmax[32];
-  Prefix found;
-  int token;
+struct Prefix {
+  unsigned cnt;            // tokens before the group in the order
+  unsigned long long mass;
+  uint32_t key;            // the group's key (or its place in the bins' list)
 };
+
+template <int NT>
+struct Shared {
+  unsigned long long tab[64];
+  unsigned long long wmass[32];
+  unsigned wcnt[32], wcnt2[32];
+  Prefix found;
+  float zmax;
+  int fallback, token;
+};
+
+// Block-wide exclusive prefix of (count, weight); the totals too.
+template <int NT>
+__device__ __forceinline__ void block_scan(unsigned& c, unsigned long long& m, unsigned* c_all, unsigned long long* m_all,
+                                           Shared<NT>& s) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  unsigned ic = c;
+  unsigned long long im = m;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned tc = __shfl_up_sync(0xffffffffu, ic, o);
+    const unsigned long long tm = __shfl_up_sync(0xffffffffu, im, o);
+    if (lane >= o) ic += tc, im += tm;
+  }
+  if (lane == 31) s.wcnt[warp] = ic, s.wmass[warp] = im;
+  __syncthreads();
+  unsigned bc = 0, tc = 0;
+  unsigned long long bm = 0, tm = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w == warp) bc = tc, bm = tm;
+    tc += s.wcnt[w];
+    tm += s.wmass[w];
+  }
+  c = bc + ic - c;
+  m = bm + im - m;
+  *c_all = tc;
+  *m_all = tm;
+  __syncthreads();
+}
+
+// Adds a weight to a pair of words; the carry goes up.
+__device__ __forceinline__ void add_weight(unsigned* lo, unsigned* hi, unsigned long long w) {
+  const unsigned l = static_cast<unsigned>(w);
+  const unsigned old = atomicAdd(lo, l);
+  const unsigned up = static_cast<unsigned>(w >> 32) + (old + l < old ? 1u : 0u);
+  if (up) atomicAdd(hi, up);
+}
 
 // Block-wide: the group of equal keys in which the order's count (BY_COUNT) or weight reaches `target`
-// (1 <= target <= the row's).
+// (1 <= target <= the row's), among the tokens whose key begins with at.key, `bits` bits being open.
 template <int DTYPE, bool BY_COUNT>
-__device__ Prefix descend(const void* row, int V, const WeightScale& ws, unsigned long long target, Smem& s) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  Prefix at = {0u, 0ull, 0u};
-  int bits = DTYPE == 1 ? 16 : 32;     // key bits still to be fixed
-  uint32_t fixed = 0;                  // the digits found so far, right-aligned
+__device__ Prefix descend(const Row<DTYPE>& row, const WeightScale& ws, unsigned long long target, Prefix at, int bits,
+                          unsigned* digits, Shared<Geo<DTYPE>::kThreads>& s) {
+  constexpr int NT = Geo<DTYPE>::kThreads, PER = kBins / NT, VEC = Geo<DTYPE>::kVec;
+  const int tid = threadIdx.x;
+  unsigned *cnt = digits, *lo = digits + kBins, *hi = digits + 2 * kBins;
   while (bits > 0) {
     const int digit = bits < kDigitBits ? bits : kDigitBits;
     bits -= digit;
-    for (int i = tid; i < kBins; i += kThreads) s.cnt[i] = s.lo[i] = s.hi[i] = 0u;
+    for (int i = tid; i < 3 * kBins; i += NT) digits[i] = 0u;
     __syncthreads();
-    for (int i = tid; i < V; i += kThreads) {
-      const float z = row_logit<DTYPE>(row, i);
-      uint32_t key = sample_key(z);
-      if (DTYPE == 1) key >>= 16;
-      if ((static_cast<unsigned long long>(key) >> (bits + digit)) != fixed || !(z > ninf())) continue;
-      const unsigned d = (key >> bits) & ((1u << digit) - 1u);
-      const unsigned long long w = weight_of(z, ws, s.tab);
-      atomicAdd(&s.cnt[d], 1u);
-      const unsigned lo = static_cast<unsigned>(w);
-      const unsigned old = atomicAdd(&s.lo[d], lo);
-      const unsigned up = static_cast<unsigned>(w >> 32) + (old + lo < old ? 1u : 0u);
-      if (up) atomicAdd(&s.hi[d], up);
+    for (int u = tid; u < row.units; u += NT) {
+      typename Row<DTYPE>::Raw x[VEC];
+      row.load(u, x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float z = value_of<DTYPE>(x[e]);
+        const uint32_t key = sample_key<DTYPE>(z);
+        if ((static_cast<unsigned long long>(key) >> (bits + digit)) != at.key || !(z > ninf())) continue;
+        const unsigned d = (key >> bits) & ((1u << digit) - 1u);
+        atomicAdd(&cnt[d], 1u);
+        add_weight(&lo[d], &hi[d], weight_of(z, ws, s.tab));
+      }
     }
     __syncthreads();
-    // thread t holds the bins 2t, 2t + 1 from the top; a block scan gives what lies before them
-    unsigned c[2];
-    unsigned long long m[2];
+    // thread t holds PER bins from the top
+    unsigned c[PER], bc = 0, all_c;
+    unsigned long long m[PER], bm = 0, all_m;
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int bin = kBins - 1 - (2 * tid + e);
-      c[e] = s.cnt[bin];
-      m[e] = (static_cast<unsigned long long>(s.hi[bin]) << 32) + s.lo[bin];
+    for (int e = 0; e < PER; ++e) {
+      const int bin = kBins - 1 - (PER * tid + e);
+      c[e] = cnt[bin];
+      m[e] = (static_cast<unsigned long long>(hi[bin]) << 32) + lo[bin];
+      bc += c[e];
+      bm += m[e];
     }
-    unsigned ic = c[0] + c[1];
-    unsigned long long im = m[0] + m[1];
+    block_scan<NT>(bc, bm, &all_c, &all_m, s);
+    bc += at.cnt;
+    bm += at.mass;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned tc = __shfl_up_sync(0xffffffffu, ic, o);
-      const unsigned long long tm = __shfl_up_sync(0xffffffffu, im, o);
-      if (lane >= o) ic += tc, im += tm;
-    }
-    if (lane == 31) s.wcnt[warp] = ic, s.wmass[warp] = im;
-    __syncthreads();
-    for (int k = 0; k < warp; ++k) ic += s.wcnt[k], im += s.wmass[k];
-    unsigned bc = at.cnt + ic - c[0] - c[1];
-    unsigned long long bm = at.mass + im - m[0] - m[1];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
+    for (int e = 0; e < PER; ++e) {
       const bool before = BY_COUNT ? bc < target : bm < target;
       const bool reached = BY_COUNT ? bc + c[e] >= target : bm + m[e] >= target;
-      if (before && reached) s.found = {bc, bm, static_cast<uint32_t>((fixed << digit) | (kBins - 1 - (2 * tid + e)))};
+      if (before && reached) s.found = {bc, bm, static_cast<uint32_t>((at.key << digit) | (kBins - 1 - (PER * tid + e)))};
       bc += c[e];
       bm += m[e];
     }
     __syncthreads();
     at = s.found;
-    fixed = at.key;
     __syncthreads();
   }
   return at;
 }
 
-// Block-wide sum of a count and a weight.
-__device__ void block_sum(unsigned& c, unsigned long long& m, Smem& s) {
-#pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    c += __shfl_xor_sync(0xffffffffu, c, o);
-    m += __shfl_xor_sync(0xffffffffu, m, o);
-  }
-  if ((threadIdx.x & 31) == 0) s.wcnt[threadIdx.x / 32] = c, s.wmass[threadIdx.x / 32] = m;
-  __syncthreads();
-  c = 0;
-  m = 0;
-  for (int k = 0; k < kThreads / 32; ++k) c += s.wcnt[k], m += s.wmass[k];
-  __syncthreads();
-}
-
 template <int DTYPE>
-__global__ void __launch_bounds__(kThreads) sample_kernel_row(const SampleParams p) {
-  extern __shared__ __align__(16) uint8_t raw[];
-  Smem& s = *reinterpret_cast<Smem*>(raw);
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, V = p.V;
-  const int esz = DTYPE == 1 ? 2 : 4;
-  const void* row = static_cast<const uint8_t*>(p.logits) + static_cast<long long>(r) * p.stride * esz;
-  if (tid < 64) s.tab[tid] = kExp2Table[tid];
-  // the row's largest logit
-  float mx = ninf();
-  for (int i = tid; i < V; i += kThreads) mx = fmaxf(mx, row_logit<DTYPE>(row, i));
-  mx = warp_max(mx);
-  if (lane == 0) s.wmax[tid / 32] = mx;
-  __syncthreads();
-  mx = warp_max(s.wmax[lane]);
-  __syncthreads();
+__global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) sample_kernel_row(const SampleParams p) {
+  using G = Geo<DTYPE>;
+  using Raw = typename G::Raw;
+  constexpr int NT = G::kThreads, VEC = G::kVec, PER = G::kPer, NW = NT / 32, SPAN = NT * PER;
+  extern __shared__ __align__(16) unsigned dyn[];
+  unsigned* hist = dyn;                                           // [SPAN] counts (fp32: then weights, low and high words)
+  unsigned* digits = DTYPE == 1 ? dyn : dyn + G::kHistWords;      // the general descent's
+  uint16_t* list = reinterpret_cast<uint16_t*>(dyn + G::kHistWords + G::kDigitWords);   // non-empty bins
+  __shared__ Shared<NT> s;
+  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Row<DTYPE> row(static_cast<const Raw*>(p.logits) + static_cast<long long>(r) * p.stride, p.V);
 
   float T = p.temperature ? p.temperature[r] : p.temperature0;
   int k = p.top_k ? p.top_k[r] : p.top_k0;
   const float top_p = p.top_p ? p.top_p[r] : p.top_p0, min_p = p.min_p ? p.min_p[r] : p.min_p0;
+  const float uniform = p.uniforms[r];
   if (!(T > 0.f)) {   // greedy: the first of the order
     T = 1.f;
     k = 1;
   }
-  const WeightScale ws = weight_scale(mx, T);
-  const unsigned long long least = min_p > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(min_p) * kWeightOne)) : 0ull;
+  if (tid < 64) s.tab[tid] = kExp2Table[tid];
+  if (tid == 0) s.fallback = 0;
+  const bool need_max = DTYPE == 0 || k == 1;
+  const bool filter = p.filtered != nullptr;
 
-  // finite tokens and their weight; those of at least min_p
-  unsigned n_all = 0, n_min = 0;
-  unsigned long long m_all = 0, m_min = 0;
-  for (int i = tid; i < V; i += kThreads) {
-    const float z = row_logit<DTYPE>(row, i);
-    if (!(z > ninf())) continue;
-    const unsigned long long w = weight_of(z, ws, s.tab);
-    ++n_all;
-    m_all += w;
-    if (w >= least) ++n_min, m_min += w;
-  }
-  block_sum(n_all, m_all, s);
-  block_sum(n_min, m_min, s);
-
-  unsigned n = 0;
-  unsigned long long mass = 0;
-  int token = -1;
-  float prob = 0.f;
-  Prefix cut = {0u, 0ull, 0u};
-  if (n_all > 0) {
-    n = n_all;
-    mass = m_all;
-    if (k > 0 && static_cast<unsigned>(k) < n) {
-      const Prefix g = descend<DTYPE, true>(row, V, ws, k, s);
-      n = k;
-      mass = g.mass + (k - g.cnt) * weight_of(key_logit(DTYPE == 1 ? g.key << 16 | (g.key & 0x8000u ? 0u : 0xffffu) : g.key), ws, s.tab);
-    }
-    if (top_p < 1.f) {
-      const double goal = ceil(fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(mass));
-      unsigned long long target = goal < 1.0 ? 1ull : static_cast<unsigned long long>(goal);
-      if (target > mass) target = mass;
-      const Prefix g = descend<DTYPE, false>(row, V, ws, target, s);
-      const unsigned long long w = weight_of(key_logit(DTYPE == 1 ? g.key << 16 | (g.key & 0x8000u ? 0u : 0xffffu) : g.key), ws, s.tab);
-      const unsigned in = static_cast<unsigned>((target - g.mass + w - 1) / w);
-      if (g.cnt + in < n) n = g.cnt + in, mass = g.mass + in * w;
-    }
-    if (min_p > 0.f && n_min < n) {
-      n = n_min > 0 ? n_min : 1;
-      mass = n_min > 0 ? m_min : kWeightOne;
-    }
-    // the draw
-    const float u = p.uniforms[r];
-    const double td = u > 0.f ? floor(static_cast<double>(u) * static_cast<double>(mass)) : 0.0;
-    unsigned long long t = td >= static_cast<double>(mass) ? mass - 1 : static_cast<unsigned long long>(td);
-    if (t >= mass) t = mass - 1;
-    const Prefix g = descend<DTYPE, false>(row, V, ws, t + 1, s);
-    const float z = key_logit(DTYPE == 1 ? g.key << 16 | (g.key & 0x8000u ? 0u : 0xffffu) : g.key);
-    const unsigned long long w = weight_of(z, ws, s.tab);
-    unsigned rank = static_cast<unsigned>((t + 1 - g.mass + w - 1) / w) - 1;   // among the equal ones
-    prob = static_cast<float>(static_cast<double>(w) / static_cast<double>(mass));
-    if (p.filtered) cut = descend<DTYPE, true>(row, V, ws, n, s);
-    // the rank-th token with that logit: contiguous shares, a scan of their counts
-    const int share = (V + kThreads - 1) / kThreads, i0 = min(V, tid * share), i1 = min(V, i0 + share);
-    unsigned mine = 0, eq_cut = 0;
-    const float zc = p.filtered ? key_logit(DTYPE == 1 ? cut.key << 16 | (cut.key & 0x8000u ? 0u : 0xffffu) : cut.key) : 0.f;
-    for (int i = i0; i < i1; ++i) {
-      const float x = row_logit<DTYPE>(row, i);
-      mine += x == z;
-      eq_cut += x == zc;
-    }
-    unsigned a = mine, e = eq_cut;
+  // the largest logit, where it is needed before the weights
+  float zmax = ninf();
+  if (need_max) {
+#pragma unroll 4
+    for (int u = tid; u < row.units; u += NT) {
+      Raw x[VEC];
+      row.load(u, x);
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned ta = __shfl_up_sync(0xffffffffu, a, o), te = __shfl_up_sync(0xffffffffu, e, o);
-      if (lane >= o) a += ta, e += te;
+      for (int e = 0; e < VEC; ++e) zmax = fmaxf(zmax, value_of<DTYPE>(x[e]));   // fmaxf drops NaN
     }
-    if (lane == 31) s.cnt[tid / 32] = a, s.lo[tid / 32] = e;
+    zmax = warp_max(zmax);
+    if (lane == 0) s.wmass[warp] = __float_as_uint(zmax);
     __syncthreads();
-    for (int q = 0; q < tid / 32; ++q) a += s.cnt[q], e += s.lo[q];
-    a -= mine;
-    e -= eq_cut;
-    if (rank >= a && rank < a + mine) {
-      unsigned left = rank - a;
-      for (int i = i0; i < i1; ++i)
-        if (row_logit<DTYPE>(row, i) == z && left-- == 0) {
-          s.token = i;
+    for (int w = 0; w < NW; ++w) zmax = fmaxf(zmax, __uint_as_float(static_cast<unsigned>(s.wmass[w])));
+    __syncthreads();
+  }
+
+  // what the last pass needs: the drawn value and its rank among its equals, the cut's value and how
+  // many of its equals are kept
+  unsigned n = 0, rank = 0, cut_eq = 0;
+  float z_draw = 0.f, z_cut = 0.f, prob = 0.f;
+  bool any = true, whole_ties = true;   // whole_ties: every token equal to the cut's is kept
+  if (k == 1) {
+    any = zmax > ninf();
+    n = any ? 1u : 0u;
+    z_draw = z_cut = zmax;
+    cut_eq = 1;
+    whole_ties = false;
+    prob = any ? 1.f : 0.f;
+  } else {
+    WeightScale ws = weight_scale(zmax, T);
+    const unsigned long long least =
+        min_p > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(min_p) * kWeightOne)) : 0ull;
+    // histogram
+    for (int i = tid; i < G::kHistWords; i += NT) hist[i] = 0u;
+    __syncthreads();
+    unsigned n_min = 0, n_all;
+    unsigned long long m_min = 0, m_all;
+    bool out_of_range = false;
+#pragma unroll 2
+    for (int u = tid; u < row.units; u += NT) {
+      Raw x[VEC];
+      row.load(u, x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const int b = bin_of<DTYPE>(x[e]);
+        if (b >= 0) {
+          atomicAdd(&hist[b], 1u);
+          if (DTYPE == 0) {
+            const unsigned long long w = weight_of(value_of<DTYPE>(x[e]), ws, s.tab);
+            if (w) add_weight(&hist[SPAN + b], &hist[2 * SPAN + b], w);
+            if (w >= least) ++n_min, m_min += w;
+          }
+        }
+        out_of_range |= b == -2;
+      }
+    }
+    if (out_of_range) s.fallback = 1;
+    __syncthreads();
+    // the non-empty bins, in order
+    unsigned filled = 0, listed;
+    unsigned long long none = 0, none_all;
+#pragma unroll
+    for (int e = 0; e < PER; ++e) filled += hist[tid * PER + e] != 0u;
+    unsigned at = filled;
+    block_scan<NT>(at, none, &listed, &none_all, s);
+#pragma unroll
+    for (int e = 0; e < PER; ++e)
+      if (hist[tid * PER + e]) list[at++] = static_cast<uint16_t>(tid * PER + e);
+    __syncthreads();
+    if (DTYPE == 1 && listed > 0) {
+      zmax = bin_value(list[0]);
+      ws = weight_scale(zmax, T);
+    }
+    // below -2^8 the weights have to be zero (one unknown weight would be wrong)
+    bool general = s.fallback || (listed > 0 && (list[0] == kLowBin || (hist[kLowBin] && weight_of(-256.f, ws, s.tab) != 0ull)));
+    const int share = (listed + NT - 1) / NT, i0 = min(static_cast<int>(listed), tid * share), i1 = min(static_cast<int>(listed), i0 + share);
+    auto bin_weight = [&](int b) -> unsigned long long {   // of one token (bf16) or the whole bin (fp32)
+      if (DTYPE == 0) return (static_cast<unsigned long long>(hist[2 * SPAN + b]) << 32) + hist[SPAN + b];
+      return b == kLowBin ? 0ull : weight_of(bin_value(b), ws, s.tab);
+    };
+    unsigned my_cnt = 0;
+    unsigned long long my_mass = 0;
+    if (!general) {
+      for (int i = i0; i < i1; ++i) {
+        const int b = list[i];
+        const unsigned c = hist[b];
+        const unsigned long long w = bin_weight(b);
+        my_cnt += c;
+        my_mass += DTYPE == 1 ? c * w : w;
+        if (DTYPE == 1 && w >= least) n_min += c, m_min += c * w;
+      }
+      block_scan<NT>(my_cnt, my_mass, &n_all, &m_all, s);
+    }
+    // the list's group in which a count or a weight reaches the target
+    auto search = [&](bool by_count, unsigned long long target) -> Prefix {
+      unsigned c = my_cnt;
+      unsigned long long m = my_mass;
+      for (int i = i0; i < i1; ++i) {
+        if (by_count ? c >= target : m >= target) break;
+        const int b = list[i];
+        const unsigned bc = hist[b];
+        const unsigned long long bm = DTYPE == 1 ? bc * bin_weight(b) : bin_weight(b);
+        if (by_count ? c + bc >= target : m + bm >= target) s.found = {c, m, static_cast<uint32_t>(b)};
+        c += bc;
+        m += bm;
+      }
+      __syncthreads();
+      const Prefix f = s.found;
+      __syncthreads();
+      return f;
+    };
+    if (general) {
+      // the general way needs the maximum and the totals first
+      float top = ninf();
+      for (int u = tid; u < row.units; u += NT) {
+        Raw x[VEC];
+        row.load(u, x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) top = fmaxf(top, value_of<DTYPE>(x[e]));
+      }
+      top = warp_max(top);
+      __syncthreads();
+      if (lane == 0) s.wmass[warp] = __float_as_uint(top);
+      __syncthreads();
+      for (int w = 0; w < NW; ++w) top = fmaxf(top, __uint_as_float(static_cast<unsigned>(s.wmass[w])));
+      __syncthreads();
+      ws = weight_scale(top, T);
+      n_min = 0;
+      m_min = 0;
+      unsigned c = 0;
+      unsigned long long m = 0;
+      for (int u = tid; u < row.units; u += NT) {
+        Raw x[VEC];
+        row.load(u, x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const float z = value_of<DTYPE>(x[e]);
+          if (!(z > ninf())) continue;
+          const unsigned long long w = weight_of(z, ws, s.tab);
+          ++c;
+          m += w;
+          if (w >= least) ++n_min, m_min += w;
+        }
+      }
+      block_scan<NT>(c, m, &n_all, &m_all, s);
+    }
+    if (min_p > 0.f) {
+      unsigned c = n_min;
+      unsigned long long m = m_min;
+      block_scan<NT>(c, m, &n_min, &m_min, s);
+    }
+    any = n_all > 0;
+    if (any) {
+      // the group of equal logits in which the order reaches a target: its value, and what lies before it
+      struct Group {
+        float z;
+        unsigned cnt;
+        unsigned long long mass, w;
+      };
+      auto reach = [&](bool by_count, unsigned long long target) -> Group {
+        Prefix g = {0u, 0ull, 0u};
+        if (general) {
+          g = by_count ? descend<DTYPE, true>(row, ws, target, g, DTYPE == 1 ? 16 : 32, digits, s)
+                       : descend<DTYPE, false>(row, ws, target, g, DTYPE == 1 ? 16 : 32, digits, s);
+        } else {
+          g = search(by_count, target);
+          if (DTYPE == 1 && g.key != kLowBin) {
+            const float z = bin_value(g.key);
+            return {z, g.cnt, g.mass, weight_of(z, ws, s.tab)};
+          }
+          if (g.key == kLowBin) {
+            // among the logits below -2^8 (a count went there): their weights are zero, all digits are open.
+            // In bf16 the descent's histogram takes the list's place: no search comes after it.
+            const Prefix low = {0u, 0ull, 0u};
+            g = descend<DTYPE, true>(row, ws, target, low, DTYPE == 1 ? 16 : 32, digits, s);
+            if (DTYPE == 1) general = true;
+          } else {
+            g.key = bin_key16(g.key);
+            g = by_count ? descend<DTYPE, true>(row, ws, target, g, 16, digits, s)
+                         : descend<DTYPE, false>(row, ws, target, g, 16, digits, s);
+          }
+        }
+        const float z = key_value<DTYPE>(g.key);
+        return {z, g.cnt, g.mass, weight_of(z, ws, s.tab)};
+      };
+      n = n_all;
+      unsigned long long mass = m_all;
+      Group cut = {0.f, 0u, 0ull, 0ull};
+      bool cut_known = false;
+      if (k > 0 && static_cast<unsigned>(k) < n) {
+        cut = reach(true, k);
+        cut_known = true;
+        n = k;
+        mass = cut.mass + (k - cut.cnt) * cut.w;
+      }
+      if (top_p < 1.f) {
+        const double goal = ceil(fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(mass));
+        unsigned long long target = goal < 1.0 ? 1ull : static_cast<unsigned long long>(goal);
+        if (target > mass) target = mass;
+        const Group g = reach(false, target);
+        const unsigned in = static_cast<unsigned>((target - g.mass + g.w - 1) / g.w);
+        if (g.cnt + in < n) {
+          n = g.cnt + in;
+          mass = g.mass + in * g.w;
+          cut = g;
+          cut_known = true;
+        }
+      }
+      if (min_p > 0.f && n_min < n) {
+        n = n_min > 0 ? n_min : 1;
+        mass = n_min > 0 ? m_min : kWeightOne;
+        cut_known = false;
+      }
+      // the draw
+      const double td = uniform > 0.f ? floor(static_cast<double>(uniform) * static_cast<double>(mass)) : 0.0;
+      unsigned long long t = td >= static_cast<double>(mass) ? mass - 1 : static_cast<unsigned long long>(td);
+      if (t >= mass) t = mass - 1;
+      const Group g = reach(false, t + 1);
+      z_draw = g.z;
+      rank = static_cast<unsigned>((t + 1 - g.mass + g.w - 1) / g.w) - 1;
+      prob = static_cast<float>(static_cast<double>(g.w) / static_cast<double>(mass));
+      if (filter) {
+        if (n == n_all) {
+          z_cut = ninf();   // everything above -inf stays
+        } else {
+          if (!cut_known) cut = reach(true, n);
+          z_cut = cut.z;
+          cut_eq = n - cut.cnt;
+          whole_ties = false;
+        }
+      }
+    }
+  }
+
+  // ordered passes: warp w takes a contiguous share of the units, so that equal logits can be counted in
+  // index order.  First the equal ones per warp, then the drawn token, then the filtered row.
+  const int per_warp = (row.units + NW - 1) / NW, u0 = min(row.units, warp * per_warp), u1 = min(row.units, u0 + per_warp);
+  int token = -1;
+  if (any) {
+    unsigned eq = 0, eq_cut = 0;
+#pragma unroll 4
+    for (int u = u0 + lane; u < u1; u += 32) {
+      Raw x[VEC];
+      row.load(u, x);
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        const float z = value_of<DTYPE>(x[e]);
+        eq += z == z_draw;
+        eq_cut += z == z_cut;
+      }
+    }
+    eq = __reduce_add_sync(0xffffffffu, eq);
+    eq_cut = __reduce_add_sync(0xffffffffu, eq_cut);
+    if (lane == 0) s.wcnt[warp] = eq, s.wcnt2[warp] = eq_cut;
+    __syncthreads();
+    unsigned before = 0, before_cut = 0;
+    for (int w = 0; w < warp; ++w) before += s.wcnt[w], before_cut += s.wcnt2[w];
+    if (rank >= before && rank < before + eq) {   // the drawn token is in this warp's share
+      unsigned left = rank - before;
+      for (int base = u0; base < u1; base += 32) {
+        const int u = base + lane;
+        Raw x[VEC];
+        unsigned here = 0;
+        if (u < u1) {
+          row.load(u, x);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(x[e]) == z_draw;
+        }
+        unsigned incl = here;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const unsigned all = __shfl_sync(0xffffffffu, incl, 31);
+        if (left < all) {
+          if (left >= incl - here && left < incl) {
+            unsigned skip = left - (incl - here);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+              if (value_of<DTYPE>(x[e]) == z_draw && skip-- == 0) s.token = row.first(u) + e;
+          }
           break;
         }
+        left -= all;
+      }
     }
-    if (p.filtered) {
-      const unsigned keep_eq = n - cut.cnt;   // of the tokens equal to the cut's logit
-      for (int i = i0; i < i1; ++i) {
-        const float x = row_logit<DTYPE>(row, i);
-        const bool keep = x > zc || (x == zc && e < keep_eq);
-        e += x == zc;
-        const long long at = static_cast<long long>(r) * p.filtered_stride + i;
-        if (DTYPE == 1)
-          static_cast<uint16_t*>(p.filtered)[at] = keep ? static_cast<const uint16_t*>(row)[i] : 0xff80u;
-        else
-          static_cast<float*>(p.filtered)[at] = keep ? static_cast<const float*>(row)[i] : ninf();
+    if (filter) {
+      Raw* out = static_cast<Raw*>(p.filtered) + static_cast<long long>(r) * p.filtered_stride;
+      constexpr Raw kDrop = static_cast<Raw>(DTYPE == 1 ? 0xff80u : 0xff800000u);
+      // 16-byte stores where the output row lies as the input row does
+      const bool vec = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.p)) & 15u) == 0;
+      unsigned seen = before_cut;   // equal to the cut before this step of the warp
+      const bool ordered = !whole_ties;
+      for (int base = u0; base < u1; base += 32) {
+        const int u = base + lane;
+        const bool in = u < u1;
+        Raw x[VEC];
+        unsigned here = 0;
+        if (in) {
+          row.load(u, x);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(x[e]) == z_cut;
+        }
+        unsigned rank_cut = seen;
+        if (ordered && __any_sync(0xffffffffu, here != 0u)) {
+          unsigned incl = here;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += v;
+          }
+          rank_cut = seen + incl - here;
+          seen += __shfl_sync(0xffffffffu, incl, 31);
+        }
+        if (in) {
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) {
+            const float z = value_of<DTYPE>(x[e]);
+            const bool tie = z == z_cut;
+            const bool keep = z > z_cut || (ordered && tie && rank_cut < cut_eq);
+            rank_cut += tie;
+            if (!keep) x[e] = kDrop;
+          }
+          const int f = row.first(u), c = row.count(u);
+          if (vec && u > 0 && c == VEC) {
+            uint4 v;
+            memcpy(&v, x, 16);
+            __stcs(reinterpret_cast<uint4*>(out + f), v);
+          } else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+              if (e < c) out[f + e] = x[e];
+          }
+        }
       }
     }
     __syncthreads();
     token = s.token;
-  } else if (p.filtered) {
-    for (int i = tid; i < V; i += kThreads) {
-      const long long at = static_cast<long long>(r) * p.filtered_stride + i;
-      if (DTYPE == 1)
-        static_cast<uint16_t*>(p.filtered)[at] = 0xff80u;
-      else
-        static_cast<float*>(p.filtered)[at] = ninf();
-    }
+  } else if (filter) {
+    Raw* out = static_cast<Raw*>(p.filtered) + static_cast<long long>(r) * p.filtered_stride;
+    for (int i = tid; i < p.V; i += NT) out[i] = static_cast<Raw>(DTYPE == 1 ? 0xff80u : 0xff800000u);
   }
   if (tid == 0) {
     p.tokens[r] = token;
@@ -268,14 +612,19 @@ __global__ void __launch_bounds__(kThreads) sample_kernel_row(const SampleParams
   }
 }
 
+template <int DTYPE>
+cudaError_t launch(const SampleParams& p, cudaStream_t stream) {
+  // above the default limit: asked for once per device, cheap to repeat
+  cudaError_t e = cudaFuncSetAttribute(sample_kernel_row<DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DTYPE>());
+  if (e != cudaSuccess) return e;
+  sample_kernel_row<DTYPE><<<p.R, Geo<DTYPE>::kThreads, smem_bytes<DTYPE>(), stream>>>(p);
+  return cudaGetLastError();
+}
+
 }  // namespace
 
 cudaError_t launch_sample(int dtype, const SampleParams& p, cudaStream_t stream) {
-  const void* fn = dtype == 1 ? reinterpret_cast<const void*>(&sample_kernel_row<1>)
-                              : reinterpret_cast<const void*>(&sample_kernel_row<0>);
-  SampleParams copy = p;
-  void* args[] = {&copy};
-  return cudaLaunchKernel(fn, dim3(p.R), dim3(kThreads), args, sizeof(Smem), stream);
+  return dtype == 1 ? launch<1>(p, stream) : launch<0>(p, stream);
 }
 
 }  // namespace sv
