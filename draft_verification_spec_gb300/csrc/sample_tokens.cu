@@ -21,7 +21,7 @@
 //
 // Bound: shared-memory atomics of the histogram (one per token, at most a few of a warp's 32 falling
 // on one bin), then the last passes, which read the row from L2.
-#include <cuda_bf16.h>
+#include <atomic>
 
 #include "sample_weight.cuh"
 #include "step_internal.h"
@@ -34,6 +34,8 @@ constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;   // the general descent
 constexpr int kMagLow = (127 - 40) * 128, kMags = 48 * 128;   // magnitudes of the histogram, in 7-bit mantissa steps
 constexpr int kHist = 2 * kMags + 2;                      // positive, zero, negative, below -2^8
 constexpr int kZeroBin = kMags, kLowBin = kHist - 1;
+
+constexpr int kGather = 4096;                             // fp32: tokens of one bin that are looked through in shared memory
 
 template <int DTYPE>
 struct Geo;
@@ -49,7 +51,7 @@ struct Geo<0> {   // fp32: counts and weights
   using Raw = uint32_t;
   static constexpr int kThreads = 1024, kVec = 4, kPer = 13;
   static constexpr int kHistWords = 3 * kThreads * kPer;
-  static constexpr int kDigitWords = 3 * kBins;
+  static constexpr int kDigitWords = 3 * kBins + kGather;
 };
 static_assert(Geo<1>::kThreads * Geo<1>::kPer >= kHist && Geo<0>::kThreads * Geo<0>::kPer >= kHist, "every bin has a thread");
 static_assert(Geo<1>::kHistWords >= 3 * kBins, "the general descent fits the histogram");
@@ -125,6 +127,21 @@ struct Row {
   }
 };
 
+// f(unit, values) for the units [begin, end) in steps of `stride`, BATCH loads in flight at a time.
+template <int DTYPE, int BATCH, typename F>
+__device__ __forceinline__ void walk(const Row<DTYPE>& row, int begin, int end, int stride, F f) {
+  constexpr int VEC = Geo<DTYPE>::kVec;
+  for (int u = begin; u < end; u += BATCH * stride) {
+    typename Row<DTYPE>::Raw x[BATCH][VEC];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (u + i * stride < end) row.load(u + i * stride, x[i]);
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (u + i * stride < end) f(u + i * stride, x[i]);
+  }
+}
+
 struct Prefix {
   unsigned cnt;            // tokens before the group in the order
   unsigned long long mass;
@@ -139,6 +156,7 @@ struct Shared {
   Prefix found;
   float zmax;
   int fallback, token;
+  unsigned gathered;
 };
 
 // Block-wide exclusive prefix of (count, weight); the totals too.
@@ -179,11 +197,13 @@ __device__ __forceinline__ void add_weight(unsigned* lo, unsigned* hi, unsigned 
   if (up) atomicAdd(hi, up);
 }
 
-// Block-wide: the group of equal keys in which the order's count (BY_COUNT) or weight reaches `target`
-// (1 <= target <= the row's), among the tokens whose key begins with at.key, `bits` bits being open.
-template <int DTYPE, bool BY_COUNT>
-__device__ Prefix descend(const Row<DTYPE>& row, const WeightScale& ws, unsigned long long target, Prefix at, int bits,
-                          unsigned* digits, Shared<Geo<DTYPE>::kThreads>& s) {
+// Block-wide: the group of equal keys in which the order's count or weight reaches `target` (1 <= target
+// <= the row's), among the tokens whose key begins with at.key, `bits` bits being open.  With `gathered`
+// >= 0 those tokens' keys are in `keys`, else the row is read, once per 11 bits.
+template <int DTYPE>
+__device__ __noinline__ Prefix descend(const Row<DTYPE>& row, const WeightScale& ws, bool by_count, unsigned long long target,
+                                       Prefix at, int bits, unsigned* digits, const uint32_t* keys, int gathered,
+                                       Shared<Geo<DTYPE>::kThreads>& s) {
   constexpr int NT = Geo<DTYPE>::kThreads, PER = kBins / NT, VEC = Geo<DTYPE>::kVec;
   const int tid = threadIdx.x;
   unsigned *cnt = digits, *lo = digits + kBins, *hi = digits + 2 * kBins;
@@ -192,18 +212,22 @@ __device__ Prefix descend(const Row<DTYPE>& row, const WeightScale& ws, unsigned
     bits -= digit;
     for (int i = tid; i < 3 * kBins; i += NT) digits[i] = 0u;
     __syncthreads();
-    for (int u = tid; u < row.units; u += NT) {
-      typename Row<DTYPE>::Raw x[VEC];
-      row.load(u, x);
+    auto take = [&](uint32_t key, float z) {
+      if ((static_cast<unsigned long long>(key) >> (bits + digit)) != at.key || !(z > ninf())) return;
+      const unsigned d = (key >> bits) & ((1u << digit) - 1u);
+      atomicAdd(&cnt[d], 1u);
+      add_weight(&lo[d], &hi[d], weight_of(z, ws, s.tab));
+    };
+    if (gathered >= 0) {
+      for (int i = tid; i < gathered; i += NT) take(keys[i], key_value<DTYPE>(keys[i]));
+    } else {
+      walk<DTYPE, 2>(row, tid, row.units, NT, [&](int, typename Row<DTYPE>::Raw (&x)[VEC]) {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float z = value_of<DTYPE>(x[e]);
-        const uint32_t key = sample_key<DTYPE>(z);
-        if ((static_cast<unsigned long long>(key) >> (bits + digit)) != at.key || !(z > ninf())) continue;
-        const unsigned d = (key >> bits) & ((1u << digit) - 1u);
-        atomicAdd(&cnt[d], 1u);
-        add_weight(&lo[d], &hi[d], weight_of(z, ws, s.tab));
-      }
+        for (int e = 0; e < VEC; ++e) {
+          const float z = value_of<DTYPE>(x[e]);
+          take(sample_key<DTYPE>(z), z);
+        }
+      });
     }
     __syncthreads();
     // thread t holds PER bins from the top
@@ -222,8 +246,8 @@ __device__ Prefix descend(const Row<DTYPE>& row, const WeightScale& ws, unsigned
     bm += at.mass;
 #pragma unroll
     for (int e = 0; e < PER; ++e) {
-      const bool before = BY_COUNT ? bc < target : bm < target;
-      const bool reached = BY_COUNT ? bc + c[e] >= target : bm + m[e] >= target;
+      const bool before = by_count ? bc < target : bm < target;
+      const bool reached = by_count ? bc + c[e] >= target : bm + m[e] >= target;
       if (before && reached) s.found = {bc, bm, static_cast<uint32_t>((at.key << digit) | (kBins - 1 - (PER * tid + e)))};
       bc += c[e];
       bm += m[e];
@@ -233,6 +257,27 @@ __device__ Prefix descend(const Row<DTYPE>& row, const WeightScale& ws, unsigned
     __syncthreads();
   }
   return at;
+}
+
+// fp32, block-wide: the same among the tokens of one bin (16 open bits), whose keys are gathered first.
+template <int DTYPE>
+__device__ __noinline__ Prefix descend_bin(const Row<DTYPE>& row, const WeightScale& ws, bool by_count,
+                                           unsigned long long target, Prefix at, unsigned tokens, unsigned* digits,
+                                           Shared<Geo<DTYPE>::kThreads>& s) {
+  constexpr int NT = Geo<DTYPE>::kThreads, VEC = Geo<DTYPE>::kVec;
+  uint32_t* keys = digits + 3 * kBins;
+  if (tokens > kGather) return descend<DTYPE>(row, ws, by_count, target, at, 16, digits, nullptr, -1, s);
+  if (threadIdx.x == 0) s.gathered = 0u;
+  __syncthreads();
+  walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, typename Row<DTYPE>::Raw (&x)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const uint32_t key = sample_key<DTYPE>(value_of<DTYPE>(x[e]));
+      if (key >> 16 == at.key) keys[atomicAdd(&s.gathered, 1u)] = key;
+    }
+  });
+  __syncthreads();
+  return descend<DTYPE>(row, ws, by_count, target, at, 16, digits, keys, static_cast<int>(tokens), s);
 }
 
 template <int DTYPE>
@@ -264,13 +309,10 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
   // the largest logit, where it is needed before the weights
   float zmax = ninf();
   if (need_max) {
-#pragma unroll 4
-    for (int u = tid; u < row.units; u += NT) {
-      Raw x[VEC];
-      row.load(u, x);
+    walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, Raw (&x)[VEC]) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) zmax = fmaxf(zmax, value_of<DTYPE>(x[e]));   // fmaxf drops NaN
-    }
+    });
     zmax = warp_max(zmax);
     if (lane == 0) s.wmass[warp] = __float_as_uint(zmax);
     __syncthreads();
@@ -295,15 +337,12 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     const unsigned long long least =
         min_p > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(min_p) * kWeightOne)) : 0ull;
     // histogram
-    for (int i = tid; i < G::kHistWords; i += NT) hist[i] = 0u;
+    for (int i = tid; i < G::kHistWords / 4; i += NT) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
     unsigned n_min = 0, n_all;
     unsigned long long m_min = 0, m_all;
     bool out_of_range = false;
-#pragma unroll 2
-    for (int u = tid; u < row.units; u += NT) {
-      Raw x[VEC];
-      row.load(u, x);
+    walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, Raw (&x)[VEC]) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const int b = bin_of<DTYPE>(x[e]);
@@ -317,7 +356,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         }
         out_of_range |= b == -2;
       }
-    }
+    });
     if (out_of_range) s.fallback = 1;
     __syncthreads();
     // the non-empty bins, in order
@@ -424,8 +463,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       auto reach = [&](bool by_count, unsigned long long target) -> Group {
         Prefix g = {0u, 0ull, 0u};
         if (general) {
-          g = by_count ? descend<DTYPE, true>(row, ws, target, g, DTYPE == 1 ? 16 : 32, digits, s)
-                       : descend<DTYPE, false>(row, ws, target, g, DTYPE == 1 ? 16 : 32, digits, s);
+          g = descend<DTYPE>(row, ws, by_count, target, g, DTYPE == 1 ? 16 : 32, digits, nullptr, -1, s);
         } else {
           g = search(by_count, target);
           if (DTYPE == 1 && g.key != kLowBin) {
@@ -436,12 +474,12 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
             // among the logits below -2^8 (a count went there): their weights are zero, all digits are open.
             // In bf16 the descent's histogram takes the list's place: no search comes after it.
             const Prefix low = {0u, 0ull, 0u};
-            g = descend<DTYPE, true>(row, ws, target, low, DTYPE == 1 ? 16 : 32, digits, s);
+            g = descend<DTYPE>(row, ws, true, target, low, DTYPE == 1 ? 16 : 32, digits, nullptr, -1, s);
             if (DTYPE == 1) general = true;
           } else {
+            const unsigned tokens = hist[g.key];
             g.key = bin_key16(g.key);
-            g = by_count ? descend<DTYPE, true>(row, ws, target, g, 16, digits, s)
-                         : descend<DTYPE, false>(row, ws, target, g, 16, digits, s);
+            g = descend_bin<DTYPE>(row, ws, by_count, target, g, tokens, digits, s);
           }
         }
         const float z = key_value<DTYPE>(g.key);
@@ -502,51 +540,50 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
   int token = -1;
   if (any) {
     unsigned eq = 0, eq_cut = 0;
-#pragma unroll 4
-    for (int u = u0 + lane; u < u1; u += 32) {
-      Raw x[VEC];
-      row.load(u, x);
+    walk<DTYPE, 4>(row, u0 + lane, u1, 32, [&](int, Raw (&x)[VEC]) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
         const float z = value_of<DTYPE>(x[e]);
         eq += z == z_draw;
         eq_cut += z == z_cut;
       }
-    }
+    });
     eq = __reduce_add_sync(0xffffffffu, eq);
     eq_cut = __reduce_add_sync(0xffffffffu, eq_cut);
     if (lane == 0) s.wcnt[warp] = eq, s.wcnt2[warp] = eq_cut;
     __syncthreads();
-    unsigned before = 0, before_cut = 0;
-    for (int w = 0; w < warp; ++w) before += s.wcnt[w], before_cut += s.wcnt2[w];
-    if (rank >= before && rank < before + eq) {   // the drawn token is in this warp's share
-      unsigned left = rank - before;
-      for (int base = u0; base < u1; base += 32) {
-        const int u = base + lane;
+    unsigned before_cut = 0, before = 0;
+    int owner = 0;
+    for (int w = 0; w < NW; ++w) {
+      if (w < warp) before_cut += s.wcnt2[w];
+      if (owner == w && rank - before >= s.wcnt[w]) before += s.wcnt[w], ++owner;
+    }
+    __syncthreads();
+    {
+      // the drawn token is in warp `owner`'s share: the whole block looks for it, each thread in
+      // consecutive units
+      const int o0 = min(row.units, owner * per_warp), o1 = min(row.units, o0 + per_warp);
+      const int per = (o1 - o0 + NT - 1) / NT, a0 = min(o1, o0 + tid * per), a1 = min(o1, a0 + per);
+      unsigned here = 0, all;
+      unsigned long long none = 0, none_all;
+      for (int u = a0; u < a1; ++u) {
         Raw x[VEC];
-        unsigned here = 0;
-        if (u < u1) {
+        row.load(u, x);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(x[e]) == z_draw;
+      }
+      unsigned first = here;
+      block_scan<NT>(first, none, &all, &none_all, s);
+      const unsigned want = rank - before;
+      if (want >= first && want < first + here) {
+        unsigned skip = want - first;
+        for (int u = a0; u < a1; ++u) {
+          Raw x[VEC];
           row.load(u, x);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(x[e]) == z_draw;
+          for (int e = 0; e < VEC; ++e)
+            if (value_of<DTYPE>(x[e]) == z_draw && skip-- == 0) s.token = row.first(u) + e;
         }
-        unsigned incl = here;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        const unsigned all = __shfl_sync(0xffffffffu, incl, 31);
-        if (left < all) {
-          if (left >= incl - here && left < incl) {
-            unsigned skip = left - (incl - here);
-#pragma unroll
-            for (int e = 0; e < VEC; ++e)
-              if (value_of<DTYPE>(x[e]) == z_draw && skip-- == 0) s.token = row.first(u) + e;
-          }
-          break;
-        }
-        left -= all;
       }
     }
     if (filter) {
@@ -556,45 +593,51 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       const bool vec = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.p)) & 15u) == 0;
       unsigned seen = before_cut;   // equal to the cut before this step of the warp
       const bool ordered = !whole_ties;
-      for (int base = u0; base < u1; base += 32) {
-        const int u = base + lane;
-        const bool in = u < u1;
-        Raw x[VEC];
-        unsigned here = 0;
-        if (in) {
-          row.load(u, x);
+      constexpr int kAhead = 4;   // loads in flight
+      for (int base = u0; base < u1; base += 32 * kAhead) {
+        Raw x[kAhead][VEC];
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(x[e]) == z_cut;
-        }
-        unsigned rank_cut = seen;
-        if (ordered && __any_sync(0xffffffffu, here != 0u)) {
-          unsigned incl = here;
+        for (int i = 0; i < kAhead; ++i)
+          if (base + i * 32 + lane < u1) row.load(base + i * 32 + lane, x[i]);
 #pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += v;
+        for (int i = 0; i < kAhead; ++i) {
+          const int u = base + i * 32 + lane;
+          const bool in = u < u1;
+          unsigned here = 0;
+          if (in) {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(x[i][e]) == z_cut;
           }
-          rank_cut = seen + incl - here;
-          seen += __shfl_sync(0xffffffffu, incl, 31);
-        }
-        if (in) {
+          unsigned rank_cut = seen;
+          if (ordered && __any_sync(0xffffffffu, here != 0u)) {
+            unsigned incl = here;
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) {
-            const float z = value_of<DTYPE>(x[e]);
-            const bool tie = z == z_cut;
-            const bool keep = z > z_cut || (ordered && tie && rank_cut < cut_eq);
-            rank_cut += tie;
-            if (!keep) x[e] = kDrop;
+            for (int o = 1; o < 32; o <<= 1) {
+              const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+              if (lane >= o) incl += v;
+            }
+            rank_cut = seen + incl - here;
+            seen += __shfl_sync(0xffffffffu, incl, 31);
           }
-          const int f = row.first(u), c = row.count(u);
-          if (vec && u > 0 && c == VEC) {
-            uint4 v;
-            memcpy(&v, x, 16);
-            __stcs(reinterpret_cast<uint4*>(out + f), v);
-          } else {
+          if (in) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-              if (e < c) out[f + e] = x[e];
+            for (int e = 0; e < VEC; ++e) {
+              const float z = value_of<DTYPE>(x[i][e]);
+              const bool tie = z == z_cut;
+              const bool keep = z > z_cut || (ordered && tie && rank_cut < cut_eq);
+              rank_cut += tie;
+              if (!keep) x[i][e] = kDrop;
+            }
+            const int f = row.first(u), c = row.count(u);
+            if (vec && u > 0 && c == VEC) {
+              uint4 v;
+              memcpy(&v, x[i], 16);
+              __stcs(reinterpret_cast<uint4*>(out + f), v);
+            } else {
+#pragma unroll
+              for (int e = 0; e < VEC; ++e)
+                if (e < c) out[f + e] = x[i][e];
+            }
           }
         }
       }
@@ -614,9 +657,15 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
 
 template <int DTYPE>
 cudaError_t launch(const SampleParams& p, cudaStream_t stream) {
-  // above the default limit: asked for once per device, cheap to repeat
-  cudaError_t e = cudaFuncSetAttribute(sample_kernel_row<DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DTYPE>());
+  static std::atomic<unsigned long long> asked{0};   // devices whose limit has been raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
+  if (dev >= 64 || !(asked.load() >> dev & 1)) {
+    e = cudaFuncSetAttribute(sample_kernel_row<DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DTYPE>());
+    if (e != cudaSuccess) return e;
+    if (dev < 64) asked.fetch_or(1ull << dev);
+  }
   sample_kernel_row<DTYPE><<<p.R, Geo<DTYPE>::kThreads, smem_bytes<DTYPE>(), stream>>>(p);
   return cudaGetLastError();
 }

@@ -425,6 +425,36 @@ def test_sample_ties_zeros_infinities(sv, dtype):
         _check_sample(sv, z.to(dt).cuda(), u, **s)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_sample_logits_of_any_size(sv, dtype):
+    """Masks of -1e9 and of the type's lowest value, logits in the hundreds and thousands, and vanishing ones."""
+    dt, V = DTYPES[dtype], 3000
+    g = torch.Generator().manual_seed(21)
+    z = torch.randn(8, V, generator=g) * 3.0
+    low = torch.finfo(dt).min
+    z[0, 100:] = -1e9
+    z[1, 5:] = low
+    z[2, ::2] = -300.0 - torch.arange(V // 2) % 50
+    z[3] = z[3] * 400.0
+    z[4, ::7] = torch.randn(len(z[4, ::7]), generator=g) * 1e-20
+    z[5] = -500.0 + z[5]
+    z[6] = low
+    z[6, 9] = -1e30
+    z[7] = z[7] * 1e-18
+    z, u = z.to(dt).cuda(), torch.rand(8, generator=g).cuda()
+    for s in SETTINGS + [dict(top_k=2000), dict(top_k=2999, top_p=0.99), dict(T=100.0, top_p=0.9), dict(T=1e4, top_k=1700)]:
+        _check_sample(sv, z, u, **s)
+
+
+def test_sample_crowded_bins(sv):
+    """fp32 logits of which thousands share their 16 top bits."""
+    z = 3.0 + torch.rand(3, 40000, generator=torch.Generator().manual_seed(2)) * 0.01
+    z[2, 10000:] = -7.0
+    u = torch.rand(3, generator=torch.Generator().manual_seed(3)).cuda()
+    for s in (dict(), dict(top_k=777, top_p=0.9), dict(top_p=0.4), dict(min_p=0.997)):
+        _check_sample(sv, z.cuda(), u, **s)
+
+
 def test_sample_uniform_ends(sv):
     """u = 0 takes the most likely token; the largest u below 1 (and 1, and beyond) a kept one."""
     z, _ = _logits(6, 5000, "f32", seed=8)
