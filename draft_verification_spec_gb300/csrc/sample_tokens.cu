@@ -9,8 +9,8 @@
 // whose inclusive prefix weight is strictly above u x the weight of the n.  Every question is "which
 // element of the order does a count or a weight reach".
 //
-// One CTA per row.  A histogram over the 16 top bits of the logits (those of magnitude 2^-40 to 2^8,
-// in descending order, and zero: 12,290 bins) answers it: the non-empty bins, a few hundred to a few
+// One CTA per row.  A histogram over the 16 top bits of the logits (those of magnitude 2^-32 to 2^8,
+// in descending order, and zero: 10,242 bins) answers it: the non-empty bins, a few hundred to a few
 // thousand, become a list whose counts and weights are summed once over the block, and a question is
 // a search in those sums.  A bf16 bin is one value, so its weight is count x weight and the row needs
 // neither its maximum first nor an exponential per token.  An fp32 bin also sums its tokens' weights,
@@ -22,6 +22,7 @@
 // Bound: shared-memory atomics of the histogram (one per token, at most a few of a warp's 32 falling
 // on one bin), then the last passes, which read the row from L2.
 #include <atomic>
+#include <cuda_bf16.h>
 
 #include "sample_weight.cuh"
 #include "step_internal.h"
@@ -31,7 +32,7 @@ namespace sv {
 namespace {
 
 constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;   // the general descent
-constexpr int kMagLow = (127 - 40) * 128, kMags = 48 * 128;   // magnitudes of the histogram, in 7-bit mantissa steps
+constexpr int kMagLow = (127 - 32) * 128, kMags = 40 * 128;   // magnitudes of the histogram, in 7-bit mantissa steps
 constexpr int kHist = 2 * kMags + 2;                      // positive, zero, negative, below -2^8
 constexpr int kZeroBin = kMags, kLowBin = kHist - 1;
 
@@ -42,14 +43,14 @@ struct Geo;
 template <>
 struct Geo<1> {   // bf16: counts only
   using Raw = uint16_t;
-  static constexpr int kThreads = 512, kVec = 8, kPer = 25;   // bins per thread: odd, so a warp's reads fall on distinct banks
+  static constexpr int kThreads = 512, kVec = 8, kPer = 21;   // bins per thread: odd, so a warp's reads fall on distinct banks
   static constexpr int kHistWords = kThreads * kPer;
   static constexpr int kDigitWords = 0;                   // the general descent reuses the histogram
 };
 template <>
 struct Geo<0> {   // fp32: counts and weights
   using Raw = uint32_t;
-  static constexpr int kThreads = 1024, kVec = 4, kPer = 13;
+  static constexpr int kThreads = 1024, kVec = 4, kPer = 11;
   static constexpr int kHistWords = 3 * kThreads * kPer;
   static constexpr int kDigitWords = 3 * kBins + kGather;
 };
@@ -77,16 +78,15 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// Bin of a finite logit's 16 top bits; -1: not drawn (-inf, NaN); -2: outside the bins' range.
+// Bin of a logit whose magnitude is in the bins' range (mi = its place there); of the others: zero, those
+// below -2^8, -1 for -inf and NaN (never drawn), -2 for what has no bin.
+__device__ __forceinline__ int bin_in_range(int mi, bool neg) { return neg ? kZeroBin + 1 + mi : kZeroBin - 1 - mi; }
 template <int DTYPE>
-__device__ __forceinline__ int bin_of(typename Geo<DTYPE>::Raw b) {
-  const uint32_t top = DTYPE == 1 ? b : static_cast<uint32_t>(b) >> 16;
-  const int mag = top & 0x7fff, mi = mag - kMagLow;
-  const bool neg = top & 0x8000;
-  if (mi >= 0 && mi < kMags) return neg ? kZeroBin + 1 + mi : kZeroBin - 1 - mi;
-  if (mi < 0) return (DTYPE == 1 ? mag : static_cast<int>(b & 0x7fffffffu)) == 0 ? kZeroBin : -2;
-  const bool nan = DTYPE == 1 ? mag > 0x7f80 : (static_cast<uint32_t>(b) & 0x7fffffffu) > 0x7f800000u;
-  return nan || (neg && mag == 0x7f80) ? -1 : neg ? kLowBin : -2;
+__device__ __forceinline__ int bin_other(typename Geo<DTYPE>::Raw b) {
+  const uint32_t bits = DTYPE == 1 ? static_cast<uint32_t>(b) << 16 : static_cast<uint32_t>(b), mag = bits & 0x7fffffffu;
+  if (mag == 0u) return kZeroBin;
+  if (mag > 0x7f800000u || bits == 0xff800000u) return -1;
+  return static_cast<int>(mag >> 16) >= kMagLow + kMags && (bits >> 31) ? kLowBin : -2;
 }
 // A bin's value with the lowest magnitude (bf16: its value); its key's 16 top bits.
 __device__ __forceinline__ float bin_value(int bin) {
@@ -142,6 +142,28 @@ __device__ __forceinline__ void walk(const Row<DTYPE>& row, int begin, int end, 
   }
 }
 
+// How many of a piece's values equal v; which are greater (masks of the values' width).
+template <int DTYPE>
+struct Compare;
+template <>
+struct Compare<1> {
+  __nv_bfloat162 v;
+  __device__ __forceinline__ explicit Compare(float x) : v(__float2bfloat162_rn(x)) {}
+  __device__ __forceinline__ unsigned eq(uint32_t w) const { return __heq2_mask(*reinterpret_cast<__nv_bfloat162*>(&w), v); }
+  __device__ __forceinline__ unsigned gt(uint32_t w) const { return __hgt2_mask(*reinterpret_cast<__nv_bfloat162*>(&w), v); }
+  static constexpr unsigned kOnes = 0x00010001u, kDropWord = 0xff80ff80u;
+  static __device__ __forceinline__ unsigned total(unsigned packed) { return (packed & 0xffffu) + (packed >> 16); }
+};
+template <>
+struct Compare<0> {
+  float v;
+  __device__ __forceinline__ explicit Compare(float x) : v(x) {}
+  __device__ __forceinline__ unsigned eq(uint32_t w) const { return __uint_as_float(w) == v ? 0xffffffffu : 0u; }
+  __device__ __forceinline__ unsigned gt(uint32_t w) const { return __uint_as_float(w) > v ? 0xffffffffu : 0u; }
+  static constexpr unsigned kOnes = 1u, kDropWord = 0xff800000u;
+  static __device__ __forceinline__ unsigned total(unsigned packed) { return packed; }
+};
+
 struct Prefix {
   unsigned cnt;            // tokens before the group in the order
   unsigned long long mass;
@@ -154,7 +176,10 @@ struct Shared {
   unsigned long long wmass[32];
   unsigned wcnt[32], wcnt2[32];
   Prefix found;
-  float zmax;
+  float c_hi, c_lo;                  // the scale of the weights
+  unsigned long long least, target;  // min-p's weight; the weight that is looked for
+  float prob;
+  unsigned group_in;                 // how many of a group's tokens reach the target
   int fallback, token;
   unsigned gathered;
 };
@@ -174,18 +199,20 @@ __device__ __forceinline__ void block_scan(unsigned& c, unsigned long long& m, u
   }
   if (lane == 31) s.wcnt[warp] = ic, s.wmass[warp] = im;
   __syncthreads();
-  unsigned bc = 0, tc = 0;
-  unsigned long long bm = 0, tm = 0;
+  unsigned wc = lane < NT / 32 ? s.wcnt[lane] : 0u;
+  unsigned long long wm = lane < NT / 32 ? s.wmass[lane] : 0ull;
 #pragma unroll
-  for (int w = 0; w < NT / 32; ++w) {
-    if (w == warp) bc = tc, bm = tm;
-    tc += s.wcnt[w];
-    tm += s.wmass[w];
+  for (int o = 1; o < NT / 32; o <<= 1) {
+    const unsigned tc = __shfl_up_sync(0xffffffffu, wc, o);
+    const unsigned long long tm = __shfl_up_sync(0xffffffffu, wm, o);
+    if (lane >= o) wc += tc, wm += tm;
   }
-  c = bc + ic - c;
-  m = bm + im - m;
-  *c_all = tc;
-  *m_all = tm;
+  const unsigned bc = __shfl_sync(0xffffffffu, wc, warp > 0 ? warp - 1 : 0);
+  const unsigned long long bm = __shfl_sync(0xffffffffu, wm, warp > 0 ? warp - 1 : 0);
+  *c_all = __shfl_sync(0xffffffffu, wc, NT / 32 - 1);
+  *m_all = __shfl_sync(0xffffffffu, wm, NT / 32 - 1);
+  c = (warp > 0 ? bc : 0u) + ic - c;
+  m = (warp > 0 ? bm : 0ull) + im - m;
   __syncthreads();
 }
 
@@ -280,6 +307,120 @@ __device__ __noinline__ Prefix descend_bin(const Row<DTYPE>& row, const WeightSc
   return descend<DTYPE>(row, ws, by_count, target, at, 16, digits, keys, static_cast<int>(tokens), s);
 }
 
+// Block-wide largest logit (NaN left out).
+template <int DTYPE>
+__device__ __noinline__ float row_max(const Row<DTYPE>& row, Shared<Geo<DTYPE>::kThreads>& s) {
+  constexpr int NT = Geo<DTYPE>::kThreads, VEC = Geo<DTYPE>::kVec;
+  float top = ninf();
+  walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, typename Row<DTYPE>::Raw (&x)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) top = fmaxf(top, value_of<DTYPE>(x[e]));
+  });
+  top = warp_max(top);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) s.wcnt2[threadIdx.x >> 5] = __float_as_uint(top);
+  __syncthreads();
+  for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, __uint_as_float(s.wcnt2[w]));
+  __syncthreads();
+  return top;
+}
+
+struct Totals {
+  unsigned n_all, n_min;               // tokens above -inf, those of at least min-p's weight
+  unsigned long long m_all, m_min;     // their weights
+};
+
+// The general way's totals.
+template <int DTYPE>
+__device__ __noinline__ Totals row_totals(const Row<DTYPE>& row, const WeightScale& ws, unsigned long long least,
+                                          Shared<Geo<DTYPE>::kThreads>& s) {
+  constexpr int NT = Geo<DTYPE>::kThreads, VEC = Geo<DTYPE>::kVec;
+  Totals t = {0u, 0u, 0ull, 0ull};
+  walk<DTYPE, 1>(row, threadIdx.x, row.units, NT, [&](int, typename Row<DTYPE>::Raw (&x)[VEC]) {
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) {
+      const float z = value_of<DTYPE>(x[e]);
+      if (!(z > ninf())) continue;
+      const unsigned long long w = weight_of(z, ws, s.tab);
+      ++t.n_all;
+      t.m_all += w;
+      if (w >= least) ++t.n_min, t.m_min += w;
+    }
+  });
+  unsigned c = t.n_all;
+  unsigned long long m = t.m_all;
+  block_scan<NT>(c, m, &t.n_all, &t.m_all, s);
+  return t;
+}
+
+// A thread's share [i0, i1) of the list of non-empty bins, and what lies before it.
+template <int DTYPE>
+struct Bins {
+  static constexpr int SPAN = Geo<DTYPE>::kThreads * Geo<DTYPE>::kPer;
+  const unsigned* hist;
+  const uint16_t* list;
+  unsigned* digits;
+  int i0, i1;
+  unsigned cnt;
+  unsigned long long mass;
+  bool general;
+  // weight of one token (bf16) or of the whole bin (fp32)
+  __device__ __forceinline__ unsigned long long weight(int b, const WeightScale& ws, const unsigned long long* tab) const {
+    if (DTYPE == 0) return (static_cast<unsigned long long>(hist[2 * SPAN + b]) << 32) + hist[SPAN + b];
+    return b == kLowBin ? 0ull : weight_of(bin_value(b), ws, tab);
+  }
+};
+
+// A group of equal logits, what lies before it in the order, a token's weight.
+struct Group {
+  float z;
+  unsigned cnt;
+  unsigned long long mass, w;
+};
+
+// Block-wide: the group in which the order's count or weight reaches the target.
+template <int DTYPE>
+__device__ __noinline__ Group reach(const Row<DTYPE>& row, const WeightScale& ws, Bins<DTYPE>& bins, bool by_count,
+                                    unsigned long long target, Shared<Geo<DTYPE>::kThreads>& s) {
+  constexpr int kBitsAll = DTYPE == 1 ? 16 : 32;
+  Prefix g = {0u, 0ull, 0u};
+  if (bins.general) {
+    g = descend<DTYPE>(row, ws, by_count, target, g, kBitsAll, bins.digits, nullptr, -1, s);
+  } else {
+    unsigned c = bins.cnt;
+    unsigned long long m = bins.mass;
+    for (int i = bins.i0; i < bins.i1; ++i) {
+      if (by_count ? c >= target : m >= target) break;
+      const int b = bins.list[i];
+      const unsigned bc = bins.hist[b];
+      const unsigned long long w = bins.weight(b, ws, s.tab), bm = DTYPE == 1 ? bc * w : w;
+      if (by_count ? c + bc >= target : m + bm >= target) s.found = {c, m, static_cast<uint32_t>(b)};
+      c += bc;
+      m += bm;
+    }
+    __syncthreads();
+    g = s.found;
+    __syncthreads();
+    if (DTYPE == 1 && g.key != kLowBin) {
+      const float z = bin_value(g.key);
+      return {z, g.cnt, g.mass, weight_of(z, ws, s.tab)};
+    }
+    if (g.key == kLowBin) {
+      // among the logits below -2^8 (a count went there): their weights are zero, all digits are open.
+      // In bf16 the descent's histogram takes the list's place: later questions go the general way.
+      const Prefix low = {0u, 0ull, 0u};
+      g = descend<DTYPE>(row, ws, true, target, low, kBitsAll, bins.digits, nullptr, -1, s);
+      if (DTYPE == 1) bins.general = true;
+    } else {
+      const unsigned tokens = bins.hist[g.key];
+      g.key = bin_key16(g.key);
+      g = descend_bin<DTYPE>(row, ws, by_count, target, g, tokens, bins.digits, s);
+    }
+  }
+  const float z = key_value<DTYPE>(g.key);
+  return {z, g.cnt, g.mass, weight_of(z, ws, s.tab)};
+}
+
 template <int DTYPE>
 __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) sample_kernel_row(const SampleParams p) {
   using G = Geo<DTYPE>;
@@ -302,23 +443,18 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     k = 1;
   }
   if (tid < 64) s.tab[tid] = kExp2Table[tid];
-  if (tid == 0) s.fallback = 0;
+  if (tid == 0) {   // 64-bit floating point is slow here: one thread does what there is of it
+    s.fallback = 0;
+    const WeightScale w = weight_scale(0.f, T);
+    s.c_hi = w.c_hi;
+    s.c_lo = w.c_lo;
+    s.least = min_p > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(min_p) * kWeightOne)) : 0ull;
+  }
   const bool need_max = DTYPE == 0 || k == 1;
   const bool filter = p.filtered != nullptr;
 
   // the largest logit, where it is needed before the weights
-  float zmax = ninf();
-  if (need_max) {
-    walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, Raw (&x)[VEC]) {
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) zmax = fmaxf(zmax, value_of<DTYPE>(x[e]));   // fmaxf drops NaN
-    });
-    zmax = warp_max(zmax);
-    if (lane == 0) s.wmass[warp] = __float_as_uint(zmax);
-    __syncthreads();
-    for (int w = 0; w < NW; ++w) zmax = fmaxf(zmax, __uint_as_float(static_cast<unsigned>(s.wmass[w])));
-    __syncthreads();
-  }
+  float zmax = need_max ? row_max<DTYPE>(row, s) : ninf();
 
   // what the last pass needs: the drawn value and its rank among its equals, the cut's value and how
   // many of its equals are kept
@@ -333,19 +469,21 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     whole_ties = false;
     prob = any ? 1.f : 0.f;
   } else {
-    WeightScale ws = weight_scale(zmax, T);
-    const unsigned long long least =
-        min_p > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(min_p) * kWeightOne)) : 0ull;
     // histogram
     for (int i = tid; i < G::kHistWords / 4; i += NT) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
     __syncthreads();
+    WeightScale ws = {zmax, s.c_hi, s.c_lo};
+    const unsigned long long least = s.least;
     unsigned n_min = 0, n_all;
     unsigned long long m_min = 0, m_all;
     bool out_of_range = false;
     walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, Raw (&x)[VEC]) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const int b = bin_of<DTYPE>(x[e]);
+        const uint32_t top = DTYPE == 1 ? x[e] : static_cast<uint32_t>(x[e]) >> 16;
+        const int mi = static_cast<int>(top & 0x7fffu) - kMagLow;
+        int b = bin_in_range(mi, top & 0x8000u);
+        if (static_cast<unsigned>(mi) >= static_cast<unsigned>(kMags)) b = bin_other<DTYPE>(x[e]);
         if (b >= 0) {
           atomicAdd(&hist[b], 1u);
           if (DTYPE == 0) {
@@ -372,80 +510,36 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     __syncthreads();
     if (DTYPE == 1 && listed > 0) {
       zmax = bin_value(list[0]);
-      ws = weight_scale(zmax, T);
+      ws.zmax = zmax;
     }
+    Bins<DTYPE> bins;
+    const int share = (listed + NT - 1) / NT;
+    bins.hist = hist;
+    bins.list = list;
+    bins.digits = digits;
+    bins.i0 = min(static_cast<int>(listed), tid * share);
+    bins.i1 = min(static_cast<int>(listed), bins.i0 + share);
+    bins.cnt = 0u;
+    bins.mass = 0ull;
     // below -2^8 the weights have to be zero (one unknown weight would be wrong)
-    bool general = s.fallback || (listed > 0 && (list[0] == kLowBin || (hist[kLowBin] && weight_of(-256.f, ws, s.tab) != 0ull)));
-    const int share = (listed + NT - 1) / NT, i0 = min(static_cast<int>(listed), tid * share), i1 = min(static_cast<int>(listed), i0 + share);
-    auto bin_weight = [&](int b) -> unsigned long long {   // of one token (bf16) or the whole bin (fp32)
-      if (DTYPE == 0) return (static_cast<unsigned long long>(hist[2 * SPAN + b]) << 32) + hist[SPAN + b];
-      return b == kLowBin ? 0ull : weight_of(bin_value(b), ws, s.tab);
-    };
-    unsigned my_cnt = 0;
-    unsigned long long my_mass = 0;
-    if (!general) {
-      for (int i = i0; i < i1; ++i) {
+    bins.general = s.fallback || (listed > 0 && (list[0] == kLowBin || (hist[kLowBin] && weight_of(-256.f, ws, s.tab) != 0ull)));
+    if (!bins.general) {
+      for (int i = bins.i0; i < bins.i1; ++i) {
         const int b = list[i];
         const unsigned c = hist[b];
-        const unsigned long long w = bin_weight(b);
-        my_cnt += c;
-        my_mass += DTYPE == 1 ? c * w : w;
+        const unsigned long long w = bins.weight(b, ws, s.tab);
+        bins.cnt += c;
+        bins.mass += DTYPE == 1 ? c * w : w;
         if (DTYPE == 1 && w >= least) n_min += c, m_min += c * w;
       }
-      block_scan<NT>(my_cnt, my_mass, &n_all, &m_all, s);
-    }
-    // the list's group in which a count or a weight reaches the target
-    auto search = [&](bool by_count, unsigned long long target) -> Prefix {
-      unsigned c = my_cnt;
-      unsigned long long m = my_mass;
-      for (int i = i0; i < i1; ++i) {
-        if (by_count ? c >= target : m >= target) break;
-        const int b = list[i];
-        const unsigned bc = hist[b];
-        const unsigned long long bm = DTYPE == 1 ? bc * bin_weight(b) : bin_weight(b);
-        if (by_count ? c + bc >= target : m + bm >= target) s.found = {c, m, static_cast<uint32_t>(b)};
-        c += bc;
-        m += bm;
-      }
-      __syncthreads();
-      const Prefix f = s.found;
-      __syncthreads();
-      return f;
-    };
-    if (general) {
-      // the general way needs the maximum and the totals first
-      float top = ninf();
-      for (int u = tid; u < row.units; u += NT) {
-        Raw x[VEC];
-        row.load(u, x);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) top = fmaxf(top, value_of<DTYPE>(x[e]));
-      }
-      top = warp_max(top);
-      __syncthreads();
-      if (lane == 0) s.wmass[warp] = __float_as_uint(top);
-      __syncthreads();
-      for (int w = 0; w < NW; ++w) top = fmaxf(top, __uint_as_float(static_cast<unsigned>(s.wmass[w])));
-      __syncthreads();
-      ws = weight_scale(top, T);
-      n_min = 0;
-      m_min = 0;
-      unsigned c = 0;
-      unsigned long long m = 0;
-      for (int u = tid; u < row.units; u += NT) {
-        Raw x[VEC];
-        row.load(u, x);
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) {
-          const float z = value_of<DTYPE>(x[e]);
-          if (!(z > ninf())) continue;
-          const unsigned long long w = weight_of(z, ws, s.tab);
-          ++c;
-          m += w;
-          if (w >= least) ++n_min, m_min += w;
-        }
-      }
-      block_scan<NT>(c, m, &n_all, &m_all, s);
+      block_scan<NT>(bins.cnt, bins.mass, &n_all, &m_all, s);
+    } else {
+      ws.zmax = row_max<DTYPE>(row, s);
+      const Totals t = row_totals<DTYPE>(row, ws, least, s);
+      n_all = t.n_all;
+      m_all = t.m_all;
+      n_min = t.n_min;
+      m_min = t.m_min;
     }
     if (min_p > 0.f) {
       unsigned c = n_min;
@@ -454,53 +548,28 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     }
     any = n_all > 0;
     if (any) {
-      // the group of equal logits in which the order reaches a target: its value, and what lies before it
-      struct Group {
-        float z;
-        unsigned cnt;
-        unsigned long long mass, w;
-      };
-      auto reach = [&](bool by_count, unsigned long long target) -> Group {
-        Prefix g = {0u, 0ull, 0u};
-        if (general) {
-          g = descend<DTYPE>(row, ws, by_count, target, g, DTYPE == 1 ? 16 : 32, digits, nullptr, -1, s);
-        } else {
-          g = search(by_count, target);
-          if (DTYPE == 1 && g.key != kLowBin) {
-            const float z = bin_value(g.key);
-            return {z, g.cnt, g.mass, weight_of(z, ws, s.tab)};
-          }
-          if (g.key == kLowBin) {
-            // among the logits below -2^8 (a count went there): their weights are zero, all digits are open.
-            // In bf16 the descent's histogram takes the list's place: no search comes after it.
-            const Prefix low = {0u, 0ull, 0u};
-            g = descend<DTYPE>(row, ws, true, target, low, DTYPE == 1 ? 16 : 32, digits, nullptr, -1, s);
-            if (DTYPE == 1) general = true;
-          } else {
-            const unsigned tokens = hist[g.key];
-            g.key = bin_key16(g.key);
-            g = descend_bin<DTYPE>(row, ws, by_count, target, g, tokens, digits, s);
-          }
-        }
-        const float z = key_value<DTYPE>(g.key);
-        return {z, g.cnt, g.mass, weight_of(z, ws, s.tab)};
-      };
       n = n_all;
       unsigned long long mass = m_all;
       Group cut = {0.f, 0u, 0ull, 0ull};
       bool cut_known = false;
       if (k > 0 && static_cast<unsigned>(k) < n) {
-        cut = reach(true, k);
+        cut = reach<DTYPE>(row, ws, bins, true, k, s);
         cut_known = true;
         n = k;
         mass = cut.mass + (k - cut.cnt) * cut.w;
       }
       if (top_p < 1.f) {
-        const double goal = ceil(fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(mass));
-        unsigned long long target = goal < 1.0 ? 1ull : static_cast<unsigned long long>(goal);
-        if (target > mass) target = mass;
-        const Group g = reach(false, target);
-        const unsigned in = static_cast<unsigned>((target - g.mass + g.w - 1) / g.w);
+        if (tid == 0) {
+          const double goal = ceil(fmax(static_cast<double>(top_p), 0.0) * static_cast<double>(mass));
+          const unsigned long long t = goal < 1.0 ? 1ull : static_cast<unsigned long long>(goal);
+          s.target = t > mass ? mass : t;
+        }
+        __syncthreads();
+        const unsigned long long target = s.target;
+        const Group g = reach<DTYPE>(row, ws, bins, false, target, s);
+        if (tid == 0) s.group_in = static_cast<unsigned>((target - g.mass + g.w - 1) / g.w);
+        __syncthreads();
+        const unsigned in = s.group_in;
         if (g.cnt + in < n) {
           n = g.cnt + in;
           mass = g.mass + in * g.w;
@@ -514,18 +583,27 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         cut_known = false;
       }
       // the draw
-      const double td = uniform > 0.f ? floor(static_cast<double>(uniform) * static_cast<double>(mass)) : 0.0;
-      unsigned long long t = td >= static_cast<double>(mass) ? mass - 1 : static_cast<unsigned long long>(td);
-      if (t >= mass) t = mass - 1;
-      const Group g = reach(false, t + 1);
+      if (tid == 0) {
+        const double td = uniform > 0.f ? floor(static_cast<double>(uniform) * static_cast<double>(mass)) : 0.0;
+        const unsigned long long t = td >= static_cast<double>(mass) ? mass - 1 : static_cast<unsigned long long>(td);
+        s.target = (t >= mass ? mass - 1 : t) + 1;
+      }
+      __syncthreads();
+      const unsigned long long target = s.target;
+      const Group g = reach<DTYPE>(row, ws, bins, false, target, s);
+      if (tid == 0) {
+        s.group_in = static_cast<unsigned>((target - g.mass + g.w - 1) / g.w);
+        s.prob = static_cast<float>(static_cast<double>(g.w) / static_cast<double>(mass));
+      }
+      __syncthreads();
       z_draw = g.z;
-      rank = static_cast<unsigned>((t + 1 - g.mass + g.w - 1) / g.w) - 1;
-      prob = static_cast<float>(static_cast<double>(g.w) / static_cast<double>(mass));
+      rank = s.group_in - 1;
+      prob = s.prob;
       if (filter) {
         if (n == n_all) {
           z_cut = ninf();   // everything above -inf stays
         } else {
-          if (!cut_known) cut = reach(true, n);
+          if (!cut_known) cut = reach<DTYPE>(row, ws, bins, true, n, s);
           z_cut = cut.z;
           cut_eq = n - cut.cnt;
           whole_ties = false;
@@ -540,14 +618,19 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
   int token = -1;
   if (any) {
     unsigned eq = 0, eq_cut = 0;
+    const Compare<DTYPE> drawn(z_draw), cutoff(z_cut);
+    const bool ordered = filter && !whole_ties;
     walk<DTYPE, 4>(row, u0 + lane, u1, 32, [&](int, Raw (&x)[VEC]) {
+      uint32_t w[4];
+      memcpy(w, x, 16);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        const float z = value_of<DTYPE>(x[e]);
-        eq += z == z_draw;
-        eq_cut += z == z_cut;
+      for (int e = 0; e < 4; ++e) {
+        eq += drawn.eq(w[e]) & Compare<DTYPE>::kOnes;
+        if (ordered) eq_cut += cutoff.eq(w[e]) & Compare<DTYPE>::kOnes;
       }
     });
+    eq = Compare<DTYPE>::total(eq);
+    eq_cut = Compare<DTYPE>::total(eq_cut);
     eq = __reduce_add_sync(0xffffffffu, eq);
     eq_cut = __reduce_add_sync(0xffffffffu, eq_cut);
     if (lane == 0) s.wcnt[warp] = eq, s.wcnt2[warp] = eq_cut;
@@ -588,12 +671,10 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     }
     if (filter) {
       Raw* out = static_cast<Raw*>(p.filtered) + static_cast<long long>(r) * p.filtered_stride;
-      constexpr Raw kDrop = static_cast<Raw>(DTYPE == 1 ? 0xff80u : 0xff800000u);
       // 16-byte stores where the output row lies as the input row does
       const bool vec = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(row.p)) & 15u) == 0;
       unsigned seen = before_cut;   // equal to the cut before this step of the warp
-      const bool ordered = !whole_ties;
-      constexpr int kAhead = 4;   // loads in flight
+      constexpr int kAhead = 4;     // loads in flight
       for (int base = u0; base < u1; base += 32 * kAhead) {
         Raw x[kAhead][VEC];
 #pragma unroll
@@ -603,37 +684,51 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         for (int i = 0; i < kAhead; ++i) {
           const int u = base + i * 32 + lane;
           const bool in = u < u1;
-          unsigned here = 0;
+          uint32_t w[4] = {0u, 0u, 0u, 0u}, keep[4], tie[4] = {0u, 0u, 0u, 0u};
+          if (in) memcpy(w, x[i], 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) keep[e] = cutoff.gt(w[e]);
+          if (ordered) {
+            unsigned some = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              tie[e] = in ? cutoff.eq(w[e]) : 0u;
+              some |= tie[e];
+            }
+            if (__any_sync(0xffffffffu, some != 0u)) {
+              unsigned here = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) here += tie[e] & Compare<DTYPE>::kOnes;
+              here = Compare<DTYPE>::total(here);
+              unsigned incl = here;
+#pragma unroll
+              for (int o = 1; o < 32; o <<= 1) {
+                const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
+                if (lane >= o) incl += v;
+              }
+              unsigned rank_cut = seen + incl - here;
+              seen += __shfl_sync(0xffffffffu, incl, 31);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+#pragma unroll
+                for (int q = 0; q < VEC / 4; ++q) {   // the word's values in index order
+                  const unsigned part = DTYPE == 1 ? 0xffffu << (16 * q) : 0xffffffffu;
+                  if (tie[e] & part) {
+                    if (rank_cut < cut_eq) keep[e] |= part;
+                    ++rank_cut;
+                  }
+                }
+              }
+            }
+          }
           if (in) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(x[i][e]) == z_cut;
-          }
-          unsigned rank_cut = seen;
-          if (ordered && __any_sync(0xffffffffu, here != 0u)) {
-            unsigned incl = here;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-              const unsigned v = __shfl_up_sync(0xffffffffu, incl, o);
-              if (lane >= o) incl += v;
-            }
-            rank_cut = seen + incl - here;
-            seen += __shfl_sync(0xffffffffu, incl, 31);
-          }
-          if (in) {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) {
-              const float z = value_of<DTYPE>(x[i][e]);
-              const bool tie = z == z_cut;
-              const bool keep = z > z_cut || (ordered && tie && rank_cut < cut_eq);
-              rank_cut += tie;
-              if (!keep) x[i][e] = kDrop;
-            }
+            for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep[e]) | (Compare<DTYPE>::kDropWord & ~keep[e]);
             const int f = row.first(u), c = row.count(u);
             if (vec && u > 0 && c == VEC) {
-              uint4 v;
-              memcpy(&v, x[i], 16);
-              __stcs(reinterpret_cast<uint4*>(out + f), v);
+              __stcs(reinterpret_cast<uint4*>(out + f), make_uint4(w[0], w[1], w[2], w[3]));
             } else {
+              memcpy(x[i], w, 16);
 #pragma unroll
               for (int e = 0; e < VEC; ++e)
                 if (e < c) out[f + e] = x[i][e];
