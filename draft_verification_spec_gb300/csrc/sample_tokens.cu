@@ -106,39 +106,51 @@ struct Row {
   using Raw = typename Geo<DTYPE>::Raw;
   static constexpr int VEC = Geo<DTYPE>::kVec;
   const Raw* p;
-  int V, head, units;
+  int V, head, full, units;   // units 1 .. full are whole pieces
   __device__ __forceinline__ Row(const void* base, int v) : p(static_cast<const Raw*>(base)), V(v) {
     const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 15u) / static_cast<int>(sizeof(Raw));
     head = min(V, mis ? VEC - mis : 0);
-    units = 1 + (V - head + VEC - 1) / VEC;
+    full = (V - head) / VEC;
+    units = full + 2;
   }
+  __device__ __forceinline__ bool whole(int u) const { return u > 0 && u <= full; }
   __device__ __forceinline__ int first(int u) const { return u == 0 ? 0 : head + (u - 1) * VEC; }
   __device__ __forceinline__ int count(int u) const { return u == 0 ? head : min(VEC, V - first(u)); }
-  // the unit's values; places beyond its count hold -inf
-  __device__ __forceinline__ void load(int u, Raw (&x)[VEC]) const {
+  // the first or the last unit's values; places beyond its count hold -inf
+  __device__ __noinline__ uint4 edge(int u) const {
+    Raw x[VEC];
     const int i0 = first(u), n = count(u);
-    if (n == VEC && u > 0) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(p + i0));
-      memcpy(x, &v, 16);
-    } else {
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) x[e] = e < n ? __ldg(p + i0 + e) : static_cast<Raw>(DTYPE == 1 ? 0xff80u : 0xff800000u);
-    }
+    for (int e = 0; e < VEC; ++e) x[e] = e < n ? __ldg(p + i0 + e) : static_cast<Raw>(DTYPE == 1 ? 0xff80u : 0xff800000u);
+    uint4 v;
+    memcpy(&v, x, 16);
+    return v;
+  }
+  // a whole piece near unit u (for the edges any one; zeros if there is none): a load without a branch
+  __device__ __forceinline__ uint4 near(int u) const {
+    return full > 0 ? __ldg(reinterpret_cast<const uint4*>(p + head) + min(max(u - 1, 0), full - 1)) : make_uint4(0u, 0u, 0u, 0u);
+  }
+  __device__ __forceinline__ uint4 load(int u) const { return whole(u) ? near(u) : edge(u); }
+  static __device__ __forceinline__ Raw value(const uint4& v, int e) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    return DTYPE == 1 ? static_cast<Raw>(w[e / 2] >> (16 * (e & 1))) : static_cast<Raw>(w[e & 3]);
   }
 };
 
-// f(unit, values) for the units [begin, end) in steps of `stride`, BATCH loads in flight at a time.
+// f(unit, piece) for the units [begin, end) in steps of `stride`, BATCH loads in flight at a time.
 template <int DTYPE, int BATCH, typename F>
 __device__ __forceinline__ void walk(const Row<DTYPE>& row, int begin, int end, int stride, F f) {
-  constexpr int VEC = Geo<DTYPE>::kVec;
   for (int u = begin; u < end; u += BATCH * stride) {
-    typename Row<DTYPE>::Raw x[BATCH][VEC];
+    uint4 x[BATCH];
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i)
-      if (u + i * stride < end) row.load(u + i * stride, x[i]);
+    for (int i = 0; i < BATCH; ++i) x[i] = row.near(u + i * stride);
 #pragma unroll
-    for (int i = 0; i < BATCH; ++i)
-      if (u + i * stride < end) f(u + i * stride, x[i]);
+    for (int i = 0; i < BATCH; ++i) {
+      const int at = u + i * stride;
+      if (at >= end) break;
+      if (!row.whole(at)) x[i] = row.edge(at);
+      f(at, x[i]);
+    }
   }
 }
 
@@ -248,10 +260,10 @@ __device__ __noinline__ Prefix descend(const Row<DTYPE>& row, const WeightScale&
     if (gathered >= 0) {
       for (int i = tid; i < gathered; i += NT) take(keys[i], key_value<DTYPE>(keys[i]));
     } else {
-      walk<DTYPE, 2>(row, tid, row.units, NT, [&](int, typename Row<DTYPE>::Raw (&x)[VEC]) {
+      walk<DTYPE, 2>(row, tid, row.units, NT, [&](int, const uint4& piece) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
-          const float z = value_of<DTYPE>(x[e]);
+          const float z = value_of<DTYPE>(Row<DTYPE>::value(piece, e));
           take(sample_key<DTYPE>(z), z);
         }
       });
@@ -296,10 +308,10 @@ __device__ __noinline__ Prefix descend_bin(const Row<DTYPE>& row, const WeightSc
   if (tokens > kGather) return descend<DTYPE>(row, ws, by_count, target, at, 16, digits, nullptr, -1, s);
   if (threadIdx.x == 0) s.gathered = 0u;
   __syncthreads();
-  walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, typename Row<DTYPE>::Raw (&x)[VEC]) {
+  walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, const uint4& piece) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const uint32_t key = sample_key<DTYPE>(value_of<DTYPE>(x[e]));
+      const uint32_t key = sample_key<DTYPE>(value_of<DTYPE>(Row<DTYPE>::value(piece, e)));
       if (key >> 16 == at.key) keys[atomicAdd(&s.gathered, 1u)] = key;
     }
   });
@@ -312,9 +324,9 @@ template <int DTYPE>
 __device__ __noinline__ float row_max(const Row<DTYPE>& row, Shared<Geo<DTYPE>::kThreads>& s) {
   constexpr int NT = Geo<DTYPE>::kThreads, VEC = Geo<DTYPE>::kVec;
   float top = ninf();
-  walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, typename Row<DTYPE>::Raw (&x)[VEC]) {
+  walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, const uint4& piece) {
 #pragma unroll
-    for (int e = 0; e < VEC; ++e) top = fmaxf(top, value_of<DTYPE>(x[e]));
+    for (int e = 0; e < VEC; ++e) top = fmaxf(top, value_of<DTYPE>(Row<DTYPE>::value(piece, e)));
   });
   top = warp_max(top);
   __syncthreads();
@@ -336,10 +348,10 @@ __device__ __noinline__ Totals row_totals(const Row<DTYPE>& row, const WeightSca
                                           Shared<Geo<DTYPE>::kThreads>& s) {
   constexpr int NT = Geo<DTYPE>::kThreads, VEC = Geo<DTYPE>::kVec;
   Totals t = {0u, 0u, 0ull, 0ull};
-  walk<DTYPE, 1>(row, threadIdx.x, row.units, NT, [&](int, typename Row<DTYPE>::Raw (&x)[VEC]) {
+  walk<DTYPE, 1>(row, threadIdx.x, row.units, NT, [&](int, const uint4& piece) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const float z = value_of<DTYPE>(x[e]);
+      const float z = value_of<DTYPE>(Row<DTYPE>::value(piece, e));
       if (!(z > ninf())) continue;
       const unsigned long long w = weight_of(z, ws, s.tab);
       ++t.n_all;
@@ -477,17 +489,18 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     unsigned n_min = 0, n_all;
     unsigned long long m_min = 0, m_all;
     bool out_of_range = false;
-    walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, Raw (&x)[VEC]) {
+    walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, const uint4& piece) {
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const uint32_t top = DTYPE == 1 ? x[e] : static_cast<uint32_t>(x[e]) >> 16;
+        const Raw x = Row<DTYPE>::value(piece, e);
+        const uint32_t top = DTYPE == 1 ? x : static_cast<uint32_t>(x) >> 16;
         const int mi = static_cast<int>(top & 0x7fffu) - kMagLow;
         int b = bin_in_range(mi, top & 0x8000u);
-        if (static_cast<unsigned>(mi) >= static_cast<unsigned>(kMags)) b = bin_other<DTYPE>(x[e]);
+        if (static_cast<unsigned>(mi) >= static_cast<unsigned>(kMags)) b = bin_other<DTYPE>(x);
         if (b >= 0) {
           atomicAdd(&hist[b], 1u);
           if (DTYPE == 0) {
-            const unsigned long long w = weight_of(value_of<DTYPE>(x[e]), ws, s.tab);
+            const unsigned long long w = weight_of(value_of<DTYPE>(x), ws, s.tab);
             if (w) add_weight(&hist[SPAN + b], &hist[2 * SPAN + b], w);
             if (w >= least) ++n_min, m_min += w;
           }
@@ -620,9 +633,8 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     unsigned eq = 0, eq_cut = 0;
     const Compare<DTYPE> drawn(z_draw), cutoff(z_cut);
     const bool ordered = filter && !whole_ties;
-    walk<DTYPE, 4>(row, u0 + lane, u1, 32, [&](int, Raw (&x)[VEC]) {
-      uint32_t w[4];
-      memcpy(w, x, 16);
+    walk<DTYPE, 4>(row, u0 + lane, u1, 32, [&](int, const uint4& piece) {
+      const uint32_t w[4] = {piece.x, piece.y, piece.z, piece.w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         eq += drawn.eq(w[e]) & Compare<DTYPE>::kOnes;
@@ -650,10 +662,9 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       unsigned here = 0, all;
       unsigned long long none = 0, none_all;
       for (int u = a0; u < a1; ++u) {
-        Raw x[VEC];
-        row.load(u, x);
+        const uint4 piece = row.load(u);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(x[e]) == z_draw;
+        for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(Row<DTYPE>::value(piece, e)) == z_draw;
       }
       unsigned first = here;
       block_scan<NT>(first, none, &all, &none_all, s);
@@ -661,11 +672,10 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       if (want >= first && want < first + here) {
         unsigned skip = want - first;
         for (int u = a0; u < a1; ++u) {
-          Raw x[VEC];
-          row.load(u, x);
+          const uint4 piece = row.load(u);
 #pragma unroll
           for (int e = 0; e < VEC; ++e)
-            if (value_of<DTYPE>(x[e]) == z_draw && skip-- == 0) s.token = row.first(u) + e;
+            if (value_of<DTYPE>(Row<DTYPE>::value(piece, e)) == z_draw && skip-- == 0) s.token = row.first(u) + e;
         }
       }
     }
@@ -676,16 +686,15 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       unsigned seen = before_cut;   // equal to the cut before this step of the warp
       constexpr int kAhead = 4;     // loads in flight
       for (int base = u0; base < u1; base += 32 * kAhead) {
-        Raw x[kAhead][VEC];
+        uint4 x[kAhead];
 #pragma unroll
-        for (int i = 0; i < kAhead; ++i)
-          if (base + i * 32 + lane < u1) row.load(base + i * 32 + lane, x[i]);
+        for (int i = 0; i < kAhead; ++i) x[i] = row.near(base + i * 32 + lane);
 #pragma unroll
         for (int i = 0; i < kAhead; ++i) {
           const int u = base + i * 32 + lane;
           const bool in = u < u1;
-          uint32_t w[4] = {0u, 0u, 0u, 0u}, keep[4], tie[4] = {0u, 0u, 0u, 0u};
-          if (in) memcpy(w, x[i], 16);
+          if (in && !row.whole(u)) x[i] = row.edge(u);
+          uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w}, keep[4], tie[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
           for (int e = 0; e < 4; ++e) keep[e] = cutoff.gt(w[e]);
           if (ordered) {
@@ -724,14 +733,15 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
           if (in) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) w[e] = (w[e] & keep[e]) | (Compare<DTYPE>::kDropWord & ~keep[e]);
-            const int f = row.first(u), c = row.count(u);
-            if (vec && u > 0 && c == VEC) {
-              __stcs(reinterpret_cast<uint4*>(out + f), make_uint4(w[0], w[1], w[2], w[3]));
+            const uint4 piece = make_uint4(w[0], w[1], w[2], w[3]);
+            const int f = row.first(u);
+            if (vec && row.whole(u)) {
+              __stcs(reinterpret_cast<uint4*>(out + f), piece);
             } else {
-              memcpy(x[i], w, 16);
+              const int c = row.count(u);
 #pragma unroll
               for (int e = 0; e < VEC; ++e)
-                if (e < c) out[f + e] = x[i][e];
+                if (e < c) out[f + e] = Row<DTYPE>::value(piece, e);
             }
           }
         }
