@@ -54,7 +54,7 @@ struct Geo<0> {   // fp32: counts and weights
   static constexpr int kHistWords = 3 * kThreads * kPer;
   static constexpr int kDigitWords = 3 * kBins + kGather;
 };
-static_assert(Geo<1>::kThreads * Geo<1>::kPer >= kHist && Geo<0>::kThreads * Geo<0>::kPer >= kHist, "every bin has a thread");
+static_assert(Geo<1>::kThreads * Geo<1>::kPer > kHist && Geo<0>::kThreads * Geo<0>::kPer > kHist, "every bin has a thread");
 static_assert(Geo<1>::kHistWords >= 3 * kBins, "the general descent fits the histogram");
 
 template <int DTYPE>
@@ -78,13 +78,20 @@ __device__ __forceinline__ float key_value(uint32_t k) {
   return __uint_as_float((k & 0x80000000u) ? (k & 0x7fffffffu) : ~k);
 }
 
-// Bin of a logit whose magnitude is in the bins' range (mi = its place there); of the others: zero, those
-// below -2^8, -1 for -inf and NaN (never drawn), -2 for what has no bin.
-__device__ __forceinline__ int bin_in_range(int mi, bool neg) { return neg ? kZeroBin + 1 + mi : kZeroBin - 1 - mi; }
+// Bins are numbered in the order's direction; in the histogram, where the fast path has three
+// instructions for a logit's place, the positive magnitudes come first, then the negative ones, zero
+// and those below -2^8.
+__device__ __forceinline__ int place_of(int bin) {
+  return bin < kZeroBin ? kZeroBin - 1 - bin : bin == kZeroBin ? 2 * kMags : bin == kLowBin ? kLowBin : bin - 1;
+}
+__device__ __forceinline__ unsigned place_in_range(uint32_t top) {   // top: 16 bits, magnitude in the bins' range
+  return top + (top >> 15) * static_cast<unsigned>(kMags - 0x8000) - kMagLow;
+}
+// Of the other logits: zero, those below -2^8; -1 for -inf and NaN (never drawn), -2 for what has no bin.
 template <int DTYPE>
-__device__ __forceinline__ int bin_other(typename Geo<DTYPE>::Raw b) {
+__device__ __forceinline__ int place_other(typename Geo<DTYPE>::Raw b) {
   const uint32_t bits = DTYPE == 1 ? static_cast<uint32_t>(b) << 16 : static_cast<uint32_t>(b), mag = bits & 0x7fffffffu;
-  if (mag == 0u) return kZeroBin;
+  if (mag == 0u) return 2 * kMags;
   if (mag > 0x7f800000u || bits == 0xff800000u) return -1;
   return static_cast<int>(mag >> 16) >= kMagLow + kMags && (bits >> 31) ? kLowBin : -2;
 }
@@ -378,7 +385,7 @@ struct Bins {
   bool general;
   // weight of one token (bf16) or of the whole bin (fp32)
   __device__ __forceinline__ unsigned long long weight(int b, const WeightScale& ws, const unsigned long long* tab) const {
-    if (DTYPE == 0) return (static_cast<unsigned long long>(hist[2 * SPAN + b]) << 32) + hist[SPAN + b];
+    if (DTYPE == 0) return (static_cast<unsigned long long>(hist[2 * SPAN + place_of(b)]) << 32) + hist[SPAN + place_of(b)];
     return b == kLowBin ? 0ull : weight_of(bin_value(b), ws, tab);
   }
 };
@@ -404,7 +411,7 @@ __device__ __noinline__ Group reach(const Row<DTYPE>& row, const WeightScale& ws
     for (int i = bins.i0; i < bins.i1; ++i) {
       if (by_count ? c >= target : m >= target) break;
       const int b = bins.list[i];
-      const unsigned bc = bins.hist[b];
+      const unsigned bc = bins.hist[place_of(b)];
       const unsigned long long w = bins.weight(b, ws, s.tab), bm = DTYPE == 1 ? bc * w : w;
       if (by_count ? c + bc >= target : m + bm >= target) s.found = {c, m, static_cast<uint32_t>(b)};
       c += bc;
@@ -424,7 +431,7 @@ __device__ __noinline__ Group reach(const Row<DTYPE>& row, const WeightScale& ws
       g = descend<DTYPE>(row, ws, true, target, low, kBitsAll, bins.digits, nullptr, -1, s);
       if (DTYPE == 1) bins.general = true;
     } else {
-      const unsigned tokens = bins.hist[g.key];
+      const unsigned tokens = bins.hist[place_of(g.key)];
       g.key = bin_key16(g.key);
       g = descend_bin<DTYPE>(row, ws, by_count, target, g, tokens, bins.digits, s);
     }
@@ -489,37 +496,53 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     unsigned n_min = 0, n_all;
     unsigned long long m_min = 0, m_all;
     bool out_of_range = false;
+    auto count = [&](Raw x, unsigned at) {
+      atomicAdd(&hist[at], 1u);
+      if (DTYPE == 0) {
+        const unsigned long long w = weight_of(value_of<DTYPE>(x), ws, s.tab);
+        if (w) add_weight(&hist[SPAN + at], &hist[2 * SPAN + at], w);
+        if (w >= least) ++n_min, m_min += w;
+      }
+    };
     walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, const uint4& piece) {
+      bool fast = true;   // all of the piece in the bins' range
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
-        const Raw x = Row<DTYPE>::value(piece, e);
-        const uint32_t top = DTYPE == 1 ? x : static_cast<uint32_t>(x) >> 16;
-        const int mi = static_cast<int>(top & 0x7fffu) - kMagLow;
-        int b = bin_in_range(mi, top & 0x8000u);
-        if (static_cast<unsigned>(mi) >= static_cast<unsigned>(kMags)) b = bin_other<DTYPE>(x);
-        if (b >= 0) {
-          atomicAdd(&hist[b], 1u);
-          if (DTYPE == 0) {
-            const unsigned long long w = weight_of(value_of<DTYPE>(x), ws, s.tab);
-            if (w) add_weight(&hist[SPAN + b], &hist[2 * SPAN + b], w);
-            if (w >= least) ++n_min, m_min += w;
-          }
+        const uint32_t x = Row<DTYPE>::value(piece, e), top = DTYPE == 1 ? x : x >> 16;
+        fast = fast && (top & 0x7fffu) - kMagLow < static_cast<unsigned>(kMags);
+      }
+      if (fast) {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) {
+          const Raw x = Row<DTYPE>::value(piece, e);
+          count(x, place_in_range(DTYPE == 1 ? x : static_cast<uint32_t>(x) >> 16));
         }
-        out_of_range |= b == -2;
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < VEC; ++e) {
+          const uint32_t word = DTYPE == 1 ? (e < 4 ? (e < 2 ? piece.x : piece.y) : (e < 6 ? piece.z : piece.w)) >> (16 * (e & 1))
+                                           : (e < 2 ? (e < 1 ? piece.x : piece.y) : (e < 3 ? piece.z : piece.w));
+          const Raw x = static_cast<Raw>(word);
+          const uint32_t top = DTYPE == 1 ? x : static_cast<uint32_t>(x) >> 16;
+          const int at = (top & 0x7fffu) - kMagLow < static_cast<unsigned>(kMags) ? static_cast<int>(place_in_range(top)) : place_other<DTYPE>(x);
+          if (at >= 0) count(x, at);
+          out_of_range |= at == -2;
+        }
       }
     });
     if (out_of_range) s.fallback = 1;
     __syncthreads();
     // the non-empty bins, in order
-    unsigned filled = 0, listed;
+    unsigned filled = 0, listed;   // this thread's bins that are not empty
     unsigned long long none = 0, none_all;
 #pragma unroll
-    for (int e = 0; e < PER; ++e) filled += hist[tid * PER + e] != 0u;
-    unsigned at = filled;
+    for (int e = 0; e < PER; ++e) {
+      const int bin = min(tid * PER + e, kHist);   // the word behind the bins is zero
+      filled |= (hist[bin == kHist ? kHist : place_of(bin)] != 0u ? 1u : 0u) << e;
+    }
+    unsigned at = __popc(filled);
     block_scan<NT>(at, none, &listed, &none_all, s);
-#pragma unroll
-    for (int e = 0; e < PER; ++e)
-      if (hist[tid * PER + e]) list[at++] = static_cast<uint16_t>(tid * PER + e);
+    for (unsigned left = filled; left; left &= left - 1) list[at++] = static_cast<uint16_t>(tid * PER + __ffs(left) - 1);
     __syncthreads();
     if (DTYPE == 1 && listed > 0) {
       zmax = bin_value(list[0]);
@@ -539,7 +562,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     if (!bins.general) {
       for (int i = bins.i0; i < bins.i1; ++i) {
         const int b = list[i];
-        const unsigned c = hist[b];
+        const unsigned c = hist[place_of(b)];
         const unsigned long long w = bins.weight(b, ws, s.tab);
         bins.cnt += c;
         bins.mass += DTYPE == 1 ? c * w : w;
