@@ -6,6 +6,9 @@
 
 #include "attention_tc.cuh"
 
+#ifndef TC_ROWS
+#define TC_ROWS 64
+#endif
 namespace sv {
 
 template <>
@@ -13,9 +16,9 @@ const void* attn_mma_fn<true>(int dp, int bm);
 template <>
 const void* attn_mma_fn<false>(int dp, int bm);
 template <>
-const void* attn_tc_fn<true>(int dp);
+const void* attn_tc_fn<true>(int dp, bool wide);
 template <>
-const void* attn_tc_fn<false>(int dp);
+const void* attn_tc_fn<false>(int dp, bool wide);
 
 // One warp per row of the item that begins in CTA blockIdx.x's run and goes on in others': the
 // partials in key order, each scaled by 2^(its maximum - the largest).  fp32.
@@ -99,34 +102,35 @@ static cudaError_t resident(const void* fn, int threads, int smem, int* out) {
 }
 
 static const void* kernel_of(bool bf16, const AttnPlan& plan) {
-  if (plan.kind == 2) return bf16 ? attn_tc_fn<true>(plan.dp) : attn_tc_fn<false>(plan.dp);
+  if (plan.kind >= 2) return bf16 ? attn_tc_fn<true>(plan.dp, plan.kind == 3) : attn_tc_fn<false>(plan.dp, plan.kind == 3);
   return bf16 ? attn_mma_fn<true>(plan.dp, plan.bm) : attn_mma_fn<false>(plan.dp, plan.bm);
 }
 
 cudaError_t attention_plan(bool bf16, int kind, int D, int sms, AttnPlan* plan) {
   plan->kind = kind;
-  plan->bm = kind == 0 ? 16 : kind == 1 ? 64 : kTcBM;
-  plan->bn = kind == 2 ? kTcBN : kAttnBN;
+  plan->bm = kind == 0 ? 16 : kind == 1 ? 64 : kind == 2 ? 128 : 256;
+  plan->bn = kind >= 2 ? kTcBN : kAttnBN;
   plan->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
   int threads = kAttnThreads;
-  if (kind == 2) {
-    plan->smem = plan->dp == 64 ? AttnTcGeom<64>::kSmem : AttnTcGeom<128>::kSmem;
+  if (kind >= 2) {
+    plan->smem = kind == 2 ? (plan->dp == 64 ? AttnTcGeom<64, false>::kSmem : AttnTcGeom<128, false>::kSmem)
+                           : (plan->dp == 64 ? AttnTcGeom<64, true>::kSmem : AttnTcGeom<128, true>::kSmem);
     threads = kTcThreads;
   } else {
     plan->smem = bf16 ? attn_mma_smem<true>(plan->dp, plan->bm) : attn_mma_smem<false>(plan->dp, plan->bm);
   }
   int occ = 0;
   const cudaError_t e = resident(kernel_of(bf16, *plan), threads, plan->smem, &occ);
-  plan->grid = sms * (kind == 2 ? 1 : occ);   // the tcgen05 kernel takes all of an SM's TMEM
+  plan->grid = sms * (kind >= 2 ? 1 : occ);   // the tcgen05 kernel takes all of an SM's TMEM
   return e;
 }
 
 // The 16-row kernel where the rows of a request and key head fit one tile; the tcgen05 kernel where
 // they are more than 64, heads are of 64 to 128 values and pages are whole TMA boxes; else 64-row tiles.
 int attention_kind(int rows, int D, int page_size, float scale) {
-  if (rows <= 16) return 0;
   const bool pow2 = (page_size & (page_size - 1)) == 0;
-  return rows > 64 && D >= 64 && D <= 128 && pow2 && page_size >= 8 && scale > 0.f ? 2 : 1;
+  if (rows > TC_ROWS && D >= 64 && D <= 128 && pow2 && page_size >= 8 && scale > 0.f) return rows > 128 ? 3 : 2;
+  return rows <= 16 ? 0 : 1;
 }
 
 // cuTensorMapEncodeTiled, looked up once through the runtime (the library does not link the driver).
@@ -172,8 +176,8 @@ cudaError_t launch_attention(bool bf16, const AttnPlan& plan, const AttnParams& 
   AttnMaps m = maps;
   void* tc[] = {m.k, m.v, &copy};
   void* mma[] = {&copy};
-  return cudaLaunchKernel(kernel_of(bf16, plan), dim3(plan.grid), dim3(plan.kind == 2 ? kTcThreads : kAttnThreads),
-                          plan.kind == 2 ? tc : mma, plan.smem, stream);
+  return cudaLaunchKernel(kernel_of(bf16, plan), dim3(plan.grid), dim3(plan.kind >= 2 ? kTcThreads : kAttnThreads),
+                          plan.kind >= 2 ? tc : mma, plan.smem, stream);
 }
 
 cudaError_t launch_attention_combine(int dtype, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream) {

@@ -1,19 +1,23 @@
-// Attention of new tokens over a paged cache, tcgen05 kernel: 256-row tiles, pages that TMA can copy.
+// Attention of new tokens over a paged cache, tcgen05 kernel: pages that TMA can copy, heads of 64 to
+// 128 values.
 //
-// One CTA per SM works through its run of (item, key tile) units.  A tile's 256 rows are two halves
-// of 128 (the M of one MMA) that share every key tile of 128 keys.  Ten warps:
+// One CTA per SM works through its run of (item, key tile) units, 128 keys a tile.  Ten warps:
 //   0-3, 4-7  softmax of half 0 and 1: a thread owns a row (TMEM lane): reads the row's 128 scores,
 //             keeps the running maximum and sum, writes the probabilities back over the scores as
 //             the second MMA's A operand, and rescales O in TMEM;
 //   8         TMA producer: one box per page, head and 64 dims, 128-byte swizzle;
 //   9         MMA issuer: S = Q K^T (both operands in shared memory) and O += P V (P in TMEM).
-// The two halves alternate: while one half's softmax runs, the tensor core works on the other's.
-// TMEM (512 columns): S0 | S1 | O0 | O1, P_i in S_i's columns.
+// TMEM (512 columns): S0 | S1 | O0 | O1, P_i in S_i's columns.  The two halves alternate: while one
+// half's softmax runs, the tensor core works on the other's.  With more than 128 rows an item's halves
+// are its rows 0-127 and 128-255, which share every key tile; with fewer they are the same rows over
+// the even and the odd key tiles, joined at the end.  (One half alone would leave the tensor core, the
+// softmax and the copies waiting for one another.)
 //
 // O is rescaled only when a row's maximum grows by more than 2^8 over the reference its exponentials
 // use; until then the probabilities may reach 2^8, which neither type overflows and the final division
-// by the sum undoes.  S(j) is committed after P V(j-1) of the same half in issue order, so a softmax
-// thread that has seen S(j) may touch O.
+// by the sum undoes.  S(j) is committed after the same half's previous P V in issue order, so a softmax
+// thread that has seen S(j) may touch O.  P V starts on the first 64 keys while the softmax is at the
+// others.
 //
 // Keys at or beyond the item's last one: pages that lie wholly there are read at an out-of-range page
 // coordinate, which TMA fills with zeros; the rest of the last page can hold anything, so its value
@@ -32,17 +36,22 @@
 namespace sv {
 
 constexpr int kTcThreads = 320;
-constexpr int kTcBN = 128, kTcBM = 256;
+constexpr int kTcBN = 128;
 
-template <int DP>
+// WIDE: row tiles of 256 (else 128), which take a second 128-row query buffer.
+template <int DP, bool WIDE>
 struct AttnTcGeom {
-  static constexpr int kTile = 128 * DP * 2;                 // one half's Q, one tile's K or V
-  static constexpr int kKStages = DP == 64 ? 4 : 3, kVStages = DP == 64 ? 4 : 2;
-  static constexpr int kSmem = 1024 + (2 + kKStages + kVStages) * kTile;
+  static constexpr int kBM = WIDE ? 256 : 128;
+  static constexpr int kTile = 128 * DP * 2;                 // 128 rows of Q, one tile's K or V
+  static constexpr int kKStages = DP == 64 ? 5 : 3, kVStages = DP == 64 ? 5 : WIDE ? 2 : 3;
+  static constexpr int kSmem = 1024 + (kBM / 128 + kKStages + kVStages) * kTile;
 };
 
 struct AttnTcBars {
-  unsigned long long k_full[4], k_empty[4], v_full[4], v_empty[4], s_full[2], p_full[2], o_full[2], q_full[2], drain;
+  unsigned long long k_full[5], k_empty[5], v_full[5], v_empty[5];
+  unsigned long long s_full[2], p_first[2], p_full[2], o_full[2], q_full[2];
+  unsigned long long x_full, x_free;   // half 1's share of a joined item: there, and read
+  unsigned long long drain;
 };
 
 // ------------------------------------------------------------------------------------ PTX wrappers
@@ -65,11 +74,26 @@ __device__ __forceinline__ void tc_commit(uint32_t bar) {
 }
 __device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for this thread's TMEM loads; the registers pass through it, so that nothing reads them earlier.
+__device__ __forceinline__ void tc_wait_ld(uint32_t* r) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void mbar_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+// True in one lane of a converged warp, the same one every time.  (The compiler knows that a branch on
+// it runs in one lane and keeps the operands of what is issued there in uniform registers.)
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// One arrival for the warp, after all its lanes.
+__device__ __forceinline__ void mbar_arrive_warp(uint32_t bar) {
+  __syncwarp();
+  if (elected()) asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 // 32 consecutive columns of this thread's TMEM lane.
 __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t* r) {
@@ -82,6 +106,13 @@ __device__ __forceinline__ void tc_ld32(uint32_t addr, uint32_t* r) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
+__device__ __forceinline__ void tc_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
@@ -91,6 +122,23 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
+}
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t f2_pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ void f2_unpack(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t f2_fma(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t f2_add(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
 }
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int d, int token, int head, int page,
                                         uint32_t bar) {
@@ -111,13 +159,23 @@ struct TcWait {
   volatile int* abort;
   long long limit;
   int32_t* status;
-  // Waits for the phase; false once the limit has passed or another warp gave up.
+  // Waits for the phase; false once the limit has passed or another warp gave up.  The clock (whose read
+  // takes longer than most waits) is looked at only after a thousand polls.
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
-    if (mbar_try(bar, parity)) return true;
+#pragma unroll 1
+    for (int k = 0; k < 1024; ++k)
+      if (mbar_try(bar, parity)) return true;
+    return slowly(bar, parity);
+  }
+  // The same for a whole warp.
+  __device__ __forceinline__ bool warp(uint32_t bar, uint32_t parity) const {
+    return __all_sync(0xffffffffu, (*this)(bar, parity)) != 0;
+  }
+  __device__ __noinline__ bool slowly(uint32_t bar, uint32_t parity) const {
     const unsigned long long t0 = global_ns();
     while (true) {
 #pragma unroll 1
-      for (int k = 0; k < 16; ++k)
+      for (int k = 0; k < 256; ++k)
         if (mbar_try(bar, parity)) return true;
       if (*abort) return false;
       if (static_cast<long long>(global_ns() - t0) > limit) {
@@ -129,21 +187,22 @@ struct TcWait {
   }
 };
 
-template <bool BF16, int DP>
+template <bool BF16, int DP, bool WIDE>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   using A = AttnType<BF16>;
-  using Geo = AttnTcGeom<DP>;
-  constexpr int BM = kTcBM, BN = kTcBN, SUB = DP / 64, KST = Geo::kKStages, VST = Geo::kVStages, TILE = Geo::kTile;
+  using Geo = AttnTcGeom<DP, WIDE>;
+  constexpr int BM = Geo::kBM, BN = kTcBN, SUB = DP / 64, KST = Geo::kKStages, VST = Geo::kVStages, TILE = Geo::kTile;
   extern __shared__ uint8_t smem_raw[];
   __shared__ AttnSchedSmem<kTcThreads> sched;
   __shared__ __align__(8) AttnTcBars bars;
+  __shared__ float2 s_ml[128];
   __shared__ uint32_t s_tmem;
   __shared__ int s_abort;
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
-  const uint32_t s_q = base, s_k = base + 2 * TILE, s_v = s_k + KST * TILE;
+  const uint32_t s_q = base, s_k = base + (BM / 128) * TILE, s_v = s_k + KST * TILE;
 
   const AttnSplit split = attn_split<BN>(p, BM, sched);
   const int cta = blockIdx.x;
@@ -154,7 +213,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
   if (tid == 0) {
     s_abort = 0;
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 5; ++i) {
       mbar_init(smem_addr(&bars.k_full[i]), 1);
       mbar_init(smem_addr(&bars.k_empty[i]), 1);
       mbar_init(smem_addr(&bars.v_full[i]), 1);
@@ -162,10 +221,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.s_full[i]), 1);
-      mbar_init(smem_addr(&bars.p_full[i]), 128);
+      mbar_init(smem_addr(&bars.p_first[i]), 4);
+      mbar_init(smem_addr(&bars.p_full[i]), 4);
       mbar_init(smem_addr(&bars.o_full[i]), 1);
-      mbar_init(smem_addr(&bars.q_full[i]), 128);
+      mbar_init(smem_addr(&bars.q_full[i]), 4);
     }
+    mbar_init(smem_addr(&bars.x_full), 4);
+    mbar_init(smem_addr(&bars.x_free), 4);
     mbar_init(smem_addr(&bars.drain), 1);
     mbar_fence_init();
   }
@@ -210,9 +272,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const uint32_t ph = which ? (g / VST) & 1 : (g / KST) & 1;
           const uint32_t full = smem_addr(which ? &bars.v_full[st] : &bars.k_full[st]);
           const uint32_t empty = smem_addr(which ? &bars.v_empty[st] : &bars.k_empty[st]);
-          ok = __all_sync(0xffffffffu, ok && wait(empty, ph ^ 1));
+          ok = wait.warp(empty, ph ^ 1);
           if (!ok) break;
-          if (lane == 0) mbar_arrive_tx(full, TILE);
+          if (elected()) mbar_arrive_tx(full, TILE);
           __syncwarp();
           if (lane < boxes) {
             const uint32_t dst = (which ? s_v : s_k) + st * TILE + lane * rows * 128;
@@ -241,43 +303,61 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t kCommon = (1u << 4) | (kType << 7) | (kType << 10) | ((128u >> 4) << 24);
     constexpr uint32_t kIdescS = kCommon | ((128u >> 3) << 17);
     constexpr uint32_t kIdescO = kCommon | (1u << 16) | ((static_cast<uint32_t>(DP) >> 3) << 17);
-    unsigned g = 0, nh_tiles[2] = {0, 0}, segs[2] = {0, 0};
+    unsigned g = 0, done[2] = {0, 0}, segs[2] = {0, 0};   // key tiles so far; tiles and items per half
     bool ok = true;
-    auto issue_s = [&](int half, int st) {
+    auto issue_s = [&](int half, int q, int st) {
 #pragma unroll
       for (int k = 0; k < DP / 16; ++k) {
         const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-        tc_mma_ss(tmem + half * 128, tc_desc(s_q + half * TILE + off, 16), tc_desc(s_k + st * TILE + off, 16), kIdescS, k > 0);
+        tc_mma_ss(tmem + half * 128, tc_desc(s_q + q * TILE + off, 16), tc_desc(s_k + st * TILE + off, 16), kIdescS, k > 0);
       }
+      tc_commit(smem_addr(&bars.s_full[half]));
     };
-    auto issue_o = [&](int half, int st, bool acc) {
+    // O += P V of one half, in two steps as the probabilities come
+    auto add_pv = [&](int half, int st, bool acc) -> bool {
 #pragma unroll
-      for (int k = 0; k < BN / 16; ++k)
-        tc_mma_ts(tmem + 256 + half * 128, tmem + half * 128 + k * 8, tc_desc(s_v + st * TILE + k * 2048, 16384), kIdescO,
-                  acc || k > 0);
+      for (int step = 0; step < 2; ++step) {
+        if (!wait.warp(smem_addr(step ? &bars.p_full[half] : &bars.p_first[half]), done[half] & 1)) return false;
+        tc_fence_after();
+        if (elected()) {
+#pragma unroll
+          for (int k = step * 4; k < step * 4 + 4; ++k)
+            tc_mma_ts(tmem + 256 + half * 128, tmem + half * 128 + k * 8, tc_desc(s_v + st * TILE + k * 2048, 16384), kIdescO,
+                      acc || k > 0);
+        }
+        __syncwarp();
+      }
+      ++done[half];
+      return true;
+    };
+    auto key_tile = [&](unsigned t) {   // waits for key tile t of the CTA
+      const bool there = wait.warp(smem_addr(&bars.k_full[t % KST]), (t / KST) & 1);
+      tc_fence_after();
+      return there;
     };
     while (ok) {
       const int kt0 = cur.first + cur.at;
       const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
-      const int nh = r1 - r0 > 128 ? 2 : 1;
+      const bool joined = r1 - r0 <= 128;
       int lo, hi;
       attn_keys(p, cur.req, r0, r1, &lo, &hi);
-      for (int h = 0; ok && h < nh; ++h) ok = __all_sync(0xffffffffu, wait(smem_addr(&bars.q_full[h]), segs[h]++ & 1));
-      if (ok) ok = __all_sync(0xffffffffu, wait(smem_addr(&bars.k_full[g % KST]), (g / KST) & 1));
-      if (!ok) break;
-      tc_fence_after();
-      if (lane == 0) {
-        for (int h = 0; h < nh; ++h) {
-          issue_s(h, g % KST);
-          tc_commit(smem_addr(&bars.s_full[h]));
+      ok = wait.warp(smem_addr(&bars.q_full[0]), segs[0]++ & 1);
+      if (ok && !joined) ok = wait.warp(smem_addr(&bars.q_full[1]), segs[1]++ & 1);
+      // the first scores of both halves
+      for (int h = 0; ok && h < 2; ++h) {
+        const int j = joined ? h : 0;
+        if (j >= len) break;
+        ok = key_tile(g + j);
+        if (ok && elected()) {
+          issue_s(h, joined ? 0 : h, (g + j) % KST);
+          if (joined || h == 1) tc_commit(smem_addr(&bars.k_empty[(g + j) % KST]));
         }
-        tc_commit(smem_addr(&bars.k_empty[g % KST]));
+        __syncwarp();
       }
-      __syncwarp();
-      for (int j = 0; j < len; ++j, ++g) {
-        const int vst = g % VST, kn = (g + 1) % KST;
-        ok = __all_sync(0xffffffffu, wait(smem_addr(&bars.v_full[vst]), (g / VST) & 1));
+      for (int j = 0; ok && j < len; ++j, ++g) {
+        const int vst = g % VST;
+        ok = wait.warp(smem_addr(&bars.v_full[vst]), (g / VST) & 1);
         if (!ok) break;
         const int valid = hi - (kt0 + j) * BN;
         if (valid < BN) {   // the item's last key tile: value rows that are not its own become zero
@@ -288,39 +368,32 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           fence_async_smem();
           __syncwarp();
         }
-        for (int h = 0; h < nh; ++h) {
-          ok = __all_sync(0xffffffffu, wait(smem_addr(&bars.p_full[h]), nh_tiles[h] & 1));
+        const int step = joined ? 2 : 1, next = j + step;   // this half's next key tile
+        for (int h = joined ? j & 1 : 0; ok && h < (joined ? (j & 1) + 1 : 2); ++h) {
+          ok = add_pv(h, vst, j >= step);
           if (!ok) break;
-          ++nh_tiles[h];
-          tc_fence_after();
-          if (lane == 0) {
-            issue_o(h, vst, j > 0);
-            if (j + 1 == len) tc_commit(smem_addr(&bars.o_full[h]));
-            if (h + 1 == nh) tc_commit(smem_addr(&bars.v_empty[vst]));
+          const bool last = joined || h == 1;   // the last half to read this tile
+          if (elected()) {
+            if (next >= len) tc_commit(smem_addr(&bars.o_full[h]));
+            if (last) tc_commit(smem_addr(&bars.v_empty[vst]));
           }
           __syncwarp();
-          if (j + 1 < len) {
-            if (h == 0) {
-              ok = __all_sync(0xffffffffu, wait(smem_addr(&bars.k_full[kn]), ((g + 1) / KST) & 1));
-              if (!ok) break;
-              tc_fence_after();
-            }
-            if (lane == 0) {
-              issue_s(h, kn);
-              tc_commit(smem_addr(&bars.s_full[h]));
-              if (h + 1 == nh) tc_commit(smem_addr(&bars.k_empty[kn]));
+          if (next < len) {
+            if (joined || h == 0) ok = key_tile(g + step);
+            if (ok && elected()) {
+              issue_s(h, joined ? 0 : h, (g + step) % KST);
+              if (last) tc_commit(smem_addr(&bars.k_empty[(g + step) % KST]));
             }
             __syncwarp();
           }
         }
-        if (!ok) break;
       }
       u += len;
       if (!ok || u >= u_end) break;
       attn_next<BN>(p, BM, &cur);
     }
     if (!ok) {   // gave up: the MMAs in flight finish before TMEM is freed
-      if (lane == 0) tc_commit(smem_addr(&bars.drain));
+      if (elected()) tc_commit(smem_addr(&bars.drain));
       const unsigned long long t0 = global_ns();
       while (!mbar_try(smem_addr(&bars.drain), 0) && global_ns() - t0 < 100000000ull) {
       }
@@ -331,124 +404,187 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const int half = warp >> 2, row = tid & 127;   // row of the half = TMEM lane
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + half * 128, t_o = tmem + lanes + 256 + half * 128;
-    const uint32_t bar_s = smem_addr(&bars.s_full[half]), bar_p = smem_addr(&bars.p_full[half]);
-    unsigned tiles = 0, segs = 0;
-    bool ok = true;
+    const uint32_t bar_s = smem_addr(&bars.s_full[half]);
+    unsigned tiles = 0, segs = 0, joins = 0;
+    bool ok = true, owed = false;   // owed: half 0 may still read this half's O and statistics
     while (ok) {
       const int kt0 = cur.first + cur.at;
       const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
-      if (r1 - r0 > half * 128) {
-        const int r = r0 + half * 128 + row;
-        const bool mine = r < r1;
-        const bool busy = r0 + half * 128 + (warp & 3) * 32 < r1;   // some row of this warp exists
-        {
-          const int tok = cur.req.q0 + r / p.G, head = cur.h * p.G + r % p.G;
-          const uint8_t* src = p.q + (tok * p.q_token + head * p.q_head) * 2;
-          const uint32_t dst = s_q + half * TILE + row * 128;
+      const bool joined = r1 - r0 <= 128;
+      const int h0 = r0 + (joined ? 0 : half * 128), r = h0 + row;
+      const bool mine = r < r1;
+      const bool busy = h0 + (warp & 3) * 32 < r1;   // some row of this warp exists
+      if (half == 0 || !joined) {
+        const int tok = cur.req.q0 + r / p.G, head = cur.h * p.G + r % p.G;
+        const uint8_t* src = p.q + (tok * p.q_token + head * p.q_head) * 2;
+        const uint32_t dst = s_q + half * TILE + row * 128;
 #pragma unroll
-          for (int c = 0; c < DP / 8; ++c) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (mine && c * 8 < p.c.D) v = __ldg(reinterpret_cast<const uint4*>(src + c * 16));
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)),
-                         "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
-                         : "memory");
-          }
-          fence_async_smem();
-          mbar_arrive(smem_addr(&bars.q_full[half]));
+        for (int c = 0; c < DP / 8; ++c) {
+          uint4 v = make_uint4(0, 0, 0, 0);
+          if (mine && c * 8 < p.c.D) v = __ldg(reinterpret_cast<const uint4*>(src + c * 16));
+          asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)),
+                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       : "memory");
         }
-        int row_lo = 0, row_hi = 0;
-        if (mine) attn_keys(p, cur.req, r, r + 1, &row_lo, &row_hi);
-        // key tiles in [free_lo, free_hi) need no mask for any row of the warp
-        const int w_hi = __reduce_min_sync(0xffffffffu, mine ? row_hi : 0x7fffffff);
-        const int w_lo = __reduce_max_sync(0xffffffffu, mine ? row_lo : 0);
-        float m = ninf(), l = 0.f;
-        for (int j = 0; j < len; ++j, ++tiles) {
-          ok = __all_sync(0xffffffffu, wait(bar_s, tiles & 1));
-          if (!ok) break;
-          tc_fence_after();
-          if (busy) {
-            uint32_t s[128];
-#pragma unroll
-            for (int c = 0; c < 4; ++c) tc_ld32(t_s + c * 32, s + c * 32);
-            tc_wait_ld();
-            const int k0 = (kt0 + j) * BN;
-            if (k0 + BN > w_hi || k0 < w_lo) {
-              const int a = row_lo - k0, b = row_hi - k0;
-#pragma unroll
-              for (int i = 0; i < 128; ++i) s[i] = i >= a && i < b ? s[i] : 0xff800000u;
-            }
-            float t[4] = {ninf(), ninf(), ninf(), ninf()};
-#pragma unroll
-            for (int i = 0; i < 128; i += 8)
-#pragma unroll
-              for (int c = 0; c < 4; ++c)
-                t[c] = fmaxf(fmaxf(t[c], __uint_as_float(s[i + c])), __uint_as_float(s[i + c + 4]));
-            // in units of the scaled scores (the scale is positive)
-            const float top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale_log2);
-            const bool grow = top - m > 8.f || (m == ninf() && top > m);
-            if (__any_sync(0xffffffffu, grow)) {
-              const float ref = top == ninf() ? 0.f : top;
-              const float f = ex2(m - ref);
-              l *= f;
-              m = top;
-              if (j > 0) {
-#pragma unroll 1
-                for (int c = 0; c < DP / 32; ++c) {
-                  uint32_t o[32];
-                  tc_ld32(t_o + c * 32, o);
-                  tc_wait_ld();
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                  tc_st32(t_o + c * 32, o);
-                }
-              }
-            }
-            const float ref = m == ninf() ? 0.f : m;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              uint32_t pk[32];
-#pragma unroll
-              for (int i = 0; i < 32; ++i) {
-                const float x = ex2(fmaf(__uint_as_float(s[c * 64 + 2 * i]), p.scale_log2, -ref));
-                const float y = ex2(fmaf(__uint_as_float(s[c * 64 + 2 * i + 1]), p.scale_log2, -ref));
-                sum[(2 * i) & 3] += x;
-                sum[(2 * i + 1) & 3] += y;
-                pk[i] = A::pack(x, y);
-              }
-              tc_st32(t_s + c * 32, pk);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            tc_wait_st();
-          }
-          tc_fence_before();
-          mbar_arrive(bar_p);
-        }
+        fence_async_smem();
+        mbar_arrive_warp(smem_addr(&bars.q_full[half]));
+      }
+      if (owed) {
+        ok = wait.warp(smem_addr(&bars.x_free), (joins - 1) & 1);
         if (!ok) break;
-        ok = __all_sync(0xffffffffu, wait(smem_addr(&bars.o_full[half]), segs & 1));
+        tc_fence_after();
+        owed = false;
+      }
+      int row_lo = 0, row_hi = 0;
+      if (mine) attn_keys(p, cur.req, r, r + 1, &row_lo, &row_hi);
+      // key tiles inside [w_lo, w_hi) need no mask for any row of the warp
+      const int w_hi = __reduce_min_sync(0xffffffffu, mine ? row_hi : 0x7fffffff);
+      const int w_lo = __reduce_max_sync(0xffffffffu, mine ? row_lo : 0);
+      const int j0 = joined ? half : 0, step = joined ? 2 : 1;
+      float m = ninf(), l = 0.f;
+      for (int j = j0; j < len; j += step, ++tiles) {
+        ok = wait.warp(bar_s, tiles & 1);
+        if (!ok) break;
+        tc_fence_after();
+        if (busy) {
+          // the scores are read twice, 32 columns at a time, the next ones in flight: held at once they
+          // would not fit the registers
+          uint32_t s[2][32];
+          const int k0 = (kt0 + j) * BN, lo = row_lo - k0, hi = row_hi - k0;
+          const bool masked = k0 + BN > w_hi || k0 < w_lo;
+          auto mask = [&](uint32_t (&x)[32], int c) {
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) x[i] = c * 32 + i >= lo && c * 32 + i < hi ? x[i] : 0xff800000u;
+            }
+          };
+          float t[4] = {ninf(), ninf(), ninf(), ninf()};
+          tc_ld32(t_s, s[0]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tc_wait_ld(s[c & 1]);
+            tc_ld32(t_s + ((c + 1) & 3) * 32, s[(c + 1) & 1]);   // the last one: the first columns again
+            mask(s[c & 1], c);
+#pragma unroll
+            for (int i = 0; i < 32; i += 8)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                t[e] = fmaxf(fmaxf(t[e], __uint_as_float(s[c & 1][i + e])), __uint_as_float(s[c & 1][i + e + 4]));
+          }
+          // in units of the scaled scores (the scale is positive)
+          const float top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale_log2);
+          const bool grow = top - m > 8.f || (m == ninf() && top > m);
+          if (__any_sync(0xffffffffu, grow)) {
+            const float ref = top == ninf() ? 0.f : top;
+            const float f = ex2(m - ref);
+            l *= f;
+            m = top;
+            if (j > j0) {
+#pragma unroll 1
+              for (int c = 0; c < DP / 32; ++c) {
+                uint32_t o[32];
+                tc_ld32(t_o + c * 32, o);
+                tc_wait_ld(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                tc_st32(t_o + c * 32, o);
+              }
+            }
+          }
+          const float ref = m == ninf() ? 0.f : m;
+          const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), ref2 = f2_pack(-ref, -ref);
+          uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            tc_wait_ld(s[c & 1]);
+            if (c < 3) tc_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
+            uint32_t (&x)[32] = s[c & 1];
+            mask(x, c);
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              const uint64_t z = f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, ref2);
+              float e0, e1;
+              f2_unpack(z, e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[i & 1] = f2_add(sum[i & 1], f2_pack(e0, e1));
+              pk[i] = A::pack(e0, e1);
+            }
+            tc_st16(t_s + c * 16, pk);   // columns whose scores have been read
+            if (c == 1) {
+              tc_wait_st();
+              tc_fence_before();
+              mbar_arrive_warp(smem_addr(&bars.p_first[half]));
+            }
+          }
+          float a, b, c, d;
+          f2_unpack(sum[0], a, b);
+          f2_unpack(sum[1], c, d);
+          l += (a + b) + (c + d);
+          tc_wait_st();
+        } else {
+          mbar_arrive_warp(smem_addr(&bars.p_first[half]));
+        }
+        tc_fence_before();
+        mbar_arrive_warp(smem_addr(&bars.p_full[half]));
+      }
+      if (!ok) break;
+      if (j0 < len) {
+        ok = wait.warp(smem_addr(&bars.o_full[half]), segs & 1);
         ++segs;
         if (!ok) break;
         tc_fence_after();
+      }
+      float f0 = 1.f, f1 = 0.f;   // the halves' factors
+      if (joined) {
+        ++joins;
+        if (half == 1) {
+          s_ml[row] = make_float2(m, l);
+          tc_fence_before();
+          mbar_arrive_warp(smem_addr(&bars.x_full));
+          owed = true;
+        } else {
+          ok = wait.warp(smem_addr(&bars.x_full), (joins - 1) & 1);
+          if (!ok) break;
+          tc_fence_after();
+          const float2 other = s_ml[row];
+          const float top = fmaxf(m, other.x), ref = top == ninf() ? 0.f : top;
+          f0 = ex2(m - ref);
+          f1 = ex2(other.x - ref);
+          m = top;
+          l = l * f0 + other.y * f1;
+        }
+      }
+      if (half == 0 || !joined) {
         const bool whole = len == cur.count;
         const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        f0 *= inv;
+        f1 *= inv;
+        const bool both = joined && len > 1;
         const long long tok = cur.req.q0 + r / p.G;
         const long long orow = tok * p.Hq + cur.h * p.G + r % p.G;
-        const long long prow = static_cast<long long>(2 * cta + (u == u_begin ? 0 : 1)) * BM + half * 128 + row;
+        const long long prow = static_cast<long long>(2 * cta + (u == u_begin ? 0 : 1)) * BM + (r - r0);
         if (busy) {
 #pragma unroll 1
           for (int c = 0; c < DP / 32; ++c) {
-            uint32_t o[32];
+            uint32_t o[32], o1[32];
             __syncwarp();
             tc_ld32(t_o + c * 32, o);
-            tc_wait_ld();
+            tc_ld32(t_o + (both ? 128 : 0) + c * 32, o1);
+            tc_wait_ld(o);
+            tc_wait_ld(o1);
 #pragma unroll
             for (int i = 0; i < 32; i += 8) {
               const int d = c * 32 + i;
               if (!mine || d >= p.c.D) continue;
               float f[8];
 #pragma unroll
-              for (int e = 0; e < 8; ++e) f[e] = __uint_as_float(o[i + e]) * inv;
+              for (int e = 0; e < 8; ++e) {
+                f[e] = __uint_as_float(o[i + e]) * f0;
+                if (both) f[e] = fmaf(__uint_as_float(o1[i + e]), f1, f[e]);
+              }
               if (whole) {
                 *reinterpret_cast<uint4*>(p.out + (orow * p.c.D + d) * 2) =
                     make_uint4(A::pack(f[0], f[1]), A::pack(f[2], f[3]), A::pack(f[4], f[5]), A::pack(f[6], f[7]));
@@ -467,6 +603,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : ninf();
         }
         tc_fence_before();
+        if (joined) mbar_arrive_warp(smem_addr(&bars.x_free));
       }
       u += len;
       if (u >= u_end) break;
@@ -482,6 +619,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 }
 
 template <bool BF16>
-const void* attn_tc_fn(int dp);
+const void* attn_tc_fn(int dp, bool wide);
 
 }  // namespace sv

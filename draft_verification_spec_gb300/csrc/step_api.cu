@@ -89,8 +89,8 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
   if (sm_count(&sms) != SPEC_OK) return 0;
   const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
   size_t most = 0;   // over the kernels that rows and dim admit
-  for (int kind = 0; kind < 3; ++kind) {
-    if ((kind == 0) != (rows <= 16) || (kind == 2 && (rows <= 64 || dim < 64 || dim > 128))) continue;
+  for (int kind = 0; kind < 4; ++kind) {
+    if (kind < 2 ? (kind == 0) != (rows <= 16) : (dim < 64 || dim > 128 || (kind == 3) != (rows > 128))) continue;
     sv::AttnPlan plan;
     if (sv::attention_plan(dtype == SPEC_BF16, kind, dim, sms, &plan) != cudaSuccess) return 0;
     const size_t n = partial_bytes(plan, dim);
@@ -119,7 +119,7 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   const long long rows = static_cast<long long>(max_q) * G;
   sv::AttnMaps maps;
   int kind = sv::attention_kind(static_cast<int>(rows < 1024 ? rows : 1024), batch->dim, batch->page_size, scale);
-  if (kind == 2 && !sv::attention_maps(bf16, internal_batch(*batch), &maps)) kind = 1;
+  if (kind >= 2 && !sv::attention_maps(bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
   sv::AttnPlan plan;
   if (sv::attention_plan(bf16, kind, batch->dim, sms, &plan) != cudaSuccess) return SPEC_ERR_CUDA;
   if (ws_bytes < kStatusBytes + partial_bytes(plan, batch->dim)) return SPEC_ERR_WORKSPACE;

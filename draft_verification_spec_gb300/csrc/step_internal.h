@@ -44,7 +44,7 @@ struct AttnParams {
 
 // Kernel families of the attention: rows per tile, keys per tile.
 struct AttnPlan {
-  int kind;                  // 0: 16-row tiles, 1: 64-row tiles (mma.sync); 2: 256-row tiles (tcgen05)
+  int kind;                  // 0: 16-row tiles, 1: 64-row tiles (mma.sync); 2, 3: 128- and 256-row tiles (tcgen05)
   int bm, bn, grid, smem, dp;
 };
 
