@@ -1,12 +1,13 @@
 // Attention of new tokens over a paged cache, tcgen05 kernel: pages that TMA can copy, heads of 64 to
 // 128 values.
 //
-// One CTA per SM works through its run of (item, key tile) units, 128 keys a tile.  Ten warps:
+// One CTA per SM works through its run of (item, key tile) units, 128 keys a tile.  Eleven warps:
 //   0-3, 4-7  softmax of half 0 and 1: a thread owns a row (TMEM lane): reads the row's 128 scores,
 //             keeps the running maximum and sum, writes the probabilities back over the scores as
 //             the second MMA's A operand, and rescales O in TMEM;
 //   8         TMA producer: one box per page, head and 64 dims, 128-byte swizzle;
-//   9         MMA issuer: S = Q K^T (both operands in shared memory) and O += P V (P in TMEM).
+//   9         MMA issuer, one thread: S = Q K^T (both operands in shared memory) and O += P V (P in TMEM);
+//   10        clears the value rows behind an item's last key (see below).
 // TMEM (512 columns): S0 | S1 | O0 | O1, P_i in S_i's columns.  The two halves alternate: while one
 // half's softmax runs, the tensor core works on the other's.  With more than 128 rows an item's halves
 // are its rows 0-127 and 128-255, which share every key tile; with fewer they are the same rows over
@@ -35,7 +36,7 @@
 
 namespace sv {
 
-constexpr int kTcThreads = 320;
+constexpr int kTcThreads = 352;
 constexpr int kTcBN = 128;
 
 // WIDE: row tiles of 256 (else 128), which take a second 128-row query buffer.
@@ -51,6 +52,7 @@ struct AttnTcBars {
   unsigned long long k_full[5], k_empty[5], v_full[5], v_empty[5];
   unsigned long long s_full[2], p_first[2], p_full[2], o_full[2], q_full[2];
   unsigned long long x_full, x_free;   // half 1's share of a joined item: there, and read
+  unsigned long long clean_me[5], v_clean[5];   // a value slot to be cleared: asked for, done
   unsigned long long drain;
 };
 
@@ -218,6 +220,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       mbar_init(smem_addr(&bars.k_empty[i]), 1);
       mbar_init(smem_addr(&bars.v_full[i]), 1);
       mbar_init(smem_addr(&bars.v_empty[i]), 1);
+      mbar_init(smem_addr(&bars.clean_me[i]), 1);
+      mbar_init(smem_addr(&bars.v_clean[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.s_full[i]), 1);
@@ -282,6 +286,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int s = 0; s < SUB; ++s) tma_box(dst + s * 128 * 128, which ? &map_v : &map_k, s * 64, tok, cur.h, pg, full);
           }
           __syncwarp();
+          if (which && (kt0 + j + 1) * BN > hi) mbar_arrive_warp(smem_addr(&bars.clean_me[st]));
         }
       }
       u += len;
@@ -299,105 +304,128 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
   } else if (warp == 9) {
     // -------------------------------------------------------------------------------- MMA issuer
+    // The whole loop runs in one elected thread: a warp-wide wait costs three times a thread's, and
+    // whatever the issuer spends between two products is time the tensor core stands still.
     constexpr uint32_t kType = BF16 ? 1u : 0u;
     constexpr uint32_t kCommon = (1u << 4) | (kType << 7) | (kType << 10) | ((128u >> 4) << 24);
     constexpr uint32_t kIdescS = kCommon | ((128u >> 3) << 17);
     constexpr uint32_t kIdescO = kCommon | (1u << 16) | ((static_cast<uint32_t>(DP) >> 3) << 17);
-    unsigned g = 0, done[2] = {0, 0}, segs[2] = {0, 0};   // key tiles so far; tiles and items per half
     bool ok = true;
-    auto issue_s = [&](int half, int q, int st) {
+    if (elected()) {
+      unsigned g = 0, done[2] = {0, 0}, segs[2] = {0, 0};   // key tiles so far; tiles and items per half
+      unsigned cleaned = 0;                                 // phases of v_clean, a bit per slot
+      auto issue_s = [&](int half, int q, int st) {
+        const uint64_t a = tc_desc(s_q + q * TILE, 16), b = tc_desc(s_k + st * TILE, 16);
 #pragma unroll
-      for (int k = 0; k < DP / 16; ++k) {
-        const uint32_t off = (k / 4) * 16384 + (k % 4) * 32;
-        tc_mma_ss(tmem + half * 128, tc_desc(s_q + q * TILE + off, 16), tc_desc(s_k + st * TILE + off, 16), kIdescS, k > 0);
-      }
-      tc_commit(smem_addr(&bars.s_full[half]));
-    };
-    // O += P V of one half, in two steps as the probabilities come
-    auto add_pv = [&](int half, int st, bool acc) -> bool {
-#pragma unroll
-      for (int step = 0; step < 2; ++step) {
-        if (!wait.warp(smem_addr(step ? &bars.p_full[half] : &bars.p_first[half]), done[half] & 1)) return false;
-        tc_fence_after();
-        if (elected()) {
-#pragma unroll
-          for (int k = step * 4; k < step * 4 + 4; ++k)
-            tc_mma_ts(tmem + 256 + half * 128, tmem + half * 128 + k * 8, tc_desc(s_v + st * TILE + k * 2048, 16384), kIdescO,
-                      acc || k > 0);
+        for (int k = 0; k < DP / 16; ++k) {
+          const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
+          tc_mma_ss(tmem + half * 128, a + off, b + off, kIdescS, k > 0);
         }
-        __syncwarp();
+        tc_commit(smem_addr(&bars.s_full[half]));
+      };
+      // O += P V of one half, in two steps as the probabilities come
+      auto add_pv = [&](int half, int st, bool acc) -> bool {
+        const uint64_t b = tc_desc(s_v + st * TILE, 16384);
+        const uint32_t d = tmem + 256 + half * 128, a = tmem + half * 128;
+        if (!wait(smem_addr(&bars.p_first[half]), done[half] & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 0; k < 4; ++k) tc_mma_ts(d, a + k * 8, b + (k * 2048 >> 4), kIdescO, acc || k > 0);
+        if (!wait(smem_addr(&bars.p_full[half]), done[half] & 1)) return false;
+        tc_fence_after();
+#pragma unroll
+        for (int k = 4; k < 8; ++k) tc_mma_ts(d, a + k * 8, b + (k * 2048 >> 4), kIdescO, true);
+        ++done[half];
+        return true;
+      };
+      auto key_tile = [&](unsigned t) {   // waits for key tile t of the CTA
+        const bool there = wait(smem_addr(&bars.k_full[t % KST]), (t / KST) & 1);
+        tc_fence_after();
+        return there;
+      };
+      while (ok) {
+        const int kt0 = cur.first + cur.at;
+        const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
+        const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
+        const bool joined = r1 - r0 <= 128;
+        int lo, hi;
+        attn_keys(p, cur.req, r0, r1, &lo, &hi);
+        const int clean_from = hi / BN - kt0;   // tiles from here on end behind the item's last key
+        ok = wait(smem_addr(&bars.q_full[0]), segs[0]++ & 1);
+        if (ok && !joined) ok = wait(smem_addr(&bars.q_full[1]), segs[1]++ & 1);
+        // the first scores of both halves
+        for (int h = 0; ok && h < 2; ++h) {
+          const int j = joined ? h : 0;
+          if (j >= len) break;
+          ok = key_tile(g + j);
+          if (ok) issue_s(h, joined ? 0 : h, (g + j) % KST);
+          if (ok && (joined || h == 1)) tc_commit(smem_addr(&bars.k_empty[(g + j) % KST]));
+        }
+        const int step = joined ? 2 : 1;
+        for (int j = 0; ok && j < len; ++j, ++g) {
+          const int vst = g % VST, next = j + step;   // this half's next key tile
+          ok = wait(smem_addr(&bars.v_full[vst]), (g / VST) & 1);
+          if (ok && j >= clean_from) {
+            ok = wait(smem_addr(&bars.v_clean[vst]), cleaned >> vst & 1);
+            cleaned ^= 1u << vst;
+          }
+          for (int h = joined ? j & 1 : 0; ok && h < (joined ? (j & 1) + 1 : 2); ++h) {
+            ok = add_pv(h, vst, j >= step);
+            if (!ok) break;
+            const bool last = joined || h == 1;   // the last half to read this tile
+            if (next < len) {
+              if (joined || h == 0) ok = key_tile(g + step);
+              if (!ok) break;
+              issue_s(h, joined ? 0 : h, (g + step) % KST);
+              if (last) tc_commit(smem_addr(&bars.k_empty[(g + step) % KST]));
+            } else {
+              tc_commit(smem_addr(&bars.o_full[h]));
+            }
+            if (last) tc_commit(smem_addr(&bars.v_empty[vst]));
+          }
+        }
+        u += len;
+        if (!ok || u >= u_end) break;
+        attn_next<BN>(p, BM, &cur);
       }
-      ++done[half];
-      return true;
-    };
-    auto key_tile = [&](unsigned t) {   // waits for key tile t of the CTA
-      const bool there = wait.warp(smem_addr(&bars.k_full[t % KST]), (t / KST) & 1);
-      tc_fence_after();
-      return there;
-    };
+      if (!ok) {   // gave up: the MMAs in flight finish before TMEM is freed
+        tc_commit(smem_addr(&bars.drain));
+        const unsigned long long t0 = global_ns();
+        while (!mbar_try(smem_addr(&bars.drain), 0) && global_ns() - t0 < 100000000ull) {
+        }
+      }
+    }
+    __syncwarp();
+  } else if (warp == 10) {
+    // ---------------------------------------------------------------- value rows behind the last key
+    // The producer asks for a slot after it has armed the slot's v_full; the slot is not armed again
+    // before the issuer has seen it cleared, so no phase of the three barriers is ever missed.
+    unsigned g = 0, asked = 0;   // phases of clean_me, a bit per slot
+    bool ok = true;
     while (ok) {
       const int kt0 = cur.first + cur.at;
       const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
-      const bool joined = r1 - r0 <= 128;
       int lo, hi;
       attn_keys(p, cur.req, r0, r1, &lo, &hi);
-      ok = wait.warp(smem_addr(&bars.q_full[0]), segs[0]++ & 1);
-      if (ok && !joined) ok = wait.warp(smem_addr(&bars.q_full[1]), segs[1]++ & 1);
-      // the first scores of both halves
-      for (int h = 0; ok && h < 2; ++h) {
-        const int j = joined ? h : 0;
-        if (j >= len) break;
-        ok = key_tile(g + j);
-        if (ok && elected()) {
-          issue_s(h, joined ? 0 : h, (g + j) % KST);
-          if (joined || h == 1) tc_commit(smem_addr(&bars.k_empty[(g + j) % KST]));
-        }
-        __syncwarp();
-      }
-      for (int j = 0; ok && j < len; ++j, ++g) {
-        const int vst = g % VST;
-        ok = wait.warp(smem_addr(&bars.v_full[vst]), (g / VST) & 1);
+      for (int j = max(hi / BN - kt0, 0); ok && j < len; ++j) {
+        const unsigned t = g + j, st = t % VST;
+        ok = wait.warp(smem_addr(&bars.clean_me[st]), asked >> st & 1);
+        asked ^= 1u << st;
+        if (ok) ok = wait.warp(smem_addr(&bars.v_full[st]), (t / VST) & 1);
         if (!ok) break;
-        const int valid = hi - (kt0 + j) * BN;
-        if (valid < BN) {   // the item's last key tile: value rows that are not its own become zero
-          for (int i = max(valid, 0) * 8 + lane; i < BN * 8; i += 32)
+        const int valid = max(hi - (kt0 + j) * BN, 0);
+        for (int i = valid * 8 + lane; i < BN * 8; i += 32)
 #pragma unroll
-            for (int s = 0; s < SUB; ++s)
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(s_v + vst * TILE + s * 16384 + i * 16), "r"(0u) : "memory");
-          fence_async_smem();
-          __syncwarp();
-        }
-        const int step = joined ? 2 : 1, next = j + step;   // this half's next key tile
-        for (int h = joined ? j & 1 : 0; ok && h < (joined ? (j & 1) + 1 : 2); ++h) {
-          ok = add_pv(h, vst, j >= step);
-          if (!ok) break;
-          const bool last = joined || h == 1;   // the last half to read this tile
-          if (elected()) {
-            if (next >= len) tc_commit(smem_addr(&bars.o_full[h]));
-            if (last) tc_commit(smem_addr(&bars.v_empty[vst]));
-          }
-          __syncwarp();
-          if (next < len) {
-            if (joined || h == 0) ok = key_tile(g + step);
-            if (ok && elected()) {
-              issue_s(h, joined ? 0 : h, (g + step) % KST);
-              if (last) tc_commit(smem_addr(&bars.k_empty[(g + step) % KST]));
-            }
-            __syncwarp();
-          }
-        }
+          for (int s = 0; s < SUB; ++s)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(s_v + st * TILE + s * 16384 + i * 16), "r"(0u) : "memory");
+        fence_async_smem();
+        mbar_arrive_warp(smem_addr(&bars.v_clean[st]));
       }
+      g += len;
       u += len;
-      if (!ok || u >= u_end) break;
+      if (u >= u_end) break;
       attn_next<BN>(p, BM, &cur);
-    }
-    if (!ok) {   // gave up: the MMAs in flight finish before TMEM is freed
-      if (elected()) tc_commit(smem_addr(&bars.drain));
-      const unsigned long long t0 = global_ns();
-      while (!mbar_try(smem_addr(&bars.drain), 0) && global_ns() - t0 < 100000000ull) {
-      }
-      __syncwarp();
     }
   } else {
     // ------------------------------------------------------------------------------------ softmax
