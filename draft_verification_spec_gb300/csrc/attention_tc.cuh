@@ -312,36 +312,51 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     constexpr uint32_t kIdescO = kCommon | (1u << 16) | ((static_cast<uint32_t>(DP) >> 3) << 17);
     bool ok = true;
     if (elected()) {
-      unsigned g = 0, done[2] = {0, 0}, segs[2] = {0, 0};   // key tiles so far; tiles and items per half
-      unsigned cleaned = 0;                                 // phases of v_clean, a bit per slot
-      auto issue_s = [&](int half, int q, int st) {
-        const uint64_t a = tc_desc(s_q + q * TILE, 16), b = tc_desc(s_k + st * TILE, 16);
+      // rings of slots: the next one to use, its phase, the operand's descriptor
+      struct Ring {
+        uint32_t slot, phase, full, empty;
+        uint64_t desc;
+      };
+      const uint64_t desc_q = tc_desc(s_q, 16), desc_k = tc_desc(s_k, 16), desc_v = tc_desc(s_v, 16384);
+      Ring kr = {0, 0, smem_addr(bars.k_full), smem_addr(bars.k_empty), desc_k};
+      Ring vr = {0, 0, smem_addr(bars.v_full), smem_addr(bars.v_empty), desc_v};
+      auto next_k = [&] {
+        kr.full += 8;
+        kr.empty += 8;
+        kr.desc += TILE >> 4;
+        if (++kr.slot == KST) kr = {0, kr.phase ^ 1, smem_addr(bars.k_full), smem_addr(bars.k_empty), desc_k};
+      };
+      auto next_v = [&] {
+        vr.full += 8;
+        vr.empty += 8;
+        vr.desc += TILE >> 4;
+        if (++vr.slot == VST) vr = {0, vr.phase ^ 1, smem_addr(bars.v_full), smem_addr(bars.v_empty), desc_v};
+      };
+      unsigned pv_phase = 0, q_phase = 0, cleaned = 0;   // phases, a bit per half or slot
+      const uint32_t bar_s = smem_addr(bars.s_full), bar_o = smem_addr(bars.o_full);
+      const uint32_t bar_p1 = smem_addr(bars.p_first), bar_p2 = smem_addr(bars.p_full);
+      auto issue_s = [&](int half, uint64_t q) {
+        const uint32_t d = tmem + half * 128;
 #pragma unroll
         for (int k = 0; k < DP / 16; ++k) {
           const uint32_t off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
-          tc_mma_ss(tmem + half * 128, a + off, b + off, kIdescS, k > 0);
+          tc_mma_ss(d, q + off, kr.desc + off, kIdescS, k > 0);
         }
-        tc_commit(smem_addr(&bars.s_full[half]));
+        tc_commit(bar_s + half * 8);
       };
       // O += P V of one half, in two steps as the probabilities come
-      auto add_pv = [&](int half, int st, bool acc) -> bool {
-        const uint64_t b = tc_desc(s_v + st * TILE, 16384);
-        const uint32_t d = tmem + 256 + half * 128, a = tmem + half * 128;
-        if (!wait(smem_addr(&bars.p_first[half]), done[half] & 1)) return false;
+      auto add_pv = [&](int half, bool acc) -> bool {
+        const uint32_t a = tmem + half * 128, d = a + 256, ph = pv_phase >> half & 1;
+        if (!wait(bar_p1 + half * 8, ph)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tc_mma_ts(d, a + k * 8, b + (k * 2048 >> 4), kIdescO, acc || k > 0);
-        if (!wait(smem_addr(&bars.p_full[half]), done[half] & 1)) return false;
+        for (int k = 0; k < 4; ++k) tc_mma_ts(d, a + k * 8, vr.desc + (k * 2048 >> 4), kIdescO, acc || k > 0);
+        if (!wait(bar_p2 + half * 8, ph)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int k = 4; k < 8; ++k) tc_mma_ts(d, a + k * 8, b + (k * 2048 >> 4), kIdescO, true);
-        ++done[half];
+        for (int k = 4; k < 8; ++k) tc_mma_ts(d, a + k * 8, vr.desc + (k * 2048 >> 4), kIdescO, true);
+        pv_phase ^= 1u << half;
         return true;
-      };
-      auto key_tile = [&](unsigned t) {   // waits for key tile t of the CTA
-        const bool there = wait(smem_addr(&bars.k_full[t % KST]), (t / KST) & 1);
-        tc_fence_after();
-        return there;
       };
       while (ok) {
         const int kt0 = cur.first + cur.at;
@@ -351,37 +366,49 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         int lo, hi;
         attn_keys(p, cur.req, r0, r1, &lo, &hi);
         const int clean_from = hi / BN - kt0;   // tiles from here on end behind the item's last key
-        ok = wait(smem_addr(&bars.q_full[0]), segs[0]++ & 1);
-        if (ok && !joined) ok = wait(smem_addr(&bars.q_full[1]), segs[1]++ & 1);
-        // the first scores of both halves
-        for (int h = 0; ok && h < 2; ++h) {
-          const int j = joined ? h : 0;
-          if (j >= len) break;
-          ok = key_tile(g + j);
-          if (ok) issue_s(h, joined ? 0 : h, (g + j) % KST);
-          if (ok && (joined || h == 1)) tc_commit(smem_addr(&bars.k_empty[(g + j) % KST]));
+        for (int h = 0; ok && h < (joined ? 1 : 2); ++h) {
+          ok = wait(smem_addr(&bars.q_full[h]), q_phase >> h & 1);
+          q_phase ^= 1u << h;
         }
-        const int step = joined ? 2 : 1;
-        for (int j = 0; ok && j < len; ++j, ++g) {
-          const int vst = g % VST, next = j + step;   // this half's next key tile
-          ok = wait(smem_addr(&bars.v_full[vst]), (g / VST) & 1);
+        // the first scores of both halves
+        for (int j = 0; ok && j < (joined ? min(len, 2) : 1); ++j) {
+          ok = wait(kr.full, kr.phase);
+          if (!ok) break;
+          tc_fence_after();
+          issue_s(joined ? j : 0, desc_q);
+          if (!joined) issue_s(1, desc_q + (TILE >> 4));
+          tc_commit(kr.empty);
+          next_k();
+        }
+        for (int j = 0; ok && j < len; ++j) {
+          ok = wait(vr.full, vr.phase);
           if (ok && j >= clean_from) {
-            ok = wait(smem_addr(&bars.v_clean[vst]), cleaned >> vst & 1);
-            cleaned ^= 1u << vst;
+            ok = wait(smem_addr(&bars.v_clean[vr.slot]), cleaned >> vr.slot & 1);
+            cleaned ^= 1u << vr.slot;
           }
-          for (int h = joined ? j & 1 : 0; ok && h < (joined ? (j & 1) + 1 : 2); ++h) {
-            ok = add_pv(h, vst, j >= step);
-            if (!ok) break;
-            const bool last = joined || h == 1;   // the last half to read this tile
-            if (next < len) {
-              if (joined || h == 0) ok = key_tile(g + step);
-              if (!ok) break;
-              issue_s(h, joined ? 0 : h, (g + step) % KST);
-              if (last) tc_commit(smem_addr(&bars.k_empty[(g + step) % KST]));
-            } else {
-              tc_commit(smem_addr(&bars.o_full[h]));
-            }
-            if (last) tc_commit(smem_addr(&bars.v_empty[vst]));
+          if (!ok) break;
+          const int first = joined ? j & 1 : 0;
+          const bool more = j + (joined ? 2 : 1) < len;   // the half has a key tile after this one
+          if (!(ok = add_pv(first, j >= (joined ? 2 : 1)))) break;
+          if (more) {
+            if (!(ok = wait(kr.full, kr.phase))) break;
+            tc_fence_after();
+            issue_s(first, desc_q);
+          } else {
+            tc_commit(bar_o + first * 8);
+          }
+          if (!joined) {
+            if (!(ok = add_pv(1, j > 0))) break;
+            if (more)
+              issue_s(1, desc_q + (TILE >> 4));
+            else
+              tc_commit(bar_o + 8);
+          }
+          tc_commit(vr.empty);
+          next_v();
+          if (more) {
+            tc_commit(kr.empty);
+            next_k();
           }
         }
         u += len;
