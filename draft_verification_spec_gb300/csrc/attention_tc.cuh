@@ -17,8 +17,7 @@
 // O is rescaled only when a row's maximum grows by more than 2^8 over the reference its exponentials
 // use; until then the probabilities may reach 2^8, which neither type overflows and the final division
 // by the sum undoes.  S(j) is committed after the same half's previous P V in issue order, so a softmax
-// thread that has seen S(j) may touch O.  P V starts on the first 64 keys while the softmax is at the
-// others.
+// thread that has seen S(j) may touch O.
 //
 // Keys at or beyond the item's last one: pages that lie wholly there are read at an out-of-range page
 // coordinate, which TMA fills with zeros; the rest of the last page can hold anything, so its value
@@ -50,7 +49,7 @@ struct AttnTcGeom {
 
 struct AttnTcBars {
   unsigned long long k_full[5], k_empty[5], v_full[5], v_empty[5];
-  unsigned long long s_full[2], p_first[2], p_full[2], o_full[2], q_full[2];
+  unsigned long long s_full[2], p_full[2], o_full[2], q_full[2];
   unsigned long long x_full, x_free;   // half 1's share of a joined item: there, and read
   unsigned long long clean_me[5], v_clean[5];   // a value slot to be cleared: asked for, done
   unsigned long long drain;
@@ -225,7 +224,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_addr(&bars.s_full[i]), 1);
-      mbar_init(smem_addr(&bars.p_first[i]), 4);
       mbar_init(smem_addr(&bars.p_full[i]), 4);
       mbar_init(smem_addr(&bars.o_full[i]), 1);
       mbar_init(smem_addr(&bars.q_full[i]), 4);
@@ -334,7 +332,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       };
       unsigned pv_phase = 0, q_phase = 0, cleaned = 0;   // phases, a bit per half or slot
       const uint32_t bar_s = smem_addr(bars.s_full), bar_o = smem_addr(bars.o_full);
-      const uint32_t bar_p1 = smem_addr(bars.p_first), bar_p2 = smem_addr(bars.p_full);
+      const uint32_t bar_p = smem_addr(bars.p_full);
       auto issue_s = [&](int half, uint64_t q) {
         const uint32_t d = tmem + half * 128;
 #pragma unroll
@@ -344,17 +342,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         tc_commit(bar_s + half * 8);
       };
-      // O += P V of one half, in two steps as the probabilities come
+      // O += P V of one half
       auto add_pv = [&](int half, bool acc) -> bool {
-        const uint32_t a = tmem + half * 128, d = a + 256, ph = pv_phase >> half & 1;
-        if (!wait(bar_p1 + half * 8, ph)) return false;
+        const uint32_t a = tmem + half * 128, d = a + 256;
+        if (!wait(bar_p + half * 8, pv_phase >> half & 1)) return false;
         tc_fence_after();
 #pragma unroll
-        for (int k = 0; k < 4; ++k) tc_mma_ts(d, a + k * 8, vr.desc + (k * 2048 >> 4), kIdescO, acc || k > 0);
-        if (!wait(bar_p2 + half * 8, ph)) return false;
-        tc_fence_after();
-#pragma unroll
-        for (int k = 4; k < 8; ++k) tc_mma_ts(d, a + k * 8, vr.desc + (k * 2048 >> 4), kIdescO, true);
+        for (int k = 0; k < 8; ++k) tc_mma_ts(d, a + k * 8, vr.desc + (k * 2048 >> 4), kIdescO, acc || k > 0);
         pv_phase ^= 1u << half;
         return true;
       };
@@ -503,84 +497,68 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (!ok) break;
         tc_fence_after();
         if (busy) {
-          // the scores are read twice, 32 columns at a time, the next ones in flight: held at once they
-          // would not fit the registers
-          uint32_t s[2][32];
+          // One pass over the scores, 32 columns at a time with the next ones in flight: maximum,
+          // exponentials against the reference so far, their sum.  Only where the maximum has outgrown
+          // the reference (always in an item's first tile) the pass is done again with the new one.
           const int k0 = (kt0 + j) * BN, lo = row_lo - k0, hi = row_hi - k0;
           const bool masked = k0 + BN > w_hi || k0 < w_lo;
-          auto mask = [&](uint32_t (&x)[32], int c) {
-            if (masked) {
+          const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
+          uint32_t pk[64];
+          while (true) {
+            const float ref = m == ninf() ? 0.f : m;
+            const uint64_t ref2 = f2_pack(-ref, -ref);
+            uint32_t s[2][32];
+            float t[4] = {ninf(), ninf(), ninf(), ninf()};
+            uint64_t sum[2] = {0ull, 0ull};
+            tc_ld32(t_s, s[0]);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = c * 32 + i >= lo && c * 32 + i < hi ? x[i] : 0xff800000u;
+            for (int c = 0; c < 4; ++c) {
+              uint32_t (&x)[32] = s[c & 1];
+              tc_wait_ld(x);
+              if (c < 3) tc_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
+              if (masked) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) x[i] = c * 32 + i >= lo && c * 32 + i < hi ? x[i] : 0xff800000u;
+              }
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float x0 = __uint_as_float(x[2 * i]), x1 = __uint_as_float(x[2 * i + 1]);
+                t[i & 3] = fmaxf(fmaxf(t[i & 3], x0), x1);
+                float e0, e1;
+                f2_unpack(f2_fma(f2_pack(x0, x1), scale2, ref2), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum[i & 1] = f2_add(sum[i & 1], f2_pack(e0, e1));
+                pk[c * 16 + i] = A::pack(e0, e1);
+              }
             }
-          };
-          float t[4] = {ninf(), ninf(), ninf(), ninf()};
-          tc_ld32(t_s, s[0]);
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tc_wait_ld(s[c & 1]);
-            tc_ld32(t_s + ((c + 1) & 3) * 32, s[(c + 1) & 1]);   // the last one: the first columns again
-            mask(s[c & 1], c);
-#pragma unroll
-            for (int i = 0; i < 32; i += 8)
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                t[e] = fmaxf(fmaxf(t[e], __uint_as_float(s[c & 1][i + e])), __uint_as_float(s[c & 1][i + e + 4]));
-          }
-          // in units of the scaled scores (the scale is positive)
-          const float top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale_log2);
-          const bool grow = top - m > 8.f || (m == ninf() && top > m);
-          if (__any_sync(0xffffffffu, grow)) {
-            const float ref = top == ninf() ? 0.f : top;
-            const float f = ex2(m - ref);
+            // in units of the scaled scores (the scale is positive)
+            const float top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale_log2);
+            const bool grow = top - m > 8.f || (m == ninf() && top > m);
+            if (!__any_sync(0xffffffffu, grow)) {
+              float a, b, c, d;
+              f2_unpack(sum[0], a, b);
+              f2_unpack(sum[1], c, d);
+              l += (a + b) + (c + d);
+              break;
+            }
+            const float f = ex2(m - (top == ninf() ? 0.f : top));
             l *= f;
             m = top;
             if (j > j0) {
 #pragma unroll 1
               for (int c = 0; c < DP / 32; ++c) {
-                uint32_t o[32];
-                tc_ld32(t_o + c * 32, o);
-                tc_wait_ld(o);
+                tc_ld32(t_o + c * 32, s[0]);
+                tc_wait_ld(s[0]);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                tc_st32(t_o + c * 32, o);
+                for (int i = 0; i < 32; ++i) s[0][i] = __float_as_uint(__uint_as_float(s[0][i]) * f);
+                tc_st32(t_o + c * 32, s[0]);
               }
             }
           }
-          const float ref = m == ninf() ? 0.f : m;
-          const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2), ref2 = f2_pack(-ref, -ref);
-          uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            tc_wait_ld(s[c & 1]);
-            if (c < 3) tc_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
-            uint32_t (&x)[32] = s[c & 1];
-            mask(x, c);
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const uint64_t z = f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale2, ref2);
-              float e0, e1;
-              f2_unpack(z, e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum[i & 1] = f2_add(sum[i & 1], f2_pack(e0, e1));
-              pk[i] = A::pack(e0, e1);
-            }
-            tc_st16(t_s + c * 16, pk);   // columns whose scores have been read
-            if (c == 1) {
-              tc_wait_st();
-              tc_fence_before();
-              mbar_arrive_warp(smem_addr(&bars.p_first[half]));
-            }
-          }
-          float a, b, c, d;
-          f2_unpack(sum[0], a, b);
-          f2_unpack(sum[1], c, d);
-          l += (a + b) + (c + d);
+          tc_st32(t_s, pk);
+          tc_st32(t_s + 32, pk + 32);
           tc_wait_st();
-        } else {
-          mbar_arrive_warp(smem_addr(&bars.p_first[half]));
         }
         tc_fence_before();
         mbar_arrive_warp(smem_addr(&bars.p_full[half]));
