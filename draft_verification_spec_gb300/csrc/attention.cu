@@ -63,7 +63,8 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p, i
       }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const long long row = static_cast<long long>(cur.req.q0 + (r0 + r) / p.G) * p.Hq + cur.h * p.G + (r0 + r) % p.G;
+    const int tok = attn_token(p, r0 + r);
+    const long long row = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r0 + r - tok * p.G);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int d = lane * 4 + i * 128;

@@ -170,7 +170,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
     // query fragments: rows lane/4 and lane/4 + 8 of the warp's 16
     uint32_t qf[Geo::kQReg ? KS : 1][4];
     auto q_ptr = [&](int r) {
-      const int tok = cur.req.q0 + r / p.G, head = cur.h * p.G + r % p.G;
+      const int tok = cur.req.q0 + attn_token(p, r), head = cur.h * p.G + r - (attn_token(p, r)) * p.G;
       return p.q + (tok * p.q_token + head * p.q_head) * 2;
     };
     if constexpr (Geo::kQReg) {
@@ -341,8 +341,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
       }
       if (whole) {
         const float inv = ll > 0.f ? 1.f / ll : 0.f;
-        const long long tok = cur.req.q0 + (r0 + r) / p.G;
-        const long long row = tok * p.Hq + cur.h * p.G + (r0 + r) % p.G;
+        const int tok = attn_token(p, r0 + r);
+        const long long row = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r0 + r - tok * p.G);
         uint2 w = make_uint2(A::pack(acc.x * inv, acc.y * inv), A::pack(acc.z * inv, acc.w * inv));
         *reinterpret_cast<uint2*>(p.out + (row * D + d) * 2) = w;
         if (d == 0 && p.lse) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : ninf();

@@ -27,11 +27,16 @@ __device__ __forceinline__ AttnReq attn_request(const PagedBatch& c, int b) {
   return r;
 }
 
+// r / G (G_inv = ceil(2^64 / G), 0 for G = 1): exact for every 32-bit r.
+__device__ __forceinline__ int attn_token(const AttnParams& p, int r) {
+  return p.G_inv ? static_cast<int>(__umul64hi(static_cast<unsigned long long>(r), p.G_inv)) : r;
+}
+
 // Keys [lo, hi) that rows [r0, r1) of the request can see.
 __device__ __forceinline__ void attn_keys(const AttnParams& p, const AttnReq& r, int r0, int r1, int* lo, int* hi) {
-  const int first = r.kv - r.nq + r0 / p.G, last = r.kv - r.nq + (r1 - 1) / p.G;
-  *hi = p.causal ? max(min(last + 1, r.kv), 0) : r.kv;
-  *lo = p.window > 0 ? max(first - p.window + 1, 0) : 0;
+  const int at = r.kv - r.nq;
+  *hi = p.causal ? max(min(at + attn_token(p, r1 - 1) + 1, r.kv), 0) : r.kv;
+  *lo = p.window > 0 ? max(at + attn_token(p, r0) - p.window + 1, 0) : 0;
 }
 // First key tile and number of key tiles of row tile t (an item has one at least: its rows are
 // written even where they see no key).
@@ -46,15 +51,21 @@ __device__ __forceinline__ int attn_tiles(const AttnParams& p, const AttnReq& r,
 __device__ __forceinline__ int attn_row_tiles(const AttnParams& p, const AttnReq& r, int bm) {
   return (r.nq * p.G + bm - 1) / bm;
 }
+// Units of request b, all key heads; the request's lanes (p.lanes, a power of two: one where a request is
+// one row tile) share the row tiles, and every one of them gets the sum.
 template <int BN>
-__device__ __forceinline__ long long attn_request_units(const AttnParams& p, const AttnReq& r, int bm) {
-  const int nt = attn_row_tiles(p, r, bm);
+__device__ __forceinline__ long long attn_request_units(const AttnParams& p, int b, int bm) {
   long long n = 0;
-  for (int t = 0; t < nt; ++t) {
-    int first;
-    n += attn_tiles<BN>(p, r, t, bm, &first);
+  if (b < p.c.B) {
+    const AttnReq r = attn_request(p.c, b);
+    const int nt = attn_row_tiles(p, r, bm);
+    for (int t = threadIdx.x & (p.lanes - 1); t < nt; t += p.lanes) {
+      int first;
+      n += attn_tiles<BN>(p, r, t, bm, &first);
+    }
   }
-  return n;
+  for (int o = p.lanes / 2; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n * p.c.Hkv;
 }
 
 struct AttnSplit {
@@ -75,16 +86,19 @@ struct AttnCursor {
 template <int THREADS>
 struct AttnSchedSmem {
   long long warp[THREADS / 32];
-  long long rem;
+  long long rem, units;
   int b;
 };
 
 // Block-wide: the units of the call and how many CTAs share them.
 template <int BN, int THREADS>
 __device__ __forceinline__ AttnSplit attn_split(const AttnParams& p, int bm, AttnSchedSmem<THREADS>& s) {
+  const int per = THREADS / p.lanes;   // requests at a time (THREADS is a multiple of 32, lanes at most 32)
   long long mine = 0;
-  for (int b = threadIdx.x; b < p.c.B; b += THREADS)
-    mine += attn_request_units<BN>(p, attn_request(p.c, b), bm) * p.c.Hkv;
+  for (int base = 0; base < p.c.B; base += per) {
+    const long long n = attn_request_units<BN>(p, base + threadIdx.x / p.lanes, bm);
+    if ((threadIdx.x & (p.lanes - 1)) == 0) mine += n;
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
   if ((threadIdx.x & 31) == 0) s.warp[threadIdx.x / 32] = mine;
@@ -99,31 +113,14 @@ __device__ __forceinline__ AttnSplit attn_split(const AttnParams& p, int bm, Att
   return sp;
 }
 
-// The item at unit `rem` of request b's units.
-template <int BN>
-__device__ __forceinline__ void attn_enter(const AttnParams& p, int bm, int b, long long rem, AttnCursor* c) {
-  c->b = b;
-  c->req = attn_request(p.c, b);
-  const long long per_head = attn_request_units<BN>(p, c->req, bm);
-  c->h = static_cast<int>(rem / per_head);
-  rem -= per_head * c->h;
-  c->t = 0;
-  while (true) {
-    c->count = attn_tiles<BN>(p, c->req, c->t, bm, &c->first);
-    if (rem < c->count) break;
-    rem -= c->count;
-    ++c->t;
-  }
-  c->at = static_cast<int>(rem);
-}
-
 // Block-wide: the position of unit u (u < total).
 template <int BN, int THREADS>
 __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, long long u, AttnSchedSmem<THREADS>& s) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x / 32;
-  for (int base = 0; base < p.c.B; base += THREADS) {
-    const int b = base + threadIdx.x;
-    const long long mine = b < p.c.B ? attn_request_units<BN>(p, attn_request(p.c, b), bm) * p.c.Hkv : 0;
+  const int lane = threadIdx.x & 31, w = threadIdx.x / 32, per = THREADS / p.lanes;
+  for (int base = 0; base < p.c.B; base += per) {
+    const int b = base + threadIdx.x / p.lanes;
+    const long long units = attn_request_units<BN>(p, b, bm);
+    const long long mine = (threadIdx.x & (p.lanes - 1)) == 0 ? units : 0;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -141,13 +138,41 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
     if (u >= incl - mine && u < incl) {
       s.b = b;
       s.rem = u - (incl - mine);
+      s.units = units;
     }
     __syncthreads();
     if (u < all) break;
     u -= all;
   }
   AttnCursor c;
-  attn_enter<BN>(p, bm, s.b, s.rem, &c);
+  c.b = s.b;
+  c.req = attn_request(p.c, c.b);
+  const long long per_head = s.units / p.c.Hkv;
+  long long rem = s.rem;
+  c.h = static_cast<int>(rem / per_head);
+  rem -= per_head * c.h;
+  // the row tile: 32 at a time, every warp for itself
+  const int nt = attn_row_tiles(p, c.req, bm);
+  for (int t0 = 0; t0 < nt; t0 += 32) {
+    int first = 0;
+    const long long mine = t0 + lane < nt ? attn_tiles<BN>(p, c.req, t0 + lane, bm, &first) : 0;
+    long long incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > rem);
+    if (hit) {
+      const int k = __ffs(hit) - 1;
+      c.t = t0 + k;
+      c.count = static_cast<int>(__shfl_sync(0xffffffffu, mine, k));
+      c.first = __shfl_sync(0xffffffffu, first, k);
+      c.at = static_cast<int>(rem - __shfl_sync(0xffffffffu, incl - mine, k));
+      break;
+    }
+    rem -= __shfl_sync(0xffffffffu, incl, 31);
+  }
   __syncthreads();
   return c;
 }

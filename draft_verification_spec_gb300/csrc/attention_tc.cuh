@@ -465,7 +465,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const bool mine = r < r1;
       const bool busy = h0 + (warp & 3) * 32 < r1;   // some row of this warp exists
       if (half == 0 || !joined) {
-        const int tok = cur.req.q0 + r / p.G, head = cur.h * p.G + r % p.G;
+        const int tok = cur.req.q0 + attn_token(p, r), head = cur.h * p.G + r - (attn_token(p, r)) * p.G;
         const uint8_t* src = p.q + (tok * p.q_token + head * p.q_head) * 2;
         const uint32_t dst = s_q + half * TILE + row * 128;
 #pragma unroll
@@ -596,8 +596,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         f0 *= inv;
         f1 *= inv;
         const bool both = joined && len > 1;
-        const long long tok = cur.req.q0 + r / p.G;
-        const long long orow = tok * p.Hq + cur.h * p.G + r % p.G;
+        const int tok = attn_token(p, r);
+        const long long orow = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r - tok * p.G);
         const long long prow = static_cast<long long>(2 * cta + (u == u_begin ? 0 : 1)) * BM + (r - r0);
         if (busy) {
 #pragma unroll 1

@@ -133,6 +133,8 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   p.lse = out_lse;
   p.Hq = q_heads;
   p.G = G;
+  p.G_inv = G > 1 ? ~0ull / G + 1 : 0ull;
+  for (p.lanes = 1; p.lanes < 32 && static_cast<long long>(p.lanes) * plan.bm < rows;) p.lanes *= 2;
   p.causal = causal != 0;
   p.window = window;
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);

@@ -32,6 +32,8 @@ struct AttnParams {
   uint8_t* out;              // [N, Hq, D]
   float* lse;                // [N, Hq] or null
   int Hq, G;                 // query heads, query heads per key head
+  unsigned long long G_inv;  // ceil(2^64 / G), 0 for G = 1
+  int lanes;                 // threads that share a request's row tiles when the work is divided
   int causal, window;
   float scale_log2;          // softmax scale x log2(e)
   float* part_o;             // [2 n, BM, D] partial rows of items that more than one CTA works on
