@@ -20,32 +20,24 @@ const void* attn_tc_fn<true>(int dp, bool wide);
 template <>
 const void* attn_tc_fn<false>(int dp, bool wide);
 
-// One warp per row of the item that begins in CTA blockIdx.x's run and goes on in others': the
-// partials in key order, each scaled by 2^(its maximum - the largest).  fp32.
-template <int BN, int DTYPE>
+// Joins the item that CTA blockIdx.x left a record of: one warp per row, the partials in key order,
+// each scaled by 2^(its maximum - the largest).  fp32.
+template <bool BF16>
 __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p, int bm) {
-  __shared__ AttnSchedSmem<128> sched;
-  const AttnSplit split = attn_split<BN>(p, bm, sched);
-  const int c1 = blockIdx.x;
-  if (c1 + 1 >= split.n) return;
-  const long long u0 = split.begin(c1), u1 = split.begin(c1 + 1);
-  const AttnCursor cur = attn_locate<BN>(p, bm, u1 - 1, sched);
-  const long long start = u1 - 1 - cur.at, end = start + cur.count;
-  if (start < u0 || end <= u1) return;
-  const int c2 = split.owner(end - 1);
-  const int r0 = cur.t * bm, rows = min(cur.req.nq * p.G - r0, bm);
+  using A = AttnType<BF16>;
+  const int c1 = blockIdx.x, lane = threadIdx.x & 31, D = p.c.D;
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int lane = threadIdx.x & 31, D = p.c.D;
-  for (int r = blockIdx.y * 4 + threadIdx.x / 32; r < rows; r += gridDim.y * 4) {
-    auto slot = [&](int c) { return static_cast<long long>(c == c1 && start != u0 ? 2 * c + 1 : 2 * c) * bm + r; };
+  const AttnJoin j = p.joins[c1];
+  for (int r = blockIdx.y * 4 + threadIdx.x / 32; r < j.rows; r += gridDim.y * 4) {
+    auto slot = [&](int c) { return static_cast<long long>(c == c1 ? j.slot : 2 * c) * bm + r; };
     float m = ninf();
-    for (int c = c1 + lane; c <= c2; c += 32) m = fmaxf(m, __ldcg(p.part_ml + slot(c) * 2));
+    for (int c = c1 + lane; c <= j.last; c += 32) m = fmaxf(m, __ldcg(p.part_ml + slot(c) * 2));
     m = warp_maxf(m);
     const float ref = m == ninf() ? 0.f : m;
     float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
     float l = 0.f;
 #pragma unroll 4
-    for (int c = c1; c <= c2; ++c) {
+    for (int c = c1; c <= j.last; ++c) {
       const long long s = slot(c);
       const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.part_ml + s * 2));
       const float f = ex2(ml.x - ref);
@@ -63,16 +55,14 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p, i
       }
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int tok = attn_token(p, r0 + r);
-    const long long row = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r0 + r - tok * p.G);
+    const int tok = attn_token(p, j.row0 + r);
+    const long long row = static_cast<long long>(j.token0 + tok) * p.Hq + j.head0 + (j.row0 + r - tok * p.G);
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int d = lane * 4 + i * 128;
-      if (d < D) {
-        using A = AttnType<DTYPE == 1>;
+      if (d < D)
         *reinterpret_cast<uint2*>(p.out + (row * D + d) * 2) =
             make_uint2(A::pack(acc[i].x * inv, acc[i].y * inv), A::pack(acc[i].z * inv, acc[i].w * inv));
-      }
     }
     if (lane == 0 && p.lse) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : ninf();
   }
@@ -181,7 +171,7 @@ cudaError_t launch_attention(bool bf16, const AttnPlan& plan, const AttnParams& 
                           plan.kind >= 2 ? tc : mma, plan.smem, stream);
 }
 
-cudaError_t launch_attention_combine(int dtype, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream) {
+cudaError_t launch_attention_combine(bool bf16, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -191,11 +181,8 @@ cudaError_t launch_attention_combine(int dtype, const AttnPlan& plan, const Attn
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (plan.bn == 64)
-    return dtype == 1 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 1>, p, plan.bm)
-                      : cudaLaunchKernelEx(&cfg, attn_combine_kernel<64, 2>, p, plan.bm);
-  return dtype == 1 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 1>, p, plan.bm)
-                    : cudaLaunchKernelEx(&cfg, attn_combine_kernel<128, 2>, p, plan.bm);
+  return bf16 ? cudaLaunchKernelEx(&cfg, attn_combine_kernel<true>, p, plan.bm)
+              : cudaLaunchKernelEx(&cfg, attn_combine_kernel<false>, p, plan.bm);
 }
 
 }  // namespace sv

@@ -106,7 +106,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
   const AttnSplit split = attn_split<BN>(p, BM, sched);
   const int cta = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (cta >= split.n) return;
+  if (cta >= split.n) {
+    if (tid == 0) attn_leave_join(p, split, cta, BM, 0, 0, nullptr);
+    return;
+  }
   long long u = split.begin(cta);
   const long long u_begin = u, u_end = split.begin(cta + 1);
   AttnCursor cur = attn_locate<BN>(p, BM, u, sched);
@@ -352,8 +355,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(mm, ll);
       }
     }
+    if (u + len >= u_end) {
+      if (tid == 0) attn_leave_join(p, split, cta, BM, u_begin, u, &cur);
+      break;
+    }
     u += len;
-    if (u >= u_end) break;
     __syncthreads();
     attn_next<BN>(p, BM, &cur);
   }

@@ -177,6 +177,25 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
   return c;
 }
 
+// One thread of every CTA, at its last item (u: the unit at which it took the item up; u_begin: its first
+// unit) or, without work, with cur = null: leaves the record for the combine kernel.
+__device__ __forceinline__ void attn_leave_join(const AttnParams& p, const AttnSplit& sp, int cta, int bm, long long u_begin,
+                                                long long u, const AttnCursor* cur) {
+  AttnJoin j = {};
+  if (cur) {
+    const long long start = u - cur->at, end = start + cur->count;
+    if (start >= u_begin && end > sp.begin(cta + 1)) {
+      j.row0 = cur->t * bm;
+      j.rows = min(cur->req.nq * p.G - j.row0, bm);
+      j.token0 = cur->req.q0;
+      j.head0 = cur->h * p.G;
+      j.last = sp.owner(end - 1);
+      j.slot = start == u_begin ? 2 * cta : 2 * cta + 1;
+    }
+  }
+  p.joins[cta] = j;
+}
+
 // The item after the cursor's (the caller knows that there is one).
 template <int BN>
 __device__ __forceinline__ void attn_next(const AttnParams& p, int bm, AttnCursor* c) {

@@ -208,7 +208,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const AttnSplit split = attn_split<BN>(p, BM, sched);
   const int cta = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;");
-  if (cta >= split.n) return;
+  if (cta >= split.n) {
+    if (tid == 0) attn_leave_join(p, split, cta, BM, 0, 0, nullptr);
+    return;
+  }
   const long long u_begin = split.begin(cta), u_end = split.begin(cta + 1);
   AttnCursor cur = attn_locate<BN>(p, BM, u_begin, sched);
 
@@ -638,8 +641,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_before();
         if (joined) mbar_arrive_warp(smem_addr(&bars.x_free));
       }
+      if (u + len >= u_end) {
+        if (tid == 0) attn_leave_join(p, split, cta, BM, u_begin, u, &cur);
+        break;
+      }
       u += len;
-      if (u >= u_end) break;
       attn_next<BN>(p, BM, &cur);
     }
   }

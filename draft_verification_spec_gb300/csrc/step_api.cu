@@ -36,7 +36,7 @@ spec_status_t sm_count(int* sms) {
 }
 
 size_t partial_bytes(const sv::AttnPlan& plan, int D) {
-  return static_cast<size_t>(plan.grid) * 2 * plan.bm * (D + 2) * sizeof(float);
+  return static_cast<size_t>(plan.grid) * (sizeof(sv::AttnJoin) + 2 * plan.bm * (D + 2) * sizeof(float));
 }
 
 // The batch description's checks; `cache`: keys and values are addressed.
@@ -140,14 +140,15 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   p.status = reinterpret_cast<int32_t*>(ws);
-  p.part_ml = reinterpret_cast<float*>(ws + kStatusBytes);
+  p.joins = reinterpret_cast<sv::AttnJoin*>(ws + kStatusBytes);
+  p.part_ml = reinterpret_cast<float*>(p.joins + plan.grid);
   p.part_o = p.part_ml + static_cast<size_t>(plan.grid) * 2 * plan.bm * 2;
   p.min_units = 256 / plan.bn;   // a CTA of its own: 256 keys at least
   p.wait_limit = kWaitNs;
   p.n_max = plan.grid;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sv::launch_attention(bf16, plan, p, maps, s) != cudaSuccess) return SPEC_ERR_CUDA;
-  return sv::launch_attention_combine(dtype, plan, p, s) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  return sv::launch_attention_combine(bf16, plan, p, s) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
 spec_status_t spec_rope_append(const spec_rope_tensors_t* t, int dtype, int q_heads, const spec_paged_batch_t* batch,

@@ -25,6 +25,15 @@ struct PagedBatch {
   int Hkv, D;
 };
 
+// The item that begins in a CTA's run and goes on in others': what the combine kernel joins.
+struct alignas(16) AttnJoin {
+  int rows, row0;            // rows of the item (0: no such item), first row
+  int token0, head0;         // the request's first new token, the key head's first query head
+  int last;                  // last CTA that works on it
+  int slot;                  // this CTA's partial
+  int pad[2];
+};
+
 struct AttnParams {
   PagedBatch c;
   const uint8_t* q;
@@ -38,6 +47,7 @@ struct AttnParams {
   float scale_log2;          // softmax scale x log2(e)
   float* part_o;             // [2 n, BM, D] partial rows of items that more than one CTA works on
   float* part_ml;            // [2 n, BM, 2] their maximum and sum
+  AttnJoin* joins;           // [n]
   int min_units;             // fewest key tiles worth a CTA of their own
   int n_max;                 // CTAs launched
   long long wait_limit;      // ns per bounded wait (tcgen05 kernel)
@@ -60,7 +70,7 @@ int attention_kind(int rows, int D, int page_size, float scale);
 cudaError_t attention_plan(bool bf16, int kind, int D, int sms, AttnPlan* plan);
 bool attention_maps(bool bf16, const PagedBatch& c, AttnMaps* maps);   // false: TMA cannot describe the caches
 cudaError_t launch_attention(bool bf16, const AttnPlan& plan, const AttnParams& p, const AttnMaps& maps, cudaStream_t stream);
-cudaError_t launch_attention_combine(int dtype, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream);
+cudaError_t launch_attention_combine(bool bf16, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream);
 
 struct RopeParams {
   PagedBatch c;              // k / v may be null: nothing is stored
