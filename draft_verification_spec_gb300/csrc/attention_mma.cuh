@@ -107,18 +107,23 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
   const int cta = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;");
   if (cta >= split.n) {
-    if (tid == 0) attn_leave_join(p, split, cta, BM, 0, 0, nullptr);
+    if (tid == 0) attn_leave_join(p, split, cta, BM, nullptr, false);
     return;
   }
-  long long u = split.begin(cta);
-  const long long u_begin = u, u_end = split.begin(cta + 1);
-  AttnCursor cur = attn_locate<BN>(p, BM, u, sched);
+  const long long u_begin = split.begin(cta), u_end = split.begin(cta + 1);
+  AttnCursor cur = attn_locate<BN>(p, BM, u_begin, sched);
+  int k0, k1;
+  cur.share(p, u_begin, u_end, &k0, &k1);
+  if (k1 <= k0) {   // nothing but an item's overhead
+    if (tid == 0) attn_leave_join(p, split, cta, BM, nullptr, false);
+    return;
+  }
+  bool later = false;   // not the CTA's first item
   const uint32_t smem_base = smem_addr(smem);
   const int D = p.c.D, P = p.c.page_size;
 
   while (true) {
-    const int kt0 = cur.first + cur.at;
-    const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
+    const int kt0 = cur.first + k0, len = k1 - k0;
     const int rows = cur.req.nq * p.G, r0 = cur.t * BM, r1 = min(rows, r0 + BM);
     int lo, hi;
     attn_keys(p, cur.req, r0, r1, &lo, &hi);
@@ -322,7 +327,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
     }
     __syncthreads();
     const bool whole = len == cur.count;
-    const int slot = 2 * cta + (u == u_begin ? 0 : 1);
+    const int slot = 2 * cta + (later ? 1 : 0);
     for (int id = tid; id < BM * (DP / 4); id += kAttnThreads) {
       const int r = id / (DP / 4), d = (id % (DP / 4)) * 4;
       if (r0 + r >= r1 || d >= D) continue;
@@ -355,13 +360,15 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
         if (d == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(mm, ll);
       }
     }
-    if (u + len >= u_end) {
-      if (tid == 0) attn_leave_join(p, split, cta, BM, u_begin, u, &cur);
+    AttnCursor next = cur;
+    if (!attn_next<BN>(p, BM, u_end, &next)) {
+      if (tid == 0) attn_leave_join(p, split, cta, BM, &cur, later);
       break;
     }
-    u += len;
+    cur = next;
+    cur.share(p, u_begin, u_end, &k0, &k1);
+    later = true;
     __syncthreads();
-    attn_next<BN>(p, BM, &cur);
   }
 }
 

@@ -1,12 +1,14 @@
 // Work split of the paged attention.
 //
 // An item is one tile of query rows (the new tokens of a request x the query heads of one key
-// head, token-major) of one (request, key head); its units are the key tiles it has to read.  The
-// units of all items, in the order (request, key head, row tile, key tile), are cut into n equal
-// runs, one per CTA, whatever the lengths are: a long cache with few rows is split over many CTAs
-// and a short one shares a CTA.  An item that crosses a cut leaves one partial result (maximum,
-// sum, unnormalised rows) per CTA, and the combine kernel joins them in the order of the keys, so
-// results do not depend on timing.  Lengths are read on the device: the host knows only bounds.
+// head, token-major) of one (request, key head).  It costs a unit per key tile that it has to read, and
+// `overhead` units before them (queries in, rows out, the pipeline filled anew).  The units of all
+// items, in the order (request, key head, row tile, key tile), are cut into n equal runs, one per CTA,
+// whatever the lengths are: a long cache with few rows is split over many CTAs and a short one shares
+// a CTA.  (Without the overhead CTAs with many short items ended a third later than the others.)  An
+// item that crosses a cut leaves one partial result (maximum, sum, unnormalised rows) per CTA, and the
+// combine kernel joins them in the order of the keys, so results do not depend on timing.  Lengths are
+// read on the device: the host knows only bounds.
 #pragma once
 
 #include "spec_device.cuh"
@@ -61,7 +63,7 @@ __device__ __forceinline__ long long attn_request_units(const AttnParams& p, int
     const int nt = attn_row_tiles(p, r, bm);
     for (int t = threadIdx.x & (p.lanes - 1); t < nt; t += p.lanes) {
       int first;
-      n += attn_tiles<BN>(p, r, t, bm, &first);
+      n += p.overhead + attn_tiles<BN>(p, r, t, bm, &first);
     }
   }
   for (int o = p.lanes / 2; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -75,12 +77,18 @@ struct AttnSplit {
   __device__ __forceinline__ int owner(long long u) const { return static_cast<int>(((u + 1) * n - 1) / total); }
 };
 
-// Position of a unit: the item and the unit's index in it.
+// An item, where it starts among the call's units, its key tiles.
 struct AttnCursor {
   int b, h, t;
   AttnReq req;
-  int first, count;   // the item's key tiles
-  int at;             // the unit's place among them
+  int first, count;
+  long long start;
+  // The key tiles [k0, k1) of the item in the run [begin, end) of a CTA (none if k1 <= k0).
+  __device__ __forceinline__ void share(const AttnParams& p, long long begin, long long end, int* k0, int* k1) const {
+    const long long t = start + p.overhead;
+    *k0 = begin > t ? static_cast<int>(begin - t) : 0;
+    *k1 = end - t < count ? static_cast<int>(end - t) : count;
+  }
 };
 
 template <int THREADS>
@@ -113,10 +121,11 @@ __device__ __forceinline__ AttnSplit attn_split(const AttnParams& p, int bm, Att
   return sp;
 }
 
-// Block-wide: the position of unit u (u < total).
+// Block-wide: the item that unit u belongs to (u < total).
 template <int BN, int THREADS>
 __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, long long u, AttnSchedSmem<THREADS>& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x / 32, per = THREADS / p.lanes;
+  long long before = 0;   // units of the requests before this step's
   for (int base = 0; base < p.c.B; base += per) {
     const int b = base + threadIdx.x / p.lanes;
     const long long units = attn_request_units<BN>(p, b, bm);
@@ -135,14 +144,14 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
       if (k < w) incl += s.warp[k];
       all += s.warp[k];
     }
-    if (u >= incl - mine && u < incl) {
+    if (u - before >= incl - mine && u - before < incl) {
       s.b = b;
-      s.rem = u - (incl - mine);
+      s.rem = u - before - (incl - mine);
       s.units = units;
     }
     __syncthreads();
-    if (u < all) break;
-    u -= all;
+    if (u - before < all) break;
+    before += all;
   }
   AttnCursor c;
   c.b = s.b;
@@ -155,7 +164,7 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
   const int nt = attn_row_tiles(p, c.req, bm);
   for (int t0 = 0; t0 < nt; t0 += 32) {
     int first = 0;
-    const long long mine = t0 + lane < nt ? attn_tiles<BN>(p, c.req, t0 + lane, bm, &first) : 0;
+    const long long mine = t0 + lane < nt ? p.overhead + attn_tiles<BN>(p, c.req, t0 + lane, bm, &first) : 0;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -166,9 +175,9 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
     if (hit) {
       const int k = __ffs(hit) - 1;
       c.t = t0 + k;
-      c.count = static_cast<int>(__shfl_sync(0xffffffffu, mine, k));
+      c.count = static_cast<int>(__shfl_sync(0xffffffffu, mine, k)) - p.overhead;
       c.first = __shfl_sync(0xffffffffu, first, k);
-      c.at = static_cast<int>(rem - __shfl_sync(0xffffffffu, incl - mine, k));
+      c.start = u - (rem - __shfl_sync(0xffffffffu, incl - mine, k));
       break;
     }
     rem -= __shfl_sync(0xffffffffu, incl, 31);
@@ -177,41 +186,42 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
   return c;
 }
 
-// One thread of every CTA, at its last item (u: the unit at which it took the item up; u_begin: its first
-// unit) or, without work, with cur = null: leaves the record for the combine kernel.
-__device__ __forceinline__ void attn_leave_join(const AttnParams& p, const AttnSplit& sp, int cta, int bm, long long u_begin,
-                                                long long u, const AttnCursor* cur) {
+// One thread of every CTA, at its last item (`later`: it is not the CTA's first) or, without work, with
+// cur = null: leaves the record for the combine kernel.
+__device__ __forceinline__ void attn_leave_join(const AttnParams& p, const AttnSplit& sp, int cta, int bm, const AttnCursor* cur,
+                                                bool later) {
   AttnJoin j = {};
   if (cur) {
-    const long long start = u - cur->at, end = start + cur->count;
-    if (start >= u_begin && end > sp.begin(cta + 1)) {
+    int k0, k1;
+    cur->share(p, sp.begin(cta), sp.begin(cta + 1), &k0, &k1);
+    if (k0 == 0 && k1 < cur->count) {
       j.row0 = cur->t * bm;
       j.rows = min(cur->req.nq * p.G - j.row0, bm);
       j.token0 = cur->req.q0;
       j.head0 = cur->h * p.G;
-      j.last = sp.owner(end - 1);
-      j.slot = start == u_begin ? 2 * cta : 2 * cta + 1;
+      j.last = sp.owner(cur->start + p.overhead + cur->count - 1);
+      j.slot = 2 * cta + (later ? 1 : 0);
     }
   }
   p.joins[cta] = j;
 }
 
-// The item after the cursor's (the caller knows that there is one).
+// The next item with key tiles in a run that ends at `end`; false if there is none.
 template <int BN>
-__device__ __forceinline__ void attn_next(const AttnParams& p, int bm, AttnCursor* c) {
-  c->at = 0;
-  if (++c->t < attn_row_tiles(p, c->req, bm)) {
-    c->count = attn_tiles<BN>(p, c->req, c->t, bm, &c->first);
-    return;
-  }
-  c->t = 0;
-  if (++c->h == p.c.Hkv) {
-    c->h = 0;
-    do {
-      c->req = attn_request(p.c, ++c->b);
-    } while (c->req.nq == 0);
+__device__ __forceinline__ bool attn_next(const AttnParams& p, int bm, long long end, AttnCursor* c) {
+  c->start += p.overhead + c->count;
+  if (c->start + p.overhead >= end) return false;
+  if (++c->t >= attn_row_tiles(p, c->req, bm)) {
+    c->t = 0;
+    if (++c->h == p.c.Hkv) {
+      c->h = 0;
+      do {
+        c->req = attn_request(p.c, ++c->b);
+      } while (c->req.nq == 0);
+    }
   }
   c->count = attn_tiles<BN>(p, c->req, c->t, bm, &c->first);
+  return true;
 }
 
 }  // namespace sv

@@ -209,11 +209,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const int cta = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;");
   if (cta >= split.n) {
-    if (tid == 0) attn_leave_join(p, split, cta, BM, 0, 0, nullptr);
+    if (tid == 0) attn_leave_join(p, split, cta, BM, nullptr, false);
     return;
   }
   const long long u_begin = split.begin(cta), u_end = split.begin(cta + 1);
   AttnCursor cur = attn_locate<BN>(p, BM, u_begin, sched);
+  int k0, k1;   // the item's key tiles that are this CTA's
+  cur.share(p, u_begin, u_end, &k0, &k1);
+  if (k1 <= k0) {   // nothing but an item's overhead
+    if (tid == 0) attn_leave_join(p, split, cta, BM, nullptr, false);
+    return;
+  }
 
   if (tid == 0) {
     s_abort = 0;
@@ -245,7 +251,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const TcWait wait{&s_abort, p.wait_limit, p.status};
-  long long u = u_begin;
 
   if (warp == 8) {
     // ------------------------------------------------------------------------------ TMA producer
@@ -253,8 +258,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     unsigned g = 0;                                                      // key tiles of this CTA so far
     bool ok = true;
     while (ok) {
-      const int kt0 = cur.first + cur.at;
-      const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
+      const int kt0 = cur.first + k0, len = k1 - k0;
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
       int lo, hi;
       attn_keys(p, cur.req, r0, r1, &lo, &hi);
@@ -290,9 +294,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           if (which && (kt0 + j + 1) * BN > hi) mbar_arrive_warp(smem_addr(&bars.clean_me[st]));
         }
       }
-      u += len;
-      if (u >= u_end) break;
-      attn_next<BN>(p, BM, &cur);
+      if (!attn_next<BN>(p, BM, u_end, &cur)) break;
+      cur.share(p, u_begin, u_end, &k0, &k1);
     }
     if (!ok) {
       // gave up: the copies in flight still land before the block's memory is given back
@@ -356,8 +359,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return true;
       };
       while (ok) {
-        const int kt0 = cur.first + cur.at;
-        const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
+        const int kt0 = cur.first + k0, len = k1 - k0;
         const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
         const bool joined = r1 - r0 <= 128;
         int lo, hi;
@@ -408,9 +410,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             next_k();
           }
         }
-        u += len;
-        if (!ok || u >= u_end) break;
-        attn_next<BN>(p, BM, &cur);
+        if (!ok || !attn_next<BN>(p, BM, u_end, &cur)) break;
+        cur.share(p, u_begin, u_end, &k0, &k1);
       }
       if (!ok) {   // gave up: the MMAs in flight finish before TMEM is freed
         tc_commit(smem_addr(&bars.drain));
@@ -427,8 +428,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     unsigned g = 0, asked = 0;   // phases of clean_me, a bit per slot
     bool ok = true;
     while (ok) {
-      const int kt0 = cur.first + cur.at;
-      const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
+      const int kt0 = cur.first + k0, len = k1 - k0;
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
       int lo, hi;
       attn_keys(p, cur.req, r0, r1, &lo, &hi);
@@ -447,9 +447,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_arrive_warp(smem_addr(&bars.v_clean[st]));
       }
       g += len;
-      u += len;
-      if (u >= u_end) break;
-      attn_next<BN>(p, BM, &cur);
+      if (!attn_next<BN>(p, BM, u_end, &cur)) break;
+      cur.share(p, u_begin, u_end, &k0, &k1);
     }
   } else {
     // ------------------------------------------------------------------------------------ softmax
@@ -458,10 +457,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     const uint32_t t_s = tmem + lanes + half * 128, t_o = tmem + lanes + 256 + half * 128;
     const uint32_t bar_s = smem_addr(&bars.s_full[half]);
     unsigned tiles = 0, segs = 0, joins = 0;
+    bool later = false;             // not the CTA's first item
     bool ok = true, owed = false;   // owed: half 0 may still read this half's O and statistics
     while (ok) {
-      const int kt0 = cur.first + cur.at;
-      const int len = static_cast<int>(min(static_cast<long long>(cur.count - cur.at), u_end - u));
+      const int kt0 = cur.first + k0, len = k1 - k0;
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
       const bool joined = r1 - r0 <= 128;
       const int h0 = r0 + (joined ? 0 : half * 128), r = h0 + row;
@@ -601,7 +600,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         const bool both = joined && len > 1;
         const int tok = attn_token(p, r);
         const long long orow = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r - tok * p.G);
-        const long long prow = static_cast<long long>(2 * cta + (u == u_begin ? 0 : 1)) * BM + (r - r0);
+        const long long prow = static_cast<long long>(2 * cta + (later ? 1 : 0)) * BM + (r - r0);
         if (busy) {
 #pragma unroll 1
           for (int c = 0; c < DP / 32; ++c) {
@@ -641,12 +640,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         tc_fence_before();
         if (joined) mbar_arrive_warp(smem_addr(&bars.x_free));
       }
-      if (u + len >= u_end) {
-        if (tid == 0) attn_leave_join(p, split, cta, BM, u_begin, u, &cur);
+      AttnCursor next = cur;
+      if (!attn_next<BN>(p, BM, u_end, &next)) {
+        if (tid == 0) attn_leave_join(p, split, cta, BM, &cur, later);
         break;
       }
-      u += len;
-      attn_next<BN>(p, BM, &cur);
+      cur = next;
+      cur.share(p, u_begin, u_end, &k0, &k1);
+      later = true;
     }
   }
   tc_fence_before();

@@ -143,7 +143,11 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   p.joins = reinterpret_cast<sv::AttnJoin*>(ws + kStatusBytes);
   p.part_ml = reinterpret_cast<float*>(p.joins + plan.grid);
   p.part_o = p.part_ml + static_cast<size_t>(plan.grid) * 2 * plan.bm * 2;
-  p.min_units = 256 / plan.bn;   // a CTA of its own: 256 keys at least
+  // an item's fixed cost in key tiles.  Measured, 64 requests x 4 tokens, ragged to 4096 keys (mma.sync):
+  // 0: 140, 1: 127, 2: 115, 3: 113, 4: 114 us; 32 x 17 tokens, 64 query heads, ragged to 16384 (tcgen05):
+  // 0: 248, 2: 234, 3: 224, 4: 220, 6: 220 us.
+  p.overhead = plan.kind >= 2 ? 4 : 3;
+  p.min_units = 256 / plan.bn + p.overhead;   // a CTA of its own: 256 keys at least
   p.wait_limit = kWaitNs;
   p.n_max = plan.grid;
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -48,7 +48,8 @@ struct AttnParams {
   float* part_o;             // [2 n, BM, D] partial rows of items that more than one CTA works on
   float* part_ml;            // [2 n, BM, 2] their maximum and sum
   AttnJoin* joins;           // [n]
-  int min_units;             // fewest key tiles worth a CTA of their own
+  int overhead;              // an item's cost beside its key tiles, in key tiles
+  int min_units;             // fewest units worth a CTA of their own
   int n_max;                 // CTAs launched
   long long wait_limit;      // ns per bounded wait (tcgen05 kernel)
   int32_t* status;
