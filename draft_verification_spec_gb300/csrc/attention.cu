@@ -6,9 +6,6 @@
 
 #include "attention_tc.cuh"
 
-#ifndef TC_ROWS
-#define TC_ROWS 64
-#endif
 namespace sv {
 
 template <>
@@ -116,11 +113,14 @@ cudaError_t attention_plan(bool bf16, int kind, int D, int sms, AttnPlan* plan) 
   return e;
 }
 
-// The 16-row kernel where the rows of a request and key head fit one tile; the tcgen05 kernel where
-// they are more than 64, heads are of 64 to 128 values and pages are whole TMA boxes; else 64-row tiles.
+// The tcgen05 kernel where a request and key head have more than 16 rows, heads are of 64 to 128 values and
+// pages are whole TMA boxes; else 16- and 64-row tiles by mma.sync.  Measured, tcgen05 against mma.sync: 64
+// requests over caches ragged to 4096 keys, 8 key heads of 128: 16 rows 120 : 113 us, 32 rows 115 : 160, 64
+// rows 130 : 188; single tokens (4 rows) to 8192 keys 235 : 195 (a 128-row product for 4 rows, and one warp's
+// softmax in the way of every key tile).
 int attention_kind(int rows, int D, int page_size, float scale) {
   const bool pow2 = (page_size & (page_size - 1)) == 0;
-  if (rows > TC_ROWS && D >= 64 && D <= 128 && pow2 && page_size >= 8 && scale > 0.f) return rows > 128 ? 3 : 2;
+  if (rows > 16 && D >= 64 && D <= 128 && pow2 && page_size >= 8 && scale > 0.f) return rows > 128 ? 3 : 2;
   return rows <= 16 ? 0 : 1;
 }
 

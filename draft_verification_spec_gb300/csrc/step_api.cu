@@ -90,7 +90,7 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
   const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
   size_t most = 0;   // over the kernels that rows and dim admit
   for (int kind = 0; kind < 4; ++kind) {
-    if (kind < 2 ? (kind == 0) != (rows <= 16) : (dim < 64 || dim > 128 || (kind == 3) != (rows > 128))) continue;
+    if ((kind == 0) != (rows <= 16) || (kind >= 2 && (dim < 64 || dim > 128 || (kind == 3) != (rows > 128)))) continue;
     sv::AttnPlan plan;
     if (sv::attention_plan(dtype == SPEC_BF16, kind, dim, sms, &plan) != cudaSuccess) return 0;
     const size_t n = partial_bytes(plan, dim);

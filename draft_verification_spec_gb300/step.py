@@ -22,6 +22,8 @@ from typing import Optional
 import torch
 
 _CODES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+_device = torch.cuda.current_device
+_current_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stream(), without the object around it
 
 
 # the ABI's structures, packed in one go (a ctypes field costs as much as a check): native alignment
@@ -30,69 +32,87 @@ _ROPE = struct.Struct("@PPPPPqqqqqqqqqq")            # spec_rope_tensors_t
 _SAMPLING = struct.Struct("@fiffPPPP")               # spec_sampling_t
 
 
-def _top():
+_lib = None
+_workspace = None
+
+
+def _bind():
+    """The package's library and workspaces (looked up once: this module is imported by the package)."""
+    global _lib, _workspace
     import draft_verification_spec_gb300 as m
-    return m
+    _lib, _workspace = m.lib(), m._workspace_of
+    return _lib
+
+
+def _check(code, where):
+    import draft_verification_spec_gb300 as m
+    m._check(code, where)
 
 
 def _raw_stream(stream, index):
-    return torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    return _current_stream(index) if stream is None else stream.cuda_stream
 
 
-def _on(*named):
-    """Every (tensor, name) is on the current device; its index."""
-    index = torch.cuda.current_device()
-    for t, name in named:
-        if t is not None and t.get_device() != index:
-            raise ValueError(f"{name} must be on the current device cuda:{index}, it is on {t.device}")
-    return index
+def _where(t, name, index):
+    return ValueError(f"{name} must be on the current device cuda:{index}, it is on {t.device}")
 
 
-def _fresh(stream, *shape, dtype, device):
+def _fresh(stream, shape, dtype, device):
     t = torch.empty(shape, dtype=dtype, device=device)
     if stream is not None:
         t.record_stream(stream)
     return t
 
 
-def _int32(t, name, dim):
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-    if t.dim() != dim or (t.shape[-1] > 1 and t.stride(-1) != 1) or (dim == 2 and t.shape[0] > 1 and t.stride(0) < t.shape[1]):
-        raise ValueError(f"{name} must be a {dim}-dimensional tensor with contiguous rows")
-
-
-def _heads(t, name, n=None, dim=None):
-    """A [tokens, heads, dim] tensor whose heads are contiguous."""
-    if t.dim() != 3 or (n is not None and t.shape[0] != n) or (dim is not None and t.shape[2] != dim):
-        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(t.shape)}")
-    if t.numel() and t.shape[2] > 1 and t.stride(2) != 1:
+def _heads(t, name, index, n=None, dim=None):
+    """Strides of a [tokens, heads, dim] tensor on the current device whose heads are contiguous."""
+    if t.get_device() != index:
+        raise _where(t, name, index)
+    s = t.shape
+    if len(s) != 3 or (n is not None and s[0] != n) or (dim is not None and s[2] != dim):
+        raise ValueError(f"{name} must be [tokens, heads, dim], got {tuple(s)}")
+    st = t.stride()
+    if st[2] != 1 and s[2] > 1 and s[0] and s[1]:
         raise ValueError(f"{name}: the values of a head must be contiguous")
+    return st
 
 
-def _batch(k_cache, v_cache, page_table, kv_lens, cu_q, tokens, kv_heads, dim, dtype):
-    _int32(kv_lens, "kv_lens", 1)
-    _int32(cu_q, "cu_q", 1)
-    B = kv_lens.shape[0]
-    if cu_q.shape[0] != B + 1:
-        raise ValueError(f"cu_q has {cu_q.shape[0]} entries, expected {B + 1}")
+def _batch(k_cache, v_cache, page_table, kv_lens, cu_q, tokens, kv_heads, dim, dtype, index):
+    """spec_paged_batch_t of checked tensors."""
+    if kv_lens.dtype != torch.int32 or cu_q.dtype != torch.int32:
+        raise TypeError(f"kv_lens and cu_q must be torch.int32, got {kv_lens.dtype} and {cu_q.dtype}")
+    if kv_lens.get_device() != index or cu_q.get_device() != index:
+        raise _where(cu_q if kv_lens.get_device() == index else kv_lens, "kv_lens and cu_q", index)
+    ls, cs = kv_lens.shape, cu_q.shape
+    if len(ls) != 1 or len(cs) != 1 or cs[0] != ls[0] + 1 or not (kv_lens.is_contiguous() and cu_q.is_contiguous()):
+        raise ValueError(f"kv_lens and cu_q must be contiguous, of B and B + 1 entries, got {tuple(ls)} and {tuple(cs)}")
+    B = ls[0]
     if k_cache is None:
         return _BATCH.pack(0, 0, 0, 0, 0, 0, 0, 0, 0, 0, kv_heads, dim, 0, 0, 0, B, kv_lens.data_ptr(), cu_q.data_ptr(), tokens)
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.dim() != 4 or t.shape != k_cache.shape or t.shape[2] != kv_heads or t.shape[3] != dim:
-            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected [pages, page_size, {kv_heads}, {dim}]")
-    ks, vs = k_cache.stride(), v_cache.stride()
-    if (ks[3] != 1 or vs[3] != 1) and dim > 1:
+    if k_cache.get_device() != index or v_cache.get_device() != index or page_table.get_device() != index:
+        bad = next(t for t in (k_cache, v_cache, page_table) if t.get_device() != index)
+        raise _where(bad, "k_cache, v_cache and page_table", index)
+    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+        raise TypeError(f"k_cache and v_cache must be {dtype}, got {k_cache.dtype} and {v_cache.dtype}")
+    s = k_cache.shape
+    if len(s) != 4 or v_cache.shape != s or s[2] != kv_heads or s[3] != dim:
+        raise ValueError(f"k_cache and v_cache must be [pages, page_size, {kv_heads}, {dim}], got {tuple(s)} and "
+                         f"{tuple(v_cache.shape)}")
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    if (k3 != 1 or v3 != 1) and dim > 1:
         raise ValueError("k_cache and v_cache: the values of a head must be contiguous")
-    _int32(page_table, "page_table", 2)
-    rows, width = page_table.shape
-    if rows != B:
-        raise ValueError(f"page_table has {rows} rows, expected {B}")
-    return _BATCH.pack(k_cache.data_ptr(), v_cache.data_ptr(), ks[0], ks[1], ks[2], vs[0], vs[1], vs[2],
-                       k_cache.shape[0], k_cache.shape[1], kv_heads, dim, page_table.data_ptr(),
-                       max(page_table.stride(0), width), width, B, kv_lens.data_ptr(), cu_q.data_ptr(), tokens)
+    if page_table.dtype != torch.int32:
+        raise TypeError(f"page_table must be torch.int32, got {page_table.dtype}")
+    if page_table.dim() != 2 or page_table.shape[0] != B:
+        raise ValueError(f"page_table must be [{B}, pages of a request], got {tuple(page_table.shape)}")
+    width = page_table.shape[1]
+    row, col = page_table.stride()
+    if (width > 1 and col != 1) or (B > 1 and row < width):
+        raise ValueError("page_table must have contiguous rows that do not overlap")
+    return _BATCH.pack(k_cache.data_ptr(), v_cache.data_ptr(), k0, k1, k2, v0, v1, v2, s[0], s[1], kv_heads, dim,
+                       page_table.data_ptr(), row if row > width else width, width, B, kv_lens.data_ptr(), cu_q.data_ptr(),
+                       tokens)
 
 
 _ws_bytes: dict = {}
@@ -108,34 +128,34 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     own included.  ``scale`` defaults to dim ** -0.5.  Returns out [tokens, q_heads, dim], with
     ``want_lse`` (out, lse [tokens, q_heads] float32); a row that sees no key gives 0 and -inf.
     """
-    m = _top()
-    code = _CODES.get(q.dtype)
-    if code not in (1, 2):
-        raise TypeError(f"q must be bfloat16 or float16, got {q.dtype}")
-    _heads(q, "q")
-    index = _on((q, "q"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"), (kv_lens, "kv_lens"),
-                (cu_q, "cu_q"), (out, "out"))
+    lib = _lib or _bind()
+    dtype = q.dtype
+    code = _CODES.get(dtype)
+    if code != 1 and code != 2:
+        raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
+    index = _device()
+    q_token, q_head, _ = _heads(q, "q", index)
     n, hq, d = q.shape
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, page_size, kv_heads, dim]")
     hkv = k_cache.shape[2]
-    c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, hkv, d, q.dtype)
+    c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, hkv, d, dtype, index)
     if out is None:
-        out = _fresh(stream, n, hq, d, dtype=q.dtype, device=q.device)
-    elif out.shape != q.shape or out.dtype != q.dtype or not out.is_contiguous():
-        raise ValueError("out must be a contiguous tensor of q's shape and dtype")
-    lse = _fresh(stream, n, hq, dtype=torch.float32, device=q.device) if want_lse else None
+        out = _fresh(stream, (n, hq, d), dtype, q.device)
+    elif out.shape != q.shape or out.dtype != dtype or out.get_device() != index or not out.is_contiguous():
+        raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
+    lse = _fresh(stream, (n, hq), torch.float32, q.device) if want_lse else None
     key = (index, code, hq, hkv, d, max_q)
     need = _ws_bytes.get(key)
     if need is None:
-        need = _ws_bytes[key] = int(m.lib().spec_attention_workspace_bytes(code, hq, hkv, d, int(max_q)))
+        need = _ws_bytes[key] = lib.spec_attention_workspace_bytes(code, hq, hkv, d, max_q)
     raw = _raw_stream(stream, index)
-    buf = (workspace or m._workspace_of(index, raw)).get_step(need, stream)
-    q_token, q_head, _ = q.stride()
-    m._check(m.lib().spec_chunk_attention(q.data_ptr(), q_token, q_head, code, hq, c, max_q,
-                                          d ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
-                                          None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), raw),
-             "spec_chunk_attention")
+    buf = (workspace or _workspace(index, raw)).get_step(need, stream)
+    err = lib.spec_chunk_attention(q.data_ptr(), q_token, q_head, code, hq, c, max_q, d ** -0.5 if scale is None else scale,
+                                   causal, window, out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(),
+                                   buf.numel(), raw)
+    if err:
+        _check(err, "spec_chunk_attention")
     return (out, lse) if want_lse else out
 
 
@@ -164,6 +184,7 @@ class RopePlan:
         if not theta > 0:
             raise ValueError("theta must be positive")
         self.head_dim, self.rotary_dim, self.theta, self.layout = int(head_dim), r, float(theta), layout
+        self.interleaved = int(layout == "interleaved")
         self.frequencies, self.factor = self._frequencies(r, float(theta), scaling)
         turns = [int(round(f / (2.0 * math.pi) * 2.0 ** 64)) % 2 ** 64 for f in self.frequencies]
         signed = [t - 2 ** 64 if t >= 2 ** 63 else t for t in turns]
@@ -211,45 +232,50 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
     rotated queries (in ``q_out``, which may be q).  ``k_out`` receives the rotated keys too (may be k);
     it is required where k_cache, v_cache and page_table are None and nothing is stored.
     """
-    m = _top()
-    code = _CODES.get(q.dtype)
+    lib = _lib or _bind()
+    dtype = q.dtype
+    code = _CODES.get(dtype)
     if code is None:
-        raise TypeError(f"q must be float32, bfloat16 or float16, got {q.dtype}")
-    _heads(q, "q")
+        raise TypeError(f"q must be float32, bfloat16 or float16, got {dtype}")
+    index = _device()
+    q0, q1, _ = _heads(q, "q", index)
     n, hq, d = q.shape
-    _heads(k, "k", n, d)
-    index = _on((q, "q"), (k, "k"), (v, "v"), (k_cache, "k_cache"), (v_cache, "v_cache"), (page_table, "page_table"),
-                (kv_lens, "kv_lens"), (cu_q, "cu_q"), (q_out, "q_out"), (k_out, "k_out"), (rope.turns, "rope"))
+    k0, k1, _ = _heads(k, "k", index, n, d)
+    hkv = k.shape[1]
+    if k.dtype != dtype:
+        raise TypeError(f"k must be {dtype}, got {k.dtype}")
     if rope.head_dim != d:
         raise ValueError(f"the plan is for heads of {rope.head_dim}, q has {d}")
-    if k.dtype != q.dtype:
-        raise TypeError(f"k must be {q.dtype}, got {k.dtype}")
+    if rope.turns.get_device() != index:
+        raise _where(rope.turns, "the plan", index)
+    v0 = v1 = vp = o0 = o1 = op = 0
+    ws = None
+    raw = _raw_stream(stream, index)
     if k_cache is not None:
-        _heads(v, "v", n, d)
-        if v.dtype != q.dtype:
-            raise TypeError(f"v must be {q.dtype}, got {v.dtype}")
-        if v.shape[1] != k.shape[1]:
-            raise ValueError(f"v has {v.shape[1]} heads, k {k.shape[1]}")
+        v0, v1, _ = _heads(v, "v", index, n, d)
+        if v.dtype != dtype or v.shape[1] != hkv:
+            raise (TypeError if v.dtype != dtype else ValueError)(f"v must be {dtype} of {hkv} heads, got {v.dtype} of {v.shape[1]}")
+        vp = v.data_ptr()
+        ws = (workspace or _workspace(index, raw)).get_step(256, stream).data_ptr()
     elif k_out is None:
         raise ValueError("k_out is required where there is no cache")
-    c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, k.shape[1], d, q.dtype)
+    c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, hkv, d, dtype, index)
     if q_out is None:
-        q_out = _fresh(stream, n, hq, d, dtype=q.dtype, device=q.device)
-    for t, like, name in ((q_out, q, "q_out"), (k_out, k, "k_out")):
-        if t is not None:
-            if t.shape != like.shape or t.dtype != like.dtype:
-                raise ValueError(f"{name} must have the shape and dtype of the tensor it holds")
-            _heads(t, name)
-    raw = _raw_stream(stream, index)
-    stored = k_cache is not None
-    ws = (workspace or m._workspace_of(index, raw)).get_step(256, stream).data_ptr() if stored else None
-    qs, ks, vs = q.stride(), k.stride(), v.stride() if stored else (0, 0, 0)
-    qo, ko = q_out.stride(), (0, 0, 0) if k_out is None else k_out.stride()
-    r = _ROPE.pack(q.data_ptr(), k.data_ptr(), v.data_ptr() if stored else 0, q_out.data_ptr(),
-                   0 if k_out is None else k_out.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], qo[0], qo[1],
-                   ko[0], ko[1])
-    m._check(m.lib().spec_rope_append(r, code, hq, c, rope.turns.data_ptr(), rope.rotary_dim, rope.factor,
-                                      rope.layout == "interleaved", ws, raw), "spec_rope_append")
+        q_out = _fresh(stream, (n, hq, d), dtype, q.device)
+        w0, w1 = hq * d, d
+    else:
+        w0, w1, _ = _heads(q_out, "q_out", index, n, d)
+        if q_out.shape[1] != hq or q_out.dtype != dtype:
+            raise ValueError("q_out must have q's shape and dtype")
+    if k_out is not None:
+        o0, o1, _ = _heads(k_out, "k_out", index, n, d)
+        if k_out.shape[1] != hkv or k_out.dtype != dtype:
+            raise ValueError("k_out must have k's shape and dtype")
+        op = k_out.data_ptr()
+    r = _ROPE.pack(q.data_ptr(), k.data_ptr(), vp, q_out.data_ptr(), op, q0, q1, k0, k1, v0, v1, w0, w1, o0, o1)
+    err = lib.spec_rope_append(r, code, hq, c, rope.turns.data_ptr(), rope.rotary_dim, rope.factor, rope.interleaved, ws, raw)
+    if err:
+        _check(err, "spec_rope_append")
     return q_out
 
 
@@ -281,15 +307,19 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     all, temperature 0 is greedy.  With ``want_filtered`` the truncated logits come too: what
     verify_chain / verify_block take as the distribution that the token was drawn from.
     """
-    m = _top()
+    lib = _lib or _bind()
     if logits.dim() != 2:
         raise ValueError("logits must be [rows, V]")
-    code = _CODES.get(logits.dtype)
-    if code not in (0, 1):
-        raise TypeError(f"logits must be bfloat16 or float32, got {logits.dtype}")
+    dtype = logits.dtype
+    code = _CODES.get(dtype)
+    if code != 0 and code != 1:
+        raise TypeError(f"logits must be bfloat16 or float32, got {dtype}")
     R, V = logits.shape
-    index, dev = _on((logits, "logits"), (uniforms, "uniforms")), logits.device
-    if (V > 1 and logits.stride(1) != 1) or (R > 1 and logits.stride(0) < V):
+    index, dev = _device(), logits.device
+    if logits.get_device() != index or uniforms.get_device() != index:
+        raise _where(uniforms if logits.get_device() == index else logits, "logits and uniforms", index)
+    row, col = logits.stride()
+    if (V > 1 and col != 1) or (R > 1 and row < V):
         raise ValueError("logits: the values of a row must be contiguous, and rows must not overlap")
     if uniforms.dtype != torch.float32 or tuple(uniforms.shape) != (R,) or not uniforms.is_contiguous():
         raise ValueError(f"uniforms must be a contiguous float32 tensor of {R}")
@@ -299,23 +329,24 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     m0, m1 = _setting("min_p", min_p, torch.float32, R, index)
     c = _SAMPLING.pack(t0, k0, p0, m0, t1, k1, p1, m1)
     if out is None:
-        out = SampleOutput(_fresh(stream, R, dtype=torch.int32, device=dev), _fresh(stream, R, dtype=torch.float32, device=dev),
-                           _fresh(stream, R, dtype=torch.int32, device=dev),
-                           _fresh(stream, R, V, dtype=logits.dtype, device=dev) if want_filtered else None)
+        out = SampleOutput(_fresh(stream, R, torch.int32, dev), _fresh(stream, R, torch.float32, dev),
+                           _fresh(stream, R, torch.int32, dev), _fresh(stream, (R, V), dtype, dev) if want_filtered else None)
     else:
-        for t, name, dtype in ((out.tokens, "tokens", torch.int32), (out.probs, "probs", torch.float32),
+        for t, name, kind in ((out.tokens, "tokens", torch.int32), (out.probs, "probs", torch.float32),
                                (out.kept, "kept", torch.int32)):
-            if t.dtype != dtype or tuple(t.shape) != (R,) or not t.is_contiguous() or t.device != dev:
-                raise ValueError(f"out.{name} must be a contiguous {dtype} tensor of {R} on {dev}")
+            if t.dtype != kind or tuple(t.shape) != (R,) or not t.is_contiguous() or t.device != dev:
+                raise ValueError(f"out.{name} must be a contiguous {kind} tensor of {R} on {dev}")
         f = out.filtered
         if f is not None and (f.dtype != logits.dtype or f.shape != logits.shape or f.device != dev or
                               (V > 1 and f.stride(1) != 1) or (R > 1 and f.stride(0) < V)):
             raise ValueError("out.filtered must have the shape, dtype and device of logits and contiguous rows")
     f = out.filtered
-    m._check(m.lib().spec_sample_tokens(logits.data_ptr(), max(logits.stride(0), V), code, R, V, uniforms.data_ptr(), c,
-                                        out.tokens.data_ptr(), out.probs.data_ptr(), out.kept.data_ptr(),
-                                        None if f is None else f.data_ptr(), V if f is None else max(f.stride(0), V),
-                                        _raw_stream(stream, index)), "spec_sample_tokens")
+    err = lib.spec_sample_tokens(logits.data_ptr(), row if row > V else V, code, R, V, uniforms.data_ptr(), c,
+                                 out.tokens.data_ptr(), out.probs.data_ptr(), out.kept.data_ptr(),
+                                 None if f is None else f.data_ptr(), V if f is None else max(f.stride(0), V),
+                                 _raw_stream(stream, index))
+    if err:
+        _check(err, "spec_sample_tokens")
     return out
 
 
