@@ -43,6 +43,7 @@ struct Geo;
 template <>
 struct Geo<1> {   // bf16: counts only
   using Raw = uint16_t;
+  // 512 threads: 222 us for 1088 rows of 128000 with the filtered rows; 256: 260, 384: 243, 1024: 256 us
   static constexpr int kThreads = 512, kVec = 8, kPer = 21;   // bins per thread: odd, so a warp's reads fall on distinct banks
   static constexpr int kHistWords = kThreads * kPer;
   static constexpr int kDigitWords = 0;                   // the general descent reuses the histogram
@@ -533,6 +534,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     if (out_of_range) s.fallback = 1;
     __syncthreads();
     // the non-empty bins, in order
+    static_assert(PER <= 32, "a bit per bin");
     unsigned filled = 0, listed;   // this thread's bins that are not empty
     unsigned long long none = 0, none_all;
 #pragma unroll
