@@ -16,7 +16,7 @@ namespace sv {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 template <int DTYPE>
 struct RopeType;
@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
 }  // namespace
 
 cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream) {
-  const int vec = dtype == 0 ? 4 : 8, esz = dtype == 0 ? 4 : 2;
+  const int vec = dtype == 0 ? 4 : 8;
   // whole 16-byte pieces: sizes, strides and bases
   const long long strides[] = {p.q_token, p.q_head, p.k_token, p.k_head, p.qo_token, p.qo_head,
                                p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0, p.c.k ? p.v_token : 0, p.c.k ? p.v_head : 0};
@@ -297,7 +297,9 @@ cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream) {
     if (dtype == 2) rope_scalar_kernel<2><<<grid, block, smem, stream>>>(p);
     return cudaGetLastError();
   }
-  // few tokens: a CTA each; many: as many tokens a CTA as leave about a thousand units (four a thread)
+  // few tokens: a CTA each; many: as many tokens a CTA as make about 2048 pieces.  8192 tokens of 40 + 8 heads
+  // of 128, bf16 (201 MB): 41 us with 128 threads and 2048 pieces (4.9 TB/s, 72 % of measured HBM), 43 with
+  // 1024, 49 with 4096; 256 threads 45 us; four pieces in flight a thread instead of two 47 us.
   const int units = (p.Hq + 2 * p.c.Hkv) * (p.c.D / vec);
   int per = p.c.N <= 608 ? 1 : 2048 / (units > 0 ? units : 1);
   per = per < 1 ? 1 : per > kRopeMaxTokens ? kRopeMaxTokens : per;
