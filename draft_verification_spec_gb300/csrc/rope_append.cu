@@ -157,8 +157,8 @@ template <int DTYPE, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, int per_cta) {
   using T = typename RopeType<DTYPE>::T;
   using Pc = Piece<DTYPE>;
-  constexpr int VEC = Pc::VEC;
-  extern __shared__ float2 s_cs[];   // [per_cta][rotary / 2]
+  constexpr int VEC = Pc::VEC, PP = INTERLEAVED ? VEC / 2 : VEC;   // values of a piece, pairs of a unit
+  extern __shared__ __align__(16) float2 s_cs[];   // [per_cta][rotary / 2]
   __shared__ long long s_k[kRopeMaxTokens], s_v[kRopeMaxTokens];
   __shared__ int s_pos[kRopeMaxTokens], s_req[kRopeMaxTokens];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -169,6 +169,18 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   const int rot_units = (p.Hq + Hk) * per_head;
   const int units = rot_units + (p.c.k ? Hk * (D / VEC) : 0);   // per token
   const int total = tokens * units;
+  // quotients of small numbers by the sizes above: floor(n ceil(2^32 / d) / 2^32) is exact while n d < 2^32
+  // (n < 2^16: at most 8 tokens of 2048 pieces; d < 2^16); sizes of 1 wrap to 0 and are handled apart
+  auto inverse = [](int d) { return d > 1 ? 0xffffffffu / static_cast<unsigned>(d) + 1u : 0u; };
+  const unsigned inv_units = inverse(units), inv_head = inverse(per_head), inv_value = inverse(D / VEC);
+  auto quotient = [](int n, unsigned inv) { return inv ? static_cast<int>(__umulhi(static_cast<unsigned>(n), inv)) : n; };
+  // strides fit 32 bits here: one wide multiplication per address
+  const int q_token = static_cast<int>(p.q_token), k_token = static_cast<int>(p.k_token), v_token = static_cast<int>(p.v_token);
+  const int q_head = static_cast<int>(p.q_head), k_head = static_cast<int>(p.k_head), v_head = static_cast<int>(p.v_head);
+  const int qo_token = static_cast<int>(p.qo_token), ko_token = static_cast<int>(p.ko_token);
+  const int qo_head = static_cast<int>(p.qo_head), ko_head = static_cast<int>(p.ko_head);
+  const int kc_head = static_cast<int>(p.c.k_head), vc_head = static_cast<int>(p.c.v_head);
+  auto at2 = [](int i, int si, int j, int sj) { return static_cast<long long>(i) * si + static_cast<long long>(j) * sj; };
 
   struct Unit {
     Pc a, b;
@@ -176,29 +188,29 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
     int t, kind, at;   // kind 0: rotate, 1: copy
   };
   auto load = [&](int u, Unit& x) {
-    x.t = u / units;
+    x.t = quotient(u, inv_units);
     int r = u - x.t * units;
-    const long long n = n0 + x.t;
+    const int n = n0 + x.t;
     const T* src;
     if (r < rot_units) {
-      const int h = r / per_head, j = r - h * per_head, hk = h - p.Hq;
+      const int h = quotient(r, inv_head), j = r - h * per_head, hk = h - p.Hq;
       x.kind = j < turn ? 0 : 1;
       x.at = j < turn ? j * VEC : p.rotary + (j - turn) * VEC;
-      src = hk < 0 ? reinterpret_cast<const T*>(p.q) + n * p.q_token + h * p.q_head
-                   : reinterpret_cast<const T*>(p.k) + n * p.k_token + hk * p.k_head;
-      x.d0 = hk < 0 ? reinterpret_cast<T*>(p.q_out) + n * p.qo_token + h * p.qo_head
-                    : (p.k_out ? reinterpret_cast<T*>(p.k_out) + n * p.ko_token + hk * p.ko_head : nullptr);
-      x.d1 = hk < 0 || !p.c.k ? nullptr : reinterpret_cast<T*>(p.c.k) + hk * p.c.k_head;
+      src = hk < 0 ? reinterpret_cast<const T*>(p.q) + at2(n, q_token, h, q_head)
+                   : reinterpret_cast<const T*>(p.k) + at2(n, k_token, hk, k_head);
+      x.d0 = hk < 0 ? reinterpret_cast<T*>(p.q_out) + at2(n, qo_token, h, qo_head)
+                    : (p.k_out ? reinterpret_cast<T*>(p.k_out) + at2(n, ko_token, hk, ko_head) : nullptr);
+      x.d1 = hk < 0 || !p.c.k ? nullptr : reinterpret_cast<T*>(p.c.k) + at2(hk, kc_head, 0, 0);
       x.a.load(src + x.at);
       if (!INTERLEAVED && x.kind == 0) x.b.load(src + x.at + half);
     } else {
       r -= rot_units;
-      const int h = r / (D / VEC), j = r - h * (D / VEC);
+      const int h = quotient(r, inv_value), j = r - h * (D / VEC);
       x.kind = 2;
       x.at = j * VEC;
       x.d0 = nullptr;
-      x.d1 = reinterpret_cast<T*>(p.c.v) + h * p.c.v_head;
-      x.a.load(reinterpret_cast<const T*>(p.v) + n * p.v_token + h * p.v_head + x.at);
+      x.d1 = reinterpret_cast<T*>(p.c.v) + at2(h, vc_head, 0, 0);
+      x.a.load(reinterpret_cast<const T*>(p.v) + at2(n, v_token, h, v_head) + x.at);
     }
   };
   Unit cur;
@@ -234,7 +246,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   for (int i = tid; i < tokens * half; i += kRopeThreads) {
     const int t = i / half;
     const float2 c = phase_cs(p.freq[i - t * half] * static_cast<unsigned long long>(static_cast<long long>(s_pos[t])));
-    s_cs[i] = make_float2(c.x * p.factor, c.y * p.factor);
+    // two pairs' angles together, then the units side by side: the lanes' 16-byte reads fall on distinct banks
+    const int j = i - t * half, e = j & (PP - 1);
+    s_cs[t * half + ((e >> 1) * turn + j / PP) * 2 + (e & 1)] = make_float2(c.x * p.factor, c.y * p.factor);
   }
   __syncthreads();
   while (u < total) {
@@ -242,23 +256,23 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
     const int un = u + kRopeThreads;
     if (un < total) load(un, next);
     if (s_req[cur.t]) {
-      const float2* cs = s_cs + cur.t * half;
       if (cur.kind == 0) {
-        if (INTERLEAVED) {
+        const float4* cs = reinterpret_cast<const float4*>(s_cs + cur.t * half) + cur.at / VEC;
 #pragma unroll
-          for (int i = 0; i < VEC; i += 2) {
-            const float2 c = cs[(cur.at + i) / 2];
-            const float x = cur.a.get(i), y = cur.a.get(i + 1);
-            cur.a.put(i, x * c.x - y * c.y);
-            cur.a.put(i + 1, y * c.x + x * c.y);
-          }
-        } else {
+        for (int i = 0; i < PP; i += 2) {
+          const float4 w = cs[(i >> 1) * turn];   // cos, sin of pairs i and i + 1
 #pragma unroll
-          for (int i = 0; i < VEC; ++i) {
-            const float2 c = cs[cur.at + i];
-            const float x = cur.a.get(i), y = cur.b.get(i);
-            cur.a.put(i, x * c.x - y * c.y);
-            cur.b.put(i, y * c.x + x * c.y);
+          for (int e = 0; e < 2; ++e) {
+            const float c = e ? w.z : w.x, s = e ? w.w : w.y;
+            if (INTERLEAVED) {
+              const float x = cur.a.get(2 * (i + e)), y = cur.a.get(2 * (i + e) + 1);
+              cur.a.put(2 * (i + e), x * c - y * s);
+              cur.a.put(2 * (i + e) + 1, y * c + x * s);
+            } else {
+              const float x = cur.a.get(i + e), y = cur.b.get(i + e);
+              cur.a.put(i + e, x * c - y * s);
+              cur.b.put(i + e, y * c + x * s);
+            }
           }
         }
       }
@@ -286,7 +300,8 @@ cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream) {
   const long long strides[] = {p.q_token, p.q_head, p.k_token, p.k_head, p.qo_token, p.qo_head,
                                p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0, p.c.k ? p.v_token : 0, p.c.k ? p.v_head : 0};
   bool whole = p.c.D % vec == 0 && p.rotary % (p.interleaved ? vec : 2 * vec) == 0;
-  for (long long s : strides) whole = whole && s % vec == 0;
+  for (long long s : strides) whole = whole && s % vec == 0 && s >= 0 && s < (1ll << 31);
+  whole = whole && p.c.k_head < (1ll << 31) && p.c.v_head < (1ll << 31);
   const void* bases[] = {p.q, p.k, p.c.k ? p.v : nullptr, p.q_out, p.k_out};
   for (const void* b : bases) whole = whole && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
   if (!whole) {

@@ -36,7 +36,7 @@ constexpr int kMagLow = (127 - 32) * 128, kMags = 40 * 128;   // magnitudes of t
 constexpr int kHist = 2 * kMags + 2;                      // positive, zero, negative, below -2^8
 constexpr int kZeroBin = kMags, kLowBin = kHist - 1;
 
-constexpr int kGather = 4096;                             // fp32: tokens of one bin that are looked through in shared memory
+constexpr int kGather = 8192;                             // fp32: tokens of one bin that are looked through in shared memory
 
 template <int DTYPE>
 struct Geo;
@@ -316,11 +316,15 @@ __device__ __noinline__ Prefix descend_bin(const Row<DTYPE>& row, const WeightSc
   if (tokens > kGather) return descend<DTYPE>(row, ws, by_count, target, at, 16, digits, nullptr, -1, s);
   if (threadIdx.x == 0) s.gathered = 0u;
   __syncthreads();
+  // the bin's logits by their bits: 16 top bits, or zero of either sign
+  const bool zero = at.key == 0x8000u;
+  const uint32_t want = zero ? 0u : (at.key & 0x8000u ? at.key & 0x7fffu : 0xffffu & ~at.key);
+  const int shift = zero ? 0 : 16;
   walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, const uint4& piece) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
-      const uint32_t key = sample_key<DTYPE>(value_of<DTYPE>(Row<DTYPE>::value(piece, e)));
-      if (key >> 16 == at.key) keys[atomicAdd(&s.gathered, 1u)] = key;
+      const uint32_t x = Row<DTYPE>::value(piece, e);
+      if ((zero ? x & 0x7fffffffu : x) >> shift == want) keys[atomicAdd(&s.gathered, 1u)] = sample_key<DTYPE>(value_of<DTYPE>(x));
     }
   });
   __syncthreads();
@@ -497,12 +501,13 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     unsigned n_min = 0, n_all;
     unsigned long long m_min = 0, m_all;
     bool out_of_range = false;
+    const bool count_min = min_p > 0.f;
     auto count = [&](Raw x, unsigned at) {
       atomicAdd(&hist[at], 1u);
       if (DTYPE == 0) {
         const unsigned long long w = weight_of(value_of<DTYPE>(x), ws, s.tab);
         if (w) add_weight(&hist[SPAN + at], &hist[2 * SPAN + at], w);
-        if (w >= least) ++n_min, m_min += w;
+        if (count_min && w >= least) ++n_min, m_min += w;
       }
     };
     walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, const uint4& piece) {
