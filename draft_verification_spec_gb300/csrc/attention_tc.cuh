@@ -251,6 +251,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   tc_fence_after();
   const uint32_t tmem = s_tmem;
   const TcWait wait{&s_abort, p.wait_limit, p.status};
+  unsigned issued = 0;   // producer: key tiles whose copies were issued
 
   if (warp == 8) {
     // ------------------------------------------------------------------------------ TMA producer
@@ -297,15 +298,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       if (!attn_next<BN>(p, BM, u_end, &cur)) break;
       cur.share(p, u_begin, u_end, &k0, &k1);
     }
-    if (!ok) {
-      // gave up: the copies in flight still land before the block's memory is given back
-      for (unsigned i = g > 4 ? g - 4 : 0; i <= g; ++i) {
-        const unsigned long long t0 = global_ns();
-        while (!(mbar_try(smem_addr(&bars.k_full[i % KST]), (i / KST) & 1) && mbar_try(smem_addr(&bars.v_full[i % VST]), (i / VST) & 1)) &&
-               global_ns() - t0 < 20000000ull) {
-        }
-      }
-    }
+    issued = g;
   } else if (warp == 9) {
     // -------------------------------------------------------------------------------- MMA issuer
     // The whole loop runs in one elected thread: a warp-wide wait costs three times a thread's, and
@@ -652,6 +645,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (warp == 8 && s_abort) {   // gave up: the copies in flight still land before the block's memory is given back
+    for (unsigned i = issued > KST + VST ? issued - KST - VST : 0; i <= issued; ++i) {
+      const unsigned long long t0 = global_ns();
+      while (!(mbar_try(smem_addr(&bars.k_full[i % KST]), (i / KST) & 1) && mbar_try(smem_addr(&bars.v_full[i % VST]), (i / VST) & 1)) &&
+             global_ns() - t0 < 20000000ull) {
+      }
+    }
+  }
   if (warp == 9) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));

@@ -81,9 +81,20 @@ bool attention_types(int dtype) { return dtype == SPEC_BF16 || dtype == SPEC_F16
 
 }  // namespace
 
+// No C++ exception (a lock or a cache entry that cannot be had) leaves a C entry.
+template <typename F>
+auto guarded(F f, decltype(f()) failed) -> decltype(f()) {
+  try {
+    return f();
+  } catch (...) {
+    return failed;
+  }
+}
+
 extern "C" {
 
 size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int dim, int max_q) {
+  return guarded([&]() -> size_t {
   if (!attention_types(dtype) || kv_heads < 1 || q_heads < kv_heads || dim < 8 || dim > 256 || max_q < 0) return 0;
   int sms = 0;
   if (sm_count(&sms) != SPEC_OK) return 0;
@@ -97,11 +108,13 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
     most = n > most ? n : most;
   }
   return kStatusBytes + (most + 255) / 256 * 256;
+  }, static_cast<size_t>(0));
 }
 
 spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
                                    const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
                                    void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> spec_status_t {
   const sv::ApiRange range("spec_chunk_attention");
   if (!attention_types(dtype) || q_heads < 1 || max_q < 0 || window < 0 || !std::isfinite(scale)) return SPEC_ERR_INVALID_ARG;
   spec_status_t st = check_batch(batch, true, 2);
@@ -155,11 +168,13 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sv::launch_attention(bf16, plan, p, maps, s) != cudaSuccess) return SPEC_ERR_CUDA;
   return sv::launch_attention_combine(bf16, plan, p, s) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  }, SPEC_ERR_CUDA);
 }
 
 spec_status_t spec_rope_append(const spec_rope_tensors_t* t, int dtype, int q_heads, const spec_paged_batch_t* batch,
                                const unsigned long long* freq, int rotary_dim, float factor, int interleaved,
                                void* workspace, void* stream) {
+  return guarded([&]() -> spec_status_t {
   const sv::ApiRange range("spec_rope_append");
   if (!t || (dtype != SPEC_F32 && dtype != SPEC_BF16 && dtype != SPEC_F16) || q_heads < 0) return SPEC_ERR_INVALID_ARG;
   const bool cache = batch && batch->k;
@@ -196,12 +211,14 @@ spec_status_t spec_rope_append(const spec_rope_tensors_t* t, int dtype, int q_he
   p.interleaved = interleaved != 0;
   p.status = static_cast<int32_t*>(workspace);
   return sv::launch_rope(dtype, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  }, SPEC_ERR_CUDA);
 }
 
 spec_status_t spec_sample_tokens(const void* logits, long long row_stride, int dtype, int rows, int V,
                                  const float* uniforms, const spec_sampling_t* how, int32_t* out_tokens,
                                  float* out_probs, int32_t* out_kept, void* out_filtered, long long filtered_stride,
                                  void* stream) {
+  return guarded([&]() -> spec_status_t {
   const sv::ApiRange range("spec_sample_tokens");
   if ((dtype != SPEC_F32 && dtype != SPEC_BF16) || rows < 0 || V < 1 || !how) return SPEC_ERR_INVALID_ARG;
   if (V > kMaxSampleV) return SPEC_ERR_UNSUPPORTED;
@@ -231,6 +248,7 @@ spec_status_t spec_sample_tokens(const void* logits, long long row_stride, int d
   p.filtered = out_filtered;
   p.filtered_stride = filtered_stride;
   return sv::launch_sample(dtype, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  }, SPEC_ERR_CUDA);
 }
 
 }  // extern "C"

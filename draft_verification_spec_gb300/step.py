@@ -145,7 +145,7 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     elif out.shape != q.shape or out.dtype != dtype or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
     lse = _fresh(stream, (n, hq), torch.float32, q.device) if want_lse else None
-    key = (index, code, hq, hkv, d, max_q)
+    key = (index, code, hq, hkv, d, max_q if max_q < 129 else 129)   # more than 128 rows are all alike
     need = _ws_bytes.get(key)
     if need is None:
         need = _ws_bytes[key] = lib.spec_attention_workspace_bytes(code, hq, hkv, d, max_q)

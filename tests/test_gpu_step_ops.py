@@ -199,6 +199,27 @@ def test_attention_page_range_status(sv):
         assert torch.equal(got, sv.chunk_attention(q, zk, zv, table, lens, cu, nq))
 
 
+@pytest.mark.parametrize("nq", [1, 17])
+def test_attention_and_rope_far_pages(sv, nq):
+    """A cache of more than 2^31 values: page offsets pass 32 bits."""
+    dt, page, hkv, d = torch.bfloat16, 16, 8, 128
+    pages = 2 ** 31 // (page * hkv * d) + 64
+    kc, vc = (torch.empty(pages, page, hkv, d, dtype=dt, device="cuda") for _ in range(2))
+    ids = torch.tensor([[pages - 1, 3, pages - 7, pages // 2 + 1]], dtype=torch.int32, device="cuda")
+    small_k, small_v = (torch.randn(4, page, hkv, d, device="cuda").to(dt) for _ in range(2))
+    kc[ids[0].long()], vc[ids[0].long()] = small_k, small_v
+    near = torch.arange(4, dtype=torch.int32, device="cuda")[None]
+    lens, cu = torch.tensor([60], dtype=torch.int32, device="cuda"), torch.tensor([0, nq], dtype=torch.int32, device="cuda")
+    q = torch.randn(nq, 16, d, device="cuda").to(dt)
+    got = sv.chunk_attention(q, kc, vc, ids, lens, cu, nq)
+    assert torch.equal(got, sv.chunk_attention(q, small_k, small_v, near, lens, cu, nq))
+    plan, k = sv.RopePlan(d), torch.randn(nq, hkv, d, device="cuda").to(dt)
+    sv.rope_append(q, k, k, plan, kc, vc, ids, lens, cu)
+    sv.rope_append(q, k, k, plan, small_k, small_v, near, lens, cu)
+    assert torch.equal(kc[ids[0].long()], small_k) and torch.equal(vc[ids[0].long()], small_v)
+    assert sv.default_workspace().status() == 0
+
+
 def test_attention_refusals(sv):
     kc, vc, table, lens, cu = _batch([2], [20], 16, 2, 64, torch.bfloat16, 4)
     q = torch.randn(2, 4, 64).to(torch.bfloat16).cuda()
@@ -453,6 +474,21 @@ def test_sample_crowded_bins(sv):
     u = torch.rand(3, generator=torch.Generator().manual_seed(3)).cuda()
     for s in (dict(), dict(top_k=777, top_p=0.9), dict(top_p=0.4), dict(min_p=0.997)):
         _check_sample(sv, z.cuda(), u, **s)
+
+
+def test_sample_far_rows(sv):
+    """Rows that lie more than 2^31 values apart, in the logits and in the filtered output."""
+    V, far = 3001, 2 ** 31 + 8
+    store = torch.zeros(far + V, dtype=torch.bfloat16, device="cuda")
+    z = store.as_strided((2, V), (far, 1))
+    z[0], z[1] = torch.randn(2, V, device="cuda").to(torch.bfloat16)
+    keep = torch.empty_like(store).as_strided((2, V), (far, 1))
+    u = torch.rand(2, device="cuda")
+    want = sv.sample_tokens(z.contiguous(), u, 0.8, 40, want_filtered=True)
+    out = sv.SampleOutput(torch.empty_like(want.tokens), torch.empty_like(want.probs), torch.empty_like(want.kept), keep)
+    sv.sample_tokens(z, u, 0.8, 40, out=out)
+    assert torch.equal(out.tokens, want.tokens) and torch.equal(out.kept, want.kept)
+    assert torch.equal(out.filtered.contiguous(), want.filtered)
 
 
 def test_sample_uniform_ends(sv):
