@@ -94,10 +94,11 @@ static const void* kernel_of(bool bf16, const AttnPlan& plan) {
   return bf16 ? attn_mma_fn<true>(plan.dp, plan.bm) : attn_mma_fn<false>(plan.dp, plan.bm);
 }
 
-cudaError_t attention_plan(bool bf16, int kind, int D, int sms, AttnPlan* plan) {
+cudaError_t attention_plan(bool bf16, int kind, int rows, int D, int sms, AttnPlan* plan) {
   plan->kind = kind;
   plan->bm = kind == 0 ? 16 : kind == 1 ? 64 : kind == 2 ? 128 : 256;
   plan->bn = kind >= 2 ? kTcBN : kAttnBN;
+  plan->rows = rows < 1 ? 1 : rows < plan->bm ? rows : plan->bm;
   plan->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
   int threads = kAttnThreads;
   if (kind >= 2) {
@@ -176,7 +177,8 @@ cudaError_t launch_attention_combine(bool bf16, const AttnPlan& plan, const Attn
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.gridDim = dim3(plan.grid, plan.bm <= 16 ? 4 : 16, 1);
+  // four rows a warp where an item has as many as it may, a warp a row in 16-row tiles
+  cfg.gridDim = dim3(plan.grid, plan.bm <= 16 ? 4 : (plan.rows + 15) / 16, 1);
   cfg.blockDim = dim3(128, 1, 1);
   cfg.stream = stream;
   cfg.attrs = attr;

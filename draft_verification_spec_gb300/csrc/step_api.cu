@@ -103,7 +103,7 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
   for (int kind = 0; kind < 4; ++kind) {
     if ((kind == 0) != (rows <= 16) || (kind >= 2 && (dim < 64 || dim > 128 || (kind == 3) != (rows > 128)))) continue;
     sv::AttnPlan plan;
-    if (sv::attention_plan(dtype == SPEC_BF16, kind, dim, sms, &plan) != cudaSuccess) return 0;
+    if (sv::attention_plan(dtype == SPEC_BF16, kind, 1, dim, sms, &plan) != cudaSuccess) return 0;
     const size_t n = partial_bytes(plan, dim);
     most = n > most ? n : most;
   }
@@ -134,7 +134,7 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   int kind = sv::attention_kind(static_cast<int>(rows < 1024 ? rows : 1024), batch->dim, batch->page_size, scale);
   if (kind >= 2 && !sv::attention_maps(bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
   sv::AttnPlan plan;
-  if (sv::attention_plan(bf16, kind, batch->dim, sms, &plan) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (sv::attention_plan(bf16, kind, static_cast<int>(rows < 1024 ? rows : 1024), batch->dim, sms, &plan) != cudaSuccess) return SPEC_ERR_CUDA;
   if (ws_bytes < kStatusBytes + partial_bytes(plan, batch->dim)) return SPEC_ERR_WORKSPACE;
   sv::AttnParams p;
   std::memset(&p, 0, sizeof(p));

@@ -59,6 +59,7 @@ struct AttnParams {
 struct AttnPlan {
   int kind;                  // 0: 16-row tiles, 1: 64-row tiles (mma.sync); 2, 3: 128- and 256-row tiles (tcgen05)
   int bm, bn, grid, smem, dp;
+  int rows;                  // the most rows of an item that the caller's bound allows
 };
 
 // TMA descriptors of the two caches.
@@ -68,7 +69,7 @@ struct AttnMaps {
 };
 
 int attention_kind(int rows, int D, int page_size, float scale);
-cudaError_t attention_plan(bool bf16, int kind, int D, int sms, AttnPlan* plan);
+cudaError_t attention_plan(bool bf16, int kind, int rows, int D, int sms, AttnPlan* plan);
 bool attention_maps(bool bf16, const PagedBatch& c, AttnMaps* maps);   // false: TMA cannot describe the caches
 cudaError_t launch_attention(bool bf16, const AttnPlan& plan, const AttnParams& p, const AttnMaps& maps, cudaStream_t stream);
 cudaError_t launch_attention_combine(bool bf16, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream);
