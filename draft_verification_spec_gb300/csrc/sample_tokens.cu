@@ -9,7 +9,8 @@
 // whose inclusive prefix weight is strictly above u x the weight of the n.  Every question is "which
 // element of the order does a count or a weight reach".
 //
-// One CTA per row.  A histogram over the 16 top bits of the logits (those of magnitude 2^-32 to 2^8,
+// One CTA per row, or, where rows are few, a cluster of CTAs (`Cl`) with a share of the row each: histograms
+// are added up over the cluster, and every CTA goes on with the same sums.  A histogram over the 16 top bits of the logits (those of magnitude 2^-32 to 2^8,
 // in descending order, and zero: 10,242 bins) answers it: the non-empty bins, a few hundred to a few
 // thousand, become a list whose counts and weights are summed once over the block, and a question is
 // a search in those sums.  A bf16 bin is one value, so its weight is count x weight and the row needs
@@ -25,6 +26,7 @@
 #include <cuda_bf16.h>
 
 #include "sample_weight.cuh"
+#include "spec_async.cuh"
 #include "step_internal.h"
 
 namespace sv {
@@ -35,6 +37,7 @@ constexpr int kDigitBits = 11, kBins = 1 << kDigitBits;   // the general descent
 constexpr int kMagLow = (127 - 32) * 128, kMags = 40 * 128;   // magnitudes of the histogram, in 7-bit mantissa steps
 constexpr int kHist = 2 * kMags + 2;                      // positive, zero, negative, below -2^8
 constexpr int kZeroBin = kMags, kLowBin = kHist - 1;
+constexpr int kOutside = kHist + 1;                       // the histogram's word for logits without a bin (word kHist stays zero)
 
 constexpr int kGather = 8192;                             // fp32: tokens of one bin that are looked through in shared memory
 
@@ -55,7 +58,7 @@ struct Geo<0> {   // fp32: counts and weights
   static constexpr int kHistWords = 3 * kThreads * kPer;
   static constexpr int kDigitWords = 3 * kBins + kGather;
 };
-static_assert(Geo<1>::kThreads * Geo<1>::kPer > kHist && Geo<0>::kThreads * Geo<0>::kPer > kHist, "every bin has a thread");
+static_assert(Geo<1>::kThreads * Geo<1>::kPer > kHist + 1 && Geo<0>::kThreads * Geo<0>::kPer > kHist + 1, "every bin has a thread");
 static_assert(Geo<1>::kHistWords >= 3 * kBins, "the general descent fits the histogram");
 
 template <int DTYPE>
@@ -115,11 +118,14 @@ struct Row {
   static constexpr int VEC = Geo<DTYPE>::kVec;
   const Raw* p;
   int V, head, full, units;   // units 1 .. full are whole pieces
-  __device__ __forceinline__ Row(const void* base, int v) : p(static_cast<const Raw*>(base)), V(v) {
+  int u0, u1;                 // this CTA's units
+  __device__ __forceinline__ Row(const void* base, int v, int rank, int ctas) : p(static_cast<const Raw*>(base)), V(v) {
     const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(base) & 15u) / static_cast<int>(sizeof(Raw));
     head = min(V, mis ? VEC - mis : 0);
     full = (V - head) / VEC;
     units = full + 2;
+    u0 = units * rank / ctas;
+    u1 = units * (rank + 1) / ctas;
   }
   __device__ __forceinline__ bool whole(int u) const { return u > 0 && u <= full; }
   __device__ __forceinline__ int first(int u) const { return u == 0 ? 0 : head + (u - 1) * VEC; }
@@ -190,7 +196,7 @@ struct Prefix {
   uint32_t key;            // the group's key (or its place in the bins' list)
 };
 
-template <int NT>
+template <int NT, bool Cl>
 struct Shared {
   unsigned long long tab[64];
   unsigned long long wmass[32];
@@ -200,14 +206,86 @@ struct Shared {
   unsigned long long least, target;  // min-p's weight; the weight that is looked for
   float prob;
   unsigned group_in;                 // how many of a group's tokens reach the target
-  int fallback, token;
+  int token;
   unsigned gathered;
+  // what the CTAs of a cluster tell one another, in two places in turn
+  int rank, ctas, turn;
+  struct {
+    unsigned a, b;
+    unsigned long long m;
+    float top;
+  } said[2];
 };
 
+template <typename T>
+__device__ __forceinline__ const T* of_peer(const T* p, int rank) {
+  const T* q;
+  asm volatile("mapa.u64 %0, %1, %2;" : "=l"(q) : "l"(p), "r"(rank));
+  return q;
+}
+
+// Sums over the cluster (`lower`: over the CTAs before this one) and its largest value, with one cluster
+// barrier: what was said last but one has been read by everybody who passed the last one.
+template <int NT, bool Cl>
+__device__ __noinline__ float cluster_sum(unsigned& a, unsigned& b, unsigned long long& m, float top, bool lower, Shared<NT, Cl>& s) {
+  const int t = s.turn;
+  if (threadIdx.x == 0) s.said[t].a = a, s.said[t].b = b, s.said[t].m = m, s.said[t].top = top;
+  cluster_sync();
+  a = b = 0u;
+  m = 0ull;
+  for (int r = 0; r < s.ctas; ++r) {
+    const auto* o = of_peer(&s.said[t], r);
+    top = fmaxf(top, o->top);
+    if (lower && r >= s.rank) continue;
+    a += o->a;
+    b += o->b;
+    m += o->m;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0) s.turn = t ^ 1;
+  __syncthreads();
+  return top;
+}
+
+// Adds up the cluster's copies of an array of 4 n counts and, behind it (weights), of the low and high words
+// of 4 n 64-bit sums.  Every CTA sums a share, then fetches the others'.
+template <int NT, bool Cl>
+__device__ __noinline__ void cluster_merge(unsigned* words, int n, bool weights, Shared<NT, Cl>& s) {
+  uint4* c = reinterpret_cast<uint4*>(words);
+  const int me = s.rank, i0 = n * me / s.ctas, i1 = n * (me + 1) / s.ctas;
+  cluster_sync();
+  for (int i = i0 + threadIdx.x; i < i1; i += NT) {
+    uint4 x = c[i], lo = make_uint4(0u, 0u, 0u, 0u), hi = lo;
+    if (weights) lo = c[n + i], hi = c[2 * n + i];
+    for (int k = 1; k < s.ctas; ++k) {
+      const uint4* o = of_peer(c, (me + k) % s.ctas);
+      const uint4 y = o[i];
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      if (weights) {
+        const uint4 l = o[n + i], h = o[2 * n + i];
+        lo.x += l.x, lo.y += l.y, lo.z += l.z, lo.w += l.w;
+        hi.x += h.x + (lo.x < l.x), hi.y += h.y + (lo.y < l.y), hi.z += h.z + (lo.z < l.z), hi.w += h.w + (lo.w < l.w);
+      }
+    }
+    c[i] = x;
+    if (weights) c[n + i] = lo, c[2 * n + i] = hi;
+  }
+  cluster_sync();
+  for (int k = 1; k < s.ctas; ++k) {
+    const int r = (me + k) % s.ctas, j0 = n * r / s.ctas, j1 = n * (r + 1) / s.ctas;
+    const uint4* o = of_peer(c, r);
+    for (int i = j0 + threadIdx.x; i < j1; i += NT) {
+      c[i] = o[i];
+      if (weights) c[n + i] = o[n + i], c[2 * n + i] = o[2 * n + i];
+    }
+  }
+  cluster_sync();   // nobody changes its words before all have fetched them
+}
+
 // Block-wide exclusive prefix of (count, weight); the totals too.
-template <int NT>
+template <int NT, bool Cl>
 __device__ __forceinline__ void block_scan(unsigned& c, unsigned long long& m, unsigned* c_all, unsigned long long* m_all,
-                                           Shared<NT>& s) {
+                                           Shared<NT, Cl>& s) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   unsigned ic = c;
   unsigned long long im = m;
@@ -247,10 +325,10 @@ __device__ __forceinline__ void add_weight(unsigned* lo, unsigned* hi, unsigned 
 // Block-wide: the group of equal keys in which the order's count or weight reaches `target` (1 <= target
 // <= the row's), among the tokens whose key begins with at.key, `bits` bits being open.  With `gathered`
 // >= 0 those tokens' keys are in `keys`, else the row is read, once per 11 bits.
-template <int DTYPE>
+template <int DTYPE, bool Cl>
 __device__ __noinline__ Prefix descend(const Row<DTYPE>& row, const WeightScale& ws, bool by_count, unsigned long long target,
                                        Prefix at, int bits, unsigned* digits, const uint32_t* keys, int gathered,
-                                       Shared<Geo<DTYPE>::kThreads>& s) {
+                                       Shared<Geo<DTYPE>::kThreads, Cl>& s) {
   constexpr int NT = Geo<DTYPE>::kThreads, PER = kBins / NT, VEC = Geo<DTYPE>::kVec;
   const int tid = threadIdx.x;
   unsigned *cnt = digits, *lo = digits + kBins, *hi = digits + 2 * kBins;
@@ -268,7 +346,7 @@ __device__ __noinline__ Prefix descend(const Row<DTYPE>& row, const WeightScale&
     if (gathered >= 0) {
       for (int i = tid; i < gathered; i += NT) take(keys[i], key_value<DTYPE>(keys[i]));
     } else {
-      walk<DTYPE, 2>(row, tid, row.units, NT, [&](int, const uint4& piece) {
+      walk<DTYPE, 2>(row, row.u0 + tid, row.u1, NT, [&](int, const uint4& piece) {
 #pragma unroll
         for (int e = 0; e < VEC; ++e) {
           const float z = value_of<DTYPE>(Row<DTYPE>::value(piece, e));
@@ -277,6 +355,7 @@ __device__ __noinline__ Prefix descend(const Row<DTYPE>& row, const WeightScale&
       });
     }
     __syncthreads();
+    if (Cl && gathered < 0) cluster_merge<NT, Cl>(digits, kBins / 4, true, s);
     // thread t holds PER bins from the top
     unsigned c[PER], bc = 0, all_c;
     unsigned long long m[PER], bm = 0, all_m;
@@ -288,7 +367,7 @@ __device__ __noinline__ Prefix descend(const Row<DTYPE>& row, const WeightScale&
       bc += c[e];
       bm += m[e];
     }
-    block_scan<NT>(bc, bm, &all_c, &all_m, s);
+    block_scan<NT, Cl>(bc, bm, &all_c, &all_m, s);
     bc += at.cnt;
     bm += at.mass;
 #pragma unroll
@@ -307,20 +386,20 @@ __device__ __noinline__ Prefix descend(const Row<DTYPE>& row, const WeightScale&
 }
 
 // fp32, block-wide: the same among the tokens of one bin (16 open bits), whose keys are gathered first.
-template <int DTYPE>
+template <int DTYPE, bool Cl>
 __device__ __noinline__ Prefix descend_bin(const Row<DTYPE>& row, const WeightScale& ws, bool by_count,
                                            unsigned long long target, Prefix at, unsigned tokens, unsigned* digits,
-                                           Shared<Geo<DTYPE>::kThreads>& s) {
+                                           Shared<Geo<DTYPE>::kThreads, Cl>& s) {
   constexpr int NT = Geo<DTYPE>::kThreads, VEC = Geo<DTYPE>::kVec;
   uint32_t* keys = digits + 3 * kBins;
-  if (tokens > kGather) return descend<DTYPE>(row, ws, by_count, target, at, 16, digits, nullptr, -1, s);
+  if (tokens > kGather) return descend<DTYPE, Cl>(row, ws, by_count, target, at, 16, digits, nullptr, -1, s);
   if (threadIdx.x == 0) s.gathered = 0u;
   __syncthreads();
   // the bin's logits by their bits: 16 top bits, or zero of either sign
   const bool zero = at.key == 0x8000u;
   const uint32_t want = zero ? 0u : (at.key & 0x8000u ? at.key & 0x7fffu : 0xffffu & ~at.key);
   const int shift = zero ? 0 : 16;
-  walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, const uint4& piece) {
+  walk<DTYPE, 4>(row, row.u0 + threadIdx.x, row.u1, NT, [&](int, const uint4& piece) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const uint32_t x = Row<DTYPE>::value(piece, e);
@@ -328,15 +407,27 @@ __device__ __noinline__ Prefix descend_bin(const Row<DTYPE>& row, const WeightSc
     }
   });
   __syncthreads();
-  return descend<DTYPE>(row, ws, by_count, target, at, 16, digits, keys, static_cast<int>(tokens), s);
+  if (Cl) {   // the others' keys behind one's own
+    cluster_sync();
+    unsigned have = s.gathered;
+    for (int k = 1; k < s.ctas; ++k) {
+      const int r = (s.rank + k) % s.ctas;
+      const unsigned n = *of_peer(&s.gathered, r);
+      const uint32_t* o = of_peer(keys, r);
+      for (unsigned i = threadIdx.x; i < n; i += NT) keys[have + i] = o[i];
+      have += n;
+    }
+    cluster_sync();   // nobody gathers again before all have copied
+  }
+  return descend<DTYPE, Cl>(row, ws, by_count, target, at, 16, digits, keys, static_cast<int>(tokens), s);
 }
 
 // Block-wide largest logit (NaN left out).
-template <int DTYPE>
-__device__ __noinline__ float row_max(const Row<DTYPE>& row, Shared<Geo<DTYPE>::kThreads>& s) {
+template <int DTYPE, bool Cl>
+__device__ __noinline__ float row_max(const Row<DTYPE>& row, Shared<Geo<DTYPE>::kThreads, Cl>& s) {
   constexpr int NT = Geo<DTYPE>::kThreads, VEC = Geo<DTYPE>::kVec;
   float top = ninf();
-  walk<DTYPE, 4>(row, threadIdx.x, row.units, NT, [&](int, const uint4& piece) {
+  walk<DTYPE, 4>(row, row.u0 + threadIdx.x, row.u1, NT, [&](int, const uint4& piece) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) top = fmaxf(top, value_of<DTYPE>(Row<DTYPE>::value(piece, e)));
   });
@@ -346,6 +437,11 @@ __device__ __noinline__ float row_max(const Row<DTYPE>& row, Shared<Geo<DTYPE>::
   __syncthreads();
   for (int w = 0; w < NT / 32; ++w) top = fmaxf(top, __uint_as_float(s.wcnt2[w]));
   __syncthreads();
+  if (Cl) {
+    unsigned a = 0, b = 0;
+    unsigned long long m = 0;
+    top = cluster_sum<NT, Cl>(a, b, m, top, false, s);
+  }
   return top;
 }
 
@@ -355,12 +451,12 @@ struct Totals {
 };
 
 // The general way's totals.
-template <int DTYPE>
+template <int DTYPE, bool Cl>
 __device__ __noinline__ Totals row_totals(const Row<DTYPE>& row, const WeightScale& ws, unsigned long long least,
-                                          Shared<Geo<DTYPE>::kThreads>& s) {
+                                          Shared<Geo<DTYPE>::kThreads, Cl>& s) {
   constexpr int NT = Geo<DTYPE>::kThreads, VEC = Geo<DTYPE>::kVec;
   Totals t = {0u, 0u, 0ull, 0ull};
-  walk<DTYPE, 1>(row, threadIdx.x, row.units, NT, [&](int, const uint4& piece) {
+  walk<DTYPE, 1>(row, row.u0 + threadIdx.x, row.u1, NT, [&](int, const uint4& piece) {
 #pragma unroll
     for (int e = 0; e < VEC; ++e) {
       const float z = value_of<DTYPE>(Row<DTYPE>::value(piece, e));
@@ -373,7 +469,11 @@ __device__ __noinline__ Totals row_totals(const Row<DTYPE>& row, const WeightSca
   });
   unsigned c = t.n_all;
   unsigned long long m = t.m_all;
-  block_scan<NT>(c, m, &t.n_all, &t.m_all, s);
+  block_scan<NT, Cl>(c, m, &t.n_all, &t.m_all, s);
+  if (Cl) {
+    unsigned none = 0;
+    cluster_sum<NT, Cl>(t.n_all, none, t.m_all, 0.f, false, s);
+  }
   return t;
 }
 
@@ -403,13 +503,13 @@ struct Group {
 };
 
 // Block-wide: the group in which the order's count or weight reaches the target.
-template <int DTYPE>
+template <int DTYPE, bool Cl>
 __device__ __noinline__ Group reach(const Row<DTYPE>& row, const WeightScale& ws, Bins<DTYPE>& bins, bool by_count,
-                                    unsigned long long target, Shared<Geo<DTYPE>::kThreads>& s) {
+                                    unsigned long long target, Shared<Geo<DTYPE>::kThreads, Cl>& s) {
   constexpr int kBitsAll = DTYPE == 1 ? 16 : 32;
   Prefix g = {0u, 0ull, 0u};
   if (bins.general) {
-    g = descend<DTYPE>(row, ws, by_count, target, g, kBitsAll, bins.digits, nullptr, -1, s);
+    g = descend<DTYPE, Cl>(row, ws, by_count, target, g, kBitsAll, bins.digits, nullptr, -1, s);
   } else {
     unsigned c = bins.cnt;
     unsigned long long m = bins.mass;
@@ -433,19 +533,19 @@ __device__ __noinline__ Group reach(const Row<DTYPE>& row, const WeightScale& ws
       // among the logits below -2^8 (a count went there): their weights are zero, all digits are open.
       // In bf16 the descent's histogram takes the list's place: later questions go the general way.
       const Prefix low = {0u, 0ull, 0u};
-      g = descend<DTYPE>(row, ws, true, target, low, kBitsAll, bins.digits, nullptr, -1, s);
+      g = descend<DTYPE, Cl>(row, ws, true, target, low, kBitsAll, bins.digits, nullptr, -1, s);
       if (DTYPE == 1) bins.general = true;
     } else {
       const unsigned tokens = bins.hist[place_of(g.key)];
       g.key = bin_key16(g.key);
-      g = descend_bin<DTYPE>(row, ws, by_count, target, g, tokens, bins.digits, s);
+      g = descend_bin<DTYPE, Cl>(row, ws, by_count, target, g, tokens, bins.digits, s);
     }
   }
   const float z = key_value<DTYPE>(g.key);
   return {z, g.cnt, g.mass, weight_of(z, ws, s.tab)};
 }
 
-template <int DTYPE>
+template <int DTYPE, bool Cl>
 __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) sample_kernel_row(const SampleParams p) {
   using G = Geo<DTYPE>;
   using Raw = typename G::Raw;
@@ -454,9 +554,10 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
   unsigned* hist = dyn;                                           // [SPAN] counts (fp32: then weights, low and high words)
   unsigned* digits = DTYPE == 1 ? dyn : dyn + G::kHistWords;      // the general descent's
   uint16_t* list = reinterpret_cast<uint16_t*>(dyn + G::kHistWords + G::kDigitWords);   // non-empty bins
-  __shared__ Shared<NT> s;
-  const int r = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const Row<DTYPE> row(static_cast<const Raw*>(p.logits) + static_cast<long long>(r) * p.stride, p.V);
+  __shared__ Shared<NT, Cl> s;
+  const int ctas = Cl ? static_cast<int>(cluster_ncta()) : 1, cta = Cl ? static_cast<int>(cluster_rank()) : 0;
+  const int r = blockIdx.x / ctas, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const Row<DTYPE> row(static_cast<const Raw*>(p.logits) + static_cast<long long>(r) * p.stride, p.V, cta, ctas);
 
   float T = p.temperature ? p.temperature[r] : p.temperature0;
   int k = p.top_k ? p.top_k[r] : p.top_k0;
@@ -468,17 +569,21 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
   }
   if (tid < 64) s.tab[tid] = kExp2Table[tid];
   if (tid == 0) {   // 64-bit floating point is slow here: one thread does what there is of it
-    s.fallback = 0;
+    s.rank = cta;
+    s.ctas = ctas;
+    s.turn = 0;
+    s.token = -1;
     const WeightScale w = weight_scale(0.f, T);
     s.c_hi = w.c_hi;
     s.c_lo = w.c_lo;
     s.least = min_p > 0.f ? static_cast<unsigned long long>(ceil(static_cast<double>(min_p) * kWeightOne)) : 0ull;
   }
+  __syncthreads();
   const bool need_max = DTYPE == 0 || k == 1;
   const bool filter = p.filtered != nullptr;
 
   // the largest logit, where it is needed before the weights
-  float zmax = need_max ? row_max<DTYPE>(row, s) : ninf();
+  float zmax = need_max ? row_max<DTYPE, Cl>(row, s) : ninf();
 
   // what the last pass needs: the drawn value and its rank among its equals, the cut's value and how
   // many of its equals are kept
@@ -510,7 +615,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         if (count_min && w >= least) ++n_min, m_min += w;
       }
     };
-    walk<DTYPE, 4>(row, tid, row.units, NT, [&](int, const uint4& piece) {
+    walk<DTYPE, 4>(row, row.u0 + tid, row.u1, NT, [&](int, const uint4& piece) {
       bool fast = true;   // all of the piece in the bins' range
 #pragma unroll
       for (int e = 0; e < VEC; ++e) {
@@ -536,8 +641,9 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         }
       }
     });
-    if (out_of_range) s.fallback = 1;
+    if (out_of_range) atomicAdd(&hist[kOutside], 1u);
     __syncthreads();
+    if (Cl) cluster_merge<NT, Cl>(hist, SPAN / 4, DTYPE == 0, s);
     // the non-empty bins, in order
     static_assert(PER <= 32, "a bit per bin");
     unsigned filled = 0, listed;   // this thread's bins that are not empty
@@ -548,7 +654,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       filled |= (hist[bin == kHist ? kHist : place_of(bin)] != 0u ? 1u : 0u) << e;
     }
     unsigned at = __popc(filled);
-    block_scan<NT>(at, none, &listed, &none_all, s);
+    block_scan<NT, Cl>(at, none, &listed, &none_all, s);
     for (unsigned left = filled; left; left &= left - 1) list[at++] = static_cast<uint16_t>(tid * PER + __ffs(left) - 1);
     __syncthreads();
     if (DTYPE == 1 && listed > 0) {
@@ -565,7 +671,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     bins.cnt = 0u;
     bins.mass = 0ull;
     // below -2^8 the weights have to be zero (one unknown weight would be wrong)
-    bins.general = s.fallback || (listed > 0 && (list[0] == kLowBin || (hist[kLowBin] && weight_of(-256.f, ws, s.tab) != 0ull)));
+    bins.general = hist[kOutside] || (listed > 0 && (list[0] == kLowBin || (hist[kLowBin] && weight_of(-256.f, ws, s.tab) != 0ull)));
     if (!bins.general) {
       for (int i = bins.i0; i < bins.i1; ++i) {
         const int b = list[i];
@@ -575,19 +681,20 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         bins.mass += DTYPE == 1 ? c * w : w;
         if (DTYPE == 1 && w >= least) n_min += c, m_min += c * w;
       }
-      block_scan<NT>(bins.cnt, bins.mass, &n_all, &m_all, s);
+      block_scan<NT, Cl>(bins.cnt, bins.mass, &n_all, &m_all, s);
     } else {
-      ws.zmax = row_max<DTYPE>(row, s);
-      const Totals t = row_totals<DTYPE>(row, ws, least, s);
+      ws.zmax = row_max<DTYPE, Cl>(row, s);
+      const Totals t = row_totals<DTYPE, Cl>(row, ws, least, s);
       n_all = t.n_all;
       m_all = t.m_all;
       n_min = t.n_min;
       m_min = t.m_min;
     }
     if (min_p > 0.f) {
-      unsigned c = n_min;
+      unsigned c = n_min, none = 0;
       unsigned long long m = m_min;
-      block_scan<NT>(c, m, &n_min, &m_min, s);
+      block_scan<NT, Cl>(c, m, &n_min, &m_min, s);
+      if (Cl && (DTYPE == 0 || bins.general)) cluster_sum<NT, Cl>(n_min, none, m_min, 0.f, false, s);   // else: counted from the merged bins
     }
     any = n_all > 0;
     if (any) {
@@ -596,7 +703,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       Group cut = {0.f, 0u, 0ull, 0ull};
       bool cut_known = false;
       if (k > 0 && static_cast<unsigned>(k) < n) {
-        cut = reach<DTYPE>(row, ws, bins, true, k, s);
+        cut = reach<DTYPE, Cl>(row, ws, bins, true, k, s);
         cut_known = true;
         n = k;
         mass = cut.mass + (k - cut.cnt) * cut.w;
@@ -609,7 +716,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         }
         __syncthreads();
         const unsigned long long target = s.target;
-        const Group g = reach<DTYPE>(row, ws, bins, false, target, s);
+        const Group g = reach<DTYPE, Cl>(row, ws, bins, false, target, s);
         if (tid == 0) s.group_in = static_cast<unsigned>((target - g.mass + g.w - 1) / g.w);
         __syncthreads();
         const unsigned in = s.group_in;
@@ -633,7 +740,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       }
       __syncthreads();
       const unsigned long long target = s.target;
-      const Group g = reach<DTYPE>(row, ws, bins, false, target, s);
+      const Group g = reach<DTYPE, Cl>(row, ws, bins, false, target, s);
       if (tid == 0) {
         s.group_in = static_cast<unsigned>((target - g.mass + g.w - 1) / g.w);
         s.prob = static_cast<float>(static_cast<double>(g.w) / static_cast<double>(mass));
@@ -646,7 +753,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         if (n == n_all) {
           z_cut = ninf();   // everything above -inf stays
         } else {
-          if (!cut_known) cut = reach<DTYPE>(row, ws, bins, true, n, s);
+          if (!cut_known) cut = reach<DTYPE, Cl>(row, ws, bins, true, n, s);
           z_cut = cut.z;
           cut_eq = n - cut.cnt;
           whole_ties = false;
@@ -657,8 +764,8 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
 
   // ordered passes: warp w takes a contiguous share of the units, so that equal logits can be counted in
   // index order.  First the equal ones per warp, then the drawn token, then the filtered row.
-  const int per_warp = (row.units + NW - 1) / NW, u0 = min(row.units, warp * per_warp), u1 = min(row.units, u0 + per_warp);
-  int token = -1;
+  const int per_warp = (row.u1 - row.u0 + NW - 1) / NW;
+  const int u0 = min(row.u1, row.u0 + warp * per_warp), u1 = min(row.u1, u0 + per_warp);
   if (any) {
     unsigned eq = 0, eq_cut = 0;
     const Compare<DTYPE> drawn(z_draw), cutoff(z_cut);
@@ -677,17 +784,22 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
     eq_cut = __reduce_add_sync(0xffffffffu, eq_cut);
     if (lane == 0) s.wcnt[warp] = eq, s.wcnt2[warp] = eq_cut;
     __syncthreads();
-    unsigned before_cut = 0, before = 0;
-    int owner = 0;
+    unsigned before = 0, before_cut = 0;   // equal ones in the CTAs before this one, then in the warps too
+    if (Cl) {
+      unsigned long long none = 0;
+      for (int w = 0; w < NW; ++w) before += s.wcnt[w], before_cut += s.wcnt2[w];
+      cluster_sum<NT, Cl>(before, before_cut, none, 0.f, true, s);
+    }
+    int owner = rank >= before ? 0 : NW;
     for (int w = 0; w < NW; ++w) {
       if (w < warp) before_cut += s.wcnt2[w];
       if (owner == w && rank - before >= s.wcnt[w]) before += s.wcnt[w], ++owner;
     }
     __syncthreads();
-    {
+    if (!Cl || owner < NW) {
       // the drawn token is in warp `owner`'s share: the whole block looks for it, each thread in
       // consecutive units
-      const int o0 = min(row.units, owner * per_warp), o1 = min(row.units, o0 + per_warp);
+      const int o0 = min(row.u1, row.u0 + owner * per_warp), o1 = min(row.u1, o0 + per_warp);
       const int per = (o1 - o0 + NT - 1) / NT, a0 = min(o1, o0 + tid * per), a1 = min(o1, a0 + per);
       unsigned here = 0, all;
       unsigned long long none = 0, none_all;
@@ -697,7 +809,7 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
         for (int e = 0; e < VEC; ++e) here += value_of<DTYPE>(Row<DTYPE>::value(piece, e)) == z_draw;
       }
       unsigned first = here;
-      block_scan<NT>(first, none, &all, &none_all, s);
+      block_scan<NT, Cl>(first, none, &all, &none_all, s);
       const unsigned want = rank - before;
       if (want >= first && want < first + here) {
         unsigned skip = want - first;
@@ -778,37 +890,58 @@ __global__ void __launch_bounds__(Geo<DTYPE>::kThreads, DTYPE == 1 ? 2 : 1) samp
       }
     }
     __syncthreads();
-    token = s.token;
-  } else if (filter) {
-    Raw* out = static_cast<Raw*>(p.filtered) + static_cast<long long>(r) * p.filtered_stride;
-    for (int i = tid; i < p.V; i += NT) out[i] = static_cast<Raw>(DTYPE == 1 ? 0xff80u : 0xff800000u);
+    if (tid == 0 && s.token >= 0) p.tokens[r] = s.token;
+  } else {
+    if (filter) {
+      Raw* out = static_cast<Raw*>(p.filtered) + static_cast<long long>(r) * p.filtered_stride;
+      const int i0 = row.u0 < row.units ? row.first(row.u0) : p.V, i1 = row.u1 < row.units ? row.first(row.u1) : p.V;
+      for (int i = i0 + tid; i < i1; i += NT) out[i] = static_cast<Raw>(DTYPE == 1 ? 0xff80u : 0xff800000u);
+    }
+    if (tid == 0 && cta == 0) p.tokens[r] = -1;
   }
-  if (tid == 0) {
-    p.tokens[r] = token;
+  if (tid == 0 && cta == 0) {
     if (p.probs) p.probs[r] = prob;
     if (p.kept) p.kept[r] = static_cast<int32_t>(n);
   }
+  if (Cl) cluster_sync();   // no CTA leaves while another reads its memory
 }
 
-template <int DTYPE>
-cudaError_t launch(const SampleParams& p, cudaStream_t stream) {
-  static std::atomic<unsigned long long> asked{0};   // devices whose limit has been raised
+template <int DTYPE, bool Cl>
+cudaError_t launch(const SampleParams& p, int ctas, cudaStream_t stream) {
+  static std::atomic<unsigned long long> asked{0};   // devices whose limit of shared memory has been raised
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !(asked.load() >> dev & 1)) {
-    e = cudaFuncSetAttribute(sample_kernel_row<DTYPE>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DTYPE>());
+    e = cudaFuncSetAttribute(sample_kernel_row<DTYPE, Cl>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes<DTYPE>());
     if (e != cudaSuccess) return e;
     if (dev < 64) asked.fetch_or(1ull << dev);
   }
-  sample_kernel_row<DTYPE><<<p.R, Geo<DTYPE>::kThreads, smem_bytes<DTYPE>(), stream>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = ctas;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.gridDim = dim3(p.R * ctas, 1, 1);
+  cfg.blockDim = dim3(Geo<DTYPE>::kThreads, 1, 1);
+  cfg.dynamicSmemBytes = smem_bytes<DTYPE>();
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = Cl ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, sample_kernel_row<DTYPE, Cl>, p);
 }
 
 }  // namespace
 
-cudaError_t launch_sample(int dtype, const SampleParams& p, cudaStream_t stream) {
-  return dtype == 1 ? launch<1>(p, stream) : launch<0>(p, stream);
+cudaError_t launch_sample(int dtype, const SampleParams& p, int sms, cudaStream_t stream) {
+  // as many CTAs a row as leave each an SM and 8192 tokens, at most 8.  One row of 128000 bf16: 32 us with one
+  // CTA, 30.6 with 2, 28.2 with 4, 27.7 with 8 (adding up the histograms takes 7 of them); 64 rows of
+  // 100003 fp32: 130 us with one, 113 with 2.
+  int ctas = 1;
+  while (ctas < 8 && p.R * ctas * 2 <= sms && p.V >= ctas * 2 * 8192) ctas *= 2;
+  if (ctas == 1) return dtype == 1 ? launch<1, false>(p, 1, stream) : launch<0, false>(p, 1, stream);
+  return dtype == 1 ? launch<1, true>(p, ctas, stream) : launch<0, true>(p, ctas, stream);
 }
 
 }  // namespace sv

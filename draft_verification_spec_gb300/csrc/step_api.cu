@@ -247,7 +247,10 @@ spec_status_t spec_sample_tokens(const void* logits, long long row_stride, int d
   p.kept = out_kept;
   p.filtered = out_filtered;
   p.filtered_stride = filtered_stride;
-  return sv::launch_sample(dtype, p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  int sms = 0;
+  const spec_status_t st = sm_count(&sms);
+  if (st != SPEC_OK) return st;
+  return sv::launch_sample(dtype, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
   }, SPEC_ERR_CUDA);
 }
 

@@ -101,6 +101,6 @@ struct SampleParams {
   void* filtered;
   long long filtered_stride;
 };
-cudaError_t launch_sample(int dtype, const SampleParams& p, cudaStream_t stream);
+cudaError_t launch_sample(int dtype, const SampleParams& p, int sms, cudaStream_t stream);
 
 }  // namespace sv
