@@ -129,6 +129,8 @@ class Workspace:
         if self.buf is not None:
             _check(lib().spec_workspace_init(_ptr(self.buf), self.buf.numel(), _stream_ptr(stream)),
                    "spec_workspace_init")
+        if self.step_buf is not None:
+            _check(lib().spec_workspace_init(_ptr(self.step_buf), 256, _stream_ptr(stream)), "spec_workspace_init")
 
 
 _workspaces: dict = {}

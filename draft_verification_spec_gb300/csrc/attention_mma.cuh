@@ -13,6 +13,11 @@
 // warp 16 rows.  Keys and values come by 16-byte asynchronous copies, row addresses a key tile ahead
 // from the page table, in a ring of STAGES tiles; 16-byte pieces are permuted by the row's low bits,
 // which makes the matrix loads free of bank conflicts.
+//
+// Bound: HBM (a key and value byte meets 4 rows x 4 flop at most in its main use).  Measured, heads 32/8 of
+// 128, bf16: 64 single tokens over caches ragged to 8192 keys (1.14 GB) 192-195 us, 5.9 TB/s, 86 % of the
+// measured copy; 64 x 4 tokens to 4096 keys (634 MB) 111-113 us, 83 %.  What is left is the start, the tail
+// and the ring filled anew for every item.
 #pragma once
 
 #include <cuda_bf16.h>

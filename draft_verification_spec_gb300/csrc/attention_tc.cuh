@@ -24,6 +24,11 @@
 // rows are zeroed in shared memory before the MMA reads them (0 x NaN would be NaN); scores are
 // selected, not multiplied.
 //
+// Bound and measured, heads of 128, bf16: 2 x 2048 tokens behind 14336, 32/8 heads (1.03 TFLOP) 728 us, 1.42
+// PFLOP/s, 75 % of the measured matrix rate: a half's softmax (1200 cycles a tile) and its two products (1024)
+// follow one another, and the other half fills most of the gap.  32 x 17 tokens, 64/8 heads, ragged to 16384
+// keys (1.11 GB) 216-220 us, 5.1 TB/s, 75 % of the measured copy: 136 rows take two halves of 128.
+//
 // Every wait is bounded: after `wait_limit` the kernel sets the status word, drains its copies and
 // MMAs, frees TMEM and returns.
 #pragma once
