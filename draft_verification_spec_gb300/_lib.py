@@ -49,6 +49,8 @@ SIGNATURES = {
     "spec_attention_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
     "spec_chunk_attention": (c_int, [c_void_p, c_longlong, c_longlong, c_int, c_int, c_void_p, c_int, c_float,
                                      c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
+    "spec_chunk_attention_tuned": (c_int, [c_void_p, c_longlong, c_longlong, c_int, c_int, c_void_p, c_int, c_float,
+                                           c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
     "spec_rope_append": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_float, c_int, c_void_p,
                                  c_void_p]),
     "spec_sample_tokens": (c_int, [c_void_p, c_longlong, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,

@@ -186,8 +186,8 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
   return c;
 }
 
-// One thread of every CTA, at its last item (`later`: it is not the CTA's first) or, without work, with
-// cur = null: leaves the record for the combine kernel.
+// One thread of every CTA, at its last item (`later`: it is not the CTA's first) or, without work (or not
+// yet done), with cur = null: leaves the record for the combine kernel, an empty one for null.
 __device__ __forceinline__ void attn_leave_join(const AttnParams& p, const AttnSplit& sp, int cta, int bm, const AttnCursor* cur,
                                                 bool later) {
   AttnJoin j = {};

@@ -30,7 +30,7 @@
 // keys (1.11 GB) 216-220 us, 5.1 TB/s, 75 % of the measured copy: 136 rows take two halves of 128.
 //
 // Every wait is bounded: after `wait_limit` the kernel sets the status word, drains its copies and
-// MMAs, frees TMEM and returns.
+// MMAs, frees TMEM and returns, its record for the combine kernel empty.
 #pragma once
 
 #include <cuda.h>
@@ -163,13 +163,14 @@ __device__ __forceinline__ uint64_t tc_desc(uint32_t addr, uint32_t lead) {
 
 struct TcWait {
   volatile int* abort;
-  long long limit;
+  long long limit;   // 0: every wait gives up at once
   int32_t* status;
   // Waits for the phase; false once the limit has passed or another warp gave up.  The clock (whose read
   // takes longer than most waits) is looked at only after a thousand polls.
   __device__ __forceinline__ bool operator()(uint32_t bar, uint32_t parity) const {
+    const int polls = limit > 0 ? 1024 : 0;
 #pragma unroll 1
-    for (int k = 0; k < 1024; ++k)
+    for (int k = 0; k < polls; ++k)
       if (mbar_try(bar, parity)) return true;
     return slowly(bar, parity);
   }
@@ -179,17 +180,16 @@ struct TcWait {
   }
   __device__ __noinline__ bool slowly(uint32_t bar, uint32_t parity) const {
     const unsigned long long t0 = global_ns();
-    while (true) {
+    while (limit > 0) {
 #pragma unroll 1
       for (int k = 0; k < 256; ++k)
         if (mbar_try(bar, parity)) return true;
       if (*abort) return false;
-      if (static_cast<long long>(global_ns() - t0) > limit) {
-        *abort = 1;
-        atomicOr(status, kStatusTimeout);
-        return false;
-      }
+      if (static_cast<long long>(global_ns() - t0) > limit) break;
     }
+    *abort = 1;
+    atomicOr(status, kStatusTimeout);
+    return false;
   }
 };
 
@@ -227,6 +227,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 
   if (tid == 0) {
+    // A CTA that gives up leaves this empty record: the combine kernel runs all the same, and what the
+    // workspace held before must not lead it anywhere.
+    attn_leave_join(p, split, cta, BM, nullptr, false);
     s_abort = 0;
     for (int i = 0; i < 5; ++i) {
       mbar_init(smem_addr(&bars.k_full[i]), 1);

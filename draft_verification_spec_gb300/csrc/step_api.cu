@@ -114,6 +114,14 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
 spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
                                    const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
                                    void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream) {
+  return spec_chunk_attention_tuned(q, q_token, q_head, dtype, q_heads, batch, max_q, scale, causal, window, out, out_lse,
+                                    workspace, ws_bytes, stream, nullptr);
+}
+
+spec_status_t spec_chunk_attention_tuned(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
+                                         const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
+                                         void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream,
+                                         const spec_tuning_t* tuning) {
   return guarded([&]() -> spec_status_t {
   const sv::ApiRange range("spec_chunk_attention");
   if (!attention_types(dtype) || q_heads < 1 || max_q < 0 || window < 0 || !std::isfinite(scale)) return SPEC_ERR_INVALID_ARG;
@@ -163,7 +171,8 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
   // one key tile is worth a CTA of its own.  A single token over 1024 keys, 8 key heads: 12.4 us; two tiles
   // 13.3, four 15.2 us.
   p.min_units = 1 + p.overhead;
-  p.wait_limit = kWaitNs;
+  const long long wait_us = tuning ? tuning->wait_limit_us : 0;
+  p.wait_limit = wait_us == 0 ? kWaitNs : wait_us < 0 ? 0 : wait_us < kWaitNs ? wait_us * 1000 : kWaitNs * 1000;
   p.n_max = plan.grid;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (sv::launch_attention(bf16, plan, p, maps, s) != cudaSuccess) return SPEC_ERR_CUDA;

@@ -120,13 +120,14 @@ _ws_bytes: dict = {}
 
 def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, *, causal: bool = True,
                     window: int = 0, scale: Optional[float] = None, want_lse: bool = False, out=None, stream=None,
-                    workspace=None):
+                    workspace=None, tuning=None):
     """Attention of the new tokens q [tokens, q_heads, dim] over the paged cache (spec_chunk_attention).
 
     ``max_q`` bounds the new tokens of a request.  ``causal``: a token sees the keys up to its own;
     otherwise all of its request.  ``window`` > 0: only keys within that many positions back, its
     own included.  ``scale`` defaults to dim ** -0.5.  Returns out [tokens, q_heads, dim], with
     ``want_lse`` (out, lse [tokens, q_heads] float32); a row that sees no key gives 0 and -inf.
+    ``tuning``: a Tuning, of which the wait limit counts here (spec_chunk_attention_tuned).
     """
     lib = _lib or _bind()
     dtype = q.dtype
@@ -151,9 +152,9 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
         need = _ws_bytes[key] = lib.spec_attention_workspace_bytes(code, hq, hkv, d, max_q)
     raw = _raw_stream(stream, index)
     buf = (workspace or _workspace(index, raw)).get_step(need, stream)
-    err = lib.spec_chunk_attention(q.data_ptr(), q_token, q_head, code, hq, c, max_q, d ** -0.5 if scale is None else scale,
-                                   causal, window, out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(),
-                                   buf.numel(), raw)
+    args = (q.data_ptr(), q_token, q_head, code, hq, c, max_q, d ** -0.5 if scale is None else scale, causal, window,
+            out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), raw)
+    err = lib.spec_chunk_attention(*args) if tuning is None else lib.spec_chunk_attention_tuned(*args, tuning.ref())
     if err:
         _check(err, "spec_chunk_attention")
     return (out, lse) if want_lse else out

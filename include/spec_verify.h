@@ -376,6 +376,17 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
                                    const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
                                    void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream);
 
+/*
+ * spec_chunk_attention with tuning->wait_limit_us (its meaning above; default
+ * 2 s) for the waits inside the kernel; the other knobs are the
+ * verification's and are not read.  tuning may be NULL.  After a wait that ran
+ * out the outputs are unspecified, and nothing else is written.
+ */
+spec_status_t spec_chunk_attention_tuned(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
+                                         const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
+                                         void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream,
+                                         const spec_tuning_t* tuning);
+
 /* New tokens of spec_rope_append; strides in elements, values of a head contiguous. */
 typedef struct spec_rope_tensors {
   const void* q;        /* [tokens, q_heads, dim] */

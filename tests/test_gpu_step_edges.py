@@ -1,0 +1,51 @@
+"""Edges of the step operators on the GPU: waits that run out, buffers and streams that are shared, windows, lengths
+and sizes at their limits."""
+import pytest
+import torch
+
+from tests import step_reference as R
+from tests.test_gpu_step_ops import _batch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module")
+def sv():
+    import draft_verification_spec_gb300 as m
+    m.lib()
+    return m
+
+
+def _guarded(shape, dtype, pad=4096):
+    """A tensor in the middle of a buffer of ones, and the buffer's two ends."""
+    n = 1
+    for s in shape:
+        n *= s
+    flat = torch.ones(n + 2 * pad, dtype=dtype, device="cuda")
+    return flat[pad:pad + n].view(shape), (flat[:pad], flat[pad + n:])
+
+
+@pytest.mark.parametrize("d,nq,hq", [(64, 17, 4), (128, 40, 16), (128, 4, 8)])
+def test_attention_wait_that_runs_out_writes_nothing(sv, d, nq, hq):
+    """Every bounded wait gives up at once: the status says so, and whatever records an earlier, larger call has left in
+    the workspace, the kernel that joins split rows writes no row of this one; the next call is right."""
+    dt, hkv = torch.bfloat16, 2
+    ws = sv.Workspace()
+    big = _batch([4 * nq] * 6, [3000] * 6, 16, hkv, d, dt, 3)
+    big_q = torch.randn(24 * nq, hq, d).to(dt).cuda()
+    sv.chunk_attention(big_q, *big, 4 * nq, workspace=ws)                # splits items: leaves records
+    kc, vc, table, lens, cu = _batch([nq], [700], 16, hkv, d, dt, 4)
+    q = torch.randn(nq, hq, d).to(dt).cuda()
+    want = sv.chunk_attention(q, kc, vc, table, lens, cu, nq, workspace=ws)
+    sv.chunk_attention(big_q, *big, 4 * nq, workspace=ws)
+    assert ws.status() == 0
+    out, ends = _guarded((nq, hq, d), dt)
+    got = sv.chunk_attention(q, kc, vc, table, lens, cu, nq, out=out, workspace=ws, tuning=sv.Tuning(wait_limit_us=-1))
+    waits = nq * hq // hkv > 16                                          # the kernel for few rows waits for nothing
+    assert ws.status() == (4 if waits else 0)
+    assert all((e == 1).all() for e in ends)
+    assert torch.equal(got, torch.ones_like(got) if waits else want)
+    sv.chunk_attention(q, kc, vc, table, lens, cu, nq, out=out, workspace=ws)
+    assert ws.status() == 0 and torch.equal(out, want)
+    sv.chunk_attention(q, kc, vc, table, lens, cu, nq, out=out, workspace=ws, tuning=sv.Tuning(wait_limit_us=10 ** 6))
+    assert ws.status() == 0 and torch.equal(out, want)
