@@ -169,8 +169,9 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
   const int rot_units = (p.Hq + Hk) * per_head;
   const int units = rot_units + (p.c.k ? Hk * (D / VEC) : 0);   // per token
   const int total = tokens * units;
-  // quotients of small numbers by the sizes above: floor(n ceil(2^32 / d) / 2^32) is exact while n d < 2^32
-  // (n < 2^16: at most 8 tokens of 2048 pieces; d < 2^16); sizes of 1 wrap to 0 and are handled apart
+  // quotients of small numbers by the sizes above: floor(n ceil(2^32 / d) / 2^32) is exact while n d < 2^32.
+  // d < 2^16 (the launch sees to it) and n < 2^16: several tokens have 2048 pieces together, one fewer than
+  // 2^16.  Sizes of 1 wrap to 0 and are handled apart.
   auto inverse = [](int d) { return d > 1 ? 0xffffffffu / static_cast<unsigned>(d) + 1u : 0u; };
   const unsigned inv_units = inverse(units), inv_head = inverse(per_head), inv_value = inverse(D / VEC);
   auto quotient = [](int n, unsigned inv) { return inv ? static_cast<int>(__umulhi(static_cast<unsigned>(n), inv)) : n; };
@@ -302,6 +303,9 @@ cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream) {
   bool whole = p.c.D % vec == 0 && p.rotary % (p.interleaved ? vec : 2 * vec) == 0;
   for (long long s : strides) whole = whole && s % vec == 0 && s >= 0 && s < (1ll << 31);
   whole = whole && p.c.k_head < (1ll << 31) && p.c.v_head < (1ll << 31);
+  // the piece kernel's 32-bit quotients (above) hold up to 65,535 pieces a token
+  const long long units = (p.Hq + 2ll * p.c.Hkv) * (p.c.D / vec);
+  whole = whole && units < (1 << 16);
   const void* bases[] = {p.q, p.k, p.c.k ? p.v : nullptr, p.q_out, p.k_out};
   for (const void* b : bases) whole = whole && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
   if (!whole) {
@@ -315,8 +319,7 @@ cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream) {
   // few tokens: a CTA each; many: as many tokens a CTA as make about 2048 pieces.  8192 tokens of 40 + 8 heads
   // of 128, bf16 (201 MB): 41 us with 128 threads and 2048 pieces (4.9 TB/s, 72 % of measured HBM), 43 with
   // 1024, 49 with 4096; 256 threads 45 us; four pieces in flight a thread instead of two 47 us.
-  const int units = (p.Hq + 2 * p.c.Hkv) * (p.c.D / vec);
-  int per = p.c.N <= 608 ? 1 : 2048 / (units > 0 ? units : 1);
+  int per = p.c.N <= 608 ? 1 : static_cast<int>(2048 / (units > 0 ? units : 1));
   per = per < 1 ? 1 : per > kRopeMaxTokens ? kRopeMaxTokens : per;
   const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);
   const size_t smem = sizeof(float2) * (p.rotary / 2) * per;

@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import step_reference as R
-from tests.test_gpu_step_ops import _batch
+from tests.test_gpu_step_ops import _batch, _rope
 
 pytestmark = pytest.mark.gpu
 
@@ -49,3 +49,9 @@ def test_attention_wait_that_runs_out_writes_nothing(sv, d, nq, hq):
     assert ws.status() == 0 and torch.equal(out, want)
     sv.chunk_attention(q, kc, vc, table, lens, cu, nq, out=out, workspace=ws, tuning=sv.Tuning(wait_limit_us=10 ** 6))
     assert ws.status() == 0 and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("hq,hkv,dtype", [(155, 50, "f32"), (156, 50, "f32"), (200, 50, "f32"), (500, 50, "bf16")])
+def test_rope_of_very_wide_tokens(sv, hq, hkv, dtype):
+    """Tokens of 65,280 to 76,800 16-byte pieces: on either side of what the piece kernel's quotients hold."""
+    _rope(sv, [2, 1], [2, 20], 16, hq, hkv, 1024, dtype=dtype, seed=hq)

@@ -1,0 +1,23 @@
+"""What the step operators launch, seen by a runtime that launches nothing (no device)."""
+from tests.fake_runtime import with_fake_runtime
+
+
+def test_rope_of_tokens_too_wide_for_the_quotients(tmp_path):
+    """rope_kernel divides a piece's number by the pieces of a token in 32 bits, which is exact up to 65,535 pieces; a wider
+    token takes the kernel without such quotients."""
+    for pieces in (65537, 76800):       # in integers: the last pieces of such a token would be taken for the next one's
+        inverse = 0xffffffff // pieces + 1
+        assert any((n * inverse >> 32) != 0 for n in (pieces - 1, pieces - 2))
+    assert all((n * (0xffffffff // d + 1) >> 32) == n // d for d in (2, 3, 4097, 65533, 65535) for n in range(d))
+    out = with_fake_runtime(tmp_path, """
+def kernel(q_heads, kv_heads, dim, dtype):
+    fake.fake_clear()
+    t = struct.pack("@PPPPPqqqqqqqqqq", 4096, 4096, 4096, 4096, 0, *([1 << 20, 1024] * 5))
+    b = batch(kv_heads=kv_heads, dim=dim, k_head=1024, v_head=1024, k_token=1 << 20, v_token=1 << 20, tokens=3)
+    assert lib.spec_rope_append(t, dtype, q_heads, b, 4096, dim, 1.0, 0, 4096, None) == 0
+    (name, grid, _, _), = launches()
+    return "scalar" if "rope_scalar_kernel" in name else "pieces"
+
+print(kernel(32, 8, 128, 1), kernel(155, 50, 1024, 0), kernel(156, 50, 1024, 0), kernel(200, 50, 1024, 0), kernel(500, 50, 1024, 1))
+""")
+    assert out.split() == ["pieces", "pieces", "scalar", "scalar", "scalar"]
