@@ -22,6 +22,7 @@ cache).
 from __future__ import annotations
 
 import ctypes
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -88,31 +89,50 @@ class Workspace:
 
     Zero-filled once when (re)allocated; the kernels keep it consistent.  One
     workspace per stream: calls that share one must be ordered on a stream.
+    A buffer that a larger call outgrows is kept: a captured graph may hold its
+    address.  (Each is at least twice the one before, so together they are
+    smaller than the last.)
     """
 
     def __init__(self, device=None):
         self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
         self.buf: Optional[torch.Tensor] = None
         self.step_buf: Optional[torch.Tensor] = None    # the step operators' status word and partial results
+        self._outgrown: list = []
+        self._growing = threading.Lock()
+
+    def _grow(self, old: Optional[torch.Tensor], need: int, clear: Optional[int], stream) -> torch.Tensor:
+        """A buffer of `need` bytes at least in place of `old`, its first `clear` bytes (None: all) zero-filled."""
+        size = max(need, 4096 if old is None else 2 * old.numel())
+        # torch's allocator returns 512-byte aligned blocks (>= the 256 the library requires)
+        buf = torch.empty(size, dtype=torch.uint8, device=self.device)
+        if stream is not None:
+            buf.record_stream(stream)
+        _check(lib().spec_workspace_init(_ptr(buf), size if clear is None else clear, _stream_ptr(stream)),
+               "spec_workspace_init")
+        if old is not None:
+            self._outgrown.append(old)
+        return buf
 
     def get_step(self, need: int, stream) -> torch.Tensor:
         """The buffer of the step operators (rope_append, chunk_attention), at least `need` bytes."""
-        if self.step_buf is None or self.step_buf.numel() < need:
-            buf = torch.empty(max(need, 4096), dtype=torch.uint8, device=self.device)
-            if stream is not None:
-                buf.record_stream(stream)
-            _check(lib().spec_workspace_init(_ptr(buf), 256, _stream_ptr(stream)), "spec_workspace_init")
-            self.step_buf = buf
-        return self.step_buf
+        buf = self.step_buf
+        if buf is None or buf.numel() < need:
+            with self._growing:
+                buf = self.step_buf
+                if buf is None or buf.numel() < need:
+                    buf = self.step_buf = self._grow(buf, need, 256, stream)
+        return buf
 
     def get(self, B: int, K: int, V: int, dtype_code: int, stream) -> torch.Tensor:
         need = int(lib().spec_workspace_bytes(B, K, V, dtype_code))
-        if self.buf is None or self.buf.numel() < need:
-            # torch's allocator returns 512-byte aligned blocks (>= the 256 the library requires)
-            self.buf = torch.empty(max(need, 4096), dtype=torch.uint8, device=self.device)
-            _check(lib().spec_workspace_init(_ptr(self.buf), self.buf.numel(), _stream_ptr(stream)),
-                   "spec_workspace_init")
-        return self.buf
+        buf = self.buf
+        if buf is None or buf.numel() < need:
+            with self._growing:
+                buf = self.buf
+                if buf is None or buf.numel() < need:
+                    buf = self.buf = self._grow(buf, need, None, stream)
+        return buf
 
     def status(self, stream=None) -> int:
         """Read and clear the device status words (synchronises the stream)."""

@@ -55,3 +55,29 @@ def test_attention_wait_that_runs_out_writes_nothing(sv, d, nq, hq):
 def test_rope_of_very_wide_tokens(sv, hq, hkv, dtype):
     """Tokens of 65,280 to 76,800 16-byte pieces: on either side of what the piece kernel's quotients hold."""
     _rope(sv, [2, 1], [2, 20], 16, hq, hkv, 1024, dtype=dtype, seed=hq)
+
+
+def test_graph_of_a_workspace_that_grew_later(sv):
+    """A graph captured with a workspace for single tokens; a prompt over the same workspace needs a larger buffer; the
+    graph's replays write neither over memory that others have got since, nor wrong rows."""
+    dt, hq, hkv, d = torch.bfloat16, 8, 2, 128
+    ws = sv.Workspace()
+    kc, vc, table, lens, cu = _batch([1], [2000], 16, hkv, d, dt, 4)
+    q = torch.randn(1, hq, d).to(dt).cuda()
+    want = sv.chunk_attention(q, kc, vc, table, lens, cu, 1)
+    out = torch.empty_like(want)
+    sv.chunk_attention(q, kc, vc, table, lens, cu, 1, out=out, workspace=ws)
+    size = ws.step_buf.numel()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        sv.chunk_attention(q, kc, vc, table, lens, cu, 1, out=out, workspace=ws)
+    big = _batch([200], [300], 16, hkv, d, dt, 5)
+    sv.chunk_attention(torch.randn(200, hq, d).to(dt).cuda(), *big, 200, workspace=ws)
+    assert ws.step_buf.numel() > size
+    others = [torch.zeros(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    out.zero_()
+    for _ in range(3):
+        g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out, want) and not any(o.any() for o in others)
+    assert ws.status() == 0
