@@ -111,7 +111,7 @@ class Workspace:
         _check(lib().spec_workspace_init(_ptr(buf), size if clear is None else clear, _stream_ptr(stream)),
                "spec_workspace_init")
         if old is not None:
-            self._outgrown.append(old)
+            self._outgrown.append((old, clear))
         return buf
 
     def get_step(self, need: int, stream) -> torch.Tensor:
@@ -135,22 +135,25 @@ class Workspace:
         return buf
 
     def status(self, stream=None) -> int:
-        """Read and clear the device status words (synchronises the stream)."""
-        found = 0
-        for buf in (self.buf, self.step_buf):
+        """Read and clear the device status words, outgrown buffers' too (synchronises the stream).
+
+        The gravest report: a timeout, then a token range, then a page range (their codes rise in that order).
+        """
+        found = []
+        for buf in [self.buf, self.step_buf] + [b for b, _ in self._outgrown]:
             if buf is None:
                 continue
             out = ctypes.c_int32(0)
             _check(lib().spec_get_status(_ptr(buf), _stream_ptr(stream), ctypes.byref(out)), "spec_get_status")
-            found = found or out.value
-        return found
+            if out.value:
+                found.append(out.value)
+        return min(found, default=0)
 
     def reset(self, stream=None):
-        if self.buf is not None:
-            _check(lib().spec_workspace_init(_ptr(self.buf), self.buf.numel(), _stream_ptr(stream)),
-                   "spec_workspace_init")
-        if self.step_buf is not None:
-            _check(lib().spec_workspace_init(_ptr(self.step_buf), 256, _stream_ptr(stream)), "spec_workspace_init")
+        for buf, clear in [(self.buf, None), (self.step_buf, 256)] + self._outgrown:
+            if buf is not None:
+                _check(lib().spec_workspace_init(_ptr(buf), buf.numel() if clear is None else clear,
+                                                 _stream_ptr(stream)), "spec_workspace_init")
 
 
 _workspaces: dict = {}

@@ -81,3 +81,15 @@ def test_graph_of_a_workspace_that_grew_later(sv):
     torch.cuda.synchronize()
     assert torch.equal(out, want) and not any(o.any() for o in others)
     assert ws.status() == 0
+
+
+def test_status_survives_a_larger_call(sv):
+    """rope_append reports a page; an attention over the same workspace needs a larger buffer before anybody looks."""
+    dt = torch.bfloat16
+    ws = sv.Workspace()
+    kc, vc, table, lens, cu = _batch([2], [40], 16, 2, 64, dt, 4)
+    q, k = torch.randn(2, 4, 64).to(dt).cuda(), torch.randn(2, 2, 64).to(dt).cuda()
+    bad = torch.full_like(table, -1)
+    sv.rope_append(q, k, k, sv.RopePlan(64), kc, vc, bad, lens, cu, workspace=ws)
+    sv.chunk_attention(q, kc, vc, table, lens, cu, 2, workspace=ws)
+    assert ws.status() == 7 and ws.status() == 0

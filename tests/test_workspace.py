@@ -48,7 +48,7 @@ def test_outgrown_buffers_stay_alive(ws):
             assert get(n).numel() >= n and get(1).data_ptr() == get(n).data_ptr()
         assert alive() is not None and alive().data_ptr() == address
     # and they are few and small: together less than the two that are in use
-    kept = [b for b in ws._outgrown]
+    kept = [b for b, _ in ws._outgrown]
     assert len(kept) <= 12 and sum(b.numel() for b in kept) < ws.buf.numel() + ws.step_buf.numel()
 
 
@@ -60,3 +60,27 @@ def test_threads_that_grow_a_workspace_get_one_buffer(ws, monkeypatch):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert len(set(got)) == 1 and not ws._outgrown
+
+
+def test_status_of_an_outgrown_buffer_is_not_lost(ws):
+    _report(ws.get_step(256, None), 7)            # a small call reports a page
+    ws.get_step(1 << 20, None)                    # a larger one follows before anybody looks
+    assert ws.status() == 7 and ws.status() == 0
+    _report(ws.get(1, 3, 100, 0, None), 5)
+    ws.get(1000, 3, 100, 0, None)
+    assert ws.status() == 5 and ws.status() == 0
+
+
+def test_status_names_the_gravest_report(ws):
+    """Timeout before token range before page range, whichever operator's buffer holds it."""
+    for first, second, want in ((5, 7, 5), (5, 4, 4), (4, 7, 4), (0, 7, 7), (0, 4, 4)):
+        _report(ws.get(1, 3, 100, 0, None), first)
+        _report(ws.get_step(256, None), second)
+        assert ws.status() == want and ws.status() == 0
+
+
+def test_reset_clears_outgrown_buffers_too(ws):
+    _report(ws.get_step(256, None), 4)
+    _report(ws.get_step(1 << 20, None), 7)
+    ws.reset()
+    assert ws.status() == 0
