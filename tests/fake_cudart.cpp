@@ -1,5 +1,6 @@
 // A stand-in for the CUDA runtime that launches nothing: the host code of libspecverify.so runs against it on a machine
 // without a device, and every launch is written down (kernel name, grid, block, thread that made it).
+#include <chrono>
 #include <cstddef>
 #include <cstdio>
 #include <cstring>
@@ -34,17 +35,20 @@ std::vector<Launch>& launches() {
   return v;
 }
 int delay_ms = 0;
+thread_local bool bound = false;   // a context is current on this thread
 thread_local Config pushed;
 
 int launch(const void* fn, Dim grid, Dim block) {
   {
     std::lock_guard<std::mutex> lk(mu);
+    bound = true;
     launches().push_back({names()[fn], grid, block, std::hash<std::thread::id>()(std::this_thread::get_id())});
   }
   if (delay_ms) std::this_thread::sleep_for(std::chrono::milliseconds(delay_ms));
   return 0;
 }
-int encode(...) { return 0; }   // cuTensorMapEncodeTiled: every cache can be described
+// cuTensorMapEncodeTiled: every cache can be described, by a thread that has a context (else CUDA_ERROR_INVALID_CONTEXT)
+int encode(...) { return bound ? 0 : 201; }
 }  // namespace
 
 extern "C" {
@@ -127,6 +131,10 @@ int cudaOccupancyMaxActiveBlocksPerMultiprocessorWithFlags(int* n, const void*, 
 }
 int cudaOccupancyMaxActiveClusters(int* n, const void*, const void*) {
   *n = 8;
+  return 0;
+}
+int cudaSetDevice(int) {
+  bound = true;
   return 0;
 }
 int cudaStreamSynchronize(void*) { return 0; }

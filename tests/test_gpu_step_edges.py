@@ -93,3 +93,19 @@ def test_status_survives_a_larger_call(sv):
     sv.rope_append(q, k, k, sv.RopePlan(64), kc, vc, bad, lens, cu, workspace=ws)
     sv.chunk_attention(q, kc, vc, table, lens, cu, 2, workspace=ws)
     assert ws.status() == 7 and ws.status() == 0
+
+
+def test_attention_first_call_of_a_thread(sv):
+    """A thread's first call runs the same kernel as every other: equal bit for bit."""
+    import threading
+    dt, nq = torch.bfloat16, 20
+    c = _batch([nq] * 2, [1500, 750], 16, 2, 128, dt, 2)
+    q = torch.randn(2 * nq, 8, 128).to(dt).cuda()
+    want = sv.chunk_attention(q, *c, nq)
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(3):
+        t = threading.Thread(target=lambda: got.append(sv.chunk_attention(q, *c, nq)))
+        t.start()
+        t.join()
+    assert all(torch.equal(g, want) for g in got) and len(got) == 3

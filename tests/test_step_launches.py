@@ -21,3 +21,25 @@ def kernel(q_heads, kv_heads, dim, dtype):
 print(kernel(32, 8, 128, 1), kernel(155, 50, 1024, 0), kernel(156, 50, 1024, 0), kernel(200, 50, 1024, 0), kernel(500, 50, 1024, 1))
 """)
     assert out.split() == ["pieces", "pieces", "scalar", "scalar", "scalar"]
+
+
+def test_attention_on_a_thread_without_a_context(tmp_path):
+    """A thread's first call into CUDA has no current context yet, without which TMA descriptors cannot be made: it gets one,
+    and the kernel that every other call of these sizes runs."""
+    out = with_fake_runtime(tmp_path, """
+import threading
+
+def call():
+    b = batch(tokens=20)
+    assert lib.spec_chunk_attention(4096, 256, 64, 1, 4, b, 20, 0.1, 1, 0, 4096, None, 4096, 1 << 30, None) == 0
+
+def twice():
+    call()
+    call()
+
+t = threading.Thread(target=twice)
+t.start()
+t.join()
+print(*["tc" if "attn_tc_kernel" in l[0] else "mma" for l in launches()[::2]])
+""")
+    assert out.split() == ["tc", "tc"]
