@@ -175,6 +175,9 @@ spec_status_t spec_chunk_attention_tuned(const void* q, long long q_token, long 
   p.wait_limit = wait_us == 0 ? kWaitNs : wait_us < 0 ? 0 : wait_us < kWaitNs ? wait_us * 1000 : kWaitNs * 1000;
   p.n_max = plan.grid;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
+  // The two kernels talk through the workspace: another thread's call with the same one must not come between.
+  static std::mutex pair;
+  std::lock_guard<std::mutex> lk(pair);
   if (sv::launch_attention(bf16, plan, p, maps, s) != cudaSuccess) return SPEC_ERR_CUDA;
   return sv::launch_attention_combine(bf16, plan, p, s) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
   }, SPEC_ERR_CUDA);

@@ -368,7 +368,7 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
  * dim a multiple of 8, at most 256; q_heads a multiple of kv_heads.
  * Rows of tokens that no request has stay unwritten.  Results do not depend
  * on timing.  Two launches, the second chained by programmatic dependent
- * launch.  Waits inside the kernel are bounded (2 s); one that runs out sets
+ * launch; threads may share a workspace whose calls go to one stream.  Waits inside the kernel are bounded (2 s); one that runs out sets
  * SPEC_ERR_DEVICE_TIMEOUT in the status word, and the outputs are then
  * unspecified.
  */

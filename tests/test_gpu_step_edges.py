@@ -109,3 +109,26 @@ def test_attention_first_call_of_a_thread(sv):
         t.start()
         t.join()
     assert all(torch.equal(g, want) for g in got) and len(got) == 3
+
+
+def test_attention_from_threads_on_one_stream(sv):
+    """Threads that share the default workspace of a stream: calls of different sizes, every one right."""
+    import threading
+    dt, hq, hkv, d = torch.bfloat16, 8, 2, 128
+    cases = []
+    for i, (nq, kv) in enumerate(((1, 3000), (3, 900), (20, 1500))):
+        c = _batch([nq] * 2, [kv, kv // 2], 16, hkv, d, dt, i)
+        q = torch.randn(2 * nq, hq, d).to(dt).cuda()
+        cases.append((q, c, nq, sv.chunk_attention(q, *c, nq)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(q, c, nq, want):
+        for _ in range(200):
+            if not torch.equal(sv.chunk_attention(q, *c, nq), want):
+                bad.append(nq)
+
+    threads = [threading.Thread(target=work, args=a) for a in cases]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not bad and sv.default_workspace().status() == 0

@@ -43,3 +43,27 @@ t.join()
 print(*["tc" if "attn_tc_kernel" in l[0] else "mma" for l in launches()[::2]])
 """)
     assert out.split() == ["tc", "tc"]
+
+
+def test_attention_launches_its_two_kernels_together(tmp_path):
+    """Two threads on one stream and workspace: no call's kernel comes between another's pair, which talk through it."""
+    out = with_fake_runtime(tmp_path, """
+import threading
+fake.fake_delay(30)
+b = batch(tokens=4)
+
+def call(max_q):
+    assert lib.spec_chunk_attention(4096, 256, 64, 1, 4, b, max_q, 0.1, 1, 0, 4096, None, 4096, 1 << 30, None) == 0
+
+call(4)
+fake.fake_clear()
+threads = [threading.Thread(target=lambda n=n: [call(n) for _ in range(4)]) for n in (4, 5, 40)]
+[t.start() for t in threads]
+[t.join() for t in threads]
+done = launches()
+assert len(done) == 24
+for a, c in zip(done[::2], done[1::2]):
+    assert "combine" not in a[0] and "combine" in c[0] and a[3] == c[3], done
+print("pairs")
+""")
+    assert out.split() == ["pairs"]
