@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
     // page id of this thread's key of tile j (-1: nothing to read)
     auto page_of = [&](int j) -> int {
       const int key = (kt0 + j) * BN + (tid & (BN - 1));
-      if (j >= len || key >= hi) return -1;
+      if (j >= len || key < lo || key >= hi) return -1;   // also of the first tile what lies before the window
       const int pg = __ldg(table + key / P);
       if (pg < 0 || pg >= p.c.pages) {
         atomicOr(p.status, kStatusPageRange);

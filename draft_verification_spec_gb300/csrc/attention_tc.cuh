@@ -19,8 +19,8 @@
 // by the sum undoes.  S(j) is committed after the same half's previous P V in issue order, so a softmax
 // thread that has seen S(j) may touch O.
 //
-// Keys at or beyond the item's last one: pages that lie wholly there are read at an out-of-range page
-// coordinate, which TMA fills with zeros; the rest of the last page can hold anything, so its value
+// Keys before the item's first one or at or beyond its last one: pages that lie wholly there are read at an
+// out-of-range page coordinate, which TMA fills with zeros; the rest of the last page can hold anything, so its value
 // rows are zeroed in shared memory before the MMA reads them (0 x NaN would be NaN); scores are
 // selected, not multiplied.
 //
@@ -275,8 +275,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int j = 0; ok && j < len; ++j, ++g) {
         // this lane's boxes: page `i` of the tile (i = lane: at most 16 pages of 8 tokens and more)
         const int key = (kt0 + j) * BN + lane * rows;
-        int pg = p.c.pages;   // out of range: zeros
-        if (lane < boxes && key < hi) {
+        int pg = p.c.pages;   // out of range: zeros.  So too what lies wholly before the window: its page may be gone
+        if (lane < boxes && key < hi && key + rows > lo) {
           pg = __ldg(table + key / P);
           if (pg < 0 || pg >= p.c.pages) {
             atomicOr(p.status, kStatusPageRange);

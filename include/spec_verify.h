@@ -358,7 +358,9 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
  * over the keys t < kv_lens[b] with, for causal != 0, t <= position of n and,
  * for window > 0, t > position of n - window.  A row that sees no key gives
  * out = 0, lse = -inf.  Keys and values at or beyond kv_lens[b] are never
- * used (they may be anything); those before it must be finite.
+ * used (they may be anything); those before it must be finite, except in
+ * pages that lie wholly behind the window of all the request's new tokens:
+ * those are not looked at, nor are their ids.
  *   q         [tokens, q_heads, dim] with strides (multiples of 16 bytes)
  *   dtype     SPEC_BF16 or SPEC_F16, of q, k, v and out
  *   max_q     an upper bound of the new tokens per request (chooses the

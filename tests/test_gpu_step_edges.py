@@ -132,3 +132,31 @@ def test_attention_from_threads_on_one_stream(sv):
     [t.start() for t in threads]
     [t.join() for t in threads]
     assert not bad and sv.default_workspace().status() == 0
+
+
+@pytest.mark.parametrize("page", [8, 16, 24, 128])
+@pytest.mark.parametrize("nq,hq,d", [(1, 8, 128), (4, 4, 64), (40, 8, 256), (17, 8, 128), (150, 8, 64), (300, 4, 128)])
+def test_attention_window_ignores_pages_behind_it(sv, nq, hq, d, page):
+    """A cache that has given up the pages behind the window: no entry in the table, or another request's page with
+    anything in it.  Nothing is reported and the rows are those of the whole cache."""
+    dt, hkv, window = torch.bfloat16, 2, 100
+    kv = [nq + 310, nq + 700, nq + 20]
+    kc, vc, table, lens, cu = _batch([nq] * 3, kv, page, hkv, d, dt, page + nq)
+    q = torch.randn(3 * nq, hq, d).to(dt).cuda()
+    want, want_lse = sv.chunk_attention(q, kc, vc, table, lens, cu, nq, window=window, want_lse=True)
+    if page == 16:
+        ro, rl, size, spread = R.attention(q, kc, vc, table, lens, cu, True, window, d ** -0.5)
+        bo, bl = R.attention_bounds(dt, size, spread, d)
+        assert ((want.cpu().double() - ro).abs() <= bo).all()
+    junk = kc.shape[0]     # one page more, of NaN
+    kc, vc = (torch.cat([c, torch.full_like(c[:1], float("nan"))]) for c in (kc, vc))
+    for stale in (-1, junk):
+        t = table.clone()
+        for b, n in enumerate(kv):
+            t[b, : max(0, n - nq - window + 1) // page] = stale    # pages that end at or before the first visible key
+        for causal in (True, False):
+            full = want if causal else sv.chunk_attention(q, kc, vc, table, lens, cu, nq, window=window, causal=False)
+            got, lse = sv.chunk_attention(q, kc, vc, t, lens, cu, nq, window=window, causal=causal, want_lse=True)
+            assert sv.default_workspace().status() == 0
+            assert torch.equal(got, full)
+            assert not causal or torch.equal(lse, want_lse)
