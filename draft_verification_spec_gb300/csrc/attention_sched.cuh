@@ -38,7 +38,11 @@ __device__ __forceinline__ int attn_token(const AttnParams& p, int r) {
 __device__ __forceinline__ void attn_keys(const AttnParams& p, const AttnReq& r, int r0, int r1, int* lo, int* hi) {
   const int at = r.kv - r.nq;
   *hi = p.causal ? max(min(at + attn_token(p, r1 - 1) + 1, r.kv), 0) : r.kv;
-  *lo = p.window > 0 ? max(at + attn_token(p, r0) - p.window + 1, 0) : 0;
+  *lo = 0;
+  if (p.window > 0) {   // in 64 bits: a position below 0 less a window of 2^31 - 1 does not fit 32
+    const long long w = static_cast<long long>(at) + attn_token(p, r0) + 1 - p.window;
+    *lo = w > 0 ? static_cast<int>(w) : 0;
+  }
 }
 // First key tile and number of key tiles of row tile t (an item has one at least: its rows are
 // written even where they see no key).

@@ -125,8 +125,9 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
 
     ``max_q`` bounds the new tokens of a request.  ``causal``: a token sees the keys up to its own;
     otherwise all of its request.  ``window`` > 0: only keys within that many positions back, its
-    own included (pages wholly behind it may be gone).  ``scale`` defaults to dim ** -0.5.  Returns out [tokens, q_heads, dim], with
-    ``want_lse`` (out, lse [tokens, q_heads] float32); a row that sees no key gives 0 and -inf.
+    own included (pages wholly behind it may be gone).  ``scale`` defaults to dim ** -0.5.  Returns
+    out [tokens, q_heads, dim], with ``want_lse`` (out, lse [tokens, q_heads] float32); a row that
+    sees no key gives 0 and -inf.
     ``tuning``: a Tuning, of which the wait limit counts here (spec_chunk_attention_tuned).
     """
     lib = _lib or _bind()

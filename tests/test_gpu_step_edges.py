@@ -160,3 +160,17 @@ def test_attention_window_ignores_pages_behind_it(sv, nq, hq, d, page):
             assert sv.default_workspace().status() == 0
             assert torch.equal(got, full)
             assert not causal or torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 8, 2 ** 30])
+@pytest.mark.parametrize("hq,d", [(2, 64), (8, 64), (16, 128), (8, 256)])
+def test_attention_window_as_wide_as_its_type(sv, hq, d, window):
+    """Such a window hides nothing, whatever the position, that of tokens before the request's first one included."""
+    dt, hkv, new, kv = torch.bfloat16, 2, [17, 40, 17, 1, 3], [9, 33, 300, 0, 3]
+    kc, vc, table, lens, cu = _batch(new, kv, 16, hkv, d, dt, hq)
+    q = torch.randn(sum(new), hq, d).to(dt).cuda()
+    for causal in (True, False):
+        want = sv.chunk_attention(q, kc, vc, table, lens, cu, 40, causal=causal, want_lse=True)
+        got = sv.chunk_attention(q, kc, vc, table, lens, cu, 40, causal=causal, window=window, want_lse=True)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert sv.default_workspace().status() == 0
