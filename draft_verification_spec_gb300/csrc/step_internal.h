@@ -51,7 +51,7 @@ struct AttnParams {
   int overhead;              // an item's cost beside its key tiles, in key tiles
   int min_units;             // fewest units worth a CTA of their own
   int n_max;                 // CTAs launched
-  long long wait_limit;      // ns per bounded wait (tcgen05 kernel); 0: every wait gives up at once
+  long long wait_limit;      // ns per bounded wait (tcgen05 kernel); 0: the first one gives up at once
   int32_t* status;
 };
 

@@ -379,9 +379,10 @@ spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q
                                    void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream);
 
 /*
- * spec_chunk_attention with tuning->wait_limit_us (its meaning above; default
- * 2 s) for the waits inside the kernel; the other knobs are the
- * verification's and are not read.  tuning may be NULL.  After a wait that ran
+ * spec_chunk_attention with tuning->wait_limit_us for the waits inside the
+ * kernel (0: 2 s; < 0: the first wait gives up at once, and those that wait
+ * for what it would have brought); the other knobs are the verification's and
+ * are not read.  tuning may be NULL.  After a wait that ran
  * out the outputs are unspecified, and nothing else is written.
  */
 spec_status_t spec_chunk_attention_tuned(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
