@@ -17,15 +17,22 @@
 namespace sv {
 
 struct AttnReq {
-  int q0, nq, kv;
+  int q0, nq;
+  int kv;   // keys that the table holds
+  int at;   // position of the first new token: counted from the request's length, whatever the table holds
 };
+// Keys of a request that its row of the table can hold (and that tile arithmetic in 32 bits can).
+__device__ __forceinline__ int attn_capacity(const PagedBatch& c) {
+  const long long cap = static_cast<long long>(c.table_width) * c.page_size;
+  return cap < 0x7fffff00ll ? static_cast<int>(cap) : 0x7fffff00;
+}
 __device__ __forceinline__ AttnReq attn_request(const PagedBatch& c, int b) {
   AttnReq r;
-  const long long cap = static_cast<long long>(c.table_width) * c.page_size;
   r.q0 = min(max(__ldg(c.cu_q + b), 0), c.N);
   r.nq = max(min(__ldg(c.cu_q + b + 1), c.N) - r.q0, 0);
   const int kv = max(__ldg(c.kv_lens + b), 0);
-  r.kv = kv > cap ? static_cast<int>(cap) : kv;
+  r.kv = min(kv, attn_capacity(c));
+  r.at = kv - r.nq;
   return r;
 }
 
@@ -36,12 +43,11 @@ __device__ __forceinline__ int attn_token(const AttnParams& p, int r) {
 
 // Keys [lo, hi) that rows [r0, r1) of the request can see.
 __device__ __forceinline__ void attn_keys(const AttnParams& p, const AttnReq& r, int r0, int r1, int* lo, int* hi) {
-  const int at = r.kv - r.nq;
-  *hi = p.causal ? max(min(at + attn_token(p, r1 - 1) + 1, r.kv), 0) : r.kv;
+  *hi = p.causal ? max(min(r.at + attn_token(p, r1 - 1) + 1, r.kv), 0) : r.kv;
   *lo = 0;
   if (p.window > 0) {   // in 64 bits: a position below 0 less a window of 2^31 - 1 does not fit 32
-    const long long w = static_cast<long long>(at) + attn_token(p, r0) + 1 - p.window;
-    *lo = w > 0 ? static_cast<int>(w) : 0;
+    const long long w = static_cast<long long>(r.at) + attn_token(p, r0) + 1 - p.window;
+    *lo = w > 0 ? static_cast<int>(min(w, static_cast<long long>(r.kv))) : 0;
   }
 }
 // First key tile and number of key tiles of row tile t (an item has one at least: its rows are
@@ -64,6 +70,7 @@ __device__ __forceinline__ long long attn_request_units(const AttnParams& p, int
   long long n = 0;
   if (b < p.c.B) {
     const AttnReq r = attn_request(p.c, b);
+    if (r.nq > 0 && r.at + r.nq > r.kv && blockIdx.x == 0) atomicOr(p.status, kStatusPageRange);   // positions beyond the table
     const int nt = attn_row_tiles(p, r, bm);
     for (int t = threadIdx.x & (p.lanes - 1); t < nt; t += p.lanes) {
       int first;

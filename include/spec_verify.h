@@ -324,10 +324,12 @@ spec_status_t spec_verify_tuned(const void* target_logits, const void* draft_log
  * are described by their strides).  Lengths are read on the device only.
  * kv_lens[b] counts the new tokens; 0 (an idle slot) and less than the
  * number of new tokens are allowed: the tokens before position 0 see
- * nothing and are not stored.  Lengths beyond table_width * page_size are
- * cut to it.  Page ids are looked at only where a token is read or written;
- * one outside [0, pages) reads as zeros, is not written, and sets
- * SPEC_ERR_PAGE_RANGE in the status word.
+ * nothing and are not stored.  Positions are counted from kv_lens[b] also
+ * where it is beyond table_width * page_size: the tokens that the table has no
+ * page for are neither stored nor seen, and SPEC_ERR_PAGE_RANGE is set.  Page
+ * ids are looked at only where a token is read or written; one outside
+ * [0, pages) reads as zeros, is not written, and sets SPEC_ERR_PAGE_RANGE in
+ * the status word.
  */
 typedef struct spec_paged_batch {
   void* k;

@@ -174,3 +174,37 @@ def test_attention_window_as_wide_as_its_type(sv, hq, d, window):
         got = sv.chunk_attention(q, kc, vc, table, lens, cu, 40, causal=causal, window=window, want_lse=True)
         assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
     assert sv.default_workspace().status() == 0
+
+
+@pytest.mark.parametrize("window", [0, 20, 5])
+@pytest.mark.parametrize("nq,hq,d", [(1, 4, 64), (20, 4, 64), (20, 8, 256), (150, 4, 128)])
+def test_attention_length_beyond_the_table(sv, nq, hq, d, window):
+    """More tokens than the table has pages for: reported, and the rows' positions stay what rope_append makes of them;
+    they see the keys that the table holds."""
+    dt, page, cols, hkv = torch.bfloat16, 16, 13, 2
+    cap, kv = page * cols, [page * cols + 4, page * cols - 3, page * cols + 60]
+    kc, vc, table, lens, cu = _batch([nq] * 3, [min(k, cap) for k in kv], page, hkv, d, dt, nq)
+    q = torch.randn(3 * nq, hq, d).to(dt).cuda()
+    out, lse = sv.chunk_attention(q, kc, vc, table[:, :cols], torch.tensor(kv, dtype=torch.int32, device="cuda"), cu, nq,
+                                  window=window, want_lse=True)
+    assert sv.default_workspace().status() == 7 and sv.default_workspace().status() == 0
+    kd, vd, qd = kc.double().cpu(), vc.double().cpu(), q.double().cpu()
+    ids = table.cpu().long()
+    for b, n in enumerate(kv):
+        K, V = (c[ids[b, :cols]].flatten(0, 1)[:n] for c in (kd, vd))
+        for i in range(nq):
+            pos = n - nq + i
+            see = slice(max(0, pos - window + 1) if window else 0, max(0, min(cap, pos + 1)))
+            for h in range(hq):
+                row, g = b * nq + i, h // (hq // hkv)
+                k, v = K[see, g], V[see, g]
+                if len(k) == 0:
+                    assert float(lse[row, h]) == float("-inf") and not out[row, h].any()
+                    continue
+                x = k @ qd[row, h] * d ** -0.5
+                w = torch.softmax(x, 0)
+                spread = (k.abs() @ qd[row, h].abs() * d ** -0.5).max()
+                bo, bl = R.attention_bounds(dt, w @ v.abs(), spread, d)
+                assert ((out[row, h].double().cpu() - w @ v).abs() <= bo).all()
+                want = float(torch.logsumexp(x, 0))
+                assert abs(float(lse[row, h]) - want) <= float(bl) + abs(want) * 2.0 ** -23
