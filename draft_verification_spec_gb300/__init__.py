@@ -105,9 +105,8 @@ class Workspace:
         """A buffer of `need` bytes at least in place of `old`, its first `clear` bytes (None: all) zero-filled."""
         size = max(need, 4096 if old is None else 2 * old.numel())
         # torch's allocator returns 512-byte aligned blocks (>= the 256 the library requires)
-        buf = torch.empty(size, dtype=torch.uint8, device=self.device)
-        if stream is not None:
-            buf.record_stream(stream)
+        with torch.cuda.stream(stream):   # the memory of the stream that clears and uses it (None: the current one)
+            buf = torch.empty(size, dtype=torch.uint8, device=self.device)
         _check(lib().spec_workspace_init(_ptr(buf), size if clear is None else clear, _stream_ptr(stream)),
                "spec_workspace_init")
         if old is not None:

@@ -8,9 +8,10 @@
 
 A batch is packed: tokens ``cu_q[b]:cu_q[b+1]`` are the new ones of request b, the last of its
 ``kv_lens[b]`` tokens; its token t is slot ``t % page_size`` of page ``page_table[b, t // page_size]``
-of caches [pages, page_size, kv_heads, dim].  Lengths stay on the device.  As in the rest of the
-package, this file checks arguments, allocates outputs and passes pointers; the contracts are in
-include/spec_verify.h.
+of caches [pages, page_size, kv_heads, dim].  Lengths stay on the device.  With ``stream=`` a call runs
+on that stream: it waits for nothing on the current one (the caller orders the two), and its tensors'
+memory is kept until it is done.  As in the rest of the package, this file checks arguments, allocates
+outputs and passes pointers; the contracts are in include/spec_verify.h.
 """
 from __future__ import annotations
 
@@ -58,10 +59,22 @@ def _where(t, name, index):
 
 
 def _fresh(stream, shape, dtype, device):
-    t = torch.empty(shape, dtype=dtype, device=device)
-    if stream is not None:
-        t.record_stream(stream)
+    """An output.  With a stream it is that stream's memory, for the current stream to read: the current stream's free memory
+    may still be read by work that is queued there, which the kernel on `stream` would not wait for."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    here = torch.cuda.current_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(here)
     return t
+
+
+def _used_on(stream, *tensors):
+    """Memory of the caller's tensors is not handed out again before the work queued on `stream` is done with it."""
+    for t in tensors:
+        if isinstance(t, torch.Tensor):
+            t.record_stream(stream)
 
 
 def _heads(t, name, index, n=None, dim=None):
@@ -155,6 +168,8 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     buf = (workspace or _workspace(index, raw)).get_step(need, stream)
     args = (q.data_ptr(), q_token, q_head, code, hq, c, max_q, d ** -0.5 if scale is None else scale, causal, window,
             out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), raw)
+    if stream is not None:
+        _used_on(stream, q, k_cache, v_cache, page_table, kv_lens, cu_q, out)
     err = lib.spec_chunk_attention(*args) if tuning is None else lib.spec_chunk_attention_tuned(*args, tuning.ref())
     if err:
         _check(err, "spec_chunk_attention")
@@ -275,6 +290,8 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
             raise ValueError("k_out must have k's shape and dtype")
         op = k_out.data_ptr()
     r = _ROPE.pack(q.data_ptr(), k.data_ptr(), vp, q_out.data_ptr(), op, q0, q1, k0, k1, v0, v1, w0, w1, o0, o1)
+    if stream is not None:
+        _used_on(stream, q, k, v, rope.turns, k_cache, v_cache, page_table, kv_lens, cu_q, q_out, k_out)
     err = lib.spec_rope_append(r, code, hq, c, rope.turns.data_ptr(), rope.rotary_dim, rope.factor, rope.interleaved, ws, raw)
     if err:
         _check(err, "spec_rope_append")
@@ -343,6 +360,8 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
                               (V > 1 and f.stride(1) != 1) or (R > 1 and f.stride(0) < V)):
             raise ValueError("out.filtered must have the shape, dtype and device of logits and contiguous rows")
     f = out.filtered
+    if stream is not None:
+        _used_on(stream, logits, uniforms, temperature, top_k, top_p, min_p, out.tokens, out.probs, out.kept, f)
     err = lib.spec_sample_tokens(logits.data_ptr(), row if row > V else V, code, R, V, uniforms.data_ptr(), c,
                                  out.tokens.data_ptr(), out.probs.data_ptr(), out.kept.data_ptr(),
                                  None if f is None else f.data_ptr(), V if f is None else max(f.stride(0), V),

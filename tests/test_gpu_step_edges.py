@@ -208,3 +208,54 @@ def test_attention_length_beyond_the_table(sv, nq, hq, d, window):
                 assert ((out[row, h].double().cpu() - w @ v).abs() <= bo).all()
                 want = float(torch.logsumexp(x, 0))
                 assert abs(float(lse[row, h]) - want) <= float(bl) + abs(want) * 2.0 ** -23
+
+
+def test_calls_on_another_stream_leave_queued_work_alone(sv):
+    """The current stream's free memory may still be read by work that is queued there: a call on another stream must not
+    get it for its outputs or its workspace, and its own tensors' memory must last until it is done."""
+    dt, nq, hq, hkv, d = torch.bfloat16, 20, 8, 2, 128
+    c = _batch([nq] * 2, [1500, 750], 16, hkv, d, dt, 2)
+    q = torch.randn(2 * nq, hq, d).to(dt).cuda()
+    k = torch.randn(2 * nq, hkv, d).to(dt).cuda()
+    logits, u = torch.randn(8, 4096, device="cuda"), torch.rand(8, device="cuda")
+    plan = sv.RopePlan(d)
+    side, rotated = torch.cuda.Stream(), torch.empty_like(k)
+
+    def attention(stream):
+        return sv.chunk_attention(q, *c, nq, stream=stream, want_lse=True)
+
+    def rope(stream):
+        return (sv.rope_append(q, k, None, plan, None, None, None, *c[3:], k_out=rotated, stream=stream),)
+
+    def sample(stream):
+        s = sv.sample_tokens(logits, u, 0.8, 40, want_filtered=True, stream=stream)
+        return s.tokens, s.probs, s.kept, s.filtered
+
+    for call in (attention, rope, sample):
+        want = [t.clone() for t in call(None)]
+        torch.cuda.synchronize()
+        for _ in range(3):
+            # blocks of the outputs' sizes, freed while a kernel that reads them is still to run
+            held = [torch.full_like(t, 5) for t in want for _ in range(4)]
+            torch.cuda.synchronize()
+            torch.cuda._sleep(20_000_000)                      # some 10 ms on the current stream
+            read = [h + 1 for h in held]
+            del held
+            got = call(side)
+            side.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(got, want))
+            torch.cuda.synchronize()
+            assert all((r == 6).all() for r in read)
+    # an input that the caller drops while the other stream has not come to it
+    torch.cuda.synchronize()
+    want = sv.sample_tokens(logits, u, 0.8, 40).tokens
+    torch.cuda.synchronize()
+    mine, mine_u = logits.clone(), u.clone()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(20_000_000)
+    got = sv.sample_tokens(mine, mine_u, 0.8, 40, stream=side)
+    del mine, mine_u
+    over = [torch.full_like(logits, -1.0) for _ in range(4)] + [torch.zeros_like(u) for _ in range(4)]
+    torch.cuda.synchronize()
+    assert torch.equal(got.tokens, want) and len(over) == 8
