@@ -95,7 +95,10 @@ class Workspace:
     """
 
     def __init__(self, device=None):
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        device = torch.device("cuda" if device is None else device)
+        if device.type == "cuda" and device.index is None:
+            device = torch.device("cuda", torch.cuda.current_device())
+        self.device = device
         self.buf: Optional[torch.Tensor] = None
         self.step_buf: Optional[torch.Tensor] = None    # the step operators' status word and partial results
         self._outgrown: list = []

@@ -58,6 +58,15 @@ def _where(t, name, index):
     return ValueError(f"{name} must be on the current device cuda:{index}, it is on {t.device}")
 
 
+def _step_buffer(workspace, index, raw, need, stream):
+    """The workspace's buffer (None: the default workspace of the stream) of `need` bytes at least."""
+    if workspace is None:
+        workspace = _workspace(index, raw)
+    elif workspace.device.type != "cuda" or workspace.device.index != index:
+        raise ValueError(f"workspace must be on the current device cuda:{index}, it is on {workspace.device}")
+    return workspace.get_step(need, stream)
+
+
 def _fresh(stream, shape, dtype, device):
     """An output.  With a stream it is that stream's memory, for the current stream to read: the current stream's free memory
     may still be read by work that is queued there, which the kernel on `stream` would not wait for."""
@@ -165,7 +174,7 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     if need is None:
         need = _ws_bytes[key] = lib.spec_attention_workspace_bytes(code, hq, hkv, d, max_q)
     raw = _raw_stream(stream, index)
-    buf = (workspace or _workspace(index, raw)).get_step(need, stream)
+    buf = _step_buffer(workspace, index, raw, need, stream)
     args = (q.data_ptr(), q_token, q_head, code, hq, c, max_q, d ** -0.5 if scale is None else scale, causal, window,
             out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), raw)
     if stream is not None:
@@ -273,7 +282,7 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
         if v.dtype != dtype or v.shape[1] != hkv:
             raise (TypeError if v.dtype != dtype else ValueError)(f"v must be {dtype} of {hkv} heads, got {v.dtype} of {v.shape[1]}")
         vp = v.data_ptr()
-        ws = (workspace or _workspace(index, raw)).get_step(256, stream).data_ptr()
+        ws = _step_buffer(workspace, index, raw, 256, stream).data_ptr()
     elif k_out is None:
         raise ValueError("k_out is required where there is no cache")
     c = _batch(k_cache, v_cache, page_table, kv_lens, cu_q, n, hkv, d, dtype, index)

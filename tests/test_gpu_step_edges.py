@@ -259,3 +259,16 @@ def test_calls_on_another_stream_leave_queued_work_alone(sv):
     over = [torch.full_like(logits, -1.0) for _ in range(4)] + [torch.zeros_like(u) for _ in range(4)]
     torch.cuda.synchronize()
     assert torch.equal(got.tokens, want) and len(over) == 8
+
+
+def test_workspace_of_another_device_is_refused(sv):
+    kc, vc, table, lens, cu = _batch([2], [20], 16, 2, 64, torch.bfloat16, 4)
+    q, k = torch.randn(2, 4, 64).to(torch.bfloat16).cuda(), torch.randn(2, 2, 64).to(torch.bfloat16).cuda()
+    plan = sv.RopePlan(64)
+    for ws in (sv.Workspace("cpu"), sv.Workspace("cuda:1")):
+        with pytest.raises(ValueError):
+            sv.chunk_attention(q, kc, vc, table, lens, cu, 2, workspace=ws)
+        with pytest.raises(ValueError):
+            sv.rope_append(q, k, k, plan, kc, vc, table, lens, cu, workspace=ws)
+    want = sv.chunk_attention(q, kc, vc, table, lens, cu, 2)
+    assert torch.equal(want, sv.chunk_attention(q, kc, vc, table, lens, cu, 2, workspace=sv.Workspace("cuda")))

@@ -84,3 +84,13 @@ def test_reset_clears_outgrown_buffers_too(ws):
     _report(ws.get_step(1 << 20, None), 7)
     ws.reset()
     assert ws.status() == 0
+
+
+def test_step_operators_refuse_a_workspace_elsewhere(monkeypatch):
+    """Its address would be followed on the current device."""
+    from draft_verification_spec_gb300 import step
+    monkeypatch.setattr(sv, "lib", FakeLibrary)
+    monkeypatch.setattr(sv, "_stream_ptr", lambda stream: None)
+    for device in ("cpu", "cuda:1"):
+        with pytest.raises(ValueError, match="workspace must be on the current device cuda:0"):
+            step._step_buffer(sv.Workspace(device), 0, 0, 256, None)
