@@ -58,6 +58,11 @@ def _where(t, name, index):
     return ValueError(f"{name} must be on the current device cuda:{index}, it is on {t.device}")
 
 
+def _int(v):
+    """A bound or count for a C int: what is beyond it stands for as much as the largest one (a refused one stays refused)."""
+    return v if -0x80000000 <= v <= 0x7fffffff else 0x7fffffff if v > 0 else -0x80000000
+
+
 def _step_buffer(workspace, index, raw, need, stream):
     """The workspace's buffer (None: the default workspace of the stream) of `need` bytes at least."""
     if workspace is None:
@@ -158,6 +163,7 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     if code != 1 and code != 2:
         raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
     index = _device()
+    max_q, window = _int(max_q), _int(window)
     q_token, q_head, _ = _heads(q, "q", index)
     n, hq, d = q.shape
     if k_cache.dim() != 4:
@@ -318,7 +324,7 @@ class SampleOutput:
 def _setting(name, value, dtype, rows, index):
     """(number, pointer) of a setting that is a number or a tensor of one per row."""
     if not isinstance(value, torch.Tensor):
-        return value, 0
+        return (_int(value) if dtype == torch.int32 else value), 0
     if value.get_device() != index:
         raise ValueError(f"{name} must be a number or on the current device cuda:{index}, it is on {value.device}")
     if value.dtype != dtype or tuple(value.shape) != (rows,) or not value.is_contiguous():

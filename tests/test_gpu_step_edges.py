@@ -272,3 +272,23 @@ def test_workspace_of_another_device_is_refused(sv):
             sv.rope_append(q, k, k, plan, kc, vc, table, lens, cu, workspace=ws)
     want = sv.chunk_attention(q, kc, vc, table, lens, cu, 2)
     assert torch.equal(want, sv.chunk_attention(q, kc, vc, table, lens, cu, 2, workspace=sv.Workspace("cuda")))
+
+
+def test_integers_beyond_32_bits(sv):
+    """A window or a number of tokens that no C int holds: as much as the largest one, and no less than nothing."""
+    kc, vc, table, lens, cu = _batch([20, 3], [90, 200], 16, 2, 64, torch.bfloat16, 4)
+    q = torch.randn(23, 8, 64).to(torch.bfloat16).cuda()
+    want = sv.chunk_attention(q, kc, vc, table, lens, cu, 20)
+    for window in (2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1, 2 ** 64 + 1):
+        assert torch.equal(want, sv.chunk_attention(q, kc, vc, table, lens, cu, 20, window=window))
+        assert torch.equal(want, sv.chunk_attention(q, kc, vc, table, lens, cu, max_q=window))
+    for bad in (-1, -2 ** 31, -2 ** 32, -2 ** 32 + 5):
+        with pytest.raises(sv.SpecError):
+            sv.chunk_attention(q, kc, vc, table, lens, cu, 20, window=bad)
+        with pytest.raises(sv.SpecError):
+            sv.chunk_attention(q, kc, vc, table, lens, cu, bad)
+    z, u = torch.randn(2, 500, device="cuda"), torch.rand(2, device="cuda")
+    want = sv.sample_tokens(z, u).tokens
+    for top_k in (2 ** 31 - 1, 2 ** 31, 2 ** 40, -2 ** 40):
+        out = sv.sample_tokens(z, u, top_k=top_k)
+        assert torch.equal(out.tokens, want) and (out.kept == 500).all()
