@@ -321,6 +321,16 @@ class SampleOutput:
     filtered: Optional[torch.Tensor] = None  # [rows, V]: the kept tokens' logits, -inf elsewhere
 
 
+def _overlap(a, b):
+    """Whether two [rows, V] tensors of one type and shape, values of a row contiguous, share memory."""
+    (rows, V), size = a.shape, a.element_size()
+    sa, sb = (t.stride(0) if rows > 1 else V for t in (a, b))
+    gap = (b.data_ptr() - a.data_ptr()) // size
+    if rows == 0 or gap >= (rows - 1) * sa + V or -gap >= (rows - 1) * sb + V:
+        return False
+    return sa != sb or not V <= gap % sa <= sa - V     # rows side by side in one buffer are apart
+
+
 def _setting(name, value, dtype, rows, index):
     """(number, pointer) of a setting that is a number or a tensor of one per row."""
     if not isinstance(value, torch.Tensor):
@@ -374,6 +384,8 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
         if f is not None and (f.dtype != logits.dtype or f.shape != logits.shape or f.device != dev or
                               (V > 1 and f.stride(1) != 1) or (R > 1 and f.stride(0) < V)):
             raise ValueError("out.filtered must have the shape, dtype and device of logits and contiguous rows")
+        if f is not None and _overlap(logits, f):
+            raise ValueError("out.filtered must not overlap logits")
     f = out.filtered
     if stream is not None:
         _used_on(stream, logits, uniforms, temperature, top_k, top_p, min_p, out.tokens, out.probs, out.kept, f)

@@ -292,3 +292,16 @@ def test_integers_beyond_32_bits(sv):
     for top_k in (2 ** 31 - 1, 2 ** 31, 2 ** 40, -2 ** 40):
         out = sv.sample_tokens(z, u, top_k=top_k)
         assert torch.equal(out.tokens, want) and (out.kept == 500).all()
+
+
+def test_sample_filtered_over_its_own_logits_is_refused(sv):
+    z = torch.randn(3, 1000, device="cuda")
+    u = torch.rand(3, device="cuda")
+    fresh = lambda f: sv.SampleOutput(*(torch.empty(3, dtype=t, device="cuda") for t in (torch.int32, torch.float32, torch.int32)), f)  # noqa: E731
+    both = torch.randn(3, 2000, device="cuda")
+    for f, logits in ((z, z), (both[:, 500:1500], both[:, :1000])):
+        with pytest.raises(ValueError):
+            sv.sample_tokens(logits, u, 0.8, 40, out=fresh(f))
+    want = sv.sample_tokens(both[:, :1000], u, 0.8, 40, want_filtered=True)
+    got = sv.sample_tokens(both[:, :1000], u, 0.8, 40, out=fresh(both[:, 1000:]))    # side by side: apart
+    assert torch.equal(got.filtered, want.filtered) and torch.equal(got.tokens, want.tokens)
