@@ -4,7 +4,7 @@ import pytest
 import torch
 
 from tests import step_reference as R
-from tests.test_gpu_step_ops import _batch, _rope
+from tests.test_gpu_step_ops import DTYPES, _batch, _check_sample, _rope
 
 pytestmark = pytest.mark.gpu
 
@@ -305,3 +305,76 @@ def test_sample_filtered_over_its_own_logits_is_refused(sv):
     want = sv.sample_tokens(both[:, :1000], u, 0.8, 40, want_filtered=True)
     got = sv.sample_tokens(both[:, :1000], u, 0.8, 40, out=fresh(both[:, 1000:]))    # side by side: apart
     assert torch.equal(got.filtered, want.filtered) and torch.equal(got.tokens, want.tokens)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [32768, 65537, 131071])
+def test_sample_clusters_ties_zeros_infinities(sv, dtype, V):
+    """Rows shared by 2 to 8 CTAs: no logit above -inf, NaN, +inf, zeros of both signs, ties across the CTAs' shares."""
+    dt, inf, nan = DTYPES[dtype], float("inf"), float("nan")
+    z = torch.zeros(10, V)
+    z[1, ::2] = -0.0
+    z[2] = -inf
+    z[3] = -inf
+    z[3, V - 3] = -5.0
+    z[4, 100:] = -inf
+    z[5, ::3] = nan
+    z[6, 10] = z[6, V // 2] = z[6, V - 1] = inf
+    z[7] = nan
+    z[8] = torch.arange(V) // (V // 6) * 1.0
+    z[9, : V - 7] = -inf                     # all that counts is the last CTA's
+    u = torch.tensor([0.5, 0.999, 0.5, 0.999, 0.9999999, 0.3, 0.7, 0.1, 0.0, 0.6]).cuda()
+    z = z.to(dt).cuda()
+    for s in (dict(), dict(top_k=V // 2 + 7), dict(top_p=0.5), dict(T=0.0), dict(min_p=0.5), dict(top_k=V - 9, top_p=0.7)):
+        _check_sample(sv, z, u, **s)
+    for r in range(10):                      # a row alone takes the largest cluster
+        _check_sample(sv, z[r:r + 1], u[r:r + 1], top_p=0.6, top_k=V // 3)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("V", [32768, 100003])
+def test_sample_clusters_logits_of_any_size(sv, dtype, V):
+    """The general descent and the bins below -2^8 in clusters: masks of -1e9 and of the type's lowest value, logits in the
+    hundreds and thousands, vanishing ones."""
+    dt = DTYPES[dtype]
+    g = torch.Generator().manual_seed(V)
+    z = torch.randn(8, V, generator=g) * 3.0
+    low = torch.finfo(dt).min
+    z[0, 100:] = -1e9
+    z[1, 5:] = low
+    z[2, ::2] = -300.0 - torch.arange((V + 1) // 2) % 50
+    z[3] = z[3] * 400.0
+    z[4, ::7] = torch.randn(len(z[4, ::7]), generator=g) * 1e-20
+    z[5] = -500.0 + z[5]
+    z[6] = low
+    z[6, V - 9] = -1e30
+    z[7] = z[7] * 1e-18
+    z, u = z.to(dt).cuda(), torch.rand(8, generator=g).cuda()
+    for s in (dict(), dict(T=0.0), dict(T=0.6), dict(top_k=17), dict(top_p=0.9), dict(min_p=0.05), dict(top_k=V - V // 3),
+              dict(top_k=V - 1, top_p=0.99), dict(T=100.0, top_p=0.9), dict(T=1e4, top_k=V // 2),
+              dict(T=0.8, top_k=400, top_p=0.95, min_p=0.01)):
+        _check_sample(sv, z, u, **s)
+        _check_sample(sv, z[3:4], u[3:4], **s)
+
+
+def test_sample_clusters_crowded_bins(sv):
+    """fp32 logits of which thousands share their 16 top bits, more and fewer than a CTA gathers, in shares of several CTAs."""
+    z = 3.0 + torch.rand(3, 70000, generator=torch.Generator().manual_seed(2)) * 0.01
+    z[1, ::9] = 3.5
+    z[2, 10000:] = -7.0
+    u = torch.rand(3, generator=torch.Generator().manual_seed(3)).cuda()
+    for s in (dict(), dict(top_k=777, top_p=0.9), dict(top_p=0.4), dict(min_p=0.997), dict(top_k=9000)):
+        _check_sample(sv, z.cuda(), u, **s)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 9, 10, 18, 19, 38, 39, 76, 77])
+def test_sample_rows_per_cluster(sv, dtype, rows):
+    """Every size of cluster on 152 SMs (8, 4, 2 CTAs a row and one), settings of their own, rows out of line with 16 bytes."""
+    V = 65537
+    g = torch.Generator().manual_seed(rows)
+    z = (torch.randn(rows, V, generator=g) * 2.0).to(DTYPES[dtype]).cuda()
+    u = torch.rand(rows, generator=g).cuda()
+    pick = lambda v, t: torch.tensor(v, dtype=t)[torch.randint(len(v), (rows,), generator=g)].cuda()  # noqa: E731
+    _check_sample(sv, z, u, pick([0.0, 0.5, 1.0, 1.5], torch.float32), pick([0, 1, 20, 5000], torch.int32),
+                  pick([1.0, 0.9, 0.5], torch.float32), pick([0.0, 0.1], torch.float32))
