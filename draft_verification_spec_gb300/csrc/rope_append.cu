@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kRopeThreads) rope_kernel(const RopeParams p, 
 
 }  // namespace
 
-cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream) {
+cudaError_t launch_rope(int dtype, const RopeParams& p, int sms, cudaStream_t stream) {
   const int vec = dtype == 0 ? 4 : 8;
   // whole 16-byte pieces: sizes, strides and bases
   const long long strides[] = {p.q_token, p.q_head, p.k_token, p.k_head, p.qo_token, p.qo_head,
@@ -319,7 +319,7 @@ cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream) {
   // few tokens: a CTA each; many: as many tokens a CTA as make about 2048 pieces.  8192 tokens of 40 + 8 heads
   // of 128, bf16 (201 MB): 41 us with 128 threads and 2048 pieces (4.9 TB/s, 72 % of measured HBM), 43 with
   // 1024, 49 with 4096; 256 threads 45 us; four pieces in flight a thread instead of two 47 us.
-  int per = p.c.N <= 608 ? 1 : static_cast<int>(2048 / (units > 0 ? units : 1));
+  int per = p.c.N <= 4 * sms ? 1 : static_cast<int>(2048 / (units > 0 ? units : 1));
   per = per < 1 ? 1 : per > kRopeMaxTokens ? kRopeMaxTokens : per;
   const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);
   const size_t smem = sizeof(float2) * (p.rotary / 2) * per;

@@ -84,7 +84,7 @@ struct RopeParams {
   int Hq, rotary, interleaved;
   int32_t* status;
 };
-cudaError_t launch_rope(int dtype, const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_rope(int dtype, const RopeParams& p, int sms, cudaStream_t stream);
 
 struct SampleParams {
   const void* logits;
