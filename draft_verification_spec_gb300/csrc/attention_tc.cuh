@@ -16,7 +16,8 @@
 //
 // O is rescaled only when a row's maximum grows by more than 2^8 over the reference its exponentials
 // use; until then the probabilities may reach 2^8, which neither type overflows and the final division
-// by the sum undoes.  S(j) is committed after the same half's previous P V in issue order, so a softmax
+// by the sum undoes.  They are rounded to the operands' type (the A operand has B's): see the mma.sync kernel
+// for what that costs.  S(j) is committed after the same half's previous P V in issue order, so a softmax
 // thread that has seen S(j) may touch O.
 //
 // Keys before the item's first one or at or beyond its last one: pages that lie wholly there are read at an
@@ -24,10 +25,11 @@
 // rows are zeroed in shared memory before the MMA reads them (0 x NaN would be NaN); scores are
 // selected, not multiplied.
 //
-// Bound and measured, heads of 128, bf16: 2 x 2048 tokens behind 14336, 32/8 heads (1.03 TFLOP) 728 us, 1.42
-// PFLOP/s, 75 % of the measured matrix rate: a half's softmax (1200 cycles a tile) and its two products (1024)
-// follow one another, and the other half fills most of the gap.  32 x 17 tokens, 64/8 heads, ragged to 16384
-// keys (1.11 GB) 216-220 us, 5.1 TB/s, 75 % of the measured copy: 136 rows take two halves of 128.
+// Bound and measured, heads of 128, bf16: 2 x 2048 tokens behind 14336, 32/8 heads (1.03 TFLOP) 728-761 us (by
+// the machine), 1.35-1.42 PFLOP/s, 72-75 % of the measured matrix rate: a half's softmax (1200 cycles a tile)
+// and its two products (1024) follow one another, and the other half fills most of the gap.  32 x 17 tokens,
+// 64/8 heads, ragged to 16384 keys (1.11 GB) 218-224 us, 5.0 TB/s, 74 % of the measured copy: 136 rows take two
+// halves of 128.
 //
 // Every wait is bounded: after `wait_limit` the kernel sets the status word, drains its copies and
 // MMAs, frees TMEM and returns, its record for the combine kernel empty.

@@ -4,8 +4,9 @@
 //
 // for the pairs (x, y) = (j, j + r/2) (half layout) or (2j, 2j + 1) (interleaved) of the first r
 // values of a head.  f_j comes as the fraction of a turn per position, scaled by 2^64, so the phase
-// is one 64-bit product: whole turns fall out by the wrap, and a position of 10^6 keeps the phase
-// to 2^-44 of a turn where an fp32 product would have lost all but four bits of it.
+// is one 64-bit product: whole turns fall out by the wrap.  The frequencies are rounded from 64-bit floating
+// point, which at a position of 10^6 leaves the phase exact to 2^-35 of a turn, where an fp32 product would
+// have lost all but four bits of it.
 #include "spec_device.cuh"
 #include "step_internal.h"
 
@@ -47,8 +48,8 @@ __device__ __forceinline__ float2 phase_cs(unsigned long long phase) {
   return make_float2(c, s);
 }
 
-// Any size, alignment and stride: one CTA per token: the token's request and cache slot, its r/2 angles in shared memory, then every
-// head's values, 1 pair (or 1 value behind the rotated part) per thread and step.
+// Any size, alignment and stride: one CTA per token: the token's request and cache slot, its r/2 angles in shared
+// memory, then every head's values, 1 pair (or 1 value behind the rotated part) per thread and step.
 template <int DTYPE>
 __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(const RopeParams p) {
   using T = typename RopeType<DTYPE>::T;
@@ -316,9 +317,11 @@ cudaError_t launch_rope(int dtype, const RopeParams& p, int sms, cudaStream_t st
     if (dtype == 2) rope_scalar_kernel<2><<<grid, block, smem, stream>>>(p);
     return cudaGetLastError();
   }
-  // few tokens: a CTA each; many: as many tokens a CTA as make about 2048 pieces.  8192 tokens of 40 + 8 heads
-  // of 128, bf16 (201 MB): 41 us with 128 threads and 2048 pieces (4.9 TB/s, 72 % of measured HBM), 43 with
-  // 1024, 49 with 4096; 256 threads 45 us; four pieces in flight a thread instead of two 47 us.
+  // few tokens: a CTA each; many: as many tokens a CTA as make about 2048 pieces.  40 + 8 heads of 128, bf16, on
+  // the device, a CTA a token against 2048 pieces: 304 tokens 4.7 : 5.5 us, 608 (four an SM) 7.1 : 8.4, 1088
+  // 9.2 : 10.4, 2048 13.8 : 13.2; so the rule changes over early rather than late.  8192 tokens (201 MB) take
+  // 39 us (5.2 TB/s, 76 % of measured HBM); with quotients by division 41, then 43 with 1024 pieces, 49 with
+  // 4096, 45 with 256 threads, 47 with four pieces in flight a thread instead of two.
   int per = p.c.N <= 4 * sms ? 1 : static_cast<int>(2048 / (units > 0 ? units : 1));
   per = per < 1 ? 1 : per > kRopeMaxTokens ? kRopeMaxTokens : per;
   const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);

@@ -169,8 +169,8 @@ spec_status_t spec_chunk_attention_tuned(const void* q, long long q_token, long 
     // 0: 140, 1: 127, 2: 115, 3: 113, 4: 114 us; 32 x 17 tokens, 64 query heads, ragged to 16384 (tcgen05):
     // 0: 248, 2: 234, 3: 224, 4: 220, 6: 220 us.
     p.overhead = plan.kind >= 2 ? 4 : 3;
-    // one key tile is worth a CTA of its own.  A single token over 1024 keys, 8 key heads: 12.4 us; two tiles
-    // 13.3, four 15.2 us.
+    // fewest units worth a CTA: an item's cost and one key tile.  A single token over 1024 keys, 8 key heads
+    // (152 units, so 38 CTAs of four): 12.4 us; with two tiles (31 CTAs) 13.3, with four (22) 15.2 us.
     p.min_units = 1 + p.overhead;
     const long long wait_us = tuning ? tuning->wait_limit_us : 0;
     p.wait_limit = wait_us == 0 ? kWaitNs : wait_us < 0 ? 0 : wait_us < kWaitNs ? wait_us * 1000 : kWaitNs * 1000;

@@ -154,7 +154,7 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     otherwise all of its request.  ``window`` > 0: only keys within that many positions back, its
     own included (pages wholly behind it may be gone).  ``scale`` defaults to dim ** -0.5.  Returns
     out [tokens, q_heads, dim], with ``want_lse`` (out, lse [tokens, q_heads] float32); a row that
-    sees no key gives 0 and -inf.
+    sees no key gives 0 and -inf, rows of tokens that no request has stay unwritten.
     ``tuning``: a Tuning, of which the wait limit counts here (spec_chunk_attention_tuned).
     """
     lib = _lib or _bind()
@@ -262,7 +262,8 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
 
     q [tokens, q_heads, dim], k and v [tokens, kv_heads, dim], float32, bfloat16 or float16.  Returns the
     rotated queries (in ``q_out``, which may be q).  ``k_out`` receives the rotated keys too (may be k);
-    it is required where k_cache, v_cache and page_table are None and nothing is stored.
+    it is required where k_cache, v_cache and page_table are None and nothing is stored.  Rows of tokens
+    that no request has stay unwritten.
     """
     lib = _lib or _bind()
     dtype = q.dtype
@@ -349,7 +350,8 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     logits [rows, V] bfloat16 or float32 (rows may be strided), uniforms [rows] float32.  Each setting is
     a number or a tensor of one per row (float32, top_k int32); top_k <= 0, top_p >= 1 and min_p <= 0 keep
     all, temperature 0 is greedy.  With ``want_filtered`` the truncated logits come too: what
-    verify_chain / verify_block take as the distribution that the token was drawn from.
+    verify_chain / verify_block take as the distribution that the token was drawn from (their
+    ``temperature`` is one for the batch, so rows sampled at others are not theirs to verify).
     """
     lib = _lib or _bind()
     if logits.dim() != 2:

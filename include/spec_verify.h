@@ -414,7 +414,9 @@ typedef struct spec_rope_tensors {
  *   dtype     SPEC_F32, SPEC_BF16 or SPEC_F16, of every tensor
  *   workspace as spec_chunk_attention's (status word only); may be NULL
  *             without a cache
- * dim at most 1024.  One launch.
+ * dim at most 1024.  Rows of q_out and k_out of tokens that no request has
+ * stay unwritten.  q_out and k_out overlap no input but q and k themselves,
+ * with the same strides.  One launch.
  */
 spec_status_t spec_rope_append(const spec_rope_tensors_t* t, int dtype, int q_heads, const spec_paged_batch_t* batch,
                                const unsigned long long* freq, int rotary_dim, float factor, int interleaved,
@@ -422,7 +424,7 @@ spec_status_t spec_rope_append(const spec_rope_tensors_t* t, int dtype, int q_he
 
 /* Sampling settings: a scalar each, or a device array of one per row where its pointer is not NULL. */
 typedef struct spec_sampling {
-  float temperature;             /* <= 0: greedy */
+  float temperature;             /* 0: greedy (a negative one is refused; in an array <= 0 is greedy) */
   int top_k;                     /* <= 0: all */
   float top_p;                   /* >= 1: all */
   float min_p;                   /* <= 0: all */
@@ -441,8 +443,8 @@ typedef struct spec_sampling {
  *        first n_k;
  *   n_m  the tokens with w >= min_p.
  * The token drawn is the first whose inclusive prefix weight is strictly
- * above uniforms[r] x the weight of the kept ones.  Temperature <= 0 (or
- * NaN in an array) keeps the first token alone.
+ * above uniforms[r] x the weight of the kept ones.  Temperature 0 (in an
+ * array <= 0 or NaN) keeps the first token alone.
  *   logits       [rows, V] SPEC_BF16 or SPEC_F32, rows row_stride apart
  *   uniforms     [rows] float32 in [0, 1) (clamped to it)
  *   out_tokens   [rows] int32; -1 for a row without a logit above -inf
@@ -451,8 +453,9 @@ typedef struct spec_sampling {
  *   out_kept     [rows] int32 or NULL: n (0 for such a row)
  *   out_filtered [rows, V] of the logits' type, rows filtered_stride apart,
  *                or NULL: the kept tokens' logits, -inf elsewhere (what the
- *                verification calls take as the truncated distribution); must
- *                not overlap logits
+ *                verification calls take as the truncated distribution, at
+ *                their one temperature for the batch); must not overlap
+ *                logits
  * NaN logits count as -inf.  Sums are exact integers (weights in units of
  * 2^-44), so results do not depend on timing.  V <= 262144.  One launch, no
  * workspace.
