@@ -456,8 +456,10 @@ typedef struct spec_sampling {
  *                verification calls take as the truncated distribution, at
  *                their one temperature for the batch); must not overlap
  *                logits
- * NaN logits count as -inf.  Sums are exact integers (weights in units of
- * 2^-44), so results do not depend on timing.  V <= 262144.  One launch, no
+ * NaN logits count as -inf.  Weights are in units of 2^-44 of the largest:
+ * nearer ones than that are equal, min_p's too, and a probability is exact to
+ * 2^-45 / (weight of the kept ones) or fp32's rounding.  Their sums are exact
+ * integers, so results do not depend on timing.  V <= 262144.  One launch, no
  * workspace.
  */
 spec_status_t spec_sample_tokens(const void* logits, long long row_stride, int dtype, int rows, int V,
