@@ -406,8 +406,9 @@ def draft_budget(draft, tokens, temperature: float, budget: Optional[int] = None
     return n_out, depth, conf
 
 
-from .step import RopePlan, SampleOutput, chunk_attention, rope_append, sample_tokens  # noqa: E402
+from .step import FP4Cache, RopePlan, SampleOutput, chunk_attention, rope_append, sample_tokens  # noqa: E402
 
 __all__ = ["verify_chain", "verify_block", "overlap_alpha", "alloc_budget", "alloc_budget_adaptive",
            "draft_budget", "Workspace", "VerifyOutput", "Tuning", "SpecError", "lib",
-           "chunk_attention", "rope_append", "sample_tokens", "RopePlan", "SampleOutput"]
+           "chunk_attention", "rope_append", "sample_tokens", "RopePlan", "SampleOutput",
+           "FP4Cache"]

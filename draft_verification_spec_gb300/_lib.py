@@ -51,6 +51,17 @@ SIGNATURES = {
                                      c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p]),
     "spec_chunk_attention_tuned": (c_int, [c_void_p, c_longlong, c_longlong, c_int, c_int, c_void_p, c_int, c_float,
                                            c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p, c_void_p]),
+    "spec_chunk_attention_sinks": (c_int, [c_void_p, c_longlong, c_longlong, c_int, c_int, c_void_p, c_int, c_float,
+                                           c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t, c_void_p,
+                                           c_void_p]),
+    "spec_attention_fp4_workspace_bytes": (c_size_t, [c_int, c_int, c_int, c_int, c_int]),
+    "spec_chunk_attention_fp4": (c_int, [c_void_p, c_longlong, c_longlong, c_int, c_int, c_void_p, c_void_p, c_int,
+                                         c_float, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p, c_size_t,
+                                         c_void_p, c_void_p]),
+    "spec_rope_append_fp4": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_void_p, c_int, c_float, c_int,
+                                     c_void_p, c_void_p]),
+    "spec_fp4_values": (c_int, [c_void_p, c_longlong, c_longlong, c_longlong, c_void_p, c_longlong, c_longlong,
+                                c_longlong, c_float, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
     "spec_rope_append": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_float, c_int, c_void_p,
                                  c_void_p]),
     "spec_sample_tokens": (c_int, [c_void_p, c_longlong, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,
@@ -84,4 +95,4 @@ def header_symbols(header: str) -> list[str]:
     import re
     text = open(header).read()
     text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
-    return sorted(set(re.findall(r"\b(spec_[a-z_]+)\s*\(", text)))
+    return sorted(set(re.findall(r"\b(spec_[a-z0-9_]+)\s*\(", text)))

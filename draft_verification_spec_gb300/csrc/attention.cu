@@ -4,18 +4,31 @@
 #include <mutex>
 #include <tuple>
 
+#include "attention_fp4.cuh"
 #include "attention_tc.cuh"
 
 namespace sv {
 
 template <>
-const void* attn_mma_fn<true>(int dp, int bm);
+const void* attn_mma_fn<true, false>(int dp, int bm);
 template <>
-const void* attn_mma_fn<false>(int dp, int bm);
+const void* attn_mma_fn<false, false>(int dp, int bm);
 template <>
-const void* attn_tc_fn<true>(int dp, bool wide);
+const void* attn_mma_fn<true, true>(int dp, int bm);
 template <>
-const void* attn_tc_fn<false>(int dp, bool wide);
+const void* attn_mma_fn<false, true>(int dp, int bm);
+template <>
+const void* attn_tc_fn<true, false>(int dp, bool wide);
+template <>
+const void* attn_tc_fn<false, false>(int dp, bool wide);
+template <>
+const void* attn_tc_fn<true, true>(int dp, bool wide);
+template <>
+const void* attn_tc_fn<false, true>(int dp, bool wide);
+template <>
+const void* attn_fp4_fn<true>(int dp);
+template <>
+const void* attn_fp4_fn<false>(int dp);
 
 // Joins the item that CTA blockIdx.x left a record of: one warp per row, the partials in key order,
 // each scaled by 2^(its maximum - the largest).  fp32.
@@ -51,7 +64,7 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p, i
         }
       }
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l > 0.f ? p.v_unit / l : 0.f;
     const int tok = attn_token(p, j.row0 + r);
     const long long row = static_cast<long long>(j.token0 + tok) * p.Hq + j.head0 + (j.row0 + r - tok * p.G);
 #pragma unroll
@@ -89,15 +102,20 @@ static cudaError_t resident(const void* fn, int threads, int smem, int* out) {
   return cudaSuccess;
 }
 
-static const void* kernel_of(bool bf16, const AttnPlan& plan) {
-  if (plan.kind >= 2) return bf16 ? attn_tc_fn<true>(plan.dp, plan.kind == 3) : attn_tc_fn<false>(plan.dp, plan.kind == 3);
-  return bf16 ? attn_mma_fn<true>(plan.dp, plan.bm) : attn_mma_fn<false>(plan.dp, plan.bm);
+template <bool BF16, bool SINKS>
+static const void* kernel_of(const AttnPlan& plan) {
+  return plan.kind >= 2 ? attn_tc_fn<BF16, SINKS>(plan.dp, plan.kind == 3) : attn_mma_fn<BF16, SINKS>(plan.dp, plan.bm);
+}
+static const void* kernel_of(const AttnForm& form, const AttnPlan& plan) {
+  if (form.fp4) return form.bf16 ? attn_fp4_fn<true>(plan.dp) : attn_fp4_fn<false>(plan.dp);
+  if (form.sinks) return form.bf16 ? kernel_of<true, true>(plan) : kernel_of<false, true>(plan);
+  return form.bf16 ? kernel_of<true, false>(plan) : kernel_of<false, false>(plan);
 }
 
-cudaError_t attention_plan(bool bf16, int kind, int rows, int D, int sms, AttnPlan* plan) {
+cudaError_t attention_plan(const AttnForm& form, int kind, int rows, int D, int sms, AttnPlan* plan) {
   plan->kind = kind;
   plan->bm = kind == 0 ? 16 : kind == 1 ? 64 : kind == 2 ? 128 : 256;
-  plan->bn = kind >= 2 ? kTcBN : kAttnBN;
+  plan->bn = kind >= 2 ? kTcBN : form.fp4 ? kFp4BN : kAttnBN;
   plan->rows = rows < 1 ? 1 : rows < plan->bm ? rows : plan->bm;
   plan->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
   int threads = kAttnThreads;
@@ -105,11 +123,13 @@ cudaError_t attention_plan(bool bf16, int kind, int rows, int D, int sms, AttnPl
     plan->smem = kind == 2 ? (plan->dp == 64 ? AttnTcGeom<64, false>::kSmem : AttnTcGeom<128, false>::kSmem)
                            : (plan->dp == 64 ? AttnTcGeom<64, true>::kSmem : AttnTcGeom<128, true>::kSmem);
     threads = kTcThreads;
+  } else if (form.fp4) {
+    plan->smem = attn_fp4_smem(plan->dp);
   } else {
-    plan->smem = bf16 ? attn_mma_smem<true>(plan->dp, plan->bm) : attn_mma_smem<false>(plan->dp, plan->bm);
+    plan->smem = form.bf16 ? attn_mma_smem<true>(plan->dp, plan->bm) : attn_mma_smem<false>(plan->dp, plan->bm);
   }
   int occ = 0;
-  const cudaError_t e = resident(kernel_of(bf16, *plan), threads, plan->smem, &occ);
+  const cudaError_t e = resident(kernel_of(form, *plan), threads, plan->smem, &occ);
   plan->grid = sms * (kind >= 2 ? 1 : occ);   // the tcgen05 kernel takes all of an SM's TMEM
   return e;
 }
@@ -125,6 +145,11 @@ int attention_kind(int rows, int D, int page_size, float scale) {
   const bool pow2 = (page_size & (page_size - 1)) == 0;
   if (rows > 16 && D >= 64 && D <= 128 && pow2 && page_size >= 8 && scale > 0.f) return rows > 128 ? 3 : 2;
   return rows <= 16 ? 0 : 1;
+}
+
+// Over caches in 4 bits.
+int attention_fp4_kind(int rows, int D, float scale) {
+  return 0;
 }
 
 // cuTensorMapEncodeTiled, looked up once through the runtime (the library does not link the driver).
@@ -172,12 +197,13 @@ bool attention_maps(bool bf16, const PagedBatch& c, AttnMaps* maps) {
          encode_cache(bf16, c, c.v, c.v_page, c.v_token, c.v_head, reinterpret_cast<CUtensorMap*>(maps->v));
 }
 
-cudaError_t launch_attention(bool bf16, const AttnPlan& plan, const AttnParams& p, const AttnMaps& maps, cudaStream_t stream) {
+cudaError_t launch_attention(const AttnForm& form, const AttnPlan& plan, const AttnParams& p, const AttnMaps& maps,
+                             cudaStream_t stream) {
   AttnParams copy = p;
   AttnMaps m = maps;
   void* tc[] = {m.k, m.v, &copy};
   void* mma[] = {&copy};
-  return cudaLaunchKernel(kernel_of(bf16, plan), dim3(plan.grid), dim3(plan.kind >= 2 ? kTcThreads : kAttnThreads),
+  return cudaLaunchKernel(kernel_of(form, plan), dim3(plan.grid), dim3(plan.kind >= 2 ? kTcThreads : kAttnThreads),
                           plan.kind >= 2 ? tc : mma, plan.smem, stream);
 }
 

@@ -1,0 +1,461 @@
+// Attention of new tokens over a paged cache held in 4 bits (step_internal.h: Fp4Scales), mma.sync kernel: any page
+// size, head sizes up to 256, tiles of 16 rows.
+//
+// The same formula and the same work division as the kernel over 16-bit caches (attention_mma.cuh), over
+//   k = unit scale[block] code: code e2m1, scale e4m3, a block 16 values along the head.
+// A code (2 significant bits) times a scale (4) is exact in half precision, whatever both are, so the tensor core gets
+// the keys and values that the bits stand for, in f16; the units (powers of two) are factors of the scores and of the
+// rows.  Queries: f16 as they are; bf16 ones as f16 relative to the power of two at the row's largest value, which is
+// exact down to 2^-14 of it and loses 2^-25 of it at most below that.  Probabilities are rounded to f16, up to
+// 2^14 (see kShift): 2^-12 relative down to 2^-20 of the reference.  Statistics and O are fp32.
+//
+// Tiles: 128 keys, of which every warp takes 32 for itself: it looks up their pages, copies them into a ring of its own
+// and works on them, so nothing in the loop waits for another warp.  A lane reads from shared memory just the bytes
+// whose values it hands to the tensor core: the order of the values in a contraction is free, so a lane's 4 of every
+// 16 are 32 consecutive values of a key, 16 bytes (the queries are laid out to match), and its columns of O are 16
+// consecutive values.  For P V two keys' nibbles are brought together in a byte before the conversion, which then
+// gives the pair that the tensor core wants.
+#pragma once
+
+#include "attention_mma.cuh"
+
+namespace sv {
+
+constexpr int kFp4BN = 128;         // keys of a tile
+constexpr int kFp4WarpKeys = 32;    // of which a warp takes this many
+// Probabilities are 2^kShift times the weights against the reference, which lie between 0 and 2^kGrow.
+constexpr float kFp4Shift = 6.f, kFp4Grow = 8.f;
+
+template <int DP>
+struct AttnFp4Geom {
+  static constexpr int kRow = DP / 2, kScale = DP / 16;   // bytes of a key's codes and scales
+  static constexpr int kCodes = kFp4WarpKeys * kRow, kScales = kFp4WarpKeys * kScale;
+  static constexpr int kStage = 2 * (kCodes + kScales);   // one warp's K codes, V codes, K scales, V scales
+  static constexpr int kStages = DP == 256 ? 2 : DP == 128 ? 3 : 4;
+  static constexpr int kSmem = 4 * kStages * kStage;
+  static_assert(4 * 16 * DP * 4 <= kSmem || DP == 64, "the output staging fits the ring");
+};
+
+// Byte offset of 16-byte piece c of key r in a warp's tile of codes.  The pieces are permuted so that the
+// lanes of one read phase fall on distinct banks: K, two keys of four lanes each; V, four keys two apart of two pieces each.
+template <int DP>
+__device__ __forceinline__ uint32_t fp4_k_piece(int r, int c) {
+  return static_cast<uint32_t>(r * (DP / 2) + ((DP == 256 ? c ^ ((r & 1) << 2) : c) << 4));
+}
+template <int DP>
+__device__ __forceinline__ uint32_t fp4_v_piece(int r, int c) {
+  constexpr int per = 256 / DP;                      // keys of a 128-byte line
+  const int line = r / per, in = r % per * (DP / 32) + c;
+  const int x = DP == 64 ? (line & 1) << 1 : DP == 128 ? (line & 3) << 1 : ((r >> 1) & 3) << 1;
+  return static_cast<uint32_t>(line * 128 + ((in ^ x) << 4));
+}
+
+// Four bytes of two codes each -> four pairs of f16 (low nibble first).
+__device__ __forceinline__ void fp4_pairs(uint32_t w, uint32_t (&r)[4]) {
+  asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+      : "r"(w));
+}
+// Two e4m3 scales -> two f16.
+__device__ __forceinline__ uint32_t fp4_scales(uint32_t two) {
+  uint32_t r;
+  asm("{\n\t.reg .b16 s;\n\tcvt.u16.u32 s, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, s;\n\t}" : "=r"(r) : "r"(two));
+  return r;
+}
+__device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+template <int N>
+__device__ __forceinline__ void cp_async_some(uint32_t dst, const void* src, bool valid) {
+  const int n = valid ? N : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ long long shfl64(long long v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
+
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams p) {
+  using A = AttnType<BF16>;
+  using H = AttnType<false>;   // the products are of f16 values
+  using Geo = AttnFp4Geom<DP>;
+  constexpr int BM = 16, BN = kFp4BN, WK = kFp4WarpKeys, NT = WK / 8, DT = DP / 8, STAGES = Geo::kStages;
+  constexpr int WORDS = DP / 32;         // words of 8 codes that a lane reads of a key, of K
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ AttnSchedSmem<kAttnThreads> sched;
+  __shared__ float s_ml[4][BM][2];
+  float* s_o = reinterpret_cast<float*>(smem);   // [4][BM][DP] after the last key tile
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const AttnSplit split = attn_split<BN, true>(p, BM, sched);
+  const int cta = blockIdx.x;
+  asm volatile("griddepcontrol.launch_dependents;");
+  if (cta >= split.n) {
+    if (tid == 0) attn_leave_join(p, split, cta, BM, nullptr, false);
+    return;
+  }
+  const long long u_begin = split.begin(cta), u_end = split.begin(cta + 1);
+  AttnCursor cur = attn_locate<BN, true>(p, BM, u_begin, sched);
+  int k0, k1;
+  cur.share(p, u_begin, u_end, &k0, &k1);
+  if (k1 <= k0) {   // nothing but an item's overhead
+    if (tid == 0) attn_leave_join(p, split, cta, BM, nullptr, false);
+    return;
+  }
+  bool later = false;   // not the CTA's first item
+  const uint32_t ring = smem_addr(smem) + warp * STAGES * Geo::kStage;
+  const int D = p.c.D, P = p.c.page_size;
+
+  while (true) {
+    const int len = k1 - k0;
+    const int rows = cur.req.nq * p.G, r0 = cur.t * BM, r1 = min(rows, r0 + BM);
+    int lo, hi;
+    attn_keys(p, cur.req, r0, r1, &lo, &hi);
+    const int32_t* table = p.c.table + static_cast<long long>(cur.b) * p.c.table_stride;
+    const uint8_t* kbase = p.c.k + cur.h * p.c.k_head;
+    const uint8_t* vbase = p.c.v + cur.h * p.c.v_head;
+    const uint8_t* ksbase = p.s.k + cur.h * p.s.k_head;
+    const uint8_t* vsbase = p.s.v + cur.h * p.s.v_head;
+
+    auto tile = [&](int j) { return cur.template tile<true>(k0 + j); };   // the CTA's tile number j of the item
+    // page id of this lane's key of tile j (-1: nothing to read)
+    auto page_of = [&](int j) -> int {
+      const int key = tile(j) * BN + warp * WK + lane;
+      if (j >= len || (key < lo && key >= p.sinks) || key >= hi) return -1;   // also what lies before the window
+      const int pg = __ldg(table + key / P);
+      if (pg < 0 || pg >= p.c.pages) {
+        atomicOr(p.status, kStatusPageRange);
+        return -1;
+      }
+      return pg;
+    };
+    // copies of tile j, whose page ids are there
+    auto load_tile = [&](int j, int pg) {
+      if (j < len) {
+        const uint32_t st = ring + j % STAGES * Geo::kStage;
+        const int in = (tile(j) * BN + warp * WK + lane) % P;
+        const bool has = pg >= 0;
+        const unsigned there = __ballot_sync(0xffffffffu, has);
+        const long long pl = has ? pg : 0;
+        const long long ko = pl * p.c.k_page + in * p.c.k_token, vo = pl * p.c.v_page + in * p.c.v_token;
+        const uint8_t* ks = ksbase + (has ? pl * p.s.k_page + in * p.s.k_token : 0);
+        const uint8_t* vs = vsbase + (has ? pl * p.s.v_page + in * p.s.v_token : 0);
+        const uint32_t dks = st + 2 * Geo::kCodes + lane * Geo::kScale, dvs = dks + Geo::kScales;
+        if (p.s.whole) {
+          constexpr int CH = DP / 32;        // 16-byte pieces of a key
+#pragma unroll
+          for (int i = 0; i < CH; ++i) {
+            const int r = i * (32 / CH) + lane / CH, c = lane % CH;
+            const bool ok = there >> r & 1;
+            const long long k_at = shfl64(ko, r), v_at = shfl64(vo, r);
+            cp_async16(st + fp4_k_piece<DP>(r, c), ok ? kbase + k_at + c * 16 : kbase, ok);
+            cp_async16(st + Geo::kCodes + fp4_v_piece<DP>(r, c), ok ? vbase + v_at + c * 16 : vbase, ok);
+          }
+          cp_async_some<Geo::kScale>(dks, ks, has);
+          cp_async_some<Geo::kScale>(dvs, vs, has);
+        } else {                             // heads that are not DP values long, or looser alignment: 8 bytes, scales one by one
+          for (int c = 0; c < DP / 16; ++c) {
+            const bool ok = has && c * 16 < D;
+            cp_async_some<8>(st + fp4_k_piece<DP>(lane, c >> 1) + (c & 1) * 8, ok ? kbase + ko + c * 8 : kbase, ok);
+            cp_async_some<8>(st + Geo::kCodes + fp4_v_piece<DP>(lane, c >> 1) + (c & 1) * 8, ok ? vbase + vo + c * 8 : vbase, ok);
+            const uint32_t a = ok ? __ldg(ks + c) : 0u, b = ok ? __ldg(vs + c) : 0u;
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(dks + c), "r"(a) : "memory");
+            asm volatile("st.shared.u8 [%0], %1;" ::"r"(dvs + c), "r"(b) : "memory");
+          }
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    // the first tiles' copies
+    int pg_next;
+    {
+      int pg[STAGES];
+#pragma unroll
+      for (int j = 0; j < STAGES; ++j) pg[j] = page_of(j);
+#pragma unroll
+      for (int j = 0; j < STAGES - 1; ++j) load_tile(j, pg[j]);
+      pg_next = pg[STAGES - 1];
+    }
+
+    // query fragments of rows g and g + 8: step s takes this lane's values 4 s .. 4 s + 3
+    uint32_t qf[DP / 16][4];
+    float factor[2];   // of the scores: softmax scale, the keys' unit, the queries' power of two
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + g + i * 8;
+      const uint8_t* q = nullptr;
+      if (r < r1) {
+        const int tok = attn_token(p, r);
+        q = p.q + ((cur.req.q0 + tok) * p.q_token + (cur.h * p.G + r - tok * p.G) * p.q_head) * 2;
+      }
+      float top = 0.f;
+#pragma unroll
+      for (int w = 0; w < WORDS; ++w) {
+        const int d = DP == 64 ? t * 16 + w * 8 : (w / 4) * 128 + t * 32 + (w % 4) * 8;
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (q && d < D) x = __ldg(reinterpret_cast<const uint4*>(q + d * 2));
+        qf[2 * w][i] = x.x;
+        qf[2 * w][2 + i] = x.y;
+        qf[2 * w + 1][i] = x.z;
+        qf[2 * w + 1][2 + i] = x.w;
+        if (BF16) {
+          const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
+        }
+      }
+      factor[i] = p.scale_log2;
+      if (BF16) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int e = max(1, min(static_cast<int>(__float_as_uint(top) >> 23), 253));   // 2^(e - 127) <= top < twice that
+        const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 1.f;
+        factor[i] *= top > 0.f ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 1.f;
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint32_t x = qf[s][2 * h + i];
+            qf[s][2 * h + i] = H::pack(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
+          }
+      }
+    }
+    // key range of this lane's two rows
+    int row_lo[2], row_hi[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int r = r0 + g + i * 8;
+      row_lo[i] = 0;
+      row_hi[i] = 0;
+      if (r < r1) attn_keys(p, cur.req, r, r + 1, &row_lo[i], &row_hi[i]);
+    }
+    // keys inside [w_lo, w_hi) need no mask for any row of the tile (rows that do not exist are not written)
+    const int w_hi = __reduce_min_sync(0xffffffffu, min(r0 + g < r1 ? row_hi[0] : 0x7fffffff, r0 + g + 8 < r1 ? row_hi[1] : 0x7fffffff));
+    const int w_lo = __reduce_max_sync(0xffffffffu, max(row_lo[0], row_lo[1]));
+
+    float o[DT][4];
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
+    float m[2] = {ninf(), ninf()}, l[2] = {0.f, 0.f};   // reference so far, sum of 2^(s - reference + shift)
+
+    for (int j = 0; j < len; ++j) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
+      __syncwarp();
+      load_tile(j + STAGES - 1, pg_next);
+      pg_next = page_of(j + STAGES);
+      const uint32_t sk = ring + j % STAGES * Geo::kStage, sv_ = sk + Geo::kCodes;
+      const uint32_t sks = sk + 2 * Geo::kCodes, svs = sks + Geo::kScales;
+
+      // S = Q K^T: 16 rows x this warp's 32 keys
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
+        const int r = n * 8 + g;
+        uint32_t w[WORDS], sc[DP == 256 ? 2 : 1];
+        if constexpr (DP == 64) {
+          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(sk + fp4_k_piece<DP>(r, t >> 1) + (t & 1) * 8));
+          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc[0]) : "r"(sks + r * Geo::kScale + t));
+        } else {
+#pragma unroll
+          for (int h = 0; h < DP / 128; ++h) {
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
+                         : "r"(sk + fp4_k_piece<DP>(r, h * 4 + t)));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc[h]) : "r"(sks + r * Geo::kScale + h * 8 + t * 2));
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < WORDS; ++i) {
+          // the scale of this word's block, twice
+          const uint32_t two = fp4_scales(sc[i / 4]);
+          const uint32_t f = DP == 64 || i % 4 < 2 ? __byte_perm(two, two, 0x1010) : __byte_perm(two, two, 0x3232);
+          uint32_t b[4];
+          fp4_pairs(w[i], b);
+          H::mma(s[n], qf[2 * i], mul2(b[0], f), mul2(b[1], f));
+          H::mma(s[n], qf[2 * i + 1], mul2(b[2], f), mul2(b[3], f));
+        }
+      }
+
+      // masks, reference and sum
+      const int key0 = tile(j) * BN + warp * WK;
+      float mx[2] = {m[0], m[1]};
+      const bool masked = key0 + WK > w_hi || key0 < w_lo;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x = s[n][e] * factor[e >> 1];
+          if (masked) {
+            const int key = key0 + n * 8 + t * 2 + (e & 1), i = e >> 1;
+            x = (key >= row_lo[i] || key < p.sinks) && key < row_hi[i] ? x : ninf();
+          }
+          s[n][e] = x;
+          mx[e >> 1] = fmaxf(mx[e >> 1], x);
+        }
+      bool grow = false;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
+        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
+        grow = grow || mx[i] - m[i] > kFp4Grow || (m[i] == ninf() && mx[i] > m[i]);
+      }
+      if (__any_sync(0xffffffffu, grow)) {   // the first keys, or a maximum that has outgrown the reference
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const float f = ex2(m[i] - (mx[i] == ninf() ? 0.f : mx[i]));
+          l[i] *= f;
+          m[i] = mx[i];
+#pragma unroll
+          for (int d = 0; d < DT; ++d) {
+            o[d][2 * i] *= f;
+            o[d][2 * i + 1] *= f;
+          }
+        }
+      }
+      const float ref[2] = {(m[0] == ninf() ? 0.f : m[0]) - kFp4Shift, (m[1] == ninf() ? 0.f : m[1]) - kFp4Shift};
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = ex2(s[n][e] - ref[e >> 1]);
+          l[e >> 1] += s[n][e];
+        }
+
+      // O += P V
+#pragma unroll
+      for (int k = 0; k < WK / 16; ++k) {
+        const uint32_t a[4] = {H::pack(s[2 * k][0], s[2 * k][1]), H::pack(s[2 * k][2], s[2 * k][3]),
+                               H::pack(s[2 * k + 1][0], s[2 * k + 1][1]), H::pack(s[2 * k + 1][2], s[2 * k + 1][3])};
+        constexpr int VW = DP / 64;   // words of 8 codes of a key that are this lane's columns
+        uint32_t w[4][VW], f[2][DP == 256 ? 2 : 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = k * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+          if constexpr (DP == 64)
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i][0]) : "r"(sv_ + fp4_v_piece<DP>(r, g >> 2) + (g & 3) * 4));
+          else if constexpr (DP == 128)
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(sv_ + fp4_v_piece<DP>(r, g >> 1) + (g & 1) * 8));
+          else
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                         : "r"(sv_ + fp4_v_piece<DP>(r, g)));
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {   // scales of the keys 2 t + 8 i and the next one
+          const uint32_t at = svs + (k * 16 + 2 * t + 8 * i) * Geo::kScale;
+          uint32_t x, y;
+          if constexpr (DP == 256) {
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(at + g * 2));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(y) : "r"(at + Geo::kScale + g * 2));
+            f[i][0] = fp4_scales(__byte_perm(x, y, 0x0040));
+            f[i][1] = fp4_scales(__byte_perm(x, y, 0x0051));
+          } else {
+            const int blk = DP == 64 ? g >> 1 : g;
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at + blk));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(y) : "r"(at + Geo::kScale + blk));
+            f[i][0] = fp4_scales(x | y << 8);
+          }
+        }
+#pragma unroll
+        for (int v = 0; v < VW; ++v) {
+          const int blk = DP == 256 ? v / 2 : 0;
+          uint32_t even[2][4], odd[2][4];   // columns 0, 2, 4, 6 and 1, 3, 5, 7 of the word, pairs of keys
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t x = w[2 * i][v], y = w[2 * i + 1][v];
+            fp4_pairs((x & 0x0f0f0f0fu) | ((y << 4) & 0xf0f0f0f0u), even[i]);
+            fp4_pairs(((x >> 4) & 0x0f0f0f0fu) | (y & 0xf0f0f0f0u), odd[i]);
+          }
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            H::mma(o[v * 8 + 2 * c], a, mul2(even[0][c], f[0][blk]), mul2(even[1][c], f[1][blk]));
+            H::mma(o[v * 8 + 2 * c + 1], a, mul2(odd[0][c], f[0][blk]), mul2(odd[1][c], f[1][blk]));
+          }
+        }
+      }
+      __syncwarp();   // every lane has read the tile before its slot is filled again
+    }
+
+    // join the warps' shares of the keys and write the rows
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
+      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
+      const int r = g + i * 8;
+      if (t == 0) {
+        s_ml[warp][r][0] = m[i] - kFp4Shift;
+        s_ml[warp][r][1] = l[i];
+      }
+      // column c of an 8-column product is value c DT + its number
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int d = 0; d < DT; d += 4)
+          *reinterpret_cast<float4*>(s_o + (warp * BM + r) * DP + (2 * t + c) * DT + d) =
+              make_float4(o[d][2 * i + c], o[d + 1][2 * i + c], o[d + 2][2 * i + c], o[d + 3][2 * i + c]);
+    }
+    __syncthreads();
+    const bool whole = len == cur.count;
+    const int slot = 2 * cta + (later ? 1 : 0);
+    for (int id = tid; id < BM * (DP / 4); id += kAttnThreads) {
+      const int r = id / (DP / 4), d = (id % (DP / 4)) * 4;
+      if (r0 + r >= r1 || d >= D) continue;
+      float mm = ninf();
+#pragma unroll
+      for (int w = 0; w < 4; ++w) mm = fmaxf(mm, s_ml[w][r][0]);
+      const float ref = mm == ninf() ? 0.f : mm;
+      float ll = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const float f = ex2(s_ml[w][r][0] - ref);
+        ll += f * s_ml[w][r][1];
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (w * BM + r) * DP + d);
+        acc.x += f * x.x;
+        acc.y += f * x.y;
+        acc.z += f * x.z;
+        acc.w += f * x.w;
+      }
+      if (whole) {
+        const float inv = ll > 0.f ? p.v_unit / ll : 0.f;
+        const int tok = attn_token(p, r0 + r);
+        const long long row = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r0 + r - tok * p.G);
+        *reinterpret_cast<uint2*>(p.out + (row * D + d) * 2) =
+            make_uint2(A::pack(acc.x * inv, acc.y * inv), A::pack(acc.z * inv, acc.w * inv));
+        if (d == 0 && p.lse) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : ninf();
+      } else {
+        const long long row = static_cast<long long>(slot) * BM + r;
+        *reinterpret_cast<float4*>(p.part_o + row * D + d) = acc;
+        if (d == 0) *reinterpret_cast<float2*>(p.part_ml + row * 2) = make_float2(mm, ll);
+      }
+    }
+    AttnCursor next = cur;
+    if (!attn_next<BN, true>(p, BM, u_end, &next)) {
+      if (tid == 0) attn_leave_join(p, split, cta, BM, &cur, later);
+      break;
+    }
+    cur = next;
+    cur.share(p, u_begin, u_end, &k0, &k1);
+    later = true;
+    __syncthreads();
+  }
+}
+
+template <bool BF16>
+const void* attn_fp4_fn(int dp);
+inline int attn_fp4_smem(int dp) {
+  const int ring = dp == 64 ? AttnFp4Geom<64>::kSmem : dp == 128 ? AttnFp4Geom<128>::kSmem : AttnFp4Geom<256>::kSmem;
+  return ring > 4 * 16 * dp * 4 ? ring : 4 * 16 * dp * 4;
+}
+
+}  // namespace sv

@@ -1,0 +1,13 @@
+// f16 instances of the attention over 4-bit caches.
+#include "attention_fp4.cuh"
+
+namespace sv {
+
+template <>
+const void* attn_fp4_fn<false>(int dp) {
+  return dp == 64    ? reinterpret_cast<const void*>(&attn_fp4_kernel<false, 64>)
+         : dp == 128 ? reinterpret_cast<const void*>(&attn_fp4_kernel<false, 128>)
+                     : reinterpret_cast<const void*>(&attn_fp4_kernel<false, 256>);
+}
+
+}  // namespace sv

@@ -94,7 +94,7 @@ struct AttnMmaGeom {
   static constexpr int kSmem = kStages * 2 * kTile + kQBytes + kRing * kAttnBN * 16;
 };
 
-template <bool BF16, int DP, int WM>
+template <bool BF16, int DP, int WM, bool SINKS>
 __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams p) {
   using A = AttnType<BF16>;
   using Geo = AttnMmaGeom<DP, WM>;
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int wm = warp / WN, wn = warp % WN;
-  const AttnSplit split = attn_split<BN>(p, BM, sched);
+  const AttnSplit split = attn_split<BN, SINKS>(p, BM, sched);
   const int cta = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;");
   if (cta >= split.n) {
@@ -118,7 +118,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
     return;
   }
   const long long u_begin = split.begin(cta), u_end = split.begin(cta + 1);
-  AttnCursor cur = attn_locate<BN>(p, BM, u_begin, sched);
+  AttnCursor cur = attn_locate<BN, SINKS>(p, BM, u_begin, sched);
   int k0, k1;
   cur.share(p, u_begin, u_end, &k0, &k1);
   if (k1 <= k0) {   // nothing but an item's overhead
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
   const int D = p.c.D, P = p.c.page_size;
 
   while (true) {
-    const int kt0 = cur.first + k0, len = k1 - k0;
+    const int len = k1 - k0;
     const int rows = cur.req.nq * p.G, r0 = cur.t * BM, r1 = min(rows, r0 + BM);
     int lo, hi;
     attn_keys(p, cur.req, r0, r1, &lo, &hi);
@@ -138,10 +138,12 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
     const uint8_t* kbase = p.c.k + static_cast<long long>(cur.h) * p.c.k_head * 2;
     const uint8_t* vbase = p.c.v + static_cast<long long>(cur.h) * p.c.v_head * 2;
 
+    auto tile = [&](int j) { return cur.template tile<SINKS>(k0 + j); };   // the CTA's tile number j of the item
     // page id of this thread's key of tile j (-1: nothing to read)
     auto page_of = [&](int j) -> int {
-      const int key = (kt0 + j) * BN + (tid & (BN - 1));
-      if (j >= len || key < lo || key >= hi) return -1;   // also of the first tile what lies before the window
+      const int key = tile(j) * BN + (tid & (BN - 1));
+      // also of the first tile what lies before the window
+      if (j >= len || (key < lo && !(SINKS && key < p.sinks)) || key >= hi) return -1;
       const int pg = __ldg(table + key / P);
       if (pg < 0 || pg >= p.c.pages) {
         atomicOr(p.status, kStatusPageRange);
@@ -150,7 +152,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
       return pg;
     };
     auto put_offset = [&](int j, int pg) {
-      const int key = (kt0 + j) * BN + (tid & (BN - 1));
+      const int key = tile(j) * BN + (tid & (BN - 1));
       const int in = key % P;
       longlong2 o = make_longlong2(-1, -1);
       if (pg >= 0)
@@ -265,14 +267,14 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
       }
 
       // masks, running maximum and sum
-      const int kb = (kt0 + j) * BN + wn * KPW + (lane & 3) * 2;
+      const int kb = tile(j) * BN + wn * KPW + (lane & 3) * 2;
       float mx[2] = {m[0], m[1]};
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int key = kb + n * 8 + (e & 1), i = e >> 1;
-          const float x = key >= row_lo[i] && key < row_hi[i] ? s[n][e] * p.scale_log2 : ninf();
+          const float x = (key >= row_lo[i] || (SINKS && key < p.sinks)) && key < row_hi[i] ? s[n][e] * p.scale_log2 : ninf();
           s[n][e] = x;
           mx[i] = fmaxf(mx[i], x);
         }
@@ -368,7 +370,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
       }
     }
     AttnCursor next = cur;
-    if (!attn_next<BN>(p, BM, u_end, &next)) {
+    if (!attn_next<BN, SINKS>(p, BM, u_end, &next)) {
       if (tid == 0) attn_leave_join(p, split, cta, BM, &cur, later);
       break;
     }
@@ -379,7 +381,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool SINKS>
 const void* attn_mma_fn(int dp, int bm);
 template <bool BF16>
 int attn_mma_smem(int dp, int bm) {

@@ -4,14 +4,14 @@
 namespace sv {
 
 template <>
-const void* attn_mma_fn<false>(int dp, int bm) {
+const void* attn_mma_fn<false, false>(int dp, int bm) {
   if (bm == 16)
-    return dp == 64    ? reinterpret_cast<const void*>(&attn_mma_kernel<false, 64, 1>)
-           : dp == 128 ? reinterpret_cast<const void*>(&attn_mma_kernel<false, 128, 1>)
-                       : reinterpret_cast<const void*>(&attn_mma_kernel<false, 256, 1>);
-  return dp == 64    ? reinterpret_cast<const void*>(&attn_mma_kernel<false, 64, 4>)
-         : dp == 128 ? reinterpret_cast<const void*>(&attn_mma_kernel<false, 128, 4>)
-                     : reinterpret_cast<const void*>(&attn_mma_kernel<false, 256, 4>);
+    return dp == 64    ? reinterpret_cast<const void*>(&attn_mma_kernel<false, 64, 1, false>)
+           : dp == 128 ? reinterpret_cast<const void*>(&attn_mma_kernel<false, 128, 1, false>)
+                       : reinterpret_cast<const void*>(&attn_mma_kernel<false, 256, 1, false>);
+  return dp == 64    ? reinterpret_cast<const void*>(&attn_mma_kernel<false, 64, 4, false>)
+         : dp == 128 ? reinterpret_cast<const void*>(&attn_mma_kernel<false, 128, 4, false>)
+                     : reinterpret_cast<const void*>(&attn_mma_kernel<false, 256, 4, false>);
 }
 
 }  // namespace sv

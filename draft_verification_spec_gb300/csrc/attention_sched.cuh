@@ -50,14 +50,17 @@ __device__ __forceinline__ void attn_keys(const AttnParams& p, const AttnReq& r,
     *lo = w > 0 ? static_cast<int>(min(w, static_cast<long long>(r.kv))) : 0;
   }
 }
-// First key tile and number of key tiles of row tile t (an item has one at least: its rows are
-// written even where they see no key).
-template <int BN>
-__device__ __forceinline__ int attn_tiles(const AttnParams& p, const AttnReq& r, int t, int bm, int* first) {
+// Number of key tiles of row tile t (an item has one at least: its rows are written even where they see no
+// key).  They are the first `front` ones, which hold the first tokens that stay visible (SINKS), and those from
+// `first` on, where the window begins; the tiles between the two are not looked at.
+template <int BN, bool SINKS>
+__device__ __forceinline__ int attn_tiles(const AttnParams& p, const AttnReq& r, int t, int bm, int* first, int* front) {
   const int r0 = t * bm, r1 = min(r.nq * p.G, r0 + bm);
   int lo, hi;
   attn_keys(p, r, r0, r1, &lo, &hi);
   *first = lo / BN;
+  *front = SINKS ? min((min(p.sinks, hi) + BN - 1) / BN, *first) : 0;
+  if (SINKS) return max(*front + max((hi + BN - 1) / BN - *first, 0), 1);
   return max((hi + BN - 1) / BN - *first, 1);
 }
 __device__ __forceinline__ int attn_row_tiles(const AttnParams& p, const AttnReq& r, int bm) {
@@ -65,7 +68,7 @@ __device__ __forceinline__ int attn_row_tiles(const AttnParams& p, const AttnReq
 }
 // Units of request b, all key heads; the request's lanes (p.lanes, a power of two: one where a request is
 // one row tile) share the row tiles, and every one of them gets the sum.
-template <int BN>
+template <int BN, bool SINKS>
 __device__ __forceinline__ long long attn_request_units(const AttnParams& p, int b, int bm) {
   long long n = 0;
   if (b < p.c.B) {
@@ -73,8 +76,8 @@ __device__ __forceinline__ long long attn_request_units(const AttnParams& p, int
     if (r.nq > 0 && r.at + r.nq > r.kv && blockIdx.x == 0) atomicOr(p.status, kStatusPageRange);   // positions beyond the table
     const int nt = attn_row_tiles(p, r, bm);
     for (int t = threadIdx.x & (p.lanes - 1); t < nt; t += p.lanes) {
-      int first;
-      n += p.overhead + attn_tiles<BN>(p, r, t, bm, &first);
+      int first, front;
+      n += p.overhead + attn_tiles<BN, SINKS>(p, r, t, bm, &first, &front);
     }
   }
   for (int o = p.lanes / 2; o; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
@@ -92,8 +95,18 @@ struct AttnSplit {
 struct AttnCursor {
   int b, h, t;
   AttnReq req;
-  int first, count;
+  int first, front, count;
   long long start;
+  // Its key tile number j; the first number whose tile is `tile` or behind it.
+  template <bool SINKS>
+  __device__ __forceinline__ int tile(int j) const {
+    return SINKS && j < front ? j : first + j - front;
+  }
+  template <bool SINKS>
+  __device__ __forceinline__ int number(int tile) const {
+    if (!SINKS) return tile - first;
+    return tile < front ? tile : front + max(tile - first, 0);
+  }
   // The key tiles [k0, k1) of the item in the run [begin, end) of a CTA (none if k1 <= k0).
   __device__ __forceinline__ void share(const AttnParams& p, long long begin, long long end, int* k0, int* k1) const {
     const long long t = start + p.overhead;
@@ -110,12 +123,12 @@ struct AttnSchedSmem {
 };
 
 // Block-wide: the units of the call and how many CTAs share them.
-template <int BN, int THREADS>
+template <int BN, bool SINKS, int THREADS>
 __device__ __forceinline__ AttnSplit attn_split(const AttnParams& p, int bm, AttnSchedSmem<THREADS>& s) {
   const int per = THREADS / p.lanes;   // requests at a time (THREADS is a multiple of 32, lanes at most 32)
   long long mine = 0;
   for (int base = 0; base < p.c.B; base += per) {
-    const long long n = attn_request_units<BN>(p, base + threadIdx.x / p.lanes, bm);
+    const long long n = attn_request_units<BN, SINKS>(p, base + threadIdx.x / p.lanes, bm);
     if ((threadIdx.x & (p.lanes - 1)) == 0) mine += n;
   }
 #pragma unroll
@@ -133,13 +146,13 @@ __device__ __forceinline__ AttnSplit attn_split(const AttnParams& p, int bm, Att
 }
 
 // Block-wide: the item that unit u belongs to (u < total).
-template <int BN, int THREADS>
+template <int BN, bool SINKS, int THREADS>
 __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, long long u, AttnSchedSmem<THREADS>& s) {
   const int lane = threadIdx.x & 31, w = threadIdx.x / 32, per = THREADS / p.lanes;
   long long before = 0;   // units of the requests before this step's
   for (int base = 0; base < p.c.B; base += per) {
     const int b = base + threadIdx.x / p.lanes;
-    const long long units = attn_request_units<BN>(p, b, bm);
+    const long long units = attn_request_units<BN, SINKS>(p, b, bm);
     const long long mine = (threadIdx.x & (p.lanes - 1)) == 0 ? units : 0;
     long long incl = mine;
 #pragma unroll
@@ -174,8 +187,8 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
   // the row tile: 32 at a time, every warp for itself
   const int nt = attn_row_tiles(p, c.req, bm);
   for (int t0 = 0; t0 < nt; t0 += 32) {
-    int first = 0;
-    const long long mine = t0 + lane < nt ? p.overhead + attn_tiles<BN>(p, c.req, t0 + lane, bm, &first) : 0;
+    int first = 0, front = 0;
+    const long long mine = t0 + lane < nt ? p.overhead + attn_tiles<BN, SINKS>(p, c.req, t0 + lane, bm, &first, &front) : 0;
     long long incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -188,6 +201,7 @@ __device__ __forceinline__ AttnCursor attn_locate(const AttnParams& p, int bm, l
       c.t = t0 + k;
       c.count = static_cast<int>(__shfl_sync(0xffffffffu, mine, k)) - p.overhead;
       c.first = __shfl_sync(0xffffffffu, first, k);
+      c.front = SINKS ? __shfl_sync(0xffffffffu, front, k) : 0;
       c.start = u - (rem - __shfl_sync(0xffffffffu, incl - mine, k));
       break;
     }
@@ -218,7 +232,7 @@ __device__ __forceinline__ void attn_leave_join(const AttnParams& p, const AttnS
 }
 
 // The next item with key tiles in a run that ends at `end`; false if there is none.
-template <int BN>
+template <int BN, bool SINKS>
 __device__ __forceinline__ bool attn_next(const AttnParams& p, int bm, long long end, AttnCursor* c) {
   c->start += p.overhead + c->count;
   if (c->start + p.overhead >= end) return false;
@@ -231,7 +245,7 @@ __device__ __forceinline__ bool attn_next(const AttnParams& p, int bm, long long
       } while (c->req.nq == 0);
     }
   }
-  c->count = attn_tiles<BN>(p, c->req, c->t, bm, &c->first);
+  c->count = attn_tiles<BN, SINKS>(p, c->req, c->t, bm, &c->first, &c->front);
   return true;
 }
 

@@ -197,7 +197,7 @@ struct TcWait {
   }
 };
 
-template <bool BF16, int DP, bool WIDE>
+template <bool BF16, int DP, bool WIDE, bool SINKS>
 __global__ void __launch_bounds__(kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   using A = AttnType<BF16>;
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const uint32_t base = (smem_addr(smem_raw) + 1023u) & ~1023u;
   const uint32_t s_q = base, s_k = base + (BM / 128) * TILE, s_v = s_k + KST * TILE;
 
-  const AttnSplit split = attn_split<BN>(p, BM, sched);
+  const AttnSplit split = attn_split<BN, SINKS>(p, BM, sched);
   const int cta = blockIdx.x;
   asm volatile("griddepcontrol.launch_dependents;");
   if (cta >= split.n) {
@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     return;
   }
   const long long u_begin = split.begin(cta), u_end = split.begin(cta + 1);
-  AttnCursor cur = attn_locate<BN>(p, BM, u_begin, sched);
+  AttnCursor cur = attn_locate<BN, SINKS>(p, BM, u_begin, sched);
   int k0, k1;   // the item's key tiles that are this CTA's
   cur.share(p, u_begin, u_end, &k0, &k1);
   if (k1 <= k0) {   // nothing but an item's overhead
@@ -272,16 +272,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // without a limit the first wait gives up at once; the other warps, whose tiles never come, follow
     bool ok = p.wait_limit > 0 || wait.give_up();
     while (ok) {
-      const int kt0 = cur.first + k0, len = k1 - k0;
+      const int len = k1 - k0;
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
       int lo, hi;
       attn_keys(p, cur.req, r0, r1, &lo, &hi);
       const int32_t* table = p.c.table + static_cast<long long>(cur.b) * p.c.table_stride;
       for (int j = 0; ok && j < len; ++j, ++g) {
         // this lane's boxes: page `i` of the tile (i = lane: at most 16 pages of 8 tokens and more)
-        const int key = (kt0 + j) * BN + lane * rows;
+        const int kt = cur.template tile<SINKS>(k0 + j), key = kt * BN + lane * rows;
         int pg = p.c.pages;   // out of range: zeros.  So too what lies wholly before the window: its page may be gone
-        if (lane < boxes && key < hi && key + rows > lo) {
+        if (lane < boxes && key < hi && (key + rows > lo || (SINKS && key < p.sinks))) {
           pg = __ldg(table + key / P);
           if (pg < 0 || pg >= p.c.pages) {
             atomicOr(p.status, kStatusPageRange);
@@ -305,10 +305,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             for (int s = 0; s < SUB; ++s) tma_box(dst + s * 128 * 128, which ? &map_v : &map_k, s * 64, tok, cur.h, pg, full);
           }
           __syncwarp();
-          if (which && (kt0 + j + 1) * BN > hi) mbar_arrive_warp(smem_addr(&bars.clean_me[st]));
+          if (which && (kt + 1) * BN > hi) mbar_arrive_warp(smem_addr(&bars.clean_me[st]));
         }
       }
-      if (!attn_next<BN>(p, BM, u_end, &cur)) break;
+      if (!attn_next<BN, SINKS>(p, BM, u_end, &cur)) break;
       cur.share(p, u_begin, u_end, &k0, &k1);
     }
     issued = g;
@@ -365,12 +365,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         return true;
       };
       while (ok) {
-        const int kt0 = cur.first + k0, len = k1 - k0;
+        const int len = k1 - k0;
         const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
         const bool joined = r1 - r0 <= 128;
         int lo, hi;
         attn_keys(p, cur.req, r0, r1, &lo, &hi);
-        const int clean_from = hi / BN - kt0;   // tiles from here on end behind the item's last key
+        const int clean_from = cur.template number<SINKS>(hi / BN) - k0;   // tiles from here on end behind the item's last key
         for (int h = 0; ok && h < (joined ? 1 : 2); ++h) {
           ok = wait(smem_addr(&bars.q_full[h]), q_phase >> h & 1);
           q_phase ^= 1u << h;
@@ -416,7 +416,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
             next_k();
           }
         }
-        if (!ok || !attn_next<BN>(p, BM, u_end, &cur)) break;
+        if (!ok || !attn_next<BN, SINKS>(p, BM, u_end, &cur)) break;
         cur.share(p, u_begin, u_end, &k0, &k1);
       }
       if (!ok) {   // gave up: the MMAs in flight finish before TMEM is freed
@@ -434,17 +434,17 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     unsigned g = 0, asked = 0;   // phases of clean_me, a bit per slot
     bool ok = true;
     while (ok) {
-      const int kt0 = cur.first + k0, len = k1 - k0;
+      const int len = k1 - k0;
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
       int lo, hi;
       attn_keys(p, cur.req, r0, r1, &lo, &hi);
-      for (int j = max(hi / BN - kt0, 0); ok && j < len; ++j) {
+      for (int j = max(cur.template number<SINKS>(hi / BN) - k0, 0); ok && j < len; ++j) {
         const unsigned t = g + j, st = t % VST;
         ok = wait.warp(smem_addr(&bars.clean_me[st]), asked >> st & 1);
         asked ^= 1u << st;
         if (ok) ok = wait.warp(smem_addr(&bars.v_full[st]), (t / VST) & 1);
         if (!ok) break;
-        const int valid = max(hi - (kt0 + j) * BN, 0);
+        const int valid = max(hi - cur.template tile<SINKS>(k0 + j) * BN, 0);
         for (int i = valid * 8 + lane; i < BN * 8; i += 32)
 #pragma unroll
           for (int s = 0; s < SUB; ++s)
@@ -453,7 +453,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         mbar_arrive_warp(smem_addr(&bars.v_clean[st]));
       }
       g += len;
-      if (!attn_next<BN>(p, BM, u_end, &cur)) break;
+      if (!attn_next<BN, SINKS>(p, BM, u_end, &cur)) break;
       cur.share(p, u_begin, u_end, &k0, &k1);
     }
   } else {
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     bool later = false;             // not the CTA's first item
     bool ok = true, owed = false;   // owed: half 0 may still read this half's O and statistics
     while (ok) {
-      const int kt0 = cur.first + k0, len = k1 - k0;
+      const int len = k1 - k0;
       const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
       const bool joined = r1 - r0 <= 128;
       const int h0 = r0 + (joined ? 0 : half * 128), r = h0 + row;
@@ -508,8 +508,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           // One pass over the scores, 32 columns at a time with the next ones in flight: maximum,
           // exponentials against the reference so far, their sum.  Only where the maximum has outgrown
           // the reference (always in an item's first tile) the pass is done again with the new one.
-          const int k0 = (kt0 + j) * BN, lo = row_lo - k0, hi = row_hi - k0;
-          const bool masked = k0 + BN > w_hi || k0 < w_lo;
+          const int key0 = cur.template tile<SINKS>(k0 + j) * BN, lo = row_lo - key0, hi = row_hi - key0;
+          const int sinks = SINKS ? p.sinks - key0 : 0;
+          const bool masked = key0 + BN > w_hi || key0 < w_lo;
           const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
           uint32_t pk[64];
           while (true) {
@@ -526,7 +527,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
               if (c < 3) tc_ld32(t_s + (c + 1) * 32, s[(c + 1) & 1]);
               if (masked) {
 #pragma unroll
-                for (int i = 0; i < 32; ++i) x[i] = c * 32 + i >= lo && c * 32 + i < hi ? x[i] : 0xff800000u;
+                for (int i = 0; i < 32; ++i)
+                  x[i] = (c * 32 + i >= lo || (SINKS && c * 32 + i < sinks)) && c * 32 + i < hi ? x[i] : 0xff800000u;
               }
 #pragma unroll
               for (int i = 0; i < 16; ++i) {
@@ -647,7 +649,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         if (joined) mbar_arrive_warp(smem_addr(&bars.x_free));
       }
       AttnCursor next = cur;
-      if (!attn_next<BN>(p, BM, u_end, &next)) {
+      if (!attn_next<BN, SINKS>(p, BM, u_end, &next)) {
         if (tid == 0) attn_leave_join(p, split, cta, BM, &cur, later);
         break;
       }
@@ -672,7 +674,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
 }
 
-template <bool BF16>
+template <bool BF16, bool SINKS>
 const void* attn_tc_fn(int dp, bool wide);
 
 }  // namespace sv

@@ -1,0 +1,15 @@
+// bf16 instances of the tcgen05 attention kernel with first tokens that stay visible.
+#include "attention_tc.cuh"
+
+namespace sv {
+
+template <>
+const void* attn_tc_fn<true, true>(int dp, bool wide) {
+  if (wide)
+    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, true, true>)
+                    : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, true, true>);
+  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, false, true>)
+                  : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, false, true>);
+}
+
+}  // namespace sv

@@ -4,12 +4,12 @@
 namespace sv {
 
 template <>
-const void* attn_tc_fn<false>(int dp, bool wide) {
+const void* attn_tc_fn<false, false>(int dp, bool wide) {
   if (wide)
-    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<false, 64, true>)
-                    : reinterpret_cast<const void*>(&attn_tc_kernel<false, 128, true>);
-  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<false, 64, false>)
-                  : reinterpret_cast<const void*>(&attn_tc_kernel<false, 128, false>);
+    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<false, 64, true, false>)
+                    : reinterpret_cast<const void*>(&attn_tc_kernel<false, 128, true, false>);
+  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<false, 64, false, false>)
+                  : reinterpret_cast<const void*>(&attn_tc_kernel<false, 128, false, false>);
 }
 
 }  // namespace sv

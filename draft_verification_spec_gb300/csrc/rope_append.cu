@@ -7,46 +7,11 @@
 // is one 64-bit product: whole turns fall out by the wrap.  The frequencies are rounded from 64-bit floating
 // point, which at a position of 10^6 leaves the phase exact to 2^-35 of a turn, where an fp32 product would
 // have lost all but four bits of it.
-#include "spec_device.cuh"
-#include "step_internal.h"
-
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
+#include "rope_device.cuh"
 
 namespace sv {
 
 namespace {
-
-constexpr int kRopeThreads = 128;
-
-template <int DTYPE>
-struct RopeType;
-template <>
-struct RopeType<0> {
-  using T = float;
-};
-template <>
-struct RopeType<1> {
-  using T = __nv_bfloat16;
-};
-template <>
-struct RopeType<2> {
-  using T = __half;
-};
-__device__ __forceinline__ float to_f(float x) { return x; }
-__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
-__device__ __forceinline__ void from_f(float x, float* y) { *y = x; }
-__device__ __forceinline__ void from_f(float x, __nv_bfloat16* y) { *y = __float2bfloat16_rn(x); }
-__device__ __forceinline__ void from_f(float x, __half* y) { *y = __float2half_rn(x); }
-
-// cos and sin of 2 pi phase / 2^64.
-__device__ __forceinline__ float2 phase_cs(unsigned long long phase) {
-  const float half_turns = static_cast<float>(static_cast<int>(phase >> 32)) * 4.656612873077393e-10f;   // 2^-31
-  float s, c;
-  sincospif(half_turns, &s, &c);
-  return make_float2(c, s);
-}
 
 // Any size, alignment and stride: one CTA per token: the token's request and cache slot, its r/2 angles in shared
 // memory, then every head's values, 1 pair (or 1 value behind the rotated part) per thread and step.
@@ -121,20 +86,6 @@ __global__ void __launch_bounds__(kRopeThreads) rope_scalar_kernel(const RopePar
 
 
 constexpr int kRopeMaxTokens = 8;   // tokens per CTA: one warp each finds the request and the slot
-
-// Largest b with cu[b] <= n, by a 32-way search of one warp (-1: none).
-__device__ __forceinline__ int request_of(const int32_t* cu, int B, int n, int lane) {
-  int lo = -1, hi = B + 1;   // cu[lo] <= n < cu[hi], with cu[-1] = -inf and cu[B + 1] = +inf
-  while (hi - lo > 1) {
-    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    const bool le = at < hi && __ldg(cu + at) <= n;
-    const int k = __popc(__ballot_sync(0xffffffffu, le));
-    const int nlo = lo + k * step;
-    hi = min(hi, nlo + step);
-    lo = nlo;
-  }
-  return lo;
-}
 
 // 16-byte pieces of VEC values; V of a token's pieces are pairs of pieces (half layout), single
 // pieces of pairs (interleaved), or copies.

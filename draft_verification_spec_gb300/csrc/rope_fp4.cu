@@ -1,0 +1,393 @@
+// Rotary positions of new tokens and the write of keys and values into a paged cache held in 4 bits; what such a cache
+// stands for.
+//
+// The rotation is that of the 16-bit caches (rope_append.cu).  A rotated key is rounded to fp32 and to its type (what a
+// 16-bit cache would hold) and then, as the values are, held in blocks of 16 along the head:
+//   scale = e4m3 nearest to (largest magnitude / (6 unit)), within [2^-9, 448];  code = e2m1 nearest to x / (scale unit),
+// ties to the even code.  A block with a NaN gets the scale NaN; what is beyond 6 x 448 units is held as that.
+//
+// Codes are whole numbers, so they must not hang on a rounding on the way:
+// - x has 11 significant bits at most and scale x unit 4, so a quotient is either exactly on a border between two codes
+//   or at least 2^-11 of its size away from it (a border has 3 bits).  x times the reciprocal is off by 2^-23; rounding
+//   that to half precision (11 bits) lands on the border in the first case and off it in the second.
+// - largest / (6 unit) is exact where it is a tie of e4m3 (5 bits), and further from one than fp32's rounding elsewhere.
+// - a rotated key's fp32 error, (|x| + |y|) 2^-21.5 at most, can move its rounding to 16 bits.  Where both ends of that
+//   interval do not give the same scale and codes (1 block in some 10^4), the keys in question are rotated in 64 bits.
+//
+// Bound: HBM: q read and written, k and v read, 4.5 bits a value written, no reuse.
+#include "rope_device.cuh"
+
+namespace sv {
+
+namespace {
+
+constexpr int kFp4MaxTokens = 8;   // tokens per CTA: one warp each finds the request and the slot
+
+// The e4m3 scale (as a byte) of a block whose largest magnitude is `top`, and 1 / (scale unit).
+__device__ __forceinline__ uint32_t block_scale(float top, bool nan, float unit, float* inverse) {
+  const float want = fminf(fmaxf(__fdiv_rn(top, 6.f * unit), 0.001953125f), 448.f);
+  uint16_t two;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(want));
+  uint32_t half2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(two));
+  *inverse = __frcp_rn(__low2float(*reinterpret_cast<const __half2*>(&half2)) * unit);
+  return nan ? 0x7fu : two & 0xffu;
+}
+// Codes of two values, the first in the low half of the byte.
+__device__ __forceinline__ uint32_t two_codes(float x, float y, float inverse) {
+  const float2 q = __half22float2(__floats2half2_rn(x * inverse, y * inverse));
+  uint32_t r;
+  asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\tcvt.u32.u8 %0, c;\n\t}" : "=r"(r) : "f"(q.y), "f"(q.x));
+  return r;
+}
+// A block of 16: its scale; its codes, eight to a word.
+struct Block {
+  uint32_t scale;
+  uint2 codes;
+  __device__ __forceinline__ bool operator!=(const Block& b) const {
+    return scale != b.scale || codes.x != b.codes.x || codes.y != b.codes.y;
+  }
+};
+__device__ __forceinline__ Block hold(const float (&x)[16], float unit) {
+  float top = 0.f;
+  bool nan = false;
+#pragma unroll
+  for (int i = 0; i < 16; ++i) {
+    top = fmaxf(top, fabsf(x[i]));
+    nan = nan || x[i] != x[i];
+  }
+  Block b;
+  float inverse;
+  b.scale = block_scale(top, nan, unit, &inverse);
+  uint32_t w[2] = {0u, 0u};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i / 4] |= two_codes(x[2 * i], x[2 * i + 1], inverse) << (i % 4 * 8);
+  b.codes = make_uint2(w[0], w[1]);
+  return b;
+}
+
+template <typename T>
+__device__ __forceinline__ float rounded(float x) {
+  T y;
+  from_f(x, &y);
+  return to_f(y);
+}
+// x cos a - y sin a (turn = -1) or x cos a + y sin a (turn = 1) in 64 bits, rounded to fp32.
+__device__ __noinline__ float rotated_exactly(float x, float y, float turn, unsigned long long phase, float factor) {
+  double s, c;
+  sincospi(static_cast<double>(static_cast<long long>(phase)) * 0x1p-63, &s, &c);
+  return __double2float_rn((x * c + static_cast<double>(turn) * y * s) * factor);
+}
+
+template <typename T>
+__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
+  uint4 raw[2] = {__ldg(reinterpret_cast<const uint4*>(p)), __ldg(reinterpret_cast<const uint4*>(p) + 1)};
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = to_f(reinterpret_cast<const T*>(raw)[i]);
+}
+template <typename T>
+__device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
+  uint4 raw[2];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) from_f(x[i], reinterpret_cast<T*>(raw) + i);
+  reinterpret_cast<uint4*>(p)[0] = raw[0];
+  reinterpret_cast<uint4*>(p)[1] = raw[1];
+}
+
+// Byte offsets of a token's slot in the four arrays (-1: not stored), its position, whether a request has it.
+struct Slot {
+  long long k, v, ks, vs;
+  int pos, has;
+};
+// One warp: the slot of new token n.
+__device__ __forceinline__ Slot slot_of(const RopeParams& p, const Fp4Scales& s, int n, int lane) {
+  const int b = request_of(p.c.cu_q, p.c.B, n, lane);
+  Slot r = {-1, -1, -1, -1, 0, b >= 0 && b < p.c.B};
+  if (r.has) {
+    r.pos = __ldg(p.c.kv_lens + b) - (__ldg(p.c.cu_q + b + 1) - n);
+    if (r.pos >= 0) {
+      const int col = r.pos / p.c.page_size, in = r.pos % p.c.page_size;
+      const int pg = col < p.c.table_width ? __ldg(p.c.table + b * p.c.table_stride + col) : -1;
+      if (pg < 0 || pg >= p.c.pages) {
+        if (lane == 0) atomicOr(p.status, kStatusPageRange);
+      } else {
+        r.k = pg * p.c.k_page + in * p.c.k_token;
+        r.v = pg * p.c.v_page + in * p.c.v_token;
+        r.ks = pg * s.k_page + in * s.k_token;
+        r.vs = pg * s.v_page + in * s.v_token;
+      }
+    }
+  }
+  return r;
+}
+
+// The form for whole blocks: the rotated part is whole blocks (half layout: each half is), rows are 16-byte aligned.
+// A CTA takes `per_cta` tokens; a thread takes a block of 16 values, or a block and its partner where they turn
+// together.
+template <int DTYPE, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_fp4_kernel(const RopeParams p, const Fp4Scales s, float k_unit, float v_unit, int per_cta) {
+  using T = typename RopeType<DTYPE>::T;
+  constexpr int PP = INTERLEAVED ? 8 : 16;   // pairs of a unit
+  extern __shared__ __align__(16) float2 s_cs[];   // [per_cta][rotary / 2]
+  __shared__ Slot slots[kFp4MaxTokens];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n0 = blockIdx.x * per_cta, tokens = min(per_cta, p.c.N - n0);
+  const int half = p.rotary / 2, D = p.c.D, Hk = p.c.Hkv;
+  const int turn = half / PP;                // rotated units per head
+  const int per_head = turn + (D - p.rotary) / 16;
+  const int rot_units = (p.Hq + Hk) * per_head, units = rot_units + Hk * (D / 16);
+
+  for (int t = warp; t < tokens; t += kRopeThreads / 32) {
+    const Slot r = slot_of(p, s, n0 + t, lane);
+    if (lane == 0) slots[t] = r;
+  }
+  __syncthreads();
+  for (int i = tid; i < tokens * half; i += kRopeThreads) {
+    const int t = i / half, j = i - t * half, e = j % PP;
+    const float2 c = phase_cs(p.freq[j] * static_cast<unsigned long long>(static_cast<long long>(slots[t].pos)));
+    // two pairs' angles together, then the units side by side: the lanes' 16-byte reads fall on distinct banks
+    s_cs[t * half + ((e >> 1) * turn + j / PP) * 2 + (e & 1)] = make_float2(c.x * p.factor, c.y * p.factor);
+  }
+  __syncthreads();
+
+  for (int u = tid; u < tokens * units; u += kRopeThreads) {
+    const int t = u / units, n = n0 + t;
+    int r = u - t * units;
+    const Slot& slot = slots[t];
+    if (!slot.has) continue;
+    float a[16], b[16];
+    if (r >= rot_units) {   // values
+      r -= rot_units;
+      const int h = r / (D / 16), j = r - h * (D / 16);
+      if (slot.v < 0) continue;
+      load16(reinterpret_cast<const T*>(p.v) + n * p.v_token + h * p.v_head + j * 16, a);
+      const Block x = hold(a, v_unit);
+      *reinterpret_cast<uint2*>(p.c.v + slot.v + h * p.c.v_head + j * 8) = x.codes;
+      s.v[slot.vs + h * s.v_head + j] = static_cast<uint8_t>(x.scale);
+      continue;
+    }
+    const int h = r / per_head, j = r - h * per_head, hk = h - p.Hq;
+    const bool rotate = j < turn, pair = rotate && !INTERLEAVED;
+    const int at = rotate ? j * 16 : p.rotary + (j - turn) * 16;
+    const T* src = hk < 0 ? reinterpret_cast<const T*>(p.q) + n * p.q_token + h * p.q_head
+                          : reinterpret_cast<const T*>(p.k) + n * p.k_token + hk * p.k_head;
+    T* dst = hk < 0 ? reinterpret_cast<T*>(p.q_out) + n * p.qo_token + h * p.qo_head
+                    : (p.k_out ? reinterpret_cast<T*>(p.k_out) + n * p.ko_token + hk * p.ko_head : nullptr);
+    load16(src + at, a);
+    if (pair) load16(src + at + half, b);
+    const bool held = hk >= 0 && slot.k >= 0;
+    float a0[16], b0[16];   // as they were: for the error, and for the exact rotation
+    if (rotate) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        a0[i] = a[i];
+        if (!INTERLEAVED) b0[i] = b[i];
+      }
+      const float4* cs = reinterpret_cast<const float4*>(s_cs + t * half) + j;
+#pragma unroll
+      for (int i = 0; i < PP; i += 2) {
+        const float4 w = cs[(i >> 1) * turn];   // cos, sin of pairs i and i + 1
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float c = e ? w.z : w.x, sn = e ? w.w : w.y;
+          float& x = INTERLEAVED ? a[2 * (i + e)] : a[i + e];
+          float& y = INTERLEAVED ? a[2 * (i + e) + 1] : b[i + e];
+          const float x1 = x * c - y * sn, y1 = y * c + x * sn;
+          x = x1;
+          y = y1;
+        }
+      }
+    }
+    if (dst) {
+      store16(dst + at, a);
+      if (pair) store16(dst + at + half, b);
+    }
+    if (!held) continue;
+    uint8_t* codes = p.c.k + slot.k + hk * p.c.k_head;
+    uint8_t* scales = s.k + slot.ks + hk * s.k_head;
+#pragma unroll
+    for (int which = 0; which < (INTERLEAVED ? 1 : 2); ++which) {
+      if (which && !pair) break;
+      float (&x)[16] = which ? b : a;
+      if (rotate) {
+        // both ends of each key's error interval, the larger in magnitude in x: scales rise with the largest magnitude and
+        // codes with the value, so two equal blocks mean that no key between the ends makes another one
+        auto partner = [&](int i) { return INTERLEAVED ? a0[i ^ 1] : which ? a0[i] : b0[i]; };
+        auto self = [&](int i) { return which ? b0[i] : a0[i]; };
+        float lo[16];
+        bool clear = true;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const float e = (fabsf(self(i)) + fabsf(partner(i))) * fabsf(p.factor) * 4.76837158203125e-7f;   // 2^-21
+          const float below = rounded<T>(x[i] - e), above = rounded<T>(x[i] + e);
+          const bool up = fabsf(above) >= fabsf(below);
+          clear = clear && below == above;
+          x[i] = up ? above : below;
+          lo[i] = up ? below : above;
+        }
+        if (!clear) {
+          if (hold(x, k_unit) != hold(lo, k_unit)) {
+            const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(slot.pos));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              if (lo[i] == x[i]) continue;
+              const int k = INTERLEAVED ? j * 8 + i / 2 : j * 16 + i;
+              const bool second = INTERLEAVED ? i & 1 : which;
+              x[i] = rounded<T>(rotated_exactly(self(i), partner(i), second ? 1.f : -1.f, p.freq[k] * pos, p.factor));
+            }
+          }
+        }
+      }
+      const Block y = hold(x, k_unit);
+      const int i = at + which * half;
+      *reinterpret_cast<uint2*>(codes + i / 2) = y.codes;
+      scales[i / 16] = static_cast<uint8_t>(y.scale);
+    }
+  }
+}
+
+// Any rotated part, alignment and stride of the new tokens: a warp takes a head of a token, a lane every 32nd value, 16 lanes
+// a block.  The head is read whole before anything of it is written, so it may be rotated in place.
+template <int DTYPE>
+__global__ void __launch_bounds__(kRopeThreads)
+    rope_fp4_scalar_kernel(const RopeParams p, const Fp4Scales s, float k_unit, float v_unit) {
+  using T = typename RopeType<DTYPE>::T;
+  const int n = blockIdx.x, lane = threadIdx.x & 31;
+  const Slot slot = slot_of(p, s, n, lane);
+  if (!slot.has) return;
+  const int half = p.rotary / 2, D = p.c.D;
+  const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(slot.pos));
+  for (int h = threadIdx.x / 32; h < p.Hq + 2 * p.c.Hkv; h += kRopeThreads / 32) {
+    const int kind = h < p.Hq ? 0 : h < p.Hq + p.c.Hkv ? 1 : 2;   // query, key, value
+    const int hk = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.c.Hkv;
+    const T* src = kind == 0   ? reinterpret_cast<const T*>(p.q) + n * p.q_token + hk * p.q_head
+                   : kind == 1 ? reinterpret_cast<const T*>(p.k) + n * p.k_token + hk * p.k_head
+                               : reinterpret_cast<const T*>(p.v) + n * p.v_token + hk * p.v_head;
+    float x[8];     // what is held, or the rotated query
+    float plain[8];   // the rotated key as rope_append rounds it
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = i * 32 + lane;
+      x[i] = plain[i] = 0.f;
+      if (c >= D) continue;
+      x[i] = plain[i] = to_f(src[c]);
+      if (kind == 2 || c >= p.rotary) continue;
+      const int k = p.interleaved ? c / 2 : c % half;
+      const bool second = p.interleaved ? c & 1 : c >= half;
+      const float y = to_f(src[p.interleaved ? c ^ 1 : second ? c - half : c + half]);
+      const unsigned long long phase = p.freq[k] * pos;
+      const float2 w = phase_cs(phase);
+      const float cs = w.x * p.factor, sn = w.y * p.factor, self = x[i];
+      x[i] = plain[i] = second ? self * cs + y * sn : self * cs - y * sn;
+      if (kind == 1) {
+        const float e = (fabsf(self) + fabsf(y)) * fabsf(p.factor) * 4.76837158203125e-7f;   // 2^-21
+        if (rounded<T>(x[i] - e) != rounded<T>(x[i] + e)) x[i] = rotated_exactly(self, y, second ? 1.f : -1.f, phase, p.factor);
+      }
+    }
+    __syncwarp();
+    T* dst = kind == 0 ? reinterpret_cast<T*>(p.q_out) + n * p.qo_token + hk * p.qo_head
+             : kind == 1 && p.k_out ? reinterpret_cast<T*>(p.k_out) + n * p.ko_token + hk * p.ko_head : nullptr;
+    const bool held = kind == 1 ? slot.k >= 0 : kind == 2 && slot.v >= 0;
+    uint8_t* codes = kind == 1 ? p.c.k + slot.k + hk * p.c.k_head : p.c.v + slot.v + hk * p.c.v_head;
+    uint8_t* scales = kind == 1 ? s.k + slot.ks + hk * s.k_head : s.v + slot.vs + hk * s.v_head;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = i * 32 + lane;
+      if (dst && c < D) from_f(plain[i], dst + c);
+      if (!held || i * 32 >= D) continue;     // the same for the whole warp
+      const float y = rounded<T>(x[i]);
+      float top = fabsf(y);
+      int nan = y != y;
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) {
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        nan |= __shfl_xor_sync(0xffffffffu, nan, o);
+      }
+      float inverse;
+      const uint32_t scale = block_scale(top, nan, kind == 1 ? k_unit : v_unit, &inverse);
+      const uint32_t two = two_codes(y, __shfl_down_sync(0xffffffffu, y, 1), inverse);
+      if (c < D && lane % 2 == 0) codes[c / 2] = static_cast<uint8_t>(two);
+      if (c < D && lane % 16 == 0) scales[c / 16] = static_cast<uint8_t>(scale);
+    }
+  }
+}
+
+// A thread a block: 8 bytes of codes and a scale -> 16 values.  Bound: HBM, 0.56 bytes read and 2 (or 4) written a value.
+template <int DTYPE>
+__global__ void __launch_bounds__(256) fp4_values_kernel(const Fp4Values p) {
+  using T = typename RopeType<DTYPE>::T;
+  const unsigned blocks = p.dim / 16, row = p.heads * blocks;   // of a head, of a token
+  const long long total = static_cast<long long>(p.pages) * p.page_size * row;
+  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
+    const long long token = i / row;
+    const unsigned in_row = static_cast<unsigned>(i - token * row), h = in_row / blocks, j = in_row - h * blocks;
+    const long long page = token / p.page_size;
+    const int in = static_cast<int>(token - page * p.page_size);
+    const uint2 codes = __ldg(reinterpret_cast<const uint2*>(p.codes + page * p.page + in * p.token + h * p.head + j * 8));
+    const uint16_t sc = __ldg(p.scales + page * p.s_page + in * p.s_token + h * p.s_head + j);
+    uint32_t half2;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(sc));
+    const float scale = __low2float(*reinterpret_cast<const __half2*>(&half2)) * p.unit;
+    __align__(16) T out[16];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      const uint32_t c = w ? codes.y : codes.x;
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const uint16_t two = static_cast<uint16_t>(c >> (8 * b) & 0xffu);
+        uint32_t v;
+        asm("{\n\t.reg .b8 x;\n\tcvt.u8.u16 x, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x;\n\t}" : "=r"(v) : "h"(two));
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+        from_f(f.x * scale, out + w * 8 + 2 * b);
+        from_f(f.y * scale, out + w * 8 + 2 * b + 1);
+      }
+    }
+    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + i * 16);
+#pragma unroll
+    for (int k = 0; k < static_cast<int>(sizeof(out) / 16); ++k) dst[k] = reinterpret_cast<const uint4*>(out)[k];
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, float k_unit, float v_unit, int sms,
+                            cudaStream_t stream) {
+  const long long strides[] = {p.q_token, p.q_head, p.k_token, p.k_head, p.v_token, p.v_head, p.qo_token, p.qo_head,
+                               p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0};
+  bool whole = p.rotary % (p.interleaved ? 16 : 32) == 0;
+  for (long long st : strides) whole = whole && st % 8 == 0;
+  const void* bases[] = {p.q, p.k, p.v, p.q_out, p.k_out};
+  for (const void* b : bases) whole = whole && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
+  if (!whole) {
+    const dim3 grid(p.c.N), block(kRopeThreads);
+    if (dtype == 1) rope_fp4_scalar_kernel<1><<<grid, block, 0, stream>>>(p, s, k_unit, v_unit);
+    if (dtype == 2) rope_fp4_scalar_kernel<2><<<grid, block, 0, stream>>>(p, s, k_unit, v_unit);
+    return cudaGetLastError();
+  }
+  // few tokens: a CTA each; many: as many tokens a CTA as make about 1024 blocks
+  const long long blocks = (p.Hq + 2ll * p.c.Hkv) * (p.c.D / 16);
+  int per = p.c.N <= 4 * sms ? 1 : static_cast<int>(1024 / blocks);
+  per = per < 1 ? 1 : per > kFp4MaxTokens ? kFp4MaxTokens : per;
+  const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);
+  const size_t smem = sizeof(float2) * (p.rotary / 2) * per;
+  const int kind = dtype * 2 + (p.interleaved ? 1 : 0);
+  if (kind == 2) rope_fp4_kernel<1, false><<<grid, block, smem, stream>>>(p, s, k_unit, v_unit, per);
+  if (kind == 3) rope_fp4_kernel<1, true><<<grid, block, smem, stream>>>(p, s, k_unit, v_unit, per);
+  if (kind == 4) rope_fp4_kernel<2, false><<<grid, block, smem, stream>>>(p, s, k_unit, v_unit, per);
+  if (kind == 5) rope_fp4_kernel<2, true><<<grid, block, smem, stream>>>(p, s, k_unit, v_unit, per);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_fp4_values(int dtype, const Fp4Values& p, int sms, cudaStream_t stream) {
+  const long long total = static_cast<long long>(p.pages) * p.page_size * p.heads * (p.dim / 16);
+  if (total == 0) return cudaSuccess;
+  const long long want = (total + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(want < 16ll * sms ? want : 16ll * sms)), block(256);
+  if (dtype == 0) fp4_values_kernel<0><<<grid, block, 0, stream>>>(p);
+  if (dtype == 1) fp4_values_kernel<1><<<grid, block, 0, stream>>>(p);
+  if (dtype == 2) fp4_values_kernel<2><<<grid, block, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace sv

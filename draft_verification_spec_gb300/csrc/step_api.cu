@@ -2,6 +2,7 @@
 // the cache write, sampling): argument checks, kernel choice, launches.
 #include <cmath>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 
@@ -39,8 +40,9 @@ size_t partial_bytes(const sv::AttnPlan& plan, int D) {
   return static_cast<size_t>(plan.grid) * (sizeof(sv::AttnJoin) + 2 * plan.bm * (D + 2) * sizeof(float));
 }
 
-// The batch description's checks; `cache`: keys and values are addressed.
-spec_status_t check_batch(const spec_paged_batch_t* b, bool cache, int esz) {
+// The batch description's checks; `cache`: keys and values are addressed, whose bases and strides (in units of
+// `esz` bytes) are multiples of `align` bytes.
+spec_status_t check_batch(const spec_paged_batch_t* b, bool cache, int esz, int align = 16) {
   if (!b || b->batch < 0 || b->tokens < 0 || b->kv_heads < 1 || b->dim < 1) return SPEC_ERR_INVALID_ARG;
   if (b->batch > 0 && (!b->cu_q || !b->kv_lens)) return SPEC_ERR_INVALID_ARG;
   if (!cache) return SPEC_OK;
@@ -48,8 +50,8 @@ spec_status_t check_batch(const spec_paged_batch_t* b, bool cache, int esz) {
   if (b->pages < 1 || b->page_size < 1 || b->table_width < 0 || b->table_stride < b->table_width) return SPEC_ERR_INVALID_ARG;
   const long long st[6] = {b->k_page, b->k_token, b->k_head, b->v_page, b->v_token, b->v_head};
   for (long long s : st)
-    if (s < 0 || (s * esz) % 16 != 0) return SPEC_ERR_INVALID_ARG;
-  if (!aligned(b->k, 16) || !aligned(b->v, 16)) return SPEC_ERR_INVALID_ARG;
+    if (s < 0 || (s * esz) % align != 0) return SPEC_ERR_INVALID_ARG;
+  if (!aligned(b->k, align) || !aligned(b->v, align)) return SPEC_ERR_INVALID_ARG;
   return SPEC_OK;
 }
 
@@ -77,6 +79,37 @@ sv::PagedBatch internal_batch(const spec_paged_batch_t& b) {
   return c;
 }
 
+// A power of two between 2^-64 and 2^64.
+bool fp4_unit(float u) {
+  int e = 0;
+  return std::isfinite(u) && std::frexp(u, &e) == 0.5f && e >= -63 && e <= 65;
+}
+
+spec_status_t check_scales(const spec_paged_batch_t* b, const spec_fp4_scales_t* s) {
+  if (!s || !s->k || !s->v || !fp4_unit(s->k_unit) || !fp4_unit(s->v_unit)) return SPEC_ERR_INVALID_ARG;
+  for (long long x : {s->k_page, s->k_token, s->k_head, s->v_page, s->v_token, s->v_head})
+    if (x < 0) return SPEC_ERR_INVALID_ARG;
+  return b->dim % 16 != 0 || b->dim > 256 ? SPEC_ERR_UNSUPPORTED : SPEC_OK;
+}
+
+sv::Fp4Scales internal_scales(const spec_paged_batch_t& b, const spec_fp4_scales_t& f) {
+  sv::Fp4Scales s;
+  s.k = static_cast<uint8_t*>(f.k);
+  s.v = static_cast<uint8_t*>(f.v);
+  s.k_page = f.k_page;
+  s.k_token = f.k_token;
+  s.k_head = f.k_head;
+  s.v_page = f.v_page;
+  s.v_token = f.v_token;
+  s.v_head = f.v_head;
+  bool whole = (b.dim == 64 || b.dim == 128 || b.dim == 256) && aligned(b.k, 16) && aligned(b.v, 16) &&
+               aligned(f.k, b.dim / 16) && aligned(f.v, b.dim / 16);
+  for (long long x : {b.k_page, b.k_token, b.k_head, b.v_page, b.v_token, b.v_head}) whole = whole && x % 16 == 0;
+  for (long long x : {f.k_page, f.k_token, f.k_head, f.v_page, f.v_token, f.v_head}) whole = whole && x % (b.dim / 16) == 0;
+  s.whole = whole;
+  return s;
+}
+
 bool attention_types(int dtype) { return dtype == SPEC_BF16 || dtype == SPEC_F16; }
 
 // No C++ exception (a lock or a cache entry that cannot be had) leaves a C entry.
@@ -89,26 +122,170 @@ auto guarded(F f, decltype(f()) failed) -> decltype(f()) {
   }
 }
 
+size_t attention_workspace(int dtype, int q_heads, int kv_heads, int dim, int max_q, bool fp4) {
+  if (!attention_types(dtype) || kv_heads < 1 || q_heads < kv_heads || dim < 8 || dim > 256 || max_q < 0) return 0;
+  if (fp4 && dim % 16 != 0) return 0;
+  int sms = 0;
+  if (sm_count(&sms) != SPEC_OK) return 0;
+  const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
+  size_t most = 0;   // over the kernels that rows and dim admit, with first tokens kept or not
+  for (int kind = 0; kind < 4; ++kind) {
+    if (!fp4 && ((kind == 0) != (rows <= 16) || (kind >= 2 && (dim < 64 || dim > 128 || (kind == 3) != (rows > 128))))) continue;
+    if (fp4 && kind != sv::attention_fp4_kind(static_cast<int>(rows < 1024 ? rows : 1024), dim, 1.f) && kind != 0) continue;
+    for (int sinks = 0; sinks < (fp4 ? 1 : 2); ++sinks) {
+      sv::AttnPlan plan;
+      if (sv::attention_plan({dtype == SPEC_BF16, sinks != 0, fp4}, kind, 1, dim, sms, &plan) != cudaSuccess) return 0;
+      const size_t n = partial_bytes(plan, dim);
+      most = n > most ? n : most;
+    }
+  }
+  return kStatusBytes + (most + 255) / 256 * 256;
+}
+
+struct AttentionCall {
+  const void* q;
+  long long q_token, q_head;
+  int dtype, q_heads;
+  const spec_paged_batch_t* batch;
+  const spec_fp4_scales_t* scales;   // null: the cache has q's type
+  int max_q;
+  float scale;
+  int causal, window, sinks;
+  void* out;
+  float* lse;
+  void* workspace;
+  size_t ws_bytes;
+  cudaStream_t stream;
+  const spec_tuning_t* tuning;
+};
+
+// Kernels that talk through a workspace: another thread's call with the same one must not come between a call's launches.
+std::mutex g_pair;
+
+spec_status_t run_attention(const AttentionCall& a) {
+  const spec_paged_batch_t* batch = a.batch;
+  const bool fp4 = a.scales != nullptr;
+  if (!attention_types(a.dtype) || a.q_heads < 1 || a.max_q < 0 || a.window < 0 || a.sinks < 0 || !std::isfinite(a.scale))
+    return SPEC_ERR_INVALID_ARG;
+  spec_status_t st = fp4 ? check_batch(batch, true, 1, 8) : check_batch(batch, true, 2);
+  if (st != SPEC_OK) return st;
+  if (a.q_heads % batch->kv_heads != 0) return SPEC_ERR_INVALID_ARG;
+  if (batch->dim % 8 != 0 || batch->dim > 256) return SPEC_ERR_UNSUPPORTED;
+  if (fp4 && (st = check_scales(batch, a.scales)) != SPEC_OK) return st;
+  if (batch->batch == 0 || batch->tokens == 0) return SPEC_OK;
+  if (!a.q || !a.out || !aligned(a.q, 16) || !aligned(a.out, 16) || (a.q_token * 2) % 16 != 0 || (a.q_head * 2) % 16 != 0)
+    return SPEC_ERR_INVALID_ARG;
+  if (!a.workspace || !aligned(a.workspace, 256)) return SPEC_ERR_WORKSPACE;
+  int sms = 0;
+  if ((st = sm_count(&sms)) != SPEC_OK) return st;
+  const sv::AttnForm form = {a.dtype == SPEC_BF16, a.window > 0 && a.sinks > 0, fp4};
+  const int G = a.q_heads / batch->kv_heads;
+  const long long all_rows = static_cast<long long>(a.max_q) * G;
+  const int rows = static_cast<int>(all_rows < 1024 ? all_rows : 1024);
+  sv::AttnMaps maps;
+  int kind = fp4 ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);
+  if (!fp4 && kind >= 2 && !sv::attention_maps(form.bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
+  sv::AttnPlan plan;
+  if (sv::attention_plan(form, kind, rows, batch->dim, sms, &plan) != cudaSuccess) return SPEC_ERR_CUDA;
+  if (a.ws_bytes < kStatusBytes + partial_bytes(plan, batch->dim)) return SPEC_ERR_WORKSPACE;
+  sv::AttnParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = internal_batch(*batch);
+  p.q = static_cast<const uint8_t*>(a.q);
+  p.q_token = a.q_token;
+  p.q_head = a.q_head;
+  p.out = static_cast<uint8_t*>(a.out);
+  p.lse = a.lse;
+  p.Hq = a.q_heads;
+  p.G = G;
+  p.G_inv = G > 1 ? ~0ull / G + 1 : 0ull;
+  for (p.lanes = 1; p.lanes < 32 && static_cast<long long>(p.lanes) * plan.bm < all_rows;) p.lanes *= 2;
+  p.causal = a.causal != 0;
+  p.window = a.window;
+  p.sinks = form.sinks ? a.sinks : 0;
+  p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 * (fp4 ? a.scales->k_unit : 1.f));
+  if (!std::isfinite(p.scale_log2)) return SPEC_ERR_INVALID_ARG;
+  p.v_unit = fp4 ? a.scales->v_unit : 1.f;
+  if (fp4) p.s = internal_scales(*batch, *a.scales);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.status = reinterpret_cast<int32_t*>(ws);
+  p.joins = reinterpret_cast<sv::AttnJoin*>(ws + kStatusBytes);
+  p.part_ml = reinterpret_cast<float*>(p.joins + plan.grid);
+  p.part_o = p.part_ml + static_cast<size_t>(plan.grid) * 2 * plan.bm * 2;
+  // an item's fixed cost in key tiles.  Measured, 64 requests x 4 tokens, ragged to 4096 keys (mma.sync):
+  // 0: 140, 1: 127, 2: 115, 3: 113, 4: 114 us; 32 x 17 tokens, 64 query heads, ragged to 16384 (tcgen05):
+  // 0: 248, 2: 234, 3: 224, 4: 220, 6: 220 us.
+  p.overhead = plan.kind >= 2 ? 4 : 3;
+  // fewest units worth a CTA: an item's cost and one key tile.  A single token over 1024 keys, 8 key heads
+  // (152 units, so 38 CTAs of four): 12.4 us; with two tiles (31 CTAs) 13.3, with four (22) 15.2 us.
+  p.min_units = 1 + p.overhead;
+  const long long wait_us = a.tuning ? a.tuning->wait_limit_us : 0;
+  p.wait_limit = wait_us == 0 ? kWaitNs : wait_us < 0 ? 0 : wait_us < kWaitNs ? wait_us * 1000 : kWaitNs * 1000;
+  p.n_max = plan.grid;
+  std::lock_guard<std::mutex> lk(g_pair);
+  if (sv::launch_attention(form, plan, p, maps, a.stream) != cudaSuccess) return SPEC_ERR_CUDA;
+  return sv::launch_attention_combine(form.bf16, plan, p, a.stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
+// rope_append's call, into a cache of the tokens' type or (scales) one held in 4 bits.
+spec_status_t run_rope(const spec_rope_tensors_t* t, int dtype, int q_heads, const spec_paged_batch_t* batch,
+                       const spec_fp4_scales_t* scales, const unsigned long long* freq, int rotary_dim, float factor,
+                       int interleaved, void* workspace, cudaStream_t stream) {
+  const bool fp4 = scales != nullptr;
+  if (!t || (dtype != SPEC_BF16 && dtype != SPEC_F16 && (fp4 || dtype != SPEC_F32)) || q_heads < 0) return SPEC_ERR_INVALID_ARG;
+  const bool cache = fp4 || (batch && batch->k);
+  spec_status_t st = fp4 ? check_batch(batch, true, 1, 8) : check_batch(batch, cache, dtype == SPEC_F32 ? 4 : 2);
+  if (st != SPEC_OK) return st;
+  if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > batch->dim || !std::isfinite(factor)) return SPEC_ERR_INVALID_ARG;
+  if (batch->dim > 1024) return SPEC_ERR_UNSUPPORTED;
+  if (fp4 && (st = check_scales(batch, scales)) != SPEC_OK) return st;
+  if (batch->batch == 0 || batch->tokens == 0) return SPEC_OK;
+  if ((q_heads > 0 && (!t->q || !t->q_out)) || !t->k || (cache && !t->v) || (rotary_dim > 0 && !freq))
+    return SPEC_ERR_INVALID_ARG;
+  if (!cache && !t->k_out) return SPEC_ERR_INVALID_ARG;
+  if (cache && (!workspace || !aligned(workspace, 256))) return SPEC_ERR_WORKSPACE;
+  sv::RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.c = internal_batch(*batch);
+  p.q = static_cast<const uint8_t*>(t->q);
+  p.k = static_cast<const uint8_t*>(t->k);
+  p.v = static_cast<const uint8_t*>(t->v);
+  p.q_out = static_cast<uint8_t*>(t->q_out);
+  p.k_out = static_cast<uint8_t*>(t->k_out);
+  p.q_token = t->q_token;
+  p.q_head = t->q_head;
+  p.k_token = t->k_token;
+  p.k_head = t->k_head;
+  p.v_token = t->v_token;
+  p.v_head = t->v_head;
+  p.qo_token = t->q_out_token;
+  p.qo_head = t->q_out_head;
+  p.ko_token = t->k_out_token;
+  p.ko_head = t->k_out_head;
+  p.freq = freq;
+  p.factor = factor;
+  p.Hq = q_heads;
+  p.rotary = rotary_dim;
+  p.interleaved = interleaved != 0;
+  p.status = static_cast<int32_t*>(workspace);
+  int sms = 0;
+  if ((st = sm_count(&sms)) != SPEC_OK) return st;
+  if (fp4)
+    return sv::launch_rope_fp4(dtype, p, internal_scales(*batch, *scales), scales->k_unit, scales->v_unit, sms, stream) == cudaSuccess
+               ? SPEC_OK : SPEC_ERR_CUDA;
+  return sv::launch_rope(dtype, p, sms, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
 
 size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int dim, int max_q) {
-  return guarded([&]() -> size_t {
-    if (!attention_types(dtype) || kv_heads < 1 || q_heads < kv_heads || dim < 8 || dim > 256 || max_q < 0) return 0;
-    int sms = 0;
-    if (sm_count(&sms) != SPEC_OK) return 0;
-    const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
-    size_t most = 0;   // over the kernels that rows and dim admit
-    for (int kind = 0; kind < 4; ++kind) {
-      if ((kind == 0) != (rows <= 16) || (kind >= 2 && (dim < 64 || dim > 128 || (kind == 3) != (rows > 128)))) continue;
-      sv::AttnPlan plan;
-      if (sv::attention_plan(dtype == SPEC_BF16, kind, 1, dim, sms, &plan) != cudaSuccess) return 0;
-      const size_t n = partial_bytes(plan, dim);
-      most = n > most ? n : most;
-    }
-    return kStatusBytes + (most + 255) / 256 * 256;
-  }, static_cast<size_t>(0));
+  return guarded([&] { return attention_workspace(dtype, q_heads, kv_heads, dim, max_q, false); }, static_cast<size_t>(0));
+}
+
+size_t spec_attention_fp4_workspace_bytes(int dtype, int q_heads, int kv_heads, int dim, int max_q) {
+  return guarded([&] { return attention_workspace(dtype, q_heads, kv_heads, dim, max_q, true); }, static_cast<size_t>(0));
 }
 
 spec_status_t spec_chunk_attention(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
@@ -122,65 +299,30 @@ spec_status_t spec_chunk_attention_tuned(const void* q, long long q_token, long 
                                          const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
                                          void* out, float* out_lse, void* workspace, size_t ws_bytes, void* stream,
                                          const spec_tuning_t* tuning) {
+  return spec_chunk_attention_sinks(q, q_token, q_head, dtype, q_heads, batch, max_q, scale, causal, window, 0, out, out_lse,
+                                    workspace, ws_bytes, stream, tuning);
+}
+
+spec_status_t spec_chunk_attention_sinks(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
+                                         const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
+                                         int sinks, void* out, float* out_lse, void* workspace, size_t ws_bytes,
+                                         void* stream, const spec_tuning_t* tuning) {
   return guarded([&]() -> spec_status_t {
     const sv::ApiRange range("spec_chunk_attention");
-    if (!attention_types(dtype) || q_heads < 1 || max_q < 0 || window < 0 || !std::isfinite(scale)) return SPEC_ERR_INVALID_ARG;
-    spec_status_t st = check_batch(batch, true, 2);
-    if (st != SPEC_OK) return st;
-    if (q_heads % batch->kv_heads != 0) return SPEC_ERR_INVALID_ARG;
-    if (batch->dim % 8 != 0 || batch->dim > 256) return SPEC_ERR_UNSUPPORTED;
-    if (batch->batch == 0 || batch->tokens == 0) return SPEC_OK;
-    if (!q || !out || !aligned(q, 16) || !aligned(out, 16) || (q_token * 2) % 16 != 0 || (q_head * 2) % 16 != 0)
-      return SPEC_ERR_INVALID_ARG;
-    if (!workspace || !aligned(workspace, 256)) return SPEC_ERR_WORKSPACE;
-    int sms = 0;
-    if ((st = sm_count(&sms)) != SPEC_OK) return st;
-    const bool bf16 = dtype == SPEC_BF16;
-    const int G = q_heads / batch->kv_heads;
-    const long long rows = static_cast<long long>(max_q) * G;
-    sv::AttnMaps maps;
-    int kind = sv::attention_kind(static_cast<int>(rows < 1024 ? rows : 1024), batch->dim, batch->page_size, scale);
-    if (kind >= 2 && !sv::attention_maps(bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
-    sv::AttnPlan plan;
-    if (sv::attention_plan(bf16, kind, static_cast<int>(rows < 1024 ? rows : 1024), batch->dim, sms, &plan) != cudaSuccess)
-      return SPEC_ERR_CUDA;
-    if (ws_bytes < kStatusBytes + partial_bytes(plan, batch->dim)) return SPEC_ERR_WORKSPACE;
-    sv::AttnParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.c = internal_batch(*batch);
-    p.q = static_cast<const uint8_t*>(q);
-    p.q_token = q_token;
-    p.q_head = q_head;
-    p.out = static_cast<uint8_t*>(out);
-    p.lse = out_lse;
-    p.Hq = q_heads;
-    p.G = G;
-    p.G_inv = G > 1 ? ~0ull / G + 1 : 0ull;
-    for (p.lanes = 1; p.lanes < 32 && static_cast<long long>(p.lanes) * plan.bm < rows;) p.lanes *= 2;
-    p.causal = causal != 0;
-    p.window = window;
-    p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.status = reinterpret_cast<int32_t*>(ws);
-    p.joins = reinterpret_cast<sv::AttnJoin*>(ws + kStatusBytes);
-    p.part_ml = reinterpret_cast<float*>(p.joins + plan.grid);
-    p.part_o = p.part_ml + static_cast<size_t>(plan.grid) * 2 * plan.bm * 2;
-    // an item's fixed cost in key tiles.  Measured, 64 requests x 4 tokens, ragged to 4096 keys (mma.sync):
-    // 0: 140, 1: 127, 2: 115, 3: 113, 4: 114 us; 32 x 17 tokens, 64 query heads, ragged to 16384 (tcgen05):
-    // 0: 248, 2: 234, 3: 224, 4: 220, 6: 220 us.
-    p.overhead = plan.kind >= 2 ? 4 : 3;
-    // fewest units worth a CTA: an item's cost and one key tile.  A single token over 1024 keys, 8 key heads
-    // (152 units, so 38 CTAs of four): 12.4 us; with two tiles (31 CTAs) 13.3, with four (22) 15.2 us.
-    p.min_units = 1 + p.overhead;
-    const long long wait_us = tuning ? tuning->wait_limit_us : 0;
-    p.wait_limit = wait_us == 0 ? kWaitNs : wait_us < 0 ? 0 : wait_us < kWaitNs ? wait_us * 1000 : kWaitNs * 1000;
-    p.n_max = plan.grid;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // The two kernels talk through the workspace: another thread's call with the same one must not come between.
-    static std::mutex pair;
-    std::lock_guard<std::mutex> lk(pair);
-    if (sv::launch_attention(bf16, plan, p, maps, s) != cudaSuccess) return SPEC_ERR_CUDA;
-    return sv::launch_attention_combine(bf16, plan, p, s) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    return run_attention({q, q_token, q_head, dtype, q_heads, batch, nullptr, max_q, scale, causal, window, sinks, out, out_lse,
+                          workspace, ws_bytes, static_cast<cudaStream_t>(stream), tuning});
+  }, SPEC_ERR_CUDA);
+}
+
+spec_status_t spec_chunk_attention_fp4(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
+                                       const spec_paged_batch_t* batch, const spec_fp4_scales_t* scales, int max_q,
+                                       float scale, int causal, int window, int sinks, void* out, float* out_lse,
+                                       void* workspace, size_t ws_bytes, void* stream, const spec_tuning_t* tuning) {
+  return guarded([&]() -> spec_status_t {
+    const sv::ApiRange range("spec_chunk_attention_fp4");
+    if (!scales) return SPEC_ERR_INVALID_ARG;
+    return run_attention({q, q_token, q_head, dtype, q_heads, batch, scales, max_q, scale, causal, window, sinks, out, out_lse,
+                          workspace, ws_bytes, static_cast<cudaStream_t>(stream), tuning});
   }, SPEC_ERR_CUDA);
 }
 
@@ -189,44 +331,42 @@ spec_status_t spec_rope_append(const spec_rope_tensors_t* t, int dtype, int q_he
                                void* workspace, void* stream) {
   return guarded([&]() -> spec_status_t {
     const sv::ApiRange range("spec_rope_append");
-    if (!t || (dtype != SPEC_F32 && dtype != SPEC_BF16 && dtype != SPEC_F16) || q_heads < 0) return SPEC_ERR_INVALID_ARG;
-    const bool cache = batch && batch->k;
-    spec_status_t st = check_batch(batch, cache, dtype == SPEC_F32 ? 4 : 2);
-    if (st != SPEC_OK) return st;
-    if (rotary_dim < 0 || rotary_dim % 2 != 0 || rotary_dim > batch->dim || !std::isfinite(factor)) return SPEC_ERR_INVALID_ARG;
-    if (batch->dim > 1024) return SPEC_ERR_UNSUPPORTED;
-    if (batch->batch == 0 || batch->tokens == 0) return SPEC_OK;
-    if ((q_heads > 0 && (!t->q || !t->q_out)) || !t->k || (cache && !t->v) || (rotary_dim > 0 && !freq))
-      return SPEC_ERR_INVALID_ARG;
-    if (!cache && !t->k_out) return SPEC_ERR_INVALID_ARG;
-    if (cache && (!workspace || !aligned(workspace, 256))) return SPEC_ERR_WORKSPACE;
-    sv::RopeParams p;
-    std::memset(&p, 0, sizeof(p));
-    p.c = internal_batch(*batch);
-    p.q = static_cast<const uint8_t*>(t->q);
-    p.k = static_cast<const uint8_t*>(t->k);
-    p.v = static_cast<const uint8_t*>(t->v);
-    p.q_out = static_cast<uint8_t*>(t->q_out);
-    p.k_out = static_cast<uint8_t*>(t->k_out);
-    p.q_token = t->q_token;
-    p.q_head = t->q_head;
-    p.k_token = t->k_token;
-    p.k_head = t->k_head;
-    p.v_token = t->v_token;
-    p.v_head = t->v_head;
-    p.qo_token = t->q_out_token;
-    p.qo_head = t->q_out_head;
-    p.ko_token = t->k_out_token;
-    p.ko_head = t->k_out_head;
-    p.freq = freq;
-    p.factor = factor;
-    p.Hq = q_heads;
-    p.rotary = rotary_dim;
-    p.interleaved = interleaved != 0;
-    p.status = static_cast<int32_t*>(workspace);
+    return run_rope(t, dtype, q_heads, batch, nullptr, freq, rotary_dim, factor, interleaved, workspace,
+                    static_cast<cudaStream_t>(stream));
+  }, SPEC_ERR_CUDA);
+}
+
+spec_status_t spec_rope_append_fp4(const spec_rope_tensors_t* t, int dtype, int q_heads, const spec_paged_batch_t* batch,
+                                   const spec_fp4_scales_t* scales, const unsigned long long* freq, int rotary_dim,
+                                   float factor, int interleaved, void* workspace, void* stream) {
+  return guarded([&]() -> spec_status_t {
+    const sv::ApiRange range("spec_rope_append_fp4");
+    if (!scales) return SPEC_ERR_INVALID_ARG;
+    return run_rope(t, dtype, q_heads, batch, scales, freq, rotary_dim, factor, interleaved, workspace,
+                    static_cast<cudaStream_t>(stream));
+  }, SPEC_ERR_CUDA);
+}
+
+spec_status_t spec_fp4_values(const void* codes, long long page, long long token, long long head, const void* scales,
+                              long long s_page, long long s_token, long long s_head, float unit, int pages,
+                              int page_size, int heads, int dim, int dtype, void* out, void* stream) {
+  return guarded([&]() -> spec_status_t {
+    const sv::ApiRange range("spec_fp4_values");
+    if (dtype != SPEC_F32 && dtype != SPEC_BF16 && dtype != SPEC_F16) return SPEC_ERR_INVALID_ARG;
+    if (pages < 0 || page_size < 1 || heads < 1 || dim < 1 || !fp4_unit(unit)) return SPEC_ERR_INVALID_ARG;
+    if (dim % 16 != 0 || dim > 256) return SPEC_ERR_UNSUPPORTED;
+    for (long long x : {page, token, head})
+      if (x < 0 || x % 8 != 0) return SPEC_ERR_INVALID_ARG;
+    for (long long x : {s_page, s_token, s_head})
+      if (x < 0) return SPEC_ERR_INVALID_ARG;
+    if (pages == 0) return SPEC_OK;
+    if (!codes || !scales || !out || !aligned(codes, 8) || !aligned(out, 16)) return SPEC_ERR_INVALID_ARG;
     int sms = 0;
-    if ((st = sm_count(&sms)) != SPEC_OK) return st;
-    return sv::launch_rope(dtype, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+    const spec_status_t st = sm_count(&sms);
+    if (st != SPEC_OK) return st;
+    const sv::Fp4Values p = {static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), page, token, head,
+                             s_page, s_token, s_head, unit, pages, page_size, heads, dim, out};
+    return sv::launch_fp4_values(dtype, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
   }, SPEC_ERR_CUDA);
 }
 

@@ -25,6 +25,14 @@ struct PagedBatch {
   int Hkv, D;
 };
 
+// Scales of a cache held in 4 bits, whose PagedBatch has strides in bytes: every 16 values along a head have
+// one e4m3 scale, a value is unit x scale x e2m1 code (two to a byte, the even one in the low half).
+struct Fp4Scales {
+  uint8_t *k, *v;
+  long long k_page, k_token, k_head, v_page, v_token, v_head;   // bytes
+  int whole;                 // heads fill the kernel's tiles, rows of codes and scales are aligned to their size
+};
+
 // The item that begins in a CTA's run and goes on in others': what the combine kernel joins.
 struct alignas(16) AttnJoin {
   int rows, row0;            // rows of the item (0: no such item), first row
@@ -43,8 +51,10 @@ struct AttnParams {
   int Hq, G;                 // query heads, query heads per key head
   unsigned long long G_inv;  // ceil(2^64 / G), 0 for G = 1
   int lanes;                 // threads that share a request's row tiles when the work is divided
-  int causal, window;
-  float scale_log2;          // softmax scale x log2(e)
+  int causal, window, sinks; // sinks: first tokens that stay visible behind a window
+  float scale_log2;          // softmax scale x log2(e) (x the keys' unit)
+  float v_unit;              // 4-bit caches: the values' unit; else 1
+  Fp4Scales s;               // 4-bit caches
   float* part_o;             // [2 n, BM, D] partial rows of items that more than one CTA works on
   float* part_ml;            // [2 n, BM, 2] their maximum and sum
   AttnJoin* joins;           // [n]
@@ -55,7 +65,11 @@ struct AttnParams {
   int32_t* status;
 };
 
-// Kernel families of the attention: rows per tile, keys per tile.
+// Kernel families of the attention: what the cache holds and whether first tokens stay visible.
+struct AttnForm {
+  bool bf16, sinks, fp4;
+};
+// Rows per tile, keys per tile.
 struct AttnPlan {
   int kind;                  // 0: 16-row tiles, 1: 64-row tiles (mma.sync); 2, 3: 128- and 256-row tiles (tcgen05)
   int bm, bn, grid, smem, dp;
@@ -69,9 +83,11 @@ struct AttnMaps {
 };
 
 int attention_kind(int rows, int D, int page_size, float scale);
-cudaError_t attention_plan(bool bf16, int kind, int rows, int D, int sms, AttnPlan* plan);
+int attention_fp4_kind(int rows, int D, float scale);
+cudaError_t attention_plan(const AttnForm& form, int kind, int rows, int D, int sms, AttnPlan* plan);
 bool attention_maps(bool bf16, const PagedBatch& c, AttnMaps* maps);   // false: TMA cannot describe the caches
-cudaError_t launch_attention(bool bf16, const AttnPlan& plan, const AttnParams& p, const AttnMaps& maps, cudaStream_t stream);
+cudaError_t launch_attention(const AttnForm& form, const AttnPlan& plan, const AttnParams& p, const AttnMaps& maps,
+                             cudaStream_t stream);
 cudaError_t launch_attention_combine(bool bf16, const AttnPlan& plan, const AttnParams& p, cudaStream_t stream);
 
 struct RopeParams {
@@ -85,6 +101,18 @@ struct RopeParams {
   int32_t* status;
 };
 cudaError_t launch_rope(int dtype, const RopeParams& p, int sms, cudaStream_t stream);
+// The same into a cache held in 4 bits.
+cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, float k_unit, float v_unit, int sms,
+                            cudaStream_t stream);
+// What a cache held in 4 bits stands for, [pages, page_size, heads, dim].
+struct Fp4Values {
+  const uint8_t *codes, *scales;
+  long long page, token, head, s_page, s_token, s_head;   // bytes
+  float unit;
+  int pages, page_size, heads, dim;
+  void* out;
+};
+cudaError_t launch_fp4_values(int dtype, const Fp4Values& p, int sms, cudaStream_t stream);
 
 struct SampleParams {
   const void* logits;

@@ -31,6 +31,7 @@ _current_stream = torch._C._cuda_getCurrentRawStream   # torch.cuda.current_stre
 _BATCH = struct.Struct("@PPqqqqqqiiiiPqiiPPi4x")     # spec_paged_batch_t
 _ROPE = struct.Struct("@PPPPPqqqqqqqqqq")            # spec_rope_tensors_t
 _SAMPLING = struct.Struct("@fiffPPPP")               # spec_sampling_t
+_SCALES = struct.Struct("@PPqqqqqqff")               # spec_fp4_scales_t
 
 
 _lib = None
@@ -104,6 +105,96 @@ def _heads(t, name, index, n=None, dim=None):
     return st
 
 
+class FP4Cache:
+    """A paged cache of keys or of values held in 4 bits: what rope_append and chunk_attention take in place of a tensor.
+
+    ``codes`` uint8 [pages, page_size, kv_heads, dim / 2] and ``scales`` float8_e4m3fn [pages, page_size,
+    kv_heads, dim / 16]: a value is unit * scale * code, two e2m1 codes to a byte (the even value low), a scale for
+    every 16 values along a head; 4.5 bits a value.  ``unit`` is a power of two: one that brings the
+    largest values of a block between 0.1 and 2688 keeps all of e4m3's digits.  dim is a multiple of 16,
+    at most 256 (64, 128 and 256 are read fastest).  A fresh cache stands for zeros; its memory is
+    [pages, kv_heads, page_size, ...], where a head's tokens of a page lie together.
+    """
+
+    def __init__(self, pages: int, page_size: int, kv_heads: int, dim: int, unit: float = 1.0, device=None):
+        device = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
+        if dim < 16 or dim % 16 or dim > 256:
+            raise ValueError(f"dim must be a multiple of 16, at most 256, got {dim}")
+        codes = torch.zeros(pages, kv_heads, page_size, dim // 2, dtype=torch.uint8, device=device)
+        scales = torch.zeros(pages, kv_heads, page_size, dim // 16, dtype=torch.uint8, device=device)
+        self._set(codes.transpose(1, 2), scales.view(torch.float8_e4m3fn).transpose(1, 2), unit)
+
+    @classmethod
+    def of(cls, codes, scales, unit: float = 1.0) -> "FP4Cache":
+        """The cache that two tensors hold (they are not copied)."""
+        self = cls.__new__(cls)
+        self._set(codes, scales, unit)
+        return self
+
+    def _set(self, codes, scales, unit):
+        if codes.dtype != torch.uint8 or scales.dtype != torch.float8_e4m3fn:
+            raise TypeError(f"codes and scales must be uint8 and float8_e4m3fn, got {codes.dtype} and {scales.dtype}")
+        s = codes.shape
+        if len(s) != 4 or s[3] % 8 or tuple(scales.shape) != (s[0], s[1], s[2], s[3] // 8):
+            raise ValueError("codes and scales must be [pages, page_size, kv_heads, dim / 2] and [..., dim / 16], got "
+                             f"{tuple(s)} and {tuple(scales.shape)}")
+        if codes.device != scales.device:
+            raise ValueError(f"codes and scales must be on one device, they are on {codes.device} and {scales.device}")
+        if (codes.stride(3) != 1 and s[3] > 1) or (scales.stride(3) != 1 and s[3] > 8):
+            raise ValueError("codes and scales: those of a head must be contiguous")
+        unit = float(unit)
+        if not (2.0 ** -64 <= unit <= 2.0 ** 64 and math.frexp(unit)[0] == 0.5):
+            raise ValueError(f"unit must be a power of two between 2^-64 and 2^64, got {unit}")
+        self.codes, self.scales, self.unit = codes, scales, unit
+        self.shape = (s[0], s[1], s[2], s[3] * 2)
+        self.device = codes.device
+
+    def dim(self) -> int:
+        return 4
+
+    def get_device(self) -> int:
+        return self.codes.get_device()
+
+    def values(self, dtype=torch.bfloat16, *, stream=None):
+        """What the cache stands for, [pages, page_size, kv_heads, dim] (spec_fp4_values); exact in bfloat16
+        and float32."""
+        lib = _lib or _bind()
+        code = _CODES.get(dtype)
+        if code is None:
+            raise TypeError(f"dtype must be float32, bfloat16 or float16, got {dtype}")
+        index = _device()
+        if self.get_device() != index:
+            raise _where(self.codes, "the cache", index)
+        out = _fresh(stream, self.shape, dtype, self.device)
+        if stream is not None:
+            _used_on(stream, self.codes, self.scales)
+        c, s = self.codes.stride(), self.scales.stride()
+        err = lib.spec_fp4_values(self.codes.data_ptr(), c[0], c[1], c[2], self.scales.data_ptr(), s[0], s[1], s[2], self.unit,
+                                  *self.shape, code, out.data_ptr(), _raw_stream(stream, index))
+        if err:
+            _check(err, "spec_fp4_values")
+        return out
+
+
+def _scales(k_cache, v_cache):
+    """spec_fp4_scales_t of two FP4Caches."""
+    k, v = k_cache.scales.stride(), v_cache.scales.stride()
+    return _SCALES.pack(k_cache.scales.data_ptr(), v_cache.scales.data_ptr(), k[0], k[1], k[2], v[0], v[1], v[2],
+                        k_cache.unit, v_cache.unit)
+
+
+def _memory(cache):
+    """The tensors of a cache."""
+    return (cache.codes, cache.scales) if isinstance(cache, FP4Cache) else (cache,)
+
+
+def _both_fp4(k_cache, v_cache):
+    fp4 = isinstance(k_cache, FP4Cache)
+    if fp4 != isinstance(v_cache, FP4Cache):
+        raise TypeError("k_cache and v_cache must both be FP4Cache or both be tensors")
+    return fp4
+
+
 def _batch(k_cache, v_cache, page_table, kv_lens, cu_q, tokens, kv_heads, dim, dtype, index):
     """spec_paged_batch_t of checked tensors."""
     if kv_lens.dtype != torch.int32 or cu_q.dtype != torch.int32:
@@ -119,12 +210,15 @@ def _batch(k_cache, v_cache, page_table, kv_lens, cu_q, tokens, kv_heads, dim, d
     if k_cache.get_device() != index or v_cache.get_device() != index or page_table.get_device() != index:
         bad = next(t for t in (k_cache, v_cache, page_table) if t.get_device() != index)
         raise _where(bad, "k_cache, v_cache and page_table", index)
-    if k_cache.dtype != dtype or v_cache.dtype != dtype:
+    fp4 = _both_fp4(k_cache, v_cache)
+    if not fp4 and (k_cache.dtype != dtype or v_cache.dtype != dtype):
         raise TypeError(f"k_cache and v_cache must be {dtype}, got {k_cache.dtype} and {v_cache.dtype}")
     s = k_cache.shape
     if len(s) != 4 or v_cache.shape != s or s[2] != kv_heads or s[3] != dim:
         raise ValueError(f"k_cache and v_cache must be [pages, page_size, {kv_heads}, {dim}], got {tuple(s)} and "
                          f"{tuple(v_cache.shape)}")
+    if fp4:
+        k_cache, v_cache = k_cache.codes, v_cache.codes
     k0, k1, k2, k3 = k_cache.stride()
     v0, v1, v2, v3 = v_cache.stride()
     if (k3 != 1 or v3 != 1) and dim > 1:
@@ -146,13 +240,15 @@ _ws_bytes: dict = {}
 
 
 def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, *, causal: bool = True,
-                    window: int = 0, scale: Optional[float] = None, want_lse: bool = False, out=None, stream=None,
-                    workspace=None, tuning=None):
-    """Attention of the new tokens q [tokens, q_heads, dim] over the paged cache (spec_chunk_attention).
+                    window: int = 0, sinks: int = 0, scale: Optional[float] = None, want_lse: bool = False, out=None,
+                    stream=None, workspace=None, tuning=None):
+    """Attention of the new tokens q [tokens, q_heads, dim] over the paged cache (spec_chunk_attention; over two
+    FP4Caches spec_chunk_attention_fp4).
 
     ``max_q`` bounds the new tokens of a request.  ``causal``: a token sees the keys up to its own;
     otherwise all of its request.  ``window`` > 0: only keys within that many positions back, its
-    own included (pages wholly behind it may be gone).  ``scale`` defaults to dim ** -0.5.  Returns
+    own included (pages wholly behind it may be gone); the first ``sinks`` keys of a request stay visible behind
+    it (spec_chunk_attention_sinks).  ``scale`` defaults to dim ** -0.5.  Returns
     out [tokens, q_heads, dim], with ``want_lse`` (out, lse [tokens, q_heads] float32); a row that
     sees no key gives 0 and -inf, rows of tokens that no request has stay unwritten.
     ``tuning``: a Tuning, of which the wait limit counts here (spec_chunk_attention_tuned).
@@ -163,7 +259,7 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     if code != 1 and code != 2:
         raise TypeError(f"q must be bfloat16 or float16, got {dtype}")
     index = _device()
-    max_q, window = _int(max_q), _int(window)
+    max_q, window, sinks = _int(max_q), _int(window), _int(sinks)
     q_token, q_head, _ = _heads(q, "q", index)
     n, hq, d = q.shape
     if k_cache.dim() != 4:
@@ -175,17 +271,27 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     elif out.shape != q.shape or out.dtype != dtype or out.get_device() != index or not out.is_contiguous():
         raise ValueError("out must be a contiguous tensor of q's shape, dtype and device")
     lse = _fresh(stream, (n, hq), torch.float32, q.device) if want_lse else None
-    key = (index, code, hq, hkv, d, max_q if max_q < 129 else 129)   # more than 128 rows are all alike
+    fp4 = isinstance(k_cache, FP4Cache)
+    key = (index, code, hq, hkv, d, max_q if max_q < 129 else 129, fp4)   # more than 128 rows are all alike
     need = _ws_bytes.get(key)
     if need is None:
-        need = _ws_bytes[key] = lib.spec_attention_workspace_bytes(code, hq, hkv, d, max_q)
+        size = lib.spec_attention_fp4_workspace_bytes if fp4 else lib.spec_attention_workspace_bytes
+        need = _ws_bytes[key] = size(code, hq, hkv, d, max_q)
     raw = _raw_stream(stream, index)
     buf = _step_buffer(workspace, index, raw, need, stream)
-    args = (q.data_ptr(), q_token, q_head, code, hq, c, max_q, d ** -0.5 if scale is None else scale, causal, window,
-            out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), raw)
     if stream is not None:
-        _used_on(stream, q, k_cache, v_cache, page_table, kv_lens, cu_q, out)
-    err = lib.spec_chunk_attention(*args) if tuning is None else lib.spec_chunk_attention_tuned(*args, tuning.ref())
+        _used_on(stream, q, *_memory(k_cache), *_memory(v_cache), page_table, kv_lens, cu_q, out)
+    q_args = (q.data_ptr(), q_token, q_head, code, hq, c)
+    mask = (max_q, d ** -0.5 if scale is None else scale, causal, window)
+    rest = (out.data_ptr(), None if lse is None else lse.data_ptr(), buf.data_ptr(), buf.numel(), raw)
+    knobs = None if tuning is None else tuning.ref()
+    if fp4:
+        err = lib.spec_chunk_attention_fp4(*q_args, _scales(k_cache, v_cache), *mask, sinks, *rest, knobs)
+    elif sinks:
+        err = lib.spec_chunk_attention_sinks(*q_args, *mask, sinks, *rest, knobs)
+    else:
+        err = lib.spec_chunk_attention(*q_args, *mask, *rest) if tuning is None else \
+            lib.spec_chunk_attention_tuned(*q_args, *mask, *rest, knobs)
     if err:
         _check(err, "spec_chunk_attention")
     return (out, lse) if want_lse else out
@@ -260,7 +366,8 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
     """Rotary positions of the new tokens and the write of rotated keys and values into the paged cache
     (spec_rope_append).
 
-    q [tokens, q_heads, dim], k and v [tokens, kv_heads, dim], float32, bfloat16 or float16.  Returns the
+    q [tokens, q_heads, dim], k and v [tokens, kv_heads, dim], float32, bfloat16 or float16 (into two FP4Caches,
+    spec_rope_append_fp4, one of the last two).  Returns the
     rotated queries (in ``q_out``, which may be q).  ``k_out`` receives the rotated keys too (may be k);
     it is required where k_cache, v_cache and page_table are None and nothing is stored.  Rows of tokens
     that no request has stay unwritten.
@@ -283,6 +390,7 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
         raise _where(rope.turns, "the plan", index)
     v0 = v1 = vp = o0 = o1 = op = 0
     ws = None
+    fp4 = _both_fp4(k_cache, v_cache)
     raw = _raw_stream(stream, index)
     if k_cache is not None:
         v0, v1, _ = _heads(v, "v", index, n, d)
@@ -307,8 +415,10 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
         op = k_out.data_ptr()
     r = _ROPE.pack(q.data_ptr(), k.data_ptr(), vp, q_out.data_ptr(), op, q0, q1, k0, k1, v0, v1, w0, w1, o0, o1)
     if stream is not None:
-        _used_on(stream, q, k, v, rope.turns, k_cache, v_cache, page_table, kv_lens, cu_q, q_out, k_out)
-    err = lib.spec_rope_append(r, code, hq, c, rope.turns.data_ptr(), rope.rotary_dim, rope.factor, rope.interleaved, ws, raw)
+        _used_on(stream, q, k, v, rope.turns, *_memory(k_cache), *_memory(v_cache), page_table, kv_lens, cu_q, q_out, k_out)
+    plan = (rope.turns.data_ptr(), rope.rotary_dim, rope.factor, rope.interleaved, ws, raw)
+    err = lib.spec_rope_append_fp4(r, code, hq, c, _scales(k_cache, v_cache), *plan) if fp4 else \
+        lib.spec_rope_append(r, code, hq, c, *plan)
     if err:
         _check(err, "spec_rope_append")
     return q_out
@@ -400,4 +510,4 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     return out
 
 
-__all__ = ["RopePlan", "SampleOutput", "chunk_attention", "rope_append", "sample_tokens"]
+__all__ = ["FP4Cache", "RopePlan", "SampleOutput", "chunk_attention", "rope_append", "sample_tokens"]

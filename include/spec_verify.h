@@ -422,6 +422,82 @@ spec_status_t spec_rope_append(const spec_rope_tensors_t* t, int dtype, int q_he
                                const unsigned long long* freq, int rotary_dim, float factor, int interleaved,
                                void* workspace, void* stream);
 
+/*
+ * spec_chunk_attention_tuned with `sinks` first tokens that a window does not
+ * hide: over the keys with, for window > 0, t > position of n - window or
+ * t < sinks (without a window they are seen as it is).  sinks 0 is
+ * spec_chunk_attention_tuned.  Pages that lie wholly behind the window of
+ * all the request's new tokens and hold none of the first `sinks` tokens are
+ * not looked at.  SPEC_ERR_INVALID_ARG for sinks < 0.
+ */
+spec_status_t spec_chunk_attention_sinks(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
+                                         const spec_paged_batch_t* batch, int max_q, float scale, int causal, int window,
+                                         int sinks, void* out, float* out_lse, void* workspace, size_t ws_bytes,
+                                         void* stream, const spec_tuning_t* tuning);
+
+/*
+ * A cache held in 4 bits.  The `dim` values of a head are blocks of 16; a
+ * value is unit x scale x code:
+ *   code   e2m1: bit 3 the sign, bits 0-2 one of 0, 0.5, 1, 1.5, 2, 3, 4, 6;
+ *          two to a byte, the even value in the low half: dim / 2 bytes
+ *   scale  e4m3 (the format without infinities): dim / 16 bytes
+ *   unit   a power of two between 2^-64 and 2^64, of all keys (values)
+ * which is 4.5 bits a value.  The codes are the batch's k and v, whose
+ * strides count bytes here; they and the bases are multiples of 8.  Scales
+ * have strides of their own, in bytes, and no alignment (where dim is 64, 128
+ * or 256, and bases and strides are multiples of 16 for codes and of dim / 16
+ * for scales, attention copies them in whole pieces).  dim a multiple of 16,
+ * at most 256.
+ */
+typedef struct spec_fp4_scales {
+  void* k;
+  void* v;
+  long long k_page, k_token, k_head;
+  long long v_page, v_token, v_head;
+  float k_unit, v_unit;
+} spec_fp4_scales_t;
+
+/* Workspace of spec_chunk_attention_fp4, as spec_attention_workspace_bytes. */
+size_t spec_attention_fp4_workspace_bytes(int dtype, int q_heads, int kv_heads, int dim, int max_q);
+
+/*
+ * spec_chunk_attention_sinks over a cache held in 4 bits; dtype is that of q
+ * and out.  Keys and values are taken for what their bits stand for, exactly;
+ * bf16 queries in half precision relative to a power of two at each row's
+ * largest value: what is below 2^-14 of that loses up to 2^-25 of it.  Scales
+ * of tokens that are seen must not be NaN.
+ */
+spec_status_t spec_chunk_attention_fp4(const void* q, long long q_token, long long q_head, int dtype, int q_heads,
+                                       const spec_paged_batch_t* batch, const spec_fp4_scales_t* scales, int max_q,
+                                       float scale, int causal, int window, int sinks, void* out, float* out_lse,
+                                       void* workspace, size_t ws_bytes, void* stream, const spec_tuning_t* tuning);
+
+/*
+ * spec_rope_append into a cache held in 4 bits.  A rotated key is rounded to
+ * fp32 and to its type, and then, as the values v are, held in blocks of 16:
+ *   scale  the e4m3 nearest to (largest magnitude / (6 unit)), within
+ *          [2^-9, 448]; NaN for a block with a NaN
+ *   code   the e2m1 nearest to x / (scale unit); ties to the even code, what
+ *          is beyond 6 (infinities too) to 6.
+ * Scales and codes are those of the exactly rotated key.  k_out receives the
+ * rotated keys as from spec_rope_append.  dtype SPEC_BF16 or SPEC_F16.  One
+ * launch.
+ */
+spec_status_t spec_rope_append_fp4(const spec_rope_tensors_t* t, int dtype, int q_heads, const spec_paged_batch_t* batch,
+                                   const spec_fp4_scales_t* scales, const unsigned long long* freq, int rotary_dim,
+                                   float factor, int interleaved, void* workspace, void* stream);
+
+/*
+ * The values that one array of a cache held in 4 bits stands for, rounded to
+ * dtype (SPEC_F32 and SPEC_BF16 hold them exactly):
+ *   codes, scales  [pages, page_size, heads, dim / 2 and dim / 16], strides
+ *                  in bytes (codes: multiples of 8)
+ *   out            [pages, page_size, heads, dim] contiguous, 16-byte aligned
+ */
+spec_status_t spec_fp4_values(const void* codes, long long page, long long token, long long head, const void* scales,
+                              long long s_page, long long s_token, long long s_head, float unit, int pages,
+                              int page_size, int heads, int dim, int dtype, void* out, void* stream);
+
 /* Sampling settings: a scalar each, or a device array of one per row where its pointer is not NULL. */
 typedef struct spec_sampling {
   float temperature;             /* 0: greedy (a negative one is refused; in an array <= 0 is greedy) */
