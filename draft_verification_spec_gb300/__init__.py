@@ -406,9 +406,10 @@ def draft_budget(draft, tokens, temperature: float, budget: Optional[int] = None
     return n_out, depth, conf
 
 
-from .step import FP4Cache, RopePlan, SampleOutput, chunk_attention, rope_append, sample_tokens  # noqa: E402
+from .step import (FP4Cache, PagePool, RopePlan, SampleOutput, assign_pages, chunk_attention, compact_pages,  # noqa: E402
+                   rope_append, sample_tokens)
 
 __all__ = ["verify_chain", "verify_block", "overlap_alpha", "alloc_budget", "alloc_budget_adaptive",
            "draft_budget", "Workspace", "VerifyOutput", "Tuning", "SpecError", "lib",
            "chunk_attention", "rope_append", "sample_tokens", "RopePlan", "SampleOutput",
-           "FP4Cache"]
+           "FP4Cache", "PagePool", "assign_pages", "compact_pages"]

@@ -62,6 +62,11 @@ SIGNATURES = {
                                      c_void_p, c_void_p]),
     "spec_fp4_values": (c_int, [c_void_p, c_longlong, c_longlong, c_longlong, c_void_p, c_longlong, c_longlong,
                                 c_longlong, c_float, c_int, c_int, c_int, c_int, c_int, c_void_p, c_void_p]),
+    "spec_pages_workspace_bytes": (c_size_t, [c_int, c_int]),
+    "spec_assign_pages": (c_int, [c_void_p, c_int, c_void_p, c_longlong, c_int, c_int, c_void_p, c_void_p, c_void_p,
+                                  c_void_p, c_longlong, c_void_p, c_size_t, c_void_p]),
+    "spec_compact_pages": (c_int, [c_void_p, c_void_p, c_longlong, c_int, c_int, c_void_p, c_longlong, c_void_p,
+                                   c_void_p, c_size_t, c_void_p]),
     "spec_rope_append": (c_int, [c_void_p, c_int, c_int, c_void_p, c_void_p, c_int, c_float, c_int, c_void_p,
                                  c_void_p]),
     "spec_sample_tokens": (c_int, [c_void_p, c_longlong, c_int, c_int, c_int, c_void_p, c_void_p, c_void_p,

@@ -276,6 +276,58 @@ spec_status_t run_rope(const spec_rope_tensors_t* t, int dtype, int q_heads, con
   return sv::launch_rope(dtype, p, sms, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
+// Workspace of the page operators: ints behind the status.
+size_t pages_ints(int pages, int rows) {
+  const size_t copies = static_cast<size_t>(rows > pages / 2 ? rows : pages / 2);
+  return 16 + static_cast<size_t>(rows) + 1 + 2 * copies + 2 * static_cast<size_t>(pages);
+}
+
+spec_status_t run_pages(bool compact, const spec_page_pool_t* pool, int page_size, const int32_t* table, long long stride,
+                        int rows, int width, const int32_t* lens, const int32_t* kept, const int32_t* parents,
+                        int32_t* out_table, long long out_stride, int32_t* out_used, void* workspace, size_t ws_bytes,
+                        cudaStream_t stream) {
+  if (!pool || pool->pages < 1 || pool->n_arrays < 0 || pool->max_bytes < 0 || (pool->n_arrays > 0 && !pool->arrays))
+    return SPEC_ERR_INVALID_ARG;
+  if (rows < 0 || width < 0 || stride < width || out_stride < width || page_size < 1) return SPEC_ERR_INVALID_ARG;
+  if (static_cast<long long>(rows) * width > 0x7fffffffll || pool->max_bytes > (1ll << 40)) return SPEC_ERR_UNSUPPORTED;
+  const bool empty = rows == 0 || width == 0;
+  if (empty && !compact) return SPEC_OK;
+  if ((!empty && (!table || !out_table)) || (compact ? !out_used : !lens || !kept)) return SPEC_ERR_INVALID_ARG;
+  if (!workspace || !aligned(workspace, 256) || ws_bytes < kStatusBytes + 4 * pages_ints(pool->pages, rows))
+    return SPEC_ERR_WORKSPACE;
+  sv::PageParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.arrays = reinterpret_cast<const sv::PageArray*>(pool->arrays);
+  p.n_arrays = pool->n_arrays;
+  p.pages = pool->pages;
+  p.page_size = page_size;
+  p.table = table;
+  p.stride = stride;
+  p.rows = rows;
+  p.width = width;
+  p.lens = lens;
+  p.kept = kept;
+  p.parents = parents;
+  p.out = out_table;
+  p.out_stride = out_stride;
+  p.used = out_used;
+  p.status = static_cast<int32_t*>(workspace);
+  int* ws = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + kStatusBytes);
+  const int copies = rows > p.pages / 2 ? rows : p.pages / 2;
+  p.counts = ws;
+  p.moves = ws + 8;
+  p.starts = ws + 16;
+  p.src = p.starts + rows + 1;
+  p.dst = p.src + copies;
+  p.list = p.dst + copies;
+  p.mark = p.list + p.pages;
+  int sms = 0;
+  const spec_status_t st = sm_count(&sms);
+  if (st != SPEC_OK) return st;
+  std::lock_guard<std::mutex> lk(g_pair);
+  return sv::launch_pages(compact, p, pool->max_bytes, sms, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+}
+
 }  // namespace
 
 extern "C" {
@@ -367,6 +419,31 @@ spec_status_t spec_fp4_values(const void* codes, long long page, long long token
     const sv::Fp4Values p = {static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), page, token, head,
                              s_page, s_token, s_head, unit, pages, page_size, heads, dim, out};
     return sv::launch_fp4_values(dtype, p, sms, static_cast<cudaStream_t>(stream)) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
+  }, SPEC_ERR_CUDA);
+}
+
+size_t spec_pages_workspace_bytes(int pages, int rows) {
+  if (pages < 1 || rows < 0) return 0;
+  return kStatusBytes + (4 * pages_ints(pages, rows) + 255) / 256 * 256;
+}
+
+spec_status_t spec_assign_pages(const spec_page_pool_t* pool, int page_size, const int32_t* table, long long table_stride,
+                                int rows, int width, const int32_t* lens, const int32_t* kept, const int32_t* parents,
+                                int32_t* out_table, long long out_stride, void* workspace, size_t ws_bytes, void* stream) {
+  return guarded([&]() -> spec_status_t {
+    const sv::ApiRange range("spec_assign_pages");
+    return run_pages(false, pool, page_size, table, table_stride, rows, width, lens, kept, parents, out_table, out_stride,
+                     nullptr, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
+  }, SPEC_ERR_CUDA);
+}
+
+spec_status_t spec_compact_pages(const spec_page_pool_t* pool, const int32_t* table, long long table_stride, int rows,
+                                 int width, int32_t* out_table, long long out_stride, int32_t* out_used, void* workspace,
+                                 size_t ws_bytes, void* stream) {
+  return guarded([&]() -> spec_status_t {
+    const sv::ApiRange range("spec_compact_pages");
+    return run_pages(true, pool, 1, table, table_stride, rows, width, nullptr, nullptr, nullptr, out_table, out_stride,
+                     out_used, workspace, ws_bytes, static_cast<cudaStream_t>(stream));
   }, SPEC_ERR_CUDA);
 }
 

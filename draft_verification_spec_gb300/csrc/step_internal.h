@@ -114,6 +114,32 @@ struct Fp4Values {
 };
 cudaError_t launch_fp4_values(int dtype, const Fp4Values& p, int sms, cudaStream_t stream);
 
+// An array of a page pool: page i is `bytes` bytes at base + i stride.
+struct PageArray {
+  uint8_t* base;
+  long long stride, bytes;
+};
+struct PageParams {
+  const PageArray* arrays;   // [n_arrays], device
+  int n_arrays, pages, page_size;
+  const int32_t* table;      // [rows, width], rows `stride` apart
+  long long stride;
+  int rows, width;
+  const int32_t *lens, *kept, *parents;   // assigning: [rows]; parents may be null
+  int32_t* out;              // the new table, rows out_stride apart
+  long long out_stride;
+  int32_t* used;             // compacting: [1]
+  int32_t* status;
+  // workspace
+  int* counts;               // [8] a CTA's share of a count
+  int* moves;                // [1]
+  int* starts;               // [rows + 1] fresh pages of the rows before
+  int *src, *dst;            // [max(rows, pages / 2)] copies (src -1: none)
+  int* list;                 // [pages] free pages
+  int* mark;                 // [pages]
+};
+cudaError_t launch_pages(bool compact, const PageParams& p, long long max_bytes, int sms, cudaStream_t stream);
+
 struct SampleParams {
   const void* logits;
   long long stride;

@@ -32,6 +32,7 @@ _BATCH = struct.Struct("@PPqqqqqqiiiiPqiiPPi4x")     # spec_paged_batch_t
 _ROPE = struct.Struct("@PPPPPqqqqqqqqqq")            # spec_rope_tensors_t
 _SAMPLING = struct.Struct("@fiffPPPP")               # spec_sampling_t
 _SCALES = struct.Struct("@PPqqqqqqff")               # spec_fp4_scales_t
+_POOL = struct.Struct("@Piiq")                       # spec_page_pool_t
 
 
 _lib = None
@@ -424,6 +425,119 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
     return q_out
 
 
+class PagePool:
+    """The arrays that the pages of a pool are made of: tensors and FP4Caches [pages, ...] of one number of pages, keys and
+    values of all layers.  A page must lie in one piece in each.  They must stay where they are while the pool is used;
+    the pool keeps them alive.  ``pages`` is needed only where there are none.
+    """
+
+    def __init__(self, caches, pages: Optional[int] = None):
+        arrays = [t for c in caches for t in _memory(c)]
+        if arrays:
+            pages = arrays[0].shape[0] if pages is None and arrays[0].dim() else pages
+        elif pages is None:
+            raise ValueError("a pool without caches needs pages")
+        device = arrays[0].device if arrays else torch.device("cuda", torch.cuda.current_device())
+        rows, self.max_bytes = [], 0
+        for t in arrays:
+            if t.dim() < 1 or t.shape[0] != pages or t.device != device:
+                raise ValueError(f"every cache must have {pages} pages and be on {device}, got {tuple(t.shape)} on {t.device}")
+            size = 1
+            for n, stride in sorted(zip(t.shape[1:], t.stride()[1:]), key=lambda x: x[1]):
+                if n != 1 and stride != size:
+                    raise ValueError(f"a page must lie in one piece, got strides {t.stride()}")
+                size *= n
+            if pages > 1 and t.stride(0) < size:
+                raise ValueError("pages must not overlap")
+            rows.append((t.data_ptr(), max(t.stride(0), size) * t.element_size(), size * t.element_size()))
+            self.max_bytes = max(self.max_bytes, rows[-1][2])
+        if pages < 1:
+            raise ValueError("a pool needs a page")
+        self.pages, self.caches, self.device = int(pages), list(caches), device
+        self.arrays = torch.tensor(rows, dtype=torch.int64, device=device)
+        self._tensors = arrays
+        self._c = _POOL.pack(self.arrays.data_ptr(), len(rows), self.pages, self.max_bytes)
+
+
+def _pool_call(pool, table, out, stream, workspace):
+    """Checked table and new table, and the workspace of a page operator."""
+    lib = _lib or _bind()
+    index = _device()
+    if pool.device.index != index or pool.device.type != "cuda":
+        raise ValueError(f"the pool must be on the current device cuda:{index}, it is on {pool.device}")
+    for t, name in ((table, "table"),) if out is None else ((table, "table"), (out, "out")):
+        if t.get_device() != index:
+            raise _where(t, name, index)
+        if t.dtype != torch.int32:
+            raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+        if t.dim() != 2:
+            raise ValueError(f"{name} must be [requests, pages of a request], got {tuple(t.shape)}")
+        row, col = t.stride()
+        if (t.shape[1] > 1 and col != 1) or (t.shape[0] > 1 and row < t.shape[1]):
+            raise ValueError(f"{name} must have contiguous rows that do not overlap")
+    if out is None:
+        out = _fresh(stream, tuple(table.shape), torch.int32, table.device)
+    elif out.shape != table.shape:
+        raise ValueError(f"out must have the table's shape {tuple(table.shape)}, got {tuple(out.shape)}")
+    elif table.numel() and _overlap(table, out):
+        raise ValueError("out must not overlap table")
+    raw = _raw_stream(stream, index)
+    buf = _step_buffer(workspace, index, raw, lib.spec_pages_workspace_bytes(pool.pages, table.shape[0]), stream)
+    if stream is not None:
+        _used_on(stream, table, out, pool.arrays, *pool._tensors)
+    stride = lambda t: max(t.stride(0), t.shape[1]) if t.shape[0] > 1 else t.shape[1]  # noqa: E731
+    return lib, out, (table.data_ptr(), stride(table), *table.shape), (out.data_ptr(), stride(out)), \
+        (buf.data_ptr(), buf.numel(), raw)
+
+
+def _per_row(t, name, table):
+    if t.get_device() != table.get_device():
+        raise _where(t, name, table.get_device())
+    if t.dtype != torch.int32 or tuple(t.shape) != (table.shape[0],) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 tensor of {table.shape[0]}")
+    return t.data_ptr()
+
+
+def assign_pages(pool: PagePool, table, lens, page_size: int, *, kept, parents=None, out=None, stream=None, workspace=None):
+    """A new page table [requests, width] in which request b holds the pages of ``lens[b]`` tokens (spec_assign_pages):
+    fork, grow, shrink, reorder and free in one.
+
+    Request b inherits the first min(``kept[b]``, lens[b]) tokens of request ``parents[b]`` of the old ``table`` (None:
+    its own; -1: nobody's).  Whole pages are shared; a page that ends inside will be written to, so one request alone
+    keeps it (the lowest; none where another request reads all of it) and the others get a copy, in every
+    cache of the pool.  Further pages are the lowest ids that nobody inherits, in the order (request, column); -1
+    behind them.  What nobody inherits is free: ``lens`` 0 frees a request.  lens, kept and parents are int32
+    tensors on the device.  Too few free or too long requests show in the workspace's status (SPEC_ERR_PAGE_RANGE), and
+    as -1 in the table.
+    """
+    lib, out, old, new, ws = _pool_call(pool, table, out, stream, workspace)
+    args = [_per_row(lens, "lens", table), _per_row(kept, "kept", table), 0 if parents is None else _per_row(parents, "parents", table)]
+    if stream is not None:
+        _used_on(stream, lens, kept, parents)
+    err = lib.spec_assign_pages(pool._c, _int(page_size), *old, *args, *new, *ws)
+    if err:
+        _check(err, "spec_assign_pages")
+    return out
+
+
+def compact_pages(pool: PagePool, table, *, out=None, used=None, stream=None, workspace=None):
+    """Moves the pages that the table names into the lowest ids, in every cache of the pool (spec_compact_pages).
+
+    Returns the new table and their number u (int32 [1] on the device): pages from u on are free.
+    """
+    if used is not None and (used.dtype != torch.int32 or tuple(used.shape) != (1,) or used.device != table.device):
+        raise ValueError(f"used must be an int32 tensor of 1 on {table.device}")
+    lib, out, old, new, ws = _pool_call(pool, table, out, stream, workspace)
+    if used is None:
+        used = _fresh(stream, (1,), torch.int32, table.device)
+    elif stream is not None:
+        _used_on(stream, used)
+    err = lib.spec_compact_pages(pool._c, *old, *new, used.data_ptr(), *ws)
+    if err:
+        _check(err, "spec_compact_pages")
+    return out, used
+
+
 @dataclass
 class SampleOutput:
     tokens: torch.Tensor                     # [rows] int32; -1 for a row without a logit above -inf
@@ -510,4 +624,5 @@ def sample_tokens(logits, uniforms, temperature=1.0, top_k=0, top_p=1.0, min_p=0
     return out
 
 
-__all__ = ["FP4Cache", "RopePlan", "SampleOutput", "chunk_attention", "rope_append", "sample_tokens"]
+__all__ = ["FP4Cache", "PagePool", "RopePlan", "SampleOutput", "assign_pages", "chunk_attention", "compact_pages", "rope_append",
+           "sample_tokens"]

@@ -498,6 +498,61 @@ spec_status_t spec_fp4_values(const void* codes, long long page, long long token
                               long long s_page, long long s_token, long long s_head, float unit, int pages,
                               int page_size, int heads, int dim, int dtype, void* out, void* stream);
 
+/*
+ * The pages of a paged cache.  A pool is what its pages are made of: arrays
+ * of `pages` pages each (keys, values, scales, of every layer), in which page i
+ * is `bytes` bytes at base + i stride.  Which request holds which is said by
+ * the table alone: a page that no row names is free.  All rows that hold
+ * pages of the pool have to be in the table.
+ */
+typedef struct spec_page_array {
+  void* base;
+  long long stride, bytes;       /* stride >= bytes */
+} spec_page_array_t;
+typedef struct spec_page_pool {
+  const spec_page_array_t* arrays;   /* device array of n_arrays; may be NULL for none */
+  int n_arrays;
+  int pages;
+  long long max_bytes;           /* the largest of their `bytes` */
+} spec_page_pool_t;
+
+/* Workspace of spec_assign_pages and spec_compact_pages (256-byte aligned, as spec_attention_workspace_bytes). */
+size_t spec_pages_workspace_bytes(int pages, int rows);
+
+/*
+ * A new table [rows, width] in which row b holds the pages of lens[b] tokens
+ * (-1 behind them): fork, grow, shrink, reorder and free in one.
+ *   - Row b inherits min(kept[b], lens[b]) tokens from row parents[b] of the
+ *     old table (parents NULL: from itself; outside [0, rows): none).
+ *   - Whole pages are shared by all rows that inherit them.  A page that ends
+ *     inside (kept % page_size != 0) will be written to, so one row alone
+ *     keeps it: the lowest of those that inherit it so, or none of them where
+ *     another row inherits all of it.  The others get a fresh page, and its
+ *     bytes are copied in every array.
+ *   - All further pages are fresh: the lowest ids that no row inherits, in the
+ *     order (row, column).
+ * Lengths below 0 count as 0.  SPEC_ERR_PAGE_RANGE is set, and the entries in
+ * question are -1 (and not copied), where a row is longer than width pages, an
+ * inherited entry is outside [0, pages), or no free page is left.
+ *   lens, kept, parents  device int32 [rows]; pages hold page_size tokens
+ *   out_table            rows out_stride apart; must not overlap table
+ * Results do not depend on timing.  Two launches.
+ */
+spec_status_t spec_assign_pages(const spec_page_pool_t* pool, int page_size, const int32_t* table, long long table_stride,
+                                int rows, int width, const int32_t* lens, const int32_t* kept, const int32_t* parents,
+                                int32_t* out_table, long long out_stride, void* workspace, size_t ws_bytes, void* stream);
+
+/*
+ * Moves the pages that the table names into the lowest ids: of u pages those
+ * with ids >= u go, in rising order, to the unused ids below u, in rising
+ * order, in every array.  out_table names them so (-1 where table has an entry outside
+ * [0, pages); other than -1 it sets SPEC_ERR_PAGE_RANGE); out_used (device
+ * int32 [1]) receives u.  out_table must not overlap table.  Two launches.
+ */
+spec_status_t spec_compact_pages(const spec_page_pool_t* pool, const int32_t* table, long long table_stride, int rows,
+                                 int width, int32_t* out_table, long long out_stride, int32_t* out_used, void* workspace,
+                                 size_t ws_bytes, void* stream);
+
 /* Sampling settings: a scalar each, or a device array of one per row where its pointer is not NULL. */
 typedef struct spec_sampling {
   float temperature;             /* 0: greedy (a negative one is refused; in an array <= 0 is greedy) */

@@ -99,7 +99,7 @@ def bounds(dtype, size, spread, reach, top, keys, dim, bits):
     return size * (1.01 * (u + up) + 2 * score.unsqueeze(-1)) + small.unsqueeze(-1) + tiny, score
 
 
-def assign(table, lens, page_size, pages, kept=None, parents=None):
+def assign(table, lens, page_size, pages, kept, parents=None):
     """New table (lists; -1 none), copies [(src, dst)] and whether everything was found."""
     B, W = len(table), len(table[0]) if table else 0
     parents = list(range(B)) if parents is None else parents
@@ -109,7 +109,7 @@ def assign(table, lens, page_size, pages, kept=None, parents=None):
         n = max(lens[b], 0)
         if n > W * page_size:
             ok, n = False, W * page_size
-        k = min(max(n if kept is None else kept[b], 0), n)
+        k = min(max(kept[b], 0), n)
         if not 0 <= parents[b] < B:
             k = 0
         need.append(-(-n // page_size))
