@@ -19,7 +19,8 @@ LIB = os.path.join(HERE, "libspecverify.so")
 SOURCES = ["row_bf16.cu", "row_f32.cu", "budget_cut.cu", "draft_conf.cu", "api.cu", "static_scratch.cu",
            "attention_mma_bf16.cu", "attention_mma_f16.cu", "attention_tc_bf16.cu", "attention_tc_f16.cu",
            "attention_mma_bf16_sinks.cu", "attention_mma_f16_sinks.cu", "attention_tc_bf16_sinks.cu",
-           "attention_tc_f16_sinks.cu", "attention_fp4_bf16.cu", "attention_fp4_f16.cu",
+           "attention_tc_f16_sinks.cu", "attention_fp4_bf16.cu", "attention_fp4_f16.cu", "attention_tc_bf16_fp4.cu",
+           "attention_tc_f16_fp4.cu",
            "attention.cu", "rope_append.cu", "rope_fp4.cu", "page_pool.cu", "sample_tokens.cu",
            "step_api.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

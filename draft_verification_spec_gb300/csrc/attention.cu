@@ -4,7 +4,6 @@
 #include <mutex>
 #include <tuple>
 
-#include "attention_fp4.cuh"
 #include "attention_tc.cuh"
 
 namespace sv {
@@ -25,6 +24,10 @@ template <>
 const void* attn_tc_fn<true, true>(int dp, bool wide);
 template <>
 const void* attn_tc_fn<false, true>(int dp, bool wide);
+template <>
+const void* attn_tc_fp4_fn<true>(int dp, bool wide);
+template <>
+const void* attn_tc_fp4_fn<false>(int dp, bool wide);
 template <>
 const void* attn_fp4_fn<true>(int dp);
 template <>
@@ -107,6 +110,8 @@ static const void* kernel_of(const AttnPlan& plan) {
   return plan.kind >= 2 ? attn_tc_fn<BF16, SINKS>(plan.dp, plan.kind == 3) : attn_mma_fn<BF16, SINKS>(plan.dp, plan.bm);
 }
 static const void* kernel_of(const AttnForm& form, const AttnPlan& plan) {
+  if (form.fp4 && plan.kind >= 2)
+    return form.bf16 ? attn_tc_fp4_fn<true>(plan.dp, plan.kind == 3) : attn_tc_fp4_fn<false>(plan.dp, plan.kind == 3);
   if (form.fp4) return form.bf16 ? attn_fp4_fn<true>(plan.dp) : attn_fp4_fn<false>(plan.dp);
   if (form.sinks) return form.bf16 ? kernel_of<true, true>(plan) : kernel_of<false, true>(plan);
   return form.bf16 ? kernel_of<true, false>(plan) : kernel_of<false, false>(plan);
@@ -122,7 +127,7 @@ cudaError_t attention_plan(const AttnForm& form, int kind, int rows, int D, int 
   if (kind >= 2) {
     plan->smem = kind == 2 ? (plan->dp == 64 ? AttnTcGeom<64, false>::kSmem : AttnTcGeom<128, false>::kSmem)
                            : (plan->dp == 64 ? AttnTcGeom<64, true>::kSmem : AttnTcGeom<128, true>::kSmem);
-    threads = kTcThreads;
+    threads = form.fp4 ? kTcFp4Threads : kTcThreads;
   } else if (form.fp4) {
     plan->smem = attn_fp4_smem(plan->dp);
   } else {
@@ -147,8 +152,9 @@ int attention_kind(int rows, int D, int page_size, float scale) {
   return rows <= 16 ? 0 : 1;
 }
 
-// Over caches in 4 bits.
+// Over caches in 4 bits: the tcgen05 kernel for more than 16 rows and heads of at most 128 values, else tiles of 16 rows.
 int attention_fp4_kind(int rows, int D, float scale) {
+  if (rows > 16 && D <= 128 && scale > 0.f) return rows > 128 ? 3 : 2;
   return 0;
 }
 
@@ -203,7 +209,7 @@ cudaError_t launch_attention(const AttnForm& form, const AttnPlan& plan, const A
   AttnMaps m = maps;
   void* tc[] = {m.k, m.v, &copy};
   void* mma[] = {&copy};
-  return cudaLaunchKernel(kernel_of(form, plan), dim3(plan.grid), dim3(plan.kind >= 2 ? kTcThreads : kAttnThreads),
+  return cudaLaunchKernel(kernel_of(form, plan), dim3(plan.grid), dim3(plan.kind < 2 ? kAttnThreads : form.fp4 ? kTcFp4Threads : kTcThreads),
                           plan.kind >= 2 ? tc : mma, plan.smem, stream);
 }
 

@@ -69,6 +69,13 @@ __device__ __forceinline__ uint32_t mul2(uint32_t a, uint32_t b) {
   asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
   return r;
 }
+// For queries of bf16 whose largest magnitude in a row is `top`: the power of two that is taken out (2^k <= top < 2^(k+1)),
+// *down its reciprocal.
+__device__ __forceinline__ float fp4_query_power(float top, float* down) {
+  const int e = max(1, min(static_cast<int>(__float_as_uint(top) >> 23), 253));
+  *down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 1.f;
+  return top > 0.f ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 1.f;
+}
 template <int N>
 __device__ __forceinline__ void cp_async_some(uint32_t dst, const void* src, bool valid) {
   const int n = valid ? N : 0;
@@ -212,9 +219,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
       if (BF16) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int e = max(1, min(static_cast<int>(__float_as_uint(top) >> 23), 253));   // 2^(e - 127) <= top < twice that
-        const float down = top > 0.f ? __uint_as_float(static_cast<uint32_t>(254 - e) << 23) : 1.f;
-        factor[i] *= top > 0.f ? __uint_as_float(static_cast<uint32_t>(e) << 23) : 1.f;
+        float down;
+        factor[i] *= fp4_query_power(top, &down);
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s)
 #pragma unroll

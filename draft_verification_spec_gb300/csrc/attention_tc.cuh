@@ -31,18 +31,25 @@
 // 64/8 heads, ragged to 16384 keys (1.11 GB) 218-224 us, 5.0 TB/s, 74 % of the measured copy: 136 rows take two
 // halves of 128.
 //
+// Over caches held in 4 bits (FP4) three warps (8, 10, 11) take the producer's place: they read codes and scales a tile
+// ahead into registers, widen them to f16 (exactly: attention_fp4.cuh) and write them where the TMA boxes would lie; tokens
+// that are not seen become zeros, so nothing has to be cleared, and any page size will do.  The queries of bf16 rows are
+// f16 relative to a power of two at the row's largest value, the probabilities f16 up to 2^14.
+//
 // Every wait is bounded: after `wait_limit` the kernel sets the status word, drains its copies and
 // MMAs, frees TMEM and returns, its record for the combine kernel empty.
 #pragma once
 
 #include <cuda.h>
 
-#include "attention_mma.cuh"
+#include "attention_fp4.cuh"
 #include "spec_async.cuh"
 
 namespace sv {
 
 constexpr int kTcThreads = 352;
+constexpr int kTcFp4Threads = 384;   // 168 registers a thread
+constexpr int kTcLoaders = 3;        // warps that widen 4-bit keys and values
 constexpr int kTcBN = 128;
 
 // WIDE: row tiles of 256 (else 128), which take a second 128-row query buffer.
@@ -197,14 +204,80 @@ struct TcWait {
   }
 };
 
-template <bool BF16, int DP, bool WIDE, bool SINKS>
-__global__ void __launch_bounds__(kTcThreads, 1)
+// A loader's share of a tile's keys (or values) in registers: units of 32 values, 16 bytes of codes and two scales.
+template <int DP>
+struct TcFp4Share {
+  static constexpr int kLanes = DP / 32;             // lanes of a key
+  static constexpr int kKeys = 32 / kLanes;          // keys of a step
+  static constexpr int kSteps = kTcBN / kKeys, kMine = (kSteps + kTcLoaders - 1) / kTcLoaders;
+  uint4 codes[kMine];
+  uint32_t scales[kMine];
+  // This lane's key of its step i (beyond the tile: none).
+  static __device__ __forceinline__ int key(int loader, int i, int lane) { return (i * kTcLoaders + loader) * kKeys + lane / kLanes; }
+  // Reads the units of the keys whose pages are given (-1: zeros); strides in bytes.
+  __device__ __forceinline__ void load(const uint8_t* codes_at, const uint8_t* scales_at, const long long* code_off,
+                                       const long long* scale_off, bool whole, int D, int lane) {
+    const int c = lane % kLanes;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      codes[i] = make_uint4(0, 0, 0, 0);
+      scales[i] = 0;
+      if (code_off[i] < 0 || c * 32 >= D) continue;
+      const uint8_t* x = codes_at + code_off[i] + c * 16;
+      const uint8_t* y = scales_at + scale_off[i] + c * 2;
+      if (whole) {
+        codes[i] = __ldg(reinterpret_cast<const uint4*>(x));
+        scales[i] = __ldg(reinterpret_cast<const uint16_t*>(y));
+      } else {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(x));
+        codes[i].x = a.x;
+        codes[i].y = a.y;
+        scales[i] = __ldg(y);
+        if (c * 32 + 16 < D) {
+          const uint2 b = __ldg(reinterpret_cast<const uint2*>(x) + 1);
+          codes[i].z = b.x;
+          codes[i].w = b.y;
+          scales[i] |= static_cast<uint32_t>(__ldg(y + 1)) << 8;
+        }
+      }
+    }
+  }
+  // Writes them as f16 into a tile: 64-value blocks of 128 rows of 128 bytes, 16-byte pieces permuted by the row.  The
+  // lanes of a store phase (8 units) take their four pieces in orders that fall on distinct banks.
+  __device__ __forceinline__ void store(uint32_t tile, int loader, int lane) const {
+    const int c = lane % kLanes;
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int r = key(loader, i, lane);
+      if (r >= kTcBN) continue;
+      const uint32_t two = fp4_scales(scales[i]), f0 = __byte_perm(two, two, 0x1010), f1 = __byte_perm(two, two, 0x3232);
+      const uint32_t at = tile + (c / 2) * 16384 + r * 128;
+      const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int o = c >= 2 ? k ^ 2 : k;            // the word of this store
+        const uint32_t word = c >= 2 ? w[k ^ 2] : w[k], f = (c >= 2) == (k < 2) ? f1 : f0;
+        uint32_t v[4];
+        fp4_pairs(word, v);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((((c & 1) * 4 + o) ^ (r & 7)) << 4)),
+                     "r"(mul2(v[0], f)), "r"(mul2(v[1], f)), "r"(mul2(v[2], f)), "r"(mul2(v[3], f))
+                     : "memory");
+      }
+    }
+  }
+};
+
+template <bool BF16, int DP, bool WIDE, bool SINKS, bool FP4>
+__global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   using A = AttnType<BF16>;
+  using M = AttnType<BF16 && !FP4>;   // the products' operands
+  constexpr int THREADS = FP4 ? kTcFp4Threads : kTcThreads;
+  constexpr float kShift = FP4 ? kFp4Shift : 0.f;   // of the probabilities, in powers of two
   using Geo = AttnTcGeom<DP, WIDE>;
   constexpr int BM = Geo::kBM, BN = kTcBN, SUB = DP / 64, KST = Geo::kKStages, VST = Geo::kVStages, TILE = Geo::kTile;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ AttnSchedSmem<kTcThreads> sched;
+  __shared__ AttnSchedSmem<THREADS> sched;
   __shared__ __align__(8) AttnTcBars bars;
   __shared__ float2 s_ml[128];
   __shared__ uint32_t s_tmem;
@@ -236,9 +309,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     attn_leave_join(p, split, cta, BM, nullptr, false);
     s_abort = 0;
     for (int i = 0; i < 5; ++i) {
-      mbar_init(smem_addr(&bars.k_full[i]), 1);
+      mbar_init(smem_addr(&bars.k_full[i]), FP4 ? kTcLoaders : 1);
       mbar_init(smem_addr(&bars.k_empty[i]), 1);
-      mbar_init(smem_addr(&bars.v_full[i]), 1);
+      mbar_init(smem_addr(&bars.v_full[i]), FP4 ? kTcLoaders : 1);
       mbar_init(smem_addr(&bars.v_empty[i]), 1);
       mbar_init(smem_addr(&bars.clean_me[i]), 1);
       mbar_init(smem_addr(&bars.v_clean[i]), 1);
@@ -265,7 +338,69 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   const TcWait wait{&s_abort, p.wait_limit, p.status};
   unsigned issued = 0;   // producer: key tiles whose copies were issued
 
-  if (warp == 8) {
+  if (FP4 && warp >= 8 && warp != 9) {
+    // ------------------------------------------------------------------ loaders of 4-bit keys and values
+    using Share = TcFp4Share<DP>;
+    const int loader = warp == 8 ? 0 : warp - 9, P = p.c.page_size;
+    Share k_share, v_share;
+    long long k_off[Share::kMine], v_off[Share::kMine], ks_off[Share::kMine], vs_off[Share::kMine];   // -1: zeros
+    int j = 0;   // tile of the item
+    // the places of this lane's keys of tile j of the item
+    auto look_up = [&] {
+      const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
+      int lo, hi;
+      attn_keys(p, cur.req, r0, r1, &lo, &hi);
+      const int32_t* table = p.c.table + static_cast<long long>(cur.b) * p.c.table_stride;
+      const int key0 = cur.template tile<SINKS>(k0 + j) * BN;
+#pragma unroll
+      for (int i = 0; i < Share::kMine; ++i) {
+        const int r = Share::key(loader, i, lane), key = key0 + r;
+        k_off[i] = -1;
+        if (r >= BN || key >= hi || (key < lo && !(SINKS && key < p.sinks))) continue;
+        const int col = key / P, in = key - col * P, pg = __ldg(table + col);
+        if (pg < 0 || pg >= p.c.pages) {
+          atomicOr(p.status, kStatusPageRange);
+          continue;
+        }
+        k_off[i] = pg * p.c.k_page + in * p.c.k_token + cur.h * p.c.k_head;
+        v_off[i] = pg * p.c.v_page + in * p.c.v_token + cur.h * p.c.v_head;
+        ks_off[i] = pg * p.s.k_page + in * p.s.k_token + cur.h * p.s.k_head;
+        vs_off[i] = pg * p.s.v_page + in * p.s.v_token + cur.h * p.s.v_head;
+      }
+#pragma unroll
+      for (int i = 0; i < Share::kMine; ++i)
+        if (k_off[i] < 0) v_off[i] = -1;
+    };
+    // the next tile of this CTA
+    auto next_tile = [&]() -> bool {
+      if (++j < k1 - k0) return true;
+      if (!attn_next<BN, SINKS>(p, BM, u_end, &cur)) return false;
+      cur.share(p, u_begin, u_end, &k0, &k1);
+      j = 0;
+      return true;
+    };
+    look_up();
+    k_share.load(p.c.k, p.s.k, k_off, ks_off, p.s.whole, p.c.D, lane);
+    v_share.load(p.c.v, p.s.v, v_off, vs_off, p.s.whole, p.c.D, lane);
+    bool ok = p.wait_limit > 0 || wait.give_up();
+    for (unsigned g = 0; ok; ++g) {   // key tiles of this CTA so far
+      const bool more = next_tile();
+      if (more) look_up();
+      ok = wait.warp(smem_addr(&bars.k_empty[g % KST]), (g / KST & 1) ^ 1);
+      if (!ok) break;
+      k_share.store(s_k + g % KST * TILE, loader, lane);
+      fence_async_smem();
+      mbar_arrive_warp(smem_addr(&bars.k_full[g % KST]));
+      if (more) k_share.load(p.c.k, p.s.k, k_off, ks_off, p.s.whole, p.c.D, lane);
+      ok = wait.warp(smem_addr(&bars.v_empty[g % VST]), (g / VST & 1) ^ 1);
+      if (!ok) break;
+      v_share.store(s_v + g % VST * TILE, loader, lane);
+      fence_async_smem();
+      mbar_arrive_warp(smem_addr(&bars.v_full[g % VST]));
+      if (!more) break;
+      v_share.load(p.c.v, p.s.v, v_off, vs_off, p.s.whole, p.c.D, lane);
+    }
+  } else if (!FP4 && warp == 8) {
     // ------------------------------------------------------------------------------ TMA producer
     const int P = p.c.page_size, rows = min(P, BN), boxes = BN / rows;   // boxes of 64 dims per tile
     unsigned g = 0;                                                      // key tiles of this CTA so far
@@ -316,7 +451,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // -------------------------------------------------------------------------------- MMA issuer
     // The whole loop runs in one elected thread: a warp-wide wait costs three times a thread's, and
     // whatever the issuer spends between two products is time the tensor core stands still.
-    constexpr uint32_t kType = BF16 ? 1u : 0u;
+    constexpr uint32_t kType = BF16 && !FP4 ? 1u : 0u;
     constexpr uint32_t kCommon = (1u << 4) | (kType << 7) | (kType << 10) | ((128u >> 4) << 24);
     constexpr uint32_t kIdescS = kCommon | ((128u >> 3) << 17);
     constexpr uint32_t kIdescO = kCommon | (1u << 16) | ((static_cast<uint32_t>(DP) >> 3) << 17);
@@ -387,7 +522,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         for (int j = 0; ok && j < len; ++j) {
           ok = wait(vr.full, vr.phase);
-          if (ok && j >= clean_from) {
+          if (!FP4 && ok && j >= clean_from) {
             ok = wait(smem_addr(&bars.v_clean[vr.slot]), cleaned >> vr.slot & 1);
             cleaned ^= 1u << vr.slot;
           }
@@ -427,7 +562,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp == 10) {
+  } else if (!FP4 && warp == 10) {
     // ---------------------------------------------------------------- value rows behind the last key
     // The producer asks for a slot after it has armed the slot's v_full; the slot is not armed again
     // before the issuer has seen it cleared, so no phase of the three barriers is ever missed.
@@ -472,7 +607,45 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int h0 = r0 + (joined ? 0 : half * 128), r = h0 + row;
       const bool mine = r < r1;
       const bool busy = h0 + (warp & 3) * 32 < r1;   // some row of this warp exists
-      if (half == 0 || !joined) {
+      float scale_log2 = p.scale_log2;
+      if constexpr (FP4) {
+        // the row in f16; both halves need its power of two, the one that owns it writes it
+        const int tok = cur.req.q0 + attn_token(p, r), head = cur.h * p.G + r - (attn_token(p, r)) * p.G;
+        const uint8_t* src = p.q + (tok * p.q_token + head * p.q_head) * 2;
+        float down = 1.f;
+        if (BF16) {
+          float top = 0.f;
+#pragma unroll
+          for (int c = 0; c < DP / 8; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (mine && c * 8 < p.c.D) v = __ldg(reinterpret_cast<const uint4*>(src + c * 16));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xffff0000u))));
+          }
+          scale_log2 *= fp4_query_power(top, &down);
+        }
+        if (half == 0 || !joined) {
+          const uint32_t dst = s_q + half * TILE + row * 128;
+#pragma unroll
+          for (int c = 0; c < DP / 8; ++c) {
+            uint4 v = make_uint4(0, 0, 0, 0);
+            if (mine && c * 8 < p.c.D) v = __ldg(reinterpret_cast<const uint4*>(src + c * 16));
+            uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            if (BF16) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                w[e] = M::pack(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xffff0000u) * down);
+            }
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)),
+                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
+                         : "memory");
+          }
+          fence_async_smem();
+          mbar_arrive_warp(smem_addr(&bars.q_full[half]));
+        }
+      } else if (half == 0 || !joined) {
         const int tok = cur.req.q0 + attn_token(p, r), head = cur.h * p.G + r - (attn_token(p, r)) * p.G;
         const uint8_t* src = p.q + (tok * p.q_token + head * p.q_head) * 2;
         const uint32_t dst = s_q + half * TILE + row * 128;
@@ -511,11 +684,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           const int key0 = cur.template tile<SINKS>(k0 + j) * BN, lo = row_lo - key0, hi = row_hi - key0;
           const int sinks = SINKS ? p.sinks - key0 : 0;
           const bool masked = key0 + BN > w_hi || key0 < w_lo;
-          const uint64_t scale2 = f2_pack(p.scale_log2, p.scale_log2);
+          const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
           uint32_t pk[64];
           while (true) {
             const float ref = m == ninf() ? 0.f : m;
-            const uint64_t ref2 = f2_pack(-ref, -ref);
+            const uint64_t ref2 = f2_pack(kShift - ref, kShift - ref);
             uint32_t s[2][32];
             float t[4] = {ninf(), ninf(), ninf(), ninf()};
             uint64_t sum[2] = {0ull, 0ull};
@@ -539,11 +712,11 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                 e0 = ex2(e0);
                 e1 = ex2(e1);
                 sum[i & 1] = f2_add(sum[i & 1], f2_pack(e0, e1));
-                pk[c * 16 + i] = A::pack(e0, e1);
+                pk[c * 16 + i] = M::pack(e0, e1);
               }
             }
             // in units of the scaled scores (the scale is positive)
-            const float top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * p.scale_log2);
+            const float top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale_log2);
             const bool grow = top - m > 8.f || (m == ninf() && top > m);
             if (!__any_sync(0xffffffffu, grow)) {
               float a, b, c, d;
@@ -602,7 +775,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (half == 0 || !joined) {
         const bool whole = len == cur.count;
-        const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        const float inv = whole ? (l > 0.f ? (FP4 ? p.v_unit : 1.f) / l : 0.f) : 1.f;
         f0 *= inv;
         f1 *= inv;
         const bool both = joined && len > 1;
@@ -641,9 +814,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (mine) {
           if (!whole)
-            *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m, l);
+            *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m - kShift, l);
           else if (p.lse)
-            p.lse[orow] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : ninf();
+            p.lse[orow] = l > 0.f ? (m - kShift + log2f(l)) * 0.69314718055994531f : ninf();
         }
         tc_fence_before();
         if (joined) mbar_arrive_warp(smem_addr(&bars.x_free));
@@ -660,7 +833,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 8 && s_abort) {   // gave up: the copies in flight still land before the block's memory is given back
+  if (!FP4 && warp == 8 && s_abort) {   // gave up: the copies in flight still land before the block's memory is given back
     for (unsigned i = issued > KST + VST ? issued - KST - VST : 0; i <= issued; ++i) {
       const unsigned long long t0 = global_ns();
       while (!(mbar_try(smem_addr(&bars.k_full[i % KST]), (i / KST) & 1) && mbar_try(smem_addr(&bars.v_full[i % VST]), (i / VST) & 1)) &&
@@ -676,5 +849,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
 
 template <bool BF16, bool SINKS>
 const void* attn_tc_fn(int dp, bool wide);
+template <bool BF16>
+const void* attn_tc_fp4_fn(int dp, bool wide);
 
 }  // namespace sv

@@ -6,10 +6,10 @@ namespace sv {
 template <>
 const void* attn_tc_fn<false, true>(int dp, bool wide) {
   if (wide)
-    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<false, 64, true, true>)
-                    : reinterpret_cast<const void*>(&attn_tc_kernel<false, 128, true, true>);
-  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<false, 64, false, true>)
-                  : reinterpret_cast<const void*>(&attn_tc_kernel<false, 128, false, true>);
+    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<false, 64, true, true, false>)
+                    : reinterpret_cast<const void*>(&attn_tc_kernel<false, 128, true, true, false>);
+  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<false, 64, false, true, false>)
+                  : reinterpret_cast<const void*>(&attn_tc_kernel<false, 128, false, true, false>);
 }
 
 }  // namespace sv

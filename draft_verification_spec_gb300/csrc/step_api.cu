@@ -182,7 +182,7 @@ spec_status_t run_attention(const AttentionCall& a) {
   const int G = a.q_heads / batch->kv_heads;
   const long long all_rows = static_cast<long long>(a.max_q) * G;
   const int rows = static_cast<int>(all_rows < 1024 ? all_rows : 1024);
-  sv::AttnMaps maps;
+  sv::AttnMaps maps = {};
   int kind = fp4 ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);
   if (!fp4 && kind >= 2 && !sv::attention_maps(form.bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
   sv::AttnPlan plan;
