@@ -48,8 +48,8 @@
 namespace sv {
 
 constexpr int kTcThreads = 352;
-constexpr int kTcFp4Threads = 384;   // 168 registers a thread
-constexpr int kTcLoaders = 3;        // warps that widen 4-bit keys and values
+constexpr int kTcLoaders = 7;        // warps that widen 4-bit keys and values
+constexpr int kTcFp4Threads = 32 * (9 + kTcLoaders);
 constexpr int kTcBN = 128;
 
 // WIDE: row tiles of 256 (else 128), which take a second 128-row query buffer.
@@ -210,25 +210,37 @@ struct TcFp4Share {
   static constexpr int kLanes = DP / 32;             // lanes of a key
   static constexpr int kKeys = 32 / kLanes;          // keys of a step
   static constexpr int kSteps = kTcBN / kKeys, kMine = (kSteps + kTcLoaders - 1) / kTcLoaders;
+  static constexpr int kRounds = (kMine * kKeys + 31) / 32;   // keys of a loader's share, 32 at a time
+  static_assert(32 % kKeys == 0, "a step's keys are held by consecutive lanes");
   uint4 codes[kMine];
-  uint32_t scales[kMine];
-  // This lane's key of its step i (beyond the tile: none).
-  static __device__ __forceinline__ int key(int loader, int i, int lane) { return (i * kTcLoaders + loader) * kKeys + lane / kLanes; }
-  // Reads the units of the keys whose pages are given (-1: zeros); strides in bytes.
-  __device__ __forceinline__ void load(const uint8_t* codes_at, const uint8_t* scales_at, const long long* code_off,
-                                       const long long* scale_off, bool whole, int D, int lane) {
-    const int c = lane % kLanes;
+  uint16_t scales[kMine];
+  // This lane's key of its step i (at or beyond the tile's end: none).  Lanes 0 to 7 have 8 keys (16 where a key is two
+  // lanes' work) and the same place in them, so that a store phase falls on distinct banks.
+  static __device__ __forceinline__ int key(int loader, int i, int lane) { return (i * kTcLoaders + loader) * kKeys + lane % kKeys; }
+  // Reads the units of the keys whose pages and slots the warp's lanes hold (lane n: key n of its share; page below 0: zeros).
+  // Strides are below 2^32 (the host sees to it): a product with one is one instruction.
+  __device__ __forceinline__ void load(const uint8_t* codes_at, uint32_t page, uint32_t token, const uint8_t* scales_at,
+                                       uint32_t s_page, uint32_t s_token, const int (&pg)[kRounds], const int (&in)[kRounds],
+                                       bool whole, int D, int lane) {
+    const int c = lane / kKeys;
+    auto wide = [](int a, uint32_t b) { return static_cast<unsigned long long>(static_cast<uint32_t>(a)) * b; };
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      codes[i] = make_uint4(0, 0, 0, 0);
-      scales[i] = 0;
-      if (code_off[i] < 0 || c * 32 >= D) continue;
-      const uint8_t* x = codes_at + code_off[i] + c * 16;
-      const uint8_t* y = scales_at + scale_off[i] + c * 2;
+      const int at = i * kKeys + lane % kKeys;
+      const int q = __shfl_sync(0xffffffffu, pg[i * kKeys / 32], at % 32), slot = __shfl_sync(0xffffffffu, in[i * kKeys / 32], at % 32);
+      const uint8_t* x = codes_at + wide(q, page) + wide(slot, token) + c * 16;
+      const uint8_t* y = scales_at + wide(q, s_page) + wide(slot, s_token) + c * 2;
       if (whole) {
-        codes[i] = __ldg(reinterpret_cast<const uint4*>(x));
-        scales[i] = __ldg(reinterpret_cast<const uint16_t*>(y));
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+            "mov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\tmov.b16 %4, 0;\n\t"
+            "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%6];\n\t@p ld.global.nc.b16 %4, [%7];\n\t}"
+            : "=&r"(codes[i].x), "=&r"(codes[i].y), "=&r"(codes[i].z), "=&r"(codes[i].w), "=&h"(scales[i])
+            : "r"(q), "l"(x), "l"(y));
       } else {
+        codes[i] = make_uint4(0, 0, 0, 0);
+        scales[i] = 0;
+        if (q < 0 || c * 32 >= D) continue;
         const uint2 a = __ldg(reinterpret_cast<const uint2*>(x));
         codes[i].x = a.x;
         codes[i].y = a.y;
@@ -237,30 +249,28 @@ struct TcFp4Share {
           const uint2 b = __ldg(reinterpret_cast<const uint2*>(x) + 1);
           codes[i].z = b.x;
           codes[i].w = b.y;
-          scales[i] |= static_cast<uint32_t>(__ldg(y + 1)) << 8;
+          scales[i] = static_cast<uint16_t>(scales[i] | __ldg(y + 1) << 8);
         }
       }
     }
   }
-  // Writes them as f16 into a tile: 64-value blocks of 128 rows of 128 bytes, 16-byte pieces permuted by the row.  The
-  // lanes of a store phase (8 units) take their four pieces in orders that fall on distinct banks.
+  // Writes them as f16 into a tile: 64-value blocks of 128 rows of 128 bytes, 16-byte pieces permuted by the row.
   __device__ __forceinline__ void store(uint32_t tile, int loader, int lane) const {
-    const int c = lane % kLanes;
+    const int c = lane / kKeys;
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const int r = key(loader, i, lane);
-      if (r >= kTcBN) continue;
+      if (i * kTcLoaders + loader >= kSteps) break;   // the same for the whole warp
       const uint32_t two = fp4_scales(scales[i]), f0 = __byte_perm(two, two, 0x1010), f1 = __byte_perm(two, two, 0x3232);
-      const uint32_t at = tile + (c / 2) * 16384 + r * 128;
+      const uint32_t at = tile + (c / 2) * 16384 + r * 128 + ((((c & 1) * 4) ^ (r & 7)) << 4);
       const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
-        const int o = c >= 2 ? k ^ 2 : k;            // the word of this store
-        const uint32_t word = c >= 2 ? w[k ^ 2] : w[k], f = (c >= 2) == (k < 2) ? f1 : f0;
+        const uint32_t f = k < 2 ? f0 : f1;
         uint32_t v[4];
-        fp4_pairs(word, v);
-        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + ((((c & 1) * 4 + o) ^ (r & 7)) << 4)),
-                     "r"(mul2(v[0], f)), "r"(mul2(v[1], f)), "r"(mul2(v[2], f)), "r"(mul2(v[3], f))
+        fp4_pairs(w[k], v);
+        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at ^ (k << 4)), "r"(mul2(v[0], f)), "r"(mul2(v[1], f)),
+                     "r"(mul2(v[2], f)), "r"(mul2(v[3], f))
                      : "memory");
       }
     }
@@ -340,65 +350,111 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
 
   if (FP4 && warp >= 8 && warp != 9) {
     // ------------------------------------------------------------------ loaders of 4-bit keys and values
+    // In the order in which the issuer asks: keys of tile g + 1, values of tile g.  Both were read a tile before, and the
+    // page ids for that a tile before that, so no latency of the table or of memory stands between two tiles.
     using Share = TcFp4Share<DP>;
     const int loader = warp == 8 ? 0 : warp - 9, P = p.c.page_size;
-    Share k_share, v_share;
-    long long k_off[Share::kMine], v_off[Share::kMine], ks_off[Share::kMine], vs_off[Share::kMine];   // -1: zeros
-    int j = 0;   // tile of the item
-    // the places of this lane's keys of tile j of the item
-    auto look_up = [&] {
-      const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
-      int lo, hi;
-      attn_keys(p, cur.req, r0, r1, &lo, &hi);
-      const int32_t* table = p.c.table + static_cast<long long>(cur.b) * p.c.table_stride;
-      const int key0 = cur.template tile<SINKS>(k0 + j) * BN;
-#pragma unroll
-      for (int i = 0; i < Share::kMine; ++i) {
-        const int r = Share::key(loader, i, lane), key = key0 + r;
-        k_off[i] = -1;
-        if (r >= BN || key >= hi || (key < lo && !(SINKS && key < p.sinks))) continue;
-        const int col = key / P, in = key - col * P, pg = __ldg(table + col);
-        if (pg < 0 || pg >= p.c.pages) {
-          atomicOr(p.status, kStatusPageRange);
-          continue;
-        }
-        k_off[i] = pg * p.c.k_page + in * p.c.k_token + cur.h * p.c.k_head;
-        v_off[i] = pg * p.c.v_page + in * p.c.v_token + cur.h * p.c.v_head;
-        ks_off[i] = pg * p.s.k_page + in * p.s.k_token + cur.h * p.s.k_head;
-        vs_off[i] = pg * p.s.v_page + in * p.s.v_token + cur.h * p.s.v_head;
-      }
-#pragma unroll
-      for (int i = 0; i < Share::kMine; ++i)
-        if (k_off[i] < 0) v_off[i] = -1;
+    struct Places {   // of a tile's keys: lane n has page (below 0: none) and slot of key n of the warp's share
+      int pg[Share::kRounds], in[Share::kRounds], head;
+      bool there;     // there is such a tile
     };
-    // the next tile of this CTA
-    auto next_tile = [&]() -> bool {
-      if (++j < k1 - k0) return true;
-      if (!attn_next<BN, SINKS>(p, BM, u_end, &cur)) return false;
+    int lo, hi, j = 0;   // the item's keys; its tile that is fetched next
+    const int32_t* table;
+    auto begin_item = [&] {
+      const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
+      attn_keys(p, cur.req, r0, r1, &lo, &hi);
+      table = p.c.table + static_cast<long long>(cur.b) * p.c.table_stride;
+    };
+    begin_item();
+    bool left = true;    // a tile is left to fetch
+    auto fetch = [&](Places& x) {
+      x.there = left;
+      if (!left) return;
+      const int key0 = cur.template tile<SINKS>(k0 + j) * BN;
+      x.head = cur.h;
+#pragma unroll
+      for (int n = 0; n < Share::kRounds; ++n) {
+        const int at = n * 32 + lane;
+        const int r = (at / Share::kKeys * kTcLoaders + loader) * Share::kKeys + at % Share::kKeys, key = key0 + r;
+        x.pg[n] = -1;
+        x.in[n] = -1;
+        if (r < BN && key < hi && (key >= lo || (SINKS && key < p.sinks))) {
+          const int col = key / P;
+          x.in[n] = key - col * P;
+          x.pg[n] = __ldg(table + col);
+        }
+      }
+      if (++j < k1 - k0) return;
+      left = attn_next<BN, SINKS>(p, BM, u_end, &cur);
+      if (!left) return;
       cur.share(p, u_begin, u_end, &k0, &k1);
+      begin_item();
       j = 0;
+    };
+    // Page ids outside the cache are reported and read as zeros.
+    auto settle = [&](Places& x) {
+#pragma unroll
+      for (int n = 0; n < Share::kRounds; ++n) {
+        const bool bad = x.pg[n] < 0 || x.pg[n] >= p.c.pages;
+        if (bad && x.in[n] >= 0) atomicOr(p.status, kStatusPageRange);
+        if (bad) x.pg[n] = -1;
+      }
+    };
+    Share k, v;
+    auto load_k = [&](const Places& x) {
+      k.load(p.c.k + x.head * p.c.k_head, static_cast<uint32_t>(p.c.k_page), static_cast<uint32_t>(p.c.k_token),
+             p.s.k + x.head * p.s.k_head, static_cast<uint32_t>(p.s.k_page), static_cast<uint32_t>(p.s.k_token), x.pg, x.in,
+             p.s.whole, p.c.D, lane);
+    };
+    auto load_v = [&](const Places& x) {
+      v.load(p.c.v + x.head * p.c.v_head, static_cast<uint32_t>(p.c.v_page), static_cast<uint32_t>(p.c.v_token),
+             p.s.v + x.head * p.s.v_head, static_cast<uint32_t>(p.s.v_page), static_cast<uint32_t>(p.s.v_token), x.pg, x.in,
+             p.s.whole, p.c.D, lane);
+    };
+    bool ok = p.wait_limit > 0 || wait.give_up();
+    unsigned g = 0;   // key tiles of this CTA so far
+    auto put_k = [&](unsigned n) -> bool {
+      const unsigned st = n % KST;
+      if (!wait.warp(smem_addr(&bars.k_empty[st]), (n / KST & 1) ^ 1)) return false;
+      k.store(s_k + st * TILE, loader, lane);
+      fence_async_smem();
+      mbar_arrive_warp(smem_addr(&bars.k_full[st]));
       return true;
     };
-    look_up();
-    k_share.load(p.c.k, p.s.k, k_off, ks_off, p.s.whole, p.c.D, lane);
-    v_share.load(p.c.v, p.s.v, v_off, vs_off, p.s.whole, p.c.D, lane);
-    bool ok = p.wait_limit > 0 || wait.give_up();
-    for (unsigned g = 0; ok; ++g) {   // key tiles of this CTA so far
-      const bool more = next_tile();
-      if (more) look_up();
-      ok = wait.warp(smem_addr(&bars.k_empty[g % KST]), (g / KST & 1) ^ 1);
-      if (!ok) break;
-      k_share.store(s_k + g % KST * TILE, loader, lane);
+    auto put_v = [&](unsigned n) -> bool {
+      const unsigned st = n % VST;
+      if (!wait.warp(smem_addr(&bars.v_empty[st]), (n / VST & 1) ^ 1)) return false;
+      v.store(s_v + st * TILE, loader, lane);
       fence_async_smem();
-      mbar_arrive_warp(smem_addr(&bars.k_full[g % KST]));
-      if (more) k_share.load(p.c.k, p.s.k, k_off, ks_off, p.s.whole, p.c.D, lane);
-      ok = wait.warp(smem_addr(&bars.v_empty[g % VST]), (g / VST & 1) ^ 1);
-      if (!ok) break;
-      v_share.store(s_v + g % VST * TILE, loader, lane);
-      fence_async_smem();
-      mbar_arrive_warp(smem_addr(&bars.v_full[g % VST]));
-      if (!more) break;
-      v_share.load(p.c.v, p.s.v, v_off, vs_off, p.s.whole, p.c.D, lane);
+      mbar_arrive_warp(smem_addr(&bars.v_full[st]));
+      return true;
+    };
+    Places now, next, after;   // tiles g, g + 1, g + 2
+    fetch(now);
+    fetch(next);
+    fetch(after);
+    settle(now);
+    load_k(now);
+    load_v(now);
+    ok = ok && put_k(0);
+    if (next.there) {
+      settle(next);
+      load_k(next);
+    }
+    while (ok) {
+      if (next.there) {
+        if (!(ok = put_k(g + 1))) break;
+        if (after.there) {
+          settle(after);
+          load_k(after);
+        }
+      }
+      if (!(ok = put_v(g))) break;
+      if (!next.there) break;
+      load_v(next);
+      next = after;
+      fetch(after);
+      ++g;
     }
   } else if (!FP4 && warp == 8) {
     // ------------------------------------------------------------------------------ TMA producer
@@ -677,7 +733,87 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
         ok = wait.warp(bar_s, tiles & 1);
         if (!ok) break;
         tc_fence_after();
-        if (busy) {
+        if (FP4 && busy) {
+          // The same with 128 registers a thread: the probabilities of 32 columns are written before the next are worked
+          // on (over scores that have been read), so the reference is settled first: from all columns where the row has
+          // none, else from the 32 at hand; what was written against an outgrown one is rescaled.
+          const int key0 = cur.template tile<SINKS>(k0 + j) * BN, lo = row_lo - key0, hi = row_hi - key0;
+          const int sinks = SINKS ? p.sinks - key0 : 0;
+          const bool masked = key0 + BN > w_hi || key0 < w_lo;
+          const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
+          uint32_t s[32];
+          // the 32 scores from column c on, masked; their maximum, scaled (the scale is positive)
+          auto scores = [&](int c) -> float {
+            tc_ld32(t_s + c, s);
+            tc_wait_ld(s);
+            if (masked) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) s[i] = (c + i >= lo || (SINKS && c + i < sinks)) && c + i < hi ? s[i] : 0xff800000u;
+            }
+            float t[4] = {ninf(), ninf(), ninf(), ninf()};
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              t[i & 3] = fmaxf(fmaxf(t[i & 3], __uint_as_float(s[2 * i])), __uint_as_float(s[2 * i + 1]));
+            return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale_log2;
+          };
+          if (__any_sync(0xffffffffu, mine && m == ninf())) {
+            float top = ninf();
+#pragma unroll 1
+            for (int c = 0; c < BN; c += 32) top = fmaxf(top, scores(c));
+            if (m == ninf()) m = top;   // O and the sum are zero so far
+          }
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            const float top = fmaxf(m, scores(c));
+            if (__any_sync(0xffffffffu, top - m > kFp4Grow)) {
+              const float f = ex2(m - (top == ninf() ? 0.f : top));
+              l *= f;
+              m = top;
+              uint32_t x[32];
+              if (j > j0) {
+#pragma unroll 1
+                for (int d = 0; d < DP; d += 32) {
+                  tc_ld32(t_o + d, x);
+                  tc_wait_ld(x);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+                  tc_st32(t_o + d, x);
+                }
+              }
+              tc_wait_st();
+#pragma unroll 1
+              for (int d = 0; d < c / 2; d += 16) {   // 16 columns hold 32 probabilities
+                tc_ld32(t_s + d, x);                  // (the 16 behind them are read along)
+                tc_wait_ld(x);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+                  x[i] = M::pack(y.x * f, y.y * f);
+                }
+                tc_st16(t_s + d, x);
+              }
+            }
+            const float ref = (m == ninf() ? 0.f : m) - kShift;
+            const uint64_t ref2 = f2_pack(-ref, -ref);
+            uint64_t sum[2] = {0ull, 0ull};
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              float e0, e1;
+              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, ref2), e0, e1);
+              e0 = ex2(e0);
+              e1 = ex2(e1);
+              sum[i & 1] = f2_add(sum[i & 1], f2_pack(e0, e1));
+              pk[i] = M::pack(e0, e1);
+            }
+            tc_st16(t_s + c / 2, pk);
+            float a, b;
+            f2_unpack(f2_add(sum[0], sum[1]), a, b);
+            l += a + b;
+          }
+          tc_wait_st();
+        }
+        if (!FP4 && busy) {
           // One pass over the scores, 32 columns at a time with the next ones in flight: maximum,
           // exponentials against the reference so far, their sum.  Only where the maximum has outgrown
           // the reference (always in an item's first tile) the pass is done again with the new one.
@@ -688,7 +824,7 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
           uint32_t pk[64];
           while (true) {
             const float ref = m == ninf() ? 0.f : m;
-            const uint64_t ref2 = f2_pack(kShift - ref, kShift - ref);
+            const uint64_t ref2 = f2_pack(-ref, -ref);
             uint32_t s[2][32];
             float t[4] = {ninf(), ninf(), ninf(), ninf()};
             uint64_t sum[2] = {0ull, 0ull};

@@ -184,6 +184,10 @@ spec_status_t run_attention(const AttentionCall& a) {
   const int rows = static_cast<int>(all_rows < 1024 ? all_rows : 1024);
   sv::AttnMaps maps = {};
   int kind = fp4 ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);
+  if (fp4 && kind >= 2)   // its strides are 32-bit numbers
+    for (long long x : {batch->k_page, batch->k_token, batch->v_page, batch->v_token, a.scales->k_page, a.scales->k_token,
+                        a.scales->v_page, a.scales->v_token})
+      if (x >= 1ll << 32) kind = 0;
   if (!fp4 && kind >= 2 && !sv::attention_maps(form.bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
   sv::AttnPlan plan;
   if (sv::attention_plan(form, kind, rows, batch->dim, sms, &plan) != cudaSuccess) return SPEC_ERR_CUDA;
