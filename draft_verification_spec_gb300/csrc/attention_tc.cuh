@@ -212,35 +212,32 @@ struct TcFp4Share {
   static constexpr int kSteps = kTcBN / kKeys, kMine = (kSteps + kTcLoaders - 1) / kTcLoaders;
   static constexpr int kRounds = (kMine * kKeys + 31) / 32;   // keys of a loader's share, 32 at a time
   static_assert(32 % kKeys == 0, "a step's keys are held by consecutive lanes");
+  static constexpr uint32_t kNone = 0xffffffffu;
   uint4 codes[kMine];
   uint16_t scales[kMine];
   // This lane's key of its step i (at or beyond the tile's end: none).  Lanes 0 to 7 have 8 keys (16 where a key is two
   // lanes' work) and the same place in them, so that a store phase falls on distinct banks.
   static __device__ __forceinline__ int key(int loader, int i, int lane) { return (i * kTcLoaders + loader) * kKeys + lane % kKeys; }
-  // Reads the units of the keys whose pages and slots the warp's lanes hold (lane n: key n of its share; page below 0: zeros).
-  // Strides are below 2^32 (the host sees to it): a product with one is one instruction.
-  __device__ __forceinline__ void load(const uint8_t* codes_at, uint32_t page, uint32_t token, const uint8_t* scales_at,
-                                       uint32_t s_page, uint32_t s_token, const int (&pg)[kRounds], const int (&in)[kRounds],
+  // Reads this lane's units of the keys at the given scales (offset in bytes; none: zeros).  The codes lie 8 times as far
+  // from their base, and the bases are those of the lane's place in a key.
+  __device__ __forceinline__ void load(const uint8_t* codes_at, const uint8_t* scales_at, const uint32_t (&at)[kMine],
                                        bool whole, int D, int lane) {
-    const int c = lane / kKeys;
-    auto wide = [](int a, uint32_t b) { return static_cast<unsigned long long>(static_cast<uint32_t>(a)) * b; };
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
-      const int at = i * kKeys + lane % kKeys;
-      const int q = __shfl_sync(0xffffffffu, pg[i * kKeys / 32], at % 32), slot = __shfl_sync(0xffffffffu, in[i * kKeys / 32], at % 32);
-      const uint8_t* x = codes_at + wide(q, page) + wide(slot, token) + c * 16;
-      const uint8_t* y = scales_at + wide(q, s_page) + wide(slot, s_token) + c * 2;
+      const uint8_t* x = codes_at + static_cast<unsigned long long>(at[i]) * 8;
+      const uint8_t* y = scales_at + at[i];
       if (whole) {
         asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ge.s32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0xffffffff;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
             "mov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\tmov.b16 %4, 0;\n\t"
             "@p ld.global.nc.v4.b32 {%0, %1, %2, %3}, [%6];\n\t@p ld.global.nc.b16 %4, [%7];\n\t}"
             : "=&r"(codes[i].x), "=&r"(codes[i].y), "=&r"(codes[i].z), "=&r"(codes[i].w), "=&h"(scales[i])
-            : "r"(q), "l"(x), "l"(y));
+            : "r"(at[i]), "l"(x), "l"(y));
       } else {
+        const int c = lane / kKeys;
         codes[i] = make_uint4(0, 0, 0, 0);
         scales[i] = 0;
-        if (q < 0 || c * 32 >= D) continue;
+        if (at[i] == kNone || c * 32 >= D) continue;
         const uint2 a = __ldg(reinterpret_cast<const uint2*>(x));
         codes[i].x = a.x;
         codes[i].y = a.y;
@@ -354,9 +351,13 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
     // page ids for that a tile before that, so no latency of the table or of memory stands between two tiles.
     using Share = TcFp4Share<DP>;
     const int loader = warp == 8 ? 0 : warp - 9, P = p.c.page_size;
-    struct Places {   // of a tile's keys: lane n has page (below 0: none) and slot of key n of the warp's share
+    struct Fetched {   // of a tile's keys: lane n has the page and slot of key n of the warp's share (slot -1: none)
       int pg[Share::kRounds], in[Share::kRounds], head;
-      bool there;     // there is such a tile
+      bool there;      // there is such a tile
+    };
+    struct Places {    // offsets of this lane's keys (Share::load)
+      uint32_t at[Share::kMine];
+      bool there;
     };
     int lo, hi, j = 0;   // the item's keys; its tile that is fetched next
     const int32_t* table;
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
     };
     begin_item();
     bool left = true;    // a tile is left to fetch
-    auto fetch = [&](Places& x) {
+    auto fetch = [&](Fetched& x) {
       x.there = left;
       if (!left) return;
       const int key0 = cur.template tile<SINKS>(k0 + j) * BN;
@@ -379,8 +380,14 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
         x.pg[n] = -1;
         x.in[n] = -1;
         if (r < BN && key < hi && (key >= lo || (SINKS && key < p.sinks))) {
-          const int col = key / P;
-          x.in[n] = key - col * P;
+          // key / P: the product with floor(2^32 / P) is the quotient or one less
+          int col = static_cast<int>(__umulhi(static_cast<unsigned>(key), p.page_inv));
+          int in = key - col * P;
+          if (in >= P) {
+            ++col;
+            in -= P;
+          }
+          x.in[n] = in;
           x.pg[n] = __ldg(table + col);
         }
       }
@@ -391,26 +398,29 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
       begin_item();
       j = 0;
     };
-    // Page ids outside the cache are reported and read as zeros.
-    auto settle = [&](Places& x) {
+    // Page ids outside the cache are reported and read as zeros.  Offsets of scales are 32-bit numbers (the host sees to it).
+    auto place = [&](const Fetched& x, Places& to) {
+      to.there = x.there;
+      uint32_t at[Share::kRounds];
 #pragma unroll
       for (int n = 0; n < Share::kRounds; ++n) {
         const bool bad = x.pg[n] < 0 || x.pg[n] >= p.c.pages;
         if (bad && x.in[n] >= 0) atomicOr(p.status, kStatusPageRange);
-        if (bad) x.pg[n] = -1;
+        at[n] = bad ? Share::kNone
+                    : static_cast<uint32_t>(x.pg[n]) * static_cast<uint32_t>(p.s.k_page) +
+                          static_cast<uint32_t>(x.in[n]) * static_cast<uint32_t>(p.s.k_token) +
+                          static_cast<uint32_t>(x.head) * static_cast<uint32_t>(p.s.k_head);
       }
+#pragma unroll
+      for (int i = 0; i < Share::kMine; ++i)
+        to.at[i] = __shfl_sync(0xffffffffu, at[i * Share::kKeys / 32], (i * Share::kKeys + lane % Share::kKeys) % 32);
     };
     Share k, v;
-    auto load_k = [&](const Places& x) {
-      k.load(p.c.k + x.head * p.c.k_head, static_cast<uint32_t>(p.c.k_page), static_cast<uint32_t>(p.c.k_token),
-             p.s.k + x.head * p.s.k_head, static_cast<uint32_t>(p.s.k_page), static_cast<uint32_t>(p.s.k_token), x.pg, x.in,
-             p.s.whole, p.c.D, lane);
-    };
-    auto load_v = [&](const Places& x) {
-      v.load(p.c.v + x.head * p.c.v_head, static_cast<uint32_t>(p.c.v_page), static_cast<uint32_t>(p.c.v_token),
-             p.s.v + x.head * p.s.v_head, static_cast<uint32_t>(p.s.v_page), static_cast<uint32_t>(p.s.v_token), x.pg, x.in,
-             p.s.whole, p.c.D, lane);
-    };
+    const int in_key = lane / Share::kKeys;   // this lane's 32 values of a key
+    const uint8_t *k_codes = p.c.k + in_key * 16, *v_codes = p.c.v + in_key * 16;
+    const uint8_t *k_scales = p.s.k + in_key * 2, *v_scales = p.s.v + in_key * 2;
+    auto load_k = [&](const Places& x) { k.load(k_codes, k_scales, x.at, p.s.whole, p.c.D, lane); };
+    auto load_v = [&](const Places& x) { v.load(v_codes, v_scales, x.at, p.s.whole, p.c.D, lane); };
     bool ok = p.wait_limit > 0 || wait.give_up();
     unsigned g = 0;   // key tiles of this CTA so far
     auto put_k = [&](unsigned n) -> bool {
@@ -429,31 +439,27 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
       mbar_arrive_warp(smem_addr(&bars.v_full[st]));
       return true;
     };
-    Places now, next, after;   // tiles g, g + 1, g + 2
-    fetch(now);
-    fetch(next);
-    fetch(after);
-    settle(now);
-    load_k(now);
-    load_v(now);
+    Fetched fetched;
+    Places next, after;   // tiles g + 1, g + 2
+    fetch(fetched);
+    place(fetched, next);
+    load_k(next);
+    load_v(next);
+    fetch(fetched);
     ok = ok && put_k(0);
-    if (next.there) {
-      settle(next);
-      load_k(next);
-    }
+    place(fetched, next);
+    if (next.there) load_k(next);
+    fetch(fetched);
     while (ok) {
+      place(fetched, after);
       if (next.there) {
         if (!(ok = put_k(g + 1))) break;
-        if (after.there) {
-          settle(after);
-          load_k(after);
-        }
+        if (after.there) load_k(after);
       }
-      if (!(ok = put_v(g))) break;
-      if (!next.there) break;
+      if (!(ok = put_v(g)) || !next.there) break;
       load_v(next);
+      fetch(fetched);
       next = after;
-      fetch(after);
       ++g;
     }
   } else if (!FP4 && warp == 8) {

@@ -107,6 +107,13 @@ sv::Fp4Scales internal_scales(const spec_paged_batch_t& b, const spec_fp4_scales
   for (long long x : {b.k_page, b.k_token, b.k_head, b.v_page, b.v_token, b.v_head}) whole = whole && x % 16 == 0;
   for (long long x : {f.k_page, f.k_token, f.k_head, f.v_page, f.v_token, f.v_head}) whole = whole && x % (b.dim / 16) == 0;
   s.whole = whole;
+  // whatever page, slot and head: within (pages - 1) page + (page_size - 1) token + (heads - 1) head bytes of the base
+  const long long most = 1ll << 32;
+  s.alike = f.k_page < most && f.k_token < most && f.k_head < most && f.k_page == f.v_page && f.k_token == f.v_token &&
+            f.k_head == f.v_head && b.k_page == 8 * f.k_page && b.k_token == 8 * f.k_token && b.k_head == 8 * f.k_head &&
+            b.v_page == b.k_page && b.v_token == b.k_token && b.v_head == b.k_head &&
+            static_cast<double>(b.pages - 1) * f.k_page + static_cast<double>(b.page_size - 1) * f.k_token +
+                    static_cast<double>(b.kv_heads - 1) * f.k_head < static_cast<double>(most - 1);
   return s;
 }
 
@@ -183,11 +190,9 @@ spec_status_t run_attention(const AttentionCall& a) {
   const long long all_rows = static_cast<long long>(a.max_q) * G;
   const int rows = static_cast<int>(all_rows < 1024 ? all_rows : 1024);
   sv::AttnMaps maps = {};
-  int kind = fp4 ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);
-  if (fp4 && kind >= 2)   // its strides are 32-bit numbers
-    for (long long x : {batch->k_page, batch->k_token, batch->v_page, batch->v_token, a.scales->k_page, a.scales->k_token,
-                        a.scales->v_page, a.scales->v_token})
-      if (x >= 1ll << 32) kind = 0;
+  sv::Fp4Scales scales = {};
+  if (fp4) scales = internal_scales(*batch, *a.scales);
+  int kind = fp4 ? (scales.alike ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : 0) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);
   if (!fp4 && kind >= 2 && !sv::attention_maps(form.bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
   sv::AttnPlan plan;
   if (sv::attention_plan(form, kind, rows, batch->dim, sms, &plan) != cudaSuccess) return SPEC_ERR_CUDA;
@@ -210,7 +215,8 @@ spec_status_t run_attention(const AttentionCall& a) {
   p.scale_log2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634 * (fp4 ? a.scales->k_unit : 1.f));
   if (!std::isfinite(p.scale_log2)) return SPEC_ERR_INVALID_ARG;
   p.v_unit = fp4 ? a.scales->v_unit : 1.f;
-  if (fp4) p.s = internal_scales(*batch, *a.scales);
+  p.s = scales;
+  p.page_inv = batch->page_size > 1 ? static_cast<unsigned>((1ull << 32) / batch->page_size) : 0xffffffffu;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.status = reinterpret_cast<int32_t*>(ws);
   p.joins = reinterpret_cast<sv::AttnJoin*>(ws + kStatusBytes);

@@ -31,6 +31,7 @@ struct Fp4Scales {
   uint8_t *k, *v;
   long long k_page, k_token, k_head, v_page, v_token, v_head;   // bytes
   int whole;                 // heads fill the kernel's tiles, rows of codes and scales are aligned to their size
+  int alike;                 // a token's scales and codes, of keys and of values, lie at offsets of 1 : 8 : 1 : 8, the first in 32 bits
 };
 
 // The item that begins in a CTA's run and goes on in others': what the combine kernel joins.
@@ -50,6 +51,7 @@ struct AttnParams {
   float* lse;                // [N, Hq] or null
   int Hq, G;                 // query heads, query heads per key head
   unsigned long long G_inv;  // ceil(2^64 / G), 0 for G = 1
+  unsigned page_inv;         // floor(2^32 / page_size), at most 2^32 - 1
   int lanes;                 // threads that share a request's row tiles when the work is divided
   int causal, window, sinks; // sinks: first tokens that stay visible behind a window
   float scale_log2;          // softmax scale x log2(e) (x the keys' unit)
