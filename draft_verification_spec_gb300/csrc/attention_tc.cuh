@@ -741,81 +741,100 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
         tc_fence_after();
         if (FP4 && busy) {
           // The same with 128 registers a thread: the probabilities of 32 columns are written before the next are worked
-          // on (over scores that have been read), so the reference is settled first: from all columns where the row has
-          // none, else from the 32 at hand; what was written against an outgrown one is rescaled.
+          // on (over scores that have been read).  An item's first reference comes from a pass over all columns; where 32
+          // columns outgrow it, they are read again, and what was written against the old one is rescaled.
           const int key0 = cur.template tile<SINKS>(k0 + j) * BN, lo = row_lo - key0, hi = row_hi - key0;
           const int sinks = SINKS ? p.sinks - key0 : 0;
           const bool masked = key0 + BN > w_hi || key0 < w_lo;
           const uint64_t scale2 = f2_pack(scale_log2, scale_log2);
-          uint32_t s[32];
-          // the 32 scores from column c on, masked; their maximum, scaled (the scale is positive)
-          auto scores = [&](int c) -> float {
-            tc_ld32(t_s + c, s);
-            tc_wait_ld(s);
+          auto mask = [&](uint32_t (&s)[32], int c) {
             if (masked) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) s[i] = (c + i >= lo || (SINKS && c + i < sinks)) && c + i < hi ? s[i] : 0xff800000u;
             }
-            float t[4] = {ninf(), ninf(), ninf(), ninf()};
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              t[i & 3] = fmaxf(fmaxf(t[i & 3], __uint_as_float(s[2 * i])), __uint_as_float(s[2 * i + 1]));
-            return fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale_log2;
           };
           if (__any_sync(0xffffffffu, mine && m == ninf())) {
-            float top = ninf();
+            float t[4] = {ninf(), ninf(), ninf(), ninf()};
 #pragma unroll 1
-            for (int c = 0; c < BN; c += 32) top = fmaxf(top, scores(c));
-            if (m == ninf()) m = top;   // O and the sum are zero so far
+            for (int c = 0; c < BN; c += 32) {
+              uint32_t s[32];
+              tc_ld32(t_s + c, s);
+              tc_wait_ld(s);
+              mask(s, c);
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                t[i & 3] = fmaxf(fmaxf(t[i & 3], __uint_as_float(s[2 * i])), __uint_as_float(s[2 * i + 1]));
+            }
+            if (m == ninf()) m = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale_log2;   // O and the sum are zero so far
           }
-#pragma unroll 1
-          for (int c = 0; c < BN; c += 32) {
-            const float top = fmaxf(m, scores(c));
+          // 32 columns: exponentials against the reference, their sum, the maximum (scaled: the scale is positive)
+          auto work = [&](uint32_t (&s)[32], int c) {
+            uint32_t pk[16];
+            float sums, top;
+            auto pass = [&] {
+              const float ref = (m == ninf() ? 0.f : m) - kShift;
+              const uint64_t ref2 = f2_pack(-ref, -ref);
+              uint64_t sum[2] = {0ull, 0ull};
+              float t[4] = {ninf(), ninf(), ninf(), ninf()};
+#pragma unroll
+              for (int i = 0; i < 16; ++i) {
+                const float x0 = __uint_as_float(s[2 * i]), x1 = __uint_as_float(s[2 * i + 1]);
+                t[i & 3] = fmaxf(fmaxf(t[i & 3], x0), x1);
+                float e0, e1;
+                f2_unpack(f2_fma(f2_pack(x0, x1), scale2, ref2), e0, e1);
+                e0 = ex2(e0);
+                e1 = ex2(e1);
+                sum[i & 1] = f2_add(sum[i & 1], f2_pack(e0, e1));
+                pk[i] = M::pack(e0, e1);
+              }
+              float a, b;
+              f2_unpack(f2_add(sum[0], sum[1]), a, b);
+              sums = a + b;
+              top = fmaxf(m, fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale_log2);
+            };
+            mask(s, c);
+            pass();
             if (__any_sync(0xffffffffu, top - m > kFp4Grow)) {
               const float f = ex2(m - (top == ninf() ? 0.f : top));
               l *= f;
               m = top;
-              uint32_t x[32];
               if (j > j0) {
 #pragma unroll 1
                 for (int d = 0; d < DP; d += 32) {
-                  tc_ld32(t_o + d, x);
-                  tc_wait_ld(x);
+                  tc_ld32(t_o + d, s);
+                  tc_wait_ld(s);
 #pragma unroll
-                  for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-                  tc_st32(t_o + d, x);
+                  for (int i = 0; i < 32; ++i) s[i] = __float_as_uint(__uint_as_float(s[i]) * f);
+                  tc_st32(t_o + d, s);
                 }
               }
               tc_wait_st();
 #pragma unroll 1
-              for (int d = 0; d < c / 2; d += 16) {   // 16 columns hold 32 probabilities
-                tc_ld32(t_s + d, x);                  // (the 16 behind them are read along)
-                tc_wait_ld(x);
+              for (int d = 0; d < c / 2; d += 16) {   // 16 columns hold 32 probabilities (the 16 behind them are read along)
+                tc_ld32(t_s + d, s);
+                tc_wait_ld(s);
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
-                  x[i] = M::pack(y.x * f, y.y * f);
+                  const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&s[i]));
+                  s[i] = M::pack(y.x * f, y.y * f);
                 }
-                tc_st16(t_s + d, x);
+                tc_st16(t_s + d, s);
               }
+              tc_wait_st();
+              tc_ld32(t_s + c, s);
+              tc_wait_ld(s);
+              mask(s, c);
+              pass();
             }
-            const float ref = (m == ninf() ? 0.f : m) - kShift;
-            const uint64_t ref2 = f2_pack(-ref, -ref);
-            uint64_t sum[2] = {0ull, 0ull};
-            uint32_t pk[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              float e0, e1;
-              f2_unpack(f2_fma(f2_pack(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, ref2), e0, e1);
-              e0 = ex2(e0);
-              e1 = ex2(e1);
-              sum[i & 1] = f2_add(sum[i & 1], f2_pack(e0, e1));
-              pk[i] = M::pack(e0, e1);
-            }
+            l += sums;
             tc_st16(t_s + c / 2, pk);
-            float a, b;
-            f2_unpack(f2_add(sum[0], sum[1]), a, b);
-            l += a + b;
+          };
+#pragma unroll 1
+          for (int c = 0; c < BN; c += 32) {
+            uint32_t s[32];
+            tc_ld32(t_s + c, s);
+            tc_wait_ld(s);
+            work(s, c);
           }
           tc_wait_st();
         }
