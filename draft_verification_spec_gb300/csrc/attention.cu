@@ -29,9 +29,9 @@ const void* attn_tc_fp4_fn<true>(int dp, bool wide);
 template <>
 const void* attn_tc_fp4_fn<false>(int dp, bool wide);
 template <>
-const void* attn_fp4_fn<true>(int dp);
+const void* attn_fp4_fn<true>(int dp, int bm);
 template <>
-const void* attn_fp4_fn<false>(int dp);
+const void* attn_fp4_fn<false>(int dp, int bm);
 
 // Joins the item that CTA blockIdx.x left a record of: one warp per row, the partials in key order,
 // each scaled by 2^(its maximum - the largest).  fp32.
@@ -112,14 +112,14 @@ static const void* kernel_of(const AttnPlan& plan) {
 static const void* kernel_of(const AttnForm& form, const AttnPlan& plan) {
   if (form.fp4 && plan.kind >= 2)
     return form.bf16 ? attn_tc_fp4_fn<true>(plan.dp, plan.kind == 3) : attn_tc_fp4_fn<false>(plan.dp, plan.kind == 3);
-  if (form.fp4) return form.bf16 ? attn_fp4_fn<true>(plan.dp) : attn_fp4_fn<false>(plan.dp);
+  if (form.fp4) return form.bf16 ? attn_fp4_fn<true>(plan.dp, plan.bm) : attn_fp4_fn<false>(plan.dp, plan.bm);
   if (form.sinks) return form.bf16 ? kernel_of<true, true>(plan) : kernel_of<false, true>(plan);
   return form.bf16 ? kernel_of<true, false>(plan) : kernel_of<false, false>(plan);
 }
 
 cudaError_t attention_plan(const AttnForm& form, int kind, int rows, int D, int sms, AttnPlan* plan) {
   plan->kind = kind;
-  plan->bm = kind == 0 ? 16 : kind == 1 ? 64 : kind == 2 ? 128 : 256;
+  plan->bm = kind == 0 ? (form.fp4 && rows <= 8 ? 8 : 16) : kind == 1 ? 64 : kind == 2 ? 128 : 256;
   plan->bn = kind >= 2 ? kTcBN : form.fp4 ? kFp4BN : kAttnBN;
   plan->rows = rows < 1 ? 1 : rows < plan->bm ? rows : plan->bm;
   plan->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
@@ -129,7 +129,7 @@ cudaError_t attention_plan(const AttnForm& form, int kind, int rows, int D, int 
                            : (plan->dp == 64 ? AttnTcGeom<64, true>::kSmem : AttnTcGeom<128, true>::kSmem);
     threads = form.fp4 ? kTcFp4Threads : kTcThreads;
   } else if (form.fp4) {
-    plan->smem = attn_fp4_smem(plan->dp);
+    plan->smem = attn_fp4_smem(plan->dp, plan->bm);
   } else {
     plan->smem = form.bf16 ? attn_mma_smem<true>(plan->dp, plan->bm) : attn_mma_smem<false>(plan->dp, plan->bm);
   }

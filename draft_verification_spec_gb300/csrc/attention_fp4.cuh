@@ -1,5 +1,5 @@
 // Attention of new tokens over a paged cache held in 4 bits (step_internal.h: Fp4Scales), mma.sync kernel: any page
-// size, head sizes up to 256, tiles of 16 rows.
+// size, head sizes up to 256, tiles of 8 or 16 rows.
 //
 // The same formula and the same work division as the kernel over 16-bit caches (attention_mma.cuh), over
 //   k = unit scale[block] code: code e2m1, scale e4m3, a block 16 values along the head.
@@ -7,13 +7,16 @@
 // the keys and values that the bits stand for, in f16; the units (powers of two) are factors of the scores and of the
 // rows.  Queries: f16 as they are; bf16 ones as f16 relative to the power of two at the row's largest value, which is
 // exact down to 2^-14 of it and loses 2^-25 of it at most below that.  Probabilities are rounded to f16, up to
-// 2^14 (see kShift): 2^-12 relative down to 2^-20 of the reference.  Statistics and O are fp32.
+// 2^14 (see kFp4Shift): 2^-12 relative down to 2^-20 of the reference.  Statistics and O are fp32.
+//
+// The products are transposed, S^T = K Q^T and O^T = V^T P^T: what is wide is the keys and the head, so they take
+// the tensor core's 16 rows, and the few query rows its 8 columns.
 //
 // Tiles: 128 keys, of which every warp takes 32 for itself: it looks up their pages, copies them into a ring of its own
 // and works on them, so nothing in the loop waits for another warp.  A lane reads from shared memory just the bytes
 // whose values it hands to the tensor core: the order of the values in a contraction is free, so a lane's 4 of every
-// 16 are 32 consecutive values of a key, 16 bytes (the queries are laid out to match), and its columns of O are 16
-// consecutive values.  For P V two keys' nibbles are brought together in a byte before the conversion, which then
+// 16 are 32 consecutive values of a key, 16 bytes (the queries are laid out to match), and its rows of O^T are 16
+// consecutive values.  For V^T two keys' nibbles are brought together in a byte before the conversion, which then
 // gives the pair that the tensor core wants.
 #pragma once
 
@@ -26,14 +29,14 @@ constexpr int kFp4WarpKeys = 32;    // of which a warp takes this many
 // Probabilities are 2^kShift times the weights against the reference, which lie between 0 and 2^kGrow.
 constexpr float kFp4Shift = 6.f, kFp4Grow = 8.f;
 
-template <int DP>
+template <int DP, int NQ>
 struct AttnFp4Geom {
   static constexpr int kRow = DP / 2, kScale = DP / 16;   // bytes of a key's codes and scales
   static constexpr int kCodes = kFp4WarpKeys * kRow, kScales = kFp4WarpKeys * kScale;
   static constexpr int kStage = 2 * (kCodes + kScales);   // one warp's K codes, V codes, K scales, V scales
   static constexpr int kStages = DP == 256 ? 2 : DP == 128 ? 3 : 4;
-  static constexpr int kSmem = 4 * kStages * kStage;
-  static_assert(4 * 16 * DP * 4 <= kSmem || DP == 64, "the output staging fits the ring");
+  static constexpr int kRing = 4 * kStages * kStage, kOut = 4 * 8 * NQ * DP * 4;   // the rows are staged over the ring
+  static constexpr int kSmem = kRing > kOut ? kRing : kOut;
 };
 
 // Byte offset of 16-byte piece c of key r in a warp's tile of codes.  The pieces are permuted so that the
@@ -83,12 +86,20 @@ __device__ __forceinline__ void cp_async_some(uint32_t dst, const void* src, boo
 }
 __device__ __forceinline__ long long shfl64(long long v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
 
-template <bool BF16, int DP>
+// 8 x 8 values of 16 bits, transposed across the warp.
+__device__ __forceinline__ uint32_t transposed(uint32_t a) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+  return r;
+}
+
+// NQ: 8-row tiles of queries.
+template <bool BF16, int DP, int NQ>
 __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams p) {
   using A = AttnType<BF16>;
   using H = AttnType<false>;   // the products are of f16 values
-  using Geo = AttnFp4Geom<DP>;
-  constexpr int BM = 16, BN = kFp4BN, WK = kFp4WarpKeys, NT = WK / 8, DT = DP / 8, STAGES = Geo::kStages;
+  using Geo = AttnFp4Geom<DP, NQ>;
+  constexpr int BM = 8 * NQ, BN = kFp4BN, WK = kFp4WarpKeys, MK = WK / 16, MD = DP / 16, STAGES = Geo::kStages;
   constexpr int WORDS = DP / 32;         // words of 8 codes that a lane reads of a key, of K
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnSchedSmem<kAttnThreads> sched;
@@ -114,6 +125,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
   bool later = false;   // not the CTA's first item
   const uint32_t ring = smem_addr(smem) + warp * STAGES * Geo::kStage;
   const int D = p.c.D, P = p.c.page_size;
+  const bool whole = p.s.whole && p.s.alike;   // keys and values in 16-byte pieces, all from one 32-bit offset
 
   while (true) {
     const int len = k1 - k0;
@@ -121,52 +133,58 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
     int lo, hi;
     attn_keys(p, cur.req, r0, r1, &lo, &hi);
     const int32_t* table = p.c.table + static_cast<long long>(cur.b) * p.c.table_stride;
-    const uint8_t* kbase = p.c.k + cur.h * p.c.k_head;
-    const uint8_t* vbase = p.c.v + cur.h * p.c.v_head;
-    const uint8_t* ksbase = p.s.k + cur.h * p.s.k_head;
-    const uint8_t* vsbase = p.s.v + cur.h * p.s.v_head;
 
     auto tile = [&](int j) { return cur.template tile<true>(k0 + j); };   // the CTA's tile number j of the item
-    // page id of this lane's key of tile j (-1: nothing to read)
-    auto page_of = [&](int j) -> int {
+    // page of this lane's key of tile j (below 0: nothing to read) and its slot
+    auto page_of = [&](int j, int* in) -> int {
       const int key = tile(j) * BN + warp * WK + lane;
+      *in = -1;
       if (j >= len || (key < lo && key >= p.sinks) || key >= hi) return -1;   // also what lies before the window
-      const int pg = __ldg(table + key / P);
-      if (pg < 0 || pg >= p.c.pages) {
-        atomicOr(p.status, kStatusPageRange);
-        return -1;
+      // key / P: the product with floor(2^32 / P) is the quotient or one less
+      int col = static_cast<int>(__umulhi(static_cast<unsigned>(key), p.page_inv));
+      *in = key - col * P;
+      if (*in >= P) {
+        ++col;
+        *in -= P;
       }
-      return pg;
+      return __ldg(table + col);
     };
     // copies of tile j, whose page ids are there
-    auto load_tile = [&](int j, int pg) {
+    auto load_tile = [&](int j, int pg, int in) {
       if (j < len) {
         const uint32_t st = ring + j % STAGES * Geo::kStage;
-        const int in = (tile(j) * BN + warp * WK + lane) % P;
-        const bool has = pg >= 0;
-        const unsigned there = __ballot_sync(0xffffffffu, has);
-        const long long pl = has ? pg : 0;
-        const long long ko = pl * p.c.k_page + in * p.c.k_token, vo = pl * p.c.v_page + in * p.c.v_token;
-        const uint8_t* ks = ksbase + (has ? pl * p.s.k_page + in * p.s.k_token : 0);
-        const uint8_t* vs = vsbase + (has ? pl * p.s.v_page + in * p.s.v_token : 0);
+        const bool has = pg >= 0 && pg < p.c.pages && in >= 0;
+        if (in >= 0 && !has) atomicOr(p.status, kStatusPageRange);
         const uint32_t dks = st + 2 * Geo::kCodes + lane * Geo::kScale, dvs = dks + Geo::kScales;
-        if (p.s.whole) {
+        if (whole) {
+          const uint32_t at = has ? static_cast<uint32_t>(pg) * static_cast<uint32_t>(p.s.k_page) +
+                                        static_cast<uint32_t>(in) * static_cast<uint32_t>(p.s.k_token) +
+                                        static_cast<uint32_t>(cur.h) * static_cast<uint32_t>(p.s.k_head)
+                                  : 0u;
+          const unsigned there = __ballot_sync(0xffffffffu, has);
           constexpr int CH = DP / 32;        // 16-byte pieces of a key
+          const int c = lane % CH;
+          const uint8_t *kc = p.c.k + c * 16, *vc = p.c.v + c * 16;
 #pragma unroll
           for (int i = 0; i < CH; ++i) {
-            const int r = i * (32 / CH) + lane / CH, c = lane % CH;
+            const int r = i * (32 / CH) + lane / CH;
+            const unsigned long long off = static_cast<unsigned long long>(__shfl_sync(0xffffffffu, at, r)) * 8;
             const bool ok = there >> r & 1;
-            const long long k_at = shfl64(ko, r), v_at = shfl64(vo, r);
-            cp_async16(st + fp4_k_piece<DP>(r, c), ok ? kbase + k_at + c * 16 : kbase, ok);
-            cp_async16(st + Geo::kCodes + fp4_v_piece<DP>(r, c), ok ? vbase + v_at + c * 16 : vbase, ok);
+            cp_async16(st + fp4_k_piece<DP>(r, c), kc + off, ok);
+            cp_async16(st + Geo::kCodes + fp4_v_piece<DP>(r, c), vc + off, ok);
           }
-          cp_async_some<Geo::kScale>(dks, ks, has);
-          cp_async_some<Geo::kScale>(dvs, vs, has);
-        } else {                             // heads that are not DP values long, or looser alignment: 8 bytes, scales one by one
+          cp_async_some<Geo::kScale>(dks, p.s.k + at, has);
+          cp_async_some<Geo::kScale>(dvs, p.s.v + at, has);
+        } else {                             // heads that are not DP values long, or other strides: 8 bytes, scales one by one
+          const long long pl = has ? pg : 0, il = has ? in : 0;
+          const uint8_t* k = p.c.k + pl * p.c.k_page + il * p.c.k_token + cur.h * p.c.k_head;
+          const uint8_t* v = p.c.v + pl * p.c.v_page + il * p.c.v_token + cur.h * p.c.v_head;
+          const uint8_t* ks = p.s.k + pl * p.s.k_page + il * p.s.k_token + cur.h * p.s.k_head;
+          const uint8_t* vs = p.s.v + pl * p.s.v_page + il * p.s.v_token + cur.h * p.s.v_head;
           for (int c = 0; c < DP / 16; ++c) {
             const bool ok = has && c * 16 < D;
-            cp_async_some<8>(st + fp4_k_piece<DP>(lane, c >> 1) + (c & 1) * 8, ok ? kbase + ko + c * 8 : kbase, ok);
-            cp_async_some<8>(st + Geo::kCodes + fp4_v_piece<DP>(lane, c >> 1) + (c & 1) * 8, ok ? vbase + vo + c * 8 : vbase, ok);
+            cp_async_some<8>(st + fp4_k_piece<DP>(lane, c >> 1) + (c & 1) * 8, ok ? k + c * 8 : k, ok);
+            cp_async_some<8>(st + Geo::kCodes + fp4_v_piece<DP>(lane, c >> 1) + (c & 1) * 8, ok ? v + c * 8 : v, ok);
             const uint32_t a = ok ? __ldg(ks + c) : 0u, b = ok ? __ldg(vs + c) : 0u;
             asm volatile("st.shared.u8 [%0], %1;" ::"r"(dks + c), "r"(a) : "memory");
             asm volatile("st.shared.u8 [%0], %1;" ::"r"(dvs + c), "r"(b) : "memory");
@@ -177,22 +195,23 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
     };
 
     // the first tiles' copies
-    int pg_next;
+    int pg_next, in_next;
     {
-      int pg[STAGES];
+      int pg[STAGES], in[STAGES];
 #pragma unroll
-      for (int j = 0; j < STAGES; ++j) pg[j] = page_of(j);
+      for (int j = 0; j < STAGES; ++j) pg[j] = page_of(j, &in[j]);
 #pragma unroll
-      for (int j = 0; j < STAGES - 1; ++j) load_tile(j, pg[j]);
+      for (int j = 0; j < STAGES - 1; ++j) load_tile(j, pg[j], in[j]);
       pg_next = pg[STAGES - 1];
+      in_next = in[STAGES - 1];
     }
 
-    // query fragments of rows g and g + 8: step s takes this lane's values 4 s .. 4 s + 3
-    uint32_t qf[DP / 16][4];
-    float factor[2];   // of the scores: softmax scale, the keys' unit, the queries' power of two
+    // query fragments: row g of every 8, step s takes this lane's values 4 s .. 4 s + 3
+    uint32_t qf[NQ][DP / 16][2];
+    float factor[NQ][2];   // of the scores of rows 2 t and 2 t + 1: softmax scale, the keys' unit, the queries' power of two
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + g + i * 8;
+    for (int n = 0; n < NQ; ++n) {
+      const int r = r0 + n * 8 + g;
       const uint8_t* q = nullptr;
       if (r < r1) {
         const int tok = attn_token(p, r);
@@ -204,10 +223,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
         const int d = DP == 64 ? t * 16 + w * 8 : (w / 4) * 128 + t * 32 + (w % 4) * 8;
         uint4 x = make_uint4(0, 0, 0, 0);
         if (q && d < D) x = __ldg(reinterpret_cast<const uint4*>(q + d * 2));
-        qf[2 * w][i] = x.x;
-        qf[2 * w][2 + i] = x.y;
-        qf[2 * w + 1][i] = x.z;
-        qf[2 * w + 1][2 + i] = x.w;
+        qf[n][2 * w][0] = x.x;
+        qf[n][2 * w][1] = x.y;
+        qf[n][2 * w + 1][0] = x.z;
+        qf[n][2 * w + 1][1] = x.w;
         if (BF16) {
           const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -215,132 +234,175 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
         }
       }
-      factor[i] = p.scale_log2;
+      float mine = p.scale_log2;
       if (BF16) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
         float down;
-        factor[i] *= fp4_query_power(top, &down);
+        mine *= fp4_query_power(top, &down);
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const uint32_t x = qf[s][2 * h + i];
-            qf[s][2 * h + i] = H::pack(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
+            const uint32_t x = qf[n][s][h];
+            qf[n][s][h] = H::pack(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
           }
       }
-    }
-    // key range of this lane's two rows
-    int row_lo[2], row_hi[2];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = r0 + g + i * 8;
-      row_lo[i] = 0;
-      row_hi[i] = 0;
-      if (r < r1) attn_keys(p, cur.req, r, r + 1, &row_lo[i], &row_hi[i]);
+      for (int c = 0; c < 2; ++c) factor[n][c] = __shfl_sync(0xffffffffu, mine, (2 * t + c) * 4);
     }
+    // key range of this lane's rows
+    int row_lo[NQ][2], row_hi[NQ][2], w_lo = 0, w_hi = 0x7fffffff;
+#pragma unroll
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int r = r0 + n * 8 + 2 * t + c;
+        row_lo[n][c] = 0;
+        row_hi[n][c] = 0;
+        if (r >= r1) continue;
+        attn_keys(p, cur.req, r, r + 1, &row_lo[n][c], &row_hi[n][c]);
+        w_lo = max(w_lo, row_lo[n][c]);
+        w_hi = min(w_hi, row_hi[n][c]);
+      }
     // keys inside [w_lo, w_hi) need no mask for any row of the tile (rows that do not exist are not written)
-    const int w_hi = __reduce_min_sync(0xffffffffu, min(r0 + g < r1 ? row_hi[0] : 0x7fffffff, r0 + g + 8 < r1 ? row_hi[1] : 0x7fffffff));
-    const int w_lo = __reduce_max_sync(0xffffffffu, max(row_lo[0], row_lo[1]));
+    w_hi = __reduce_min_sync(0xffffffffu, w_hi);
+    w_lo = __reduce_max_sync(0xffffffffu, w_lo);
 
-    float o[DT][4];
+    float o[NQ][MD][4];
+    float m[NQ][2], l[NQ][2];   // reference so far, sum of 2^(s - reference + shift)
 #pragma unroll
-    for (int i = 0; i < DT; ++i)
+    for (int n = 0; n < NQ; ++n) {
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[i][k] = 0.f;
-    float m[2] = {ninf(), ninf()}, l[2] = {0.f, 0.f};   // reference so far, sum of 2^(s - reference + shift)
+      for (int i = 0; i < MD; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[n][i][k] = 0.f;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        m[n][c] = ninf();
+        l[n][c] = 0.f;
+      }
+    }
 
     for (int j = 0; j < len; ++j) {
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
       __syncwarp();
-      load_tile(j + STAGES - 1, pg_next);
-      pg_next = page_of(j + STAGES);
+      load_tile(j + STAGES - 1, pg_next, in_next);
+      pg_next = page_of(j + STAGES, &in_next);
       const uint32_t sk = ring + j % STAGES * Geo::kStage, sv_ = sk + Geo::kCodes;
       const uint32_t sks = sk + 2 * Geo::kCodes, svs = sks + Geo::kScales;
 
-      // S = Q K^T: 16 rows x this warp's 32 keys
-      float s[NT][4];
+      // S^T = K Q^T: this warp's 32 keys x the rows
+      float s[NQ][MK][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int mk = 0; mk < MK; ++mk) {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) s[n][k] = 0.f;
-        const int r = n * 8 + g;
-        uint32_t w[WORDS], sc[DP == 256 ? 2 : 1];
-        if constexpr (DP == 64) {
-          asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(sk + fp4_k_piece<DP>(r, t >> 1) + (t & 1) * 8));
-          asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc[0]) : "r"(sks + r * Geo::kScale + t));
-        } else {
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int h = 0; h < DP / 128; ++h) {
-            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                         : "=r"(w[4 * h]), "=r"(w[4 * h + 1]), "=r"(w[4 * h + 2]), "=r"(w[4 * h + 3])
-                         : "r"(sk + fp4_k_piece<DP>(r, h * 4 + t)));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc[h]) : "r"(sks + r * Geo::kScale + h * 8 + t * 2));
+          for (int k = 0; k < 4; ++k) s[n][mk][k] = 0.f;
+        uint32_t w[2][WORDS], f[2][DP == 64 ? 1 : WORDS / 2];   // keys g and g + 8: codes, scales of blocks (twice each)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = mk * 16 + e * 8 + g;
+          uint32_t sc;
+          if constexpr (DP == 64) {
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1]) : "r"(sk + fp4_k_piece<DP>(r, t >> 1) + (t & 1) * 8));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(sks + r * Geo::kScale + t));
+            const uint32_t two = fp4_scales(sc);
+            f[e][0] = __byte_perm(two, two, 0x1010);
+          } else {
+#pragma unroll
+            for (int h = 0; h < DP / 128; ++h) {
+              asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                           : "=r"(w[e][4 * h]), "=r"(w[e][4 * h + 1]), "=r"(w[e][4 * h + 2]), "=r"(w[e][4 * h + 3])
+                           : "r"(sk + fp4_k_piece<DP>(r, h * 4 + t)));
+              asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc) : "r"(sks + r * Geo::kScale + h * 8 + t * 2));
+              const uint32_t two = fp4_scales(sc);
+              f[e][2 * h] = __byte_perm(two, two, 0x1010);
+              f[e][2 * h + 1] = __byte_perm(two, two, 0x3232);
+            }
           }
         }
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-          // the scale of this word's block, twice
-          const uint32_t two = fp4_scales(sc[i / 4]);
-          const uint32_t f = DP == 64 || i % 4 < 2 ? __byte_perm(two, two, 0x1010) : __byte_perm(two, two, 0x3232);
-          uint32_t b[4];
-          fp4_pairs(w[i], b);
-          H::mma(s[n], qf[2 * i], mul2(b[0], f), mul2(b[1], f));
-          H::mma(s[n], qf[2 * i + 1], mul2(b[2], f), mul2(b[3], f));
+          uint32_t b[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            fp4_pairs(w[e][i], b[e]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) b[e][k] = mul2(b[e][k], f[e][DP == 64 ? 0 : i / 2]);
+          }
+          const uint32_t a0[4] = {b[0][0], b[1][0], b[0][1], b[1][1]}, a1[4] = {b[0][2], b[1][2], b[0][3], b[1][3]};
+#pragma unroll
+          for (int n = 0; n < NQ; ++n) {
+            H::mma(s[n][mk], a0, qf[n][2 * i][0], qf[n][2 * i][1]);
+            H::mma(s[n][mk], a1, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
+          }
         }
       }
 
-      // masks, reference and sum
+      // masks, reference and sum; P^T as the second product's operand
       const int key0 = tile(j) * BN + warp * WK;
-      float mx[2] = {m[0], m[1]};
       const bool masked = key0 + WK > w_hi || key0 < w_lo;
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = s[n][e] * factor[e >> 1];
-          if (masked) {
-            const int key = key0 + n * 8 + t * 2 + (e & 1), i = e >> 1;
-            x = (key >= row_lo[i] || key < p.sinks) && key < row_hi[i] ? x : ninf();
-          }
-          s[n][e] = x;
-          mx[e >> 1] = fmaxf(mx[e >> 1], x);
-        }
+      float mx[NQ][2];
       bool grow = false;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 1));
-        mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], 2));
-        grow = grow || mx[i] - m[i] > kFp4Grow || (m[i] == ninf() && mx[i] > m[i]);
-      }
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          float top = m[n][c];
+#pragma unroll
+          for (int mk = 0; mk < MK; ++mk)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = s[n][mk][2 * e + c] * factor[n][c];
+              if (masked) {
+                const int key = key0 + mk * 16 + e * 8 + g;
+                x = (key >= row_lo[n][c] || key < p.sinks) && key < row_hi[n][c] ? x : ninf();
+              }
+              s[n][mk][2 * e + c] = x;
+              top = fmaxf(top, x);
+            }
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+          grow = grow || top - m[n][c] > kFp4Grow;
+          mx[n][c] = top;
+        }
       if (__any_sync(0xffffffffu, grow)) {   // the first keys, or a maximum that has outgrown the reference
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          const float f = ex2(m[i] - (mx[i] == ninf() ? 0.f : mx[i]));
-          l[i] *= f;
-          m[i] = mx[i];
+        for (int n = 0; n < NQ; ++n)
 #pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            o[d][2 * i] *= f;
-            o[d][2 * i + 1] *= f;
+          for (int c = 0; c < 2; ++c) {
+            const float f = ex2(m[n][c] - (mx[n][c] == ninf() ? 0.f : mx[n][c]));
+            l[n][c] *= f;
+            m[n][c] = mx[n][c];
+#pragma unroll
+            for (int d = 0; d < MD; ++d) {
+              o[n][d][c] *= f;
+              o[n][d][2 + c] *= f;
+            }
           }
-        }
       }
-      const float ref[2] = {(m[0] == ninf() ? 0.f : m[0]) - kFp4Shift, (m[1] == ninf() ? 0.f : m[1]) - kFp4Shift};
+      uint32_t pt[NQ][MK][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NQ; ++n) {
+        const float ref[2] = {(m[n][0] == ninf() ? 0.f : m[n][0]) - kFp4Shift, (m[n][1] == ninf() ? 0.f : m[n][1]) - kFp4Shift};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][e] = ex2(s[n][e] - ref[e >> 1]);
-          l[e >> 1] += s[n][e];
-        }
+        for (int mk = 0; mk < MK; ++mk)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float x = ex2(s[n][mk][2 * e] - ref[0]), y = ex2(s[n][mk][2 * e + 1] - ref[1]);
+            l[n][0] += x;
+            l[n][1] += y;
+            pt[n][mk][e] = transposed(H::pack(x, y));
+          }
+      }
 
-      // O += P V
+      // O^T += V^T P^T
 #pragma unroll
-      for (int k = 0; k < WK / 16; ++k) {
-        const uint32_t a[4] = {H::pack(s[2 * k][0], s[2 * k][1]), H::pack(s[2 * k][2], s[2 * k][3]),
-                               H::pack(s[2 * k + 1][0], s[2 * k + 1][1]), H::pack(s[2 * k + 1][2], s[2 * k + 1][3])};
-        constexpr int VW = DP / 64;   // words of 8 codes of a key that are this lane's columns
+      for (int k = 0; k < MK; ++k) {
+        constexpr int VW = DP / 64;   // words of 8 codes of a key that are this lane's rows
         uint32_t w[4][VW], f[2][DP == 256 ? 2 : 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
@@ -373,7 +435,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
 #pragma unroll
         for (int v = 0; v < VW; ++v) {
           const int blk = DP == 256 ? v / 2 : 0;
-          uint32_t even[2][4], odd[2][4];   // columns 0, 2, 4, 6 and 1, 3, 5, 7 of the word, pairs of keys
+          uint32_t even[2][4], odd[2][4];   // values 0, 2, 4, 6 and 1, 3, 5, 7 of the word, pairs of keys
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const uint32_t x = w[2 * i][v], y = w[2 * i + 1][v];
@@ -382,8 +444,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
           }
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            H::mma(o[v * 8 + 2 * c], a, mul2(even[0][c], f[0][blk]), mul2(even[1][c], f[1][blk]));
-            H::mma(o[v * 8 + 2 * c + 1], a, mul2(odd[0][c], f[0][blk]), mul2(odd[1][c], f[1][blk]));
+            const uint32_t a[4] = {mul2(even[0][c], f[0][blk]), mul2(odd[0][c], f[0][blk]), mul2(even[1][c], f[1][blk]),
+                                   mul2(odd[1][c], f[1][blk])};
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) H::mma(o[n][v * 4 + c], a, pt[n][k][0], pt[n][k][1]);
           }
         }
       }
@@ -394,24 +458,25 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
     asm volatile("cp.async.wait_group 0;" ::: "memory");
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 1);
-      l[i] += __shfl_xor_sync(0xffffffffu, l[i], 2);
-      const int r = g + i * 8;
-      if (t == 0) {
-        s_ml[warp][r][0] = m[i] - kFp4Shift;
-        s_ml[warp][r][1] = l[i];
+    for (int n = 0; n < NQ; ++n)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float sum = l[n][c];
+#pragma unroll
+        for (int x = 4; x < 32; x <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        const int r = n * 8 + 2 * t + c;
+        if (g == 0) {
+          s_ml[warp][r][0] = m[n][c] - kFp4Shift;
+          s_ml[warp][r][1] = sum;
+        }
+        // rows g and g + 8 of the product number d are the values 2 d and 2 d + 1 of this lane's
+#pragma unroll
+        for (int d = 0; d < MD; d += 2)
+          *reinterpret_cast<float4*>(s_o + (warp * BM + r) * DP + g * (DP / 8) + 2 * d) =
+              make_float4(o[n][d][c], o[n][d][2 + c], o[n][d + 1][c], o[n][d + 1][2 + c]);
       }
-      // column c of an 8-column product is value c DT + its number
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-#pragma unroll
-        for (int d = 0; d < DT; d += 4)
-          *reinterpret_cast<float4*>(s_o + (warp * BM + r) * DP + (2 * t + c) * DT + d) =
-              make_float4(o[d][2 * i + c], o[d + 1][2 * i + c], o[d + 2][2 * i + c], o[d + 3][2 * i + c]);
-    }
     __syncthreads();
-    const bool whole = len == cur.count;
+    const bool all = len == cur.count;
     const int slot = 2 * cta + (later ? 1 : 0);
     for (int id = tid; id < BM * (DP / 4); id += kAttnThreads) {
       const int r = id / (DP / 4), d = (id % (DP / 4)) * 4;
@@ -432,7 +497,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
         acc.z += f * x.z;
         acc.w += f * x.w;
       }
-      if (whole) {
+      if (all) {
         const float inv = ll > 0.f ? p.v_unit / ll : 0.f;
         const int tok = attn_token(p, r0 + r);
         const long long row = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r0 + r - tok * p.G);
@@ -458,10 +523,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
 }
 
 template <bool BF16>
-const void* attn_fp4_fn(int dp);
-inline int attn_fp4_smem(int dp) {
-  const int ring = dp == 64 ? AttnFp4Geom<64>::kSmem : dp == 128 ? AttnFp4Geom<128>::kSmem : AttnFp4Geom<256>::kSmem;
-  return ring > 4 * 16 * dp * 4 ? ring : 4 * 16 * dp * 4;
+const void* attn_fp4_fn(int dp, int bm);
+inline int attn_fp4_smem(int dp, int bm) {
+  if (bm == 8) return dp == 64 ? AttnFp4Geom<64, 1>::kSmem : dp == 128 ? AttnFp4Geom<128, 1>::kSmem : AttnFp4Geom<256, 1>::kSmem;
+  return dp == 64 ? AttnFp4Geom<64, 2>::kSmem : dp == 128 ? AttnFp4Geom<128, 2>::kSmem : AttnFp4Geom<256, 2>::kSmem;
 }
 
 }  // namespace sv

@@ -4,10 +4,14 @@
 namespace sv {
 
 template <>
-const void* attn_fp4_fn<false>(int dp) {
-  return dp == 64    ? reinterpret_cast<const void*>(&attn_fp4_kernel<false, 64>)
-         : dp == 128 ? reinterpret_cast<const void*>(&attn_fp4_kernel<false, 128>)
-                     : reinterpret_cast<const void*>(&attn_fp4_kernel<false, 256>);
+const void* attn_fp4_fn<false>(int dp, int bm) {
+  if (bm == 8)
+    return dp == 64    ? reinterpret_cast<const void*>(&attn_fp4_kernel<false, 64, 1>)
+           : dp == 128 ? reinterpret_cast<const void*>(&attn_fp4_kernel<false, 128, 1>)
+                       : reinterpret_cast<const void*>(&attn_fp4_kernel<false, 256, 1>);
+  return dp == 64    ? reinterpret_cast<const void*>(&attn_fp4_kernel<false, 64, 2>)
+         : dp == 128 ? reinterpret_cast<const void*>(&attn_fp4_kernel<false, 128, 2>)
+                     : reinterpret_cast<const void*>(&attn_fp4_kernel<false, 256, 2>);
 }
 
 }  // namespace sv

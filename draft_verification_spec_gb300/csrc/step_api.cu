@@ -135,13 +135,14 @@ size_t attention_workspace(int dtype, int q_heads, int kv_heads, int dim, int ma
   int sms = 0;
   if (sm_count(&sms) != SPEC_OK) return 0;
   const long long rows = static_cast<long long>(max_q) * (q_heads / kv_heads);
-  size_t most = 0;   // over the kernels that rows and dim admit, with first tokens kept or not
+  size_t most = 0;   // over the kernels that rows and dim admit
   for (int kind = 0; kind < 4; ++kind) {
     if (!fp4 && ((kind == 0) != (rows <= 16) || (kind >= 2 && (dim < 64 || dim > 128 || (kind == 3) != (rows > 128))))) continue;
     if (fp4 && kind != sv::attention_fp4_kind(static_cast<int>(rows < 1024 ? rows : 1024), dim, 1.f) && kind != 0) continue;
-    for (int sinks = 0; sinks < (fp4 ? 1 : 2); ++sinks) {
+    for (int variant = 0; variant < 2; ++variant) {   // first tokens kept or not; over 4 bits, tiles of 8 rows or 16
       sv::AttnPlan plan;
-      if (sv::attention_plan({dtype == SPEC_BF16, sinks != 0, fp4}, kind, 1, dim, sms, &plan) != cudaSuccess) return 0;
+      if (sv::attention_plan({dtype == SPEC_BF16, !fp4 && variant, fp4}, kind, fp4 && variant ? 16 : 1, dim, sms, &plan) != cudaSuccess)
+        return 0;
       const size_t n = partial_bytes(plan, dim);
       most = n > most ? n : most;
     }
