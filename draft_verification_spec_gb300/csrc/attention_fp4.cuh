@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
   using Geo = AttnFp4Geom<DP, NQ>;
   constexpr int BM = 8 * NQ, BN = kFp4BN, WK = kFp4WarpKeys, MK = WK / 16, MD = DP / 16, STAGES = Geo::kStages;
   constexpr int WORDS = DP / 32;         // words of 8 codes that a lane reads of a key, of K
+  static_assert(MK == 2, "the maximum is written out for 32 keys a warp");
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnSchedSmem<kAttnThreads> sched;
   __shared__ float s_ml[4][BM][2];
@@ -126,6 +127,15 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
   const uint32_t ring = smem_addr(smem) + warp * STAGES * Geo::kStage;
   const int D = p.c.D, P = p.c.page_size;
   const bool whole = p.s.whole && p.s.alike;   // keys and values in 16-byte pieces, all from one 32-bit offset
+  // where this lane reads in a tile: its part of key g and of keys 2 t and 2 t + 1; the other keys follow 8 and 16 keys
+  // behind, at the same place of the pieces' permutation
+  constexpr int R8 = 8 * Geo::kRow;
+  const uint32_t k_at = fp4_k_piece<DP>(g, DP == 64 ? t >> 1 : t) + (DP == 64 ? (t & 1) * 8 : 0);
+  const uint32_t k_at1 = DP == 256 ? fp4_k_piece<DP>(g, 4 + t) : 0;
+  const uint32_t ks_at = g * Geo::kScale + (DP == 64 ? t : t * 2);
+  const int vc = DP == 64 ? g >> 2 : DP == 128 ? g >> 1 : g, vb = DP == 64 ? (g & 3) * 4 : DP == 128 ? (g & 1) * 8 : 0;
+  const uint32_t v_at[2] = {fp4_v_piece<DP>(2 * t, vc) + vb, fp4_v_piece<DP>(2 * t + 1, vc) + vb};
+  const uint32_t vs_at = 2 * t * Geo::kScale + (DP == 64 ? g >> 1 : DP == 128 ? g : g * 2);
 
   while (true) {
     const int len = k1 - k0;
@@ -150,9 +160,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
       return __ldg(table + col);
     };
     // copies of tile j, whose page ids are there
-    auto load_tile = [&](int j, int pg, int in) {
+    auto load_tile = [&](int j, uint32_t st, int pg, int in) {
       if (j < len) {
-        const uint32_t st = ring + j % STAGES * Geo::kStage;
         const bool has = pg >= 0 && pg < p.c.pages && in >= 0;
         if (in >= 0 && !has) atomicOr(p.status, kStatusPageRange);
         const uint32_t dks = st + 2 * Geo::kCodes + lane * Geo::kScale, dvs = dks + Geo::kScales;
@@ -201,7 +210,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
 #pragma unroll
       for (int j = 0; j < STAGES; ++j) pg[j] = page_of(j, &in[j]);
 #pragma unroll
-      for (int j = 0; j < STAGES - 1; ++j) load_tile(j, pg[j], in[j]);
+      for (int j = 0; j < STAGES - 1; ++j) load_tile(j, ring + j * Geo::kStage, pg[j], in[j]);
       pg_next = pg[STAGES - 1];
       in_next = in[STAGES - 1];
     }
@@ -234,7 +243,15 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
         }
       }
-      float mine = p.scale_log2;
+      // a negative scale turns the query's sign, one of zero becomes too small to tell: the factors are positive
+      float mine = fmaxf(fabsf(p.scale_log2), 1e-30f);
+      if (p.scale_log2 < 0.f) {
+#pragma unroll
+        for (int s = 0; s < DP / 16; ++s) {
+          qf[n][s][0] ^= 0x80008000u;
+          qf[n][s][1] ^= 0x80008000u;
+        }
+      }
       if (BF16) {
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
@@ -284,13 +301,12 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
       }
     }
 
+    uint32_t sk = ring, free = ring + (STAGES - 1) * Geo::kStage;   // the tile to work on, the slot to fill
     for (int j = 0; j < len; ++j) {
       asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 2) : "memory");
       __syncwarp();
-      load_tile(j + STAGES - 1, pg_next, in_next);
+      load_tile(j + STAGES - 1, free, pg_next, in_next);
       pg_next = page_of(j + STAGES, &in_next);
-      const uint32_t sk = ring + j % STAGES * Geo::kStage, sv_ = sk + Geo::kCodes;
-      const uint32_t sks = sk + 2 * Geo::kCodes, svs = sks + Geo::kScales;
 
       // S^T = K Q^T: this warp's 32 keys x the rows
       float s[NQ][MK][4];
@@ -303,11 +319,11 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
         uint32_t w[2][WORDS], f[2][DP == 64 ? 1 : WORDS / 2];   // keys g and g + 8: codes, scales of blocks (twice each)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = mk * 16 + e * 8 + g;
+          const uint32_t at = sk + (2 * mk + e) * R8, ks = sk + ks_at + 2 * Geo::kCodes + (2 * mk + e) * 8 * Geo::kScale;
           uint32_t sc;
           if constexpr (DP == 64) {
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1]) : "r"(sk + fp4_k_piece<DP>(r, t >> 1) + (t & 1) * 8));
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(sks + r * Geo::kScale + t));
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1]) : "r"(at + k_at));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(ks));
             const uint32_t two = fp4_scales(sc);
             f[e][0] = __byte_perm(two, two, 0x1010);
           } else {
@@ -315,8 +331,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
             for (int h = 0; h < DP / 128; ++h) {
               asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                            : "=r"(w[e][4 * h]), "=r"(w[e][4 * h + 1]), "=r"(w[e][4 * h + 2]), "=r"(w[e][4 * h + 3])
-                           : "r"(sk + fp4_k_piece<DP>(r, h * 4 + t)));
-              asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc) : "r"(sks + r * Geo::kScale + h * 8 + t * 2));
+                           : "r"(at + (h ? k_at1 : k_at)));
+              asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc) : "r"(ks + h * 8));
               const uint32_t two = fp4_scales(sc);
               f[e][2 * h] = __byte_perm(two, two, 0x1010);
               f[e][2 * h + 1] = __byte_perm(two, two, 0x3232);
@@ -344,39 +360,37 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
       // masks, reference and sum; P^T as the second product's operand
       const int key0 = tile(j) * BN + warp * WK;
       const bool masked = key0 + WK > w_hi || key0 < w_lo;
-      float mx[NQ][2];
+      if (masked) {
+#pragma unroll
+        for (int n = 0; n < NQ; ++n)
+#pragma unroll
+          for (int mk = 0; mk < MK; ++mk)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + mk * 16 + (e >> 1) * 8 + g, c = e & 1;
+              if (!((key >= row_lo[n][c] || key < p.sinks) && key < row_hi[n][c])) s[n][mk][e] = ninf();
+            }
+      }
+      float mx[NQ][2];   // of this lane's keys: the warp's is wanted only where one of them has outgrown the reference
       bool grow = false;
 #pragma unroll
       for (int n = 0; n < NQ; ++n)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          float top = m[n][c];
-#pragma unroll
-          for (int mk = 0; mk < MK; ++mk)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float x = s[n][mk][2 * e + c] * factor[n][c];
-              if (masked) {
-                const int key = key0 + mk * 16 + e * 8 + g;
-                x = (key >= row_lo[n][c] || key < p.sinks) && key < row_hi[n][c] ? x : ninf();
-              }
-              s[n][mk][2 * e + c] = x;
-              top = fmaxf(top, x);
-            }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
-          grow = grow || top - m[n][c] > kFp4Grow;
-          mx[n][c] = top;
+          mx[n][c] = fmaxf(fmaxf(s[n][0][c], s[n][0][2 + c]), fmaxf(s[n][1][c], s[n][1][2 + c])) * factor[n][c];
+          grow = grow || mx[n][c] - m[n][c] > kFp4Grow;
         }
-      if (__any_sync(0xffffffffu, grow)) {   // the first keys, or a maximum that has outgrown the reference
+      if (__any_sync(0xffffffffu, grow)) {   // (the first keys too)
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            const float f = ex2(m[n][c] - (mx[n][c] == ninf() ? 0.f : mx[n][c]));
+            float top = fmaxf(m[n][c], mx[n][c]);
+#pragma unroll
+            for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+            const float f = ex2(m[n][c] - (top == ninf() ? 0.f : top));
             l[n][c] *= f;
-            m[n][c] = mx[n][c];
+            m[n][c] = top;
 #pragma unroll
             for (int d = 0; d < MD; ++d) {
               o[n][d][c] *= f;
@@ -387,12 +401,12 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
       uint32_t pt[NQ][MK][2];
 #pragma unroll
       for (int n = 0; n < NQ; ++n) {
-        const float ref[2] = {(m[n][0] == ninf() ? 0.f : m[n][0]) - kFp4Shift, (m[n][1] == ninf() ? 0.f : m[n][1]) - kFp4Shift};
+        const float ref[2] = {kFp4Shift - (m[n][0] == ninf() ? 0.f : m[n][0]), kFp4Shift - (m[n][1] == ninf() ? 0.f : m[n][1])};
 #pragma unroll
         for (int mk = 0; mk < MK; ++mk)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            const float x = ex2(s[n][mk][2 * e] - ref[0]), y = ex2(s[n][mk][2 * e + 1] - ref[1]);
+            const float x = ex2(fmaf(s[n][mk][2 * e], factor[n][0], ref[0])), y = ex2(fmaf(s[n][mk][2 * e + 1], factor[n][1], ref[1]));
             l[n][0] += x;
             l[n][1] += y;
             pt[n][mk][e] = transposed(H::pack(x, y));
@@ -406,29 +420,28 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
         uint32_t w[4][VW], f[2][DP == 256 ? 2 : 1];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          const int r = k * 16 + 2 * t + (i & 1) + (i >> 1) * 8;
+          const uint32_t at = sk + v_at[i & 1] + Geo::kCodes + (2 * k + (i >> 1)) * R8;
           if constexpr (DP == 64)
-            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i][0]) : "r"(sv_ + fp4_v_piece<DP>(r, g >> 2) + (g & 3) * 4));
+            asm volatile("ld.shared.u32 %0, [%1];" : "=r"(w[i][0]) : "r"(at));
           else if constexpr (DP == 128)
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(sv_ + fp4_v_piece<DP>(r, g >> 1) + (g & 1) * 8));
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[i][0]), "=r"(w[i][1]) : "r"(at));
           else
             asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                          : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
-                         : "r"(sv_ + fp4_v_piece<DP>(r, g)));
+                         : "r"(at));
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {   // scales of the keys 2 t + 8 i and the next one
-          const uint32_t at = svs + (k * 16 + 2 * t + 8 * i) * Geo::kScale;
+          const uint32_t at = sk + vs_at + 2 * Geo::kCodes + Geo::kScales + (2 * k + i) * 8 * Geo::kScale;
           uint32_t x, y;
           if constexpr (DP == 256) {
-            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(at + g * 2));
-            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(y) : "r"(at + Geo::kScale + g * 2));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(x) : "r"(at));
+            asm volatile("ld.shared.u16 %0, [%1];" : "=r"(y) : "r"(at + Geo::kScale));
             f[i][0] = fp4_scales(__byte_perm(x, y, 0x0040));
             f[i][1] = fp4_scales(__byte_perm(x, y, 0x0051));
           } else {
-            const int blk = DP == 64 ? g >> 1 : g;
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at + blk));
-            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(y) : "r"(at + Geo::kScale + blk));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(x) : "r"(at));
+            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(y) : "r"(at + Geo::kScale));
             f[i][0] = fp4_scales(x | y << 8);
           }
         }
@@ -452,6 +465,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
         }
       }
       __syncwarp();   // every lane has read the tile before its slot is filled again
+      free = sk;
+      sk = sk + Geo::kStage == ring + STAGES * Geo::kStage ? ring : sk + Geo::kStage;
     }
 
     // join the warps' shares of the keys and write the rows
