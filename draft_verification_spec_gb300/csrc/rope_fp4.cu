@@ -40,29 +40,27 @@ __device__ __forceinline__ uint32_t two_codes(float x, float y, float inverse) {
   asm("{\n\t.reg .b8 c;\n\tcvt.rn.satfinite.e2m1x2.f32 c, %1, %2;\n\tcvt.u32.u8 %0, c;\n\t}" : "=r"(r) : "f"(q.y), "f"(q.x));
   return r;
 }
-// A block of 16: its scale; its codes, eight to a word.
-struct Block {
-  uint32_t scale;
-  uint2 codes;
-  __device__ __forceinline__ bool operator!=(const Block& b) const {
-    return scale != b.scale || codes.x != b.codes.x || codes.y != b.codes.y;
-  }
+// Half a block (the other half is the neighbouring lane's, of the same warp): the block's scale, eight codes.
+struct Half {
+  uint32_t scale, codes;
 };
-__device__ __forceinline__ Block hold(const float (&x)[16], float unit) {
+// Called by the whole warp.
+__device__ __forceinline__ Half hold(const float (&x)[8], float unit) {
   float top = 0.f;
-  bool nan = false;
+  int nan = 0;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
+  for (int i = 0; i < 8; ++i) {
     top = fmaxf(top, fabsf(x[i]));
-    nan = nan || x[i] != x[i];
+    nan |= x[i] != x[i];
   }
-  Block b;
+  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+  nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
+  Half b;
   float inverse;
   b.scale = block_scale(top, nan, unit, &inverse);
-  uint32_t w[2] = {0u, 0u};
+  b.codes = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) w[i / 4] |= two_codes(x[2 * i], x[2 * i + 1], inverse) << (i % 4 * 8);
-  b.codes = make_uint2(w[0], w[1]);
+  for (int i = 0; i < 4; ++i) b.codes |= two_codes(x[2 * i], x[2 * i + 1], inverse) << (i * 8);
   return b;
 }
 
@@ -77,21 +75,6 @@ __device__ __noinline__ float rotated_exactly(float x, float y, float turn, unsi
   double s, c;
   sincospi(static_cast<double>(static_cast<long long>(phase)) * 0x1p-63, &s, &c);
   return __double2float_rn((x * c + static_cast<double>(turn) * y * s) * factor);
-}
-
-template <typename T>
-__device__ __forceinline__ void load16(const T* p, float (&x)[16]) {
-  uint4 raw[2] = {__ldg(reinterpret_cast<const uint4*>(p)), __ldg(reinterpret_cast<const uint4*>(p) + 1)};
-#pragma unroll
-  for (int i = 0; i < 16; ++i) x[i] = to_f(reinterpret_cast<const T*>(raw)[i]);
-}
-template <typename T>
-__device__ __forceinline__ void store16(T* p, const float (&x)[16]) {
-  uint4 raw[2];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) from_f(x[i], reinterpret_cast<T*>(raw) + i);
-  reinterpret_cast<uint4*>(p)[0] = raw[0];
-  reinterpret_cast<uint4*>(p)[1] = raw[1];
 }
 
 // Byte offsets of a token's slot in the four arrays (-1: not stored), its position, whether a request has it.
@@ -122,21 +105,74 @@ __device__ __forceinline__ Slot slot_of(const RopeParams& p, const Fp4Scales& s,
 }
 
 // The form for whole blocks: the rotated part is whole blocks (half layout: each half is), rows are 16-byte aligned.
-// A CTA takes `per_cta` tokens; a thread takes a block of 16 values, or a block and its partner where they turn
-// together.
+// A CTA takes `per_cta` tokens: a warp each looks up the slot, the CTA computes the angles once for all heads.  Then each
+// thread moves 16-byte pieces of 8 values (a piece and its partner where they turn together), the next one's loads
+// issued before the current one's work; two lanes hold a block.  (A thread a block reads and writes every second 16 bytes
+// at a time: 80 us for 8192 tokens of 40 + 8 heads of 128.)
 template <int DTYPE, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_fp4_kernel(const RopeParams p, const Fp4Scales s, float k_unit, float v_unit, int per_cta) {
   using T = typename RopeType<DTYPE>::T;
-  constexpr int PP = INTERLEAVED ? 8 : 16;   // pairs of a unit
+  constexpr int PP = INTERLEAVED ? 4 : 8;   // pairs of a unit
   extern __shared__ __align__(16) float2 s_cs[];   // [per_cta][rotary / 2]
   __shared__ Slot slots[kFp4MaxTokens];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int n0 = blockIdx.x * per_cta, tokens = min(per_cta, p.c.N - n0);
   const int half = p.rotary / 2, D = p.c.D, Hk = p.c.Hkv;
   const int turn = half / PP;                // rotated units per head
-  const int per_head = turn + (D - p.rotary) / 16;
-  const int rot_units = (p.Hq + Hk) * per_head, units = rot_units + Hk * (D / 16);
+  const int per_head = turn + (D - p.rotary) / 8;
+  const int rot_units = (p.Hq + Hk) * per_head, units = rot_units + Hk * (D / 8);
+  const int total = tokens * units;
+  // quotients of small numbers: floor(n ceil(2^32 / d) / 2^32) is exact while n d < 2^32 (the launch sees to it that
+  // both are below 2^16)
+  auto inverse = [](int d) { return d > 1 ? 0xffffffffu / static_cast<unsigned>(d) + 1u : 0u; };
+  const unsigned inv_units = inverse(units), inv_head = inverse(per_head), inv_value = inverse(D / 8);
+  auto quotient = [](int n, unsigned inv) { return inv ? static_cast<int>(__umulhi(static_cast<unsigned>(n), inv)) : n; };
+
+  struct Unit {
+    uint4 a, b;
+    int t, kind, h, at;   // kind 0: query, 1: key, 2: value, -1: none; at: first value of the head; + 4: rotated
+  };
+  auto load = [&](int u, Unit& x) {
+    x.kind = -1;
+    x.t = x.h = x.at = 0;
+    x.a = x.b = make_uint4(0, 0, 0, 0);
+    if (u >= total) return;
+    x.t = quotient(u, inv_units);
+    int r = u - x.t * units;
+    const int n = n0 + x.t;
+    const T* src;
+    if (r < rot_units) {
+      const int h = quotient(r, inv_head), j = r - h * per_head, hk = h - p.Hq;
+      const bool rotate = j < turn;
+      x.kind = (hk < 0 ? 0 : 1) + (rotate ? 4 : 0);
+      x.h = hk < 0 ? h : hk;
+      x.at = rotate ? j * 8 : p.rotary + (j - turn) * 8;
+      src = hk < 0 ? reinterpret_cast<const T*>(p.q) + n * p.q_token + h * p.q_head
+                   : reinterpret_cast<const T*>(p.k) + n * p.k_token + hk * p.k_head;
+      x.a = __ldg(reinterpret_cast<const uint4*>(src + x.at));
+      if (!INTERLEAVED && rotate) x.b = __ldg(reinterpret_cast<const uint4*>(src + x.at + half));
+    } else {
+      r -= rot_units;
+      x.kind = 2;
+      x.h = quotient(r, inv_value);
+      x.at = (r - x.h * (D / 8)) * 8;
+      src = reinterpret_cast<const T*>(p.v) + n * p.v_token + x.h * p.v_head;
+      x.a = __ldg(reinterpret_cast<const uint4*>(src + x.at));
+    }
+  };
+  auto widen = [](const uint4& raw, float (&x)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = to_f(reinterpret_cast<const T*>(&raw)[i]);
+  };
+  auto store = [](T* to, const float (&x)[8]) {
+    uint4 raw;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) from_f(x[i], reinterpret_cast<T*>(&raw) + i);
+    *reinterpret_cast<uint4*>(to) = raw;
+  };
+  Unit cur;
+  load(tid, cur);   // in flight while the tokens' slots are looked up
 
   for (int t = warp; t < tokens; t += kRopeThreads / 32) {
     const Slot r = slot_of(p, s, n0 + t, lane);
@@ -151,40 +187,17 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
   __syncthreads();
 
-  for (int u = tid; u < tokens * units; u += kRopeThreads) {
-    const int t = u / units, n = n0 + t;
-    int r = u - t * units;
-    const Slot& slot = slots[t];
-    if (!slot.has) continue;
-    float a[16], b[16];
-    if (r >= rot_units) {   // values
-      r -= rot_units;
-      const int h = r / (D / 16), j = r - h * (D / 16);
-      if (slot.v < 0) continue;
-      load16(reinterpret_cast<const T*>(p.v) + n * p.v_token + h * p.v_head + j * 16, a);
-      const Block x = hold(a, v_unit);
-      *reinterpret_cast<uint2*>(p.c.v + slot.v + h * p.c.v_head + j * 8) = x.codes;
-      s.v[slot.vs + h * s.v_head + j] = static_cast<uint8_t>(x.scale);
-      continue;
-    }
-    const int h = r / per_head, j = r - h * per_head, hk = h - p.Hq;
-    const bool rotate = j < turn, pair = rotate && !INTERLEAVED;
-    const int at = rotate ? j * 16 : p.rotary + (j - turn) * 16;
-    const T* src = hk < 0 ? reinterpret_cast<const T*>(p.q) + n * p.q_token + h * p.q_head
-                          : reinterpret_cast<const T*>(p.k) + n * p.k_token + hk * p.k_head;
-    T* dst = hk < 0 ? reinterpret_cast<T*>(p.q_out) + n * p.qo_token + h * p.qo_head
-                    : (p.k_out ? reinterpret_cast<T*>(p.k_out) + n * p.ko_token + hk * p.ko_head : nullptr);
-    load16(src + at, a);
-    if (pair) load16(src + at + half, b);
-    const bool held = hk >= 0 && slot.k >= 0;
-    float a0[16], b0[16];   // as they were: for the error, and for the exact rotation
-    if (rotate) {
-#pragma unroll
-      for (int i = 0; i < 16; ++i) {
-        a0[i] = a[i];
-        if (!INTERLEAVED) b0[i] = b[i];
-      }
-      const float4* cs = reinterpret_cast<const float4*>(s_cs + t * half) + j;
+  for (int u0 = 0; u0 < total; u0 += kRopeThreads) {   // the same for the whole block: warps work together below
+    Unit next;
+    load(u0 + kRopeThreads + tid, next);
+    const bool rotate = cur.kind >= 4;
+    const int kind = cur.kind & 3, n = n0 + cur.t;
+    const bool mine = cur.kind >= 0 && slots[cur.t].has;
+    float a[8], b[8];
+    widen(cur.a, a);
+    widen(cur.b, b);
+    if (mine && rotate) {
+      const float4* cs = reinterpret_cast<const float4*>(s_cs + cur.t * half) + cur.at / 8;
 #pragma unroll
       for (int i = 0; i < PP; i += 2) {
         const float4 w = cs[(i >> 1) * turn];   // cos, sin of pairs i and i + 1
@@ -199,51 +212,70 @@ __global__ void __launch_bounds__(kRopeThreads)
         }
       }
     }
-    if (dst) {
-      store16(dst + at, a);
-      if (pair) store16(dst + at + half, b);
+    const bool pair = rotate && !INTERLEAVED;
+    if (mine && kind < 2) {
+      T* dst = kind == 0 ? reinterpret_cast<T*>(p.q_out) + n * p.qo_token + cur.h * p.qo_head
+                         : (p.k_out ? reinterpret_cast<T*>(p.k_out) + n * p.ko_token + cur.h * p.ko_head : nullptr);
+      if (dst) {
+        store(dst + cur.at, a);
+        if (pair) store(dst + cur.at + half, b);
+      }
     }
-    if (!held) continue;
-    uint8_t* codes = p.c.k + slot.k + hk * p.c.k_head;
-    uint8_t* scales = s.k + slot.ks + hk * s.k_head;
+    const bool key = kind == 1;
+    const bool held = mine && kind > 0 && (key ? slots[cur.t].k : slots[cur.t].v) >= 0;
+    if (__any_sync(0xffffffffu, held)) {
+      const float unit = key ? k_unit : v_unit;
+      float a0[8], b0[8];   // as they were: for the error, and for the exact rotation
+      widen(cur.a, a0);
+      widen(cur.b, b0);
 #pragma unroll
-    for (int which = 0; which < (INTERLEAVED ? 1 : 2); ++which) {
-      if (which && !pair) break;
-      float (&x)[16] = which ? b : a;
-      if (rotate) {
-        // both ends of each key's error interval, the larger in magnitude in x: scales rise with the largest magnitude and
-        // codes with the value, so two equal blocks mean that no key between the ends makes another one
+      for (int which = 0; which < (INTERLEAVED ? 1 : 2); ++which) {
+        if (which && !__any_sync(0xffffffffu, held && pair)) break;
+        float (&x)[8] = which ? b : a;
         auto partner = [&](int i) { return INTERLEAVED ? a0[i ^ 1] : which ? a0[i] : b0[i]; };
         auto self = [&](int i) { return which ? b0[i] : a0[i]; };
-        float lo[16];
+        // both ends of each key's error interval, the larger in magnitude in x: scales rise with the largest magnitude and
+        // codes with the value, so two equal blocks mean that no key between the ends makes another one
+        float lo[8];
         bool clear = true;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 8; ++i) {
           const float e = (fabsf(self(i)) + fabsf(partner(i))) * fabsf(p.factor) * 4.76837158203125e-7f;   // 2^-21
           const float below = rounded<T>(x[i] - e), above = rounded<T>(x[i] + e);
           const bool up = fabsf(above) >= fabsf(below);
-          clear = clear && below == above;
-          x[i] = up ? above : below;
-          lo[i] = up ? below : above;
+          if (rotate) {
+            clear = clear && below == above;
+            x[i] = up ? above : below;
+          }
+          lo[i] = rotate && up ? below : rotate ? above : x[i];
         }
-        if (!clear) {
-          if (hold(x, k_unit) != hold(lo, k_unit)) {
-            const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(slot.pos));
+        Half y = hold(x, unit);
+        if (__any_sync(0xffffffffu, held && !clear)) {
+          const Half z = hold(lo, unit);
+          bool differs = y.scale != z.scale || y.codes != z.codes;
+          differs = __shfl_xor_sync(0xffffffffu, differs, 1) || differs;
+          if (__any_sync(0xffffffffu, held && differs)) {
+            const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(slots[cur.t].pos));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              if (lo[i] == x[i]) continue;
-              const int k = INTERLEAVED ? j * 8 + i / 2 : j * 16 + i;
+            for (int i = 0; i < 8; ++i) {
+              if (!held || !differs || lo[i] == x[i]) continue;
+              const int k = INTERLEAVED ? cur.at / 2 + i / 2 : cur.at + i;
               const bool second = INTERLEAVED ? i & 1 : which;
               x[i] = rounded<T>(rotated_exactly(self(i), partner(i), second ? 1.f : -1.f, p.freq[k] * pos, p.factor));
             }
+            y = hold(x, unit);
           }
         }
+        if (held && (!which || pair)) {
+          const int i = cur.at + which * half;
+          uint8_t* codes = key ? p.c.k + slots[cur.t].k + cur.h * p.c.k_head : p.c.v + slots[cur.t].v + cur.h * p.c.v_head;
+          uint8_t* scales = key ? s.k + slots[cur.t].ks + cur.h * s.k_head : s.v + slots[cur.t].vs + cur.h * s.v_head;
+          *reinterpret_cast<uint32_t*>(codes + i / 2) = y.codes;
+          if (i % 16 == 0) scales[i / 16] = static_cast<uint8_t>(y.scale);
+        }
       }
-      const Block y = hold(x, k_unit);
-      const int i = at + which * half;
-      *reinterpret_cast<uint2*>(codes + i / 2) = y.codes;
-      scales[i / 16] = static_cast<uint8_t>(y.scale);
     }
+    cur = next;
   }
 }
 
@@ -357,6 +389,8 @@ cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, 
                                p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0};
   bool whole = p.rotary % (p.interleaved ? 16 : 32) == 0;
   for (long long st : strides) whole = whole && st % 8 == 0;
+  const long long pieces = (p.Hq + 2ll * p.c.Hkv) * (p.c.D / 8);   // of a token; the kernel's quotients hold up to 2^16
+  whole = whole && pieces < (1 << 16);
   const void* bases[] = {p.q, p.k, p.v, p.q_out, p.k_out};
   for (const void* b : bases) whole = whole && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
   if (!whole) {
@@ -365,9 +399,8 @@ cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, 
     if (dtype == 2) rope_fp4_scalar_kernel<2><<<grid, block, 0, stream>>>(p, s, k_unit, v_unit);
     return cudaGetLastError();
   }
-  // few tokens: a CTA each; many: as many tokens a CTA as make about 1024 blocks
-  const long long blocks = (p.Hq + 2ll * p.c.Hkv) * (p.c.D / 16);
-  int per = p.c.N <= 4 * sms ? 1 : static_cast<int>(1024 / blocks);
+  // few tokens: a CTA each; many: as many tokens a CTA as make about 2048 pieces (as rope_append.cu)
+  int per = p.c.N <= 4 * sms ? 1 : static_cast<int>(2048 / pieces);
   per = per < 1 ? 1 : per > kFp4MaxTokens ? kFp4MaxTokens : per;
   const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);
   const size_t smem = sizeof(float2) * (p.rotary / 2) * per;
