@@ -10,11 +10,13 @@
 // - x has 11 significant bits at most and scale x unit 4, so a quotient is either exactly on a border between two codes
 //   or at least 2^-11 of its size away from it (a border has 3 bits).  x times the reciprocal is off by 2^-23; rounding
 //   that to half precision (11 bits) lands on the border in the first case and off it in the second.
-// - largest / (6 unit) is exact where it is a tie of e4m3 (5 bits), and further from one than fp32's rounding elsewhere.
+// - largest / (6 unit) in the same way: a tie of e4m3 has 5 bits, 6 times that 7.
 // - a rotated key's fp32 error, (|x| + |y|) 2^-21.5 at most, can move its rounding to 16 bits.  Where both ends of that
 //   interval do not give the same scale and codes (1 block in some 10^4), the keys in question are rotated in 64 bits.
 //
 // Bound: HBM: q read and written, k and v read, 4.5 bits a value written, no reuse.
+#include <type_traits>
+
 #include "rope_device.cuh"
 
 namespace sv {
@@ -23,15 +25,26 @@ namespace {
 
 constexpr int kFp4MaxTokens = 8;   // tokens per CTA: one warp each finds the request and the slot
 
-// The e4m3 scale (as a byte) of a block whose largest magnitude is `top`, and 1 / (scale unit).
-__device__ __forceinline__ uint32_t block_scale(float top, bool nan, float unit, float* inverse) {
-  const float want = fminf(fmaxf(__fdiv_rn(top, 6.f * unit), 0.001953125f), 448.f);
+// A cache's unit and what a largest magnitude is multiplied with.
+struct Unit4 {
+  float unit, sixth;   // 1 / (6 unit)
+};
+// The e4m3 scale (as a byte) of a block whose largest magnitude is `top` (NaN: it has one), and 1 / (scale unit).
+__device__ __forceinline__ uint32_t block_scale(float top, const Unit4& u, float* inverse) {
+  const __half2 want = __floats2half2_rn(fminf(fmaxf(top * u.sixth, 0.001953125f), 448.f), 0.f);
   uint16_t two;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(two) : "f"(0.f), "f"(want));
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(two) : "r"(*reinterpret_cast<const uint32_t*>(&want)));
   uint32_t half2;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(two));
-  *inverse = __frcp_rn(__low2float(*reinterpret_cast<const __half2*>(&half2)) * unit);
-  return nan ? 0x7fu : two & 0xffu;
+  const float scale = __low2float(*reinterpret_cast<const __half2*>(&half2)) * u.unit;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(*inverse) : "f"(scale));
+  return top != top ? 0x7fu : two & 0xffu;
+}
+// The larger; NaN if either is.
+__device__ __forceinline__ float larger(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
 }
 // Codes of two values, the first in the low half of the byte.
 __device__ __forceinline__ uint32_t two_codes(float x, float y, float inverse) {
@@ -45,24 +58,33 @@ struct Half {
   uint32_t scale, codes;
 };
 // Called by the whole warp.
-__device__ __forceinline__ Half hold(const float (&x)[8], float unit) {
-  float top = 0.f;
-  int nan = 0;
+__device__ __forceinline__ Half hold(const float (&x)[8], const Unit4& unit) {
+  float top = fabsf(x[0]);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    top = fmaxf(top, fabsf(x[i]));
-    nan |= x[i] != x[i];
-  }
-  top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-  nan |= __shfl_xor_sync(0xffffffffu, nan, 1);
+  for (int i = 1; i < 8; ++i) top = larger(top, fabsf(x[i]));
+  top = larger(top, __shfl_xor_sync(0xffffffffu, top, 1));
   Half b;
   float inverse;
-  b.scale = block_scale(top, nan, unit, &inverse);
+  b.scale = block_scale(top, unit, &inverse);
   b.codes = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) b.codes |= two_codes(x[2 * i], x[2 * i + 1], inverse) << (i * 8);
   return b;
 }
+
+// Two values rounded to T, and what they are then.
+__device__ __forceinline__ uint32_t pack2(float a, float b, __nv_bfloat16*) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack2(float a, float b, __half*) {
+  const __half2 r = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ float2 unpack2(uint32_t x, __nv_bfloat16*) {
+  return make_float2(__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u));
+}
+__device__ __forceinline__ float2 unpack2(uint32_t x, __half*) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
 template <typename T>
 __device__ __forceinline__ float rounded(float x) {
@@ -111,7 +133,7 @@ __device__ __forceinline__ Slot slot_of(const RopeParams& p, const Fp4Scales& s,
 // at a time: 80 us for 8192 tokens of 40 + 8 heads of 128.)
 template <int DTYPE, bool INTERLEAVED>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_fp4_kernel(const RopeParams p, const Fp4Scales s, float k_unit, float v_unit, int per_cta) {
+    rope_fp4_kernel(const RopeParams p, const Fp4Scales s, const Unit4 k_unit, const Unit4 v_unit, int per_cta) {
   using T = typename RopeType<DTYPE>::T;
   constexpr int PP = INTERLEAVED ? 4 : 8;   // pairs of a unit
   extern __shared__ __align__(16) float2 s_cs[];   // [per_cta][rotary / 2]
@@ -120,47 +142,15 @@ __global__ void __launch_bounds__(kRopeThreads)
   const int n0 = blockIdx.x * per_cta, tokens = min(per_cta, p.c.N - n0);
   const int half = p.rotary / 2, D = p.c.D, Hk = p.c.Hkv;
   const int turn = half / PP;                // rotated units per head
-  const int per_head = turn + (D - p.rotary) / 8;
-  const int rot_units = (p.Hq + Hk) * per_head, units = rot_units + Hk * (D / 8);
-  const int total = tokens * units;
   // quotients of small numbers: floor(n ceil(2^32 / d) / 2^32) is exact while n d < 2^32 (the launch sees to it that
   // both are below 2^16)
   auto inverse = [](int d) { return d > 1 ? 0xffffffffu / static_cast<unsigned>(d) + 1u : 0u; };
-  const unsigned inv_units = inverse(units), inv_head = inverse(per_head), inv_value = inverse(D / 8);
   auto quotient = [](int n, unsigned inv) { return inv ? static_cast<int>(__umulhi(static_cast<unsigned>(n), inv)) : n; };
+  // strides fit 32 bits here: one wide multiplication per address
+  auto at2 = [](int i, long long si, int j, long long sj) {
+    return static_cast<long long>(i) * static_cast<int>(si) + static_cast<long long>(j) * static_cast<int>(sj);
+  };
 
-  struct Unit {
-    uint4 a, b;
-    int t, kind, h, at;   // kind 0: query, 1: key, 2: value, -1: none; at: first value of the head; + 4: rotated
-  };
-  auto load = [&](int u, Unit& x) {
-    x.kind = -1;
-    x.t = x.h = x.at = 0;
-    x.a = x.b = make_uint4(0, 0, 0, 0);
-    if (u >= total) return;
-    x.t = quotient(u, inv_units);
-    int r = u - x.t * units;
-    const int n = n0 + x.t;
-    const T* src;
-    if (r < rot_units) {
-      const int h = quotient(r, inv_head), j = r - h * per_head, hk = h - p.Hq;
-      const bool rotate = j < turn;
-      x.kind = (hk < 0 ? 0 : 1) + (rotate ? 4 : 0);
-      x.h = hk < 0 ? h : hk;
-      x.at = rotate ? j * 8 : p.rotary + (j - turn) * 8;
-      src = hk < 0 ? reinterpret_cast<const T*>(p.q) + n * p.q_token + h * p.q_head
-                   : reinterpret_cast<const T*>(p.k) + n * p.k_token + hk * p.k_head;
-      x.a = __ldg(reinterpret_cast<const uint4*>(src + x.at));
-      if (!INTERLEAVED && rotate) x.b = __ldg(reinterpret_cast<const uint4*>(src + x.at + half));
-    } else {
-      r -= rot_units;
-      x.kind = 2;
-      x.h = quotient(r, inv_value);
-      x.at = (r - x.h * (D / 8)) * 8;
-      src = reinterpret_cast<const T*>(p.v) + n * p.v_token + x.h * p.v_head;
-      x.a = __ldg(reinterpret_cast<const uint4*>(src + x.at));
-    }
-  };
   auto widen = [](const uint4& raw, float (&x)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = to_f(reinterpret_cast<const T*>(&raw)[i]);
@@ -171,9 +161,6 @@ __global__ void __launch_bounds__(kRopeThreads)
     for (int i = 0; i < 8; ++i) from_f(x[i], reinterpret_cast<T*>(&raw) + i);
     *reinterpret_cast<uint4*>(to) = raw;
   };
-  Unit cur;
-  load(tid, cur);   // in flight while the tokens' slots are looked up
-
   for (int t = warp; t < tokens; t += kRopeThreads / 32) {
     const Slot r = slot_of(p, s, n0 + t, lane);
     if (lane == 0) slots[t] = r;
@@ -187,103 +174,148 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
   __syncthreads();
 
-  for (int u0 = 0; u0 < total; u0 += kRopeThreads) {   // the same for the whole block: warps work together below
-    Unit next;
-    load(u0 + kRopeThreads + tid, next);
-    const bool rotate = cur.kind >= 4;
-    const int kind = cur.kind & 3, n = n0 + cur.t;
-    const bool mine = cur.kind >= 0 && slots[cur.t].has;
-    float a[8], b[8];
-    widen(cur.a, a);
-    widen(cur.b, b);
-    if (mine && rotate) {
-      const float4* cs = reinterpret_cast<const float4*>(s_cs + cur.t * half) + cur.at / 8;
+  // the pieces of all queries, of all keys, of all values
+  auto pass = [&](auto what) {
+    constexpr int KIND = decltype(what)::value;   // 0: queries, 1: keys, 2: values
+    constexpr bool PAIR = KIND < 2 && !INTERLEAVED;
+    const int heads = KIND == 0 ? p.Hq : Hk, per_head = KIND == 2 ? D / 8 : turn + (D - p.rotary) / 8;
+    const int units = heads * per_head, total = tokens * units;
+    const unsigned inv_units = inverse(units), inv_head = inverse(per_head);
+    const T* from = reinterpret_cast<const T*>(KIND == 0 ? p.q : KIND == 1 ? p.k : p.v);
+    const long long s_token = KIND == 0 ? p.q_token : KIND == 1 ? p.k_token : p.v_token;
+    const long long s_head = KIND == 0 ? p.q_head : KIND == 1 ? p.k_head : p.v_head;
+    T* to = reinterpret_cast<T*>(KIND == 0 ? p.q_out : KIND == 1 ? p.k_out : nullptr);
+    const long long o_token = KIND == 0 ? p.qo_token : p.ko_token, o_head = KIND == 0 ? p.qo_head : p.ko_head;
+    struct Unit {
+      uint4 a, b;
+      int t, h, at;   // token (-1: none), head, first value
+      bool rotate;
+    };
+    auto load = [&](int u, Unit& x) {
+      x.t = -1;
+      x.h = x.at = 0;
+      x.rotate = false;
+      x.a = x.b = make_uint4(0, 0, 0, 0);
+      if (u >= total) return;
+      x.t = quotient(u, inv_units);
+      const int r = u - x.t * units;
+      x.h = quotient(r, inv_head);
+      const int j = r - x.h * per_head;
+      x.rotate = KIND < 2 && j < turn;
+      x.at = KIND == 2 || x.rotate ? j * 8 : p.rotary + (j - turn) * 8;
+      const T* src = from + at2(n0 + x.t, s_token, x.h, s_head) + x.at;
+      x.a = __ldg(reinterpret_cast<const uint4*>(src));
+      if (PAIR && x.rotate) x.b = __ldg(reinterpret_cast<const uint4*>(src + half));
+    };
+    Unit cur;
+    load(tid, cur);
+    for (int u0 = 0; u0 < total; u0 += kRopeThreads) {   // the same for the whole block: warps work together below
+      Unit next;
+      load(u0 + kRopeThreads + tid, next);
+      const bool mine = cur.t >= 0 && slots[cur.t].has;
+      float a[8], b[8];
+      widen(cur.a, a);
+      if (PAIR) widen(cur.b, b);
+      if (KIND < 2 && mine && cur.rotate) {
+        const float4* cs = reinterpret_cast<const float4*>(s_cs + cur.t * half) + cur.at / 8;
 #pragma unroll
-      for (int i = 0; i < PP; i += 2) {
-        const float4 w = cs[(i >> 1) * turn];   // cos, sin of pairs i and i + 1
+        for (int i = 0; i < PP; i += 2) {
+          const float4 w = cs[(i >> 1) * turn];   // cos, sin of pairs i and i + 1
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float c = e ? w.z : w.x, sn = e ? w.w : w.y;
-          float& x = INTERLEAVED ? a[2 * (i + e)] : a[i + e];
-          float& y = INTERLEAVED ? a[2 * (i + e) + 1] : b[i + e];
-          const float x1 = x * c - y * sn, y1 = y * c + x * sn;
-          x = x1;
-          y = y1;
-        }
-      }
-    }
-    const bool pair = rotate && !INTERLEAVED;
-    if (mine && kind < 2) {
-      T* dst = kind == 0 ? reinterpret_cast<T*>(p.q_out) + n * p.qo_token + cur.h * p.qo_head
-                         : (p.k_out ? reinterpret_cast<T*>(p.k_out) + n * p.ko_token + cur.h * p.ko_head : nullptr);
-      if (dst) {
-        store(dst + cur.at, a);
-        if (pair) store(dst + cur.at + half, b);
-      }
-    }
-    const bool key = kind == 1;
-    const bool held = mine && kind > 0 && (key ? slots[cur.t].k : slots[cur.t].v) >= 0;
-    if (__any_sync(0xffffffffu, held)) {
-      const float unit = key ? k_unit : v_unit;
-      float a0[8], b0[8];   // as they were: for the error, and for the exact rotation
-      widen(cur.a, a0);
-      widen(cur.b, b0);
-#pragma unroll
-      for (int which = 0; which < (INTERLEAVED ? 1 : 2); ++which) {
-        if (which && !__any_sync(0xffffffffu, held && pair)) break;
-        float (&x)[8] = which ? b : a;
-        auto partner = [&](int i) { return INTERLEAVED ? a0[i ^ 1] : which ? a0[i] : b0[i]; };
-        auto self = [&](int i) { return which ? b0[i] : a0[i]; };
-        // both ends of each key's error interval, the larger in magnitude in x: scales rise with the largest magnitude and
-        // codes with the value, so two equal blocks mean that no key between the ends makes another one
-        float lo[8];
-        bool clear = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float e = (fabsf(self(i)) + fabsf(partner(i))) * fabsf(p.factor) * 4.76837158203125e-7f;   // 2^-21
-          const float below = rounded<T>(x[i] - e), above = rounded<T>(x[i] + e);
-          const bool up = fabsf(above) >= fabsf(below);
-          if (rotate) {
-            clear = clear && below == above;
-            x[i] = up ? above : below;
+          for (int e = 0; e < 2; ++e) {
+            const float c = e ? w.z : w.x, sn = e ? w.w : w.y;
+            float& x = INTERLEAVED ? a[2 * (i + e)] : a[i + e];
+            float& y = INTERLEAVED ? a[2 * (i + e) + 1] : b[i + e];
+            const float x1 = x * c - y * sn, y1 = y * c + x * sn;
+            x = x1;
+            y = y1;
           }
-          lo[i] = rotate && up ? below : rotate ? above : x[i];
         }
-        Half y = hold(x, unit);
-        if (__any_sync(0xffffffffu, held && !clear)) {
-          const Half z = hold(lo, unit);
-          bool differs = y.scale != z.scale || y.codes != z.codes;
-          differs = __shfl_xor_sync(0xffffffffu, differs, 1) || differs;
-          if (__any_sync(0xffffffffu, held && differs)) {
-            const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(slots[cur.t].pos));
+      }
+      const bool pair = PAIR && cur.rotate;
+      if (KIND < 2 && mine && to) {
+        T* dst = to + at2(n0 + cur.t, o_token, cur.h, o_head) + cur.at;
+        store(dst, a);
+        if (pair) store(dst + half, b);
+      }
+      if constexpr (KIND > 0) {
+        const bool held = mine && (KIND == 1 ? slots[cur.t].k : slots[cur.t].v) >= 0;
+        const Unit4 unit = KIND == 1 ? k_unit : v_unit;
+        const float slack = fabsf(p.factor) * 4.76837158203125e-7f;   // 2^-21
+        float a0[8], b0[8];   // as they were: for the error, and for the exact rotation
+        widen(cur.a, a0);
+        widen(cur.b, b0);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              if (!held || !differs || lo[i] == x[i]) continue;
-              const int k = INTERLEAVED ? cur.at / 2 + i / 2 : cur.at + i;
-              const bool second = INTERLEAVED ? i & 1 : which;
-              x[i] = rounded<T>(rotated_exactly(self(i), partner(i), second ? 1.f : -1.f, p.freq[k] * pos, p.factor));
+        for (int which = 0; which < (PAIR ? 2 : 1); ++which) {
+          if (which && !__any_sync(0xffffffffu, pair)) break;
+          float (&x)[8] = which ? b : a;
+          auto partner = [&](int i) { return INTERLEAVED ? a0[i ^ 1] : which ? a0[i] : b0[i]; };
+          auto self = [&](int i) { return which ? b0[i] : a0[i]; };
+          uint32_t below[4], above[4], apart = 0;   // both ends of each key's error interval, rounded
+          if (KIND == 1) {
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              float e[2];
+#pragma unroll
+              for (int k = 0; k < 2; ++k) e[k] = cur.rotate ? (fabsf(self(i + k)) + fabsf(partner(i + k))) * slack : 0.f;
+              below[i / 2] = pack2(x[i] - e[0], x[i + 1] - e[1], static_cast<T*>(nullptr));
+              above[i / 2] = pack2(x[i] + e[0], x[i + 1] + e[1], static_cast<T*>(nullptr));
+              apart |= below[i / 2] ^ above[i / 2];
+              const float2 r = unpack2(above[i / 2], static_cast<T*>(nullptr));
+              x[i] = r.x;
+              x[i + 1] = r.y;
             }
-            y = hold(x, unit);
+          }
+          Half y = hold(x, unit);
+          if (KIND == 1 && __any_sync(0xffffffffu, held && apart != 0)) {
+            // the smaller and the larger of the two in magnitude: scales rise with the largest magnitude and codes with
+            // the value, so if these two make equal blocks, no key between the ends makes another one
+            float lo[8], hi[8];
+#pragma unroll
+            for (int i = 0; i < 8; i += 2) {
+              const float2 l = unpack2(below[i / 2], static_cast<T*>(nullptr)), h = unpack2(above[i / 2], static_cast<T*>(nullptr));
+              lo[i] = fabsf(h.x) >= fabsf(l.x) ? l.x : h.x;
+              hi[i] = fabsf(h.x) >= fabsf(l.x) ? h.x : l.x;
+              lo[i + 1] = fabsf(h.y) >= fabsf(l.y) ? l.y : h.y;
+              hi[i + 1] = fabsf(h.y) >= fabsf(l.y) ? h.y : l.y;
+            }
+            const Half z0 = hold(lo, unit), z1 = hold(hi, unit);
+            bool differs = z0.scale != z1.scale || z0.codes != z1.codes;
+            differs = __shfl_xor_sync(0xffffffffu, differs, 1) || differs;
+            if (__any_sync(0xffffffffu, held && differs)) {
+              const unsigned long long pos = held ? static_cast<unsigned long long>(static_cast<long long>(slots[cur.t].pos)) : 0ull;
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                if (!held || !differs || lo[i] == hi[i]) continue;
+                const int k = INTERLEAVED ? cur.at / 2 + i / 2 : cur.at + i;
+                const bool second = INTERLEAVED ? i & 1 : which;
+                x[i] = rounded<T>(rotated_exactly(self(i), partner(i), second ? 1.f : -1.f, p.freq[k] * pos, p.factor));
+              }
+              y = hold(x, unit);
+            }
+          }
+          if (held && (!which || pair)) {
+            const int i = cur.at + which * half;
+            uint8_t* codes = KIND == 1 ? p.c.k + slots[cur.t].k + cur.h * p.c.k_head : p.c.v + slots[cur.t].v + cur.h * p.c.v_head;
+            uint8_t* scales = KIND == 1 ? s.k + slots[cur.t].ks + cur.h * s.k_head : s.v + slots[cur.t].vs + cur.h * s.v_head;
+            *reinterpret_cast<uint32_t*>(codes + i / 2) = y.codes;
+            if (i % 16 == 0) scales[i / 16] = static_cast<uint8_t>(y.scale);
           }
         }
-        if (held && (!which || pair)) {
-          const int i = cur.at + which * half;
-          uint8_t* codes = key ? p.c.k + slots[cur.t].k + cur.h * p.c.k_head : p.c.v + slots[cur.t].v + cur.h * p.c.v_head;
-          uint8_t* scales = key ? s.k + slots[cur.t].ks + cur.h * s.k_head : s.v + slots[cur.t].vs + cur.h * s.v_head;
-          *reinterpret_cast<uint32_t*>(codes + i / 2) = y.codes;
-          if (i % 16 == 0) scales[i / 16] = static_cast<uint8_t>(y.scale);
-        }
       }
+      cur = next;
     }
-    cur = next;
-  }
+  };
+  pass(std::integral_constant<int, 2>());
+  pass(std::integral_constant<int, 1>());
+  pass(std::integral_constant<int, 0>());
 }
 
 // Any rotated part, alignment and stride of the new tokens: a warp takes a head of a token, a lane every 32nd value, 16 lanes
 // a block.  The head is read whole before anything of it is written, so it may be rotated in place.
 template <int DTYPE>
 __global__ void __launch_bounds__(kRopeThreads)
-    rope_fp4_scalar_kernel(const RopeParams p, const Fp4Scales s, float k_unit, float v_unit) {
+    rope_fp4_scalar_kernel(const RopeParams p, const Fp4Scales s, const Unit4 k_unit, const Unit4 v_unit) {
   using T = typename RopeType<DTYPE>::T;
   const int n = blockIdx.x, lane = threadIdx.x & 31;
   const Slot slot = slot_of(p, s, n, lane);
@@ -330,14 +362,10 @@ __global__ void __launch_bounds__(kRopeThreads)
       if (!held || i * 32 >= D) continue;     // the same for the whole warp
       const float y = rounded<T>(x[i]);
       float top = fabsf(y);
-      int nan = y != y;
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) {
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        nan |= __shfl_xor_sync(0xffffffffu, nan, o);
-      }
+      for (int o = 1; o < 16; o <<= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
       float inverse;
-      const uint32_t scale = block_scale(top, nan, kind == 1 ? k_unit : v_unit, &inverse);
+      const uint32_t scale = block_scale(top, kind == 1 ? k_unit : v_unit, &inverse);
       const uint32_t two = two_codes(y, __shfl_down_sync(0xffffffffu, y, 1), inverse);
       if (c < D && lane % 2 == 0) codes[c / 2] = static_cast<uint8_t>(two);
       if (c < D && lane % 16 == 0) scales[c / 16] = static_cast<uint8_t>(scale);
@@ -385,18 +413,19 @@ __global__ void __launch_bounds__(256) fp4_values_kernel(const Fp4Values p) {
 
 cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, float k_unit, float v_unit, int sms,
                             cudaStream_t stream) {
+  const Unit4 ku = {k_unit, static_cast<float>(1.0 / (6.0 * k_unit))}, vu = {v_unit, static_cast<float>(1.0 / (6.0 * v_unit))};
   const long long strides[] = {p.q_token, p.q_head, p.k_token, p.k_head, p.v_token, p.v_head, p.qo_token, p.qo_head,
                                p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0};
   bool whole = p.rotary % (p.interleaved ? 16 : 32) == 0;
-  for (long long st : strides) whole = whole && st % 8 == 0;
+  for (long long st : strides) whole = whole && st % 8 == 0 && st >= 0 && st < (1ll << 31);
   const long long pieces = (p.Hq + 2ll * p.c.Hkv) * (p.c.D / 8);   // of a token; the kernel's quotients hold up to 2^16
   whole = whole && pieces < (1 << 16);
   const void* bases[] = {p.q, p.k, p.v, p.q_out, p.k_out};
   for (const void* b : bases) whole = whole && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
   if (!whole) {
     const dim3 grid(p.c.N), block(kRopeThreads);
-    if (dtype == 1) rope_fp4_scalar_kernel<1><<<grid, block, 0, stream>>>(p, s, k_unit, v_unit);
-    if (dtype == 2) rope_fp4_scalar_kernel<2><<<grid, block, 0, stream>>>(p, s, k_unit, v_unit);
+    if (dtype == 1) rope_fp4_scalar_kernel<1><<<grid, block, 0, stream>>>(p, s, ku, vu);
+    if (dtype == 2) rope_fp4_scalar_kernel<2><<<grid, block, 0, stream>>>(p, s, ku, vu);
     return cudaGetLastError();
   }
   // few tokens: a CTA each; many: as many tokens a CTA as make about 2048 pieces (as rope_append.cu)
@@ -405,10 +434,10 @@ cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, 
   const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);
   const size_t smem = sizeof(float2) * (p.rotary / 2) * per;
   const int kind = dtype * 2 + (p.interleaved ? 1 : 0);
-  if (kind == 2) rope_fp4_kernel<1, false><<<grid, block, smem, stream>>>(p, s, k_unit, v_unit, per);
-  if (kind == 3) rope_fp4_kernel<1, true><<<grid, block, smem, stream>>>(p, s, k_unit, v_unit, per);
-  if (kind == 4) rope_fp4_kernel<2, false><<<grid, block, smem, stream>>>(p, s, k_unit, v_unit, per);
-  if (kind == 5) rope_fp4_kernel<2, true><<<grid, block, smem, stream>>>(p, s, k_unit, v_unit, per);
+  if (kind == 2) rope_fp4_kernel<1, false><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  if (kind == 3) rope_fp4_kernel<1, true><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  if (kind == 4) rope_fp4_kernel<2, false><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  if (kind == 5) rope_fp4_kernel<2, true><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
   return cudaGetLastError();
 }
 
