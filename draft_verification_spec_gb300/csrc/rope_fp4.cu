@@ -373,39 +373,52 @@ __global__ void __launch_bounds__(kRopeThreads)
   }
 }
 
-// A thread a block: 8 bytes of codes and a scale -> 16 values.  Bound: HBM, 0.56 bytes read and 2 (or 4) written a value.
+// A warp a token, a lane a block: 8 bytes of codes and a scale -> 16 values, two blocks' loads in flight.  Bound: HBM, 0.56
+// bytes read and 2 (or 4) written a value.
 template <int DTYPE>
 __global__ void __launch_bounds__(256) fp4_values_kernel(const Fp4Values p) {
   using T = typename RopeType<DTYPE>::T;
-  const unsigned blocks = p.dim / 16, row = p.heads * blocks;   // of a head, of a token
-  const long long total = static_cast<long long>(p.pages) * p.page_size * row;
-  for (long long i = blockIdx.x * 256ll + threadIdx.x; i < total; i += gridDim.x * 256ll) {
-    const long long token = i / row;
-    const unsigned in_row = static_cast<unsigned>(i - token * row), h = in_row / blocks, j = in_row - h * blocks;
+  const int blocks = p.dim / 16, row = p.heads * blocks, lane = threadIdx.x & 31;   // of a head, of a token
+  const long long tokens = static_cast<long long>(p.pages) * p.page_size;
+  for (long long token = blockIdx.x * 8ll + threadIdx.x / 32; token < tokens; token += gridDim.x * 8ll) {
     const long long page = token / p.page_size;
     const int in = static_cast<int>(token - page * p.page_size);
-    const uint2 codes = __ldg(reinterpret_cast<const uint2*>(p.codes + page * p.page + in * p.token + h * p.head + j * 8));
-    const uint16_t sc = __ldg(p.scales + page * p.s_page + in * p.s_token + h * p.s_head + j);
-    uint32_t half2;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(sc));
-    const float scale = __low2float(*reinterpret_cast<const __half2*>(&half2)) * p.unit;
-    __align__(16) T out[16];
+    const uint8_t* codes_at = p.codes + page * p.page + in * p.token;
+    const uint8_t* scales_at = p.scales + page * p.s_page + in * p.s_token;
+    T* out_at = static_cast<T*>(p.out) + token * row * 16;
+    for (int r0 = lane; r0 < row; r0 += 64) {
+      uint2 codes[2];
+      uint16_t sc[2];
 #pragma unroll
-    for (int w = 0; w < 2; ++w) {
-      const uint32_t c = w ? codes.y : codes.x;
+      for (int n = 0; n < 2; ++n) {
+        const int r = r0 + n * 32;
+        if (r >= row) continue;
+        const int h = r / blocks, j = r - h * blocks;
+        codes[n] = __ldg(reinterpret_cast<const uint2*>(codes_at + h * p.head + j * 8));
+        sc[n] = __ldg(scales_at + h * p.s_head + j);
+      }
 #pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        const uint16_t two = static_cast<uint16_t>(c >> (8 * b) & 0xffu);
-        uint32_t v;
-        asm("{\n\t.reg .b8 x;\n\tcvt.u8.u16 x, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x;\n\t}" : "=r"(v) : "h"(two));
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
-        from_f(f.x * scale, out + w * 8 + 2 * b);
-        from_f(f.y * scale, out + w * 8 + 2 * b + 1);
+      for (int n = 0; n < 2; ++n) {
+        const int r = r0 + n * 32;
+        if (r >= row) continue;
+        uint32_t half2;
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(half2) : "h"(sc[n]));
+        const float scale = __low2float(*reinterpret_cast<const __half2*>(&half2)) * p.unit;
+        __align__(16) T out[16];
+#pragma unroll
+        for (int b = 0; b < 8; ++b) {
+          const uint16_t two = static_cast<uint16_t>((b < 4 ? codes[n].x : codes[n].y) >> (8 * (b & 3)) & 0xffu);
+          uint32_t v;
+          asm("{\n\t.reg .b8 x;\n\tcvt.u8.u16 x, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, x;\n\t}" : "=r"(v) : "h"(two));
+          const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&v));
+          from_f(f.x * scale, out + 2 * b);
+          from_f(f.y * scale, out + 2 * b + 1);
+        }
+        uint4* dst = reinterpret_cast<uint4*>(out_at + r * 16);
+#pragma unroll
+        for (int k = 0; k < static_cast<int>(sizeof(out) / 16); ++k) dst[k] = reinterpret_cast<const uint4*>(out)[k];
       }
     }
-    uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(p.out) + i * 16);
-#pragma unroll
-    for (int k = 0; k < static_cast<int>(sizeof(out) / 16); ++k) dst[k] = reinterpret_cast<const uint4*>(out)[k];
   }
 }
 
@@ -428,8 +441,9 @@ cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, 
     if (dtype == 2) rope_fp4_scalar_kernel<2><<<grid, block, 0, stream>>>(p, s, ku, vu);
     return cudaGetLastError();
   }
-  // few tokens: a CTA each; many: as many tokens a CTA as make about 2048 pieces (as rope_append.cu)
-  int per = p.c.N <= 4 * sms ? 1 : static_cast<int>(2048 / pieces);
+  // few tokens: a CTA each; many: as many tokens a CTA as make about 4096 pieces.  8192 tokens of 768 pieces: 1024 pieces
+  // 64 us, 2048 48, 4096 46, 6144 53 (too few CTAs for the last wave).
+  int per = p.c.N <= 4 * sms ? 1 : static_cast<int>(4096 / pieces);
   per = per < 1 ? 1 : per > kFp4MaxTokens ? kFp4MaxTokens : per;
   const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);
   const size_t smem = sizeof(float2) * (p.rotary / 2) * per;
@@ -442,9 +456,9 @@ cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, 
 }
 
 cudaError_t launch_fp4_values(int dtype, const Fp4Values& p, int sms, cudaStream_t stream) {
-  const long long total = static_cast<long long>(p.pages) * p.page_size * p.heads * (p.dim / 16);
-  if (total == 0) return cudaSuccess;
-  const long long want = (total + 255) / 256;
+  const long long tokens = static_cast<long long>(p.pages) * p.page_size;
+  if (tokens == 0) return cudaSuccess;
+  const long long want = (tokens + 7) / 8;
   const dim3 grid(static_cast<unsigned>(want < 16ll * sms ? want : 16ll * sms)), block(256);
   if (dtype == 0) fp4_values_kernel<0><<<grid, block, 0, stream>>>(p);
   if (dtype == 1) fp4_values_kernel<1><<<grid, block, 0, stream>>>(p);
