@@ -24,7 +24,7 @@ namespace {
 
 constexpr int kPlanThreads = 1024, kCopyThreads = 256;
 constexpr int kCopyBytes = kCopyThreads * 16 * 4;   // bytes of a page that a CTA copies at a time
-constexpr int kCols = 128;                      // columns of a row that a warp takes at a time
+constexpr int kCols = 128;                      // columns of a row that a warp has in flight
 
 __device__ __forceinline__ int block_sum(int v, int* s) {
   v = warp_sum_int(v);
@@ -78,6 +78,18 @@ __device__ __forceinline__ Row row_of(const PageParams& p, int b) {
   r.part = k % p.page_size > 0;
   return r;
 }
+// Items of the table, a warp each: `cols` columns of a row, as many as give every warp one (and 512 at most).
+struct Items {
+  int cols, chunks, n;
+};
+__device__ __forceinline__ Items items_of(const PageParams& p, int warps) {
+  Items it;
+  const long long per = (static_cast<long long>(p.rows) * p.width + warps - 1) / warps;
+  it.cols = static_cast<int>(min(max((per + kCols - 1) / kCols * kCols, static_cast<long long>(kCols)), 512ll));
+  it.chunks = (p.width + it.cols - 1) / it.cols;
+  it.n = p.rows * it.chunks;
+  return it;
+}
 __device__ __forceinline__ int entry(const PageParams& p, int b, int j) { return __ldg(p.table + b * p.stride + j); }
 __device__ __forceinline__ bool valid(const PageParams& p, int pg) { return pg >= 0 && pg < p.pages; }
 
@@ -97,26 +109,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1) assign_pages_kernel(const Pag
   asm volatile("griddepcontrol.launch_dependents;");
   const int rank = cluster_rank(), n = cluster_ncta(), tid = threadIdx.x, lane = tid & 31;
   const int warp = rank * (kPlanThreads / 32) + tid / 32, warps = n * (kPlanThreads / 32);
-  const int chunks = (p.width + kCols - 1) / kCols, items = p.rows * chunks;
+  const Items items = items_of(p, warps);
   int first, last;
   share_of(p, rank, n, &first, &last);
 
   clear_marks(p, rank, n, INT_MAX);
   cluster_sync();
   // marks: -1 for a page that some row only reads, else the lowest row that will write to it
-  for (int it = warp; it < items; it += warps) {
-    const int b = it / chunks, j0 = (it - b * chunks) * kCols;
+  for (int it = warp; it < items.n; it += warps) {
+    const int b = it / items.chunks, first_col = (it - b * items.chunks) * items.cols;
     const Row r = row_of(p, b);
-    const int inherited = min(r.full + r.part, p.width);
+    const int end = min(min(r.full + r.part, p.width), first_col + items.cols);
+    for (int j0 = first_col; j0 < end; j0 += kCols) {
+      int pg[kCols / 32];
 #pragma unroll
-    for (int i = 0; i < kCols; i += 32) {
-      const int j = j0 + i + lane;
-      if (j >= inherited) continue;
-      const int pg = entry(p, r.parent, j);
-      if (valid(p, pg))
-        atomicMin(p.mark + pg, j < r.full ? -1 : b);
-      else
-        atomicOr(p.status, kStatusPageRange);
+      for (int i = 0; i < kCols / 32; ++i) {
+        const int j = j0 + i * 32 + lane;
+        pg[i] = j < end ? entry(p, r.parent, j) : -1;
+      }
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) {
+        const int j = j0 + i * 32 + lane;
+        if (j >= end) continue;
+        if (valid(p, pg[i]))
+          atomicMin(p.mark + pg[i], j < r.full ? -1 : b);
+        else
+          atomicOr(p.status, kStatusPageRange);
+      }
     }
   }
   cluster_sync();
@@ -129,25 +148,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1) assign_pages_kernel(const Pag
     int base = 0;
     for (int b0 = 0; b0 < p.rows; b0 += kPlanThreads) {
       const int b = b0 + tid;
-      int fresh = 0;
+      int fresh = 0, keep = 0, from = -1;   // fresh pages, columns that stay, the page that is copied
+      Row r = {0, 0, 0, 0};
       if (b < p.rows) {
-        const Row r = row_of(p, b);
-        fresh = r.need - r.full - r.part;
+        r = row_of(p, b);
+        keep = r.full;
         if (r.part) {
           const int pg = entry(p, r.parent, r.full);
-          if (valid(p, pg) && __ldcg(p.mark + pg) != b) ++fresh;
+          if (!valid(p, pg) || __ldcg(p.mark + pg) == b)
+            ++keep;
+          else
+            from = pg;
         }
+        fresh = r.need - keep;
       }
       int all;
       const int before = block_before(fresh, s_sum, &all);
-      if (b < p.rows) __stcg(p.starts + b, base + before);
+      if (b < p.rows) {
+        __stcg(p.plan + b, make_int4(r.parent, keep, r.need, base + before));
+        __stcg(p.src + b, from);
+      }
       base += all;
     }
-    if (tid == 0) __stcg(p.starts + p.rows, base);
+    if (tid == 0) __stcg(p.wanted, base);
   }
   cluster_sync();
   // the free pages in rising order, as many as are wanted
-  const int wanted = __ldcg(p.starts + p.rows);
+  const int wanted = __ldcg(p.wanted);
   int base = 0, there = 0;
   for (int c = 0; c < n; ++c) {
     const int k = __ldcg(p.counts + c);
@@ -164,35 +191,33 @@ __global__ void __launch_bounds__(kPlanThreads, 1) assign_pages_kernel(const Pag
   }
   cluster_sync();
   // the new table and the copies
-  for (int it = warp; it < items; it += warps) {
-    const int b = it / chunks, j0 = (it - b * chunks) * kCols;
-    const Row r = row_of(p, b);
-    int fresh = __ldcg(p.starts + b) - r.full;   // + column: the place of a fresh page in the list
-    bool own = false;                            // the page that ends inside stays this row's
-    int pg = -1;
-    if (r.part) {
-      pg = entry(p, r.parent, r.full);
-      own = !valid(p, pg) || __ldcg(p.mark + pg) == b;
-      if (own) --fresh;
-    }
-    auto fresh_page = [&](int j) { return fresh + j < there ? __ldcg(p.list + fresh + j) : -1; };
+  for (int it = warp; it < items.n; it += warps) {
+    const int b = it / items.chunks, first_col = (it - b * items.chunks) * items.cols;
+    const int4 r = __ldcg(p.plan + b);   // parent, columns that stay, columns, place of the first fresh page
+    const int from = first_col == 0 && lane == 0 ? __ldcg(p.src + b) : -1;
+    auto fresh_page = [&](int j) { return r.w + j - r.y < there ? __ldcg(p.list + r.w + j - r.y) : -1; };
+    const int end = min(p.width, first_col + items.cols);
+    for (int j0 = first_col; j0 < end; j0 += kCols) {
+      int to[kCols / 32];
 #pragma unroll
-    for (int i = 0; i < kCols; i += 32) {
-      const int j = j0 + i + lane;
-      if (j >= p.width) continue;
-      int to = -1;
-      if (j < r.full || (own && j == r.full)) {
-        to = entry(p, r.parent, j);
-        if (!valid(p, to)) to = -1;
-      } else if (j < r.need) {
-        to = fresh_page(j);
+      for (int i = 0; i < kCols / 32; ++i) {
+        const int j = j0 + i * 32 + lane;
+        to[i] = -1;
+        if (j < end && j < r.y)
+          to[i] = entry(p, r.x, j);
+        else if (j < end && j < r.z)
+          to[i] = fresh_page(j);
       }
-      p.out[b * p.out_stride + j] = to;
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) {
+        const int j = j0 + i * 32 + lane;
+        if (j < end) p.out[b * p.out_stride + j] = valid(p, to[i]) ? to[i] : -1;
+      }
     }
-    if (j0 == 0 && lane == 0) {
-      const int dst = r.part && !own ? fresh_page(r.full) : -1;
-      __stcg(p.src + b, dst >= 0 ? pg : -1);
+    if (from >= 0) {   // the first fresh page is its copy
+      const int dst = fresh_page(r.y);
       __stcg(p.dst + b, dst);
+      if (dst < 0) __stcg(p.src + b, -1);
     }
   }
   if (rank == 0 && tid == 0) __stcg(p.moves, p.rows);
@@ -203,23 +228,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_pages_kernel(const Pa
   asm volatile("griddepcontrol.launch_dependents;");
   const int rank = cluster_rank(), n = cluster_ncta(), tid = threadIdx.x, lane = tid & 31;
   const int warp = rank * (kPlanThreads / 32) + tid / 32, warps = n * (kPlanThreads / 32);
-  const int chunks = (p.width + kCols - 1) / kCols, items = p.rows * chunks;
+  const Items items = items_of(p, warps);
   int first, last;
   share_of(p, rank, n, &first, &last);
 
   clear_marks(p, rank, n, 0);
   cluster_sync();
-  for (int it = warp; it < items; it += warps) {
-    const int b = it / chunks, j0 = (it - b * chunks) * kCols;
+  for (int it = warp; it < items.n; it += warps) {
+    const int b = it / items.chunks, first_col = (it - b * items.chunks) * items.cols;
+    const int end = min(p.width, first_col + items.cols);
+    for (int j0 = first_col; j0 < end; j0 += kCols) {
+      int pg[kCols / 32];
 #pragma unroll
-    for (int i = 0; i < kCols; i += 32) {
-      const int j = j0 + i + lane;
-      if (j >= p.width) continue;
-      const int pg = entry(p, b, j);
-      if (valid(p, pg))
-        __stcg(p.mark + pg, 1);
-      else if (pg != -1)
-        atomicOr(p.status, kStatusPageRange);
+      for (int i = 0; i < kCols / 32; ++i) pg[i] = j0 + i * 32 + lane < end ? entry(p, b, j0 + i * 32 + lane) : -1;
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) {
+        if (valid(p, pg[i]))
+          __stcg(p.mark + pg[i], 1);
+        else if (pg[i] != -1)
+          atomicOr(p.status, kStatusPageRange);
+      }
     }
   }
   cluster_sync();
@@ -262,20 +290,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) compact_pages_kernel(const Pa
     *p.used = used;
   }
   cluster_sync();
-  for (int it = warp; it < items; it += warps) {
-    const int b = it / chunks, j0 = (it - b * chunks) * kCols;
+  for (int it = warp; it < items.n; it += warps) {
+    const int b = it / items.chunks, first_col = (it - b * items.chunks) * items.cols;
+    const int end = min(p.width, first_col + items.cols);
+    for (int j0 = first_col; j0 < end; j0 += kCols) {
+      int pg[kCols / 32], to[kCols / 32];
 #pragma unroll
-    for (int i = 0; i < kCols; i += 32) {
-      const int j = j0 + i + lane;
-      if (j >= p.width) continue;
-      int pg = entry(p, b, j);
-      if (valid(p, pg)) {
-        const int m = __ldcg(p.mark + pg);
-        if (m < 0) pg = -1 - m;
-      } else {
-        pg = -1;
+      for (int i = 0; i < kCols / 32; ++i) pg[i] = j0 + i * 32 + lane < end ? entry(p, b, j0 + i * 32 + lane) : -1;
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) to[i] = valid(p, pg[i]) ? __ldcg(p.mark + pg[i]) : 0;
+#pragma unroll
+      for (int i = 0; i < kCols / 32; ++i) {
+        const int j = j0 + i * 32 + lane;
+        if (j < end) p.out[b * p.out_stride + j] = !valid(p, pg[i]) ? -1 : to[i] < 0 ? -1 - to[i] : pg[i];
       }
-      p.out[b * p.out_stride + j] = pg;
     }
   }
 }

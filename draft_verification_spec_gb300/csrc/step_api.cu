@@ -290,7 +290,7 @@ spec_status_t run_rope(const spec_rope_tensors_t* t, int dtype, int q_heads, con
 // Workspace of the page operators: ints behind the status.
 size_t pages_ints(int pages, int rows) {
   const size_t copies = static_cast<size_t>(rows > pages / 2 ? rows : pages / 2);
-  return 16 + static_cast<size_t>(rows) + 1 + 2 * copies + 2 * static_cast<size_t>(pages);
+  return 16 + 4 * static_cast<size_t>(rows) + 2 * copies + 2 * static_cast<size_t>(pages);
 }
 
 spec_status_t run_pages(bool compact, const spec_page_pool_t* pool, int page_size, const int32_t* table, long long stride,
@@ -327,8 +327,9 @@ spec_status_t run_pages(bool compact, const spec_page_pool_t* pool, int page_siz
   const int copies = rows > p.pages / 2 ? rows : p.pages / 2;
   p.counts = ws;
   p.moves = ws + 8;
-  p.starts = ws + 16;
-  p.src = p.starts + rows + 1;
+  p.wanted = ws + 9;
+  p.plan = reinterpret_cast<int4*>(ws + 16);
+  p.src = ws + 16 + 4 * static_cast<size_t>(rows);
   p.dst = p.src + copies;
   p.list = p.dst + copies;
   p.mark = p.list + p.pages;

@@ -135,7 +135,8 @@ struct PageParams {
   // workspace
   int* counts;               // [8] a CTA's share of a count
   int* moves;                // [1]
-  int* starts;               // [rows + 1] fresh pages of the rows before
+  int* wanted;               // [1] fresh pages in all
+  int4* plan;                // [rows] parent, columns that stay, columns, fresh pages of the rows before
   int *src, *dst;            // [max(rows, pages / 2)] copies (src -1: none)
   int* list;                 // [pages] free pages
   int* mark;                 // [pages]
