@@ -106,6 +106,7 @@ __device__ __forceinline__ void clear_marks(const PageParams& p, int rank, int n
 
 __global__ void __launch_bounds__(kPlanThreads, 1) assign_pages_kernel(const PageParams p) {
   __shared__ int s_sum[kPlanThreads / 32];
+  __shared__ Row s_rows[kPlanThreads];   // the first rows, looked up once
   asm volatile("griddepcontrol.launch_dependents;");
   const int rank = cluster_rank(), n = cluster_ncta(), tid = threadIdx.x, lane = tid & 31;
   const int warp = rank * (kPlanThreads / 32) + tid / 32, warps = n * (kPlanThreads / 32);
@@ -113,12 +114,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) assign_pages_kernel(const Pag
   int first, last;
   share_of(p, rank, n, &first, &last);
 
+  if (tid < p.rows) s_rows[tid] = row_of(p, tid);
   clear_marks(p, rank, n, INT_MAX);
+  __syncthreads();
+  auto row = [&](int b) { return b < kPlanThreads ? s_rows[b] : row_of(p, b); };
   cluster_sync();
   // marks: -1 for a page that some row only reads, else the lowest row that will write to it
   for (int it = warp; it < items.n; it += warps) {
     const int b = it / items.chunks, first_col = (it - b * items.chunks) * items.cols;
-    const Row r = row_of(p, b);
+    const Row r = row(b);
     const int end = min(min(r.full + r.part, p.width), first_col + items.cols);
     for (int j0 = first_col; j0 < end; j0 += kCols) {
       int pg[kCols / 32];
@@ -151,7 +155,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) assign_pages_kernel(const Pag
       int fresh = 0, keep = 0, from = -1;   // fresh pages, columns that stay, the page that is copied
       Row r = {0, 0, 0, 0};
       if (b < p.rows) {
-        r = row_of(p, b);
+        r = row(b);
         keep = r.full;
         if (r.part) {
           const int pg = entry(p, r.parent, r.full);
