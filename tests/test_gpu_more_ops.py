@@ -216,6 +216,69 @@ def test_fp4_units_and_scales(sv, nq):
     _fp4(sv, [nq, nq], [77, 260], 16, 8, 4, 64, grow=30.0, seed=5)      # scores whose maximum keeps moving
 
 
+@pytest.mark.parametrize("nq", [1, 4, 40])
+def test_fp4_strides_of_all_kinds(sv, nq):
+    """Keys and values, codes and scales laid out apart, heads that are every second one of a wider cache, rows of scales at odd
+    places: the same rows as from caches of the usual layout, to rounding."""
+    new, kv, page, hkv, d = [nq, nq], [300, 77], 16, 2, 128
+    (kc, vc), (ke, ve), table, lens, cu = _fp4_batch(sv, new, kv, page, hkv, d, 21)
+    q = torch.randn(2 * nq, 8, d, generator=torch.Generator().manual_seed(2)).bfloat16().cuda()
+    ref = M.attention(q, ke, ve, table, lens, cu, True, 0, 0, d ** -0.5)
+    byte = lambda c: c.scales.view(torch.uint8)  # noqa: E731
+    nhd = lambda c: sv.FP4Cache.of(c.codes.contiguous(), byte(c).contiguous().view(torch.float8_e4m3fn))  # noqa: E731
+
+    def wide(c):
+        codes = torch.full((*c.shape[:2], 2 * hkv, d // 2), 0x77, dtype=torch.uint8, device="cuda")
+        scales = torch.full((*c.shape[:2], 2 * hkv, d // 16), 127, dtype=torch.uint8, device="cuda")
+        codes[:, :, ::2], scales[:, :, ::2] = c.codes, byte(c)
+        return sv.FP4Cache.of(codes[:, :, ::2], scales.view(torch.float8_e4m3fn)[:, :, ::2])
+
+    def odd(c):
+        scales = torch.full((*c.shape[:2], hkv, d // 16 + 3), 127, dtype=torch.uint8, device="cuda")
+        scales[..., 1:1 + d // 16] = byte(c)
+        return sv.FP4Cache.of(c.codes, scales.view(torch.float8_e4m3fn)[..., 1:1 + d // 16])
+
+    x = torch.randn(2 * nq, 4, d, generator=torch.Generator().manual_seed(4)).bfloat16().cuda()
+    mine = [sv.FP4Cache.of(c.codes.clone(), c.scales.clone()) for c in (kc, vc)]
+    sv.rope_append(q, x[:, :2], x[:, 2:], sv.RopePlan(d), *mine, table, lens, cu)
+    for form in ((nhd, nhd), (nhd, None), (None, nhd), (wide, wide), (wide, None), (odd, odd), (None, odd)):
+        k, v = (f(c) if f else sv.FP4Cache.of(c.codes.clone(), c.scales.clone()) for f, c in zip(form, (kc, vc)))
+        got, lse = sv.chunk_attention(q, k, v, table, lens, cu, nq, want_lse=True)
+        assert sv.default_workspace().status() == 0
+        _check(got, lse, ref, torch.bfloat16, max(kv), d, 4)
+        if odd not in form:
+            sv.rope_append(q, x[:, :2], x[:, 2:], sv.RopePlan(d), k, v, table, lens, cu)
+            for a, b in zip(mine, (k, v)):
+                assert torch.equal(a.codes, b.codes) and torch.equal(byte(a), byte(b))
+
+
+def test_fp4_scale_of_zero(sv):
+    """Every key that is seen counts the same."""
+    for nq in (1, 40):
+        _fp4(sv, [nq, nq], [77, 260], 16, 8, 4, 64, scale=0.0, seed=4)
+
+
+@pytest.mark.parametrize("d,nq,hq", [(64, 17, 4), (128, 40, 16), (80, 40, 4), (128, 4, 8)])
+def test_fp4_wait_that_runs_out_writes_nothing(sv, d, nq, hq):
+    """Every bounded wait gives up at once: the status says so, no row is written; the next call is right."""
+    ws = sv.Workspace()
+    (bk, bv), _, *big = _fp4_batch(sv, [4 * nq] * 6, [3000] * 6, 16, 2, d, 3)
+    big_q = torch.randn(24 * nq, hq, d).bfloat16().cuda()
+    (kc, vc), _, table, lens, cu = _fp4_batch(sv, [nq], [700], 16, 2, d, 4)
+    q = torch.randn(nq, hq, d).bfloat16().cuda()
+    want = sv.chunk_attention(q, kc, vc, table, lens, cu, nq, workspace=ws)
+    sv.chunk_attention(big_q, bk, bv, *big, 4 * nq, workspace=ws)       # splits items: leaves records
+    assert ws.status() == 0
+    out = torch.ones_like(want)
+    got = sv.chunk_attention(q, kc, vc, table, lens, cu, nq, out=out, workspace=ws, tuning=sv.Tuning(wait_limit_us=-1))
+    waits = nq * hq // 2 > 16                                           # the kernel for few rows waits for nothing
+    assert ws.status() == (4 if waits else 0)
+    assert torch.equal(got, torch.ones_like(got) if waits else want)
+    for tuning in (None, sv.Tuning(wait_limit_us=10 ** 6)):
+        sv.chunk_attention(q, kc, vc, table, lens, cu, nq, out=out, workspace=ws, tuning=tuning)
+        assert ws.status() == 0 and torch.equal(out, want)
+
+
 def test_fp4_all_numbers(sv):
     """Every e4m3 scale with every code: the values that the kernel multiplies are exact."""
     d, page = 128, 16
