@@ -126,12 +126,14 @@ __device__ __forceinline__ Slot slot_of(const RopeParams& p, const Fp4Scales& s,
   return r;
 }
 
-// The form for whole blocks: the rotated part is whole blocks (half layout: each half is), rows are 16-byte aligned.
+// The form for whole pieces: the rotated part is whole 16-byte pieces (half layout: each half is), rows are 16-byte aligned.
 // A CTA takes `per_cta` tokens: a warp each looks up the slot, the CTA computes the angles once for all heads.  Then each
 // thread moves 16-byte pieces of 8 values (a piece and its partner where they turn together), the next one's loads
 // issued before the current one's work; two lanes hold a block.  (A thread a block reads and writes every second 16 bytes
 // at a time: 80 us for 8192 tokens of 40 + 8 heads of 128.)
-template <int DTYPE, bool INTERLEAVED>
+// SINGLE: where a block has values of both halves (heads of 80), a thread takes one piece and reads its partner beside it, so
+// nothing may be rotated in place.
+template <int DTYPE, bool INTERLEAVED, bool SINGLE>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_fp4_kernel(const RopeParams p, const Fp4Scales s, const Unit4 k_unit, const Unit4 v_unit, int per_cta) {
   using T = typename RopeType<DTYPE>::T;
@@ -177,8 +179,8 @@ __global__ void __launch_bounds__(kRopeThreads)
   // the pieces of all queries, of all keys, of all values
   auto pass = [&](auto what) {
     constexpr int KIND = decltype(what)::value;   // 0: queries, 1: keys, 2: values
-    constexpr bool PAIR = KIND < 2 && !INTERLEAVED;
-    const int heads = KIND == 0 ? p.Hq : Hk, per_head = KIND == 2 ? D / 8 : turn + (D - p.rotary) / 8;
+    constexpr bool PAIR = KIND < 2 && !INTERLEAVED && !SINGLE;
+    const int heads = KIND == 0 ? p.Hq : Hk, per_head = KIND == 2 || SINGLE ? D / 8 : turn + (D - p.rotary) / 8;
     const int units = heads * per_head, total = tokens * units;
     const unsigned inv_units = inverse(units), inv_head = inverse(per_head);
     const T* from = reinterpret_cast<const T*>(KIND == 0 ? p.q : KIND == 1 ? p.k : p.v);
@@ -201,11 +203,12 @@ __global__ void __launch_bounds__(kRopeThreads)
       const int r = u - x.t * units;
       x.h = quotient(r, inv_head);
       const int j = r - x.h * per_head;
-      x.rotate = KIND < 2 && j < turn;
-      x.at = KIND == 2 || x.rotate ? j * 8 : p.rotary + (j - turn) * 8;
+      x.rotate = KIND < 2 && (SINGLE ? j * 8 < p.rotary : j < turn);
+      x.at = KIND == 2 || SINGLE || x.rotate ? j * 8 : p.rotary + (j - turn) * 8;
       const T* src = from + at2(n0 + x.t, s_token, x.h, s_head) + x.at;
       x.a = __ldg(reinterpret_cast<const uint4*>(src));
       if (PAIR && x.rotate) x.b = __ldg(reinterpret_cast<const uint4*>(src + half));
+      if (SINGLE && x.rotate) x.b = __ldg(reinterpret_cast<const uint4*>(x.at < half ? src + half : src - half));
     };
     Unit cur;
     load(tid, cur);
@@ -215,9 +218,10 @@ __global__ void __launch_bounds__(kRopeThreads)
       const bool mine = cur.t >= 0 && slots[cur.t].has;
       float a[8], b[8];
       widen(cur.a, a);
-      if (PAIR) widen(cur.b, b);
+      if (PAIR || SINGLE) widen(cur.b, b);
+      const bool behind = SINGLE && cur.at >= half;   // in the second half
       if (KIND < 2 && mine && cur.rotate) {
-        const float4* cs = reinterpret_cast<const float4*>(s_cs + cur.t * half) + cur.at / 8;
+        const float4* cs = reinterpret_cast<const float4*>(s_cs + cur.t * half) + (behind ? cur.at - half : cur.at) / 8;
 #pragma unroll
         for (int i = 0; i < PP; i += 2) {
           const float4 w = cs[(i >> 1) * turn];   // cos, sin of pairs i and i + 1
@@ -226,9 +230,9 @@ __global__ void __launch_bounds__(kRopeThreads)
             const float c = e ? w.z : w.x, sn = e ? w.w : w.y;
             float& x = INTERLEAVED ? a[2 * (i + e)] : a[i + e];
             float& y = INTERLEAVED ? a[2 * (i + e) + 1] : b[i + e];
-            const float x1 = x * c - y * sn, y1 = y * c + x * sn;
+            const float x1 = behind ? x * c + y * sn : x * c - y * sn, y1 = y * c + x * sn;
             x = x1;
-            y = y1;
+            if (!SINGLE) y = y1;
           }
         }
       }
@@ -287,8 +291,8 @@ __global__ void __launch_bounds__(kRopeThreads)
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
                 if (!held || !differs || lo[i] == hi[i]) continue;
-                const int k = INTERLEAVED ? cur.at / 2 + i / 2 : cur.at + i;
-                const bool second = INTERLEAVED ? i & 1 : which;
+                const int k = INTERLEAVED ? cur.at / 2 + i / 2 : (behind ? cur.at - half : cur.at) + i;
+                const bool second = INTERLEAVED ? i & 1 : which || behind;
                 x[i] = rounded<T>(rotated_exactly(self(i), partner(i), second ? 1.f : -1.f, p.freq[k] * pos, p.factor));
               }
               y = hold(x, unit);
@@ -317,37 +321,40 @@ template <int DTYPE>
 __global__ void __launch_bounds__(kRopeThreads)
     rope_fp4_scalar_kernel(const RopeParams p, const Fp4Scales s, const Unit4 k_unit, const Unit4 v_unit) {
   using T = typename RopeType<DTYPE>::T;
+  extern __shared__ float2 s_angles[];   // [rotary / 2]
   const int n = blockIdx.x, lane = threadIdx.x & 31;
   const Slot slot = slot_of(p, s, n, lane);
-  if (!slot.has) return;
+  if (!slot.has) return;   // the same for the whole block
   const int half = p.rotary / 2, D = p.c.D;
   const unsigned long long pos = static_cast<unsigned long long>(static_cast<long long>(slot.pos));
+  for (int j = threadIdx.x; j < half; j += kRopeThreads) {
+    const float2 w = phase_cs(p.freq[j] * pos);
+    s_angles[j] = make_float2(w.x * p.factor, w.y * p.factor);
+  }
+  __syncthreads();
   for (int h = threadIdx.x / 32; h < p.Hq + 2 * p.c.Hkv; h += kRopeThreads / 32) {
     const int kind = h < p.Hq ? 0 : h < p.Hq + p.c.Hkv ? 1 : 2;   // query, key, value
     const int hk = kind == 0 ? h : kind == 1 ? h - p.Hq : h - p.Hq - p.c.Hkv;
     const T* src = kind == 0   ? reinterpret_cast<const T*>(p.q) + n * p.q_token + hk * p.q_head
                    : kind == 1 ? reinterpret_cast<const T*>(p.k) + n * p.k_token + hk * p.k_head
                                : reinterpret_cast<const T*>(p.v) + n * p.v_token + hk * p.v_head;
-    float x[8];     // what is held, or the rotated query
-    float plain[8];   // the rotated key as rope_append rounds it
+    float x[8], self[8], partner[8];   // rotated; as they were
+    auto rotated = [&](int c) { return kind < 2 && c < p.rotary; };
+    auto pair = [&](int c) { return p.interleaved ? c / 2 : c % half; };
+    auto second = [&](int c) { return p.interleaved ? (c & 1) != 0 : c >= half; };
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = i * 32 + lane, with = !rotated(c) ? c : p.interleaved ? c ^ 1 : second(c) ? c - half : c + half;
+      self[i] = c < D ? to_f(src[c]) : 0.f;
+      partner[i] = c < D ? to_f(src[with]) : 0.f;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = i * 32 + lane;
-      x[i] = plain[i] = 0.f;
-      if (c >= D) continue;
-      x[i] = plain[i] = to_f(src[c]);
-      if (kind == 2 || c >= p.rotary) continue;
-      const int k = p.interleaved ? c / 2 : c % half;
-      const bool second = p.interleaved ? c & 1 : c >= half;
-      const float y = to_f(src[p.interleaved ? c ^ 1 : second ? c - half : c + half]);
-      const unsigned long long phase = p.freq[k] * pos;
-      const float2 w = phase_cs(phase);
-      const float cs = w.x * p.factor, sn = w.y * p.factor, self = x[i];
-      x[i] = plain[i] = second ? self * cs + y * sn : self * cs - y * sn;
-      if (kind == 1) {
-        const float e = (fabsf(self) + fabsf(y)) * fabsf(p.factor) * 4.76837158203125e-7f;   // 2^-21
-        if (rounded<T>(x[i] - e) != rounded<T>(x[i] + e)) x[i] = rotated_exactly(self, y, second ? 1.f : -1.f, phase, p.factor);
-      }
+      x[i] = self[i];
+      if (!rotated(c)) continue;
+      const float2 w = s_angles[pair(c)];
+      x[i] = second(c) ? self[i] * w.x + partner[i] * w.y : self[i] * w.x - partner[i] * w.y;
     }
     __syncwarp();
     T* dst = kind == 0 ? reinterpret_cast<T*>(p.q_out) + n * p.qo_token + hk * p.qo_head
@@ -358,14 +365,33 @@ __global__ void __launch_bounds__(kRopeThreads)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int c = i * 32 + lane;
-      if (dst && c < D) from_f(plain[i], dst + c);
+      if (dst && c < D) from_f(x[i], dst + c);
       if (!held || i * 32 >= D) continue;     // the same for the whole warp
-      const float y = rounded<T>(x[i]);
-      float top = fabsf(y);
-#pragma unroll
-      for (int o = 1; o < 16; o <<= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const Unit4& unit = kind == 1 ? k_unit : v_unit;
       float inverse;
-      const uint32_t scale = block_scale(top, kind == 1 ? k_unit : v_unit, &inverse);
+      auto scale_of = [&](float v) {          // of the 16 lanes' block
+        float top = fabsf(v);
+#pragma unroll
+        for (int o = 1; o < 16; o <<= 1) top = larger(top, __shfl_xor_sync(0xffffffffu, top, o));
+        return block_scale(top, unit, &inverse);
+      };
+      float y = rounded<T>(x[i]);
+      if (kind == 1) {   // both ends of the error interval, as in the other form
+        const float e = rotated(c) ? (fabsf(self[i]) + fabsf(partner[i])) * fabsf(p.factor) * 4.76837158203125e-7f : 0.f;   // 2^-21
+        const float below = rounded<T>(x[i] - e), above = rounded<T>(x[i] + e);
+        if (__any_sync(0xffffffffu, below != above)) {
+          const bool up = fabsf(above) >= fabsf(below);
+          const float large = up ? above : below, small = up ? below : above;
+          const uint32_t s0 = scale_of(small), c0 = two_codes(small, 0.f, inverse);
+          const uint32_t s1 = scale_of(large), c1 = two_codes(large, 0.f, inverse);
+          int differs = s0 != s1 || c0 != c1;
+#pragma unroll
+          for (int o = 1; o < 16; o <<= 1) differs |= __shfl_xor_sync(0xffffffffu, differs, o);
+          if (differs && below != above)
+            y = rounded<T>(rotated_exactly(self[i], partner[i], second(c) ? 1.f : -1.f, p.freq[pair(c)] * pos, p.factor));
+        }
+      }
+      const uint32_t scale = scale_of(y);
       const uint32_t two = two_codes(y, __shfl_down_sync(0xffffffffu, y, 1), inverse);
       if (c < D && lane % 2 == 0) codes[c / 2] = static_cast<uint8_t>(two);
       if (c < D && lane % 16 == 0) scales[c / 16] = static_cast<uint8_t>(scale);
@@ -429,7 +455,9 @@ cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, 
   const Unit4 ku = {k_unit, static_cast<float>(1.0 / (6.0 * k_unit))}, vu = {v_unit, static_cast<float>(1.0 / (6.0 * v_unit))};
   const long long strides[] = {p.q_token, p.q_head, p.k_token, p.k_head, p.v_token, p.v_head, p.qo_token, p.qo_head,
                                p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0};
-  bool whole = p.rotary % (p.interleaved ? 16 : 32) == 0;
+  bool whole = p.rotary % (p.interleaved ? 8 : 16) == 0;
+  const bool single = !p.interleaved && p.rotary % 32 != 0;
+  if (single && (p.q_out == p.q || p.k_out == p.k)) whole = false;
   for (long long st : strides) whole = whole && st % 8 == 0 && st >= 0 && st < (1ll << 31);
   const long long pieces = (p.Hq + 2ll * p.c.Hkv) * (p.c.D / 8);   // of a token; the kernel's quotients hold up to 2^16
   whole = whole && pieces < (1 << 16);
@@ -437,8 +465,9 @@ cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, 
   for (const void* b : bases) whole = whole && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
   if (!whole) {
     const dim3 grid(p.c.N), block(kRopeThreads);
-    if (dtype == 1) rope_fp4_scalar_kernel<1><<<grid, block, 0, stream>>>(p, s, ku, vu);
-    if (dtype == 2) rope_fp4_scalar_kernel<2><<<grid, block, 0, stream>>>(p, s, ku, vu);
+    const size_t smem = sizeof(float2) * (p.rotary / 2);
+    if (dtype == 1) rope_fp4_scalar_kernel<1><<<grid, block, smem, stream>>>(p, s, ku, vu);
+    if (dtype == 2) rope_fp4_scalar_kernel<2><<<grid, block, smem, stream>>>(p, s, ku, vu);
     return cudaGetLastError();
   }
   // few tokens: a CTA each; many: as many tokens a CTA as make about 4096 pieces.  8192 tokens of 768 pieces: 1024 pieces
@@ -447,11 +476,13 @@ cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, 
   per = per < 1 ? 1 : per > kFp4MaxTokens ? kFp4MaxTokens : per;
   const dim3 grid((p.c.N + per - 1) / per), block(kRopeThreads);
   const size_t smem = sizeof(float2) * (p.rotary / 2) * per;
-  const int kind = dtype * 2 + (p.interleaved ? 1 : 0);
-  if (kind == 2) rope_fp4_kernel<1, false><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
-  if (kind == 3) rope_fp4_kernel<1, true><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
-  if (kind == 4) rope_fp4_kernel<2, false><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
-  if (kind == 5) rope_fp4_kernel<2, true><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  const int kind = dtype * 4 + (p.interleaved ? 1 : single ? 2 : 0);
+  if (kind == 4) rope_fp4_kernel<1, false, false><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  if (kind == 5) rope_fp4_kernel<1, true, false><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  if (kind == 6) rope_fp4_kernel<1, false, true><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  if (kind == 8) rope_fp4_kernel<2, false, false><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  if (kind == 9) rope_fp4_kernel<2, true, false><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
+  if (kind == 10) rope_fp4_kernel<2, false, true><<<grid, block, smem, stream>>>(p, s, ku, vu, per);
   return cudaGetLastError();
 }
 

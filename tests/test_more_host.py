@@ -164,13 +164,13 @@ print(fp4(40, s=scales(v_token=72))[0], fp4(40, c=codes(tokens=40, k_page=1 << 3
 
 def rope(**kw):
     fake.fake_clear()
-    v = dict(q=4096, r=128, dim=128)
+    v = dict(q=4096, r=128, dim=128, out=8192)
     v.update(kw)
-    t = struct.pack("@PPPPPqqqqqqqqqq", v["q"], 4096, 4096, 4096, 0, *([1024, 128] * 5))
+    t = struct.pack("@PPPPPqqqqqqqqqq", v["q"], 4096, 4096, v["out"], 0, *([1024, 128] * 5))
     assert lib.spec_rope_append_fp4(t, 1, 4, codes(tokens=3, dim=v["dim"]), scales(), 4096, v["r"], 1.0, 0, 4096, None) == 0
     return "scalar" if "scalar" in launches()[0][0] else "blocks"
 
-print(rope(), rope(r=64), rope(r=48), rope(q=4104), rope(dim=80, r=80), rope(dim=96, r=96))
+print(rope(), rope(r=64), rope(r=48), rope(q=4104), rope(dim=80, r=80), rope(dim=96, r=96), rope(dim=80, r=20), rope(r=48, out=4096), rope(out=4096))
 
 def pages(n_arrays, most, rows=3):
     fake.fake_clear()
@@ -185,7 +185,7 @@ print(pages(0, 0), pages(2, 100), pages(2, 100000), pages(2000, 1 << 20))
     assert got[1] == "('mma', 128) ('mma', 128) ('tc', 512) ('tc', 512)"
     assert got[2] == "mma mma"
     assert got[3] == "mma mma tc"
-    assert got[4] == "blocks blocks scalar scalar scalar blocks"
+    assert got[4] == "blocks blocks blocks scalar blocks blocks scalar scalar blocks"
     sms = int(got[5].rsplit(" ", 1)[1].rstrip("]")) // 8
     assert got[5] == f"[8] [8, 6] [8, 42] [8, {8 * sms}]"
 
