@@ -119,7 +119,7 @@ static const void* kernel_of(const AttnForm& form, const AttnPlan& plan) {
 
 cudaError_t attention_plan(const AttnForm& form, int kind, int rows, int D, int sms, AttnPlan* plan) {
   plan->kind = kind;
-  plan->bm = kind == 0 ? (form.fp4 && rows <= 8 ? 8 : 16) : kind == 1 ? 64 : kind == 2 ? 128 : 256;
+  plan->bm = kind == 0 ? (!form.fp4 ? 16 : rows <= 8 ? 8 : rows <= 16 || D > 128 ? 16 : 32) : kind == 1 ? 64 : kind == 2 ? 128 : 256;
   plan->bn = kind >= 2 ? kTcBN : form.fp4 ? kFp4BN : kAttnBN;
   plan->rows = rows < 1 ? 1 : rows < plan->bm ? rows : plan->bm;
   plan->dp = D <= 64 ? 64 : D <= 128 ? 128 : 256;
@@ -152,9 +152,12 @@ int attention_kind(int rows, int D, int page_size, float scale) {
   return rows <= 16 ? 0 : 1;
 }
 
-// Over caches in 4 bits: the tcgen05 kernel for more than 16 rows and heads of at most 128 values, else tiles of 16 rows.
+// Over caches in 4 bits: tiles of 8, 16 or 32 rows by mma.sync for up to 32 rows, for negative scales and heads above
+// 128 values (16 rows at most there: O fills the registers), else the tcgen05 kernel.  Measured, 64 requests ragged to 8192
+// keys, 8 key heads of 128 (332 MB): 4 rows 73 us (in tiles of 16 rows 92, tcgen05 218), 16 rows 111 (235), 20 rows 147 (two
+// tiles of 16 176, tcgen05 215), 32 rows 175 (209, 240), 64 rows 248 by tcgen05 (four tiles of 16 401).
 int attention_fp4_kind(int rows, int D, float scale) {
-  if (rows > 16 && D <= 128 && scale > 0.f) return rows > 128 ? 3 : 2;
+  if (rows > 32 && D <= 128 && scale > 0.f) return rows > 128 ? 3 : 2;
   return 0;
 }
 

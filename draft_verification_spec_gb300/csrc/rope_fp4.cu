@@ -14,7 +14,9 @@
 // - a rotated key's fp32 error, (|x| + |y|) 2^-21.5 at most, can move its rounding to 16 bits.  Where both ends of that
 //   interval do not give the same scale and codes (1 block in some 10^4), the keys in question are rotated in 64 bits.
 //
-// Bound: HBM: q read and written, k and v read, 4.5 bits a value written, no reuse.
+// Bound: HBM (q read and written, k and v read, 4.5 bits a value written, no reuse) and instructions.  Measured, 8192 tokens,
+// 32 + 2 x 8 heads of 128, bf16 (177 MB): 46 us, 3.9 TB/s; heads of 80 45 us; rotated parts that are no whole pieces (40 of
+// 80) 209 us.  One token: the host's call.
 #include <type_traits>
 
 #include "rope_device.cuh"
@@ -130,7 +132,7 @@ __device__ __forceinline__ Slot slot_of(const RopeParams& p, const Fp4Scales& s,
 // A CTA takes `per_cta` tokens: a warp each looks up the slot, the CTA computes the angles once for all heads.  Then each
 // thread moves 16-byte pieces of 8 values (a piece and its partner where they turn together), the next one's loads
 // issued before the current one's work; two lanes hold a block.  (A thread a block reads and writes every second 16 bytes
-// at a time: 80 us for 8192 tokens of 40 + 8 heads of 128.)
+// at a time: 80 us for 8192 tokens; all three kinds of heads in one loop: 57.)
 // SINGLE: where a block has values of both halves (heads of 80), a thread takes one piece and reads its partner beside it, so
 // nothing may be rotated in place.
 template <int DTYPE, bool INTERLEAVED, bool SINGLE>

@@ -139,9 +139,10 @@ size_t attention_workspace(int dtype, int q_heads, int kv_heads, int dim, int ma
   for (int kind = 0; kind < 4; ++kind) {
     if (!fp4 && ((kind == 0) != (rows <= 16) || (kind >= 2 && (dim < 64 || dim > 128 || (kind == 3) != (rows > 128))))) continue;
     if (fp4 && kind != sv::attention_fp4_kind(static_cast<int>(rows < 1024 ? rows : 1024), dim, 1.f) && kind != 0) continue;
-    for (int variant = 0; variant < 2; ++variant) {   // first tokens kept or not; over 4 bits, tiles of 8 rows or 16
+    for (int variant = 0; variant < (fp4 ? 3 : 2); ++variant) {   // first tokens kept or not; over 4 bits, tiles of 8, 16, 32 rows
       sv::AttnPlan plan;
-      if (sv::attention_plan({dtype == SPEC_BF16, !fp4 && variant, fp4}, kind, fp4 && variant ? 16 : 1, dim, sms, &plan) != cudaSuccess)
+      if (sv::attention_plan({dtype == SPEC_BF16, !fp4 && variant, fp4}, kind, fp4 ? 8 << variant : 1, dim, sms, &plan) !=
+          cudaSuccess)
         return 0;
       const size_t n = partial_bytes(plan, dim);
       most = n > most ? n : most;
@@ -193,6 +194,8 @@ spec_status_t run_attention(const AttentionCall& a) {
   sv::AttnMaps maps = {};
   sv::Fp4Scales scales = {};
   if (fp4) scales = internal_scales(*batch, *a.scales);
+  // strides that are not alike (keys' and values', or codes' and scales') leave the kernel that reads a key's 8 bytes and its
+  // scales one by one: 32 x 17 tokens ragged to 16384 keys 1302 us for 257, 64 single tokens to 8192 keys 199 for 73
   int kind = fp4 ? (scales.alike ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : 0) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);
   if (!fp4 && kind >= 2 && !sv::attention_maps(form.bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
   sv::AttnPlan plan;

@@ -157,7 +157,7 @@ def fp4(max_q, c=None, s=None, scale=0.1, heads=4):
     assert st == 0, st
     return "tc" if "attn_tc_kernel" in launches()[0][0] else "mma", launches()[0][2][0]
 
-print(fp4(1), fp4(4), fp4(5), fp4(40))
+print(fp4(1), fp4(4), fp4(8), fp4(9))
 print(fp4(40, scale=-0.1)[0], fp4(40, c=codes(tokens=40, dim=256, k_head=128, v_head=128), s=scales(k_head=16, v_head=16))[0])
 print(fp4(40, s=scales(v_token=72))[0], fp4(40, c=codes(tokens=40, k_page=1 << 38, v_page=1 << 38), s=scales(k_page=1 << 35, v_page=1 << 35))[0],
       fp4(40, c=codes(tokens=40, page_size=24))[0])
@@ -182,7 +182,7 @@ print(pages(0, 0), pages(2, 100), pages(2, 100000), pages(2000, 1 << 20))
 """)
     got = out.split("\n")
     assert got[0] == "True True True True"
-    assert got[1] == "('mma', 128) ('mma', 128) ('tc', 512) ('tc', 512)"
+    assert got[1] == "('mma', 128) ('mma', 128) ('mma', 128) ('tc', 512)"
     assert got[2] == "mma mma"
     assert got[3] == "mma mma tc"
     assert got[4] == "blocks blocks blocks scalar blocks blocks scalar scalar blocks"
