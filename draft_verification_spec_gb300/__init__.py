@@ -17,7 +17,8 @@ budget over prefix confidences prod alpha.
 The operators around that call (module ``step``): ``sample_tokens`` (the
 drafts' tokens and truncated logits), ``rope_append`` (positions of the new
 tokens, cache write) and ``chunk_attention`` (the new tokens over the paged
-cache).
+cache); ``FP4Cache`` (a cache held in 4 bits), ``PagePool``, ``assign_pages``
+and ``compact_pages`` (which request holds which page).
 """
 from __future__ import annotations
 

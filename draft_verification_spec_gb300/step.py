@@ -6,6 +6,11 @@
     out = chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q)
     s = sample_tokens(logits, uniforms, temperature=0.8, top_p=0.95, want_filtered=True)
 
+    k_cache, v_cache = (FP4Cache(pages, page_size, kv_heads, head_dim) for _ in range(2))   # in place of tensors
+    pool = PagePool([k_cache, v_cache])
+    page_table = assign_pages(pool, page_table, lens, page_size, kept=kept, parents=parents)
+    page_table, used = compact_pages(pool, page_table)
+
 A batch is packed: tokens ``cu_q[b]:cu_q[b+1]`` are the new ones of request b, the last of its
 ``kv_lens[b]`` tokens; its token t is slot ``t % page_size`` of page ``page_table[b, t // page_size]``
 of caches [pages, page_size, kv_heads, dim].  Lengths stay on the device.  With ``stream=`` a call runs
