@@ -337,11 +337,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_pages_kernel(const PagePara
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const long long per = static_cast<long long>(p.n_arrays) * chunks, items = __ldcg(p.moves) * per;
   for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-    const int m = static_cast<int>(it / per), in = static_cast<int>(it - m * per), a = in / chunks;
+    const int m = static_cast<int>(it / per);
+    const long long in = it - m * per;   // array and chunk
+    const int a = static_cast<int>(in / chunks);
     const int src = __ldcg(p.src + m), dst = __ldcg(p.dst + m);
     if (src < 0) continue;
     const PageArray arr = p.arrays[a];
-    const long long from = static_cast<long long>(in - a * chunks) * kCopyBytes;
+    const long long from = (in - static_cast<long long>(a) * chunks) * kCopyBytes;
     const int bytes = static_cast<int>(min(arr.bytes - from, static_cast<long long>(kCopyBytes)));
     if (bytes <= 0) continue;
     const uint8_t* s = arr.base + src * arr.stride + from;

@@ -73,7 +73,7 @@ def _assign(sv, table, lens, page, pages, kept, parents=None, strided=False):
 
 
 @pytest.mark.parametrize("page", [1, 3, 16])
-@pytest.mark.parametrize("rows,width,pages", [(1, 1, 1), (1, 4, 7), (5, 9, 60), (70, 3, 400), (300, 2, 700), (3, 300, 1000)])
+@pytest.mark.parametrize("rows,width,pages", [(1, 1, 1), (1, 4, 7), (5, 9, 60), (70, 3, 400), (300, 2, 700), (3, 300, 1000), (1500, 2, 3300)])
 def test_assign_steps(sv, rows, width, pages, page):
     """Between two steps: some tokens dropped, some more wanted, requests that end and begin."""
     for seed in range(3):
