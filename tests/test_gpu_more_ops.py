@@ -427,7 +427,8 @@ def _append(sv, new, kv, page, hq, hkv, d, dtype="bf16", rotary=None, layout="ha
 
 @pytest.mark.parametrize("layout", ["half", "interleaved"])
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
-@pytest.mark.parametrize("d,rotary", [(64, 64), (128, 64), (80, 80), (80, 20), (128, 128), (256, 256), (96, 48), (16, 2)])
+@pytest.mark.parametrize("d,rotary", [(64, 64), (128, 64), (80, 80), (80, 20), (80, 40), (128, 128), (256, 256), (96, 48), (128, 48), (112, 112),
+                                      (48, 48), (16, 16), (16, 2), (80, 72)])
 def test_append_layouts(sv, layout, dtype, d, rotary):
     _append(sv, [1, 3, 5], [1, 20, 40], 16, 4, 2, d, dtype=dtype, rotary=rotary, layout=layout, seed=d + rotary)
 
@@ -468,7 +469,7 @@ def test_append_units_and_edges_of_the_format(sv):
         v[4] *= 2.0 ** 13
         v[5, :, 3] = math.inf
         v[6, :, 5] = -math.inf
-        v[7, :, 7] = math.nan
+        v[7, :, 7] = k[7, :, 9] = math.nan
         v[8] = -0.0
 
     for dtype in ("bf16", "f16"):
