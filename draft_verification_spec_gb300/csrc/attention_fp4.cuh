@@ -93,7 +93,6 @@ __device__ __forceinline__ void cp_async_some(uint32_t dst, const void* src, boo
   const int n = valid ? N : 0;
   asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
 }
-__device__ __forceinline__ long long shfl64(long long v, int lane) { return __shfl_sync(0xffffffffu, v, lane); }
 
 // 8 x 8 values of 16 bits, transposed across the warp.
 __device__ __forceinline__ uint32_t transposed(uint32_t a) {

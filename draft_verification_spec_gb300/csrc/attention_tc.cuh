@@ -35,7 +35,7 @@
 // 64/8 heads, ragged to 16384 keys (1.11 GB) 218-224 us, 5.0 TB/s, 74 % of the measured copy: 136 rows take two
 // halves of 128.
 //
-// Over caches held in 4 bits (FP4) three warps (8, 10, 11) take the producer's place: they read codes and scales a tile
+// Over caches held in 4 bits (FP4) seven warps (8, 10 to 15) take the producer's place: they read codes and scales a tile
 // ahead into registers, widen them to f16 (exactly: attention_fp4.cuh) and write them where the TMA boxes would lie; tokens
 // that are not seen become zeros, so nothing has to be cleared, and any page size will do.  The queries of bf16 rows are
 // f16 relative to a power of two at the row's largest value, the probabilities f16 up to 2^14.
