@@ -25,9 +25,9 @@ const void* attn_tc_fn<true, true>(int dp, bool wide);
 template <>
 const void* attn_tc_fn<false, true>(int dp, bool wide);
 template <>
-const void* attn_tc_fp4_fn<true>(int dp, bool wide);
+const void* attn_tc_fp4_fn<true>(int dp, bool wide, bool whole);
 template <>
-const void* attn_tc_fp4_fn<false>(int dp, bool wide);
+const void* attn_tc_fp4_fn<false>(int dp, bool wide, bool whole);
 template <>
 const void* attn_fp4_fn<true>(int dp, int bm);
 template <>
@@ -111,7 +111,7 @@ static const void* kernel_of(const AttnPlan& plan) {
 }
 static const void* kernel_of(const AttnForm& form, const AttnPlan& plan) {
   if (form.fp4 && plan.kind >= 2)
-    return form.bf16 ? attn_tc_fp4_fn<true>(plan.dp, plan.kind == 3) : attn_tc_fp4_fn<false>(plan.dp, plan.kind == 3);
+    return form.bf16 ? attn_tc_fp4_fn<true>(plan.dp, plan.kind == 3, form.whole) : attn_tc_fp4_fn<false>(plan.dp, plan.kind == 3, form.whole);
   if (form.fp4) return form.bf16 ? attn_fp4_fn<true>(plan.dp, plan.bm) : attn_fp4_fn<false>(plan.dp, plan.bm);
   if (form.sinks) return form.bf16 ? kernel_of<true, true>(plan) : kernel_of<false, true>(plan);
   return form.bf16 ? kernel_of<true, false>(plan) : kernel_of<false, false>(plan);

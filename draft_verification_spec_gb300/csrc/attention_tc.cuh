@@ -233,13 +233,14 @@ struct TcFp4Share {
   static __device__ __forceinline__ int key(int loader, int i, int lane) { return (i * kTcLoaders + loader) * kKeys + lane % kKeys; }
   // Reads this lane's units of the keys at the given scales (offset in bytes; none: zeros).  The codes lie 8 times as far
   // from their base, and the bases are those of the lane's place in a key.
-  __device__ __forceinline__ void load(const uint8_t* codes_at, const uint8_t* scales_at, const uint32_t (&at)[kMine],
-                                       bool whole, int D, int lane) {
+  template <bool WHOLE>
+  __device__ __forceinline__ void load(const uint8_t* codes_at, const uint8_t* scales_at, const uint32_t (&at)[kMine], int D,
+                                       int lane) {
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
       const uint8_t* x = codes_at + static_cast<unsigned long long>(at[i]) * 8;
       const uint8_t* y = scales_at + at[i];
-      if (whole) {
+      if (WHOLE) {
         asm volatile(
             "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0xffffffff;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\t"
             "mov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\tmov.b16 %4, 0;\n\t"
@@ -287,7 +288,8 @@ struct TcFp4Share {
   }
 };
 
-template <bool BF16, int DP, bool WIDE, bool SINKS, bool FP4>
+// WHOLE (FP4): heads of DP values, codes and scales aligned to whole pieces.  (As a branch of the loop: 5 % slower.)
+template <bool BF16, int DP, bool WIDE, bool SINKS, bool FP4, bool WHOLE>
 __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
     attn_tc_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const AttnParams p) {
   using A = AttnType<BF16>;
@@ -432,8 +434,8 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
     const int in_key = lane / Share::kKeys;   // this lane's 32 values of a key
     const uint8_t *k_codes = p.c.k + in_key * 16, *v_codes = p.c.v + in_key * 16;
     const uint8_t *k_scales = p.s.k + in_key * 2, *v_scales = p.s.v + in_key * 2;
-    auto load_k = [&](const Places& x) { k.load(k_codes, k_scales, x.at, p.s.whole, p.c.D, lane); };
-    auto load_v = [&](const Places& x) { v.load(v_codes, v_scales, x.at, p.s.whole, p.c.D, lane); };
+    auto load_k = [&](const Places& x) { k.template load<WHOLE>(k_codes, k_scales, x.at, p.c.D, lane); };
+    auto load_v = [&](const Places& x) { v.template load<WHOLE>(v_codes, v_scales, x.at, p.c.D, lane); };
     bool ok = p.wait_limit > 0 || wait.give_up();
     unsigned g = 0;   // key tiles of this CTA so far
     auto put_k = [&](unsigned n) -> bool {
@@ -1024,6 +1026,6 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
 template <bool BF16, bool SINKS>
 const void* attn_tc_fn(int dp, bool wide);
 template <bool BF16>
-const void* attn_tc_fp4_fn(int dp, bool wide);
+const void* attn_tc_fp4_fn(int dp, bool wide, bool whole);
 
 }  // namespace sv

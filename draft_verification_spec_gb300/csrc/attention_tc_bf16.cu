@@ -6,10 +6,10 @@ namespace sv {
 template <>
 const void* attn_tc_fn<true, false>(int dp, bool wide) {
   if (wide)
-    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, true, false, false>)
-                    : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, true, false, false>);
-  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, false, false, false>)
-                  : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, false, false, false>);
+    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, true, false, false, false>)
+                    : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, true, false, false, false>);
+  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, false, false, false, false>)
+                  : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, false, false, false, false>);
 }
 
 }  // namespace sv

@@ -3,13 +3,18 @@
 
 namespace sv {
 
-template <>
-const void* attn_tc_fp4_fn<true>(int dp, bool wide) {
+template <bool WHOLE>
+static const void* instance(int dp, bool wide) {
   if (wide)
-    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, true, true, true>)
-                    : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, true, true, true>);
-  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, false, true, true>)
-                  : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, false, true, true>);
+    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, true, true, true, WHOLE>)
+                    : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, true, true, true, WHOLE>);
+  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, false, true, true, WHOLE>)
+                  : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, false, true, true, WHOLE>);
+}
+
+template <>
+const void* attn_tc_fp4_fn<true>(int dp, bool wide, bool whole) {
+  return whole ? instance<true>(dp, wide) : instance<false>(dp, wide);
 }
 
 }  // namespace sv

@@ -6,10 +6,10 @@ namespace sv {
 template <>
 const void* attn_tc_fn<true, true>(int dp, bool wide) {
   if (wide)
-    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, true, true, false>)
-                    : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, true, true, false>);
-  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, false, true, false>)
-                  : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, false, true, false>);
+    return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, true, true, false, false>)
+                    : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, true, true, false, false>);
+  return dp == 64 ? reinterpret_cast<const void*>(&attn_tc_kernel<true, 64, false, true, false, false>)
+                  : reinterpret_cast<const void*>(&attn_tc_kernel<true, 128, false, true, false, false>);
 }
 
 }  // namespace sv

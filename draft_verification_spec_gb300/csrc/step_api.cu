@@ -141,7 +141,7 @@ size_t attention_workspace(int dtype, int q_heads, int kv_heads, int dim, int ma
     if (fp4 && kind != sv::attention_fp4_kind(static_cast<int>(rows < 1024 ? rows : 1024), dim, 1.f) && kind != 0) continue;
     for (int variant = 0; variant < (fp4 ? 3 : 2); ++variant) {   // first tokens kept or not; over 4 bits, tiles of 8, 16, 32 rows
       sv::AttnPlan plan;
-      if (sv::attention_plan({dtype == SPEC_BF16, !fp4 && variant, fp4}, kind, fp4 ? 8 << variant : 1, dim, sms, &plan) !=
+      if (sv::attention_plan({dtype == SPEC_BF16, !fp4 && variant, fp4, true}, kind, fp4 ? 8 << variant : 1, dim, sms, &plan) !=
           cudaSuccess)
         return 0;
       const size_t n = partial_bytes(plan, dim);
@@ -187,13 +187,13 @@ spec_status_t run_attention(const AttentionCall& a) {
   if (!a.workspace || !aligned(a.workspace, 256)) return SPEC_ERR_WORKSPACE;
   int sms = 0;
   if ((st = sm_count(&sms)) != SPEC_OK) return st;
-  const sv::AttnForm form = {a.dtype == SPEC_BF16, a.window > 0 && a.sinks > 0, fp4};
   const int G = a.q_heads / batch->kv_heads;
   const long long all_rows = static_cast<long long>(a.max_q) * G;
   const int rows = static_cast<int>(all_rows < 1024 ? all_rows : 1024);
   sv::AttnMaps maps = {};
   sv::Fp4Scales scales = {};
   if (fp4) scales = internal_scales(*batch, *a.scales);
+  const sv::AttnForm form = {a.dtype == SPEC_BF16, a.window > 0 && a.sinks > 0, fp4, scales.whole != 0};
   // strides that are not alike (keys' and values', or codes' and scales') leave the kernel that reads a key's 8 bytes and its
   // scales one by one: 32 x 17 tokens ragged to 16384 keys 1302 us for 257, 64 single tokens to 8192 keys 199 for 73
   int kind = fp4 ? (scales.alike ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : 0) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);

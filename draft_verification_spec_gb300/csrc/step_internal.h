@@ -67,9 +67,10 @@ struct AttnParams {
   int32_t* status;
 };
 
-// Kernel families of the attention: what the cache holds and whether first tokens stay visible.
+// Kernel families of the attention: q's type, whether first tokens stay visible, whether the cache is held in 4 bits
+// (whole: as Fp4Scales).
 struct AttnForm {
-  bool bf16, sinks, fp4;
+  bool bf16, sinks, fp4, whole;
 };
 // Rows per tile, keys per tile.
 struct AttnPlan {
