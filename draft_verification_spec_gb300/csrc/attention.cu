@@ -154,8 +154,8 @@ int attention_kind(int rows, int D, int page_size, float scale) {
 
 // Over caches in 4 bits: tiles of 8, 16 or 32 rows by mma.sync for up to 32 rows, for negative scales and heads above
 // 128 values (16 rows at most there: O fills the registers), else the tcgen05 kernel.  Measured, 64 requests ragged to 8192
-// keys, 8 key heads of 128 (332 MB): 4 rows 73 us (in tiles of 16 rows 92, tcgen05 218), 16 rows 111 (235), 20 rows 147 (two
-// tiles of 16 176, tcgen05 215), 32 rows 175 (209, 240), 64 rows 248 by tcgen05 (four tiles of 16 401).
+// keys, 8 key heads of 128 (332 MB): 4 rows 73 us (in tiles of 16 rows 92, tcgen05 208), 16 rows 111 (224), 20 rows 146 (two
+// tiles of 16 176, tcgen05 205), 32 rows 174 (209, 228); by tcgen05 40 rows 227 (two tiles of 32 305), 64 rows 230 (324).
 int attention_fp4_kind(int rows, int D, float scale) {
   if (rows > 32 && D <= 128 && scale > 0.f) return rows > 128 ? 3 : 2;
   return 0;

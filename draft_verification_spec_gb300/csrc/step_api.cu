@@ -195,7 +195,7 @@ spec_status_t run_attention(const AttentionCall& a) {
   if (fp4) scales = internal_scales(*batch, *a.scales);
   const sv::AttnForm form = {a.dtype == SPEC_BF16, a.window > 0 && a.sinks > 0, fp4, scales.whole != 0};
   // strides that are not alike (keys' and values', or codes' and scales') leave the kernel that reads a key's 8 bytes and its
-  // scales one by one: 32 x 17 tokens ragged to 16384 keys 1302 us for 257, 64 single tokens to 8192 keys 199 for 73
+  // scales one by one: 32 x 17 tokens ragged to 16384 keys 1297 us for 242, 64 single tokens to 8192 keys 199 for 73
   int kind = fp4 ? (scales.alike ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : 0) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);
   if (!fp4 && kind >= 2 && !sv::attention_maps(form.bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
   sv::AttnPlan plan;
@@ -228,8 +228,9 @@ spec_status_t run_attention(const AttentionCall& a) {
   p.part_o = p.part_ml + static_cast<size_t>(plan.grid) * 2 * plan.bm * 2;
   // an item's fixed cost in key tiles.  Measured, 64 requests x 4 tokens, ragged to 4096 keys (mma.sync):
   // 0: 140, 1: 127, 2: 115, 3: 113, 4: 114 us; 32 x 17 tokens, 64 query heads, ragged to 16384 (tcgen05):
-  // 0: 248, 2: 234, 3: 224, 4: 220, 6: 220 us.
-  p.overhead = plan.kind >= 2 ? 4 : 3;
+  // 0: 248, 2: 234, 3: 224, 4: 220, 6: 220 us.  Over 4 bits (the same 32 x 17 tokens, tcgen05): 1: 294, 2: 282, 3: 257, 4: 245,
+  // 5: 242 us; 64 single tokens to 16384 keys (mma.sync): 1: 139, 2: 134, 3: 130, 4: 131, 6: 132 us.
+  p.overhead = plan.kind >= 2 ? (fp4 ? 5 : 4) : 3;
   // fewest units worth a CTA: an item's cost and one key tile.  A single token over 1024 keys, 8 key heads
   // (152 units, so 38 CTAs of four): 12.4 us; with two tiles (31 CTAs) 13.3, with four (22) 15.2 us.
   p.min_units = 1 + p.overhead;
