@@ -35,6 +35,9 @@ constexpr int kFp4BN = 128;         // keys of a tile
 constexpr int kFp4WarpKeys = 32;    // of which a warp takes this many
 // Probabilities are 2^kShift times the weights against the reference, which lie between 0 and 2^kGrow.
 constexpr float kFp4Shift = 6.f, kFp4Grow = 8.f;
+// Least factor of a row's scores (softmax scale, unit, the queries' power of two): a smaller one, or zero, would make NaN of
+// -inf.  The products that it stands before are below 2^36 (256 x 65504 x 2688), so the scores are zero to fp32 either way.
+constexpr float kFp4Least = 1e-30f;
 
 template <int DP, int NQ>
 struct AttnFp4Geom {
@@ -252,8 +255,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
             top = fmaxf(top, fmaxf(fabsf(__uint_as_float(v[e] << 16)), fabsf(__uint_as_float(v[e] & 0xffff0000u))));
         }
       }
-      // a negative scale turns the query's sign, one of zero becomes too small to tell: the factors are positive
-      float mine = fmaxf(fabsf(p.scale_log2), 1e-30f);
+      // a negative scale turns the query's sign: the factors are positive
+      float mine = fabsf(p.scale_log2);
       if (p.scale_log2 < 0.f) {
 #pragma unroll
         for (int s = 0; s < DP / 16; ++s) {
@@ -272,7 +275,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
           for (int h = 0; h < 2; ++h)
             f[s][h] = H::pack(__uint_as_float(f[s][h] << 16) * down, __uint_as_float(f[s][h] & 0xffff0000u) * down);
       }
-      return mine;
+      return fmaxf(mine, kFp4Least);
     };
     if constexpr (Geo::kQSmem) {   // a warp each 8 rows, for all
       static_assert(NQ <= 4, "a warp each");

@@ -705,6 +705,7 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
           }
           scale_log2 *= fp4_query_power(top, &down);
         }
+        scale_log2 = fmaxf(scale_log2, kFp4Least);
         if (half == 0 || !joined) {
           const uint32_t dst = s_q + half * TILE + row * 128;
 #pragma unroll

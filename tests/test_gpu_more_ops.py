@@ -258,6 +258,16 @@ def test_fp4_scale_of_zero(sv):
         _fp4(sv, [nq, nq], [77, 260], 16, 8, 4, 64, scale=0.0, seed=4)
 
 
+@pytest.mark.parametrize("nq", [1, 5, 12, 40])
+def test_fp4_scores_too_small_to_tell(sv, nq):
+    """The product of scale, unit and the queries' power of two lies below every fp32 number, or the scale is zero and the queries
+    are large: every key that is seen counts the same."""
+    _fp4(sv, [nq, nq], [77, 260], 16, 8, 4, 128, scale=1e-30, units=(2.0 ** -64, 1.0), seed=6)
+    _fp4(sv, [nq, nq], [77, 260], 16, 8, 4, 64, scale=1e-12, grow=1e-35, seed=7)
+    _fp4(sv, [nq, nq], [77, 260], 16, 8, 4, 64, scale=0.0, grow=1e25, seed=8)
+    _fp4(sv, [nq, nq], [77, 260], 16, 8, 4, 128, dtype="f16", scale=1e-40, units=(2.0 ** -10, 1.0), seed=9)
+
+
 @pytest.mark.parametrize("d,nq,hq", [(64, 17, 4), (128, 40, 16), (80, 40, 4), (128, 4, 8)])
 def test_fp4_wait_that_runs_out_writes_nothing(sv, d, nq, hq):
     """Every bounded wait gives up at once: the status says so, no row is written; the next call is right."""
