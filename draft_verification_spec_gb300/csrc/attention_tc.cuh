@@ -21,7 +21,7 @@
 // thread that has seen S(j) may touch O.
 //
 // First tokens that stay visible behind a window (SINKS): the item's key tiles are those that hold them, then those of the
-// window; what lies between is not looked at.  2 x 2048 tokens behind 14336, window 4096, 64 first tokens (279 GFLOP) 263 us:
+// window; what lies between is not looked at.  2 x 2048 tokens behind 14336, window 4096, 64 first tokens (279 GFLOP) 258 us:
 // tiles that the mask cuts and an item's fixed cost every 35 tiles.
 //
 // Keys before the item's first one or at or beyond its last one: pages that lie wholly there are read at an
@@ -679,19 +679,17 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
     unsigned tiles = 0, segs = 0, joins = 0;
     bool later = false;             // not the CTA's first item
     bool ok = true, owed = false;   // owed: half 0 may still read this half's O and statistics
-    while (ok) {
-      const int len = k1 - k0;
-      const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
+    // Writes this half's queries of an item where the MMAs read them.  Returns the factor of the scores.
+    auto load_q = [&](const AttnCursor& it) -> float {
+      const int r0 = it.t * BM, r1 = min(it.req.nq * p.G, r0 + BM);
       const bool joined = r1 - r0 <= 128;
-      const int h0 = r0 + (joined ? 0 : half * 128), r = h0 + row;
+      const int r = r0 + (joined ? 0 : half * 128) + row;
       const bool mine = r < r1;
-      const bool busy = h0 + (warp & 3) * 32 < r1;   // some row of this warp exists
-      float scale_log2 = p.scale_log2;
+      const int tok = it.req.q0 + attn_token(p, r), head = it.h * p.G + r - (attn_token(p, r)) * p.G;
+      const uint8_t* src = p.q + (tok * p.q_token + head * p.q_head) * 2;
+      float scale_log2 = p.scale_log2, down = 1.f;
       if constexpr (FP4) {
         // the row in f16; both halves need its power of two, the one that owns it writes it
-        const int tok = cur.req.q0 + attn_token(p, r), head = cur.h * p.G + r - (attn_token(p, r)) * p.G;
-        const uint8_t* src = p.q + (tok * p.q_token + head * p.q_head) * 2;
-        float down = 1.f;
         if (BF16) {
           float top = 0.f;
 #pragma unroll
@@ -706,40 +704,38 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
           scale_log2 *= fp4_query_power(top, &down);
         }
         scale_log2 = fmaxf(scale_log2, kFp4Least);
-        if (half == 0 || !joined) {
-          const uint32_t dst = s_q + half * TILE + row * 128;
-#pragma unroll
-          for (int c = 0; c < DP / 8; ++c) {
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (mine && c * 8 < p.c.D) v = __ldg(reinterpret_cast<const uint4*>(src + c * 16));
-            uint32_t w[4] = {v.x, v.y, v.z, v.w};
-            if (BF16) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = M::pack(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xffff0000u) * down);
-            }
-            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)),
-                         "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
-                         : "memory");
-          }
-          fence_async_smem();
-          mbar_arrive_warp(smem_addr(&bars.q_full[half]));
-        }
-      } else if (half == 0 || !joined) {
-        const int tok = cur.req.q0 + attn_token(p, r), head = cur.h * p.G + r - (attn_token(p, r)) * p.G;
-        const uint8_t* src = p.q + (tok * p.q_token + head * p.q_head) * 2;
+      }
+      if (half == 0 || !joined) {
         const uint32_t dst = s_q + half * TILE + row * 128;
 #pragma unroll
         for (int c = 0; c < DP / 8; ++c) {
           uint4 v = make_uint4(0, 0, 0, 0);
           if (mine && c * 8 < p.c.D) v = __ldg(reinterpret_cast<const uint4*>(src + c * 16));
+          uint32_t w[4] = {v.x, v.y, v.z, v.w};
+          if (FP4 && BF16) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              w[e] = M::pack(__uint_as_float(w[e] << 16) * down, __uint_as_float(w[e] & 0xffff0000u) * down);
+          }
           asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(dst + (c / 8) * 16384 + (((c & 7) ^ (row & 7)) << 4)),
-                       "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
+                       "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3])
                        : "memory");
         }
         fence_async_smem();
         mbar_arrive_warp(smem_addr(&bars.q_full[half]));
       }
+      return scale_log2;
+    };
+    float scale_log2 = p.scale_log2;
+    if (!FP4) load_q(cur);
+    while (ok) {
+      const int len = k1 - k0;
+      const int r0 = cur.t * BM, r1 = min(cur.req.nq * p.G, r0 + BM);
+      const bool joined = r1 - r0 <= 128;
+      const int h0 = r0 + (joined ? 0 : half * 128), r = h0 + row;
+      const bool mine = r < r1;
+      const bool busy = h0 + (warp & 3) * 32 < r1;   // some row of this warp exists
+      if (FP4) scale_log2 = load_q(cur);
       if (owed) {
         ok = wait.warp(smem_addr(&bars.x_free), (joins - 1) & 1);
         if (!ok) break;
@@ -926,12 +922,29 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
         mbar_arrive_warp(smem_addr(&bars.p_full[half]));
       }
       if (!ok) break;
-      if (j0 < len) {
-        ok = wait.warp(smem_addr(&bars.o_full[half]), segs & 1);
-        ++segs;
+      // The next item's queries, before this one's rows are written: its first scores are on their way meanwhile (2 x 2048
+      // tokens behind 14336 683 -> 667 us, 64 prompts of 300 behind 300 298 -> 264; over 4 bits 1 % slower).  The MMAs that read
+      // the old ones are done: the half's own when its last scores are there; of a joined item's two halves, which share
+      // them, when half 0's O is (it comes after both halves' last scores).
+      auto wait_o = [&] {
+        if (j0 < len) {
+          ok = wait.warp(smem_addr(&bars.o_full[half]), segs & 1);
+          ++segs;
+        }
+      };
+      AttnCursor next = cur;
+      bool more = false;
+      if constexpr (!FP4) {
+        more = attn_next<BN, SINKS>(p, BM, u_end, &next);
+        if (joined) wait_o();
         if (!ok) break;
-        tc_fence_after();
+        if (more) load_q(next);
+        if (!joined) wait_o();
+      } else {
+        wait_o();
       }
+      if (!ok) break;
+      if (j0 < len) tc_fence_after();
       float f0 = 1.f, f1 = 0.f;   // the halves' factors
       if (joined) {
         ++joins;
@@ -1000,8 +1013,11 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
         tc_fence_before();
         if (joined) mbar_arrive_warp(smem_addr(&bars.x_free));
       }
-      AttnCursor next = cur;
-      if (!attn_next<BN, SINKS>(p, BM, u_end, &next)) {
+      if constexpr (FP4) {
+        next = cur;
+        more = attn_next<BN, SINKS>(p, BM, u_end, &next);
+      }
+      if (!more) {
         if (tid == 0) attn_leave_join(p, split, cta, BM, &cur, later);
         break;
       }
