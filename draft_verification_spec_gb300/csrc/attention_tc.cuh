@@ -29,10 +29,10 @@
 // rows are zeroed in shared memory before the MMA reads them (0 x NaN would be NaN); scores are
 // selected, not multiplied.
 //
-// Bound and measured, heads of 128, bf16: 2 x 2048 tokens behind 14336, 32/8 heads (1.03 TFLOP) 655-761 us (by
-// the machine), 1.35-1.57 PFLOP/s, 72-83 % of the measured matrix rate: a half's softmax (1200 cycles a tile)
+// Bound and measured, heads of 128, bf16: 2 x 2048 tokens behind 14336, 32/8 heads (1.03 TFLOP) 723-745 us (by
+// the machine), 1.38-1.42 PFLOP/s, 73-75 % of the measured matrix rate: a half's softmax (1200 cycles a tile)
 // and its two products (1024) follow one another, and the other half fills most of the gap.  32 x 17 tokens,
-// 64/8 heads, ragged to 16384 keys (1.11 GB) 208-224 us, 5.0-5.3 TB/s, 74-78 % of the measured copy: 136 rows take two
+// 64/8 heads, ragged to 16384 keys (1.11 GB) 218-220 us, 5.0 TB/s, 74 % of the measured copy: 136 rows take two
 // halves of 128.
 //
 // Over caches held in 4 bits (FP4) seven warps (8, 10 to 15) take the producer's place: they read codes and scales a tile
@@ -923,7 +923,7 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
       }
       if (!ok) break;
       // The next item's queries, before this one's rows are written: its first scores are on their way meanwhile (2 x 2048
-      // tokens behind 14336 683 -> 667 us, 64 prompts of 300 behind 300 298 -> 264; over 4 bits 1 % slower).  The MMAs that read
+      // tokens behind 14336 745 -> 734 us, 64 prompts of 300 behind 300 298 -> 264; over 4 bits 1 % slower).  The MMAs that read
       // the old ones are done: the half's own when its last scores are there; of a joined item's two halves, which share
       // them, when half 0's O is (it comes after both halves' last scores).
       auto wait_o = [&] {
