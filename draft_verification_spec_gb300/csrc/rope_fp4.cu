@@ -292,7 +292,8 @@ __global__ void __launch_bounds__(kRopeThreads)
               const unsigned long long pos = held ? static_cast<unsigned long long>(static_cast<long long>(slots[cur.t].pos)) : 0ull;
 #pragma unroll
               for (int i = 0; i < 8; ++i) {
-                if (!held || !differs || lo[i] == hi[i]) continue;
+                // what is not rotated is exact (and has no frequency); a NaN of it is equal to nothing
+                if (!held || !differs || !cur.rotate || lo[i] == hi[i]) continue;
                 const int k = INTERLEAVED ? cur.at / 2 + i / 2 : (behind ? cur.at - half : cur.at) + i;
                 const bool second = INTERLEAVED ? i & 1 : which || behind;
                 x[i] = rounded<T>(rotated_exactly(self(i), partner(i), second ? 1.f : -1.f, p.freq[k] * pos, p.factor));
@@ -389,7 +390,7 @@ __global__ void __launch_bounds__(kRopeThreads)
           int differs = s0 != s1 || c0 != c1;
 #pragma unroll
           for (int o = 1; o < 16; o <<= 1) differs |= __shfl_xor_sync(0xffffffffu, differs, o);
-          if (differs && below != above)
+          if (differs && rotated(c) && below != above)   // (a NaN that is not rotated is equal to nothing, and has no frequency)
             y = rounded<T>(rotated_exactly(self[i], partner[i], second(c) ? 1.f : -1.f, p.freq[pair(c)] * pos, p.factor));
         }
       }
