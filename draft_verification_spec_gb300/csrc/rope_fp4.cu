@@ -456,15 +456,16 @@ __global__ void __launch_bounds__(256) fp4_values_kernel(const Fp4Values p) {
 cudaError_t launch_rope_fp4(int dtype, const RopeParams& p, const Fp4Scales& s, float k_unit, float v_unit, int sms,
                             cudaStream_t stream) {
   const Unit4 ku = {k_unit, static_cast<float>(1.0 / (6.0 * k_unit))}, vu = {v_unit, static_cast<float>(1.0 / (6.0 * v_unit))};
-  const long long strides[] = {p.q_token, p.q_head, p.k_token, p.k_head, p.v_token, p.v_head, p.qo_token, p.qo_head,
-                               p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0};
+  const bool q = p.Hq > 0;   // without queries their pointers and strides are anything
+  const long long strides[] = {q ? p.q_token : 0, q ? p.q_head : 0, p.k_token, p.k_head, p.v_token, p.v_head,
+                               q ? p.qo_token : 0, q ? p.qo_head : 0, p.k_out ? p.ko_token : 0, p.k_out ? p.ko_head : 0};
   bool whole = p.rotary % (p.interleaved ? 8 : 16) == 0;
   const bool single = !p.interleaved && p.rotary % 32 != 0;
-  if (single && (p.q_out == p.q || p.k_out == p.k)) whole = false;
+  if (single && ((q && p.q_out == p.q) || p.k_out == p.k)) whole = false;
   for (long long st : strides) whole = whole && st % 8 == 0 && st >= 0 && st < (1ll << 31);
   const long long pieces = (p.Hq + 2ll * p.c.Hkv) * (p.c.D / 8);   // of a token; the kernel's quotients hold up to 2^16
   whole = whole && pieces < (1 << 16);
-  const void* bases[] = {p.q, p.k, p.v, p.q_out, p.k_out};
+  const void* bases[] = {q ? p.q : nullptr, p.k, p.v, q ? p.q_out : nullptr, p.k_out};
   for (const void* b : bases) whole = whole && (reinterpret_cast<uintptr_t>(b) & 15) == 0;
   if (!whole) {
     const dim3 grid(p.c.N), block(kRopeThreads);
