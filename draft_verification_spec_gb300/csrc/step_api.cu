@@ -291,6 +291,9 @@ spec_status_t run_rope(const spec_rope_tensors_t* t, int dtype, int q_heads, con
   return sv::launch_rope(dtype, p, sms, stream) == cudaSuccess ? SPEC_OK : SPEC_ERR_CUDA;
 }
 
+// Entries of a table, and pages: the page kernels count both in 32 bits, in steps of up to 1024 beyond the last one.
+constexpr long long kMaxPageEntries = 1ll << 30;
+
 // Workspace of the page operators: ints behind the status.
 size_t pages_ints(int pages, int rows) {
   const size_t copies = static_cast<size_t>(rows > pages / 2 ? rows : pages / 2);
@@ -304,7 +307,9 @@ spec_status_t run_pages(bool compact, const spec_page_pool_t* pool, int page_siz
   if (!pool || pool->pages < 1 || pool->n_arrays < 0 || pool->max_bytes < 0 || (pool->n_arrays > 0 && !pool->arrays))
     return SPEC_ERR_INVALID_ARG;
   if (rows < 0 || width < 0 || stride < width || out_stride < width || page_size < 1) return SPEC_ERR_INVALID_ARG;
-  if (static_cast<long long>(rows) * width > 0x7fffffffll || pool->max_bytes > (1ll << 40)) return SPEC_ERR_UNSUPPORTED;
+  if (static_cast<long long>(rows) * width > kMaxPageEntries || rows > kMaxPageEntries || pool->pages > kMaxPageEntries ||
+      pool->max_bytes > (1ll << 40))
+    return SPEC_ERR_UNSUPPORTED;
   const bool empty = rows == 0 || width == 0;
   if (empty && !compact) return SPEC_OK;
   if ((!empty && (!table || !out_table)) || (compact ? !out_used : !lens || !kept)) return SPEC_ERR_INVALID_ARG;
@@ -439,7 +444,7 @@ spec_status_t spec_fp4_values(const void* codes, long long page, long long token
 }
 
 size_t spec_pages_workspace_bytes(int pages, int rows) {
-  if (pages < 1 || rows < 0) return 0;
+  if (pages < 1 || rows < 0 || pages > kMaxPageEntries || rows > kMaxPageEntries) return 0;
   return kStatusBytes + (4 * pages_ints(pages, rows) + 255) / 256 * 256;
 }
 

@@ -442,6 +442,8 @@ class PagePool:
             pages = arrays[0].shape[0] if pages is None and arrays[0].dim() else pages
         elif pages is None:
             raise ValueError("a pool without caches needs pages")
+        if pages is not None and pages > 2 ** 30:
+            raise ValueError(f"a pool has 2^30 pages at most, got {pages}")
         device = arrays[0].device if arrays else torch.device("cuda", torch.cuda.current_device())
         rows, self.max_bytes = [], 0
         for t in arrays:

@@ -516,7 +516,13 @@ typedef struct spec_page_pool {
   long long max_bytes;           /* the largest of their `bytes` */
 } spec_page_pool_t;
 
-/* Workspace of spec_assign_pages and spec_compact_pages (256-byte aligned, as spec_attention_workspace_bytes). */
+/*
+ * Workspace of spec_assign_pages and spec_compact_pages (256-byte aligned, as
+ * spec_attention_workspace_bytes).  Both refuse pools of more than 2^30 pages,
+ * tables of more than 2^30 rows or entries and pages of more than 2^40 bytes
+ * in an array (SPEC_ERR_UNSUPPORTED); a table without entries is left as it
+ * is (compacting: 0 pages are used).
+ */
 size_t spec_pages_workspace_bytes(int pages, int rows);
 
 /*

@@ -1,4 +1,6 @@
 """What the operators on pages and caches in 4 bits launch and refuse, seen by a runtime that launches nothing (no device)."""
+import pytest
+
 from tests.fake_runtime import with_fake_runtime
 
 
@@ -19,3 +21,32 @@ print(rope(), rope(dim=128), rope(q=4096, out=4096), rope(q=4100, out=4099, stri
 print(rope(4096, 4096, heads=4), rope(4096, 8192, heads=4), rope(4100, 8192, heads=4), rope(4096, 8192, stride=1001, heads=4))
 """)
     assert out.split("\n")[:2] == ["blocks blocks blocks blocks blocks scalar", "scalar blocks scalar scalar"]
+
+
+def test_pools_and_tables_beyond_the_kernels_counters(tmp_path):
+    """Counters of rows, entries and pages step past the last one by up to 1024: near 2^31 they would start again below zero."""
+    out = with_fake_runtime(tmp_path, """
+def both(pages, rows, width):
+    fake.fake_clear()
+    pool = struct.pack("@Piiq", 0, 0, pages, 0)
+    table = (4096, max(width, 1), rows, width)
+    ws = (4096, 1 << 62, None)
+    a = lib.spec_assign_pages(pool, 16, *table, 4096, 4096, None, 4096, max(width, 1), *ws)
+    c = lib.spec_compact_pages(pool, *table, 4096, max(width, 1), 4096, *ws)
+    return a, c, len(launches()), lib.spec_pages_workspace_bytes(pages, rows) > 0
+
+most = 1 << 30
+print(both(most, 3, 4), both(10, most, 1), both(10, 1, most), both(10, 1 << 15, 1 << 15))
+print(both(most + 1, 3, 4), both(2 ** 31 - 1, 3, 4), both(10, 2 ** 31 - 1, 1), both(10, most + 1, 0), both(10, 3, 2 ** 29), both(10, 1, 2 ** 31 - 1))
+""")
+    fine, refused = out.split("\n")[:2]
+    assert fine == " ".join(["(0, 0, 2, True)"] * 4)
+    big = "(2, 2, 0, False)"
+    assert refused == " ".join([big] * 4 + ["(2, 2, 0, True)"] * 2)
+
+
+def test_a_pool_of_too_many_pages_is_refused():
+    import draft_verification_spec_gb300 as sv
+    for pages in (2 ** 30 + 1, 2 ** 31, 2 ** 40):
+        with pytest.raises(ValueError):
+            sv.PagePool([], pages=pages)
