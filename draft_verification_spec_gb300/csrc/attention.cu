@@ -67,7 +67,7 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p, i
         }
       }
     }
-    const float inv = l > 0.f ? p.v_unit / l : 0.f;
+    const float inv = attn_factor(l, p.v_unit);
     const int tok = attn_token(p, j.row0 + r);
     const long long row = static_cast<long long>(j.token0 + tok) * p.Hq + j.head0 + (j.row0 + r - tok * p.G);
 #pragma unroll
@@ -77,7 +77,7 @@ __global__ void __launch_bounds__(128) attn_combine_kernel(const AttnParams p, i
         *reinterpret_cast<uint2*>(p.out + (row * D + d) * 2) =
             make_uint2(A::pack(acc[i].x * inv, acc[i].y * inv), A::pack(acc[i].z * inv, acc[i].w * inv));
     }
-    if (lane == 0 && p.lse) p.lse[row] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : ninf();
+    if (lane == 0 && p.lse) p.lse[row] = attn_lse(m, l);
   }
 }
 

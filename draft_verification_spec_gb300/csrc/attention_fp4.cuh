@@ -563,12 +563,12 @@ __global__ void __launch_bounds__(kAttnThreads) attn_fp4_kernel(const AttnParams
         acc.w += f * x.w;
       }
       if (all) {
-        const float inv = ll > 0.f ? p.v_unit / ll : 0.f;
+        const float inv = attn_factor(ll, p.v_unit);
         const int tok = attn_token(p, r0 + r);
         const long long row = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r0 + r - tok * p.G);
         *reinterpret_cast<uint2*>(p.out + (row * D + d) * 2) =
             make_uint2(A::pack(acc.x * inv, acc.y * inv), A::pack(acc.z * inv, acc.w * inv));
-        if (d == 0 && p.lse) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : ninf();
+        if (d == 0 && p.lse) p.lse[row] = attn_lse(mm, ll);
       } else {
         const long long row = static_cast<long long>(slot) * BM + r;
         *reinterpret_cast<float4*>(p.part_o + row * D + d) = acc;

@@ -358,12 +358,12 @@ __global__ void __launch_bounds__(kAttnThreads) attn_mma_kernel(const AttnParams
         acc.w += f * x.w;
       }
       if (whole) {
-        const float inv = ll > 0.f ? 1.f / ll : 0.f;
+        const float inv = attn_factor(ll, 1.f);
         const int tok = attn_token(p, r0 + r);
         const long long row = static_cast<long long>(cur.req.q0 + tok) * p.Hq + cur.h * p.G + (r0 + r - tok * p.G);
         uint2 w = make_uint2(A::pack(acc.x * inv, acc.y * inv), A::pack(acc.z * inv, acc.w * inv));
         *reinterpret_cast<uint2*>(p.out + (row * D + d) * 2) = w;
-        if (d == 0 && p.lse) p.lse[row] = ll > 0.f ? (mm + log2f(ll)) * 0.69314718055994531f : ninf();
+        if (d == 0 && p.lse) p.lse[row] = attn_lse(mm, ll);
       } else {
         const long long row = static_cast<long long>(slot) * BM + r;
         *reinterpret_cast<float4*>(p.part_o + row * D + d) = acc;

@@ -41,6 +41,11 @@ __device__ __forceinline__ int attn_token(const AttnParams& p, int r) {
   return p.G_inv ? static_cast<int>(__umul64hi(static_cast<unsigned long long>(r), p.G_inv)) : r;
 }
 
+// A row's factor and lse from its maximum m and sum l (in powers of two).  The sum is zero where the row sees no key, and
+// only there: a NaN among its scores makes a NaN of it, which is no mark of an empty row.
+__device__ __forceinline__ float attn_factor(float l, float unit) { return l == 0.f ? 0.f : unit / l; }
+__device__ __forceinline__ float attn_lse(float m, float l) { return l == 0.f ? ninf() : (m + log2f(l)) * 0.69314718055994531f; }
+
 // Keys [lo, hi) that rows [r0, r1) of the request can see.
 __device__ __forceinline__ void attn_keys(const AttnParams& p, const AttnReq& r, int r0, int r1, int* lo, int* hi) {
   *hi = p.causal ? max(min(r.at + attn_token(p, r1 - 1) + 1, r.kv), 0) : r.kv;

@@ -967,7 +967,7 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
       }
       if (half == 0 || !joined) {
         const bool whole = len == cur.count;
-        const float inv = whole ? (l > 0.f ? (FP4 ? p.v_unit : 1.f) / l : 0.f) : 1.f;
+        const float inv = whole ? attn_factor(l, FP4 ? p.v_unit : 1.f) : 1.f;
         f0 *= inv;
         f1 *= inv;
         const bool both = joined && len > 1;
@@ -1008,7 +1008,7 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
           if (!whole)
             *reinterpret_cast<float2*>(p.part_ml + prow * 2) = make_float2(m - kShift, l);
           else if (p.lse)
-            p.lse[orow] = l > 0.f ? (m - kShift + log2f(l)) * 0.69314718055994531f : ninf();
+            p.lse[orow] = attn_lse(m - kShift, l);
         }
         tc_fence_before();
         if (joined) mbar_arrive_warp(smem_addr(&bars.x_free));

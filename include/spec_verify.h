@@ -359,7 +359,8 @@ size_t spec_attention_workspace_bytes(int dtype, int q_heads, int kv_heads, int 
  *   lse[n, h] = ln sum_t exp(scale q[n, h] . k[t, g]),  g = h / (q_heads / kv_heads)
  * over the keys t < kv_lens[b] with, for causal != 0, t <= position of n and,
  * for window > 0, t > position of n - window.  A row that sees no key gives
- * out = 0, lse = -inf.  Keys and values at or beyond kv_lens[b] are never
+ * out = 0, lse = -inf, and no other row does: one with a NaN among its scores
+ * has lse NaN.  Keys and values at or beyond kv_lens[b] are never
  * used (they may be anything); those before it must be finite, except in
  * pages that lie wholly behind the window of all the request's new tokens:
  * those are not looked at, nor are their ids.
