@@ -153,6 +153,10 @@ __device__ __forceinline__ void tc_st32(uint32_t addr, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+// 2^x of a whole number x <= 0 (or -inf), exactly.
+__device__ __forceinline__ float tc_power(float x) {
+  return x < -126.f ? 0.f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(x) + 127) << 23);
+}
 // Two fp32 operations in one instruction.
 __device__ __forceinline__ uint64_t f2_pack(float a, float b) {
   uint64_t r;
@@ -756,7 +760,9 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
         if (FP4 && busy) {
           // The same with 128 registers a thread: the probabilities of 32 columns are written before the next are worked
           // on (over scores that have been read).  An item's first reference comes from a pass over all columns; where 32
-          // columns outgrow it, they are read again, and what was written against the old one is rescaled.
+          // columns outgrow it, they are read again, and what was written against the old one is rescaled.  References are
+          // whole numbers (the maximum rounded up), so that the factor is a power of two: f16 probabilities, the sum and O
+          // are rescaled exactly.
           const int key0 = cur.template tile<SINKS>(k0 + j) * BN, lo = row_lo - key0, hi = row_hi - key0;
           const int sinks = SINKS ? p.sinks - key0 : 0;
           const bool masked = key0 + BN > w_hi || key0 < w_lo;
@@ -779,7 +785,7 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
               for (int i = 0; i < 16; ++i)
                 t[i & 3] = fmaxf(fmaxf(t[i & 3], __uint_as_float(s[2 * i])), __uint_as_float(s[2 * i + 1]));
             }
-            if (m == ninf()) m = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale_log2;   // O and the sum are zero so far
+            if (m == ninf()) m = ceilf(fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3])) * scale_log2);   // O and the sum are zero so far
           }
           // 32 columns: exponentials against the reference, their sum, the maximum (scaled: the scale is positive)
           auto work = [&](uint32_t (&s)[32], int c) {
@@ -809,7 +815,8 @@ __global__ void __launch_bounds__(FP4 ? kTcFp4Threads : kTcThreads, 1)
             mask(s, c);
             pass();
             if (__any_sync(0xffffffffu, top - m > kFp4Grow)) {
-              const float f = ex2(m - (top == ninf() ? 0.f : top));
+              top = ceilf(top);
+              const float f = tc_power(m - (top == ninf() ? 0.f : top));
               l *= f;
               m = top;
               if (j > j0) {

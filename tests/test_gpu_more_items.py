@@ -182,3 +182,37 @@ def test_the_reference_is_outgrown_in_the_midst_of_a_tile(sv, nq, G, B, d, bits,
     one = ref[1][(row % 3 != 0)]
     assert (one > math.log(2.0 ** 9 + 500)).all() and (one < math.log(2.0 ** 10.5 + 1500)).all()
     _check(out, lse, ref, dt, max(kv), d, bits)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("nq", [10, 40])
+def test_probabilities_are_rounded_once(sv, nq, dtype):
+    """32 keys of one weight, whose f16 is half a unit above it, and behind them in the tile a key that outgrows the reference by
+    so little more than 2^8 that the rescaled ones would be rounded up by half a unit again.  Only the 32 have values."""
+    dt, B, G, hkv, d, page = DTYPES[dtype], 100, 4, 4, 64, 64
+    L = 3 * 128 + nq
+    width = -(-L // page)
+    pages = B * width
+    up = 1.05 * 2.0 ** -11                                        # beyond a tie of 11 bits
+    weight = 7 + math.log2(1 + up)
+    outgrows = 8 + math.log2((1 + 2.0 ** -10) / (1 + up))
+    assert math.log2(1 + 2.0 ** -11) < weight - 7 and 8 < outgrows < 8.001
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(nq)).to(torch.int32).view(B, width).cuda()
+    kcodes, vcodes = (torch.zeros(pages, page, hkv, d // 2, dtype=torch.uint8) for _ in range(2))
+    kscales, vscales = (torch.full((pages, page, hkv, d // 16), 56, dtype=torch.uint8) for _ in range(2))
+    at = lambda key: (table[:, key // page].cpu().long(), key % page)  # noqa: E731
+    for key in range(256, 288):
+        kcodes[at(key)] = torch.tensor([0x22] * 8 + [0] * 24, dtype=torch.uint8)          # 1 in the first block
+        vcodes[at(key)] = torch.tensor([0x12, 0x32, 0x54, 0x76] * 8, dtype=torch.uint8)
+        vscales[at(key)] = torch.tensor([56, 59, 61, 63], dtype=torch.uint8)
+    kcodes[at(296)] = torch.tensor([0] * 8 + [0x22] * 8 + [0] * 16, dtype=torch.uint8)
+    kc, vc = (sv.FP4Cache.of(c.cuda(), x.cuda().view(torch.float8_e4m3fn)) for c, x in ((kcodes, kscales), (vcodes, vscales)))
+    q = torch.zeros(B * nq, hkv * G, d)
+    q[..., :4], q[..., 4] = 1.75, weight - 7
+    q[..., 16:20], q[..., 20] = 2.0, outgrows - 8
+    q = q.to(dt).cuda()
+    lens, cu = torch.full((B,), L, dtype=torch.int32, device="cuda"), torch.arange(B + 1, dtype=torch.int32, device="cuda") * nq
+    out, lse = sv.chunk_attention(q, kc, vc, table, lens, cu, nq, scale=math.log(2.0), want_lse=True)
+    assert sv.default_workspace().status() == 0
+    ref = _reference(q, M.values(kcodes, kscales), M.values(vcodes, vscales), table, [L] * B, [nq] * B, True, 0, 0, math.log(2.0))
+    _check(out, lse, ref, dt, L, d, 4)
