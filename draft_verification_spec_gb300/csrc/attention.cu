@@ -145,7 +145,7 @@ cudaError_t attention_plan(const AttnForm& form, int kind, int rows, int D, int 
 // rows 130 : 188; single tokens (4 rows) to 8192 keys 235 : 195 (a 128-row product for 4 rows, and one warp's
 // softmax in the way of every key tile).  Where the tcgen05 kernel has no form, mma.sync is several times slower:
 // 32 x 17 tokens, 64/8 heads of 128, ragged to 16384, pages of 24 (1.23 GB) 848, of 64 (1.11 GB) 222 us; 2 x 2048
-// tokens behind 14336, 32/8 heads, pages of 24 3535, of 128 750 us; the same with 16/4 heads of 256 5177 us.
+// tokens behind 14336, 32/8 heads, pages of 24 3535, of 128 667-745 us; the same with 16/4 heads of 256 5177 us.
 int attention_kind(int rows, int D, int page_size, float scale) {
   const bool pow2 = (page_size & (page_size - 1)) == 0;
   if (rows > 16 && D >= 64 && D <= 128 && pow2 && page_size >= 8 && scale > 0.f) return rows > 128 ? 3 : 2;
@@ -156,6 +156,9 @@ int attention_kind(int rows, int D, int page_size, float scale) {
 // 128 values (16 rows at most there: O fills the registers), else the tcgen05 kernel.  Measured, 64 requests ragged to 8192
 // keys, 8 key heads of 128 (332 MB): 4 rows 73 us (in tiles of 16 rows 92, tcgen05 208), 16 rows 111 (224), 20 rows 146 (two
 // tiles of 16 176, tcgen05 205), 32 rows 174 (209, 228); by tcgen05 40 rows 227 (two tiles of 32 305), 64 rows 230 (324).
+// 8 heads of 64, mma.sync : tcgen05: 16 rows 75 : 181, 32 rows 105 : 185, 40 rows 184 : 192, 64 rows 187 : 181, 96 rows 280 : 194.
+// Heads that are not whole pieces (80; 96 alike), which both kernels read in 8-byte steps: 16 rows 156 : 463, 32 rows 218 :
+// 462, 40 rows 383 : 428, 64 rows 408 : 462, 96 rows 585 : 458, so there the border could lie at 64 rows (12 %).
 int attention_fp4_kind(int rows, int D, float scale) {
   if (rows > 32 && D <= 128 && scale > 0.f) return rows > 128 ? 3 : 2;
   return 0;

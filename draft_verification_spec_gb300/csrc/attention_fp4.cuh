@@ -7,7 +7,7 @@
 // the keys and values that the bits stand for, in f16; the units (powers of two) are factors of the scores and of the
 // rows.  Queries: f16 as they are; bf16 ones as f16 relative to the power of two at the row's largest value, which is
 // exact down to 2^-14 of it and loses 2^-25 of it at most below that.  Probabilities are rounded to f16, up to
-// 2^14 (see kFp4Shift): 2^-12 relative down to 2^-20 of the reference.  Statistics and O are fp32.
+// 2^14 (see kFp4Shift): 2^-11 relative (half a unit of 11 bits) down to 2^-20 of the reference.  Statistics and O are fp32.
 //
 // The products are transposed, S^T = K Q^T and O^T = V^T P^T: what is wide is the keys and the head, so they take
 // the tensor core's 16 rows, and the few query rows its 8 columns.
@@ -23,8 +23,12 @@
 // the products with the scales (ALU 59 %, issue 63 %).  Measured, heads 32/8 of 128, bf16: 64 single tokens ragged to
 // 16384 keys (686 MB) 129 us, 5.3 TB/s, 78 % of the measured copy (the bf16 cache of that length is 2.4 GB).  On the way:
 // queries on the 16 rows and 64-bit offsets 260, S^T and O^T 144, the warp's maximum only where a lane has outgrown the
-// reference 129.  Four CTAs an SM instead of three 133, four stages 131.  Heads of 64 (8192 keys) 25 -> 52 us against the
-// floor, of 256 (4096 keys) 54 -> 81.
+// reference 129.  Four CTAs an SM instead of three 133, four stages 131.
+// 64 single tokens ragged to 8192 keys, floor and time: heads of 64 25, 50-54 us, of 128 49, 71-75, of 256 102, 128-133.  Other
+// heads, and strides that are not whole pieces, go through the loose reads below (8 bytes of codes, scales one by one and
+// waited for): 80 35, 134-138, 96 35, 113-117, 112 42, 118-123, 192 74, 243-248.
+// Tiles of 32 rows with heads of 128 have 255 registers a thread and spill 280 bytes of stores and 116 of loads, tiles of 16
+// rows with heads of 256 (bf16) 8 and 8; the others none.
 #pragma once
 
 #include "attention_mma.cuh"

@@ -195,7 +195,8 @@ spec_status_t run_attention(const AttentionCall& a) {
   if (fp4) scales = internal_scales(*batch, *a.scales);
   const sv::AttnForm form = {a.dtype == SPEC_BF16, a.window > 0 && a.sinks > 0, fp4, scales.whole != 0};
   // strides that are not alike (keys' and values', or codes' and scales') leave the kernel that reads a key's 8 bytes and its
-  // scales one by one: 32 x 17 tokens ragged to 16384 keys 1297 us for 242, 64 single tokens to 8192 keys 199 for 73
+  // scales one by one: 32 x 17 tokens ragged to 16384 keys 1297 us for 242, 64 single tokens to 8192 keys 199 for 73.  (Heads other
+  // than 64, 128 and 256 long take the same reads there whatever their strides: 64 single tokens of heads of 80 134-138.)
   int kind = fp4 ? (scales.alike ? sv::attention_fp4_kind(rows, batch->dim, a.scale) : 0) : sv::attention_kind(rows, batch->dim, batch->page_size, a.scale);
   if (!fp4 && kind >= 2 && !sv::attention_maps(form.bf16, internal_batch(*batch), &maps)) kind = rows <= 16 ? 0 : 1;
   sv::AttnPlan plan;
