@@ -256,7 +256,7 @@ def chunk_attention(q, k_cache, v_cache, page_table, kv_lens, cu_q, max_q: int, 
     own included (pages wholly behind it may be gone); the first ``sinks`` keys of a request stay visible behind
     it (spec_chunk_attention_sinks).  ``scale`` defaults to dim ** -0.5.  Returns
     out [tokens, q_heads, dim], with ``want_lse`` (out, lse [tokens, q_heads] float32); a row that
-    sees no key gives 0 and -inf, rows of tokens that no request has stay unwritten.
+    sees no key gives 0 and -inf (one with a NaN among its scores NaN), rows of tokens that no request has stay unwritten.
     ``tuning``: a Tuning, of which the wait limit counts here (spec_chunk_attention_tuned).
     """
     lib = _lib or _bind()
@@ -433,7 +433,7 @@ def rope_append(q, k, v, rope: RopePlan, k_cache, v_cache, page_table, kv_lens, 
 class PagePool:
     """The arrays that the pages of a pool are made of: tensors and FP4Caches [pages, ...] of one number of pages, keys and
     values of all layers.  A page must lie in one piece in each.  They must stay where they are while the pool is used;
-    the pool keeps them alive.  ``pages`` is needed only where there are none.
+    the pool keeps them alive.  ``pages`` (2^30 at most) is needed only where there are none.
     """
 
     def __init__(self, caches, pages: Optional[int] = None):

@@ -216,3 +216,94 @@ def test_probabilities_are_rounded_once(sv, nq, dtype):
     assert sv.default_workspace().status() == 0
     ref = _reference(q, M.values(kcodes, kscales), M.values(vcodes, vscales), table, [L] * B, [nq] * B, True, 0, 0, math.log(2.0))
     _check(out, lse, ref, dt, L, d, 4)
+
+
+# ------------------------------------------------------------------------------------- other calls
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (50, 10)])
+@pytest.mark.parametrize("new,kv,hq,hkv,d", [
+    ([1, 1, 2], [300, 4, 130], 128, 1, 64), ([1, 3], [260, 129], 300, 1, 64), ([1, 2], [257, 300], 130, 1, 128),   # many heads a key head
+    ([2] * 900, [2 + i % 37 for i in range(900)], 4, 2, 64),                                                       # many short requests
+    ([3], [400003], 4, 1, 64), ([20], [150001], 4, 1, 128), ([300], [70001], 2, 1, 64),                            # one long one
+])
+def test_shapes_far_from_the_usual(sv, new, kv, hq, hkv, d, window, sinks, bits):
+    _run(sv, bits, "bf16", new, kv, 32, hq, hkv, d, window, sinks, seed=len(new) + hq)
+
+
+@pytest.mark.parametrize("nq", [1, 9, 20, 70])
+@pytest.mark.parametrize("d", [64, 80, 128])
+def test_fp4_units_at_their_ends(sv, d, nq):
+    """Units of 2^-64 and 2^64, with queries that bring the scores back to size, whole items and ones that CTAs share."""
+    dt, new, kv = torch.bfloat16, [nq, nq], [nq + 5000, nq + 40]
+    for ku, vu in ((2.0 ** -64, 2.0 ** 64), (2.0 ** 64, 2.0 ** -64)):
+        (kc, vc), (ke, ve), table, lens, cu = _fp4_batch(sv, new, kv, 16, 2, d, d + nq, units=(ku, vu))
+        q = (torch.randn(2 * nq, 8, d, generator=torch.Generator().manual_seed(9)) / ku).to(dt).cuda()
+        out, lse = sv.chunk_attention(q, kc, vc, table, lens, cu, nq, want_lse=True)
+        assert sv.default_workspace().status() == 0
+        ref = _reference(q, ke, ve, table, kv, new, True, 0, 0, d ** -0.5)
+        _check(out, lse, ref, dt, max(kv), d, 4)
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+@pytest.mark.parametrize("nq", [1, 5, 20, 70])
+def test_strided_queries_and_rows_of_nobody(sv, nq, bits):
+    """Queries that are part of one projection's output, rows behind the last request's: those of out, lse, q_out and the
+    cache stay as they were."""
+    hq, hkv, d, page, more = 8, 2, 128, 16, 3
+    new, kv = [nq, 0, nq], [nq + 77, 9, nq + 200]
+    if bits == 4:
+        (kc, vc), _, table, lens, cu = _fp4_batch(sv, new, kv, page, hkv, d, 5)
+    else:
+        kc, vc, table, lens, cu = _batch(new, kv, page, hkv, d, torch.bfloat16, 5, "hnd")
+    qkv = torch.randn(2 * nq + more, hq + 2 * hkv, d, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    q = qkv[:, :hq]
+    out = torch.full((2 * nq + more, hq, d), 7.0, dtype=torch.bfloat16, device="cuda")
+    sv.chunk_attention(q, kc, vc, table, lens, cu, nq, out=out)
+    want = sv.chunk_attention(q[:2 * nq].contiguous(), kc, vc, table, lens, cu, nq)
+    assert torch.equal(out[:2 * nq], want) and (out[2 * nq:] == 7.0).all()
+    plan, q_out = sv.RopePlan(d), torch.full_like(out, 7.0)
+    held = lambda: [t.clone() for c in (kc, vc) for t in ((c.codes, c.scales.view(torch.uint8)) if bits == 4 else (c.nan_to_num(),))]  # noqa: E731
+    sv.rope_append(q, qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], plan, kc, vc, table, lens, cu, q_out=q_out)
+    first = held()
+    part = [x[:2 * nq].contiguous() for x in (q, qkv[:, hq:hq + hkv], qkv[:, hq + hkv:])]
+    want = sv.rope_append(*part, plan, kc, vc, table, lens, cu)
+    assert torch.equal(q_out[:2 * nq], want) and (q_out[2 * nq:] == 7.0).all()
+    assert all(torch.equal(a, b) for a, b in zip(first, held()))
+    assert sv.default_workspace().status() == 0
+
+
+def test_two_graphs_over_one_workspace(sv):
+    """Replayed by turns, with other lengths in between: a graph finds nothing of the other's in the workspace."""
+    d, page = 128, 16
+    (kc, vc), (ke, ve), table, lens, cu = _fp4_batch(sv, [40, 40], [3000, 700], page, 2, d, 2)
+    (k1, v1), (e1, f1), table1, lens1, cu1 = _fp4_batch(sv, [1] * 5, [900, 30, 500, 2000, 0], page, 2, d, 3)
+    q, q1 = torch.randn(80, 8, d).bfloat16().cuda(), torch.randn(5, 8, d).bfloat16().cuda()
+    ws = sv.Workspace()
+    out, out1 = torch.empty_like(q), torch.empty_like(q1)
+    pool = sv.PagePool([], pages=300)
+    pages, n, moved, packed, used = table.clone(), lens.clone(), table.clone(), table.clone(), lens[:1].clone()
+    def first():
+        sv.chunk_attention(q, kc, vc, table, lens, cu, 40, out=out, workspace=ws)
+        sv.assign_pages(pool, pages, n, page, kept=n, out=moved, workspace=ws)
+    def second():
+        sv.compact_pages(pool, moved, out=packed, used=used, workspace=ws)
+        sv.chunk_attention(q1, k1, v1, table1, lens1, cu1, 1, out=out1, workspace=ws)
+    graphs = []
+    for f in (first, second):
+        f()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f()
+        graphs.append(g)
+    for a, b in ((2500, 680), (41, 60), (3000, 700)):
+        lens.copy_(torch.tensor([a, b], dtype=torch.int32))
+        out.fill_(9.0), out1.fill_(9.0)
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, sv.chunk_attention(q, kc, vc, table, lens, cu, 40))
+        assert torch.equal(out1, sv.chunk_attention(q1, k1, v1, table1, lens1, cu1, 1))
+        want, copies, ok = M.assign(pages.tolist(), n.tolist(), page, 300, n.tolist())
+        assert ok and moved.tolist() == want and packed.tolist() == M.compact(want, 300)[0]
+    assert ws.status() == 0
