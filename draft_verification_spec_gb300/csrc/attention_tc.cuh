@@ -43,13 +43,15 @@
 // Measured, 4 bits: 32 x 17 tokens, 64/8 heads of 128, ragged to 16384 keys (352 MB, f16) 244 us; 2048 tokens behind 14336,
 // 32/8 heads (515 GFLOP) 400 us, 1.29 PFLOP/s.  A key tile takes some 3300 cycles: a half's softmax 1850 (its latency: with
 // 128 registers a thread 32 columns at a time), then its two products 1024 and the hand-overs.  The loaders are not in the
-// way (without reads or without writes 241 to 258; 392 to 398), nor are the bytes (caches of 16 bits take 232 and 340-347 us).  On
-// the way, verify block and chunk: three loaders 557; 877, seven with page ids and codes ahead 357; 498, probabilities
-// written 32 columns at a time so that 128 registers hold them 308; 471, one offset for keys and values 264; 447, maximum
-// and exponentials in one pass 258; 406, whole heads and loose ones apart 246; 399, an item's fixed cost of five key tiles
-// 242; 398, references as whole numbers 244; 400.  With whole heads of 128 bf16 spills 4 bytes of stores and 12 of loads a thread, f16 nothing.  Tried and dropped: copies into a ring of shared memory by a warp of its own 275; 433, loaders for keys and for
-// values apart 313; 475, eleven loaders with 96 registers 268; 431, three with 168 310; 447, shares of a tile that take
-// turns 243; 412, a quarter of the exponentials as polynomials 338; 583, 16 columns at a time 313; 539.
+// way (without reads or without writes 241 to 258; 392 to 398), nor are the bytes (caches of 16 bits take 232 and 340-347
+// us).  On the way, verify block and chunk: three loaders 557; 877, seven with page ids and codes ahead 357; 498,
+// probabilities written 32 columns at a time so that 128 registers hold them 308; 471, one offset for keys and values 264;
+// 447, maximum and exponentials in one pass 258; 406, whole heads and loose ones apart 246; 399, an item's fixed cost of
+// five key tiles 242; 398, references as whole numbers 244; 400.  With whole heads of 128 bf16 spills 4 bytes of stores and
+// 12 of loads a thread, f16 nothing.  Tried and dropped: copies into a ring of shared memory by a warp of its own 275; 433,
+// loaders for keys and for values apart 313; 475, eleven loaders with 96 registers 268; 431, three with 168 310; 447,
+// shares of a tile that take turns 243; 412, a quarter of the exponentials as polynomials 338; 583, 16 columns at a time
+// 313; 539.
 //
 // Every wait is bounded: after `wait_limit` the kernel sets the status word, drains its copies and
 // MMAs, frees TMEM and returns, its record for the combine kernel empty.

@@ -8,8 +8,9 @@
 //
 // Codes are whole numbers, so they must not hang on a rounding on the way:
 // - x has 11 significant bits at most and scale x unit 4, so a quotient is either exactly on a border between two codes
-//   or at least 2^-11 of its size away from it (a border has 3 bits).  x times the reciprocal is off by 1.5 x 2^-23 (the reciprocal's
-//   2^-23, the product's rounding), far less than half a unit of half precision (2^-12 at least); rounding that to half precision (11 bits) lands on the border in the first case and off it in the second.
+//   or at least 2^-11 of its size away from it (a border has 3 bits).  x times the reciprocal is off by 1.5 x 2^-23 (the
+//   reciprocal's 2^-23, the product's rounding), far less than half a unit of half precision (2^-12 at least); rounding that
+//   to half precision (11 bits) lands on the border in the first case and off it in the second.
 // - largest / (6 unit) in the same way: a tie of e4m3 has 5 bits, 6 times that 7.
 // - a rotated key's fp32 error, (|x| + |y|) 2^-21.5 at most, can move its rounding to 16 bits.  Where both ends of that
 //   interval do not give the same scale and codes (1 block in some 10^4), the keys in question are rotated in 64 bits.
